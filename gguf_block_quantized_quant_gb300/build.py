@@ -1,6 +1,6 @@
 """Builds libqg.so in-tree with nvcc for sm_103a (GB300).
 
-The CUDA sources are compiled in parallel: the C-ABI translation unit once, and
+The CUDA sources are compiled in parallel: the C-ABI and decoder-layer translation units once, and
 ``qg_fmt.cu`` once per block format (``-DQG_FMT=<GGUF type id>``).  The library links the
 shared CUDA runtime so that it shares the process's runtime state (current device,
 streams) with PyTorch.
@@ -48,7 +48,7 @@ def _flags(extra=()):
 
 
 def _units():
-    units = [(os.path.join(CSRC, "qg_abi.cu"), os.path.join(OUT_DIR, "qg_abi.o"), [])]
+    units = [(os.path.join(CSRC, f"{u}.cu"), os.path.join(OUT_DIR, f"{u}.o"), []) for u in ("qg_attn", "qg_layer", "qg_abi")]
     for name, fid in FORMATS.items():
         units.append((os.path.join(CSRC, "qg_fmt.cu"), os.path.join(OUT_DIR, f"qg_fmt_{name}.o"),
                       [f"-DQG_FMT={fid}"]))

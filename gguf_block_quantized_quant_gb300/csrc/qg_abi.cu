@@ -12,6 +12,7 @@
 #include <utility>
 
 #include "../../include/qg.h"
+#include "qg_host.h"
 #include "qg_jobs.cuh"
 #include "qg_launch.h"
 
@@ -211,7 +212,7 @@ __global__ void wait_expiry_kernel(unsigned long long limit_ns) {
 // The small kernels ask for the same L1 / shared-memory split as the engine (all shared),
 // so that an SM does not have to change its configuration between them and the engine and
 // they can run beside an engine CTA.  Set once per kernel and device.
-static bool prefer_shared(const void *kern) {
+bool prefer_shared(const void *kern) {
     static std::mutex mu;
     static std::set<std::pair<const void *, int>> done;
     int dev = 0;
@@ -452,6 +453,9 @@ void *static_ws_addr() {
 }
 
 }  // namespace
+
+int device_sms() { return current_sms(); }
+int device_sms_planning() { return planning_sms(); }
 }  // namespace qg
 
 using namespace qg;
@@ -735,6 +739,8 @@ int qg_device_error(unsigned int *err) {
         if (rc) return rc;
         all |= v;
     }
+    if (const int rc = attn_dev_err_take(&v)) return rc;
+    all |= v;
     *err = all;
     return QG_OK;
 }

@@ -1,0 +1,732 @@
+// qg_attn.cu -- attention over a paged cache: the C entry points, the kernel for few rows per
+// sequence (single tokens, short chunks) and the kernel that joins partial results.
+#include <algorithm>
+#include <mutex>
+#include <set>
+#include <utility>
+
+#include "qg_attn.cuh"
+#include "qg_launch.h"
+
+namespace qg {
+
+// ----------------------------------------------------------------------------- few rows
+// Row r of a tile is query head g = r % G of the tile's cache head and new token r / G, so the
+// G heads that share a cache head read its slots once.  Work is counted in blocks of 16 slots
+// over all (sequence, cache head, row tile) items and cut into one equal range per CTA: a long
+// sequence spreads over many CTAs and many short ones share a CTA.  An item cut by a range
+// boundary leaves partial results, which the join kernel merges in a fixed order.
+//
+// Inside a range each warp takes every NW-th block.  It has its own ring of slots in shared
+// memory, filled by tiled TMA copies that it issues itself S blocks ahead (also across items),
+// and its own running maximum and sum, so warps meet only at the end of an item.  Scores and
+// the value sums are m16n8k16 products: 16 rows x 16 slots per block.
+//
+// Bound by the read of the cache; the products take about a quarter of that time, which is
+// why the probabilities can go in as two addends (hi + lo): the value sums then keep fp32
+// accuracy instead of the 11 (8) bits of one fp16 (bf16) factor.
+constexpr int DEC_ROWS = 16;
+constexpr int DEC_BLK = 16;      // slots per block: the least page size
+constexpr int DEC_MIN_BLKS = 8;  // blocks a CTA takes at least: one per warp
+
+template <int C, int D>
+struct DecCfg {
+    static constexpr bool Q8 = C == CACHE_Q8;
+    static constexpr int ES = Q8 ? 1 : 2;
+    static constexpr int ROWB = D * ES;                      // bytes of a slot's row
+    static constexpr int PANEL = ROWB < 128 ? ROWB : 128;    // bytes of a swizzled panel row
+    static constexpr int NP = ROWB / PANEL;                  // panels
+    static constexpr int TILE = DEC_BLK * ROWB;              // K (or V) bytes of a block
+    static constexpr int STEPS = Q8 ? DEC_BLK * (D / 32) * 2 : 0;
+    static constexpr int NW = (D == 256 && !Q8) ? 4 : 8;     // warps
+    static constexpr int S = D == 256 ? 3 : (D == 128 ? (Q8 ? 5 : 3) : (Q8 ? 8 : 6));
+    static constexpr int CT = NW == 4 ? 8 : 4;               // n-tiles (of 8 columns) merged at a time
+    static constexpr uint32_t RING = (uint32_t)NW * S * 2 * TILE;
+    static constexpr uint32_t STEP_AT = RING;
+    static constexpr uint32_t MERGE_AT = STEP_AT + (uint32_t)NW * S * 2 * STEPS;
+    static constexpr uint32_t ML_AT = MERGE_AT + (uint32_t)NW * DEC_ROWS * CT * 8 * 4;
+    static constexpr uint32_t BAR_AT = ML_AT + (uint32_t)NW * DEC_ROWS * 8;
+    static constexpr uint32_t BYTES = BAR_AT + (uint32_t)NW * S * 8 + 1024 /* alignment */;
+};
+
+// The blocks of one sequence: every item (cache head, row tile) of it has the same slots.
+struct SeqWork {
+    Seq sq;
+    int nrt;        // row tiles
+    int kb0, nblk;  // first block of 16 slots and their number (at least 1)
+    int64_t cost;   // blocks of all items
+};
+__device__ __forceinline__ SeqWork seq_work(const AttnArgs &a, int b) {
+    SeqWork w;
+    w.sq = seq_of(a.bt, b);
+    w.nrt = (w.sq.n * a.G + DEC_ROWS - 1) / DEC_ROWS;
+    const int low = a.window ? max(0, w.sq.len - w.sq.n - a.window + 1) : 0;
+    w.kb0 = low / DEC_BLK;
+    w.nblk = max(1, (w.sq.len + DEC_BLK - 1) / DEC_BLK - w.kb0);
+    w.cost = (int64_t)w.nrt * a.Hk * w.nblk;
+    return w;
+}
+
+// Position in the work list.
+struct Walk {
+    SeqWork w;
+    int b, item, blk;  // item: cache head * nrt + row tile
+    int64_t left;      // blocks left in this CTA's range
+};
+__device__ __forceinline__ void walk_next(Walk &k, const AttnArgs &a, int taken) {
+    k.left -= taken;
+    k.blk += taken;
+    if (k.left <= 0 || k.blk < k.w.nblk) return;
+    k.blk = 0;
+    if (++k.item < k.w.nrt * a.Hk) return;
+    k.item = 0;
+    do {
+        k.w = seq_work(a, ++k.b);
+    } while (k.w.cost == 0);  // left > 0: a later sequence has work
+}
+
+// Blocks in all sequences, the number of CTAs that share them, and the position of block
+// `at(total, ctas)` of the list.  Whole CTA; `sh` holds 34 values.
+template <class At>
+__device__ __forceinline__ Walk walk_find(const AttnArgs &a, int64_t *sh, int64_t &total, int &ctas, int max_ctas, At at) {
+    const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5, nwarps = nt >> 5;
+    int64_t mine = 0;
+    for (int b = tid; b < a.bt.batch; b += nt) mine += seq_work(a, b).cost;
+    const int64_t first_cost = mine;  // of sequence tid when one round covers the batch
+    auto scan = [&](int64_t v, int64_t &sum) {  // inclusive prefix over the CTA's threads
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t u = __shfl_up_sync(0xffffffffu, v, o);
+            if (lane >= o) v += u;
+        }
+        __syncthreads();
+        if (lane == 31) sh[warp] = v;
+        __syncthreads();
+        int64_t before = 0;
+        sum = 0;
+        for (int i = 0; i < nwarps; ++i) {
+            if (i < warp) before += sh[i];
+            sum += sh[i];
+        }
+        return v + before;
+    };
+    int64_t incl = scan(mine, total);
+    ctas = (int)min((int64_t)max_ctas, max((int64_t)1, (total + DEC_MIN_BLKS - 1) / DEC_MIN_BLKS));
+    const int64_t want = at(total, ctas);
+    Walk k;
+    k.b = 0, k.item = 0, k.blk = 0, k.left = 0;
+    if (want < 0 || want >= total) return k;
+    int64_t base = 0;
+    for (int c0 = 0; c0 < a.bt.batch; c0 += nt) {
+        int64_t sum = total, cost = first_cost;
+        if (a.bt.batch > nt) {
+            cost = c0 + tid < a.bt.batch ? seq_work(a, c0 + tid).cost : 0;
+            incl = scan(cost, sum);
+        }
+        const int64_t lo = base + incl - cost;
+        if (want >= lo && want < lo + cost) {  // one thread of one round
+            sh[32] = c0 + tid;
+            sh[33] = want - lo;
+        }
+        base += sum;
+        if (want < base) break;
+    }
+    __syncthreads();
+    k.b = (int)sh[32];
+    const int64_t rem = sh[33];
+    k.w = seq_work(a, k.b);
+    k.item = (int)(rem / k.w.nblk);
+    k.blk = (int)(rem % k.w.nblk);
+    return k;
+}
+// The blocks cut into one range per CTA; range c starts at start(c).
+struct Ranges {
+    int64_t per;
+    int rest, ctas;
+    __device__ __forceinline__ Ranges(int64_t total, int n) : per(total / n), rest((int)(total % n)), ctas(n) {}
+    __device__ __forceinline__ int64_t start(int c) const { return per * c + rest * c / ctas; }
+};
+
+__device__ __forceinline__ void ldmatrix4(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void ldmatrix4_t(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+// c += A (16 x 16, row major) * B (16 x 8, column major)
+template <class T>
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    if constexpr (std::is_same<T, f16>::value)
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Four int8 codes of a word as fp16 pairs (exact): code + 128 goes under the exponent of 1024.
+__device__ __forceinline__ uint32_t codes_to_f16(uint32_t biased, uint32_t sel) {
+    const uint32_t m = prmt(biased, 0x64646464u, sel);
+    const __half2 r = __hsub2(*reinterpret_cast<const __half2 *>(&m), __half2half2(__ushort_as_half(0x6480)));  // 1152
+    return *reinterpret_cast<const uint32_t *>(&r);
+}
+
+template <int C, int D>
+__global__ void __launch_bounds__(DecCfg<C, D>::NW * 32, 1)
+    attn_rows_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
+    using Cfg = DecCfg<C, D>;
+    using T = typename CacheT<C>::Q;
+    constexpr int NW = Cfg::NW, S = Cfg::S, NT = D / 8;
+    extern __shared__ __align__(16) uint8_t dec_smem[];
+    __shared__ int64_t sh[34];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t base = (smem_addr(dec_smem) + 1023u) & ~1023u;
+    const uint32_t ring = base + (uint32_t)warp * S * 2 * Cfg::TILE;
+    const uint32_t steps = base + Cfg::STEP_AT + (uint32_t)warp * S * 2 * Cfg::STEPS;
+    const uint32_t bars = base + Cfg::BAR_AT + (uint32_t)warp * S * 8;
+    float *merge = reinterpret_cast<float *>(dec_smem + (base - smem_addr(dec_smem)) + Cfg::MERGE_AT);
+    float2 *ml = reinterpret_cast<float2 *>(dec_smem + (base - smem_addr(dec_smem)) + Cfg::ML_AT);
+
+    if (lane == 0) {
+        for (int s = 0; s < S; ++s) mbar_init(bars + 8 * s, 1);
+        fence_mbar_init();
+    }
+    __syncwarp();
+    griddep_wait();
+    griddep_launch_dependents();
+    int64_t total, w0 = 0, w1 = 0;
+    int ctas;
+    Walk con = walk_find(a, sh, total, ctas, (int)gridDim.x, [&](int64_t tot, int n) {
+        if ((int)blockIdx.x >= n) return (int64_t)-1;
+        const Ranges rg(tot, n);
+        w0 = rg.start(blockIdx.x);
+        w1 = rg.start(blockIdx.x + 1);
+        return w0;
+    });
+    if (w0 >= w1) return;
+    con.left = w1 - w0;
+
+    // ---- producer: this warp's next block, its page id fetched one block early
+    Walk pro = con;
+    int pblk = 0, pend = 0, ppage = 0;  // next block and end of the segment; page id of the block
+    auto seg_end = [&](const Walk &k) { return (int)min((int64_t)k.w.nblk, k.blk + k.left); };
+    auto page_of = [&](const Walk &k, int blk) {
+        const int idx = (k.w.kb0 + blk) * DEC_BLK / a.bt.page;
+        return idx < a.bt.table_width ? a.bt.pages[k.b * a.bt.table_stride + idx] : -1;
+    };
+    auto pro_seek = [&]() {  // moves on to a segment that has a block for this warp
+        while (pro.left > 0 && pblk >= pend) {
+            walk_next(pro, a, pend - pro.blk);
+            if (pro.left > 0) {
+                pblk = pro.blk + warp;
+                pend = seg_end(pro);
+            }
+        }
+        if (pro.left > 0) ppage = page_of(pro, pblk);
+    };
+    pblk = pro.blk + warp;
+    pend = seg_end(pro);
+    pro_seek();
+    auto issue = [&](int s) {  // all lanes call; lane 0 copies the block into ring slot s
+        if (pro.left <= 0) return;
+        if (lane == 0) {
+            const int slot = (pro.w.kb0 + pblk) * DEC_BLK % a.bt.page, h = pro.item / pro.w.nrt;
+            const int page = (unsigned)ppage < (unsigned)a.bt.n_pages ? ppage : a.bt.n_pages;  // out of range: zeros
+            const uint32_t kt = ring + (uint32_t)s * 2 * Cfg::TILE, vt = kt + Cfg::TILE, bar = bars + 8 * s;
+            const bool st = Cfg::Q8 && page < a.bt.n_pages;
+            if (Cfg::Q8 && !st) {  // no such page: steps of zero beside codes of zero
+                for (int i = 0; i < 2 * Cfg::STEPS; i += 16) sts128(steps + (uint32_t)s * 2 * Cfg::STEPS + i, 0, 0, 0, 0);
+            }
+            mbar_arrive_expect_tx(bar, 2 * Cfg::TILE + (st ? 2 * Cfg::STEPS : 0));
+#pragma unroll
+            for (int p = 0; p < Cfg::NP; ++p)
+                tma_load_4d(kt + p * DEC_BLK * Cfg::PANEL, &kmap, p * (Cfg::PANEL / Cfg::ES), slot, h, page, bar);
+#pragma unroll
+            for (int p = 0; p < Cfg::NP; ++p)
+                tma_load_4d(vt + p * DEC_BLK * Cfg::PANEL, &vmap, p * (Cfg::PANEL / Cfg::ES), slot, h, page, bar);
+            if (st) {
+                const int64_t at = page * a.step_stride + ((int64_t)h * a.bt.page + slot) * (D / 32);
+                bulk_g2s(steps + (uint32_t)s * 2 * Cfg::STEPS, a.kd + at, Cfg::STEPS, bar);
+                bulk_g2s(steps + (uint32_t)(s * 2 + 1) * Cfg::STEPS, a.vd + at, Cfg::STEPS, bar);
+            }
+        }
+        pblk += NW;
+        pro_seek();
+    };
+    for (int s = 0; s < S; ++s) issue(s);
+
+    const int gr = lane >> 2, gc = lane & 3;
+    int slot = 0;
+    uint32_t phase = 0;
+    while (con.left > 0) {
+        const int end = seg_end(con), taken = end - con.blk;
+        const int h = con.item / con.w.nrt, rt = con.item % con.w.nrt;
+        const Seq sq = con.w.sq;
+        const int nr = min(DEC_ROWS, sq.n * a.G - rt * DEC_ROWS);
+        // ---- queries as A fragments: rows gr, gr + 8
+        uint32_t qf[D / 16][4];
+        int hi[2], lo[2];  // visible slots of the lane's two rows
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int r = gr + 8 * i, rr = rt * DEC_ROWS + r, t = rr / a.G, g = rr % a.G;
+            const bool ok = r < nr;
+            const T *src = static_cast<const T *>(a.q) + (ok ? (int64_t)(sq.first + t) * a.ldq + (int64_t)(h * a.G + g) * a.hdq : 0);
+            const int pos = sq.len - sq.n + t;
+            hi[i] = ok ? pos : -1;
+            lo[i] = a.window ? max(0, pos - a.window + 1) : 0;
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+                if constexpr (!Cfg::Q8) {
+                    qf[k][i] = ok ? *reinterpret_cast<const uint32_t *>(src + 16 * k + 2 * gc) : 0u;
+                    qf[k][i + 2] = ok ? *reinterpret_cast<const uint32_t *>(src + 16 * k + 8 + 2 * gc) : 0u;
+                } else {  // product 2 j + s of 32-element block j takes the lane's codes 4 s .. 4 s + 3 of its 8
+                    const uint2 v = ok ? *reinterpret_cast<const uint2 *>(src + (k >> 1) * 32 + gc * 8 + (k & 1) * 4)
+                                       : make_uint2(0u, 0u);
+                    qf[k][i] = v.x;
+                    qf[k][i + 2] = v.y;
+                }
+            }
+        }
+        const int t_first = rt * DEC_ROWS / a.G, t_last = (rt * DEC_ROWS + nr - 1) / a.G;
+        const int hi_min = sq.len - sq.n + t_first;                                               // every row sees up to here
+        const int lo_max = a.window ? max(0, sq.len - sq.n + t_last - a.window + 1) : 0;          // and from here
+        const int seen_lo = a.window ? max(0, hi_min - a.window + 1) : 0;                         // some row sees from here
+        float o[NT][4];
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) o[i][j] = 0.0f;
+        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+
+        for (int blk = con.blk + warp; blk < end; blk += NW) {
+            const int key0 = (con.w.kb0 + blk) * DEC_BLK;
+            const uint32_t kt = ring + (uint32_t)slot * 2 * Cfg::TILE, vt = kt + Cfg::TILE;
+            const uint32_t ks = steps + (uint32_t)slot * 2 * Cfg::STEPS, vs = ks + Cfg::STEPS;
+            mbar_wait(bars + 8 * slot, phase);
+            // ---- scores: s[n][*] = slots 8 n + 2 gc, + 1 of rows gr, gr + 8
+            float s[2][4] = {};
+            if constexpr (!Cfg::Q8) {
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k) {
+                    const int row = (lane & 7) + ((lane >> 4) << 3), ch = 2 * k + ((lane >> 3) & 1);
+                    uint32_t f[4];
+                    ldmatrix4(kt + (ch >> 3) * DEC_BLK * 128 + row * 128 + (((ch & 7) ^ (row & 7)) << 4), f);
+                    mma16816<T>(s[0], qf[k], f[0], f[1]);
+                    mma16816<T>(s[1], qf[k], f[2], f[3]);
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < D / 32; ++j) {
+#pragma unroll
+                    for (int n = 0; n < 2; ++n) {
+                        const int row = 8 * n + gr, byte = 32 * j + 8 * gc;
+                        uint32_t addr;
+                        if constexpr (Cfg::PANEL == 128)
+                            addr = kt + (byte >> 7) * DEC_BLK * 128 + row * 128 + ((((byte >> 4) & 7) ^ (row & 7)) << 4) + (byte & 15);
+                        else
+                            addr = kt + row * 64 + (((byte >> 4) ^ ((row >> 1) & 3)) << 4) + (byte & 15);
+                        uint2 v = lds64(addr);
+                        v.x ^= 0x80808080u;
+                        v.y ^= 0x80808080u;
+                        float acc[4] = {};
+                        mma16816<T>(acc, qf[2 * j], codes_to_f16(v.x, 0x4140), codes_to_f16(v.x, 0x4342));
+                        mma16816<T>(acc, qf[2 * j + 1], codes_to_f16(v.y, 0x4140), codes_to_f16(v.y, 0x4342));
+                        // the steps of slots 8 n + 2 gc, + 1: the codes stay exact integers in the products
+                        const float d0 = half_bits_to_float(lds16(ks + ((8 * n + 2 * gc) * (D / 32) + j) * 2));
+                        const float d1 = half_bits_to_float(lds16(ks + ((8 * n + 2 * gc + 1) * (D / 32) + j) * 2));
+                        s[n][0] = fmaf(acc[0], d0, s[n][0]);
+                        s[n][1] = fmaf(acc[1], d1, s[n][1]);
+                        s[n][2] = fmaf(acc[2], d0, s[n][2]);
+                        s[n][3] = fmaf(acc[3], d1, s[n][3]);
+                    }
+                }
+            }
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) s[n][j] *= a.scale2;
+            if (key0 + DEC_BLK - 1 > hi_min || key0 < lo_max) {
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int key = key0 + 8 * n + 2 * gc + (j & 1), i = j >> 1;
+                        if (key > hi[i] || key < lo[i]) s[n][j] = -INFINITY;
+                    }
+            }
+            // ---- running maximum; the sums are rescaled only where it grew
+            float mn[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                float v = fmaxf(fmaxf(s[0][2 * i], s[0][2 * i + 1]), fmaxf(s[1][2 * i], s[1][2 * i + 1]));
+                v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
+                v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
+                mn[i] = fmaxf(m[i], v);
+            }
+            if (__any_sync(0xffffffffu, mn[0] > m[0] || mn[1] > m[1])) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const float f = mn[i] > m[i] ? exp2_approx(m[i] - mn[i]) : 1.0f;  // m = -inf: 0
+                    m[i] = mn[i];
+                    l[i] *= f;
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        o[n][2 * i] *= f;
+                        o[n][2 * i + 1] *= f;
+                    }
+                }
+            }
+            uint32_t ph[4], pl[4];  // probabilities as A fragment, hi + lo
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const float mm = m[i] == -INFINITY ? 0.0f : m[i];
+                    const float p0 = exp2_approx(s[n][2 * i] - mm), p1 = exp2_approx(s[n][2 * i + 1] - mm);
+                    l[i] += p0 + p1;
+                    const uint32_t hb = pack2<T>(p0, p1);
+                    const float2 hf = unpack2<T>(hb);
+                    ph[2 * n + i] = hb;
+                    pl[2 * n + i] = pack2<T>(p0 - hf.x, p1 - hf.y);
+                }
+            // slots that no row sees may hold anything: their values are taken as zero
+            const bool ragged = key0 + DEC_BLK > sq.len || key0 < seen_lo;
+            uint32_t vm[2] = {~0u, ~0u};
+            if (ragged) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int k0 = key0 + 8 * i + 2 * gc;
+                    vm[i] = (k0 < sq.len && k0 >= seen_lo ? 0x0000ffffu : 0u) |
+                            (k0 + 1 < sq.len && k0 + 1 >= seen_lo ? 0xffff0000u : 0u);
+                }
+            }
+            if constexpr (!Cfg::Q8) {
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k) {
+                    const int row = (lane & 7) + (((lane >> 3) & 1) << 3), ch = 2 * k + (lane >> 4);
+                    uint32_t f[4];
+                    ldmatrix4_t(vt + (ch >> 3) * DEC_BLK * 128 + row * 128 + (((ch & 7) ^ (row & 7)) << 4), f);
+                    if (ragged) {
+                        f[0] &= vm[0];
+                        f[1] &= vm[1];
+                        f[2] &= vm[0];
+                        f[3] &= vm[1];
+                    }
+                    mma16816<T>(o[2 * k], ph, f[0], f[1]);
+                    mma16816<T>(o[2 * k], pl, f[0], f[1]);
+                    mma16816<T>(o[2 * k + 1], ph, f[2], f[3]);
+                    mma16816<T>(o[2 * k + 1], pl, f[2], f[3]);
+                }
+            } else {
+                // lane (gr, gc) reads the codes gr * EPR .. of slots 2 gc, 2 gc + 1, 2 gc + 8, 2 gc + 9 in
+                // each panel: product i then covers columns gr * EPR + i
+                constexpr int EPR = Cfg::PANEL / 8;  // 16, or 8 where rows are 64 bytes
+#pragma unroll
+                for (int p = 0; p < Cfg::NP; ++p) {
+                    uint32_t w[4][EPR / 4];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const int row = 2 * gc + (q & 1) + 8 * (q >> 1);
+                        if constexpr (EPR == 16) {
+                            const uint4 v = lds128(vt + p * DEC_BLK * 128 + row * 128 + ((gr ^ (row & 7)) << 4));
+                            w[q][0] = v.x, w[q][1] = v.y, w[q][2] = v.z, w[q][3] = v.w;
+                        } else {
+                            const uint2 v = lds64(vt + row * 64 + (((gr >> 1) ^ ((row >> 1) & 3)) << 4) + (gr & 1) * 8);
+                            w[q][0] = v.x, w[q][1] = v.y;
+                        }
+#pragma unroll
+                        for (int e = 0; e < EPR / 4; ++e) w[q][e] ^= 0x80808080u;
+                    }
+                    // the steps of those slots for the 32-element block that holds the lane's columns
+                    const int j = (p * 128 + gr * EPR) >> 5;
+                    uint32_t d[2];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const uint32_t at = vs + ((2 * gc + 8 * i) * (D / 32) + j) * 2;
+                        d[i] = lds16(at) | lds16(at + (D / 32) * 2) << 16;
+                    }
+#pragma unroll
+                    for (int e = 0; e < EPR / 4; ++e) {
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) {
+                            uint32_t f[2];
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) {
+                                // byte x of two slots' words, then each under 0x64
+                                const uint32_t two = prmt(w[2 * i][e], w[2 * i + 1][e], (uint32_t)(x | (4 + x) << 4));
+                                const uint32_t c = codes_to_f16(two, 0x4140);
+                                const __half2 r = __hmul2(*reinterpret_cast<const __half2 *>(&c), *reinterpret_cast<const __half2 *>(&d[i]));
+                                f[i] = *reinterpret_cast<const uint32_t *>(&r);
+                                if (ragged) f[i] &= vm[i];
+                            }
+                            const int n = p * 16 + 4 * e + x;
+                            mma16816<T>(o[n], ph, f[0], f[1]);
+                            mma16816<T>(o[n], pl, f[0], f[1]);
+                        }
+                    }
+                }
+            }
+            __syncwarp();  // every lane has read the slot
+            issue(slot);
+            if (++slot == S) {
+                slot = 0;
+                phase ^= 1;
+            }
+        }
+
+        // ---- merge the warps' results
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
+            l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
+            if (gc == 0) ml[warp * DEC_ROWS + gr + 8 * i] = make_float2(m[i], l[i]);
+        }
+        __syncthreads();
+        float f[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            float mx = -INFINITY, sum = 0.0f;
+#pragma unroll
+            for (int w = 0; w < NW; ++w) mx = fmaxf(mx, ml[w * DEC_ROWS + gr + 8 * i].x);
+            const float mz = mx == -INFINITY ? 0.0f : mx;
+#pragma unroll
+            for (int w = 0; w < NW; ++w) {
+                const float2 v = ml[w * DEC_ROWS + gr + 8 * i];
+                sum += v.y * exp2_approx(v.x - mz);
+            }
+            f[i] = sum > 0.0f ? exp2_approx(m[i] - mz) / sum : 0.0f;
+            if (sum != sum) f[i] = sum;  // a NaN score stays one
+        }
+        const bool whole = con.blk == 0 && end == con.w.nblk;
+        float *part = a.part + (size_t)(2 * blockIdx.x + (con.blk == 0 ? 1 : 0)) * attn_part_floats(DEC_ROWS, D);
+        if (tid < nr) {
+            float mx = -INFINITY, sum = 0.0f;
+            for (int w = 0; w < NW; ++w) mx = fmaxf(mx, ml[w * DEC_ROWS + tid].x);
+            const float mz = mx == -INFINITY ? 0.0f : mx;
+            for (int w = 0; w < NW; ++w) {
+                const float2 v = ml[w * DEC_ROWS + tid];
+                sum += v.y * exp2_approx(v.x - mz);
+            }
+            const float ls = sum > 0.0f ? mz + log2_approx(sum) : sum == 0.0f ? -INFINITY : sum;
+            const int rr = rt * DEC_ROWS + tid;
+            if (!whole)
+                part[DEC_ROWS * D + tid] = ls;
+            else if (a.lse)
+                a.lse[(int64_t)(sq.first + rr / a.G) * a.Hq + h * a.G + rr % a.G] = ls * LN2;
+        }
+#pragma unroll
+        for (int c0 = 0; c0 < NT; c0 += Cfg::CT) {
+            constexpr int CW = Cfg::CT * 8;
+            if (c0) __syncthreads();
+#pragma unroll
+            for (int n = 0; n < Cfg::CT; ++n)
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    *reinterpret_cast<float2 *>(merge + (warp * DEC_ROWS + gr + 8 * i) * CW + 8 * n + 2 * gc) =
+                        make_float2(o[c0 + n][2 * i] * f[i], o[c0 + n][2 * i + 1] * f[i]);
+            __syncthreads();
+            for (int x = tid; x < nr * CW; x += NW * 32) {
+                const int r = x / CW, j = x % CW;
+                float v = 0.0f;
+#pragma unroll
+                for (int w = 0; w < NW; ++w) v += merge[(w * DEC_ROWS + r) * CW + j];
+                const int n = c0 + j / 8, e = j & 7;
+                int col;
+                if constexpr (!Cfg::Q8) {
+                    col = 8 * n + e;
+                } else {
+                    constexpr int EPR = Cfg::PANEL / 8;
+                    col = (n / EPR) * Cfg::PANEL + e * EPR + n % EPR;
+                }
+                const int rr = rt * DEC_ROWS + r;
+                if (!whole) {
+                    part[r * D + col] = v;
+                } else {
+                    const int64_t at = ((int64_t)(sq.first + rr / a.G) * a.Hq + h * a.G + rr % a.G) * D + col;
+                    if (a.out_f32)
+                        static_cast<float *>(a.out)[at] = v;
+                    else
+                        static_cast<T *>(a.out)[at] = from_f32<T>(v);
+                }
+            }
+        }
+        __syncthreads();  // ml and merge are free again
+        walk_next(con, a, taken);
+    }
+    // every copy that was issued has been waited for, unless a wait gave up: let those land
+    for (int s = 0; s < S; ++s)
+        if (lane == 0) mbar_drain(bars + 8 * s, (s < slot ? phase : phase ^ 1), DRAIN_NS);
+}
+
+// Merges the partial results of the items that range boundaries cut.  Block (x, y): the item cut
+// by boundary x + 1, if that is the first boundary inside it; row y.  Partial i carries weight
+// 2^(lse_i - max).
+template <class T, int D>
+__global__ void __launch_bounds__(D) attn_join_kernel(const AttnArgs a, int max_ctas) {
+    __shared__ int64_t sh[34];
+    griddep_wait();
+    griddep_launch_dependents();
+    const int bound = (int)blockIdx.x + 1;
+    int64_t total, at = -1;
+    int ctas;
+    const Walk k = walk_find(a, sh, total, ctas, max_ctas, [&](int64_t tot, int n) {
+        at = bound < n ? Ranges(tot, n).start(bound) : -1;
+        return at;
+    });
+    if (at < 0 || at >= total || k.blk == 0) return;
+    const int64_t s0 = at - k.blk, s1 = s0 + k.w.nblk;  // the item's blocks
+    const Ranges rg(total, ctas);
+    if (bound > 1 && rg.start(bound - 1) > s0) return;  // an earlier boundary joins it
+    const int h = k.item / k.w.nrt, rt = k.item % k.w.nrt, r = blockIdx.y;
+    if (r >= min(DEC_ROWS, k.w.sq.n * a.G - rt * DEC_ROWS)) return;
+    int last = bound;  // ranges bound - 1 .. last hold the item
+    while (last + 1 < ctas && rg.start(last + 1) < s1) ++last;
+    auto part = [&](int c) {  // the first range starts with or before the item, the others inside it
+        const bool head = c == bound - 1;
+        return a.part + (size_t)(2 * c + (head ? 1 : 0)) * attn_part_floats(DEC_ROWS, D);
+    };
+    float mx = -INFINITY;
+#pragma unroll 8
+    for (int c = bound - 1; c <= last; ++c) mx = fmaxf(mx, part(c)[DEC_ROWS * D + r]);
+    const float mz = mx == -INFINITY ? 0.0f : mx;
+    float sum = 0.0f, v = 0.0f;
+#pragma unroll 8
+    for (int c = bound - 1; c <= last; ++c) {
+        const float *p = part(c);
+        const float w = exp2_approx(p[DEC_ROWS * D + r] - mz);
+        sum += w;
+        v = fmaf(w, p[r * D + threadIdx.x], v);
+    }
+    v = sum > 0.0f ? v / sum : sum;
+    const int rr = rt * DEC_ROWS + r;
+    const int64_t row = (int64_t)(k.w.sq.first + rr / a.G) * a.Hq + h * a.G + rr % a.G;
+    if (a.out_f32)
+        static_cast<float *>(a.out)[row * D + threadIdx.x] = v;
+    else
+        static_cast<T *>(a.out)[row * D + threadIdx.x] = from_f32<T>(v);
+    if (a.lse && threadIdx.x == 0) a.lse[row] = sum > 0.0f ? (mz + log2_approx(sum)) * LN2 : sum == 0.0f ? -INFINITY : sum;
+}
+
+// ----------------------------------------------------------------------------- host
+typedef CUresult (*PFN_encode_tiled)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                     const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                                     CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+bool attn_tensor_map(CUtensorMap *map, const qg_paged &c, const void *base, int rows) {
+    static const PFN_encode_tiled encode = [] {
+        void *f = nullptr;
+        cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess) {
+            cudaGetLastError();
+            f = nullptr;
+        }
+        return reinterpret_cast<PFN_encode_tiled>(f);
+    }();
+    if (!encode) return false;
+    const int es = c.type == QG_Q8_0 ? 1 : 2, row = c.dim * es;
+    const cuuint64_t dims[4] = {(cuuint64_t)c.dim, (cuuint64_t)c.page, (cuuint64_t)c.kv_heads, (cuuint64_t)c.n_pages};
+    const cuuint64_t strides[3] = {(cuuint64_t)c.slot_stride * es, (cuuint64_t)c.head_stride * es, (cuuint64_t)c.page_stride * es};
+    const cuuint32_t box[4] = {(cuuint32_t)(std::min(row, 128) / es), (cuuint32_t)rows, 1, 1};
+    const cuuint32_t unit[4] = {1, 1, 1, 1};
+    const CUtensorMapDataType type = c.type == QG_Q8_0   ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                     : c.type == QG_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                          : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    return encode(map, type, 4, const_cast<void *>(base), dims, strides, box, unit, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  row >= 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Dynamic shared memory above 48 KB is asked for once per kernel and device.
+static bool allow_smem(const void *kern, uint32_t bytes) {
+    static std::mutex mu;
+    static std::set<std::pair<const void *, int>> done;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return false;
+    std::lock_guard<std::mutex> lock(mu);
+    if (done.count({kern, dev})) return true;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) != cudaSuccess) return false;
+    done.insert({kern, dev});
+    return true;
+}
+
+template <int C, int D>
+static int attn_rows_run(const AttnArgs &a, const qg_paged &c, int sms, cudaStream_t s) {
+    using Cfg = DecCfg<C, D>;
+    static_assert(Cfg::BYTES <= SMEM_MAX, "shared memory of the row kernel");
+    CUtensorMap km, vm;
+    if (!attn_tensor_map(&km, c, c.k, DEC_BLK) || !attn_tensor_map(&vm, c, c.v, DEC_BLK)) return QG_ECUDA;
+    auto kern = attn_rows_kernel<C, D>;
+    if (!allow_smem((const void *)kern, Cfg::BYTES)) return QG_ECUDA;
+    if (!launch_programmatic(kern, dim3((unsigned)sms), Cfg::NW * 32, Cfg::BYTES, s, a, km, vm)) return QG_ECUDA;
+    if (sms == 1) return QG_OK;
+    const int rows = (int)std::min<int64_t>(DEC_ROWS, (int64_t)a.bt.tokens * a.G);
+    auto join = attn_join_kernel<typename CacheT<C>::Q, D>;
+    return launch_programmatic(join, dim3((unsigned)(sms - 1), (unsigned)rows), D, 0, s, a, sms) ? QG_OK : QG_ECUDA;
+}
+template <int C>
+static int attn_rows_dim(const AttnArgs &a, const qg_paged &c, int sms, cudaStream_t s) {
+    return c.dim == 64 ? attn_rows_run<C, 64>(a, c, sms, s) : c.dim == 128 ? attn_rows_run<C, 128>(a, c, sms, s) : attn_rows_run<C, 256>(a, c, sms, s);
+}
+
+int attn_dev_err_take(unsigned int *err) {
+    unsigned int zero = 0;
+    if (cudaMemcpyFromSymbol(err, g_qg_dev_err, sizeof(*err)) != cudaSuccess) return QG_ECUDA;
+    if (cudaMemcpyToSymbol(g_qg_dev_err, &zero, sizeof(zero)) != cudaSuccess) return QG_ECUDA;
+    return QG_OK;
+}
+
+}  // namespace qg
+
+using namespace qg;
+
+extern "C" {
+
+size_t qg_attn_workspace_size(int dim, int q_heads, int kv_heads, int tokens, int batch) {
+    if ((dim != 64 && dim != 128 && dim != 256) || kv_heads < 1 || q_heads < 1 || q_heads % kv_heads || tokens < 1 || batch < 1)
+        return (size_t)-1;
+    const int sms = device_sms_planning();
+    return (size_t)sms * 2 * attn_part_floats(DEC_ROWS, dim) * sizeof(float);
+}
+
+int qg_attn_paged(const void *q, int64_t ldq, int64_t hdq, int q_type, int tokens, int q_heads, int max_new, float scale,
+                  int window, void *out, int out_type, float *lse, const qg_paged *cache, void *ws, size_t ws_bytes,
+                  void *stream) {
+    if (!q || !out || !cache || tokens < 1 || q_heads < 1 || max_new < 0 || window < 0 || !(scale == scale)) return QG_EINVAL;
+    if (const int rc = paged_check(*cache)) return rc;
+    if (q_type != (cache->type == QG_BF16 ? QG_BF16 : QG_F16) || (out_type != q_type && out_type != QG_F32)) return QG_EINVAL;
+    const int D = cache->dim;
+    if (q_heads % cache->kv_heads || ldq < D || hdq < D) return QG_EINVAL;
+    if (!host_aligned(q, 16) || ldq % 8 || hdq % 8 || !host_aligned(out, 16) || !host_aligned(lse, 4)) return QG_EALIGN;
+    if (!ws || ws_bytes < qg_attn_workspace_size(D, q_heads, cache->kv_heads, tokens, cache->batch)) return QG_EWORKSPACE;
+    if (!host_aligned(ws, 16)) return QG_EALIGN;
+    const int sms = device_sms();
+    if (sms < 0) return sms;
+    AttnArgs a{};
+    a.bt = paged_batch(*cache, tokens);
+    a.q = q, a.ldq = ldq, a.hdq = hdq;
+    a.out = out, a.lse = lse;
+    a.Hq = q_heads, a.Hk = cache->kv_heads, a.G = q_heads / cache->kv_heads;
+    a.out_f32 = out_type == QG_F32;
+    a.window = window;
+    a.scale2 = scale * LOG2E;
+    a.kd = static_cast<const f16 *>(cache->kd), a.vd = static_cast<const f16 *>(cache->vd);
+    a.step_stride = cache->step_stride;
+    a.part = static_cast<float *>(ws);
+    cudaStream_t s = (cudaStream_t)stream;
+    switch (cache->type) {
+    case QG_F16: return attn_rows_dim<CACHE_F16>(a, *cache, sms, s);
+    case QG_BF16: return attn_rows_dim<CACHE_BF16>(a, *cache, sms, s);
+    default: return attn_rows_dim<CACHE_Q8>(a, *cache, sms, s);
+    }
+}
+
+}  // extern "C"

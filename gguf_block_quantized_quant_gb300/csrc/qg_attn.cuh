@@ -1,0 +1,67 @@
+// qg_attn.cuh -- what the two attention kernels share: arguments, tensor maps of the cache
+// pools, the work list and the layout of partial results.
+#pragma once
+
+#include <cuda.h>
+
+#include <type_traits>
+
+#include "qg_types.cuh"
+
+namespace qg {
+
+struct AttnArgs {
+    Batch bt;
+    const void *q;
+    int64_t ldq, hdq;  // elements between tokens, between heads
+    void *out;         // tokens x Hq x D, contiguous
+    float *lse;        // tokens x Hq, or NULL
+    int Hq, Hk, G;     // G = Hq / Hk query heads share one cache head
+    int out_f32;       // out is fp32 instead of the queries' type
+    int window;        // 0: none
+    float scale2;      // scale * log2(e): the kernels work in powers of two
+    const f16 *kd, *vd;
+    int64_t step_stride;
+    float *part;       // partial results (attn_part_floats each)
+};
+
+// One partial result: rows x D fp32 (normalised), then rows base-2 logarithms of the sums.
+__host__ __device__ constexpr size_t attn_part_floats(int rows, int D) { return (size_t)rows * D + rows; }
+
+constexpr float LOG2E = 1.4426950408889634f;
+constexpr float LN2 = 0.6931471805599453f;
+
+__device__ __forceinline__ float exp2_approx(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float log2_approx(float x) {
+    float y;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ uint32_t lds16(uint32_t a) {
+    uint16_t v;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
+    return v;
+}
+
+// 4-D tiled copy global -> shared: box at (element, slot, head, page); out-of-range pages give
+// zeros.  The element coordinate is always a multiple of 128 bytes (64 where rows are 64).
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map, int e, int slot, int head, int page,
+                                            uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
+        "[%6];" ::"r"(dst),
+        "l"(map), "r"(e), "r"(slot), "r"(head), "r"(page), "r"(bar)
+        : "memory");
+}
+
+// Tensor map of one pool (keys or values): rows of `dim` elements, copied as boxes of `rows`
+// slots x one swizzled panel (128 bytes of a row, or the whole row where it is 64 bytes).
+// Host; false when the driver refuses.
+bool attn_tensor_map(CUtensorMap *map, const qg_paged &c, const void *base, int rows);
+
+}  // namespace qg

@@ -1,0 +1,39 @@
+// qg_host.h -- host helpers shared by the translation units that hold C entry points.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace qg {
+
+// SM count of the current device, or a negative status (qg_abi.cu).
+int device_sms();
+// SM count for planning when no device is usable: 152 then (qg_abi.cu).
+int device_sms_planning();
+// Asks once per kernel and device for the all-shared L1 split of the streaming engine (qg_abi.cu).
+bool prefer_shared(const void *kern);
+
+inline bool host_aligned(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
+
+// Launch with programmatic stream serialization: the kernel may start while the previous
+// kernel in the stream is still running (it must griddep_wait() before touching its data).
+template <class... KArgs, class... Args>
+bool launch_programmatic(void (*kern)(KArgs...), dim3 grid, int block, size_t smem, cudaStream_t s, const Args &...args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, kern, static_cast<KArgs>(args)...) != cudaSuccess) {
+        cudaGetLastError();
+        return false;
+    }
+    return cudaGetLastError() == cudaSuccess;
+}
+
+}  // namespace qg

@@ -90,6 +90,9 @@ int prefill_run(const PrefillCall &c, int sms);
 template <int FMT>
 int dequant_f16_run(const uint8_t *W, int N, int K, uint16_t *out, cudaStream_t s);
 
+// Reads and clears the error word of the attention kernels (qg_attn.cu).
+int attn_dev_err_take(unsigned int *err);
+
 // Format-independent kernels (qg_abi.cu).
 int launch_quant_act(const float *x, int M, int K, long ldx, int8_t *xq, float *xd, int32_t *xs,
                      cudaStream_t s);

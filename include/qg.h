@@ -68,6 +68,13 @@ enum qg_format {
     QG_IQ4_XS = 23  /* 256 elements, 136 B: fp16 d, 6-bit sub-scales, 4-bit codebook indices */
 };
 
+/* Element types of the decoder-layer operators (qg_norm_residual, qg_rope_append,
+ * qg_attn_paged), numbered by their GGUF type ids.  A cache is QG_F16, QG_BF16 or QG_Q8_0. */
+enum qg_type { QG_F32 = 0, QG_F16 = 1, QG_BF16 = 30 };
+
+/* Frequency scalings of qg_rope_turns(). */
+enum qg_rope_scaling { QG_ROPE_PLAIN = 0, QG_ROPE_LINEAR = 1, QG_ROPE_NTK = 2, QG_ROPE_YARN = 3 };
+
 /* Status codes. */
 enum qg_status {
     QG_OK = 0,
@@ -224,6 +231,99 @@ int qg_prefill_gemm(int fmt, const void *W_blocks, const float *x, float *y, int
  * qg_prefill_gemm (same device decoders).  out: N x K uint16, device memory (or page-locked
  * host memory), 4-byte aligned. */
 int qg_dequant_f16(int fmt, const void *W_blocks, int N, int K, uint16_t *out, void *stream);
+
+/* ---------------------------------------------------------------- the rest of a decoder layer
+ * The three calls below stand between the quantized projections of a decoder layer:
+ *   qg_norm_residual -> qkv projection -> qg_rope_append -> qg_attn_paged -> out projection
+ *   -> qg_norm_residual -> FFN or MoE.
+ * All their pointers are device memory. */
+
+/* Norms before and after a block, fused with its gate, residual scale and residual sum.  Per
+ * row of H elements:
+ *   t = y;  t = t * rsqrt(mean(t^2) + eps) * (w_offset + w_post)   (where w_post is given)
+ *   t = t * gate                                                   (where gate is given)
+ *   r = res + alpha * t                                            (res NULL: r = alpha * t)
+ *   x = r * rsqrt(mean(r^2) + eps) * (w_offset + w_pre)            (where x_out is given)
+ * in fp32, each output rounded once; x is formed from the unrounded r.
+ *   y: M rows ldy elements apart, y_type.  gate: y_type, rows ldgate apart (0: one row for all).
+ *   res, res_out: res_type, QG_F32 or y_type; res rows ldres apart.  w_post, w_pre: H fp32.
+ *   res_out, x_out: M x H contiguous, one of them may be NULL; res_out may be res itself
+ *   where ldres = H.  x_type: any of the three.
+ * Limits: 1 <= H <= 16384, M >= 1.  Rows of a multiple of 4 elements that start on a boundary
+ * of 4 elements take the vector path; any other alignment of whole elements works. */
+int qg_norm_residual(const void *y, int y_type, int64_t ldy, const void *res, int res_type, int64_t ldres,
+                     const float *w_post, const void *gate, int64_t ldgate, const float *w_pre, float w_offset,
+                     float alpha, float eps, void *res_out, void *x_out, int x_type, int M, int H, void *stream);
+
+/* A paged key/value cache and the sequences of one call.
+ * Key (value) e of cache head h in slot s of page p is k[p * page_stride + h * head_stride +
+ * s * slot_stride + e], strides in elements, multiples of 16 bytes; k and v are 16-byte
+ * aligned and have the same strides.  Types: QG_F16, QG_BF16, or QG_Q8_0: int8 codes with one
+ * fp16 step per 32 elements, the value being step * code (the rule of the Q8_0 block, codes
+ * and steps in pools of their own: kd, vd: n_pages pages step_stride elements apart, each
+ * kv_heads x page x dim/32 contiguous).
+ * Sequence b has the new tokens q_start[b] .. q_start[b+1] - 1 of the call, which are the
+ * last of its kv_len[b] slots; token i of n is at position kv_len[b] - n + i.  Its slot at
+ * position p is slot p % page of page pages[b * table_stride + p / page].  A position below 0
+ * (kv_len < n) marks padding: nothing is appended for it and its outputs are zero.  Lengths
+ * are held inside the arrays (token rows to the call's tokens, kv_len to table_width pages);
+ * page ids outside 0 .. n_pages - 1 read as zeros and are not written. */
+typedef struct qg_paged {
+    int type;         /* QG_F16, QG_BF16 or QG_Q8_0                                         */
+    int kv_heads;     /* cache heads                                                       */
+    int dim;          /* elements of a head: 64, 128 or 256                                */
+    int page;         /* slots per page: a multiple of 16                                  */
+    int n_pages;      /* pages in the pools                                                */
+    int batch;        /* sequences                                                         */
+    int table_width;  /* page ids per sequence                                             */
+    int pad;
+    int64_t page_stride, head_stride, slot_stride, step_stride, table_stride;
+    void *k, *v, *kd, *vd;
+    const int32_t *q_start; /* batch + 1, not decreasing                                   */
+    const int32_t *kv_len;  /* batch                                                       */
+    const int32_t *pages;   /* batch x table_stride                                        */
+} qg_paged;
+
+/* Phase increments of the rotary pairs for qg_rope_append, in units of 2^-64 turns per
+ * position: turns[j] = floor(2^64 * f_j / (2 pi)) for j < rot/2, f_j = base^(-2j/rot) scaled by
+ *   PLAIN: nothing.   LINEAR: f / factor.   NTK: base * factor^(rot/(rot-2)) as the base.
+ *   YARN: f / factor * ramp + f * (1 - ramp), ramp rising from 0 to 1 between the pairs that
+ *   turn beta_fast and beta_slow times within `original` positions.
+ * *amp (may be NULL) receives the factor of the rotated values: 0.1 ln(factor) + 1 for YARN,
+ * else 1.  Host function: turns is host memory (upload it once). */
+int qg_rope_turns(int rot, double base, int scaling, double factor, double original, double beta_fast, double beta_slow,
+                  uint64_t *turns, float *amp);
+
+/* Rotates the new tokens' queries and keys by their positions and appends keys and values to
+ * the cache.  Per token at position p and head, with w (wq or wk, dim fp32 each, may be NULL)
+ * applied to whole heads first: x = x * rsqrt(mean(x^2) + eps) * w; then pair j < rot/2,
+ *   (a, b) -> amp * (a cos - b sin, b cos + a sin),  angle = p * turns[j] * 2^-64 turns,
+ * a and b being elements j and j + rot/2 (pairs = 0) or 2j and 2j + 1 (pairs = 1); elements
+ * from rot on pass through.  The phase is a 64-bit product, exact at any position.
+ *   q, k, v: in_type; token t, head h at t * ld + h * hd elements (views of one projection's
+ *   output); every head aligned to min(16 bytes, dim/32 elements).  turns: device, rot/2.
+ *   q_out: tokens x q_heads x dim contiguous, QG_F16 (QG_BF16 beside a QG_BF16 cache). */
+int qg_rope_append(const void *q, int64_t ldq, int64_t hdq, const void *k, int64_t ldk, int64_t hdk, const void *v,
+                   int64_t ldv, int64_t hdv, int in_type, int tokens, int q_heads, const uint64_t *turns, int rot, int pairs,
+                   float amp, const float *wq, const float *wk, float eps, void *q_out, const qg_paged *cache,
+                   void *stream);
+
+/* Attention of the new tokens over the cache: for token t at position p and query head g,
+ *   o = sum_j softmax_j(scale * q.k_j) v_j   over   max(0, p - window + 1) <= j <= p
+ * (window 0: from 0), keys and values of cache head g / (q_heads / kv_heads).  Scores, the
+ * running maximum and the sums are fp32.
+ *   q: q_type (QG_BF16 beside a QG_BF16 cache, else QG_F16); token t, head g at t * ldq + g * hdq.
+ *   out: tokens x q_heads x dim contiguous, q_type or QG_F32.  lse: tokens x q_heads fp32
+ *   natural logarithms of the sums (-inf where nothing is visible), or NULL.
+ *   max_new: the longest chunk of the batch; it chooses between two kernels and nothing else.
+ *   ws: qg_attn_workspace_size(dim, q_heads, kv_heads, tokens, batch) bytes, 16-byte aligned. */
+int qg_attn_paged(const void *q, int64_t ldq, int64_t hdq, int q_type, int tokens, int q_heads, int max_new, float scale,
+                  int window, void *out, int out_type, float *lse, const qg_paged *cache, void *ws, size_t ws_bytes,
+                  void *stream);
+
+/* Bytes of qg_attn_paged's workspace ((size_t)-1: invalid arguments); depends on the current
+ * device's SM count as qg_workspace_size does. */
+size_t qg_attn_workspace_size(int dim, int q_heads, int kv_heads, int tokens, int batch);
 
 /* Bytes of workspace an operation needs; 0 means the call needs none (ws may then be
  * NULL); (size_t)-1 means the arguments are invalid.  The size depends on the shape and
