@@ -48,7 +48,7 @@ def _flags(extra=()):
 
 
 def _units():
-    units = [(os.path.join(CSRC, f"{u}.cu"), os.path.join(OUT_DIR, f"{u}.o"), []) for u in ("qg_attn", "qg_layer", "qg_abi")]
+    units = [(os.path.join(CSRC, f"{u}.cu"), os.path.join(OUT_DIR, f"{u}.o"), []) for u in ("qg_chunk", "qg_attn", "qg_layer", "qg_abi")]
     for name, fid in FORMATS.items():
         units.append((os.path.join(CSRC, "qg_fmt.cu"), os.path.join(OUT_DIR, f"qg_fmt_{name}.o"),
                       [f"-DQG_FMT={fid}"]))

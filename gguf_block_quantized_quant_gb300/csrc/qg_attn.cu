@@ -172,13 +172,6 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
                      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Four int8 codes of a word as fp16 pairs (exact): code + 128 goes under the exponent of 1024.
-__device__ __forceinline__ uint32_t codes_to_f16(uint32_t biased, uint32_t sel) {
-    const uint32_t m = prmt(biased, 0x64646464u, sel);
-    const __half2 r = __hsub2(*reinterpret_cast<const __half2 *>(&m), __half2half2(__ushort_as_half(0x6480)));  // 1152
-    return *reinterpret_cast<const uint32_t *>(&r);
-}
-
 template <int C, int D>
 __global__ void __launch_bounds__(DecCfg<C, D>::NW * 32, 1)
     attn_rows_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
@@ -474,6 +467,7 @@ __global__ void __launch_bounds__(DecCfg<C, D>::NW * 32, 1)
                     }
                 }
             }
+            fence_proxy_async_smem();
             __syncwarp();  // every lane has read the slot
             issue(slot);
             if (++slot == S) {
@@ -616,6 +610,19 @@ __global__ void __launch_bounds__(D) attn_join_kernel(const AttnArgs a, int max_
 }
 
 // ----------------------------------------------------------------------------- host
+// Dynamic shared memory above 48 KB is asked for once per kernel and device.
+bool allow_smem(const void *kern, uint32_t bytes) {
+    static std::mutex mu;
+    static std::set<std::pair<const void *, int>> done;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return false;
+    std::lock_guard<std::mutex> lock(mu);
+    if (done.count({kern, dev})) return true;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) != cudaSuccess) return false;
+    done.insert({kern, dev});
+    return true;
+}
+
 typedef CUresult (*PFN_encode_tiled)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
                                      const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
                                      CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
@@ -645,19 +652,6 @@ bool attn_tensor_map(CUtensorMap *map, const qg_paged &c, const void *base, int 
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Dynamic shared memory above 48 KB is asked for once per kernel and device.
-static bool allow_smem(const void *kern, uint32_t bytes) {
-    static std::mutex mu;
-    static std::set<std::pair<const void *, int>> done;
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return false;
-    std::lock_guard<std::mutex> lock(mu);
-    if (done.count({kern, dev})) return true;
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) != cudaSuccess) return false;
-    done.insert({kern, dev});
-    return true;
-}
-
 template <int C, int D>
 static int attn_rows_run(const AttnArgs &a, const qg_paged &c, int sms, cudaStream_t s) {
     using Cfg = DecCfg<C, D>;
@@ -681,7 +675,10 @@ int attn_dev_err_take(unsigned int *err) {
     unsigned int zero = 0;
     if (cudaMemcpyFromSymbol(err, g_qg_dev_err, sizeof(*err)) != cudaSuccess) return QG_ECUDA;
     if (cudaMemcpyToSymbol(g_qg_dev_err, &zero, sizeof(zero)) != cudaSuccess) return QG_ECUDA;
-    return QG_OK;
+    unsigned int more = 0;
+    const int rc = attn_chunk_dev_err_take(&more);
+    *err |= more;
+    return rc;
 }
 
 }  // namespace qg
@@ -694,7 +691,8 @@ size_t qg_attn_workspace_size(int dim, int q_heads, int kv_heads, int tokens, in
     if ((dim != 64 && dim != 128 && dim != 256) || kv_heads < 1 || q_heads < 1 || q_heads % kv_heads || tokens < 1 || batch < 1)
         return (size_t)-1;
     const int sms = device_sms_planning();
-    return (size_t)sms * 2 * attn_part_floats(DEC_ROWS, dim) * sizeof(float);
+    const size_t rows = (size_t)sms * 2 * attn_part_floats(DEC_ROWS, dim) * sizeof(float);
+    return std::max(rows, attn_chunk_workspace(dim, q_heads / kv_heads, tokens, batch, sms));
 }
 
 int qg_attn_paged(const void *q, int64_t ldq, int64_t hdq, int q_type, int tokens, int q_heads, int max_new, float scale,
@@ -719,9 +717,13 @@ int qg_attn_paged(const void *q, int64_t ldq, int64_t hdq, int q_type, int token
     a.window = window;
     a.scale2 = scale * LOG2E;
     a.kd = static_cast<const f16 *>(cache->kd), a.vd = static_cast<const f16 *>(cache->vd);
+    a.kc = cache->k, a.vc = cache->v;
+    a.page_stride = cache->page_stride, a.head_stride = cache->head_stride, a.slot_stride = cache->slot_stride;
     a.step_stride = cache->step_stride;
     a.part = static_cast<float *>(ws);
     cudaStream_t s = (cudaStream_t)stream;
+    // one row tile of 16 per sequence and cache head: the row kernel reads the cache once
+    if ((int64_t)max_new * a.G > DEC_ROWS) return attn_chunk(a, *cache, static_cast<uint8_t *>(ws), sms, s);
     switch (cache->type) {
     case QG_F16: return attn_rows_dim<CACHE_F16>(a, *cache, sms, s);
     case QG_BF16: return attn_rows_dim<CACHE_BF16>(a, *cache, sms, s);

@@ -20,8 +20,9 @@ struct AttnArgs {
     int out_f32;       // out is fp32 instead of the queries' type
     int window;        // 0: none
     float scale2;      // scale * log2(e): the kernels work in powers of two
+    const void *kc, *vc;  // pools (read directly by the 8-bit chunk kernel)
     const f16 *kd, *vd;
-    int64_t step_stride;
+    int64_t page_stride, head_stride, slot_stride, step_stride;
     float *part;       // partial results (attn_part_floats each)
 };
 
@@ -63,5 +64,17 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map
 // slots x one swizzled panel (128 bytes of a row, or the whole row where it is 64 bytes).
 // Host; false when the driver refuses.
 bool attn_tensor_map(CUtensorMap *map, const qg_paged &c, const void *base, int rows);
+
+// Four int8 codes of a word as fp16 pairs (exact): code + 128 goes under the exponent of 1024.
+__device__ __forceinline__ uint32_t codes_to_f16(uint32_t biased, uint32_t sel) {
+    const uint32_t m = prmt(biased, 0x64646464u, sel);
+    const __half2 r = __hsub2(*reinterpret_cast<const __half2 *>(&m), __half2half2(__ushort_as_half(0x6480)));  // 1152
+    return *reinterpret_cast<const uint32_t *>(&r);
+}
+
+// The chunk kernel (qg_chunk.cu): many rows per sequence, and its workspace.
+int attn_chunk(const AttnArgs &a, const qg_paged &c, uint8_t *ws, int sms, cudaStream_t s);
+size_t attn_chunk_workspace(int D, int G, int tokens, int batch, int sms);
+int attn_chunk_dev_err_take(unsigned int *err);
 
 }  // namespace qg

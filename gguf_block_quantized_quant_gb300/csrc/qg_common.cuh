@@ -188,6 +188,12 @@ __device__ __forceinline__ void bulk_g2s(uint32_t dst, const void *src, uint32_t
         : "memory");
 }
 
+// Orders this thread's earlier generic-proxy accesses of shared memory before its later
+// async-proxy (bulk copy) writes to the same bytes.
+__device__ __forceinline__ void fence_proxy_async_smem() {
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
 // Programmatic dependent launch: a kernel launched with the programmatic-serialization
 // attribute may start before the previous kernel in the stream has finished; it must call
 // griddep_wait() before reading anything that kernel writes.  The previous kernel calls

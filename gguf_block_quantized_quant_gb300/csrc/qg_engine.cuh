@@ -97,12 +97,6 @@ struct AccSink {
     __device__ __forceinline__ void add(int m, float v) { acc[m] += v; }
 };
 
-// Orders this thread's earlier generic-proxy accesses of shared memory before its later
-// async-proxy (bulk copy) writes to the same bytes.
-__device__ __forceinline__ void fence_proxy_async_smem() {
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-}
-
 // NCW: warps of the CTA (engine_ncw(), or 12 for large one-token launches, see plan_ncw).
 template <int FMT, int T, int MT, int NCW, class Job>
 __global__ void __launch_bounds__(NCW * 32, 1) engine_kernel(const Job job) {

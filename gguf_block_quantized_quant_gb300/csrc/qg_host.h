@@ -13,6 +13,9 @@ int device_sms_planning();
 // Asks once per kernel and device for the all-shared L1 split of the streaming engine (qg_abi.cu).
 bool prefer_shared(const void *kern);
 
+// Asks once per kernel and device for `bytes` of dynamic shared memory (qg_attn.cu).
+bool allow_smem(const void *kern, uint32_t bytes);
+
 inline bool host_aligned(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
 
 // Launch with programmatic stream serialization: the kernel may start while the previous

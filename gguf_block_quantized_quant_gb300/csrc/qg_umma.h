@@ -45,6 +45,19 @@ __host__ __device__ constexpr uint32_t umma_idesc_f16(int M, int N) {
     return (1u << 4) | (0u << 7) | (0u << 10) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
+// kind::f16 with A K-major (or in tensor memory) and B as given: bf16 operands, and B with its N
+// elements contiguous (MN-major) where b_mn.
+__host__ __device__ constexpr uint32_t umma_idesc_16(int M, int N, bool is_bf16, bool b_mn) {
+    return (1u << 4) | ((is_bf16 ? 1u : 0u) << 7) | ((is_bf16 ? 1u : 0u) << 10) | ((b_mn ? 1u : 0u) << 16) |
+           ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+// The descriptor of an MN-major, 128-byte-swizzled 16-bit tile: rows of 64 MN elements (128 bytes)
+// per K index, 8 of them an atom; panel_bytes to the next 64 MN elements, 1024 to the next 8 K.
+__host__ __device__ constexpr uint64_t umma_desc_mnmajor_sw128(uint32_t smem_addr, uint32_t panel_bytes) {
+    return umma_smem_desc(smem_addr, panel_bytes, UMMA_ATOM_BYTES, UMMA_SW128);
+}
+
 // Byte offset of fp16 element (row r, k) inside a K-major 128-byte-swizzled tile of 64 k.
 __host__ __device__ constexpr uint32_t sw128_offset(uint32_t r, uint32_t k) {
     return r * 128u + ((((k >> 3) ^ (r & 7u)) & 7u) << 4) + (k & 7u) * 2u;
