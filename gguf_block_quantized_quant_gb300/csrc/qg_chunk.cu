@@ -44,10 +44,21 @@ struct ChunkCfg {
     static constexpr int NP = D / 64;            // 128-byte panels of a row
     static constexpr uint32_t QB = 128 * D * 2;
     static constexpr uint32_t TILE = BN * D * 2;
+    // Warpgroups: one per row tile, one whose first two warps issue the products and the copies, and
+    // one that converts 8-bit codes
     static constexpr int MMA_WARP = 4 * NQ;
-    static constexpr int PROD_WARPS = Q8 ? 4 : 1;
-    static constexpr int THREADS = (4 * NQ + 1 + PROD_WARPS) * 32;
-    static constexpr int NBAR = 2 * NS + NQ + 2 * NQ * SB + NQ;
+    static constexpr int CONV_WARP = MMA_WARP + 4;
+    static constexpr int WGS = NQ + 1 + (Q8 ? 1 : 0);
+    static constexpr int THREADS = WGS * 128;
+    // Registers per thread at launch, and where each kind of warpgroup goes from there (0: stays).
+    // Their sums are the same, so every increase is met by a decrease.
+    static constexpr int LAUNCH_REGS = WGS == 2 ? 255 : WGS == 3 ? 168 : 128;
+    static constexpr int ROW_REGS = WGS == 2 ? 0 : !Q8 ? 208 : NQ == 2 ? 152 : 216;
+    static constexpr int ISSUE_REGS = WGS == 2 ? 0 : !Q8 ? 88 : NQ == 2 ? 72 : 104;
+    static constexpr int CONV_REGS = !Q8 ? 0 : NQ == 2 ? 136 : 184;
+    static_assert(WGS == 2 || NQ * ROW_REGS + ISSUE_REGS + CONV_REGS == WGS * LAUNCH_REGS, "registers");
+    static constexpr bool HOLD = !Q8 || BN == 64;  // a row's scores fit a thread's registers
+    static constexpr int NBAR = 2 * NS + NQ + 3 * NQ * SB;
     static constexpr uint32_t KV_AT = NQ * QB;
     static constexpr uint32_t BAR_AT = KV_AT + NS * TILE;
     static constexpr uint32_t BYTES = BAR_AT + NBAR * 8 + 16 + 1024 /* alignment */;
@@ -81,6 +92,11 @@ static ChunkPlan chunk_plan_at(uint8_t *p, int64_t tiles) {
 }
 
 constexpr int PLAN_THREADS = 1024;
+
+// An item costs its slot tiles and CHUNK_OV more for loading the queries and writing the result, in
+// the same unit; a range that ends inside that part leaves the item to the next CTA.
+constexpr int CHUNK_OV = 2;
+constexpr int CHUNK_MIN_UNITS = 3;  // a CTA takes at least
 
 // Inclusive prefix of v over the block; sum: the block's total.
 __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t *sh, int64_t &sum) {
@@ -141,7 +157,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) attn_plan_kernel(const AttnArgs 
                 t.kb0 = from / bn;
                 t.nt = max(1, (end + bn - 1) / bn - t.kb0);
                 // q_start that decreases could list more tiles than the call's tokens make: those are left out
-                if (tiles_before + r < max_tiles) cost = (int64_t)t.nt * a.Hk;
+                if (tiles_before + r < max_tiles) cost = (int64_t)(t.nt + CHUNK_OV) * a.Hk;
             }
             int64_t sum;
             const int64_t inc = block_scan(cost, sh, sum);
@@ -164,14 +180,16 @@ __global__ void __launch_bounds__(PLAN_THREADS) attn_plan_kernel(const AttnArgs 
 // Position in the work list: every role of a CTA walks it by itself.
 struct ChunkWalk {
     ChunkTile t;
-    int rt, h, blk;
-    int64_t left;  // tiles left in this CTA's range
+    int rt, h, u;  // row tile, cache head, unit of the item
+    int64_t left;  // units left in this CTA's range
+    __device__ __forceinline__ int blk() const { return max(0, u - CHUNK_OV); }  // first slot tile of the segment
+    __device__ __forceinline__ int end() const { return (int)min((int64_t)t.nt, max((int64_t)0, u + left - CHUNK_OV)); }
 };
 __device__ __forceinline__ ChunkTile chunk_tile(const ChunkPlan &p, int rt) {
     const int4 x = reinterpret_cast<const int4 *>(p.tile + rt)[0], y = reinterpret_cast<const int4 *>(p.tile + rt)[1];
     return ChunkTile{x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
 }
-// The position of tile `at` of the list; whole warp.
+// The position of unit `at` of the list; whole warp.
 __device__ __forceinline__ ChunkWalk chunk_find(const ChunkPlan &p, int nrt, int64_t at) {
     const int lane = threadIdx.x & 31;
     int lo = 0, n = nrt;  // the row tile is in [lo, lo + n)
@@ -186,27 +204,41 @@ __device__ __forceinline__ ChunkWalk chunk_find(const ChunkPlan &p, int nrt, int
     k.t = chunk_tile(p, lo);
     const int64_t rem = at - p.prefix[lo];
     k.rt = lo;
-    k.h = (int)(rem / k.t.nt);
-    k.blk = (int)(rem % k.t.nt);
+    k.h = (int)(rem / (k.t.nt + CHUNK_OV));
+    k.u = (int)(rem % (k.t.nt + CHUNK_OV));
     k.left = 0;
     return k;
 }
-__device__ __forceinline__ int chunk_end(const ChunkWalk &k) { return (int)min((int64_t)k.t.nt, k.blk + k.left); }
-__device__ __forceinline__ void chunk_next(ChunkWalk &k, const ChunkPlan &p, int Hk, int taken) {
-    k.left -= taken;
-    k.blk += taken;
-    if (k.left <= 0 || k.blk < k.t.nt) return;
-    k.blk = 0;
+// On to the next item of the range; left is 0 at its end.
+__device__ __forceinline__ void chunk_next(ChunkWalk &k, const ChunkPlan &p, int Hk) {
+    k.left -= k.t.nt + CHUNK_OV - k.u;
+    k.u = 0;
+    // a rest of CHUNK_OV units or less holds no slot tile
+    if (k.left <= CHUNK_OV) {
+        k.left = 0;
+        return;
+    }
     if (++k.h < Hk) return;
     k.h = 0;
     k.t = chunk_tile(p, ++k.rt);
 }
 __device__ __forceinline__ int chunk_ctas(int64_t total, int max_ctas) {
-    return (int)min((int64_t)max_ctas, max((int64_t)1, total));
+    return (int)min((int64_t)max_ctas, max((int64_t)1, total / CHUNK_MIN_UNITS));
 }
-// CTA c takes the tiles from start(c).
+// CTA c takes the units from start(c).
 __device__ __forceinline__ int64_t chunk_start(int64_t total, int ctas, int c) {
     return total / ctas * c + (int)(total % ctas) * c / ctas;
+}
+
+// x / d and x % d for 0 <= x < 2^31 with m = ceil(2^32 / d).
+__device__ __forceinline__ int fast_div(int x, int d, uint32_t m, int &rem) {
+    int q = d == 1 ? x : (int)__umulhi((uint32_t)x, m);
+    rem = x - q * d;
+    if (rem < 0) {
+        --q;
+        rem += d;
+    }
+    return q;
 }
 
 // ----------------------------------------------------------------------------- kernel
@@ -227,7 +259,10 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
     auto q_full = [&](int q) { return bars + 8u * (2 * NS + q); };
     auto s_full = [&](int q, int b) { return bars + 8u * (2 * NS + NQ + q * SB + b); };
     auto p_full = [&](int q, int b) { return bars + 8u * (2 * NS + NQ + NQ * SB + q * SB + b); };
-    auto pv_done = [&](int q) { return bars + 8u * (2 * NS + NQ + 2 * NQ * SB + q); };
+    // tile n of a row tile uses score buffer n % SB, and its value product that one's barrier: a full
+    // score buffer says that the product SB tiles back is complete, so a wait for product n or n - 1
+    // finds its barrier at most one phase away and the parity is unambiguous
+    auto pv_done = [&](int q, int b) { return bars + 8u * (2 * NS + NQ + 2 * NQ * SB + q * SB + b); };
     const uint32_t taddr_slot = bars + 8u * Cfg::NBAR;
 
     if (tid == 0) {
@@ -237,8 +272,8 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
         }
         for (int q = 0; q < NQ; ++q) {
             mbar_init(q_full(q), 128);
-            mbar_init(pv_done(q), 1);
             for (int b = 0; b < SB; ++b) {
+                mbar_init(pv_done(q, b), 1);
                 mbar_init(s_full(q, b), 1);
                 mbar_init(p_full(q, b), 128);
             }
@@ -257,47 +292,65 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
     const int ctas = chunk_ctas(total, gridDim.x);
     const int64_t w0 = (int)blockIdx.x < ctas ? chunk_start(total, ctas, blockIdx.x) : 0;
     const int64_t w1 = (int)blockIdx.x < ctas ? chunk_start(total, ctas, blockIdx.x + 1) : 0;
-    ChunkWalk k;
-    k.left = 0;
+    ChunkWalk k{};
     if (w1 > w0) {
         k = chunk_find(plan, *plan.nrt, w0);
         k.left = w1 - w0;
+        if (k.end() <= k.blk()) k.left = 0;  // the range ends before the item's first slot tile
     }
     uint32_t units = 0;  // key and value tiles so far: tile u sits in slot u % NS
 
     if (warp < 4 * NQ) {
         // ------------------------------------------------------------ a row per thread
-        const int q = warp >> 2, r = tid & 127;
+        if constexpr (Cfg::ROW_REGS > 0) set_max_regs<true, Cfg::ROW_REGS>();
+        const int q = warp >> 2, r = tid & 127, wr = r & ~31;  // wr: first row of the warp
         const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
         const uint32_t ocol = lanes + Cfg::O_COL + q * D;
+        const uint32_t qtile = base + q * Cfg::QB;
+        const uint32_t mG = (uint32_t)((0x100000000ull + a.G - 1) / a.G);
+        constexpr int CPR = D / 8;  // 16-byte chunks of a row
+        uint4 qv[CPR];              // the warp's 32 rows, 32 chunks a step
+        // chunk ch of a row, in the products' operand layout; a warp touches its own rows only
+        auto qat = [&](int row, int ch) { return qtile + (ch >> 3) * (128 * 128) + row * 128 + (((ch & 7) ^ (row & 7)) << 4); };
+        auto fetch_q = [&](const ChunkWalk &w) {
+            const int nrows = w.t.n * a.G, row0 = w.t.row0 + 128 * q;
+#pragma unroll
+            for (int i = 0; i < CPR; ++i) {
+                const int x = i * 32 + lane, rr = row0 + wr + x / CPR;
+                int g;
+                const int t = fast_div(rr, a.G, mG, g);
+                qv[i] = make_uint4(0u, 0u, 0u, 0u);
+                if (rr < nrows)
+                    qv[i] = *reinterpret_cast<const uint4 *>(static_cast<const T *>(a.q) + (int64_t)(w.t.first + t) * a.ldq +
+                                                             (int64_t)(w.h * a.G + g) * a.hdq + 8 * (x % CPR));
+            }
+        };
         uint32_t done = 0;  // slot tiles of this row tile so far
+        if (k.left > 0) fetch_q(k);
         while (k.left > 0) {
-            const int end = chunk_end(k), taken = end - k.blk;
+            const int blk0 = k.blk(), end = k.end();
             const int nrows = k.t.n * a.G, row0 = k.t.row0 + 128 * q;
+            ChunkWalk nk = k;
+            chunk_next(nk, plan, a.Hk);
             if (row0 < nrows) {
                 // ---- the queries into shared memory (the products that read the last ones are complete)
-                constexpr int CPR = D / 8;  // 16-byte chunks of a row
-#pragma unroll 8
+#pragma unroll
                 for (int i = 0; i < CPR; ++i) {
-                    const int x = i * 128 + r, row = x / CPR, ch = x % CPR, rr = row0 + row;
-                    uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                    if (rr < nrows) {
-                        v = *reinterpret_cast<const uint4 *>(static_cast<const T *>(a.q) + (int64_t)(k.t.first + rr / a.G) * a.ldq +
-                                                             (int64_t)(k.h * a.G + rr % a.G) * a.hdq + 8 * ch);
-                        v.x ^= qsign, v.y ^= qsign, v.z ^= qsign, v.w ^= qsign;
-                    }
-                    sts128(base + q * Cfg::QB + (ch >> 3) * (128 * 128) + row * 128 + (((ch & 7) ^ (row & 7)) << 4), v.x, v.y, v.z, v.w);
+                    const int x = i * 32 + lane, row = wr + x / CPR, ch = x % CPR;
+                    sts128(qat(row, ch), qv[i].x ^ qsign, qv[i].y ^ qsign,
+                           qv[i].z ^ qsign, qv[i].w ^ qsign);
                 }
                 fence_proxy_async_smem();
                 mbar_arrive(q_full(q));
 
                 const int rr = row0 + r, pos0 = k.t.len - k.t.n;
-                const int pos = pos0 + rr / a.G;
+                int g;
+                const int pos = pos0 + fast_div(rr, a.G, mG, g);
                 const int hi = rr < nrows ? pos : -1, lo = a.window ? max(0, pos - a.window + 1) : 0;
                 const int hi_min = pos0 + row0 / a.G;  // every row sees up to here, and from lo_max on
                 const int lo_max = a.window ? max(0, pos0 + (min(row0 + 128, nrows) - 1) / a.G - a.window + 1) : 0;
                 float m = -INFINITY, l = 0.0f;
-                for (int j = k.blk; j < end; ++j, ++done) {
+                for (int j = blk0; j < end; ++j, ++done) {
                     const int buf = SB == 1 ? 0 : (int)(done & 1);
                     const uint32_t scol = lanes + (q * SB + buf) * BN;
                     const int key0 = (k.t.kb0 + j) * BN;
@@ -305,8 +358,9 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
                     const bool edge = key0 + BN - 1 > hi_min || key0 < lo_max;
                     mbar_wait(s_full(q, buf), (done / SB) & 1);
                     tc_fence_after();
-                    uint32_t s[2][32];
-                    float mx = -INFINITY;
+                    // All scores of the row in registers (HOLD), or 32 at a time in two passes where the
+                    // converting warps leave too few registers
+                    uint32_t s[Cfg::HOLD ? BN / 32 : 2][32];
                     auto mask = [&](uint32_t (&v)[32], int c0) {
                         if (edge) {
 #pragma unroll
@@ -314,19 +368,38 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
                                 if (c0 + i > c_hi || c0 + i < c_lo) v[i] = 0xff800000u;  // -inf
                         }
                     };
-                    tmem_ld32(scol, s[0]);
-#pragma unroll
-                    for (int c = 0; c < BN / 32; ++c) {
-                        tmem_wait_ld(s[c & 1]);
-                        if (c + 1 < BN / 32) tmem_ld32(scol + 32 * (c + 1), s[(c + 1) & 1]);
-                        mask(s[c & 1], 32 * c);
+                    auto top = [&](const uint32_t (&v)[32]) {
                         float x[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) x[i & 3] = fmaxf(x[i & 3], __uint_as_float(s[c & 1][i]));
-                        mx = fmaxf(mx, fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])));
+                        for (int i = 0; i < 32; i += 2)
+                            x[(i / 2) & 3] = fmaxf(fmaxf(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), x[(i / 2) & 3]);
+                        return fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+                    };
+                    float mx = -INFINITY;
+                    if constexpr (Cfg::HOLD) {
+#pragma unroll
+                        for (int c = 0; c < BN / 32; ++c) tmem_ld32(scol + 32 * c, s[c]);
+                        tmem_wait_ld(s[0]);
+#pragma unroll
+                        for (int c = 1; c < BN / 32; ++c) tmem_loaded(s[c]);
+#pragma unroll
+                        for (int c = 0; c < BN / 32; ++c) {
+                            mask(s[c], 32 * c);
+                            mx = fmaxf(mx, top(s[c]));
+                        }
+                    } else {
+                        tmem_ld32(scol, s[0]);
+#pragma unroll
+                        for (int c = 0; c < BN / 32; ++c) {
+                            tmem_wait_ld(s[c & 1]);
+                            if (c + 1 < BN / 32) tmem_ld32(scol + 32 * (c + 1), s[(c + 1) & 1]);
+                            mask(s[c & 1], 32 * c);
+                            mx = fmaxf(mx, top(s[c & 1]));
+                        }
+                        tmem_ld32(scol, s[0]);
                     }
                     // ---- rescale where some row of the warp needs it (the first tile starts O afresh)
-                    if (j == k.blk) {
+                    if (j == blk0) {
                         m = mx;
                     } else {
                         const bool grown = (mx - m) * a.scale2 > 8.0f || (m == -INFINITY && mx > m);
@@ -334,89 +407,125 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
                             const float mn = fmaxf(m, mx), f = mn > m ? exp2_approx((m - mn) * a.scale2) : 1.0f;
                             m = mn;
                             l *= f;
-                            mbar_wait(pv_done(q), (done - 1) & 1);
+                            mbar_wait(pv_done(q, (done - 1) % SB), ((done - 1) / SB) & 1);
                             tc_fence_after();
+#pragma unroll 1
+                            for (int c = 0; c < D; c += 16) {
+                                uint32_t o[16];
+                                tmem_ld16(ocol + c, o);
 #pragma unroll
-                            for (int c = 0; c < D; c += 32) {
-                                uint32_t o[32];
-                                tmem_ld32(ocol + c, o);
-                                tmem_wait_ld(o);
-#pragma unroll
-                                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                                tmem_st32(ocol + c, o);
+                                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                                tmem_st16(ocol + c, o);
                             }
                             tmem_wait_st();
                         }
                     }
                     const float mz = (m == -INFINITY ? 0.0f : m) * a.scale2;
                     // ---- P over S: chunk c of 32 scores becomes columns 16 c .. 16 c + 15, which were read before
-                    float sum[4] = {};
-                    tmem_ld32(scol, s[0]);
+                    const uint64_t sc2 = pack_f32x2(a.scale2, a.scale2), mz2 = pack_f32x2(-mz, -mz);
+                    uint64_t sum[2] = {0ull, 0ull};
 #pragma unroll
                     for (int c = 0; c < BN / 32; ++c) {
-                        tmem_wait_ld(s[c & 1]);
-                        if (c + 1 < BN / 32) tmem_ld32(scol + 32 * (c + 1), s[(c + 1) & 1]);
-                        mask(s[c & 1], 32 * c);
+                        uint32_t(&v)[32] = s[Cfg::HOLD ? c : c & 1];
+                        if constexpr (!Cfg::HOLD) {
+                            tmem_wait_ld(v);
+                            if (c + 1 < BN / 32) tmem_ld32(scol + 32 * (c + 1), s[(c + 1) & 1]);
+                            mask(v, 32 * c);
+                        }
                         uint32_t p[16];
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
-                            const float p0 = exp2_approx(fmaf(__uint_as_float(s[c & 1][2 * i]), a.scale2, -mz));
-                            const float p1 = exp2_approx(fmaf(__uint_as_float(s[c & 1][2 * i + 1]), a.scale2, -mz));
-                            sum[(2 * i) & 3] += p0;
-                            sum[(2 * i + 1) & 3] += p1;
-                            p[i] = pack2<T>(p0, p1);
+                            const uint64_t x = fma_f32x2(pack_b32x2(v[2 * i], v[2 * i + 1]), sc2, mz2);
+                            float x0, x1;
+                            unpack_f32x2(x, x0, x1);
+                            x0 = exp2_approx(x0);
+                            x1 = exp2_approx(x1);
+                            sum[i & 1] = add_f32x2(sum[i & 1], pack_f32x2(x0, x1));
+                            p[i] = pack2<T>(x0, x1);
                         }
                         tmem_st16(scol + 16 * c, p);
                     }
-                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                    float l0, l1, l2, l3;
+                    unpack_f32x2(sum[0], l0, l1);
+                    unpack_f32x2(sum[1], l2, l3);
+                    l += (l0 + l1) + (l2 + l3);
                     tmem_wait_st();
                     tc_fence_before();
                     mbar_arrive(p_full(q, buf));
                 }
-                // ---- result.  A full score buffer says that the products SB tiles back are complete, so
-                // the wait for the last ones must not take an older phase of the same parity for them
-                if (SB == 2 && taken > 1) mbar_wait(pv_done(q), done & 1);
-                mbar_wait(pv_done(q), (done - 1) & 1);
+                if (nk.left > 0) fetch_q(nk);  // the next item's queries come in under the last product
+                // ---- result
+                mbar_wait(pv_done(q, (done - 1) % SB), ((done - 1) / SB) & 1);
                 tc_fence_after();
-                const bool whole = k.blk == 0 && end == k.t.nt;
+                const bool whole = blk0 == 0 && end == k.t.nt;
                 const float inv = l > 0.0f ? 1.0f / l : l;  // nothing visible: 0
                 const float ls = l > 0.0f ? (m == -INFINITY ? 0.0f : m) * a.scale2 + log2_approx(l) : l == 0.0f ? -INFINITY : l;
-                float *part = a.part + (size_t)(2 * blockIdx.x + (k.blk == 0 ? 1 : 0)) * attn_part_floats(Cfg::ROWS, D);
-                const int pr = 128 * q + r;
-                const int64_t orow = (int64_t)(k.t.first + rr / a.G) * a.Hq + k.h * a.G + rr % a.G;
-#pragma unroll
-                for (int c = 0; c < D; c += 32) {
-                    uint32_t o[32];
-                    tmem_ld32(ocol + c, o);
-                    tmem_wait_ld(o);
-                    if (rr < nrows) {
-                        float v[32];
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(o[i]) * inv;
-                        if (!whole)
-                            store_vec<float, 32>(part + (size_t)pr * D + c, v);
-                        else if (a.out_f32)
-                            store_vec<float, 32>(static_cast<float *>(a.out) + orow * D + c, v);
-                        else
-                            store_vec<T, 32>(static_cast<T *>(a.out) + orow * D + c, v);
-                    }
-                }
+                float *part = a.part + (size_t)(2 * blockIdx.x + (blk0 == 0 ? 1 : 0)) * attn_part_floats(Cfg::ROWS, D);
                 if (rr < nrows) {
                     if (!whole)
-                        part[(size_t)Cfg::ROWS * D + pr] = ls;
+                        part[(size_t)Cfg::ROWS * D + 128 * q + r] = ls;
                     else if (a.lse)
-                        a.lse[orow] = ls * LN2;
+                        a.lse[(int64_t)(k.t.first + pos - pos0) * a.Hq + k.h * a.G + g] = ls * LN2;
+                }
+                // Through the queries' place in shared memory, so that a warp writes whole rows: D 16-bit
+                // values of a row, or D / 2 fp32 values in each of two rounds
+                const bool wide = !whole || a.out_f32;
+                for (int half = 0; half < (wide ? 2 : 1); ++half) {
+#pragma unroll
+                    for (int c = 0; c < D; c += 32) {
+                        if (wide && c / (D / 2) != half) continue;
+                        uint32_t o[32];
+                        tmem_ld32(ocol + c, o);
+                        tmem_wait_ld(o);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * inv);
+                        if (wide) {
+                            const int c0 = (c - half * (D / 2)) / 4;
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                sts128(qat(r, c0 + i), o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                        } else {
+                            uint32_t h[16];
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) h[i] = pack2<T>(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1]));
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                sts128(qat(r, c / 8 + i), h[4 * i], h[4 * i + 1], h[4 * i + 2], h[4 * i + 3]);
+                        }
+                    }
+                    __syncwarp();
+#pragma unroll 4
+                    for (int i = 0; i < CPR; ++i) {
+                        const int x = i * 32 + lane, row = wr + x / CPR, ch = x % CPR, orr = row0 + row;
+                        if (orr < nrows) {
+                            const uint4 v = lds128(qat(row, ch));
+                            int og;
+                            const int ot = fast_div(orr, a.G, mG, og);
+                            const int64_t orow = (int64_t)(k.t.first + ot) * a.Hq + k.h * a.G + og;
+                            uint8_t *dst = !whole ? reinterpret_cast<uint8_t *>(part + (size_t)(128 * q + row) * D) + half * (D * 2)
+                                                  : static_cast<uint8_t *>(a.out) + (wide ? orow * (D * 4) + half * (D * 2) : orow * (D * 2));
+                            *reinterpret_cast<uint4 *>(dst + 16 * ch) = v;
+                        }
+                    }
+                    __syncwarp();
                 }
                 tc_fence_before();  // the next item's products overwrite O once its P arrives
+            } else if (nk.left > 0) {
+                fetch_q(nk);
             }
-            chunk_next(k, plan, a.Hk, taken);
+            k = nk;
         }
-    } else if (warp == Cfg::MMA_WARP) {
+    } else if (warp < Cfg::CONV_WARP) {
+        if constexpr (Cfg::ISSUE_REGS > 0) set_max_regs<false, Cfg::ISSUE_REGS>();
+        if (warp == Cfg::MMA_WARP) {
         // ------------------------------------------------------------ products
         constexpr uint32_t id_s = umma_idesc_16(128, BN, BF, false), id_o = umma_idesc_16(128, D, BF, true);
+        constexpr uint32_t desc_hi = (uint32_t)(umma_desc_kmajor_sw128(0) >> 32);
+        static_assert(desc_hi == (uint32_t)(umma_desc_mnmajor_sw128(0, BN * 128) >> 32), "one upper word");
+        const uint32_t leader = lane == 0;
         uint32_t items[NQ] = {}, done[NQ] = {};
         while (k.left > 0) {
-            const int end = chunk_end(k), taken = end - k.blk;
+            const int blk0 = k.blk(), end = k.end(), taken = end - blk0;
             const int nrows = k.t.n * a.G;
             const int live = NQ == 1 || k.t.row0 + 128 >= nrows ? 1 : NQ;
             const uint32_t u0 = units;
@@ -434,17 +543,17 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
                     mbar_wait(kv_full(slot), (u / NS) & 1);
                     tc_fence_after();
                 }
-                if (lane == 0) {
-                    const uint64_t qd = umma_desc_kmajor_sw128(base + q * Cfg::QB), kd = umma_desc_kmajor_sw128(kv0 + slot * Cfg::TILE);
-                    const uint32_t buf = SB == 1 ? 0 : (n & 1);
-#pragma unroll
-                    for (int i = 0; i < D / 16; ++i)
-                        umma_f16(tmem + (q * SB + buf) * BN, qd + (uint64_t)((i / 4) * (128 * 128 / 16) + 2 * (i % 4)),
-                                 kd + (uint64_t)((i / 4) * (BN * 128 / 16) + 2 * (i % 4)), id_s, i != 0);
-                    umma_commit(s_full(q, buf));
-                    if (q == live - 1) umma_commit(kv_empty(slot));
-                }
+                const uint32_t buf = SB == 1 ? 0 : (n & 1);
+                const uint32_t qd = warp_uniform((uint32_t)umma_desc_kmajor_sw128(base + q * Cfg::QB));
+                const uint32_t kd = warp_uniform((uint32_t)umma_desc_kmajor_sw128(kv0 + slot * Cfg::TILE));
+                const uint32_t dst = warp_uniform(tmem + (q * SB + buf) * BN);
                 __syncwarp();
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i)
+                    umma_f16_w(leader, dst, qd + (i / 4) * (128 * 128 / 16) + 2 * (i % 4), kd + (i / 4) * (BN * 128 / 16) + 2 * (i % 4),
+                               desc_hi, id_s, i != 0);
+                umma_commit_w(leader, s_full(q, buf));
+                if (q == live - 1) umma_commit_w(leader, kv_empty(slot));
             };
             auto product = [&](int q, int j) {  // O += P V
                 const uint32_t u = u0 + 2 * j + 1, slot = u % NS, n = done[q] + j;
@@ -453,7 +562,7 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
                     mbar_wait(kv_full(slot), (u / NS) & 1);
                     if (!Cfg::Q8) {
                         // slots that no row sees may hold anything: their values are taken as zero
-                        const int key0 = (k.t.kb0 + k.blk + j) * BN;
+                        const int key0 = (k.t.kb0 + blk0 + j) * BN;
                         const int z0 = min(BN, max(0, seen_lo - key0)), z1 = min(BN, max(0, k.t.len - key0));
                         if (z0 > 0 || z1 < BN) {
                             for (int x = lane; x < (z0 + BN - z1) * (D / 8); x += 32) {
@@ -467,16 +576,14 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
                 }
                 mbar_wait(p_full(q, buf), (n / SB) & 1);
                 tc_fence_after();
-                if (lane == 0) {
-                    const uint64_t vd = umma_desc_mnmajor_sw128(vt, BN * 128);
-#pragma unroll
-                    for (int i = 0; i < BN / 16; ++i)
-                        umma_f16_ta(tmem + Cfg::O_COL + q * D, tmem + (q * SB + buf) * BN + 8 * i, vd + (uint64_t)(i * (2048 / 16)), id_o,
-                                    j != 0 || i != 0);
-                    umma_commit(pv_done(q));
-                    if (q == live - 1) umma_commit(kv_empty(slot));
-                }
+                const uint32_t vd = warp_uniform((uint32_t)umma_desc_mnmajor_sw128(vt, BN * 128));
+                const uint32_t dst = warp_uniform(tmem + Cfg::O_COL + q * D), src = warp_uniform(tmem + (q * SB + buf) * BN);
                 __syncwarp();
+#pragma unroll
+                for (int i = 0; i < BN / 16; ++i)
+                    umma_f16_ta_w(leader, dst, src + 8 * i, vd + i * (2048 / 16), desc_hi, id_o, j != 0 || i != 0);
+                umma_commit_w(leader, pv_done(q, buf));
+                if (q == live - 1) umma_commit_w(leader, kv_empty(slot));
             };
             if constexpr (SB == 1) {
                 for (int q = 0; q < live; ++q) scores(q, 0);
@@ -496,22 +603,22 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
             for (int q = 0; q < NQ; ++q)
                 if (q < live) done[q] += taken;
             units += 2 * taken;
-            chunk_next(k, plan, a.Hk, taken);
+            chunk_next(k, plan, a.Hk);
         }
         if (lane == 0) {
             // complete already on the normal path; after a wait gave up, let products in flight end
 #pragma unroll
             for (int q = 0; q < NQ; ++q)
-                if (done[q]) mbar_drain(pv_done(q), (done[q] - 1) & 1, DRAIN_NS);
+                if (done[q]) mbar_drain(pv_done(q, (done[q] - 1) % SB), ((done[q] - 1) / SB) & 1, DRAIN_NS);
         }
         __syncwarp();
-    } else if constexpr (!Cfg::Q8) {
+        } else if (!Cfg::Q8 && warp == Cfg::MMA_WARP + 1) {
         // ------------------------------------------------------------ copies: lane = (box of slots, panel)
         const int boxes = BN / box_rows, box = lane / Cfg::NP, panel = lane % Cfg::NP;
         const bool on = box < boxes;
         while (k.left > 0) {
-            const int end = chunk_end(k), taken = end - k.blk;
-            for (int j = k.blk; j < end; ++j) {
+            const int blk0 = k.blk(), end = k.end();
+            for (int j = blk0; j < end; ++j) {
                 const int key = (k.t.kb0 + j) * BN + box * box_rows;
                 int page = a.bt.n_pages;  // out of range: zeros
                 if (on && key < k.t.len) {
@@ -529,40 +636,65 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
                                     key % a.bt.page, k.h, page, kv_full(slot));
                 }
             }
-            chunk_next(k, plan, a.Hk, taken);
+            chunk_next(k, plan, a.Hk);
         }
         if (lane == 0)
             for (uint32_t s = 0; s < NS && s < units; ++s)
                 mbar_drain(kv_full(s), ((units - 1 - s) / NS) & 1, DRAIN_NS);
         __syncwarp();
-    } else {
+        }
+    } else if constexpr (Cfg::Q8) {
         // ------------------------------------------------------------ 8-bit codes to fp16 tiles
-        const int ct = tid - (Cfg::MMA_WARP + 1) * 32;
+        // Thread ct converts the 16-code chunks i * 128 + ct of a tile.  A block of 16 slots is always in one
+        // page: lane b of each warp looks up block b, one tile ahead of the codes' loads, which are in
+        // flight while the tile before them is converted.
+        set_max_regs<Cfg::CONV_REGS >= Cfg::LAUNCH_REGS, Cfg::CONV_REGS>();
+        const int ct = tid - Cfg::CONV_WARP * 32;
         constexpr int PER = BN * D / 16 / 128;  // 16-code chunks per thread
         constexpr int CPR = D / 16;
         struct Raw {
             uint4 c[PER];
             uint16_t d[PER];
         };
+        struct Ahead {  // a tile to come
+            ChunkWalk w;
+            int j;       // slot tile
+            int page;    // lane b: page id of block b
+        };
+        auto lookup = [&](Ahead &t) {
+            t.page = -1;
+            const int key = (t.w.t.kb0 + t.j) * BN + 16 * lane;
+            if (t.w.left > 0 && lane < BN / 16 && key < t.w.t.len) t.page = a.bt.pages[t.w.t.b * a.bt.table_stride + key / a.bt.page];
+        };
+        auto step = [&](Ahead &t) {  // the tile after
+            if (t.w.left > 0 && ++t.j >= t.w.end()) {
+                chunk_next(t.w, plan, a.Hk);
+                t.j = t.w.blk();
+            }
+        };
         Raw kr, vr;
-        ChunkWalk nx = k;  // the tile to fetch next
-        int nj = k.blk;
-        auto fetch = [&](Raw &w, bool val) {  // codes and steps of the key (value) tile at (nx, nj)
-            if (nx.left <= 0) return;
-            const int seen_lo = a.window ? max(0, nx.t.len - nx.t.n + nx.t.row0 / a.G - a.window + 1) : 0;
+        Ahead cur{}, nxt{};  // the tile whose codes are loaded next, and the one whose pages are
+        int64_t at = 0, dat = 0;  // lane b: element offsets of block b of the codes and steps; at < 0: none
+        int key0 = 0, seen_lo = 0, len = 0;
+        auto locate = [&]() {  // offsets of the tile `cur`
+            const int key = (cur.w.t.kb0 + cur.j) * BN + 16 * lane, slot = key % a.bt.page;
+            const bool ok = cur.w.left > 0 && (unsigned)cur.page < (unsigned)a.bt.n_pages;
+            at = ok ? cur.page * a.page_stride + cur.w.h * a.head_stride + slot * a.slot_stride : -1;
+            dat = ok ? cur.page * a.step_stride + ((int64_t)cur.w.h * a.bt.page + slot) * (D / 32) : 0;
+            key0 = (cur.w.t.kb0 + cur.j) * BN;
+            seen_lo = a.window ? max(0, cur.w.t.len - cur.w.t.n + cur.w.t.row0 / a.G - a.window + 1) : 0;
+            len = cur.w.left > 0 ? cur.w.t.len : 0;
+        };
+        auto fetch = [&](Raw &w, const void *codes, const f16 *steps) {
 #pragma unroll
             for (int i = 0; i < PER; ++i) {
-                const int x = i * 128 + ct, row = x / CPR, ch = x % CPR, key = (nx.t.kb0 + nj) * BN + row;
+                const int x = i * 128 + ct, row = x / CPR, ch = x % CPR, key = key0 + row;
+                const int64_t o = __shfl_sync(0xffffffffu, at, row / 16), d = __shfl_sync(0xffffffffu, dat, row / 16);
                 w.c[i] = make_uint4(0u, 0u, 0u, 0u);
                 w.d[i] = 0;
-                if (key >= seen_lo && key < nx.t.len) {
-                    const int page = a.bt.pages[nx.t.b * a.bt.table_stride + key / a.bt.page], slot = key % a.bt.page;
-                    if ((unsigned)page < (unsigned)a.bt.n_pages) {
-                        w.c[i] = *reinterpret_cast<const uint4 *>(static_cast<const int8_t *>(val ? a.vc : a.kc) + page * a.page_stride +
-                                                                  nx.h * a.head_stride + slot * a.slot_stride + 16 * ch);
-                        w.d[i] = reinterpret_cast<const uint16_t *>(val ? a.vd : a.kd)[page * a.step_stride +
-                                                                                      ((int64_t)nx.h * a.bt.page + slot) * (D / 32) + ch / 2];
-                    }
+                if (o >= 0 && key >= seen_lo && key < len) {
+                    w.c[i] = *reinterpret_cast<const uint4 *>(static_cast<const int8_t *>(codes) + o + (row % 16) * a.slot_stride + 16 * ch);
+                    w.d[i] = reinterpret_cast<const uint16_t *>(steps)[d + (row % 16) * (D / 32) + ch / 2];
                 }
             }
         };
@@ -594,21 +726,24 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
             fence_proxy_async_smem();
             mbar_arrive(kv_full(slot));
         };
-        fetch(kr, false);
-        fetch(vr, true);
-        while (k.left > 0) {
-            const int end = chunk_end(k), taken = end - k.blk;
-            for (int j = k.blk; j < end; ++j) {
-                if (++nj >= chunk_end(nx)) {
-                    chunk_next(nx, plan, a.Hk, nj - nx.blk);
-                    nj = nx.blk;
-                }
-                put(kr);
-                fetch(kr, false);
-                put(vr);
-                fetch(vr, true);
-            }
-            chunk_next(k, plan, a.Hk, taken);
+        cur.w = k;
+        cur.j = k.blk();
+        lookup(cur);
+        locate();
+        nxt = cur;
+        step(nxt);
+        lookup(nxt);
+        fetch(kr, a.kc, a.kd);
+        fetch(vr, a.vc, a.vd);
+        while (cur.w.left > 0) {
+            cur = nxt;  // its pages have arrived
+            step(nxt);
+            lookup(nxt);
+            locate();
+            put(kr);
+            fetch(kr, a.kc, a.kd);
+            put(vr);
+            fetch(vr, a.vc, a.vd);
         }
     }
     tc_fence_before();
@@ -631,9 +766,9 @@ __global__ void __launch_bounds__(256) attn_chunk_join_kernel(const AttnArgs a, 
     if (bound >= ctas) return;
     const int64_t at = chunk_start(total, ctas, bound);
     const ChunkWalk k = chunk_find(plan, *plan.nrt, at);
-    if (k.blk == 0) return;
-    const int64_t s0 = at - k.blk, s1 = s0 + k.t.nt;
-    if (bound > 1 && chunk_start(total, ctas, bound - 1) > s0) return;  // an earlier boundary joins it
+    if (k.blk() == 0) return;
+    const int64_t s0 = at - k.u, s1 = s0 + CHUNK_OV + k.t.nt;  // the item's units
+    if (bound > 1 && chunk_start(total, ctas, bound - 1) > s0 + CHUNK_OV) return;  // an earlier boundary joins it
     const int lane = threadIdx.x & 31, r = blockIdx.y * 8 + (threadIdx.x >> 5), rr = k.t.row0 + r;
     if (rr >= k.t.n * a.G) return;
     auto part = [&](int c) {
@@ -695,7 +830,12 @@ static int chunk_run(const AttnArgs &in, const qg_paged &c, uint8_t *ws, int sms
     if (!Cfg::Q8 && (!attn_tensor_map(&km, c, c.k, box) || !attn_tensor_map(&vm, c, c.v, box))) return QG_ECUDA;
     if (!launch_programmatic(attn_plan_kernel, dim3(1), PLAN_THREADS, 0, s, a, plan, Cfg::ROWS, Cfg::BN, (int)tiles)) return QG_ECUDA;
     auto kern = attn_chunk_kernel<C, D>;
-    if (!allow_smem((const void *)kern, Cfg::BYTES)) return QG_ECUDA;
+    // the warpgroups trade registers out of exactly this allocation
+    static const bool regs_ok = [] {
+        cudaFuncAttributes fa;
+        return Cfg::WGS == 2 || (cudaFuncGetAttributes(&fa, (const void *)attn_chunk_kernel<C, D>) == cudaSuccess && fa.numRegs == Cfg::LAUNCH_REGS);
+    }();
+    if (!regs_ok || !allow_smem((const void *)kern, Cfg::BYTES)) return QG_ECUDA;
     if (!launch_programmatic(kern, dim3((unsigned)sms), Cfg::THREADS, Cfg::BYTES, s, a, plan, box, qsign, km, vm)) return QG_ECUDA;
     if (sms == 1) return QG_OK;
     auto join = attn_chunk_join_kernel<T, D>;

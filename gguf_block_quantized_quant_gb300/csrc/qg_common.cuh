@@ -201,6 +201,16 @@ __device__ __forceinline__ void fence_proxy_async_smem() {
 __device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void griddep_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
+// Registers per thread of the calling warpgroup (all its warps call): up (waits until others have
+// given theirs back) or down.
+template <bool UP, int N>
+__device__ __forceinline__ void set_max_regs() {
+    if constexpr (UP)
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+    else
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 // Barrier among the NCONS threads that reach it (every warp of the engine).
 template <int NCONS>
 __device__ __forceinline__ void consumer_sync() {
