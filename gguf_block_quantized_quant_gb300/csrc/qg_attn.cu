@@ -627,7 +627,7 @@ typedef CUresult (*PFN_encode_tiled)(CUtensorMap *, CUtensorMapDataType, cuuint3
                                      const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
                                      CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
-bool attn_tensor_map(CUtensorMap *map, const qg_paged &c, const void *base, int rows) {
+static PFN_encode_tiled encode_tiled() {
     static const PFN_encode_tiled encode = [] {
         void *f = nullptr;
         cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
@@ -638,6 +638,23 @@ bool attn_tensor_map(CUtensorMap *map, const qg_paged &c, const void *base, int 
         }
         return reinterpret_cast<PFN_encode_tiled>(f);
     }();
+    return encode;
+}
+
+bool attn_query_map(CUtensorMap *map, const AttnArgs &a, bool is_bf16, int D) {
+    const PFN_encode_tiled encode = encode_tiled();
+    if (!encode) return false;
+    const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)a.G, (cuuint64_t)a.Hk, (cuuint64_t)a.bt.tokens};
+    const cuuint64_t strides[3] = {(cuuint64_t)a.hdq * 2, (cuuint64_t)a.hdq * 2 * a.G, (cuuint64_t)a.ldq * 2};
+    const cuuint32_t box[4] = {64, (cuuint32_t)a.G, 1, (cuuint32_t)(128 / a.G)};
+    const cuuint32_t unit[4] = {1, 1, 1, 1};
+    return encode(map, is_bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, const_cast<void *>(a.q), dims, strides,
+                  box, unit, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool attn_tensor_map(CUtensorMap *map, const qg_paged &c, const void *base, int rows) {
+    const PFN_encode_tiled encode = encode_tiled();
     if (!encode) return false;
     const int es = c.type == QG_Q8_0 ? 1 : 2, row = c.dim * es;
     const cuuint64_t dims[4] = {(cuuint64_t)c.dim, (cuuint64_t)c.page, (cuuint64_t)c.kv_heads, (cuuint64_t)c.n_pages};

@@ -65,6 +65,10 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map
 // Host; false when the driver refuses.
 bool attn_tensor_map(CUtensorMap *map, const qg_paged &c, const void *base, int rows);
 
+// Tensor map of the queries for boxes of 128 rows x 128 bytes: the G heads of a cache head for
+// 128 / G tokens, in that order (128 % G == 0).
+bool attn_query_map(CUtensorMap *map, const AttnArgs &a, bool is_bf16, int D);
+
 // Four int8 codes of a word as fp16 pairs (exact): code + 128 goes under the exponent of 1024.
 __device__ __forceinline__ uint32_t codes_to_f16(uint32_t biased, uint32_t sel) {
     const uint32_t m = prmt(biased, 0x64646464u, sel);

@@ -7,14 +7,22 @@
 //   * producer: one warp copies the key and value tiles through the page table, a tiled TMA copy
 //     per page and 128-byte panel (pages end inside a tile); with 8-bit caches four warps fetch
 //     the codes instead and write step * code as fp16;
-//   * MMA warp: scores S = Q K^T (128 x BN, fp32 in tensor memory), then O += P V with P from
-//     tensor memory, where it takes the place of S;
+//   * MMA warp: scores S = Q K^T (128 x BN, fp32 in tensor memory), then O += P V;
 //   * a warpgroup per row tile: each thread owns one row, so its maximum and sum need no
 //     exchange; it reads S, writes P = 2^(S - m) and, where the maximum has grown by more than
 //     2^8, rescales O.  Up to there a stale maximum is as good: O and the sum carry the same
 //     factor and P stays below 2^8.
-// With two row tiles (dim 64, 128) one tile's exponentials run under the other's products; with one
-// (dim 256, whose O takes half the tensor memory) the scores of the next tile run under them.
+// What a row tile's warpgroup does for one slot tile (read S, maximum, exponentials, write P) takes
+// about as long as the tile's two products, so something else has to fill the tensor cores under
+// it.  With dim 64 and 128 that is the other row tile.  With dim 64 the next scores run under it
+// too: a score buffer is free as soon as its rows are in registers, as P has columns of its own.
+// With dim 256, whose O fills half the tensor memory and leaves room for one row tile, a second
+// score buffer takes them.  The value product starts on the first half of P while the second is
+// made.  Measured and dropped for dim 128: P in shared memory, which frees the score buffer early
+// but makes shared memory the bound (1.83 against 1.71 ms for 4096 tokens after 28000, 32/8
+// heads, bf16).  No product relies on the order of another that writes different columns: each
+// waits for the barrier of what it overwrites, and each row tile's products are issued by a warp of
+// their own.
 // P is rounded to the value's 16-bit type, the operand type of the product: one rounding of
 // relative size 2^-12 (2^-9) per factor on average beside that of the result.
 //
@@ -38,34 +46,48 @@ struct ChunkCfg {
     static constexpr bool Q8 = C == CACHE_Q8;
     static constexpr int NQ = D == 256 ? 1 : 2;  // row tiles
     static constexpr int SB = D == 256 ? 2 : 1;  // score buffers per row tile
-    static constexpr int BN = D == 256 ? 64 : 128;
+    static constexpr int BN = 128;
     static constexpr int ROWS = NQ * 128;
-    static constexpr int NS = D == 64 ? 6 : 4;   // key/value tiles in shared memory
     static constexpr int NP = D / 64;            // 128-byte panels of a row
+    // A slot tile's keys are copied in KU units of whole panels, its values in as many of whole rows
+    static constexpr int KU = D == 256 ? 2 : 1;
+    static constexpr int PKU = NP / KU;          // panels of a key unit
+    static constexpr int VR = BN / KU;           // rows of a value unit
+    static constexpr int NS = D == 64 ? 6 : 4;  // units in shared memory
     static constexpr uint32_t QB = 128 * D * 2;
-    static constexpr uint32_t TILE = BN * D * 2;
-    // Warpgroups: one per row tile, one whose first two warps issue the products and the copies, and
-    // one that converts 8-bit codes
+    static constexpr uint32_t TILE = BN * D * 2 / KU;
+    // P goes over the scores it came from, or beside them where tensor memory has room (dim 64)
+    static constexpr bool P_OVER = D != 64;
+    // Units come in the order of their use: keys of tile j + 1 before the values of tile j where a
+    // score buffer is free by then, else after them
+    static constexpr bool KEYS_AHEAD = !P_OVER || SB == 2;
+    // Warpgroups: one per row tile, one whose first warps issue each row tile's products and the copies,
+    // and those that convert 8-bit codes
     static constexpr int MMA_WARP = 4 * NQ;
     static constexpr int CONV_WARP = MMA_WARP + 4;
-    static constexpr int WGS = NQ + 1 + (Q8 ? 1 : 0);
+    static constexpr int NCONV = !Q8 ? 0 : D == 256 ? 2 : 1;  // unit u is converted by warpgroup u % NCONV
+    static constexpr int WGS = NQ + 1 + NCONV;
     static constexpr int THREADS = WGS * 128;
     // Registers per thread at launch, and where each kind of warpgroup goes from there (0: stays).
     // Their sums are the same, so every increase is met by a decrease.
     static constexpr int LAUNCH_REGS = WGS == 2 ? 255 : WGS == 3 ? 168 : 128;
-    static constexpr int ROW_REGS = WGS == 2 ? 0 : !Q8 ? 208 : NQ == 2 ? 152 : 216;
-    static constexpr int ISSUE_REGS = WGS == 2 ? 0 : !Q8 ? 88 : NQ == 2 ? 72 : 104;
-    static constexpr int CONV_REGS = !Q8 ? 0 : NQ == 2 ? 136 : 184;
-    static_assert(WGS == 2 || NQ * ROW_REGS + ISSUE_REGS + CONV_REGS == WGS * LAUNCH_REGS, "registers");
-    static constexpr bool HOLD = !Q8 || BN == 64;  // a row's scores fit a thread's registers
-    static constexpr int NBAR = 2 * NS + NQ + 3 * NQ * SB;
-    static constexpr uint32_t KV_AT = NQ * QB;
+    static constexpr int ROW_REGS = WGS == 2 ? 0 : !Q8 ? 208 : NQ == 2 ? 152 : 208;
+    static constexpr int ISSUE_REGS = WGS == 2 ? 0 : !Q8 ? 88 : NQ == 2 ? 72 : 64;
+    static constexpr int CONV_REGS = !Q8 ? 0 : NQ == 2 ? 136 : 120;
+    static_assert(WGS == 2 || NQ * ROW_REGS + ISSUE_REGS + NCONV * CONV_REGS == WGS * LAUNCH_REGS, "registers");
+    static constexpr bool HOLD = !Q8 || D == 256;  // a row's scores fit a thread's registers
+    static constexpr int NBAR = 2 * NS + 2 * NQ + 4 * NQ * SB + 1;
+    static constexpr uint32_t OUT_AT = NQ * QB;  // 32 rows x 128 bytes of results per warp
+    static constexpr uint32_t KV_AT = OUT_AT + NQ * 4 * 4096;
     static constexpr uint32_t BAR_AT = KV_AT + NS * TILE;
-    static constexpr uint32_t BYTES = BAR_AT + NBAR * 8 + 16 + 1024 /* alignment */;
+    static constexpr uint32_t PLACES_AT = (BAR_AT + NBAR * 8 + 4 /* tensor memory address */ + 15) / 16 * 16;
+    static constexpr uint32_t BYTES = PLACES_AT + NCONV * 4 * 256 + 1024 /* alignment */;
+    static_assert(OUT_AT % 1024 == 0 && KV_AT % 1024 == 0 && BAR_AT % 16 == 0 && TILE % 1024 == 0, "alignment");
     // tensor memory columns
     static constexpr int O_COL = NQ * SB * BN;
+    static constexpr int P_COL = O_COL + NQ * D;  // where P has columns of its own
     static constexpr int COLS = 512;
-    static_assert(O_COL + NQ * D <= COLS, "tensor memory");
+    static_assert(P_COL + (P_OVER ? 0 : NQ * BN / 2) <= COLS, "tensor memory");
 };
 
 // ----------------------------------------------------------------------------- plan
@@ -244,11 +266,11 @@ __device__ __forceinline__ int fast_div(int x, int d, uint32_t m, int &rem) {
 // ----------------------------------------------------------------------------- kernel
 template <int C, int D>
 __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
-    attn_chunk_kernel(const AttnArgs a, const ChunkPlan plan, int box_rows, uint32_t qsign, const __grid_constant__ CUtensorMap kmap,
-                      const __grid_constant__ CUtensorMap vmap) {
+    attn_chunk_kernel(const AttnArgs a, const ChunkPlan plan, int box_rows, uint32_t qsign, int qcopy, const __grid_constant__ CUtensorMap kmap,
+                      const __grid_constant__ CUtensorMap vmap, const __grid_constant__ CUtensorMap qmap) {
     using Cfg = ChunkCfg<C, D>;
     using T = typename CacheT<C>::Q;
-    constexpr int NQ = Cfg::NQ, SB = Cfg::SB, BN = Cfg::BN, NS = Cfg::NS;
+    constexpr int NQ = Cfg::NQ, SB = Cfg::SB, BN = Cfg::BN, NS = Cfg::NS, KU = Cfg::KU, VR = Cfg::VR;
     constexpr bool BF = C == CACHE_BF16;
     extern __shared__ __align__(16) uint8_t ck_smem[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -259,22 +281,27 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
     auto q_full = [&](int q) { return bars + 8u * (2 * NS + q); };
     auto s_full = [&](int q, int b) { return bars + 8u * (2 * NS + NQ + q * SB + b); };
     auto p_full = [&](int q, int b) { return bars + 8u * (2 * NS + NQ + NQ * SB + q * SB + b); };
-    // tile n of a row tile uses score buffer n % SB, and its value product that one's barrier: a full
-    // score buffer says that the product SB tiles back is complete, so a wait for product n or n - 1
-    // finds its barrier at most one phase away and the parity is unambiguous
+    // tile n of a row tile uses score buffer n % SB, and its value product that one's barrier.  Before
+    // anyone waits for product n, product n - SB was waited for (for P's place, or by the scores that
+    // took its buffer), so the barrier is at most one phase away and the parity is unambiguous
     auto pv_done = [&](int q, int b) { return bars + 8u * (2 * NS + NQ + 2 * NQ * SB + q * SB + b); };
-    const uint32_t taddr_slot = bars + 8u * Cfg::NBAR;
+    auto p_half = [&](int q, int b) { return bars + 8u * (2 * NS + NQ + 3 * NQ * SB + q * SB + b); };
+    auto s_empty = [&](int q) { return bars + 8u * (2 * NS + NQ + 4 * NQ * SB + q); };
+    const uint32_t v_raw = bars + 8u * (Cfg::NBAR - 1), taddr_slot = bars + 8u * Cfg::NBAR;
 
     if (tid == 0) {
         for (int s = 0; s < NS; ++s) {
             mbar_init(kv_full(s), Cfg::Q8 ? 128 : 1);
-            mbar_init(kv_empty(s), 1);
+            mbar_init(kv_empty(s), NQ);
         }
+        mbar_init(v_raw, 1);
         for (int q = 0; q < NQ; ++q) {
-            mbar_init(q_full(q), 128);
+            mbar_init(q_full(q), qcopy ? 1 : 128);
+            mbar_init(s_empty(q), 128);
             for (int b = 0; b < SB; ++b) {
                 mbar_init(pv_done(q, b), 1);
                 mbar_init(s_full(q, b), 1);
+                mbar_init(p_half(q, b), 128);
                 mbar_init(p_full(q, b), 128);
             }
         }
@@ -309,21 +336,41 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
         const uint32_t qtile = base + q * Cfg::QB;
         const uint32_t mG = (uint32_t)((0x100000000ull + a.G - 1) / a.G);
         constexpr int CPR = D / 8;  // 16-byte chunks of a row
-        uint4 qv[CPR];              // the warp's 32 rows, 32 chunks a step
-        // chunk ch of a row, in the products' operand layout; a warp touches its own rows only
-        auto qat = [&](int row, int ch) { return qtile + (ch >> 3) * (128 * 128) + row * 128 + (((ch & 7) ^ (row & 7)) << 4); };
+        // Queries come as tiled copies where the G heads of whole tokens make 128 rows, else (and with a
+        // negative scale) through registers; either way into the products' operand layout
         auto fetch_q = [&](const ChunkWalk &w) {
+            if (!qcopy) return;
+            if (r == 0 && w.t.row0 + 128 * q < w.t.n * a.G) {
+                mbar_arrive_expect_tx(q_full(q), Cfg::QB);
+#pragma unroll
+                for (int p = 0; p < Cfg::NP; ++p)
+                    tma_load_4d(qtile + p * (128 * 128), &qmap, 64 * p, 0, w.h, w.t.first + (w.t.row0 + 128 * q) / a.G, q_full(q));
+            }
+        };
+        auto load_q = [&](const ChunkWalk &w) {
             const int nrows = w.t.n * a.G, row0 = w.t.row0 + 128 * q;
 #pragma unroll
-            for (int i = 0; i < CPR; ++i) {
-                const int x = i * 32 + lane, rr = row0 + wr + x / CPR;
-                int g;
-                const int t = fast_div(rr, a.G, mG, g);
-                qv[i] = make_uint4(0u, 0u, 0u, 0u);
-                if (rr < nrows)
-                    qv[i] = *reinterpret_cast<const uint4 *>(static_cast<const T *>(a.q) + (int64_t)(w.t.first + t) * a.ldq +
-                                                             (int64_t)(w.h * a.G + g) * a.hdq + 8 * (x % CPR));
+            for (int i0 = 0; i0 < CPR; i0 += 8) {
+                uint4 v[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int x = (i0 + i) * 32 + lane, rr = row0 + wr + x / CPR;
+                    int g;
+                    const int t = fast_div(rr, a.G, mG, g);
+                    v[i] = make_uint4(0u, 0u, 0u, 0u);
+                    if (rr < nrows)
+                        v[i] = *reinterpret_cast<const uint4 *>(static_cast<const T *>(a.q) + (int64_t)(w.t.first + t) * a.ldq +
+                                                                (int64_t)(w.h * a.G + g) * a.hdq + 8 * (x % CPR));
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int x = (i0 + i) * 32 + lane, row = wr + x / CPR, ch = x % CPR;
+                    sts128(qtile + (ch >> 3) * (128 * 128) + row * 128 + (((ch & 7) ^ (row & 7)) << 4), v[i].x ^ qsign, v[i].y ^ qsign,
+                           v[i].z ^ qsign, v[i].w ^ qsign);
+                }
             }
+            fence_proxy_async_smem();
+            mbar_arrive(q_full(q));
         };
         uint32_t done = 0;  // slot tiles of this row tile so far
         if (k.left > 0) fetch_q(k);
@@ -333,16 +380,7 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
             ChunkWalk nk = k;
             chunk_next(nk, plan, a.Hk);
             if (row0 < nrows) {
-                // ---- the queries into shared memory (the products that read the last ones are complete)
-#pragma unroll
-                for (int i = 0; i < CPR; ++i) {
-                    const int x = i * 32 + lane, row = wr + x / CPR, ch = x % CPR;
-                    sts128(qat(row, ch), qv[i].x ^ qsign, qv[i].y ^ qsign,
-                           qv[i].z ^ qsign, qv[i].w ^ qsign);
-                }
-                fence_proxy_async_smem();
-                mbar_arrive(q_full(q));
-
+                if (!qcopy) load_q(k);  // the products that read the last ones are complete
                 const int rr = row0 + r, pos0 = k.t.len - k.t.n;
                 int g;
                 const int pos = pos0 + fast_div(rr, a.G, mG, g);
@@ -358,14 +396,17 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
                     const bool edge = key0 + BN - 1 > hi_min || key0 < lo_max;
                     mbar_wait(s_full(q, buf), (done / SB) & 1);
                     tc_fence_after();
+                    if (j + 1 == end && nk.left > 0) fetch_q(nk);  // no product reads this item's queries any more
                     // All scores of the row in registers (HOLD), or 32 at a time in two passes where the
                     // converting warps leave too few registers
                     uint32_t s[Cfg::HOLD ? BN / 32 : 2][32];
                     auto mask = [&](uint32_t (&v)[32], int c0) {
                         if (edge) {
+                            const int up = c_hi - c0, down = c_lo - c0;  // visible: down .. up
+                            const uint32_t see = (up < 0 ? 0u : 0xffffffffu >> (31 - min(up, 31))) & (down > 31 ? 0u : 0xffffffffu << max(down, 0));
 #pragma unroll
                             for (int i = 0; i < 32; ++i)
-                                if (c0 + i > c_hi || c0 + i < c_lo) v[i] = 0xff800000u;  // -inf
+                                if (!(see >> i & 1u)) v[i] = 0xff800000u;  // -inf
                         }
                     };
                     auto top = [&](const uint32_t (&v)[32]) {
@@ -382,6 +423,10 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
                         tmem_wait_ld(s[0]);
 #pragma unroll
                         for (int c = 1; c < BN / 32; ++c) tmem_loaded(s[c]);
+                        if (!Cfg::P_OVER) {
+                            tc_fence_before();
+                            mbar_arrive(s_empty(q));
+                        }
 #pragma unroll
                         for (int c = 0; c < BN / 32; ++c) {
                             mask(s[c], 32 * c);
@@ -398,6 +443,10 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
                         }
                         tmem_ld32(scol, s[0]);
                     }
+                    if (!Cfg::P_OVER && done > 0) {  // P's place is free again
+                        mbar_wait(pv_done(q, 0), (done - 1) & 1);
+                        tc_fence_after();
+                    }
                     // ---- rescale where some row of the warp needs it (the first tile starts O afresh)
                     if (j == blk0) {
                         m = mx;
@@ -407,8 +456,10 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
                             const float mn = fmaxf(m, mx), f = mn > m ? exp2_approx((m - mn) * a.scale2) : 1.0f;
                             m = mn;
                             l *= f;
-                            mbar_wait(pv_done(q, (done - 1) % SB), ((done - 1) / SB) & 1);
-                            tc_fence_after();
+                            if (Cfg::P_OVER) {
+                                mbar_wait(pv_done(q, (done - 1) % SB), ((done - 1) / SB) & 1);
+                                tc_fence_after();
+                            }
 #pragma unroll 1
                             for (int c = 0; c < D; c += 16) {
                                 uint32_t o[16];
@@ -421,7 +472,7 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
                         }
                     }
                     const float mz = (m == -INFINITY ? 0.0f : m) * a.scale2;
-                    // ---- P over S: chunk c of 32 scores becomes columns 16 c .. 16 c + 15, which were read before
+                    // ---- P: chunk c of 32 scores becomes columns (words of a row) 16 c .. 16 c + 15
                     const uint64_t sc2 = pack_f32x2(a.scale2, a.scale2), mz2 = pack_f32x2(-mz, -mz);
                     uint64_t sum[2] = {0ull, 0ull};
 #pragma unroll
@@ -429,7 +480,12 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
                         uint32_t(&v)[32] = s[Cfg::HOLD ? c : c & 1];
                         if constexpr (!Cfg::HOLD) {
                             tmem_wait_ld(v);
-                            if (c + 1 < BN / 32) tmem_ld32(scol + 32 * (c + 1), s[(c + 1) & 1]);
+                            if (c + 1 < BN / 32) {
+                                tmem_ld32(scol + 32 * (c + 1), s[(c + 1) & 1]);
+                            } else if (!Cfg::P_OVER) {
+                                tc_fence_before();
+                                mbar_arrive(s_empty(q));
+                            }
                             mask(v, 32 * c);
                         }
                         uint32_t p[16];
@@ -443,7 +499,12 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
                             sum[i & 1] = add_f32x2(sum[i & 1], pack_f32x2(x0, x1));
                             p[i] = pack2<T>(x0, x1);
                         }
-                        tmem_st16(scol + 16 * c, p);
+                        tmem_st16((Cfg::P_OVER ? scol : lanes + Cfg::P_COL + q * (BN / 2)) + 16 * c, p);
+                        if (c == BN / 64 - 1) {
+                            tmem_wait_st();
+                            tc_fence_before();
+                            mbar_arrive(p_half(q, buf));
+                        }
                     }
                     float l0, l1, l2, l3;
                     unpack_f32x2(sum[0], l0, l1);
@@ -453,7 +514,6 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
                     tc_fence_before();
                     mbar_arrive(p_full(q, buf));
                 }
-                if (nk.left > 0) fetch_q(nk);  // the next item's queries come in under the last product
                 // ---- result
                 mbar_wait(pv_done(q, (done - 1) % SB), ((done - 1) / SB) & 1);
                 tc_fence_after();
@@ -467,46 +527,49 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
                     else if (a.lse)
                         a.lse[(int64_t)(k.t.first + pos - pos0) * a.Hq + k.h * a.G + g] = ls * LN2;
                 }
-                // Through the queries' place in shared memory, so that a warp writes whole rows: D 16-bit
-                // values of a row, or D / 2 fp32 values in each of two rounds
+                // 32 columns at a time through the warp's own shared memory, so that it writes whole sectors
                 const bool wide = !whole || a.out_f32;
-                for (int half = 0; half < (wide ? 2 : 1); ++half) {
+                const uint32_t st = base + Cfg::OUT_AT + warp * 4096;
+                const int per = wide ? 8 : 4;              // 16-byte chunks of a row's 32 columns
+                const int sub = lane / per, ch = lane % per, rows = 32 / per;
+                uint8_t *dst[8];                           // where the lane's rows go
 #pragma unroll
-                    for (int c = 0; c < D; c += 32) {
-                        if (wide && c / (D / 2) != half) continue;
-                        uint32_t o[32];
-                        tmem_ld32(ocol + c, o);
-                        tmem_wait_ld(o);
+                for (int i = 0; i < 8; ++i) {
+                    const int row = wr + i * rows + sub, orr = row0 + row;
+                    int og;
+                    const int ot = fast_div(min(orr, nrows - 1), a.G, mG, og);
+                    const int64_t orow = (int64_t)(k.t.first + ot) * a.Hq + k.h * a.G + og;
+                    dst[i] = orr >= nrows || i >= per ? nullptr
+                             : !whole ? reinterpret_cast<uint8_t *>(part + (size_t)(128 * q + row) * D)
+                                      : static_cast<uint8_t *>(a.out) + orow * (wide ? D * 4 : D * 2);
+                }
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * inv);
-                        if (wide) {
-                            const int c0 = (c - half * (D / 2)) / 4;
+                for (int c = 0; c < D; c += 32) {
+                    uint32_t o[32];
+                    tmem_ld32(ocol + c, o);
+                    tmem_wait_ld(o);
 #pragma unroll
-                            for (int i = 0; i < 8; ++i)
-                                sts128(qat(r, c0 + i), o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-                        } else {
-                            uint32_t h[16];
+                    for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * inv);
+                    if (wide) {
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) h[i] = pack2<T>(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1]));
+                        for (int i = 0; i < 8; ++i)
+                            sts128(st + lane * 128 + ((i ^ (lane & 7)) << 4), o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                    } else {
 #pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                sts128(qat(r, c / 8 + i), h[4 * i], h[4 * i + 1], h[4 * i + 2], h[4 * i + 3]);
-                        }
+                        for (int i = 0; i < 4; ++i)
+                            sts128(st + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4), pack2<T>(__uint_as_float(o[8 * i]), __uint_as_float(o[8 * i + 1])),
+                                   pack2<T>(__uint_as_float(o[8 * i + 2]), __uint_as_float(o[8 * i + 3])),
+                                   pack2<T>(__uint_as_float(o[8 * i + 4]), __uint_as_float(o[8 * i + 5])),
+                                   pack2<T>(__uint_as_float(o[8 * i + 6]), __uint_as_float(o[8 * i + 7])));
                     }
                     __syncwarp();
-#pragma unroll 4
-                    for (int i = 0; i < CPR; ++i) {
-                        const int x = i * 32 + lane, row = wr + x / CPR, ch = x % CPR, orr = row0 + row;
-                        if (orr < nrows) {
-                            const uint4 v = lds128(qat(row, ch));
-                            int og;
-                            const int ot = fast_div(orr, a.G, mG, og);
-                            const int64_t orow = (int64_t)(k.t.first + ot) * a.Hq + k.h * a.G + og;
-                            uint8_t *dst = !whole ? reinterpret_cast<uint8_t *>(part + (size_t)(128 * q + row) * D) + half * (D * 2)
-                                                  : static_cast<uint8_t *>(a.out) + (wide ? orow * (D * 4) + half * (D * 2) : orow * (D * 2));
-                            *reinterpret_cast<uint4 *>(dst + 16 * ch) = v;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        if (dst[i]) {
+                            const int row = i * rows + sub;
+                            *reinterpret_cast<uint4 *>(dst[i] + (wide ? 4 * c : 2 * c) + 16 * ch) =
+                                lds128(wide ? st + row * 128 + ((ch ^ (row & 7)) << 4) : st + row * 64 + ((ch ^ ((row >> 1) & 3)) << 4));
                         }
-                    }
                     __syncwarp();
                 }
                 tc_fence_before();  // the next item's products overwrite O once its P arrives
@@ -517,123 +580,165 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
         }
     } else if (warp < Cfg::CONV_WARP) {
         if constexpr (Cfg::ISSUE_REGS > 0) set_max_regs<false, Cfg::ISSUE_REGS>();
-        if (warp == Cfg::MMA_WARP) {
-        // ------------------------------------------------------------ products
+        if (warp < Cfg::MMA_WARP + NQ) {
+        // ------------------------------------------------------------ products: a warp per row tile
         constexpr uint32_t id_s = umma_idesc_16(128, BN, BF, false), id_o = umma_idesc_16(128, D, BF, true);
         constexpr uint32_t desc_hi = (uint32_t)(umma_desc_kmajor_sw128(0) >> 32);
-        static_assert(desc_hi == (uint32_t)(umma_desc_mnmajor_sw128(0, BN * 128) >> 32), "one upper word");
+        static_assert(desc_hi == (uint32_t)(umma_desc_mnmajor_sw128(0, VR * 128) >> 32), "one upper word");
         const uint32_t leader = lane == 0;
-        uint32_t items[NQ] = {}, done[NQ] = {};
-        while (k.left > 0) {
-            const int blk0 = k.blk(), end = k.end(), taken = end - blk0;
-            const int nrows = k.t.n * a.G;
-            const int live = NQ == 1 || k.t.row0 + 128 >= nrows ? 1 : NQ;
-            const uint32_t u0 = units;
-            const int seen_lo = a.window ? max(0, k.t.len - k.t.n + k.t.row0 / a.G - a.window + 1) : 0;
+        const int q = NQ == 1 ? 0 : (int)warp_uniform((uint32_t)(warp - Cfg::MMA_WARP));
+        const uint32_t s_col = warp_uniform(tmem + q * SB * BN), o_col = warp_uniform(tmem + Cfg::O_COL + q * D);
+        const uint32_t p_col = warp_uniform(Cfg::P_OVER ? tmem + q * SB * BN : tmem + Cfg::P_COL + q * (BN / 2));
+        const uint32_t q_desc = warp_uniform((uint32_t)umma_desc_kmajor_sw128(base + q * Cfg::QB));
+        uint32_t items = 0, n = 0;  // items; slot tiles of this row tile before j of the segment
+        auto scores = [&](uint32_t t) {  // S = Q K^T of this row tile's slot tile t, whose keys are the next units
+            const uint32_t buf = t % SB;
+            if (t >= SB) {  // the buffer's last scores have been read, and P that took their place
+                if (Cfg::P_OVER)
+                    mbar_wait(pv_done(q, buf), (t / SB - 1) & 1);
+                else
+                    mbar_wait(s_empty(q), (t - 1) & 1);
+            }
+            const uint32_t dst = warp_uniform(s_col + buf * BN);
 #pragma unroll
-            for (int q = 0; q < NQ; ++q)
-                if (q < live) {
-                    mbar_wait(q_full(q), items[q] & 1);
-                    ++items[q];
-                }
-            tc_fence_after();
-            auto scores = [&](int q, int j) {  // S = Q K^T of slot tile j of the segment
-                const uint32_t u = u0 + 2 * j, slot = u % NS, n = done[q] + j;
-                if (q == 0) {
-                    mbar_wait(kv_full(slot), (u / NS) & 1);
-                    tc_fence_after();
-                }
-                const uint32_t buf = SB == 1 ? 0 : (n & 1);
-                const uint32_t qd = warp_uniform((uint32_t)umma_desc_kmajor_sw128(base + q * Cfg::QB));
-                const uint32_t kd = warp_uniform((uint32_t)umma_desc_kmajor_sw128(kv0 + slot * Cfg::TILE));
-                const uint32_t dst = warp_uniform(tmem + (q * SB + buf) * BN);
-                __syncwarp();
-#pragma unroll
-                for (int i = 0; i < D / 16; ++i)
-                    umma_f16_w(leader, dst, qd + (i / 4) * (128 * 128 / 16) + 2 * (i % 4), kd + (i / 4) * (BN * 128 / 16) + 2 * (i % 4),
-                               desc_hi, id_s, i != 0);
-                umma_commit_w(leader, s_full(q, buf));
-                if (q == live - 1) umma_commit_w(leader, kv_empty(slot));
-            };
-            auto product = [&](int q, int j) {  // O += P V
-                const uint32_t u = u0 + 2 * j + 1, slot = u % NS, n = done[q] + j;
-                const uint32_t buf = SB == 1 ? 0 : (n & 1), vt = kv0 + slot * Cfg::TILE;
-                if (q == 0) {
-                    mbar_wait(kv_full(slot), (u / NS) & 1);
-                    if (!Cfg::Q8) {
-                        // slots that no row sees may hold anything: their values are taken as zero
-                        const int key0 = (k.t.kb0 + blk0 + j) * BN;
-                        const int z0 = min(BN, max(0, seen_lo - key0)), z1 = min(BN, max(0, k.t.len - key0));
-                        if (z0 > 0 || z1 < BN) {
-                            for (int x = lane; x < (z0 + BN - z1) * (D / 8); x += 32) {
-                                const int row = x / (D / 8), ch = x % (D / 8);
-                                sts128(vt + (ch >> 3) * (BN * 128) + (row < z0 ? row : row - z0 + z1) * 128 + (ch & 7) * 16, 0u, 0u, 0u, 0u);
-                            }
-                            fence_proxy_async_smem();
-                            __syncwarp();
-                        }
-                    }
-                }
-                mbar_wait(p_full(q, buf), (n / SB) & 1);
+            for (int h = 0; h < KU; ++h, ++units) {
+                const uint32_t slot = units % NS;
+                mbar_wait(kv_full(slot), (units / NS) & 1);
                 tc_fence_after();
-                const uint32_t vd = warp_uniform((uint32_t)umma_desc_mnmajor_sw128(vt, BN * 128));
-                const uint32_t dst = warp_uniform(tmem + Cfg::O_COL + q * D), src = warp_uniform(tmem + (q * SB + buf) * BN);
+                const uint32_t kd = warp_uniform((uint32_t)umma_desc_kmajor_sw128(kv0 + slot * Cfg::TILE));
+                const uint32_t qd = q_desc + h * Cfg::PKU * (128 * 128 / 16);
                 __syncwarp();
 #pragma unroll
-                for (int i = 0; i < BN / 16; ++i)
-                    umma_f16_ta_w(leader, dst, src + 8 * i, vd + i * (2048 / 16), desc_hi, id_o, j != 0 || i != 0);
-                umma_commit_w(leader, pv_done(q, buf));
-                if (q == live - 1) umma_commit_w(leader, kv_empty(slot));
-            };
-            if constexpr (SB == 1) {
-                for (int q = 0; q < live; ++q) scores(q, 0);
-                for (int j = 0; j < taken; ++j)
-                    for (int q = 0; q < live; ++q) {
-                        product(q, j);
-                        if (j + 1 < taken) scores(q, j + 1);
+                for (int i = 0; i < 4 * Cfg::PKU; ++i)
+                    umma_f16_w(leader, dst, qd + (i / 4) * (128 * 128 / 16) + 2 * (i % 4), kd + (i / 4) * (BN * 128 / 16) + 2 * (i % 4),
+                               desc_hi, id_s, (h | i) != 0);
+                if (h == KU - 1) umma_commit_w(leader, s_full(q, buf));
+                umma_commit_w(leader, kv_empty(slot));
+            }
+        };
+        auto product = [&](uint32_t t, bool fresh) {  // O (+)= P V of slot tile t, whose values are the next units
+            const uint32_t buf = t % SB, src = warp_uniform(p_col + (Cfg::P_OVER ? buf * BN : 0));
+#pragma unroll
+            for (int h = 0; h < KU; ++h, ++units) {
+                const uint32_t slot = units % NS;
+                mbar_wait(kv_full(slot), (units / NS) & 1);
+                const uint32_t vd = warp_uniform((uint32_t)umma_desc_mnmajor_sw128(kv0 + slot * Cfg::TILE, VR * 128));
+#pragma unroll
+                for (int i = 0; i < VR / 16; ++i) {
+                    const int p = h * (VR / 16) + i;  // 16 slots of P
+                    if (p == 0 || p == BN / 32) {
+                        mbar_wait(p ? p_full(q, buf) : p_half(q, buf), (t / SB) & 1);
+                        tc_fence_after();
+                        __syncwarp();
                     }
-            } else {
-                scores(0, 0);
+                    umma_f16_ta_w(leader, o_col, src + 8 * p, vd + i * (2048 / 16), desc_hi, id_o, p ? 1u : !fresh);
+                }
+                if (h == KU - 1) umma_commit_w(leader, pv_done(q, buf));
+                umma_commit_w(leader, kv_empty(slot));
+            }
+        };
+        while (k.left > 0) {
+            const int taken = k.end() - k.blk();
+            if (q == 0 || k.t.row0 + 128 < k.t.n * a.G) {
+                mbar_wait(q_full(q), items & 1);
+                ++items;
+                scores(n);
                 for (int j = 0; j < taken; ++j) {
-                    if (j + 1 < taken) scores(0, j + 1);
-                    product(0, j);
+                    if (Cfg::KEYS_AHEAD && j + 1 < taken) scores(n + j + 1);
+                    product(n + j, j == 0);
+                    if (!Cfg::KEYS_AHEAD && j + 1 < taken) scores(n + j + 1);
+                }
+                n += taken;
+            } else {  // no rows in this tile: its share of every unit's release
+                for (int j = 0; j < 2 * KU * taken; ++j, ++units) {
+                    mbar_wait(kv_full(units % NS), (units / NS) & 1);
+                    if (lane == 0) mbar_arrive(kv_empty(units % NS));
                 }
             }
-#pragma unroll
-            for (int q = 0; q < NQ; ++q)
-                if (q < live) done[q] += taken;
-            units += 2 * taken;
             chunk_next(k, plan, a.Hk);
         }
-        if (lane == 0) {
-            // complete already on the normal path; after a wait gave up, let products in flight end
-#pragma unroll
-            for (int q = 0; q < NQ; ++q)
-                if (done[q]) mbar_drain(pv_done(q, (done[q] - 1) % SB), ((done[q] - 1) / SB) & 1, DRAIN_NS);
-        }
+        // complete already on the normal path; after a wait gave up, let products in flight end
+        if (lane == 0 && n) mbar_drain(pv_done(q, (n - 1) % SB), ((n - 1) / SB) & 1, DRAIN_NS);
         __syncwarp();
-        } else if (!Cfg::Q8 && warp == Cfg::MMA_WARP + 1) {
-        // ------------------------------------------------------------ copies: lane = (box of slots, panel)
-        const int boxes = BN / box_rows, box = lane / Cfg::NP, panel = lane % Cfg::NP;
-        const bool on = box < boxes;
+        } else if (!Cfg::Q8 && warp == Cfg::MMA_WARP + NQ) {
+        // ------------------------------------------------------------ copies
+        // A unit is one box per page part and panel, each issued by a lane of its own.  Lane b looks up the
+        // page of the tile's slots 16 b .. one tile ahead.
+        struct Place {
+            int page, slot;
+        };
+        auto lookup = [&](const ChunkWalk &w, int j) {
+            Place p{a.bt.n_pages, 0};  // out of range: zeros
+            const int key = (w.t.kb0 + j) * BN + 16 * lane;
+            if (w.left > 0 && lane < BN / 16 && key < w.t.len) {
+                p.page = a.bt.pages[w.t.b * a.bt.table_stride + key / a.bt.page];
+                p.slot = key % a.bt.page;
+            }
+            return p;
+        };
+        uint32_t raws = 0;
+        auto copy = [&](const Place &p, int h, int head, bool val, int tile) {
+            const uint32_t slot = units % NS;
+            // Slots that no row sees may hold anything, and 0 * NaN is not 0: their values become zeros before
+            // the unit counts as full
+            int z0 = 0, z1 = VR;
+            if (val) {
+                const int key0 = (k.t.kb0 + tile) * BN + h * VR;
+                const int seen_lo = a.window ? max(0, k.t.len - k.t.n + k.t.row0 / a.G - a.window + 1) : 0;
+                z0 = min(VR, max(0, seen_lo - key0)), z1 = min(VR, max(0, k.t.len - key0));
+            }
+            const bool mend = z0 > 0 || z1 < VR;
+            const uint32_t bar = mend ? v_raw : kv_full(slot);
+            const int panels = val ? Cfg::NP : Cfg::PKU, rows = val ? VR : BN;
+            const int box = lane / panels, panel = lane % panels;
+            const int from = (val ? h * VR : 0) + box * box_rows;  // the box's first slot in the tile
+            int page = __shfl_sync(0xffffffffu, p.page, (from / 16) & 31);
+            const int s0 = __shfl_sync(0xffffffffu, p.slot, (from / 16) & 31);
+            if ((unsigned)page >= (unsigned)a.bt.n_pages) page = a.bt.n_pages;
+            if (units >= NS) mbar_wait(kv_empty(slot), (units / NS - 1) & 1);
+            if (lane == 0) mbar_arrive_expect_tx(bar, Cfg::TILE);
+            __syncwarp();
+            if (box < rows / box_rows)
+                tma_load_4d(kv0 + slot * Cfg::TILE + panel * (rows * 128) + box * box_rows * 128, val ? &vmap : &kmap,
+                            64 * ((val ? 0 : h * Cfg::PKU) + panel), s0, head, page, bar);
+            if (mend) {
+                mbar_wait(v_raw, raws++ & 1);
+                for (int x = lane; x < (z0 + VR - z1) * (D / 8); x += 32) {
+                    const int row = x / (D / 8), ch = x % (D / 8);
+                    sts128(kv0 + slot * Cfg::TILE + (ch >> 3) * (VR * 128) + (row < z0 ? row : row - z0 + z1) * 128 + (ch & 7) * 16, 0u, 0u, 0u, 0u);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(kv_full(slot));
+            }
+            ++units;
+        };
+        ChunkWalk nx = k;  // the tile whose pages are looked up
+        int nj = k.blk();
+        auto ahead = [&]() {
+            if (nx.left > 0 && ++nj >= nx.end()) {
+                chunk_next(nx, plan, a.Hk);
+                nj = nx.blk();
+            }
+            return lookup(nx, nj);
+        };
+        Place cur = lookup(nx, nj), next = ahead();
         while (k.left > 0) {
             const int blk0 = k.blk(), end = k.end();
-            for (int j = blk0; j < end; ++j) {
-                const int key = (k.t.kb0 + j) * BN + box * box_rows;
-                int page = a.bt.n_pages;  // out of range: zeros
-                if (on && key < k.t.len) {
-                    page = a.bt.pages[k.t.b * a.bt.table_stride + key / a.bt.page];
-                    if ((unsigned)page >= (unsigned)a.bt.n_pages) page = a.bt.n_pages;
-                }
 #pragma unroll
-                for (int v = 0; v < 2; ++v, ++units) {
-                    const uint32_t slot = units % NS;
-                    if (units >= NS) mbar_wait(kv_empty(slot), (units / NS - 1) & 1);
-                    if (lane == 0) mbar_arrive_expect_tx(kv_full(slot), Cfg::TILE);
-                    __syncwarp();
-                    if (on)
-                        tma_load_4d(kv0 + slot * Cfg::TILE + panel * (BN * 128) + box * box_rows * 128, v ? &vmap : &kmap, 64 * panel,
-                                    key % a.bt.page, k.h, page, kv_full(slot));
+            for (int h = 0; h < KU; ++h) copy(cur, h, k.h, false, 0);
+            for (int j = blk0; j < end; ++j) {
+                const Place prev = cur;
+                cur = next;
+                next = ahead();
+                if (!Cfg::KEYS_AHEAD) copy(prev, 0, k.h, true, j);
+                if (j + 1 < end) {
+#pragma unroll
+                    for (int h = 0; h < KU; ++h) copy(cur, h, k.h, false, 0);
+                }
+                if (Cfg::KEYS_AHEAD) {
+#pragma unroll
+                    for (int h = 0; h < KU; ++h) copy(prev, h, k.h, true, j);
                 }
             }
             chunk_next(k, plan, a.Hk);
@@ -645,66 +750,125 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
         }
     } else if constexpr (Cfg::Q8) {
         // ------------------------------------------------------------ 8-bit codes to fp16 tiles
-        // Thread ct converts the 16-code chunks i * 128 + ct of a tile.  A block of 16 slots is always in one
-        // page: lane b of each warp looks up block b, one tile ahead of the codes' loads, which are in
-        // flight while the tile before them is converted.
+        // Thread ct converts the 16-code chunks i * 128 + ct of its warpgroup's units.  A block of 16 slots is
+        // always in one page: lane b of each warp looks up block b of a tile, one tile ahead of the codes'
+        // loads, and leaves its offsets in a table of the warp's own; the loads of a unit are in flight
+        // while the warpgroup converts its unit before.
         set_max_regs<Cfg::CONV_REGS >= Cfg::LAUNCH_REGS, Cfg::CONV_REGS>();
-        const int ct = tid - Cfg::CONV_WARP * 32;
-        constexpr int PER = BN * D / 16 / 128;  // 16-code chunks per thread
-        constexpr int CPR = D / 16;
+        const int cw = (warp - Cfg::CONV_WARP) / 4, ct = (tid - Cfg::CONV_WARP * 32) & 127;
+        constexpr int PER = Cfg::TILE / 32 / 128;  // 16-code chunks per thread
+        constexpr int KC = Cfg::PKU * 4, VC = D / 16;  // chunks of a row in a key unit, in a value unit
+        const uint32_t places = base + Cfg::PLACES_AT + (warp - Cfg::CONV_WARP) * 256;  // two tiles x 8 blocks x (codes, steps)
         struct Raw {
             uint4 c[PER];
             uint16_t d[PER];
         };
-        struct Ahead {  // a tile to come
-            ChunkWalk w;
-            int j;       // slot tile
-            int page;    // lane b: page id of block b
+        struct Bounds {  // of a tile
+            int key0, seen_lo, len;
         };
-        auto lookup = [&](Ahead &t) {
-            t.page = -1;
-            const int key = (t.w.t.kb0 + t.j) * BN + 16 * lane;
-            if (t.w.left > 0 && lane < BN / 16 && key < t.w.t.len) t.page = a.bt.pages[t.w.t.b * a.bt.table_stride + key / a.bt.page];
+        struct Unit {
+            int on, val, h;
         };
-        auto step = [&](Ahead &t) {  // the tile after
-            if (t.w.left > 0 && ++t.j >= t.w.end()) {
-                chunk_next(t.w, plan, a.Hk);
-                t.j = t.w.blk();
+        ChunkWalk nx = k;  // the tile whose pages are looked up
+        int nj = k.blk(), npage = -1;
+        auto lookup = [&]() {
+            const int key = (nx.t.kb0 + nj) * BN + 16 * lane;
+            npage = -1;
+            if (nx.left > 0 && lane < BN / 16 && key < nx.t.len) npage = a.bt.pages[nx.t.b * a.bt.table_stride + key / a.bt.page];
+        };
+        Bounds cur{}, prev{};
+        uint32_t flip = 0;  // table half of cur
+        auto locate = [&]() {  // cur: the tile that was looked up; looks up the one after
+            __syncwarp();  // the half of the table that is written has been read
+            prev = cur;
+            flip ^= 128;
+            cur.key0 = (nx.t.kb0 + nj) * BN;
+            cur.seen_lo = a.window ? max(0, nx.t.len - nx.t.n + nx.t.row0 / a.G - a.window + 1) : 0;
+            cur.len = nx.t.len;
+            if (lane < BN / 16) {
+                const int slot = (cur.key0 + 16 * lane) % a.bt.page;
+                const bool ok = nx.left > 0 && (unsigned)npage < (unsigned)a.bt.n_pages;
+                const int64_t at = ok ? npage * a.page_stride + nx.h * a.head_stride + slot * a.slot_stride : -1;
+                const int64_t dat = ok ? npage * a.step_stride + ((int64_t)nx.h * a.bt.page + slot) * (D / 32) : 0;
+                sts128(places + flip + 16 * lane, (uint32_t)at, (uint32_t)(at >> 32), (uint32_t)dat, (uint32_t)(dat >> 32));
+            }
+            __syncwarp();
+            if (nx.left > 0 && ++nj >= nx.end()) {
+                chunk_next(nx, plan, a.Hk);
+                nj = nx.blk();
+            }
+            lookup();
+        };
+        int kt = k.blk(), vt = -1, blk0 = kt, end = k.end();  // the last key and value tiles begun
+        Unit un{k.left > 0, 0, -1};
+        auto next_unit = [&]() {  // the order of the copies
+            if (++un.h < KU) return;
+            un.h = 0;
+            const bool was_val = un.val;
+            if (!was_val) {
+                if (Cfg::KEYS_AHEAD && kt == blk0 && kt + 1 < end) {
+                    ++kt;
+                    locate();
+                } else {
+                    un.val = 1;
+                    vt = Cfg::KEYS_AHEAD ? max(blk0, kt - 1) : kt;
+                }
+            } else if (kt + 1 < end) {
+                un.val = 0;
+                ++kt;
+                locate();
+            } else if (vt < kt) {
+                ++vt;
+            } else {
+                chunk_next(k, plan, a.Hk);
+                un.val = 0;
+                un.on = k.left > 0;
+                blk0 = kt = k.blk();
+                end = k.end();
+                locate();
             }
         };
-        Raw kr, vr;
-        Ahead cur{}, nxt{};  // the tile whose codes are loaded next, and the one whose pages are
-        int64_t at = 0, dat = 0;  // lane b: element offsets of block b of the codes and steps; at < 0: none
-        int key0 = 0, seen_lo = 0, len = 0;
-        auto locate = [&]() {  // offsets of the tile `cur`
-            const int key = (cur.w.t.kb0 + cur.j) * BN + 16 * lane, slot = key % a.bt.page;
-            const bool ok = cur.w.left > 0 && (unsigned)cur.page < (unsigned)a.bt.n_pages;
-            at = ok ? cur.page * a.page_stride + cur.w.h * a.head_stride + slot * a.slot_stride : -1;
-            dat = ok ? cur.page * a.step_stride + ((int64_t)cur.w.h * a.bt.page + slot) * (D / 32) : 0;
-            key0 = (cur.w.t.kb0 + cur.j) * BN;
-            seen_lo = a.window ? max(0, cur.w.t.len - cur.w.t.n + cur.w.t.row0 / a.G - a.window + 1) : 0;
-            len = cur.w.left > 0 ? cur.w.t.len : 0;
-        };
-        auto fetch = [&](Raw &w, const void *codes, const f16 *steps) {
+        auto fetch_as = [&](Raw &w, const Unit &u, auto is_val) {
+            constexpr bool VAL = decltype(is_val)::value;
+            constexpr int CPR = VAL ? VC : KC, RPS = 128 / CPR;  // rows of a step of i
+            const bool last = !VAL || vt == kt;
+            const Bounds p = last ? cur : prev;
+            const uint32_t table = places + (last ? flip : flip ^ 128);
+            const int8_t *codes = static_cast<const int8_t *>(VAL ? a.vc : a.kc);
+            const uint16_t *steps = reinterpret_cast<const uint16_t *>(VAL ? a.vd : a.kd);
+            const int row0 = VAL ? u.h * VR : 0, r0 = ct / CPR, ch = (VAL ? 0 : u.h * KC) + ct % CPR;
+            const bool edge = p.key0 < p.seen_lo || p.key0 + BN > p.len;
 #pragma unroll
             for (int i = 0; i < PER; ++i) {
-                const int x = i * 128 + ct, row = x / CPR, ch = x % CPR, key = key0 + row;
-                const int64_t o = __shfl_sync(0xffffffffu, at, row / 16), d = __shfl_sync(0xffffffffu, dat, row / 16);
-                w.c[i] = make_uint4(0u, 0u, 0u, 0u);
+                // the step's rows lie in one block of 16, or in two where 32 rows make a step (dim 64)
+                const int row = row0 + i * RPS + r0, in = row & 15;
+                const uint4 t = lds128(table + (row >> 4) * 16);
+                const int64_t o = (int64_t)((uint64_t)t.y << 32 | t.x), d = (int64_t)((uint64_t)t.w << 32 | t.z);
+                bool ok = o >= 0;
+                if (edge) ok = ok && p.key0 + row >= p.seen_lo && p.key0 + row < p.len;
+                w.c[i] = make_uint4(0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u);  // any codes: the step is zero
                 w.d[i] = 0;
-                if (o >= 0 && key >= seen_lo && key < len) {
-                    w.c[i] = *reinterpret_cast<const uint4 *>(static_cast<const int8_t *>(codes) + o + (row % 16) * a.slot_stride + 16 * ch);
-                    w.d[i] = reinterpret_cast<const uint16_t *>(steps)[d + (row % 16) * (D / 32) + ch / 2];
+                if (ok) {
+                    w.c[i] = *reinterpret_cast<const uint4 *>(codes + o + in * a.slot_stride + 16 * ch);
+                    w.d[i] = steps[d + in * (D / 32) + ch / 2];
                 }
             }
         };
-        auto put = [&](const Raw &w) {
-            const uint32_t slot = units % NS;
-            if (units >= NS) mbar_wait(kv_empty(slot), (units / NS - 1) & 1);
-            ++units;
+        auto fetch = [&](Raw &w, const Unit &u) {
+            if (!u.on) return;
+            if (u.val)
+                fetch_as(w, u, std::true_type{});
+            else
+                fetch_as(w, u, std::false_type{});
+        };
+        auto put_as = [&](const Raw &w, uint32_t dst, auto is_val) {
+            constexpr bool VAL = decltype(is_val)::value;
+            constexpr int CPR = VAL ? VC : KC, RPS = 128 / CPR;
+            constexpr uint32_t PSTRIDE = (VAL ? VR : BN) * 128;
+            const int r0 = ct / CPR, ch = ct % CPR;
 #pragma unroll
             for (int i = 0; i < PER; ++i) {
-                const int x = i * 128 + ct, row = x / CPR, ch = x % CPR;
+                const int row = i * RPS + r0;
                 const uint32_t dd = w.d[i] | (uint32_t)w.d[i] << 16;
                 const uint32_t in[4] = {w.c[i].x, w.c[i].y, w.c[i].z, w.c[i].w};
                 uint32_t h[8];
@@ -718,32 +882,54 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
                         h[2 * e + y] = *reinterpret_cast<const uint32_t *>(&r);
                     }
                 }
-                const uint32_t row_at = kv0 + slot * Cfg::TILE + (ch >> 2) * (BN * 128) + row * 128;
+                const uint32_t row_at = dst + (ch >> 2) * PSTRIDE + row * 128;
 #pragma unroll
                 for (int y = 0; y < 2; ++y)
                     sts128(row_at + (((2 * (ch & 3) + y) ^ (row & 7)) << 4), h[4 * y], h[4 * y + 1], h[4 * y + 2], h[4 * y + 3]);
             }
+        };
+        auto put = [&](const Raw &w, const Unit &u, uint32_t n) {  // unit number n
+            const uint32_t slot = n % NS;
+            if (n >= NS) mbar_wait(kv_empty(slot), (n / NS - 1) & 1);
+            if (u.val)
+                put_as(w, kv0 + slot * Cfg::TILE, std::true_type{});
+            else
+                put_as(w, kv0 + slot * Cfg::TILE, std::false_type{});
             fence_proxy_async_smem();
             mbar_arrive(kv_full(slot));
         };
-        cur.w = k;
-        cur.j = k.blk();
-        lookup(cur);
+        Raw ra, rb;
+        lookup();
         locate();
-        nxt = cur;
-        step(nxt);
-        lookup(nxt);
-        fetch(kr, a.kc, a.kd);
-        fetch(vr, a.vc, a.vd);
-        while (cur.w.left > 0) {
-            cur = nxt;  // its pages have arrived
-            step(nxt);
-            lookup(nxt);
-            locate();
-            put(kr);
-            fetch(kr, a.kc, a.kd);
-            put(vr);
-            fetch(vr, a.vc, a.vd);
+        // every unit is listed by every warpgroup, each fetches its own
+        uint32_t n = 0;  // number of unit un
+        next_unit();
+        auto own_unit = [&](bool first) {
+            if (!first) {
+                next_unit();
+                ++n;
+            }
+            while (un.on && (int)(n % Cfg::NCONV) != cw) {
+                next_unit();
+                ++n;
+            }
+        };
+        own_unit(true);
+        Unit ua = un, ub;
+        uint32_t na = n, nb;
+        fetch(ra, ua);
+        while (ua.on) {
+            own_unit(false);
+            ub = un;
+            nb = n;
+            fetch(rb, ub);
+            put(ra, ua, na);
+            if (!ub.on) break;
+            own_unit(false);
+            ua = un;
+            na = n;
+            fetch(ra, ua);
+            put(rb, ub, nb);
         }
     }
     tc_fence_before();
@@ -825,8 +1011,11 @@ static int chunk_run(const AttnArgs &in, const qg_paged &c, uint8_t *ws, int sms
     // a scale of zero is a small one (masked scores stay -inf)
     const uint32_t qsign = a.scale2 < 0.0f ? 0x80008000u : 0u;
     a.scale2 = std::max(std::abs(a.scale2), 1e-30f);
-    const int box = gcd(c.page, Cfg::BN);
+    const int box = gcd(c.page, Cfg::VR);
     CUtensorMap km{}, vm{};
+    const bool qcopy = 128 % a.G == 0 && !qsign;
+    CUtensorMap qm{};
+    if (qcopy && !attn_query_map(&qm, a, c.type == QG_BF16, D)) return QG_ECUDA;
     if (!Cfg::Q8 && (!attn_tensor_map(&km, c, c.k, box) || !attn_tensor_map(&vm, c, c.v, box))) return QG_ECUDA;
     if (!launch_programmatic(attn_plan_kernel, dim3(1), PLAN_THREADS, 0, s, a, plan, Cfg::ROWS, Cfg::BN, (int)tiles)) return QG_ECUDA;
     auto kern = attn_chunk_kernel<C, D>;
@@ -836,7 +1025,7 @@ static int chunk_run(const AttnArgs &in, const qg_paged &c, uint8_t *ws, int sms
         return Cfg::WGS == 2 || (cudaFuncGetAttributes(&fa, (const void *)attn_chunk_kernel<C, D>) == cudaSuccess && fa.numRegs == Cfg::LAUNCH_REGS);
     }();
     if (!regs_ok || !allow_smem((const void *)kern, Cfg::BYTES)) return QG_ECUDA;
-    if (!launch_programmatic(kern, dim3((unsigned)sms), Cfg::THREADS, Cfg::BYTES, s, a, plan, box, qsign, km, vm)) return QG_ECUDA;
+    if (!launch_programmatic(kern, dim3((unsigned)sms), Cfg::THREADS, Cfg::BYTES, s, a, plan, box, qsign, (int)qcopy, km, vm, qm)) return QG_ECUDA;
     if (sms == 1) return QG_OK;
     auto join = attn_chunk_join_kernel<T, D>;
     return launch_programmatic(join, dim3((unsigned)(sms - 1), Cfg::ROWS / 8), 256, 0, s, a, plan, sms) ? QG_OK : QG_ECUDA;
