@@ -13,16 +13,17 @@
 //     2^8, rescales O.  Up to there a stale maximum is as good: O and the sum carry the same
 //     factor and P stays below 2^8.
 // What a row tile's warpgroup does for one slot tile (read S, maximum, exponentials, write P) takes
-// about as long as the tile's two products, so something else has to fill the tensor cores under
-// it.  With dim 64 and 128 that is the other row tile.  With dim 64 the next scores run under it
-// too: a score buffer is free as soon as its rows are in registers, as P has columns of its own.
-// With dim 256, whose O fills half the tensor memory and leaves room for one row tile, a second
-// score buffer takes them.  The value product starts on the first half of P while the second is
-// made.  Measured and dropped for dim 128: P in shared memory, which frees the score buffer early
-// but makes shared memory the bound (1.83 against 1.71 ms for 4096 tokens after 28000, 32/8
-// heads, bf16).  No product relies on the order of another that writes different columns: each
-// waits for the barrier of what it overwrites, and each row tile's products are issued by a warp of
-// their own.
+// about as long as the tile's two products with their latencies, so the next scores have to run
+// under it: a score buffer is free again as soon as its rows are in registers, as P has columns of
+// its own.  Tensor memory (512 columns) holds two score buffers, two P and two O at dim 64; at
+// dim 128 one score buffer on which the row tiles take turns; at dim 256, whose O fills half of it,
+// one row tile with two score buffers, P over its scores.  The value product starts on the first
+// half of P while the second is made.  Measured and dropped for dim 128 (4096 tokens after 28000,
+// 32/8 heads, bf16): P over its scores and a score buffer per row tile, so that a tile's scores
+// wait for its last value product, 1.98 ms; P in shared memory, whose bandwidth then is the bound,
+// 1.83 ms; now 1.55 ms (1.30 PFLOP/s).  No product relies on the order of another that writes different columns:
+// each waits for the barrier of what it overwrites, and each row tile's products are issued by a
+// warp of their own.
 // P is rounded to the value's 16-bit type, the operand type of the product: one rounding of
 // relative size 2^-12 (2^-9) per factor on average beside that of the result.
 //
@@ -56,11 +57,10 @@ struct ChunkCfg {
     static constexpr int NS = D == 64 ? 6 : 4;  // units in shared memory
     static constexpr uint32_t QB = 128 * D * 2;
     static constexpr uint32_t TILE = BN * D * 2 / KU;
-    // P goes over the scores it came from, or beside them where tensor memory has room (dim 64)
-    static constexpr bool P_OVER = D != 64;
-    // Units come in the order of their use: keys of tile j + 1 before the values of tile j where a
-    // score buffer is free by then, else after them
-    static constexpr bool KEYS_AHEAD = !P_OVER || SB == 2;
+    // P goes over the scores it came from where two score buffers alternate (dim 256), else beside them;
+    // with dim 128 the row tiles take turns on one score buffer
+    static constexpr bool P_OVER = D == 256, S_TURNS = D == 128;
+    static constexpr int S_COLS = S_TURNS ? BN : NQ * SB * BN;
     // Warpgroups: one per row tile, one whose first warps issue each row tile's products and the copies,
     // and those that convert 8-bit codes
     static constexpr int MMA_WARP = 4 * NQ;
@@ -76,15 +76,15 @@ struct ChunkCfg {
     static constexpr int CONV_REGS = !Q8 ? 0 : NQ == 2 ? 136 : 120;
     static_assert(WGS == 2 || NQ * ROW_REGS + ISSUE_REGS + NCONV * CONV_REGS == WGS * LAUNCH_REGS, "registers");
     static constexpr bool HOLD = !Q8 || D == 256;  // a row's scores fit a thread's registers
-    static constexpr int NBAR = 2 * NS + 2 * NQ + 4 * NQ * SB + 1;
+    static constexpr int NBAR = 2 * NS + 2 * NQ + 4 * NQ * SB + 1;  // see the barriers below
     static constexpr uint32_t OUT_AT = NQ * QB;  // 32 rows x 128 bytes of results per warp
     static constexpr uint32_t KV_AT = OUT_AT + NQ * 4 * 4096;
     static constexpr uint32_t BAR_AT = KV_AT + NS * TILE;
-    static constexpr uint32_t PLACES_AT = (BAR_AT + NBAR * 8 + 4 /* tensor memory address */ + 15) / 16 * 16;
+    static constexpr uint32_t PLACES_AT = (BAR_AT + NBAR * 8 + 8 /* tensor memory address, turn */ + 15) / 16 * 16;
     static constexpr uint32_t BYTES = PLACES_AT + NCONV * 4 * 256 + 1024 /* alignment */;
     static_assert(OUT_AT % 1024 == 0 && KV_AT % 1024 == 0 && BAR_AT % 16 == 0 && TILE % 1024 == 0, "alignment");
     // tensor memory columns
-    static constexpr int O_COL = NQ * SB * BN;
+    static constexpr int O_COL = S_COLS;
     static constexpr int P_COL = O_COL + NQ * D;  // where P has columns of its own
     static constexpr int COLS = 512;
     static_assert(P_COL + (P_OVER ? 0 : NQ * BN / 2) <= COLS, "tensor memory");
@@ -287,7 +287,7 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
     auto pv_done = [&](int q, int b) { return bars + 8u * (2 * NS + NQ + 2 * NQ * SB + q * SB + b); };
     auto p_half = [&](int q, int b) { return bars + 8u * (2 * NS + NQ + 3 * NQ * SB + q * SB + b); };
     auto s_empty = [&](int q) { return bars + 8u * (2 * NS + NQ + 4 * NQ * SB + q); };
-    const uint32_t v_raw = bars + 8u * (Cfg::NBAR - 1), taddr_slot = bars + 8u * Cfg::NBAR;
+    const uint32_t v_raw = bars + 8u * (Cfg::NBAR - 1), taddr_slot = bars + 8u * Cfg::NBAR, turn = taddr_slot + 4;
 
     if (tid == 0) {
         for (int s = 0; s < NS; ++s) {
@@ -306,6 +306,7 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
             }
         }
         fence_mbar_init();
+        asm volatile("st.volatile.shared.u32 [%0], %1;" ::"r"(turn), "r"(0u) : "memory");
     }
     if (warp == Cfg::MMA_WARP) tmem_alloc(taddr_slot, Cfg::COLS);
     tc_fence_before();
@@ -354,13 +355,12 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
                 uint4 v[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const int x = (i0 + i) * 32 + lane, rr = row0 + wr + x / CPR;
+                    // rows past the last are any rows: nothing of them is written
+                    const int x = (i0 + i) * 32 + lane, rr = min(row0 + wr + x / CPR, nrows - 1);
                     int g;
                     const int t = fast_div(rr, a.G, mG, g);
-                    v[i] = make_uint4(0u, 0u, 0u, 0u);
-                    if (rr < nrows)
-                        v[i] = *reinterpret_cast<const uint4 *>(static_cast<const T *>(a.q) + (int64_t)(w.t.first + t) * a.ldq +
-                                                                (int64_t)(w.h * a.G + g) * a.hdq + 8 * (x % CPR));
+                    v[i] = *reinterpret_cast<const uint4 *>(static_cast<const T *>(a.q) + (int64_t)(w.t.first + t) * a.ldq +
+                                                            (int64_t)(w.h * a.G + g) * a.hdq + 8 * (x % CPR));
                 }
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
@@ -390,7 +390,7 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
                 float m = -INFINITY, l = 0.0f;
                 for (int j = blk0; j < end; ++j, ++done) {
                     const int buf = SB == 1 ? 0 : (int)(done & 1);
-                    const uint32_t scol = lanes + (q * SB + buf) * BN;
+                    const uint32_t scol = lanes + (Cfg::S_TURNS ? 0 : (q * SB + buf) * BN);
                     const int key0 = (k.t.kb0 + j) * BN;
                     const int c_hi = hi - key0, c_lo = lo - key0;  // visible columns
                     const bool edge = key0 + BN - 1 > hi_min || key0 < lo_max;
@@ -587,13 +587,43 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
         static_assert(desc_hi == (uint32_t)(umma_desc_mnmajor_sw128(0, VR * 128) >> 32), "one upper word");
         const uint32_t leader = lane == 0;
         const int q = NQ == 1 ? 0 : (int)warp_uniform((uint32_t)(warp - Cfg::MMA_WARP));
-        const uint32_t s_col = warp_uniform(tmem + q * SB * BN), o_col = warp_uniform(tmem + Cfg::O_COL + q * D);
+        const uint32_t s_col = warp_uniform(tmem + (Cfg::S_TURNS ? 0 : q * SB * BN)), o_col = warp_uniform(tmem + Cfg::O_COL + q * D);
         const uint32_t p_col = warp_uniform(Cfg::P_OVER ? tmem + q * SB * BN : tmem + Cfg::P_COL + q * (BN / 2));
         const uint32_t q_desc = warp_uniform((uint32_t)umma_desc_kmajor_sw128(base + q * Cfg::QB));
-        uint32_t items = 0, n = 0;  // items; slot tiles of this row tile before j of the segment
-        auto scores = [&](uint32_t t) {  // S = Q K^T of this row tile's slot tile t, whose keys are the next units
-            const uint32_t buf = t % SB;
-            if (t >= SB) {  // the buffer's last scores have been read, and P that took their place
+        uint32_t items = 0, n = 0;  // items; slot tiles of this row tile before the segment
+        uint32_t other = 0;         // slot tiles of the other row tile before the segment (they take turns)
+        bool both_before = false;   // the segment before had rows in both tiles
+        uint32_t seg = 0;           // segments begun
+        auto wait_turn = [&](uint32_t s) {  // until row tile 0 has begun segment s; bounded as every wait
+            const unsigned long long t0 = globaltimer_ns();
+            for (uint32_t spin = 1;; ++spin) {
+                uint32_t v;
+                asm volatile("ld.volatile.shared.u32 %0, [%1];" : "=r"(v) : "r"(turn) : "memory");
+                if (__any_sync(0xffffffffu, v >= s)) break;
+                if ((spin & 255u) == 0 && __any_sync(0xffffffffu, globaltimer_ns() - t0 > WAIT_NS)) {
+                    if (lane == 0) atomicOr(&g_qg_dev_err, DEVERR_TIMEOUT);
+                    break;
+                }
+            }
+        };
+        // S = Q K^T of slot tile j of the segment, whose keys are the next units
+        auto scores = [&](int j, bool both) {
+            const uint32_t t = n + j, buf = t % SB;
+            // the buffer's last scores have been read, and P that took their place
+            if constexpr (Cfg::S_TURNS) {
+                if (q == 1) {
+                    // Row tile 0 takes segments that have no rows in this tile alone.  Its barrier's parity says
+                    // nothing until it has come to this segment, which it publishes
+                    if (j == 0) wait_turn(seg);
+                    mbar_wait(s_empty(0), (other + j) & 1);
+                } else {
+                    if (j > 0 ? both : both_before)
+                        mbar_wait(s_empty(1), (other + j - 1) & 1);
+                    else if (t > 0)
+                        mbar_wait(s_empty(0), (t - 1) & 1);
+                    if (j == 0 && lane == 0) asm volatile("st.volatile.shared.u32 [%0], %1;" ::"r"(turn), "r"(seg) : "memory");
+                }
+            } else if (t >= SB) {
                 if (Cfg::P_OVER)
                     mbar_wait(pv_done(q, buf), (t / SB - 1) & 1);
                 else
@@ -639,17 +669,21 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
         };
         while (k.left > 0) {
             const int taken = k.end() - k.blk();
+            ++seg;
             if (q == 0 || k.t.row0 + 128 < k.t.n * a.G) {
                 mbar_wait(q_full(q), items & 1);
                 ++items;
-                scores(n);
+                const bool both = NQ == 2 && k.t.row0 + 128 < k.t.n * a.G;
+                scores(0, both);
                 for (int j = 0; j < taken; ++j) {
-                    if (Cfg::KEYS_AHEAD && j + 1 < taken) scores(n + j + 1);
+                    if (j + 1 < taken) scores(j + 1, both);
                     product(n + j, j == 0);
-                    if (!Cfg::KEYS_AHEAD && j + 1 < taken) scores(n + j + 1);
                 }
+                both_before = both;
+                if (both || q == 1) other += taken;
                 n += taken;
             } else {  // no rows in this tile: its share of every unit's release
+                other += taken;
                 for (int j = 0; j < 2 * KU * taken; ++j, ++units) {
                     mbar_wait(kv_full(units % NS), (units / NS) & 1);
                     if (lane == 0) mbar_arrive(kv_empty(units % NS));
@@ -731,15 +765,12 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
                 const Place prev = cur;
                 cur = next;
                 next = ahead();
-                if (!Cfg::KEYS_AHEAD) copy(prev, 0, k.h, true, j);
                 if (j + 1 < end) {
 #pragma unroll
                     for (int h = 0; h < KU; ++h) copy(cur, h, k.h, false, 0);
                 }
-                if (Cfg::KEYS_AHEAD) {
 #pragma unroll
-                    for (int h = 0; h < KU; ++h) copy(prev, h, k.h, true, j);
-                }
+                for (int h = 0; h < KU; ++h) copy(prev, h, k.h, true, j);
             }
             chunk_next(k, plan, a.Hk);
         }
@@ -762,6 +793,7 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
         struct Raw {
             uint4 c[PER];
             uint16_t d[PER];
+            uint32_t ok;  // bit i: chunk i is a slot's, else zeros
         };
         struct Bounds {  // of a tile
             int key0, seen_lo, len;
@@ -806,12 +838,12 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
             un.h = 0;
             const bool was_val = un.val;
             if (!was_val) {
-                if (Cfg::KEYS_AHEAD && kt == blk0 && kt + 1 < end) {
+                if (kt == blk0 && kt + 1 < end) {
                     ++kt;
                     locate();
                 } else {
                     un.val = 1;
-                    vt = Cfg::KEYS_AHEAD ? max(blk0, kt - 1) : kt;
+                    vt = max(blk0, kt - 1);
                 }
             } else if (kt + 1 < end) {
                 un.val = 0;
@@ -838,6 +870,7 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
             const uint16_t *steps = reinterpret_cast<const uint16_t *>(VAL ? a.vd : a.kd);
             const int row0 = VAL ? u.h * VR : 0, r0 = ct / CPR, ch = (VAL ? 0 : u.h * KC) + ct % CPR;
             const bool edge = p.key0 < p.seen_lo || p.key0 + BN > p.len;
+            w.ok = 0;
 #pragma unroll
             for (int i = 0; i < PER; ++i) {
                 // the step's rows lie in one block of 16, or in two where 32 rows make a step (dim 64)
@@ -846,12 +879,10 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
                 const int64_t o = (int64_t)((uint64_t)t.y << 32 | t.x), d = (int64_t)((uint64_t)t.w << 32 | t.z);
                 bool ok = o >= 0;
                 if (edge) ok = ok && p.key0 + row >= p.seen_lo && p.key0 + row < p.len;
-                w.c[i] = make_uint4(0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u);  // any codes: the step is zero
-                w.d[i] = 0;
-                if (ok) {
-                    w.c[i] = *reinterpret_cast<const uint4 *>(codes + o + in * a.slot_stride + 16 * ch);
-                    w.d[i] = steps[d + in * (D / 32) + ch / 2];
-                }
+                w.ok |= (uint32_t)ok << i;
+                // every load runs (page 0 where there is no slot): a load under a branch would be waited for there
+                w.c[i] = *reinterpret_cast<const uint4 *>(codes + (ok ? o : 0) + in * a.slot_stride + 16 * ch);
+                w.d[i] = steps[(ok ? d : 0) + in * (D / 32) + ch / 2];
             }
         };
         auto fetch = [&](Raw &w, const Unit &u) {
@@ -869,7 +900,7 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
 #pragma unroll
             for (int i = 0; i < PER; ++i) {
                 const int row = i * RPS + r0;
-                const uint32_t dd = w.d[i] | (uint32_t)w.d[i] << 16;
+                const uint32_t dd = w.ok >> i & 1u ? w.d[i] | (uint32_t)w.d[i] << 16 : 0u;
                 const uint32_t in[4] = {w.c[i].x, w.c[i].y, w.c[i].z, w.c[i].w};
                 uint32_t h[8];
 #pragma unroll
