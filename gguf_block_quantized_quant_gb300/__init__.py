@@ -14,8 +14,9 @@ rows of raw blocks back to back (``row_bytes(fmt, K)`` bytes per row).
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
-import struct
 
 import torch
 
@@ -32,7 +33,6 @@ BLOCK_BYTES = {Q4_0: 18, Q4_1: 20, Q5_0: 22, Q5_1: 24, Q8_0: 34, Q2_K: 84, Q3_K:
 
 # element types (GGUF type ids) and frequency scalings of the decoder-layer operators
 F32, F16, BF16 = 0, 1, 30
-_TYPE = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16, torch.int8: Q8_0}
 ROPE_PLAIN, ROPE_LINEAR, ROPE_NTK, ROPE_YARN = 0, 1, 2, 3
 
 QG_OP_GEMV, QG_OP_GEMV_Q, QG_OP_MOE_FFN, QG_OP_FFN_SUBLAYER, QG_OP_MOE_FFN_S16, QG_OP_PREFILL = 1, 2, 3, 4, 5, 6
@@ -295,66 +295,26 @@ def qg_dequant_f16(fmt: int, W, N: int, K: int, stream=None):
 
 
 # ------------------------------------------------------------- the rest of a decoder layer
-_PAGED = struct.Struct("8i5q7Q")  # qg_paged of include/qg.h
+# These calls are marshalled in C++ (csrc/qg_torch.cpp): through ctypes the host would take many
+# times as long as the kernels of a single token.
+_module = None
 
 
-def _addr(t):
-    return None if t is None else t.data_ptr()
+def _torch_module():
+    global _module
+    if _module is None:
+        lib()
+        loader = importlib.machinery.ExtensionFileLoader("qg_torch", _build.TORCH_MODULE)
+        spec = importlib.util.spec_from_file_location("qg_torch", _build.TORCH_MODULE, loader=loader)
+        _module = importlib.util.module_from_spec(spec)
+        loader.exec_module(_module)
+    return _module
 
 
-def _rows(t, what):
-    """Rows of a tensor whose last dimension is contiguous: (address, elements between rows)."""
-    if not t.is_cuda:
-        raise ValueError(f"{what} must be a CUDA tensor")
-    if t.stride(-1) != 1 and t.shape[-1] != 1:
-        raise ValueError(f"{what} must be contiguous along its last dimension")
-    return t.data_ptr(), t.stride(0)
-
-
-def _on(device, *tensors):
-    for t in tensors:
-        if t is not None and t.device != device:
-            raise ValueError("all tensors of a call must be on one CUDA device")
-
-
-def _paged(k, v, kd, vd, q_start, kv_len, pages):
-    """The bytes of the qg_paged struct for pools k, v of shape (pages, kv_heads, page, dim)."""
-    if k.dtype not in _TYPE or k.dtype == torch.float32 or v.dtype != k.dtype or v.shape != k.shape or v.stride() != k.stride():
-        raise ValueError("cache pools are fp16, bf16 or int8 tensors of one shape, type and layout")
-    n, heads, page, dim = k.shape
-    sp, sh, ss, se = k.stride()
-    if se != 1:
-        raise ValueError("cache pools must be contiguous along the head dimension")
-    step = 0
-    if k.dtype == torch.int8:
-        if kd is None or vd is None or kd.dtype != torch.float16 or vd.dtype != torch.float16:
-            raise ValueError("an int8 cache needs fp16 steps kd and vd")
-        want = (n, heads, page, dim // 32)
-        if tuple(kd.shape) != want or tuple(vd.shape) != want or kd.stride() != vd.stride() or kd.stride()[1:] != (
-                page * (dim // 32), dim // 32, 1):
-            raise ValueError("steps have shape (pages, kv_heads, page, dim / 32), contiguous within a page")
-        step = kd.stride(0)
-    if q_start.dtype != torch.int32 or kv_len.dtype != torch.int32 or pages.dtype != torch.int32:
-        raise ValueError("q_start, kv_len and pages are int32 tensors")
-    batch = kv_len.numel()
-    if q_start.numel() != batch + 1 or pages.dim() != 2 or pages.shape[0] != batch or (pages.stride(1) != 1 and pages.shape[1] != 1):
-        raise ValueError("q_start has batch + 1 entries, kv_len batch, pages batch rows")
-    if not (q_start.is_contiguous() and kv_len.is_contiguous()):
-        raise ValueError("q_start and kv_len must be contiguous")
-    _on(k.device, v, kd, vd, q_start, kv_len, pages)
-    width = pages.shape[1]
-    return _PAGED.pack(_TYPE[k.dtype], heads, dim, page, n, batch, width, 0, sp, sh, ss, step,
-                       pages.stride(0) if batch > 1 else max(width, pages.stride(0)),
-                       k.data_ptr(), v.data_ptr(), 0 if kd is None else kd.data_ptr(), 0 if vd is None else vd.data_ptr(),
-                       q_start.data_ptr(), kv_len.data_ptr(), pages.data_ptr())
-
-
-def _heads(t, what):
-    """(address, elements between tokens, between heads) of a (tokens, heads, dim) view."""
-    if t.dim() != 3 or not t.is_cuda or t.stride(2) != 1:
-        raise ValueError(f"{what} is a CUDA tensor (tokens, heads, dim), contiguous along dim")
-    T, H, D = t.shape
-    return t.data_ptr(), t.stride(0) if T > 1 else max(D, t.stride(0)), t.stride(1) if H > 1 else D
+def _done(r, what):
+    if type(r) is int:
+        raise QGError(r, what)
+    return r
 
 
 def qg_norm_residual(y, res, w_pre, w_post=None, gate=None, alpha: float = 1.0, eps: float = 1e-6, w_offset: float = 0.0,
@@ -364,39 +324,8 @@ def qg_norm_residual(y, res, w_pre, w_post=None, gate=None, alpha: float = 1.0, 
     y: (rows, width), fp32, fp16 or bf16; res: the same shape, fp32 or y's type, or None;
     gate: y's type, (rows, width) or (width,); w_pre, w_post: fp32 (width,), w_pre None skips x.
     Returns (r, x); r has res's type (y's without res), x x_dtype (default y's)."""
-    M, H = y.shape
-    yp, ldy = _rows(y, "y")
-    _on(y.device, res, w_pre, w_post, gate, res_out, x_out)
-    if y.dtype not in (torch.float32, torch.float16, torch.bfloat16):
-        raise ValueError("y is fp32, fp16 or bf16")
-    rdt = y.dtype if res is None else res.dtype
-    rp, ldr = (None, H) if res is None else _rows(res, "res")
-    gp, ldg = None, 0
-    if gate is not None:
-        if gate.dtype != y.dtype or gate.shape[-1] != H or (gate.dim() == 2 and gate.shape[0] not in (1, M)) or gate.dim() > 2:
-            raise ValueError("gate has y's type and shape (rows, width) or (width,)")
-        gp, ldg = _rows(gate, "gate")
-        if gate.dim() == 1 or gate.shape[0] == 1:
-            ldg = 0
-    if res is not None and tuple(res.shape) != (M, H):
-        raise ValueError("res has the shape of y")
-    for w in (w_pre, w_post):
-        if w is not None and (w.dtype != torch.float32 or w.numel() != H or not w.is_contiguous()):
-            raise ValueError("norm weights are contiguous fp32 tensors of the row's width")
-    if res_out is None:
-        res_out = torch.empty((M, H), dtype=rdt, device=y.device)
-    elif tuple(res_out.shape) != (M, H) or res_out.dtype != rdt or not res_out.is_contiguous():
-        raise ValueError("res_out is contiguous, with res's shape and type")
-    if x_out is None and w_pre is not None:
-        x_out = torch.empty((M, H), dtype=x_dtype or y.dtype, device=y.device)
-    elif x_out is not None and (tuple(x_out.shape) != (M, H) or not x_out.is_contiguous() or w_pre is None):
-        raise ValueError("x_out is contiguous, with y's shape, and needs w_pre")
-    xt = F32 if x_out is None else _TYPE[x_out.dtype]
-    if M == 1:
-        ldy, ldr = H, H
-    _check(lib().qg_norm_residual(yp, _TYPE[y.dtype], ldy, rp, _TYPE[rdt], ldr, _addr(w_post), gp, ldg, _addr(w_pre), w_offset,
-                                  alpha, eps, res_out.data_ptr(), _addr(x_out), xt, M, H, _stream(stream)), "qg_norm_residual")
-    return res_out, x_out
+    return _done((_module or _torch_module()).norm_residual(
+        y, res, w_pre, w_post, gate, alpha, eps, w_offset, x_dtype, res_out, x_out, None if stream is None else stream.cuda_stream), "qg_norm_residual")
 
 
 def qg_rope_turns(rot: int, base: float = 10000.0, scaling: int = ROPE_PLAIN, factor: float = 1.0, original: float = 4096.0,
@@ -416,31 +345,9 @@ def qg_rope_append(q, nk, nv, turns, k, v, q_start, kv_len, pages, kd=None, vd=N
     positions and appends nk and nv to the pools k, v (pages, kv_heads, page, dim); the steps of
     an int8 cache go to kd, vd.  turns: int64 CUDA tensor of rot / 2.  Returns the rotated q,
     fp16 (bf16 beside a bf16 cache; q_dtype, if given, has to be that)."""
-    qp, ldq, hdq = _heads(q, "q")
-    kp, ldk, hdk = _heads(nk, "nk")
-    vp, ldv, hdv = _heads(nv, "nv")
-    T, H, D = q.shape
-    if nk.dtype != q.dtype or nv.dtype != q.dtype or nk.shape != nv.shape or nk.shape[0] != T or nk.shape[2] != D or (
-            k.dim() != 4 or nk.shape[1] != k.shape[1] or D != k.shape[3]) or q.dtype == torch.int8 or q.dtype not in _TYPE:
-        raise ValueError("q, nk and nv are of one float type, for the same tokens and the cache's heads")
-    dt = torch.bfloat16 if k.dtype == torch.bfloat16 else torch.float16
-    if q_dtype not in (None, dt):
-        raise ValueError(f"queries beside this cache are {dt}")
-    rot = 0 if turns is None else 2 * turns.numel()
-    if turns is not None and (turns.dtype != torch.int64 or not turns.is_contiguous()):
-        raise ValueError("turns is a contiguous int64 tensor")
-    for w in (wq, wk):
-        if w is not None and (w.dtype != torch.float32 or w.numel() != D or not w.is_contiguous()):
-            raise ValueError("head norm weights are contiguous fp32 tensors of dim elements")
-    if q_out is None:
-        q_out = torch.empty((T, H, D), dtype=dt, device=q.device)
-    elif tuple(q_out.shape) != (T, H, D) or q_out.dtype != dt or not q_out.is_contiguous():
-        raise ValueError("q_out is contiguous, with q's shape")
-    _on(q.device, nk, nv, turns, k, wq, wk, q_out)
-    _check(lib().qg_rope_append(qp, ldq, hdq, kp, ldk, hdk, vp, ldv, hdv, _TYPE[q.dtype], T, H, _addr(turns), rot, int(pairs), amp,
-                                _addr(wq), _addr(wk), eps, q_out.data_ptr(), _paged(k, v, kd, vd, q_start, kv_len, pages),
-                                _stream(stream)), "qg_rope_append")
-    return q_out
+    return _done((_module or _torch_module()).rope_append(
+        q, nk, nv, turns, k, v, q_start, kv_len, pages, kd, vd, pairs, amp, wq, wk, eps, q_dtype, q_out,
+        None if stream is None else stream.cuda_stream), "qg_rope_append")
 
 
 def qg_attn_workspace_size(dim: int, q_heads: int, kv_heads: int, tokens: int, batch: int) -> int:
@@ -453,30 +360,9 @@ def qg_attn_paged(q, k, v, q_start, kv_len, pages, kd=None, vd=None, max_new: in
     (pages, kv_heads, page, dim).  max_new: the longest chunk, where the caller knows it (it
     only chooses the kernel); scale: default dim ** -0.5; out_dtype: q's type or fp32; lse:
     optional fp32 (tokens, heads) output.  Returns out (tokens, heads, dim)."""
-    qp, ldq, hdq = _heads(q, "q")
-    T, H, D = q.shape
-    if k.dim() != 4 or k.shape[3] != D:
-        raise ValueError("pools have shape (pages, kv_heads, page, dim) with q's dim")
-    if q.dtype not in (torch.float16, torch.bfloat16):
-        raise ValueError("q is fp16 or bf16")
-    B = kv_len.numel()
-    if out is None:
-        out = torch.empty((T, H, D), dtype=out_dtype or q.dtype, device=q.device)
-    elif tuple(out.shape) != (T, H, D) or not out.is_contiguous() or out.dtype not in (q.dtype, torch.float32):
-        raise ValueError("out is contiguous, with q's shape, in q's type or fp32")
-    if lse is not None and (tuple(lse.shape) != (T, H) or lse.dtype != torch.float32 or not lse.is_contiguous()):
-        raise ValueError("lse is a contiguous fp32 tensor (tokens, heads)")
-    _on(q.device, k, out, lse, ws)
-    if ws is None:
-        nbytes = qg_attn_workspace_size(D, H, k.shape[1], T, B)
-        if nbytes == WS_INVALID:
-            raise QGError(QG_EINVAL, "qg_attn_workspace_size")
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
-    _check(lib().qg_attn_paged(qp, ldq, hdq, _TYPE[q.dtype], T, H, -(-T // B) if max_new is None else max_new,
-                               D ** -0.5 if scale is None else scale, window, out.data_ptr(), _TYPE.get(out.dtype, -1), _addr(lse),
-                               _paged(k, v, kd, vd, q_start, kv_len, pages), ws.data_ptr(), ws.numel(), _stream(stream)),
-           "qg_attn_paged")
-    return out
+    return _done((_module or _torch_module()).attn_paged(
+        q, k, v, q_start, kv_len, pages, kd, vd, max_new, scale, window, out_dtype, out, lse, ws,
+        None if stream is None else stream.cuda_stream), "qg_attn_paged")
 
 
 def qg_test_wait_expiry(limit_ns: int, stream=None):
