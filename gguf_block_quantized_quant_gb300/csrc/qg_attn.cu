@@ -19,47 +19,59 @@ namespace qg {
 //
 // Inside a range each warp takes every NW-th block.  It has its own ring of slots in shared
 // memory, filled by tiled TMA copies that it issues itself S blocks ahead (also across items),
-// and its own running maximum and sum, so warps meet only at the end of an item.  Scores and
-// the value sums are m16n8k16 products: 16 rows x 16 slots per block.
+// and its own running maximum and sum, so warps meet only at the end of an item.
 //
-// Bound by the read of the cache; the products take about a quarter of that time, which is
-// why the probabilities can go in as two addends (hi + lo): the value sums then keep fp32
-// accuracy instead of the 11 (8) bits of one fp16 (bf16) factor.
-constexpr int DEC_ROWS = 16;
+// Scores and value sums are m16n8k16 products with the cache as the 16-row operand: S^T = K Q^T
+// (16 slots x 8 rows) and O^T += V^T P^T (16 columns x 8 rows).  Eight query rows then fill a
+// product; with the rows as the 16-row operand half of each would be padding for the usual 4 to 8
+// heads per cache head, at twice the accumulators.  NR = 2 takes 16 rows.  P^T changes from
+// accumulator to operand layout by a transposing move within the warp.
+//
+// Bound by the read of the cache; the products take a small part of that time, which is why the
+// probabilities can go in as two addends (hi + lo): the value sums then keep fp32 accuracy
+// instead of the 11 (8) bits of one fp16 (bf16) factor.
+constexpr int DEC_ROWS = 16;     // rows of a tile at most (NR = 2)
 constexpr int DEC_BLK = 16;      // slots per block: the least page size
 constexpr int DEC_MIN_BLKS = 8;  // blocks a CTA takes at least: one per warp
 
-template <int C, int D>
+template <int C, int D, int NR>
 struct DecCfg {
     static constexpr bool Q8 = C == CACHE_Q8;
+    static constexpr int ROWS = 8 * NR;
     static constexpr int ES = Q8 ? 1 : 2;
     static constexpr int ROWB = D * ES;                      // bytes of a slot's row
     static constexpr int PANEL = ROWB < 128 ? ROWB : 128;    // bytes of a swizzled panel row
     static constexpr int NP = ROWB / PANEL;                  // panels
     static constexpr int TILE = DEC_BLK * ROWB;              // K (or V) bytes of a block
     static constexpr int STEPS = Q8 ? DEC_BLK * (D / 32) * 2 : 0;
-    static constexpr int NW = (D == 256 && !Q8) ? 4 : 8;     // warps
-    static constexpr int S = D == 256 ? 3 : (D == 128 ? (Q8 ? 5 : 3) : (Q8 ? 8 : 6));
-    static constexpr int CT = NW == 4 ? 8 : 4;               // n-tiles (of 8 columns) merged at a time
+    // Warps and ring slots: about 190 KB in flight per SM; 8-bit codes take more instructions per byte
+    // and get more warps where the accumulators leave registers for them
+    static constexpr int NW = D == 256 ? (Q8 ? (NR == 1 ? 12 : 8) : 6) : D == 128 ? (Q8 ? (NR == 1 ? 16 : 12) : 8) : (Q8 ? 16 : 12);
+    static constexpr int ROOM = (222 * 1024 - NW * ROWS * (128 + 8)) / (NW * 2 * (TILE + STEPS));
+    static constexpr int S = ROOM > 8 ? 8 : ROOM;
     static constexpr uint32_t RING = (uint32_t)NW * S * 2 * TILE;
     static constexpr uint32_t STEP_AT = RING;
+    static constexpr int MW = 32;                            // columns merged at a time
     static constexpr uint32_t MERGE_AT = STEP_AT + (uint32_t)NW * S * 2 * STEPS;
-    static constexpr uint32_t ML_AT = MERGE_AT + (uint32_t)NW * DEC_ROWS * CT * 8 * 4;
-    static constexpr uint32_t BAR_AT = ML_AT + (uint32_t)NW * DEC_ROWS * 8;
+    static constexpr uint32_t ML_AT = MERGE_AT + (uint32_t)NW * ROWS * MW * 4;
+    static constexpr uint32_t BAR_AT = ML_AT + (uint32_t)NW * ROWS * 8;
     static constexpr uint32_t BYTES = BAR_AT + (uint32_t)NW * S * 8 + 1024 /* alignment */;
+    static_assert(MERGE_AT % 16 == 0 && ML_AT % 8 == 0 && BAR_AT % 8 == 0 && S >= 2, "layout");
 };
 
 // The blocks of one sequence: every item (cache head, row tile) of it has the same slots.
+template <int ROWS>
 struct SeqWork {
     Seq sq;
     int nrt;        // row tiles
     int kb0, nblk;  // first block of 16 slots and their number (at least 1)
     int64_t cost;   // blocks of all items
 };
-__device__ __forceinline__ SeqWork seq_work(const AttnArgs &a, int b) {
-    SeqWork w;
+template <int ROWS>
+__device__ __forceinline__ SeqWork<ROWS> seq_work(const AttnArgs &a, int b) {
+    SeqWork<ROWS> w;
     w.sq = seq_of(a.bt, b);
-    w.nrt = (w.sq.n * a.G + DEC_ROWS - 1) / DEC_ROWS;
+    w.nrt = (w.sq.n * a.G + ROWS - 1) / ROWS;
     const int low = a.window ? max(0, w.sq.len - w.sq.n - a.window + 1) : 0;
     w.kb0 = low / DEC_BLK;
     w.nblk = max(1, (w.sq.len + DEC_BLK - 1) / DEC_BLK - w.kb0);
@@ -68,12 +80,14 @@ __device__ __forceinline__ SeqWork seq_work(const AttnArgs &a, int b) {
 }
 
 // Position in the work list.
+template <int ROWS>
 struct Walk {
-    SeqWork w;
+    SeqWork<ROWS> w;
     int b, item, blk;  // item: cache head * nrt + row tile
     int64_t left;      // blocks left in this CTA's range
 };
-__device__ __forceinline__ void walk_next(Walk &k, const AttnArgs &a, int taken) {
+template <int ROWS>
+__device__ __forceinline__ void walk_next(Walk<ROWS> &k, const AttnArgs &a, int taken) {
     k.left -= taken;
     k.blk += taken;
     if (k.left <= 0 || k.blk < k.w.nblk) return;
@@ -81,17 +95,17 @@ __device__ __forceinline__ void walk_next(Walk &k, const AttnArgs &a, int taken)
     if (++k.item < k.w.nrt * a.Hk) return;
     k.item = 0;
     do {
-        k.w = seq_work(a, ++k.b);
+        k.w = seq_work<ROWS>(a, ++k.b);
     } while (k.w.cost == 0);  // left > 0: a later sequence has work
 }
 
 // Blocks in all sequences, the number of CTAs that share them, and the position of block
 // `at(total, ctas)` of the list.  Whole CTA; `sh` holds 34 values.
-template <class At>
-__device__ __forceinline__ Walk walk_find(const AttnArgs &a, int64_t *sh, int64_t &total, int &ctas, int max_ctas, At at) {
+template <int ROWS, class At>
+__device__ __forceinline__ Walk<ROWS> walk_find(const AttnArgs &a, int64_t *sh, int64_t &total, int &ctas, int max_ctas, At at) {
     const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5, nwarps = nt >> 5;
     int64_t mine = 0;
-    for (int b = tid; b < a.bt.batch; b += nt) mine += seq_work(a, b).cost;
+    for (int b = tid; b < a.bt.batch; b += nt) mine += seq_work<ROWS>(a, b).cost;
     const int64_t first_cost = mine;  // of sequence tid when one round covers the batch
     auto scan = [&](int64_t v, int64_t &sum) {  // inclusive prefix over the CTA's threads
 #pragma unroll
@@ -113,14 +127,14 @@ __device__ __forceinline__ Walk walk_find(const AttnArgs &a, int64_t *sh, int64_
     int64_t incl = scan(mine, total);
     ctas = (int)min((int64_t)max_ctas, max((int64_t)1, (total + DEC_MIN_BLKS - 1) / DEC_MIN_BLKS));
     const int64_t want = at(total, ctas);
-    Walk k;
+    Walk<ROWS> k;
     k.b = 0, k.item = 0, k.blk = 0, k.left = 0;
     if (want < 0 || want >= total) return k;
     int64_t base = 0;
     for (int c0 = 0; c0 < a.bt.batch; c0 += nt) {
         int64_t sum = total, cost = first_cost;
         if (a.bt.batch > nt) {
-            cost = c0 + tid < a.bt.batch ? seq_work(a, c0 + tid).cost : 0;
+            cost = c0 + tid < a.bt.batch ? seq_work<ROWS>(a, c0 + tid).cost : 0;
             incl = scan(cost, sum);
         }
         const int64_t lo = base + incl - cost;
@@ -134,7 +148,7 @@ __device__ __forceinline__ Walk walk_find(const AttnArgs &a, int64_t *sh, int64_
     __syncthreads();
     k.b = (int)sh[32];
     const int64_t rem = sh[33];
-    k.w = seq_work(a, k.b);
+    k.w = seq_work<ROWS>(a, k.b);
     k.item = (int)(rem / k.w.nblk);
     k.blk = (int)(rem % k.w.nblk);
     return k;
@@ -159,6 +173,12 @@ __device__ __forceinline__ void ldmatrix4_t(uint32_t addr, uint32_t (&r)[4]) {
                  : "r"(addr)
                  : "memory");
 }
+// An 8 x 8 matrix of 16-bit values held two per lane (row lane / 4), transposed.
+__device__ __forceinline__ uint32_t movmatrix_t(uint32_t v) {
+    uint32_t r;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
 // c += A (16 x 16, row major) * B (16 x 8, column major)
 template <class T>
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -172,12 +192,12 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
                      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-template <int C, int D>
-__global__ void __launch_bounds__(DecCfg<C, D>::NW * 32, 1)
+template <int C, int D, int NR>
+__global__ void __launch_bounds__(DecCfg<C, D, NR>::NW * 32, 1)
     attn_rows_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
-    using Cfg = DecCfg<C, D>;
+    using Cfg = DecCfg<C, D, NR>;
     using T = typename CacheT<C>::Q;
-    constexpr int NW = Cfg::NW, S = Cfg::S, NT = D / 8;
+    constexpr int NW = Cfg::NW, S = Cfg::S, ROWS = Cfg::ROWS, MT = D / 16;  // MT: column tiles of O^T
     extern __shared__ __align__(16) uint8_t dec_smem[];
     __shared__ int64_t sh[34];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -197,7 +217,7 @@ __global__ void __launch_bounds__(DecCfg<C, D>::NW * 32, 1)
     griddep_launch_dependents();
     int64_t total, w0 = 0, w1 = 0;
     int ctas;
-    Walk con = walk_find(a, sh, total, ctas, (int)gridDim.x, [&](int64_t tot, int n) {
+    Walk<ROWS> con = walk_find<ROWS>(a, sh, total, ctas, (int)gridDim.x, [&](int64_t tot, int n) {
         if ((int)blockIdx.x >= n) return (int64_t)-1;
         const Ranges rg(tot, n);
         w0 = rg.start(blockIdx.x);
@@ -208,12 +228,12 @@ __global__ void __launch_bounds__(DecCfg<C, D>::NW * 32, 1)
     con.left = w1 - w0;
 
     // ---- producer: this warp's next block, its page id fetched one block early
-    Walk pro = con;
+    Walk<ROWS> pro = con;
     int pblk = 0, pend = 0, ppage = 0;  // next block and end of the segment; page id of the block
-    auto seg_end = [&](const Walk &k) { return (int)min((int64_t)k.w.nblk, k.blk + k.left); };
-    auto page_of = [&](const Walk &k, int blk) {
-        const int idx = (k.w.kb0 + blk) * DEC_BLK / a.bt.page;
-        return idx < a.bt.table_width ? a.bt.pages[k.b * a.bt.table_stride + idx] : -1;
+    auto seg_end = [&](const Walk<ROWS> &k) { return (int)min((int64_t)k.w.nblk, k.blk + k.left); };
+    auto page_of = [&](const Walk<ROWS> &k, int blk) {
+        const int idx = min((k.w.kb0 + blk) * DEC_BLK / a.bt.page, a.bt.table_width - 1);
+        return a.bt.pages[k.b * a.bt.table_stride + idx];
     };
     auto pro_seek = [&]() {  // moves on to a segment that has a block for this warp
         while (pro.left > 0 && pblk >= pend) {
@@ -263,61 +283,71 @@ __global__ void __launch_bounds__(DecCfg<C, D>::NW * 32, 1)
         const int end = seg_end(con), taken = end - con.blk;
         const int h = con.item / con.w.nrt, rt = con.item % con.w.nrt;
         const Seq sq = con.w.sq;
-        const int nr = min(DEC_ROWS, sq.n * a.G - rt * DEC_ROWS);
-        // ---- queries as A fragments: rows gr, gr + 8
-        uint32_t qf[D / 16][4];
-        int hi[2], lo[2];  // visible slots of the lane's two rows
+        const int nr = min(ROWS, sq.n * a.G - rt * ROWS);
+        // ---- queries as B fragments: row 8 r + gr
+        uint32_t qf[NR][MT][2];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int r = gr + 8 * i, rr = rt * DEC_ROWS + r, t = rr / a.G, g = rr % a.G;
-            const bool ok = r < nr;
-            const T *src = static_cast<const T *>(a.q) + (ok ? (int64_t)(sq.first + t) * a.ldq + (int64_t)(h * a.G + g) * a.hdq : 0);
-            const int pos = sq.len - sq.n + t;
-            hi[i] = ok ? pos : -1;
-            lo[i] = a.window ? max(0, pos - a.window + 1) : 0;
+        for (int r = 0; r < NR; ++r) {
+            // rows past the last are copies of it: nothing of them is written
+            const int rr = rt * ROWS + min(8 * r + gr, nr - 1), t = rr / a.G, g = rr % a.G;
+            const T *src = static_cast<const T *>(a.q) + (int64_t)(sq.first + t) * a.ldq + (int64_t)(h * a.G + g) * a.hdq;
 #pragma unroll
-            for (int k = 0; k < D / 16; ++k) {
+            for (int k = 0; k < MT; ++k) {
                 if constexpr (!Cfg::Q8) {
-                    qf[k][i] = ok ? *reinterpret_cast<const uint32_t *>(src + 16 * k + 2 * gc) : 0u;
-                    qf[k][i + 2] = ok ? *reinterpret_cast<const uint32_t *>(src + 16 * k + 8 + 2 * gc) : 0u;
+                    qf[r][k][0] = *reinterpret_cast<const uint32_t *>(src + 16 * k + 2 * gc);
+                    qf[r][k][1] = *reinterpret_cast<const uint32_t *>(src + 16 * k + 8 + 2 * gc);
                 } else {  // product 2 j + s of 32-element block j takes the lane's codes 4 s .. 4 s + 3 of its 8
-                    const uint2 v = ok ? *reinterpret_cast<const uint2 *>(src + (k >> 1) * 32 + gc * 8 + (k & 1) * 4)
-                                       : make_uint2(0u, 0u);
-                    qf[k][i] = v.x;
-                    qf[k][i + 2] = v.y;
+                    const uint2 v = *reinterpret_cast<const uint2 *>(src + (k >> 1) * 32 + gc * 8 + (k & 1) * 4);
+                    qf[r][k][0] = v.x;
+                    qf[r][k][1] = v.y;
                 }
             }
         }
-        const int t_first = rt * DEC_ROWS / a.G, t_last = (rt * DEC_ROWS + nr - 1) / a.G;
+        // visible slots of the lane's rows 8 r + 2 gc, + 1
+        int hi[NR][2], lo[NR][2];
+#pragma unroll
+        for (int r = 0; r < NR; ++r)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                hi[r][i] = sq.len - sq.n + (rt * ROWS + min(8 * r + 2 * gc + i, nr - 1)) / a.G;
+                lo[r][i] = a.window ? max(0, hi[r][i] - a.window + 1) : 0;
+            }
+        const int t_first = rt * ROWS / a.G, t_last = (rt * ROWS + nr - 1) / a.G;
         const int hi_min = sq.len - sq.n + t_first;                                               // every row sees up to here
         const int lo_max = a.window ? max(0, sq.len - sq.n + t_last - a.window + 1) : 0;          // and from here
         const int seen_lo = a.window ? max(0, hi_min - a.window + 1) : 0;                         // some row sees from here
-        float o[NT][4];
+        float o[NR][MT][4];  // O^T: columns 16 m + gr, + 8 of rows 8 r + 2 gc, + 1
 #pragma unroll
-        for (int i = 0; i < NT; ++i)
+        for (int r = 0; r < NR; ++r)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) o[i][j] = 0.0f;
-        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) o[r][m][j] = 0.0f;
+        float mx[NR][2], l[NR][2];
+#pragma unroll
+        for (int r = 0; r < NR; ++r) mx[r][0] = mx[r][1] = -INFINITY, l[r][0] = l[r][1] = 0.0f;
 
         for (int blk = con.blk + warp; blk < end; blk += NW) {
             const int key0 = (con.w.kb0 + blk) * DEC_BLK;
             const uint32_t kt = ring + (uint32_t)slot * 2 * Cfg::TILE, vt = kt + Cfg::TILE;
             const uint32_t ks = steps + (uint32_t)slot * 2 * Cfg::STEPS, vs = ks + Cfg::STEPS;
             mbar_wait(bars + 8 * slot, phase);
-            // ---- scores: s[n][*] = slots 8 n + 2 gc, + 1 of rows gr, gr + 8
-            float s[2][4] = {};
+            // ---- scores: s[r][0..1] slot gr, s[r][2..3] slot gr + 8, of rows 8 r + 2 gc, + 1
+            float s[NR][4] = {};
             if constexpr (!Cfg::Q8) {
+                const int row = (lane & 7) + (((lane >> 3) & 1) << 3);
 #pragma unroll
-                for (int k = 0; k < D / 16; ++k) {
-                    const int row = (lane & 7) + ((lane >> 4) << 3), ch = 2 * k + ((lane >> 3) & 1);
+                for (int k = 0; k < MT; ++k) {
+                    const int ch = 2 * k + (lane >> 4);
                     uint32_t f[4];
                     ldmatrix4(kt + (ch >> 3) * DEC_BLK * 128 + row * 128 + (((ch & 7) ^ (row & 7)) << 4), f);
-                    mma16816<T>(s[0], qf[k], f[0], f[1]);
-                    mma16816<T>(s[1], qf[k], f[2], f[3]);
+#pragma unroll
+                    for (int r = 0; r < NR; ++r) mma16816<T>(s[r], f, qf[r][k][0], qf[r][k][1]);
                 }
             } else {
 #pragma unroll
                 for (int j = 0; j < D / 32; ++j) {
+                    uint32_t f0[4], f1[4];  // codes 0..3 and 4..7 of the lane's 8 in the block, slots gr and gr + 8
 #pragma unroll
                     for (int n = 0; n < 2; ++n) {
                         const int row = 8 * n + gr, byte = 32 * j + 8 * gc;
@@ -329,67 +359,78 @@ __global__ void __launch_bounds__(DecCfg<C, D>::NW * 32, 1)
                         uint2 v = lds64(addr);
                         v.x ^= 0x80808080u;
                         v.y ^= 0x80808080u;
+                        f0[n] = codes_to_f16(v.x, 0x4140);
+                        f0[n + 2] = codes_to_f16(v.x, 0x4342);
+                        f1[n] = codes_to_f16(v.y, 0x4140);
+                        f1[n + 2] = codes_to_f16(v.y, 0x4342);
+                    }
+                    // the slots' steps: the codes stay exact integers in the products
+                    const float d0 = half_bits_to_float(lds16(ks + (gr * (D / 32) + j) * 2));
+                    const float d1 = half_bits_to_float(lds16(ks + ((gr + 8) * (D / 32) + j) * 2));
+#pragma unroll
+                    for (int r = 0; r < NR; ++r) {
                         float acc[4] = {};
-                        mma16816<T>(acc, qf[2 * j], codes_to_f16(v.x, 0x4140), codes_to_f16(v.x, 0x4342));
-                        mma16816<T>(acc, qf[2 * j + 1], codes_to_f16(v.y, 0x4140), codes_to_f16(v.y, 0x4342));
-                        // the steps of slots 8 n + 2 gc, + 1: the codes stay exact integers in the products
-                        const float d0 = half_bits_to_float(lds16(ks + ((8 * n + 2 * gc) * (D / 32) + j) * 2));
-                        const float d1 = half_bits_to_float(lds16(ks + ((8 * n + 2 * gc + 1) * (D / 32) + j) * 2));
-                        s[n][0] = fmaf(acc[0], d0, s[n][0]);
-                        s[n][1] = fmaf(acc[1], d1, s[n][1]);
-                        s[n][2] = fmaf(acc[2], d0, s[n][2]);
-                        s[n][3] = fmaf(acc[3], d1, s[n][3]);
+                        mma16816<T>(acc, f0, qf[r][2 * j][0], qf[r][2 * j][1]);
+                        mma16816<T>(acc, f1, qf[r][2 * j + 1][0], qf[r][2 * j + 1][1]);
+                        s[r][0] = fmaf(acc[0], d0, s[r][0]);
+                        s[r][1] = fmaf(acc[1], d0, s[r][1]);
+                        s[r][2] = fmaf(acc[2], d1, s[r][2]);
+                        s[r][3] = fmaf(acc[3], d1, s[r][3]);
                     }
                 }
             }
+            const bool edge = key0 + DEC_BLK - 1 > hi_min || key0 < lo_max;
+            bool grown = false;
+            float mn[NR][2];
 #pragma unroll
-            for (int n = 0; n < 2; ++n)
+            for (int r = 0; r < NR; ++r) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) s[n][j] *= a.scale2;
-            if (key0 + DEC_BLK - 1 > hi_min || key0 < lo_max) {
-#pragma unroll
-                for (int n = 0; n < 2; ++n)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const int key = key0 + 8 * n + 2 * gc + (j & 1), i = j >> 1;
-                        if (key > hi[i] || key < lo[i]) s[n][j] = -INFINITY;
-                    }
-            }
-            // ---- running maximum; the sums are rescaled only where it grew
-            float mn[2];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                float v = fmaxf(fmaxf(s[0][2 * i], s[0][2 * i + 1]), fmaxf(s[1][2 * i], s[1][2 * i + 1]));
-                v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
-                v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
-                mn[i] = fmaxf(m[i], v);
-            }
-            if (__any_sync(0xffffffffu, mn[0] > m[0] || mn[1] > m[1])) {
+                for (int j = 0; j < 4; ++j) {
+                    s[r][j] *= a.scale2;
+                    const int key = key0 + gr + 8 * (j >> 1), i = j & 1;
+                    if (edge && (key > hi[r][i] || key < lo[r][i])) s[r][j] = -INFINITY;
+                }
+                // ---- running maximum over the warp's slots
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    const float f = mn[i] > m[i] ? exp2_approx(m[i] - mn[i]) : 1.0f;  // m = -inf: 0
-                    m[i] = mn[i];
-                    l[i] *= f;
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        o[n][2 * i] *= f;
-                        o[n][2 * i + 1] *= f;
-                    }
+                    float v = fmaxf(s[r][i], s[r][2 + i]);
+                    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+                    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+                    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+                    mn[r][i] = fmaxf(mx[r][i], v);
+                    grown = grown || mn[r][i] > mx[r][i];
                 }
             }
-            uint32_t ph[4], pl[4];  // probabilities as A fragment, hi + lo
+            if (__any_sync(0xffffffffu, grown)) {  // the sums are rescaled only where it grew
 #pragma unroll
-            for (int n = 0; n < 2; ++n)
+                for (int r = 0; r < NR; ++r)
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const float mm = m[i] == -INFINITY ? 0.0f : m[i];
-                    const float p0 = exp2_approx(s[n][2 * i] - mm), p1 = exp2_approx(s[n][2 * i + 1] - mm);
-                    l[i] += p0 + p1;
+                    for (int i = 0; i < 2; ++i) {
+                        const float f = mn[r][i] > mx[r][i] ? exp2_approx(mx[r][i] - mn[r][i]) : 1.0f;  // mx = -inf: 0
+                        mx[r][i] = mn[r][i];
+                        l[r][i] *= f;
+#pragma unroll
+                        for (int m = 0; m < MT; ++m) {
+                            o[r][m][i] *= f;
+                            o[r][m][2 + i] *= f;
+                        }
+                    }
+            }
+            uint32_t ph[NR][2], pl[NR][2];  // probabilities as B fragments, hi + lo
+#pragma unroll
+            for (int r = 0; r < NR; ++r) {
+                const float z0 = mx[r][0] == -INFINITY ? 0.0f : mx[r][0], z1 = mx[r][1] == -INFINITY ? 0.0f : mx[r][1];
+#pragma unroll
+                for (int n = 0; n < 2; ++n) {
+                    const float p0 = exp2_approx(s[r][2 * n] - z0), p1 = exp2_approx(s[r][2 * n + 1] - z1);
+                    l[r][0] += p0;
+                    l[r][1] += p1;
                     const uint32_t hb = pack2<T>(p0, p1);
                     const float2 hf = unpack2<T>(hb);
-                    ph[2 * n + i] = hb;
-                    pl[2 * n + i] = pack2<T>(p0 - hf.x, p1 - hf.y);
+                    ph[r][n] = movmatrix_t(hb);
+                    pl[r][n] = movmatrix_t(pack2<T>(p0 - hf.x, p1 - hf.y));
                 }
+            }
             // slots that no row sees may hold anything: their values are taken as zero
             const bool ragged = key0 + DEC_BLK > sq.len || key0 < seen_lo;
             uint32_t vm[2] = {~0u, ~0u};
@@ -402,25 +443,27 @@ __global__ void __launch_bounds__(DecCfg<C, D>::NW * 32, 1)
                 }
             }
             if constexpr (!Cfg::Q8) {
+                const int row = (lane & 7) + ((lane >> 4) << 3);
 #pragma unroll
-                for (int k = 0; k < D / 16; ++k) {
-                    const int row = (lane & 7) + (((lane >> 3) & 1) << 3), ch = 2 * k + (lane >> 4);
+                for (int m = 0; m < MT; ++m) {
+                    const int ch = 2 * m + ((lane >> 3) & 1);
                     uint32_t f[4];
                     ldmatrix4_t(vt + (ch >> 3) * DEC_BLK * 128 + row * 128 + (((ch & 7) ^ (row & 7)) << 4), f);
                     if (ragged) {
                         f[0] &= vm[0];
-                        f[1] &= vm[1];
-                        f[2] &= vm[0];
+                        f[1] &= vm[0];
+                        f[2] &= vm[1];
                         f[3] &= vm[1];
                     }
-                    mma16816<T>(o[2 * k], ph, f[0], f[1]);
-                    mma16816<T>(o[2 * k], pl, f[0], f[1]);
-                    mma16816<T>(o[2 * k + 1], ph, f[2], f[3]);
-                    mma16816<T>(o[2 * k + 1], pl, f[2], f[3]);
+#pragma unroll
+                    for (int r = 0; r < NR; ++r) {
+                        mma16816<T>(o[r][m], f, ph[r][0], ph[r][1]);
+                        mma16816<T>(o[r][m], f, pl[r][0], pl[r][1]);
+                    }
                 }
             } else {
                 // lane (gr, gc) reads the codes gr * EPR .. of slots 2 gc, 2 gc + 1, 2 gc + 8, 2 gc + 9 in
-                // each panel: product i then covers columns gr * EPR + i
+                // each panel: product i then covers columns gr * EPR + 2 i (first 8 rows of the tile) and + 1
                 constexpr int EPR = Cfg::PANEL / 8;  // 16, or 8 where rows are 64 bytes
 #pragma unroll
                 for (int p = 0; p < Cfg::NP; ++p) {
@@ -440,29 +483,36 @@ __global__ void __launch_bounds__(DecCfg<C, D>::NW * 32, 1)
                     }
                     // the steps of those slots for the 32-element block that holds the lane's columns
                     const int j = (p * 128 + gr * EPR) >> 5;
-                    uint32_t d[2];
+                    __half2 d[2];
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         const uint32_t at = vs + ((2 * gc + 8 * i) * (D / 32) + j) * 2;
-                        d[i] = lds16(at) | lds16(at + (D / 32) * 2) << 16;
+                        const uint32_t b = lds16(at) | lds16(at + (D / 32) * 2) << 16;
+                        d[i] = *reinterpret_cast<const __half2 *>(&b);
                     }
 #pragma unroll
                     for (int e = 0; e < EPR / 4; ++e) {
 #pragma unroll
-                        for (int x = 0; x < 4; ++x) {
-                            uint32_t f[2];
+                        for (int x = 0; x < 2; ++x) {  // bytes 2 x and 2 x + 1 of the words
+                            uint32_t f[4];
 #pragma unroll
                             for (int i = 0; i < 2; ++i) {
-                                // byte x of two slots' words, then each under 0x64
-                                const uint32_t two = prmt(w[2 * i][e], w[2 * i + 1][e], (uint32_t)(x | (4 + x) << 4));
-                                const uint32_t c = codes_to_f16(two, 0x4140);
-                                const __half2 r = __hmul2(*reinterpret_cast<const __half2 *>(&c), *reinterpret_cast<const __half2 *>(&d[i]));
-                                f[i] = *reinterpret_cast<const uint32_t *>(&r);
-                                if (ragged) f[i] &= vm[i];
+                                // (a0, b0, a1, b1) of two slots' bytes, then each pair under 0x64
+                                const uint32_t two = prmt(w[2 * i][e], w[2 * i + 1][e], x ? 0x7362u : 0x5140u);
+#pragma unroll
+                                for (int y = 0; y < 2; ++y) {
+                                    const uint32_t c = codes_to_f16(two, y ? 0x4342 : 0x4140);
+                                    const __half2 v = __hmul2(*reinterpret_cast<const __half2 *>(&c), d[i]);
+                                    f[2 * i + y] = *reinterpret_cast<const uint32_t *>(&v);
+                                    if (ragged) f[2 * i + y] &= vm[i];
+                                }
                             }
-                            const int n = p * 16 + 4 * e + x;
-                            mma16816<T>(o[n], ph, f[0], f[1]);
-                            mma16816<T>(o[n], pl, f[0], f[1]);
+                            const int m = p * (EPR / 2) + 2 * e + x;
+#pragma unroll
+                            for (int r = 0; r < NR; ++r) {
+                                mma16816<T>(o[r][m], f, ph[r][0], ph[r][1]);
+                                mma16816<T>(o[r][m], f, pl[r][0], pl[r][1]);
+                            }
                         }
                     }
                 }
@@ -477,70 +527,72 @@ __global__ void __launch_bounds__(DecCfg<C, D>::NW * 32, 1)
         }
 
         // ---- merge the warps' results
+        float f[NR][2];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
-            l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
-            if (gc == 0) ml[warp * DEC_ROWS + gr + 8 * i] = make_float2(m[i], l[i]);
-        }
+        for (int r = 0; r < NR; ++r)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                l[r][i] += __shfl_xor_sync(0xffffffffu, l[r][i], 4);
+                l[r][i] += __shfl_xor_sync(0xffffffffu, l[r][i], 8);
+                l[r][i] += __shfl_xor_sync(0xffffffffu, l[r][i], 16);
+                if (gr == 0) ml[warp * ROWS + 8 * r + 2 * gc + i] = make_float2(mx[r][i], l[r][i]);
+            }
         __syncthreads();
-        float f[2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            float mx = -INFINITY, sum = 0.0f;
-#pragma unroll
-            for (int w = 0; w < NW; ++w) mx = fmaxf(mx, ml[w * DEC_ROWS + gr + 8 * i].x);
-            const float mz = mx == -INFINITY ? 0.0f : mx;
-#pragma unroll
-            for (int w = 0; w < NW; ++w) {
-                const float2 v = ml[w * DEC_ROWS + gr + 8 * i];
-                sum += v.y * exp2_approx(v.x - mz);
-            }
-            f[i] = sum > 0.0f ? exp2_approx(m[i] - mz) / sum : 0.0f;
-            if (sum != sum) f[i] = sum;  // a NaN score stays one
-        }
         const bool whole = con.blk == 0 && end == con.w.nblk;
-        float *part = a.part + (size_t)(2 * blockIdx.x + (con.blk == 0 ? 1 : 0)) * attn_part_floats(DEC_ROWS, D);
-        if (tid < nr) {
-            float mx = -INFINITY, sum = 0.0f;
-            for (int w = 0; w < NW; ++w) mx = fmaxf(mx, ml[w * DEC_ROWS + tid].x);
-            const float mz = mx == -INFINITY ? 0.0f : mx;
-            for (int w = 0; w < NW; ++w) {
-                const float2 v = ml[w * DEC_ROWS + tid];
-                sum += v.y * exp2_approx(v.x - mz);
-            }
-            const float ls = sum > 0.0f ? mz + log2_approx(sum) : sum == 0.0f ? -INFINITY : sum;
-            const int rr = rt * DEC_ROWS + tid;
-            if (!whole)
-                part[DEC_ROWS * D + tid] = ls;
-            else if (a.lse)
-                a.lse[(int64_t)(sq.first + rr / a.G) * a.Hq + h * a.G + rr % a.G] = ls * LN2;
-        }
+        float *part = a.part + (size_t)(2 * blockIdx.x + (con.blk == 0 ? 1 : 0)) * attn_part_floats(ROWS, D);
 #pragma unroll
-        for (int c0 = 0; c0 < NT; c0 += Cfg::CT) {
-            constexpr int CW = Cfg::CT * 8;
+        for (int r = 0; r < NR; ++r)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int row = 8 * r + 2 * gc + i;
+                float top = -INFINITY, sum = 0.0f;
+#pragma unroll
+                for (int w = 0; w < NW; ++w) top = fmaxf(top, ml[w * ROWS + row].x);
+                const float z = top == -INFINITY ? 0.0f : top;
+#pragma unroll
+                for (int w = 0; w < NW; ++w) {
+                    const float2 v = ml[w * ROWS + row];
+                    sum += v.y * exp2_approx(v.x - z);
+                }
+                f[r][i] = sum > 0.0f ? exp2_approx(mx[r][i] - z) / sum : 0.0f;
+                if (sum != sum) f[r][i] = sum;  // a NaN score stays one
+                if (warp == 0 && gr == 0 && row < nr) {
+                    const float ls = sum > 0.0f ? z + log2_approx(sum) : sum == 0.0f ? -INFINITY : sum;
+                    const int rr = rt * ROWS + row;
+                    if (!whole)
+                        part[ROWS * D + row] = ls;
+                    else if (a.lse)
+                        a.lse[(int64_t)(sq.first + rr / a.G) * a.Hq + h * a.G + rr % a.G] = ls * LN2;
+                }
+            }
+        // two column tiles at a time: [warp][row][32]
+#pragma unroll
+        for (int c0 = 0; c0 < MT; c0 += 2) {
+            constexpr int MW = Cfg::MW;
             if (c0) __syncthreads();
 #pragma unroll
-            for (int n = 0; n < Cfg::CT; ++n)
+            for (int m = 0; m < 2; ++m)
 #pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    *reinterpret_cast<float2 *>(merge + (warp * DEC_ROWS + gr + 8 * i) * CW + 8 * n + 2 * gc) =
-                        make_float2(o[c0 + n][2 * i] * f[i], o[c0 + n][2 * i + 1] * f[i]);
+                for (int r = 0; r < NR; ++r)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)  // place 16 m + 8 (j / 2) + gr: tile c0 + m, its row gr or gr + 8
+                        merge[(warp * ROWS + 8 * r + 2 * gc + (j & 1)) * MW + ((16 * m + 8 * (j >> 1) + gr) ^ (8 * gc))] =
+                            o[r][c0 + m][j] * f[r][j & 1];
             __syncthreads();
-            for (int x = tid; x < nr * CW; x += NW * 32) {
-                const int r = x / CW, j = x % CW;
+            for (int x = tid; x < nr * MW; x += NW * 32) {
+                const int r = x / MW, j = x % MW;
                 float v = 0.0f;
 #pragma unroll
-                for (int w = 0; w < NW; ++w) v += merge[(w * DEC_ROWS + r) * CW + j];
-                const int n = c0 + j / 8, e = j & 7;
+                for (int w = 0; w < NW; ++w) v += merge[(w * ROWS + r) * MW + (j ^ (8 * ((r >> 1) & 3)))];
+                const int m = c0 + j / 16, e = j & 15;
                 int col;
                 if constexpr (!Cfg::Q8) {
-                    col = 8 * n + e;
+                    col = 16 * m + e;
                 } else {
                     constexpr int EPR = Cfg::PANEL / 8;
-                    col = (n / EPR) * Cfg::PANEL + e * EPR + n % EPR;
+                    col = (m / (EPR / 2)) * Cfg::PANEL + (e & 7) * EPR + 2 * (m % (EPR / 2)) + (e >> 3);
                 }
-                const int rr = rt * DEC_ROWS + r;
+                const int rr = rt * ROWS + r;
                 if (!whole) {
                     part[r * D + col] = v;
                 } else {
@@ -562,16 +614,21 @@ __global__ void __launch_bounds__(DecCfg<C, D>::NW * 32, 1)
 
 // Merges the partial results of the items that range boundaries cut.  Block (x, y): the item cut
 // by boundary x + 1, if that is the first boundary inside it; row y.  Partial i carries weight
-// 2^(lse_i - max).
-template <class T, int D>
-__global__ void __launch_bounds__(D) attn_join_kernel(const AttnArgs a, int max_ctas) {
+// 2^(lse_i - max); the warps take every JOIN_WARPS-th partial.
+constexpr int JOIN_WARPS = 8;
+constexpr int JOIN_MAX = 1024;  // ranges (SMs) at most
+
+template <class T, int D, int NR>
+__global__ void __launch_bounds__(JOIN_WARPS * 32) attn_join_kernel(const AttnArgs a, int max_ctas) {
+    constexpr int ROWS = 8 * NR, V = D / 32;
     __shared__ int64_t sh[34];
+    __shared__ float wt[JOIN_MAX], red[JOIN_WARPS], acc[JOIN_WARPS][D];
     griddep_wait();
     griddep_launch_dependents();
-    const int bound = (int)blockIdx.x + 1;
+    const int bound = (int)blockIdx.x + 1, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     int64_t total, at = -1;
     int ctas;
-    const Walk k = walk_find(a, sh, total, ctas, max_ctas, [&](int64_t tot, int n) {
+    const Walk<ROWS> k = walk_find<ROWS>(a, sh, total, ctas, max_ctas, [&](int64_t tot, int n) {
         at = bound < n ? Ranges(tot, n).start(bound) : -1;
         return at;
     });
@@ -580,33 +637,53 @@ __global__ void __launch_bounds__(D) attn_join_kernel(const AttnArgs a, int max_
     const Ranges rg(total, ctas);
     if (bound > 1 && rg.start(bound - 1) > s0) return;  // an earlier boundary joins it
     const int h = k.item / k.w.nrt, rt = k.item % k.w.nrt, r = blockIdx.y;
-    if (r >= min(DEC_ROWS, k.w.sq.n * a.G - rt * DEC_ROWS)) return;
+    if (r >= min(ROWS, k.w.sq.n * a.G - rt * ROWS)) return;
     int last = bound;  // ranges bound - 1 .. last hold the item
     while (last + 1 < ctas && rg.start(last + 1) < s1) ++last;
-    auto part = [&](int c) {  // the first range starts with or before the item, the others inside it
-        const bool head = c == bound - 1;
-        return a.part + (size_t)(2 * c + (head ? 1 : 0)) * attn_part_floats(DEC_ROWS, D);
+    const int parts = last - bound + 2;
+    auto part = [&](int i) {  // the first range starts with or before the item, the others inside it
+        return a.part + (size_t)(2 * (bound - 1 + i) + (i == 0 ? 1 : 0)) * attn_part_floats(ROWS, D);
     };
     float mx = -INFINITY;
-#pragma unroll 8
-    for (int c = bound - 1; c <= last; ++c) mx = fmaxf(mx, part(c)[DEC_ROWS * D + r]);
+    for (int i = tid; i < parts; i += JOIN_WARPS * 32) mx = fmaxf(mx, wt[i] = part(i)[ROWS * D + r]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    if (lane == 0) red[warp] = mx;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < JOIN_WARPS; ++w) mx = fmaxf(mx, red[w]);
     const float mz = mx == -INFINITY ? 0.0f : mx;
-    float sum = 0.0f, v = 0.0f;
-#pragma unroll 8
-    for (int c = bound - 1; c <= last; ++c) {
-        const float *p = part(c);
-        const float w = exp2_approx(p[DEC_ROWS * D + r] - mz);
+    float sum = 0.0f, v[V] = {};
+#pragma unroll 4
+    for (int i = warp; i < parts; i += JOIN_WARPS) {
+        float x[V];
+        load_vec<float, V>(part(i) + r * D + lane * V, x);
+        const float w = exp2_approx(wt[i] - mz);
         sum += w;
-        v = fmaf(w, p[r * D + threadIdx.x], v);
+#pragma unroll
+        for (int e = 0; e < V; ++e) v[e] = fmaf(w, x[e], v[e]);
     }
-    v = sum > 0.0f ? v / sum : sum;
-    const int rr = rt * DEC_ROWS + r;
+#pragma unroll
+    for (int e = 0; e < V; ++e) acc[warp][lane * V + e] = v[e];
+    __syncthreads();  // red has been read
+    if (lane == 0) red[warp] = sum;
+    __syncthreads();
+    sum = 0.0f;
+#pragma unroll
+    for (int w = 0; w < JOIN_WARPS; ++w) sum += red[w];
+    const int rr = rt * ROWS + r;
     const int64_t row = (int64_t)(k.w.sq.first + rr / a.G) * a.Hq + h * a.G + rr % a.G;
-    if (a.out_f32)
-        static_cast<float *>(a.out)[row * D + threadIdx.x] = v;
-    else
-        static_cast<T *>(a.out)[row * D + threadIdx.x] = from_f32<T>(v);
-    if (a.lse && threadIdx.x == 0) a.lse[row] = sum > 0.0f ? (mz + log2_approx(sum)) * LN2 : sum == 0.0f ? -INFINITY : sum;
+    for (int c = tid; c < D; c += JOIN_WARPS * 32) {
+        float x = 0.0f;
+#pragma unroll
+        for (int w = 0; w < JOIN_WARPS; ++w) x += acc[w][c];
+        x = sum > 0.0f ? x / sum : sum;
+        if (a.out_f32)
+            static_cast<float *>(a.out)[row * D + c] = x;
+        else
+            static_cast<T *>(a.out)[row * D + c] = from_f32<T>(x);
+    }
+    if (a.lse && tid == 0) a.lse[row] = sum > 0.0f ? (mz + log2_approx(sum)) * LN2 : sum == 0.0f ? -INFINITY : sum;
 }
 
 // ----------------------------------------------------------------------------- host
@@ -669,23 +746,32 @@ bool attn_tensor_map(CUtensorMap *map, const qg_paged &c, const void *base, int 
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int C, int D>
+template <int C, int D, int NR>
 static int attn_rows_run(const AttnArgs &a, const qg_paged &c, int sms, cudaStream_t s) {
-    using Cfg = DecCfg<C, D>;
+    using Cfg = DecCfg<C, D, NR>;
     static_assert(Cfg::BYTES <= SMEM_MAX, "shared memory of the row kernel");
     CUtensorMap km, vm;
     if (!attn_tensor_map(&km, c, c.k, DEC_BLK) || !attn_tensor_map(&vm, c, c.v, DEC_BLK)) return QG_ECUDA;
-    auto kern = attn_rows_kernel<C, D>;
+    auto kern = attn_rows_kernel<C, D, NR>;
     if (!allow_smem((const void *)kern, Cfg::BYTES)) return QG_ECUDA;
-    if (!launch_programmatic(kern, dim3((unsigned)sms), Cfg::NW * 32, Cfg::BYTES, s, a, km, vm)) return QG_ECUDA;
-    if (sms == 1) return QG_OK;
-    const int rows = (int)std::min<int64_t>(DEC_ROWS, (int64_t)a.bt.tokens * a.G);
-    auto join = attn_join_kernel<typename CacheT<C>::Q, D>;
-    return launch_programmatic(join, dim3((unsigned)(sms - 1), (unsigned)rows), D, 0, s, a, sms) ? QG_OK : QG_ECUDA;
+    const int ctas = std::min(sms, JOIN_MAX);
+    if (!launch_programmatic(kern, dim3((unsigned)ctas), Cfg::NW * 32, Cfg::BYTES, s, a, km, vm)) return QG_ECUDA;
+    if (ctas == 1) return QG_OK;
+    const int rows = (int)std::min<int64_t>(Cfg::ROWS, (int64_t)a.bt.tokens * a.G);
+    auto join = attn_join_kernel<typename CacheT<C>::Q, D, NR>;
+    return launch_programmatic(join, dim3((unsigned)(ctas - 1), (unsigned)rows), JOIN_WARPS * 32, 0, s, a, ctas) ? QG_OK : QG_ECUDA;
 }
-template <int C>
+template <int C, int NR>
 static int attn_rows_dim(const AttnArgs &a, const qg_paged &c, int sms, cudaStream_t s) {
-    return c.dim == 64 ? attn_rows_run<C, 64>(a, c, sms, s) : c.dim == 128 ? attn_rows_run<C, 128>(a, c, sms, s) : attn_rows_run<C, 256>(a, c, sms, s);
+    return c.dim == 64    ? attn_rows_run<C, 64, NR>(a, c, sms, s)
+           : c.dim == 128 ? attn_rows_run<C, 128, NR>(a, c, sms, s)
+                          : attn_rows_run<C, 256, NR>(a, c, sms, s);
+}
+template <int NR>
+static int attn_rows(const AttnArgs &a, const qg_paged &c, int sms, cudaStream_t s) {
+    return c.type == QG_F16    ? attn_rows_dim<CACHE_F16, NR>(a, c, sms, s)
+           : c.type == QG_BF16 ? attn_rows_dim<CACHE_BF16, NR>(a, c, sms, s)
+                               : attn_rows_dim<CACHE_Q8, NR>(a, c, sms, s);
 }
 
 int attn_dev_err_take(unsigned int *err) {
@@ -741,11 +827,7 @@ int qg_attn_paged(const void *q, int64_t ldq, int64_t hdq, int q_type, int token
     cudaStream_t s = (cudaStream_t)stream;
     // one row tile of 16 per sequence and cache head: the row kernel reads the cache once
     if ((int64_t)max_new * a.G > DEC_ROWS) return attn_chunk(a, *cache, static_cast<uint8_t *>(ws), sms, s);
-    switch (cache->type) {
-    case QG_F16: return attn_rows_dim<CACHE_F16>(a, *cache, sms, s);
-    case QG_BF16: return attn_rows_dim<CACHE_BF16>(a, *cache, sms, s);
-    default: return attn_rows_dim<CACHE_Q8>(a, *cache, sms, s);
-    }
+    return (int64_t)max_new * a.G <= 8 ? attn_rows<1>(a, *cache, sms, s) : attn_rows<2>(a, *cache, sms, s);
 }
 
 }  // extern "C"

@@ -972,7 +972,7 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
 }
 
 // Merges the partial results of the items that range boundaries cut: as attn_join_kernel, block
-// (x, y) for the item cut by boundary x + 1 and rows 8 y .. 8 y + 7, one per warp.
+// (x, y) for the item cut by boundary x + 1 and the y-th quarter of its rows, each row by a warp.
 template <class T, int D>
 __global__ void __launch_bounds__(256) attn_chunk_join_kernel(const AttnArgs a, const ChunkPlan plan, int max_ctas) {
     constexpr int ROWS = ChunkCfg<CACHE_F16, D>::ROWS, V = D / 32;
@@ -986,36 +986,43 @@ __global__ void __launch_bounds__(256) attn_chunk_join_kernel(const AttnArgs a, 
     if (k.blk() == 0) return;
     const int64_t s0 = at - k.u, s1 = s0 + CHUNK_OV + k.t.nt;  // the item's units
     if (bound > 1 && chunk_start(total, ctas, bound - 1) > s0 + CHUNK_OV) return;  // an earlier boundary joins it
-    const int lane = threadIdx.x & 31, r = blockIdx.y * 8 + (threadIdx.x >> 5), rr = k.t.row0 + r;
-    if (rr >= k.t.n * a.G) return;
-    auto part = [&](int c) {
-        return a.part + (size_t)(2 * c + (c == bound - 1 ? 1 : 0)) * attn_part_floats(ROWS, D);
+    const int lane = threadIdx.x & 31;
+    auto part = [&](int i) {  // the item is in ranges bound - 1 ..
+        return a.part + (size_t)(2 * (bound - 1 + i) + (i == 0 ? 1 : 0)) * attn_part_floats(ROWS, D);
     };
     int last = bound;
     while (last + 1 < ctas && chunk_start(total, ctas, last + 1) < s1) ++last;
-    float mx = -INFINITY;
-    for (int c = bound - 1; c <= last; ++c) mx = fmaxf(mx, part(c)[(size_t)ROWS * D + r]);
-    const float mz = mx == -INFINITY ? 0.0f : mx;
-    float sum = 0.0f, v[V] = {};
+    const int parts = last - bound + 2;
 #pragma unroll 2
-    for (int c = bound - 1; c <= last; ++c) {
-        const float *p = part(c);
-        const float w = exp2_approx(p[(size_t)ROWS * D + r] - mz);
-        float x[V];
-        load_vec<float, V>(p + (size_t)r * D + lane * V, x);
-        sum += w;
+    for (int r = blockIdx.y * (ROWS / 4) + (threadIdx.x >> 5); r < (blockIdx.y + 1) * (ROWS / 4); r += 8) {
+        const int rr = k.t.row0 + r;
+        if (rr >= k.t.n * a.G) return;
+        float mx = -INFINITY;
+        for (int i = lane; i < parts; i += 32) mx = fmaxf(mx, part(i)[(size_t)ROWS * D + r]);
 #pragma unroll
-        for (int i = 0; i < V; ++i) v[i] = fmaf(w, x[i], v[i]);
+        for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        const float mz = mx == -INFINITY ? 0.0f : mx;
+        float sum = 0.0f, v[V] = {};
+#pragma unroll 4
+        for (int i = 0; i < parts; ++i) {
+            const float *p = part(i);
+            const float w = exp2_approx(p[(size_t)ROWS * D + r] - mz);
+            float x[V];
+            load_vec<float, V>(p + (size_t)r * D + lane * V, x);
+            sum += w;
+#pragma unroll
+            for (int e = 0; e < V; ++e) v[e] = fmaf(w, x[e], v[e]);
+        }
+        const float inv = sum > 0.0f ? 1.0f / sum : sum;
+#pragma unroll
+        for (int e = 0; e < V; ++e) v[e] *= inv;
+        const int64_t row = (int64_t)(k.t.first + rr / a.G) * a.Hq + k.h * a.G + rr % a.G;
+        if (a.out_f32)
+            store_vec<float, V>(static_cast<float *>(a.out) + row * D + lane * V, v);
+        else
+            store_vec<T, V>(static_cast<T *>(a.out) + row * D + lane * V, v);
+        if (a.lse && lane == 0) a.lse[row] = sum > 0.0f ? (mz + log2_approx(sum)) * LN2 : sum == 0.0f ? -INFINITY : sum;
     }
-    const float inv = sum > 0.0f ? 1.0f / sum : sum;
-#pragma unroll
-    for (int i = 0; i < V; ++i) v[i] *= inv;
-    const int64_t row = (int64_t)(k.t.first + rr / a.G) * a.Hq + k.h * a.G + rr % a.G;
-    if (a.out_f32)
-        store_vec<float, V>(static_cast<float *>(a.out) + row * D + lane * V, v);
-    else
-        store_vec<T, V>(static_cast<T *>(a.out) + row * D + lane * V, v);
-    if (a.lse && lane == 0) a.lse[row] = sum > 0.0f ? (mz + log2_approx(sum)) * LN2 : sum == 0.0f ? -INFINITY : sum;
 }
 
 // ----------------------------------------------------------------------------- host
@@ -1059,7 +1066,7 @@ static int chunk_run(const AttnArgs &in, const qg_paged &c, uint8_t *ws, int sms
     if (!launch_programmatic(kern, dim3((unsigned)sms), Cfg::THREADS, Cfg::BYTES, s, a, plan, box, qsign, (int)qcopy, km, vm, qm)) return QG_ECUDA;
     if (sms == 1) return QG_OK;
     auto join = attn_chunk_join_kernel<T, D>;
-    return launch_programmatic(join, dim3((unsigned)(sms - 1), Cfg::ROWS / 8), 256, 0, s, a, plan, sms) ? QG_OK : QG_ECUDA;
+    return launch_programmatic(join, dim3((unsigned)(sms - 1), 4), 256, 0, s, a, plan, sms) ? QG_OK : QG_ECUDA;
 }
 
 template <int C>

@@ -53,17 +53,21 @@ __global__ void __launch_bounds__(1024) norm_residual_kernel(const NormArgs a) {
     const R *res = a.res ? static_cast<const R *>(a.res) + (live ? row : 0) * a.ldres : nullptr;
     const float inv = 1.0f / (float)a.H;
 
-    float t[NV][VEC], r[NV][VEC];
+    // places past the row's end load its start and count as zero: a load under a branch would be
+    // waited for there
+    float t[NV][VEC], r[NV][VEC] = {};
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-        const int i = i0 + j * step;
+    for (int j = 0; j < NV; ++j) load_vec<Y, VEC>(y + (i0 + j * step < a.H ? i0 + j * step : 0), t[j]);
+    if (res) {
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) t[j][e] = r[j][e] = 0.0f;
-        if (live && i < a.H) {
-            load_vec<Y, VEC>(y + i, t[j]);
-            if (res) load_vec<R, VEC>(res + i, r[j]);
-        }
+        for (int j = 0; j < NV; ++j) load_vec<R, VEC>(res + (i0 + j * step < a.H ? i0 + j * step : 0), r[j]);
     }
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+        if (i0 + j * step >= a.H) {
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) t[j][e] = r[j][e] = 0.0f;
+        }
     if (a.w_post) {
         float s = 0.0f;
 #pragma unroll
@@ -73,25 +77,19 @@ __global__ void __launch_bounds__(1024) norm_residual_kernel(const NormArgs a) {
         const float k = rsqrtf(row_sum(s, red[0], warp, w0, nw) * inv + a.eps);
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int i = i0 + j * step;
-            if (i < a.H) {
-                float w[VEC];
-                load_vec<float, VEC>(a.w_post + i, w);
+            float w[VEC];
+            load_vec<float, VEC>(a.w_post + (i0 + j * step < a.H ? i0 + j * step : 0), w);
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) t[j][e] = t[j][e] * k * (a.w_off + w[e]);
-            }
+            for (int e = 0; e < VEC; ++e) t[j][e] = t[j][e] * k * (a.w_off + w[e]);
         }
     }
     if (gate) {
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int i = i0 + j * step;
-            if (i < a.H) {
-                float g[VEC];
-                load_vec<Y, VEC>(gate + i, g);
+            float g[VEC];
+            load_vec<Y, VEC>(gate + (i0 + j * step < a.H ? i0 + j * step : 0), g);
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) t[j][e] *= g[e];
-            }
+            for (int e = 0; e < VEC; ++e) t[j][e] = i0 + j * step < a.H ? t[j][e] * g[e] : 0.0f;
         }
     }
     float s = 0.0f;
