@@ -32,7 +32,10 @@ namespace qg {
 // instead of the 11 (8) bits of one fp16 (bf16) factor.
 constexpr int DEC_ROWS = 16;     // rows of a tile at most (NR = 2)
 constexpr int DEC_BLK = 16;      // slots per block: the least page size
-constexpr int DEC_MIN_BLKS = 8;  // blocks a CTA takes at least: one per warp
+// An item costs its blocks and a fixed part more, in the same unit, for its queries and the merge of the
+// warps; a range that ends inside that part leaves the item to the next CTA.
+constexpr int dec_ov(bool q8) { return q8 ? 12 : 6; }
+constexpr int DEC_MIN_BLKS = 8;  // blocks a CTA takes at least
 
 template <int C, int D, int NR>
 struct DecCfg {
@@ -47,11 +50,11 @@ struct DecCfg {
     // Warps and ring slots: about 190 KB in flight per SM; 8-bit codes take more instructions per byte
     // and get more warps where the accumulators leave registers for them
     static constexpr int NW = D == 256 ? (Q8 ? (NR == 1 ? 12 : 8) : 6) : D == 128 ? (Q8 ? (NR == 1 ? 16 : 12) : 8) : (Q8 ? 16 : 12);
-    static constexpr int ROOM = (222 * 1024 - NW * ROWS * (128 + 8)) / (NW * 2 * (TILE + STEPS));
+    static constexpr int MW = D == 256 && Q8 ? 32 : 64;      // columns merged at a time
+    static constexpr int ROOM = (222 * 1024 - NW * ROWS * (MW * 4 + 8)) / (NW * 2 * (TILE + STEPS));
     static constexpr int S = ROOM > 8 ? 8 : ROOM;
     static constexpr uint32_t RING = (uint32_t)NW * S * 2 * TILE;
     static constexpr uint32_t STEP_AT = RING;
-    static constexpr int MW = 32;                            // columns merged at a time
     static constexpr uint32_t MERGE_AT = STEP_AT + (uint32_t)NW * S * 2 * STEPS;
     static constexpr uint32_t ML_AT = MERGE_AT + (uint32_t)NW * ROWS * MW * 4;
     static constexpr uint32_t BAR_AT = ML_AT + (uint32_t)NW * ROWS * 8;
@@ -60,106 +63,82 @@ struct DecCfg {
 };
 
 // The blocks of one sequence: every item (cache head, row tile) of it has the same slots.
-template <int ROWS>
+template <int ROWS, int OV>
 struct SeqWork {
     Seq sq;
     int nrt;        // row tiles
     int kb0, nblk;  // first block of 16 slots and their number (at least 1)
-    int64_t cost;   // blocks of all items
+    __device__ __forceinline__ SeqWork() {}
+    __device__ __forceinline__ SeqWork(const AttnArgs &a, int b) : sq(seq_of(a.bt, b)) {
+        nrt = (sq.n * a.G + ROWS - 1) / ROWS;
+        const int low = a.window ? max(0, sq.len - sq.n - a.window + 1) : 0;
+        kb0 = low / DEC_BLK;
+        nblk = max(1, (sq.len + DEC_BLK - 1) / DEC_BLK - kb0);
+    }
+    __device__ __forceinline__ int64_t cost(const AttnArgs &a) const { return (int64_t)nrt * a.Hk * (nblk + OV); }
 };
-template <int ROWS>
-__device__ __forceinline__ SeqWork<ROWS> seq_work(const AttnArgs &a, int b) {
-    SeqWork<ROWS> w;
-    w.sq = seq_of(a.bt, b);
-    w.nrt = (w.sq.n * a.G + ROWS - 1) / ROWS;
-    const int low = a.window ? max(0, w.sq.len - w.sq.n - a.window + 1) : 0;
-    w.kb0 = low / DEC_BLK;
-    w.nblk = max(1, (w.sq.len + DEC_BLK - 1) / DEC_BLK - w.kb0);
-    w.cost = (int64_t)w.nrt * a.Hk * w.nblk;
-    return w;
-}
 
 // Position in the work list.
-template <int ROWS>
+template <int ROWS, int OV>
 struct Walk {
-    SeqWork<ROWS> w;
-    int b, item, blk;  // item: cache head * nrt + row tile
-    int64_t left;      // blocks left in this CTA's range
+    SeqWork<ROWS, OV> w;
+    int b, item, u;  // item: cache head * nrt + row tile; unit of the item
+    int64_t left;    // units left in this CTA's range
+    __device__ __forceinline__ int blk() const { return max(0, u - OV); }  // first block of the segment
+    __device__ __forceinline__ int end() const { return (int)min((int64_t)w.nblk, max((int64_t)0, u + left - OV)); }
+    __device__ __forceinline__ void next(const AttnArgs &a) {  // on to the next item; left is 0 at the range's end
+        left -= w.nblk + OV - u;
+        u = 0;
+        if (left <= OV) {  // a rest of OV units or less holds no block
+            left = 0;
+            return;
+        }
+        if (++item < w.nrt * a.Hk) return;
+        item = 0;
+        do {
+            w = SeqWork<ROWS, OV>(a, ++b);
+        } while (w.nrt == 0);  // left > 0: a later sequence has work
+    }
 };
-template <int ROWS>
-__device__ __forceinline__ void walk_next(Walk<ROWS> &k, const AttnArgs &a, int taken) {
-    k.left -= taken;
-    k.blk += taken;
-    if (k.left <= 0 || k.blk < k.w.nblk) return;
-    k.blk = 0;
-    if (++k.item < k.w.nrt * a.Hk) return;
-    k.item = 0;
-    do {
-        k.w = seq_work<ROWS>(a, ++k.b);
-    } while (k.w.cost == 0);  // left > 0: a later sequence has work
-}
 
-// Blocks in all sequences, the number of CTAs that share them, and the position of block
-// `at(total, ctas)` of the list.  Whole CTA; `sh` holds 34 values.
-template <int ROWS, class At>
-__device__ __forceinline__ Walk<ROWS> walk_find(const AttnArgs &a, int64_t *sh, int64_t &total, int &ctas, int max_ctas, At at) {
-    const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5, nwarps = nt >> 5;
-    int64_t mine = 0;
-    for (int b = tid; b < a.bt.batch; b += nt) mine += seq_work<ROWS>(a, b).cost;
-    const int64_t first_cost = mine;  // of sequence tid when one round covers the batch
-    auto scan = [&](int64_t v, int64_t &sum) {  // inclusive prefix over the CTA's threads
+// Units of all sequences; the first `ctas` CTAs share them.  Whole warp: lane i takes every 32nd sequence.
+template <int ROWS, int OV>
+__device__ __forceinline__ int64_t walk_total(const AttnArgs &a) {
+    int64_t n = 0;
+    for (int b = threadIdx.x & 31; b < a.bt.batch; b += 32) n += SeqWork<ROWS, OV>(a, b).cost(a);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+    return n;
+}
+// The position of unit `at` (below the total); whole warp.
+template <int ROWS, int OV>
+__device__ __forceinline__ Walk<ROWS, OV> walk_find(const AttnArgs &a, int64_t at) {
+    const int lane = threadIdx.x & 31;
+    Walk<ROWS, OV> k;
+    int64_t base = 0, rem = 0;
+    for (int c0 = 0;; c0 += 32) {  // ends: at is below the total
+        const int64_t cost = c0 + lane < a.bt.batch ? SeqWork<ROWS, OV>(a, c0 + lane).cost(a) : 0;
+        int64_t v = cost;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int64_t u = __shfl_up_sync(0xffffffffu, v, o);
             if (lane >= o) v += u;
         }
-        __syncthreads();
-        if (lane == 31) sh[warp] = v;
-        __syncthreads();
-        int64_t before = 0;
-        sum = 0;
-        for (int i = 0; i < nwarps; ++i) {
-            if (i < warp) before += sh[i];
-            sum += sh[i];
+        const unsigned m = __ballot_sync(0xffffffffu, base + v > at);
+        if (m || c0 + 32 >= a.bt.batch) {
+            const int l = m ? __ffs(m) - 1 : 31;
+            k.b = min(c0 + l, a.bt.batch - 1);
+            rem = at - base - __shfl_sync(0xffffffffu, v - cost, l);
+            break;
         }
-        return v + before;
-    };
-    int64_t incl = scan(mine, total);
-    ctas = (int)min((int64_t)max_ctas, max((int64_t)1, (total + DEC_MIN_BLKS - 1) / DEC_MIN_BLKS));
-    const int64_t want = at(total, ctas);
-    Walk<ROWS> k;
-    k.b = 0, k.item = 0, k.blk = 0, k.left = 0;
-    if (want < 0 || want >= total) return k;
-    int64_t base = 0;
-    for (int c0 = 0; c0 < a.bt.batch; c0 += nt) {
-        int64_t sum = total, cost = first_cost;
-        if (a.bt.batch > nt) {
-            cost = c0 + tid < a.bt.batch ? seq_work<ROWS>(a, c0 + tid).cost : 0;
-            incl = scan(cost, sum);
-        }
-        const int64_t lo = base + incl - cost;
-        if (want >= lo && want < lo + cost) {  // one thread of one round
-            sh[32] = c0 + tid;
-            sh[33] = want - lo;
-        }
-        base += sum;
-        if (want < base) break;
+        base += __shfl_sync(0xffffffffu, v, 31);
     }
-    __syncthreads();
-    k.b = (int)sh[32];
-    const int64_t rem = sh[33];
-    k.w = seq_work<ROWS>(a, k.b);
-    k.item = (int)(rem / k.w.nblk);
-    k.blk = (int)(rem % k.w.nblk);
+    k.w = SeqWork<ROWS, OV>(a, k.b);
+    k.item = (int)(rem / (k.w.nblk + OV));
+    k.u = (int)(rem % (k.w.nblk + OV));
+    k.left = 0;
     return k;
 }
-// The blocks cut into one range per CTA; range c starts at start(c).
-struct Ranges {
-    int64_t per;
-    int rest, ctas;
-    __device__ __forceinline__ Ranges(int64_t total, int n) : per(total / n), rest((int)(total % n)), ctas(n) {}
-    __device__ __forceinline__ int64_t start(int c) const { return per * c + rest * c / ctas; }
-};
 
 __device__ __forceinline__ void ldmatrix4(uint32_t addr, uint32_t (&r)[4]) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
@@ -198,8 +177,10 @@ __global__ void __launch_bounds__(DecCfg<C, D, NR>::NW * 32, 1)
     using Cfg = DecCfg<C, D, NR>;
     using T = typename CacheT<C>::Q;
     constexpr int NW = Cfg::NW, S = Cfg::S, ROWS = Cfg::ROWS, MT = D / 16;  // MT: column tiles of O^T
+    constexpr int OV = dec_ov(Cfg::Q8);
+    using Walk = qg::Walk<ROWS, OV>;
     extern __shared__ __align__(16) uint8_t dec_smem[];
-    __shared__ int64_t sh[34];
+    __shared__ int64_t sh[2];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t base = (smem_addr(dec_smem) + 1023u) & ~1023u;
     const uint32_t ring = base + (uint32_t)warp * S * 2 * Cfg::TILE;
@@ -215,43 +196,43 @@ __global__ void __launch_bounds__(DecCfg<C, D, NR>::NW * 32, 1)
     __syncwarp();
     griddep_wait();
     griddep_launch_dependents();
-    int64_t total, w0 = 0, w1 = 0;
-    int ctas;
-    Walk<ROWS> con = walk_find<ROWS>(a, sh, total, ctas, (int)gridDim.x, [&](int64_t tot, int n) {
-        if ((int)blockIdx.x >= n) return (int64_t)-1;
-        const Ranges rg(tot, n);
-        w0 = rg.start(blockIdx.x);
-        w1 = rg.start(blockIdx.x + 1);
-        return w0;
-    });
+    if (warp == 0) {
+        const int64_t total = walk_total<ROWS, OV>(a);
+        const int ctas = (int)min((int64_t)gridDim.x, max((int64_t)1, total / (OV + DEC_MIN_BLKS)));
+        if (lane == 0) sh[0] = total, sh[1] = ctas, a.desc[blockIdx.x].parts = 0;
+    }
+    __syncthreads();
+    const Ranges rg(sh[0], (int)sh[1]);
+    if ((int)blockIdx.x >= rg.ctas) return;
+    const int64_t w0 = rg.start(blockIdx.x), w1 = rg.start(blockIdx.x + 1);
     if (w0 >= w1) return;
+    Walk con = walk_find<ROWS, OV>(a, w0);
     con.left = w1 - w0;
+    if (con.end() <= con.blk()) return;  // the range ends before the item's first block
 
     // ---- producer: this warp's next block, its page id fetched one block early
-    Walk<ROWS> pro = con;
-    int pblk = 0, pend = 0, ppage = 0;  // next block and end of the segment; page id of the block
-    auto seg_end = [&](const Walk<ROWS> &k) { return (int)min((int64_t)k.w.nblk, k.blk + k.left); };
-    auto page_of = [&](const Walk<ROWS> &k, int blk) {
-        const int idx = min((k.w.kb0 + blk) * DEC_BLK / a.bt.page, a.bt.table_width - 1);
-        return a.bt.pages[k.b * a.bt.table_stride + idx];
-    };
-    auto pro_seek = [&]() {  // moves on to a segment that has a block for this warp
+    Walk pro = con;
+    const uint32_t mpage = (uint32_t)((0x100000000ull + a.bt.page - 1) / a.bt.page);
+    int pblk = pro.blk() + warp, pend = pro.end(), ppage = 0, pslot = 0, phead = pro.item / pro.w.nrt;
+    auto pro_seek = [&]() {  // moves on to a segment that has a block for this warp, and looks its page up
         while (pro.left > 0 && pblk >= pend) {
-            walk_next(pro, a, pend - pro.blk);
+            pro.next(a);
             if (pro.left > 0) {
-                pblk = pro.blk + warp;
-                pend = seg_end(pro);
+                pblk = pro.blk() + warp;
+                pend = pro.end();
+                phead = pro.item / pro.w.nrt;
             }
         }
-        if (pro.left > 0) ppage = page_of(pro, pblk);
+        if (pro.left > 0) {
+            const int idx = fast_div((pro.w.kb0 + pblk) * DEC_BLK, a.bt.page, mpage, pslot);
+            ppage = a.bt.pages[pro.b * a.bt.table_stride + min(idx, a.bt.table_width - 1)];
+        }
     };
-    pblk = pro.blk + warp;
-    pend = seg_end(pro);
     pro_seek();
     auto issue = [&](int s) {  // all lanes call; lane 0 copies the block into ring slot s
         if (pro.left <= 0) return;
         if (lane == 0) {
-            const int slot = (pro.w.kb0 + pblk) * DEC_BLK % a.bt.page, h = pro.item / pro.w.nrt;
+            const int slot = pslot, h = phead;
             const int page = (unsigned)ppage < (unsigned)a.bt.n_pages ? ppage : a.bt.n_pages;  // out of range: zeros
             const uint32_t kt = ring + (uint32_t)s * 2 * Cfg::TILE, vt = kt + Cfg::TILE, bar = bars + 8 * s;
             const bool st = Cfg::Q8 && page < a.bt.n_pages;
@@ -279,30 +260,34 @@ __global__ void __launch_bounds__(DecCfg<C, D, NR>::NW * 32, 1)
     const int gr = lane >> 2, gc = lane & 3;
     int slot = 0;
     uint32_t phase = 0;
-    while (con.left > 0) {
-        const int end = seg_end(con), taken = end - con.blk;
-        const int h = con.item / con.w.nrt, rt = con.item % con.w.nrt;
-        const Seq sq = con.w.sq;
-        const int nr = min(ROWS, sq.n * a.G - rt * ROWS);
-        // ---- queries as B fragments: row 8 r + gr
-        uint32_t qf[NR][MT][2];
+    // ---- queries as B fragments: row 8 r + gr
+    uint32_t qf[NR][MT][2];
+    auto load_q = [&](const Walk &k) {
+        const int h = k.item / k.w.nrt, rt = k.item % k.w.nrt, nr = min(ROWS, k.w.sq.n * a.G - rt * ROWS);
 #pragma unroll
         for (int r = 0; r < NR; ++r) {
             // rows past the last are copies of it: nothing of them is written
             const int rr = rt * ROWS + min(8 * r + gr, nr - 1), t = rr / a.G, g = rr % a.G;
-            const T *src = static_cast<const T *>(a.q) + (int64_t)(sq.first + t) * a.ldq + (int64_t)(h * a.G + g) * a.hdq;
+            const T *src = static_cast<const T *>(a.q) + (int64_t)(k.w.sq.first + t) * a.ldq + (int64_t)(h * a.G + g) * a.hdq;
 #pragma unroll
-            for (int k = 0; k < MT; ++k) {
+            for (int m = 0; m < MT; ++m) {
                 if constexpr (!Cfg::Q8) {
-                    qf[r][k][0] = *reinterpret_cast<const uint32_t *>(src + 16 * k + 2 * gc);
-                    qf[r][k][1] = *reinterpret_cast<const uint32_t *>(src + 16 * k + 8 + 2 * gc);
+                    qf[r][m][0] = *reinterpret_cast<const uint32_t *>(src + 16 * m + 2 * gc);
+                    qf[r][m][1] = *reinterpret_cast<const uint32_t *>(src + 16 * m + 8 + 2 * gc);
                 } else {  // product 2 j + s of 32-element block j takes the lane's codes 4 s .. 4 s + 3 of its 8
-                    const uint2 v = *reinterpret_cast<const uint2 *>(src + (k >> 1) * 32 + gc * 8 + (k & 1) * 4);
-                    qf[r][k][0] = v.x;
-                    qf[r][k][1] = v.y;
+                    const uint2 v = *reinterpret_cast<const uint2 *>(src + (m >> 1) * 32 + gc * 8 + (m & 1) * 4);
+                    qf[r][m][0] = v.x;
+                    qf[r][m][1] = v.y;
                 }
             }
         }
+    };
+    load_q(con);
+    while (con.left > 0) {
+        const int blk0 = con.blk(), end = con.end();
+        const int h = con.item / con.w.nrt, rt = con.item % con.w.nrt;
+        const Seq sq = con.w.sq;
+        const int nr = min(ROWS, sq.n * a.G - rt * ROWS);
         // visible slots of the lane's rows 8 r + 2 gc, + 1
         int hi[NR][2], lo[NR][2];
 #pragma unroll
@@ -327,7 +312,7 @@ __global__ void __launch_bounds__(DecCfg<C, D, NR>::NW * 32, 1)
 #pragma unroll
         for (int r = 0; r < NR; ++r) mx[r][0] = mx[r][1] = -INFINITY, l[r][0] = l[r][1] = 0.0f;
 
-        for (int blk = con.blk + warp; blk < end; blk += NW) {
+        for (int blk = blk0 + warp; blk < end; blk += NW) {
             const int key0 = (con.w.kb0 + blk) * DEC_BLK;
             const uint32_t kt = ring + (uint32_t)slot * 2 * Cfg::TILE, vt = kt + Cfg::TILE;
             const uint32_t ks = steps + (uint32_t)slot * 2 * Cfg::STEPS, vs = ks + Cfg::STEPS;
@@ -526,7 +511,16 @@ __global__ void __launch_bounds__(DecCfg<C, D, NR>::NW * 32, 1)
             }
         }
 
-        // ---- merge the warps' results
+        // ---- merge the warps' results; the next item's queries come in meanwhile
+        Walk nxt = con;
+        nxt.next(a);
+        if (nxt.left > 0) load_q(nxt);
+        const bool whole = blk0 == 0 && end == con.w.nblk;
+        if (warp == 0 && blk0 == 0 && !whole) {
+            const int64_t s0 = w1 - con.left - con.u;  // the item's first unit
+            const int parts = rg.parts(blockIdx.x, s0 + con.w.nblk + OV);
+            if (lane == 0) a.desc[blockIdx.x] = JoinDesc{parts, sq.first, h, rt * ROWS, sq.n * a.G, {}};
+        }
         float f[NR][2];
 #pragma unroll
         for (int r = 0; r < NR; ++r)
@@ -538,8 +532,7 @@ __global__ void __launch_bounds__(DecCfg<C, D, NR>::NW * 32, 1)
                 if (gr == 0) ml[warp * ROWS + 8 * r + 2 * gc + i] = make_float2(mx[r][i], l[r][i]);
             }
         __syncthreads();
-        const bool whole = con.blk == 0 && end == con.w.nblk;
-        float *part = a.part + (size_t)(2 * blockIdx.x + (con.blk == 0 ? 1 : 0)) * attn_part_floats(ROWS, D);
+        float *part = a.part + (size_t)(2 * blockIdx.x + (blk0 == 0 ? 1 : 0)) * attn_part_floats(ROWS, D);
 #pragma unroll
         for (int r = 0; r < NR; ++r)
 #pragma unroll
@@ -565,13 +558,13 @@ __global__ void __launch_bounds__(DecCfg<C, D, NR>::NW * 32, 1)
                         a.lse[(int64_t)(sq.first + rr / a.G) * a.Hq + h * a.G + rr % a.G] = ls * LN2;
                 }
             }
-        // two column tiles at a time: [warp][row][32]
+        // MW columns at a time: [warp][row][MW]
+        constexpr int MW = Cfg::MW;
 #pragma unroll
-        for (int c0 = 0; c0 < MT; c0 += 2) {
-            constexpr int MW = Cfg::MW;
+        for (int c0 = 0; c0 < MT; c0 += MW / 16) {
             if (c0) __syncthreads();
 #pragma unroll
-            for (int m = 0; m < 2; ++m)
+            for (int m = 0; m < MW / 16; ++m)
 #pragma unroll
                 for (int r = 0; r < NR; ++r)
 #pragma unroll
@@ -605,44 +598,31 @@ __global__ void __launch_bounds__(DecCfg<C, D, NR>::NW * 32, 1)
             }
         }
         __syncthreads();  // ml and merge are free again
-        walk_next(con, a, taken);
+        con = nxt;
     }
     // every copy that was issued has been waited for, unless a wait gave up: let those land
     for (int s = 0; s < S; ++s)
         if (lane == 0) mbar_drain(bars + 8 * s, (s < slot ? phase : phase ^ 1), DRAIN_NS);
 }
 
-// Merges the partial results of the items that range boundaries cut.  Block (x, y): the item cut
-// by boundary x + 1, if that is the first boundary inside it; row y.  Partial i carries weight
-// 2^(lse_i - max); the warps take every JOIN_WARPS-th partial.
+// Merges the partial results of the items that range boundaries cut.  Block (x, y): the item that
+// CTA x described, its row y.  Partial i carries weight 2^(lse_i - max); the warps take every
+// JOIN_WARPS-th partial.
 constexpr int JOIN_WARPS = 8;
 constexpr int JOIN_MAX = 1024;  // ranges (SMs) at most
 
 template <class T, int D, int NR>
-__global__ void __launch_bounds__(JOIN_WARPS * 32) attn_join_kernel(const AttnArgs a, int max_ctas) {
+__global__ void __launch_bounds__(JOIN_WARPS * 32) attn_join_kernel(const AttnArgs a) {
     constexpr int ROWS = 8 * NR, V = D / 32;
-    __shared__ int64_t sh[34];
     __shared__ float wt[JOIN_MAX], red[JOIN_WARPS], acc[JOIN_WARPS][D];
     griddep_wait();
     griddep_launch_dependents();
-    const int bound = (int)blockIdx.x + 1, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    int64_t total, at = -1;
-    int ctas;
-    const Walk<ROWS> k = walk_find<ROWS>(a, sh, total, ctas, max_ctas, [&](int64_t tot, int n) {
-        at = bound < n ? Ranges(tot, n).start(bound) : -1;
-        return at;
-    });
-    if (at < 0 || at >= total || k.blk == 0) return;
-    const int64_t s0 = at - k.blk, s1 = s0 + k.w.nblk;  // the item's blocks
-    const Ranges rg(total, ctas);
-    if (bound > 1 && rg.start(bound - 1) > s0) return;  // an earlier boundary joins it
-    const int h = k.item / k.w.nrt, rt = k.item % k.w.nrt, r = blockIdx.y;
-    if (r >= min(ROWS, k.w.sq.n * a.G - rt * ROWS)) return;
-    int last = bound;  // ranges bound - 1 .. last hold the item
-    while (last + 1 < ctas && rg.start(last + 1) < s1) ++last;
-    const int parts = last - bound + 2;
-    auto part = [&](int i) {  // the first range starts with or before the item, the others inside it
-        return a.part + (size_t)(2 * (bound - 1 + i) + (i == 0 ? 1 : 0)) * attn_part_floats(ROWS, D);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, r = blockIdx.y;
+    const JoinDesc jd = a.desc[blockIdx.x];
+    const int parts = jd.parts, rr = jd.row0 + r;
+    if (parts == 0 || rr >= jd.nrows) return;
+    auto part = [&](int i) {  // the item ends the first range and starts the others
+        return a.part + (size_t)(2 * ((int)blockIdx.x + i) + (i == 0 ? 1 : 0)) * attn_part_floats(ROWS, D);
     };
     float mx = -INFINITY;
     for (int i = tid; i < parts; i += JOIN_WARPS * 32) mx = fmaxf(mx, wt[i] = part(i)[ROWS * D + r]);
@@ -671,8 +651,7 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) attn_join_kernel(const AttnAr
     sum = 0.0f;
 #pragma unroll
     for (int w = 0; w < JOIN_WARPS; ++w) sum += red[w];
-    const int rr = rt * ROWS + r;
-    const int64_t row = (int64_t)(k.w.sq.first + rr / a.G) * a.Hq + h * a.G + rr % a.G;
+    const int64_t row = (int64_t)(jd.first + rr / a.G) * a.Hq + jd.h * a.G + rr % a.G;
     for (int c = tid; c < D; c += JOIN_WARPS * 32) {
         float x = 0.0f;
 #pragma unroll
@@ -759,7 +738,7 @@ static int attn_rows_run(const AttnArgs &a, const qg_paged &c, int sms, cudaStre
     if (ctas == 1) return QG_OK;
     const int rows = (int)std::min<int64_t>(Cfg::ROWS, (int64_t)a.bt.tokens * a.G);
     auto join = attn_join_kernel<typename CacheT<C>::Q, D, NR>;
-    return launch_programmatic(join, dim3((unsigned)(ctas - 1), (unsigned)rows), JOIN_WARPS * 32, 0, s, a, ctas) ? QG_OK : QG_ECUDA;
+    return launch_programmatic(join, dim3((unsigned)(ctas - 1), (unsigned)rows), JOIN_WARPS * 32, 0, s, a) ? QG_OK : QG_ECUDA;
 }
 template <int C, int NR>
 static int attn_rows_dim(const AttnArgs &a, const qg_paged &c, int sms, cudaStream_t s) {
@@ -795,7 +774,7 @@ size_t qg_attn_workspace_size(int dim, int q_heads, int kv_heads, int tokens, in
         return (size_t)-1;
     const int sms = device_sms_planning();
     const size_t rows = (size_t)sms * 2 * attn_part_floats(DEC_ROWS, dim) * sizeof(float);
-    return std::max(rows, attn_chunk_workspace(dim, q_heads / kv_heads, tokens, batch, sms));
+    return (size_t)sms * sizeof(JoinDesc) + std::max(rows, attn_chunk_workspace(dim, q_heads / kv_heads, tokens, batch, sms));
 }
 
 int qg_attn_paged(const void *q, int64_t ldq, int64_t hdq, int q_type, int tokens, int q_heads, int max_new, float scale,
@@ -823,10 +802,11 @@ int qg_attn_paged(const void *q, int64_t ldq, int64_t hdq, int q_type, int token
     a.kc = cache->k, a.vc = cache->v;
     a.page_stride = cache->page_stride, a.head_stride = cache->head_stride, a.slot_stride = cache->slot_stride;
     a.step_stride = cache->step_stride;
-    a.part = static_cast<float *>(ws);
+    a.desc = static_cast<JoinDesc *>(ws);
+    a.part = reinterpret_cast<float *>(a.desc + sms);
     cudaStream_t s = (cudaStream_t)stream;
     // one row tile of 16 per sequence and cache head: the row kernel reads the cache once
-    if ((int64_t)max_new * a.G > DEC_ROWS) return attn_chunk(a, *cache, static_cast<uint8_t *>(ws), sms, s);
+    if ((int64_t)max_new * a.G > DEC_ROWS) return attn_chunk(a, *cache, sms, s);
     return (int64_t)max_new * a.G <= 8 ? attn_rows<1>(a, *cache, sms, s) : attn_rows<2>(a, *cache, sms, s);
 }
 

@@ -10,6 +10,15 @@
 
 namespace qg {
 
+// What the join kernel merges: the item whose first slots a CTA took and whose end it left to others.
+// Every CTA writes its own.
+struct JoinDesc {
+    int parts;        // partial results, in this CTA's range and the ones after (0: nothing to merge)
+    int first, h;     // first token of the sequence, cache head
+    int row0, nrows;  // first row of the tile, rows of the sequence
+    int pad[3];
+};
+
 struct AttnArgs {
     Batch bt;
     const void *q;
@@ -24,10 +33,28 @@ struct AttnArgs {
     const f16 *kd, *vd;
     int64_t page_stride, head_stride, slot_stride, step_stride;
     float *part;       // partial results (attn_part_floats each)
+    JoinDesc *desc;    // one per CTA
 };
 
 // One partial result: rows x D fp32 (normalised), then rows base-2 logarithms of the sums.
 __host__ __device__ constexpr size_t attn_part_floats(int rows, int D) { return (size_t)rows * D + rows; }
+
+// Work units cut into one range per CTA; range c starts at start(c).
+struct Ranges {
+    int64_t per;
+    int rest, ctas;
+    __device__ __forceinline__ Ranges(int64_t total, int n) : per(total / n), rest((int)(total % n)), ctas(n) {}
+    __device__ __forceinline__ int64_t start(int c) const { return per * c + rest * c / ctas; }
+    // Ranges that hold a part of the item that ends before unit s1, of which range c has the first; whole warp.
+    __device__ __forceinline__ int parts(int c, int64_t s1) const {
+        int n = 1;
+        for (int i = c + 1; i < ctas; i += 32) {
+            const int k = i + (threadIdx.x & 31);
+            n += __popc(__ballot_sync(0xffffffffu, k < ctas && start(k) < s1));
+        }
+        return n;
+    }
+};
 
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LN2 = 0.6931471805599453f;
@@ -41,6 +68,17 @@ __device__ __forceinline__ float log2_approx(float x) {
     float y;
     asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+// x / d and x % d for 0 <= x < 2^31 with m = ceil(2^32 / d).
+__device__ __forceinline__ int fast_div(int x, int d, uint32_t m, int &rem) {
+    int q = d == 1 ? x : (int)__umulhi((uint32_t)x, m);
+    rem = x - q * d;
+    if (rem < 0) {
+        --q;
+        rem += d;
+    }
+    return q;
 }
 
 __device__ __forceinline__ uint32_t lds16(uint32_t a) {
@@ -77,7 +115,7 @@ __device__ __forceinline__ uint32_t codes_to_f16(uint32_t biased, uint32_t sel) 
 }
 
 // The chunk kernel (qg_chunk.cu): many rows per sequence, and its workspace.
-int attn_chunk(const AttnArgs &a, const qg_paged &c, uint8_t *ws, int sms, cudaStream_t s);
+int attn_chunk(const AttnArgs &a, const qg_paged &c, int sms, cudaStream_t s);
 size_t attn_chunk_workspace(int D, int G, int tokens, int batch, int sms);
 int attn_chunk_dev_err_take(unsigned int *err);
 

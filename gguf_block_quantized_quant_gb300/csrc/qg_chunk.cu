@@ -117,8 +117,8 @@ constexpr int PLAN_THREADS = 1024;
 
 // An item costs its slot tiles and CHUNK_OV more for loading the queries and writing the result, in
 // the same unit; a range that ends inside that part leaves the item to the next CTA.
-constexpr int CHUNK_OV = 2;
-constexpr int CHUNK_MIN_UNITS = 3;  // a CTA takes at least
+constexpr int CHUNK_OV = 3;
+constexpr int CHUNK_MIN_UNITS = 4;  // a CTA takes at least
 
 // Inclusive prefix of v over the block; sum: the block's total.
 __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t *sh, int64_t &sum) {
@@ -247,21 +247,6 @@ __device__ __forceinline__ void chunk_next(ChunkWalk &k, const ChunkPlan &p, int
 __device__ __forceinline__ int chunk_ctas(int64_t total, int max_ctas) {
     return (int)min((int64_t)max_ctas, max((int64_t)1, total / CHUNK_MIN_UNITS));
 }
-// CTA c takes the units from start(c).
-__device__ __forceinline__ int64_t chunk_start(int64_t total, int ctas, int c) {
-    return total / ctas * c + (int)(total % ctas) * c / ctas;
-}
-
-// x / d and x % d for 0 <= x < 2^31 with m = ceil(2^32 / d).
-__device__ __forceinline__ int fast_div(int x, int d, uint32_t m, int &rem) {
-    int q = d == 1 ? x : (int)__umulhi((uint32_t)x, m);
-    rem = x - q * d;
-    if (rem < 0) {
-        --q;
-        rem += d;
-    }
-    return q;
-}
 
 // ----------------------------------------------------------------------------- kernel
 template <int C, int D>
@@ -318,8 +303,9 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
 
     const int64_t total = *plan.total;
     const int ctas = chunk_ctas(total, gridDim.x);
-    const int64_t w0 = (int)blockIdx.x < ctas ? chunk_start(total, ctas, blockIdx.x) : 0;
-    const int64_t w1 = (int)blockIdx.x < ctas ? chunk_start(total, ctas, blockIdx.x + 1) : 0;
+    const Ranges rg(total, ctas);
+    const int64_t w0 = (int)blockIdx.x < ctas ? rg.start(blockIdx.x) : 0;
+    const int64_t w1 = (int)blockIdx.x < ctas ? rg.start(blockIdx.x + 1) : 0;
     ChunkWalk k{};
     if (w1 > w0) {
         k = chunk_find(plan, *plan.nrt, w0);
@@ -372,6 +358,7 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
             fence_proxy_async_smem();
             mbar_arrive(q_full(q));
         };
+        if (tid == 0) a.desc[blockIdx.x].parts = 0;
         uint32_t done = 0;  // slot tiles of this row tile so far
         if (k.left > 0) fetch_q(k);
         while (k.left > 0) {
@@ -518,6 +505,11 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
                 mbar_wait(pv_done(q, (done - 1) % SB), ((done - 1) / SB) & 1);
                 tc_fence_after();
                 const bool whole = blk0 == 0 && end == k.t.nt;
+                if (warp == 0 && blk0 == 0 && !whole) {
+                    const int64_t s0 = w1 - k.left - k.u;  // the item's first unit
+                    const int parts = rg.parts(blockIdx.x, s0 + k.t.nt + CHUNK_OV);
+                    if (lane == 0) a.desc[blockIdx.x] = JoinDesc{parts, k.t.first, k.h, k.t.row0, k.t.n * a.G, {}};
+                }
                 const float inv = l > 0.0f ? 1.0f / l : l;  // nothing visible: 0
                 const float ls = l > 0.0f ? (m == -INFINITY ? 0.0f : m) * a.scale2 + log2_approx(l) : l == 0.0f ? -INFINITY : l;
                 float *part = a.part + (size_t)(2 * blockIdx.x + (blk0 == 0 ? 1 : 0)) * attn_part_floats(Cfg::ROWS, D);
@@ -972,31 +964,22 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
 }
 
 // Merges the partial results of the items that range boundaries cut: as attn_join_kernel, block
-// (x, y) for the item cut by boundary x + 1 and the y-th quarter of its rows, each row by a warp.
+// (x, y) for the item that CTA x described and the y-th quarter of its rows, each row by a warp.
 template <class T, int D>
-__global__ void __launch_bounds__(256) attn_chunk_join_kernel(const AttnArgs a, const ChunkPlan plan, int max_ctas) {
+__global__ void __launch_bounds__(256) attn_chunk_join_kernel(const AttnArgs a) {
     constexpr int ROWS = ChunkCfg<CACHE_F16, D>::ROWS, V = D / 32;
     griddep_wait();
     griddep_launch_dependents();
-    const int64_t total = *plan.total;
-    const int ctas = chunk_ctas(total, max_ctas), bound = (int)blockIdx.x + 1;
-    if (bound >= ctas) return;
-    const int64_t at = chunk_start(total, ctas, bound);
-    const ChunkWalk k = chunk_find(plan, *plan.nrt, at);
-    if (k.blk() == 0) return;
-    const int64_t s0 = at - k.u, s1 = s0 + CHUNK_OV + k.t.nt;  // the item's units
-    if (bound > 1 && chunk_start(total, ctas, bound - 1) > s0 + CHUNK_OV) return;  // an earlier boundary joins it
-    const int lane = threadIdx.x & 31;
-    auto part = [&](int i) {  // the item is in ranges bound - 1 ..
-        return a.part + (size_t)(2 * (bound - 1 + i) + (i == 0 ? 1 : 0)) * attn_part_floats(ROWS, D);
+    const JoinDesc jd = a.desc[blockIdx.x];
+    const int parts = jd.parts, lane = threadIdx.x & 31;
+    if (parts == 0) return;
+    auto part = [&](int i) {  // the item ends the first range and starts the others
+        return a.part + (size_t)(2 * ((int)blockIdx.x + i) + (i == 0 ? 1 : 0)) * attn_part_floats(ROWS, D);
     };
-    int last = bound;
-    while (last + 1 < ctas && chunk_start(total, ctas, last + 1) < s1) ++last;
-    const int parts = last - bound + 2;
 #pragma unroll 2
     for (int r = blockIdx.y * (ROWS / 4) + (threadIdx.x >> 5); r < (blockIdx.y + 1) * (ROWS / 4); r += 8) {
-        const int rr = k.t.row0 + r;
-        if (rr >= k.t.n * a.G) return;
+        const int rr = jd.row0 + r;
+        if (rr >= jd.nrows) return;
         float mx = -INFINITY;
         for (int i = lane; i < parts; i += 32) mx = fmaxf(mx, part(i)[(size_t)ROWS * D + r]);
 #pragma unroll
@@ -1016,7 +999,7 @@ __global__ void __launch_bounds__(256) attn_chunk_join_kernel(const AttnArgs a, 
         const float inv = sum > 0.0f ? 1.0f / sum : sum;
 #pragma unroll
         for (int e = 0; e < V; ++e) v[e] *= inv;
-        const int64_t row = (int64_t)(k.t.first + rr / a.G) * a.Hq + k.h * a.G + rr % a.G;
+        const int64_t row = (int64_t)(jd.first + rr / a.G) * a.Hq + jd.h * a.G + rr % a.G;
         if (a.out_f32)
             store_vec<float, V>(static_cast<float *>(a.out) + row * D + lane * V, v);
         else
@@ -1037,14 +1020,13 @@ size_t attn_chunk_workspace(int D, int G, int tokens, int batch, int sms) {
 static int gcd(int a, int b) { return b ? gcd(b, a % b) : a; }
 
 template <int C, int D>
-static int chunk_run(const AttnArgs &in, const qg_paged &c, uint8_t *ws, int sms, cudaStream_t s) {
+static int chunk_run(const AttnArgs &in, const qg_paged &c, int sms, cudaStream_t s) {
     using Cfg = ChunkCfg<C, D>;
     using T = typename CacheT<C>::Q;
     static_assert(Cfg::BYTES <= SMEM_MAX, "shared memory of the chunk kernel");
     AttnArgs a = in;
-    a.part = reinterpret_cast<float *>(ws);
     const int64_t tiles = chunk_max_tiles(Cfg::ROWS, a.G, a.bt.tokens, a.bt.batch);
-    const ChunkPlan plan = chunk_plan_at(ws + (size_t)sms * 2 * attn_part_floats(Cfg::ROWS, D) * sizeof(float), tiles);
+    const ChunkPlan plan = chunk_plan_at(reinterpret_cast<uint8_t *>(a.part + (size_t)sms * 2 * attn_part_floats(Cfg::ROWS, D)), tiles);
     // the maximum is taken over unscaled scores: a negative scale goes into the queries' signs, and
     // a scale of zero is a small one (masked scores stay -inf)
     const uint32_t qsign = a.scale2 < 0.0f ? 0x80008000u : 0u;
@@ -1066,17 +1048,17 @@ static int chunk_run(const AttnArgs &in, const qg_paged &c, uint8_t *ws, int sms
     if (!launch_programmatic(kern, dim3((unsigned)sms), Cfg::THREADS, Cfg::BYTES, s, a, plan, box, qsign, (int)qcopy, km, vm, qm)) return QG_ECUDA;
     if (sms == 1) return QG_OK;
     auto join = attn_chunk_join_kernel<T, D>;
-    return launch_programmatic(join, dim3((unsigned)(sms - 1), 4), 256, 0, s, a, plan, sms) ? QG_OK : QG_ECUDA;
+    return launch_programmatic(join, dim3((unsigned)(sms - 1), 4), 256, 0, s, a) ? QG_OK : QG_ECUDA;
 }
 
 template <int C>
-static int chunk_dim(const AttnArgs &a, const qg_paged &c, uint8_t *ws, int sms, cudaStream_t s) {
-    return c.dim == 64 ? chunk_run<C, 64>(a, c, ws, sms, s) : c.dim == 128 ? chunk_run<C, 128>(a, c, ws, sms, s) : chunk_run<C, 256>(a, c, ws, sms, s);
+static int chunk_dim(const AttnArgs &a, const qg_paged &c, int sms, cudaStream_t s) {
+    return c.dim == 64 ? chunk_run<C, 64>(a, c, sms, s) : c.dim == 128 ? chunk_run<C, 128>(a, c, sms, s) : chunk_run<C, 256>(a, c, sms, s);
 }
-int attn_chunk(const AttnArgs &a, const qg_paged &c, uint8_t *ws, int sms, cudaStream_t s) {
-    return c.type == QG_F16    ? chunk_dim<CACHE_F16>(a, c, ws, sms, s)
-           : c.type == QG_BF16 ? chunk_dim<CACHE_BF16>(a, c, ws, sms, s)
-                               : chunk_dim<CACHE_Q8>(a, c, ws, sms, s);
+int attn_chunk(const AttnArgs &a, const qg_paged &c, int sms, cudaStream_t s) {
+    return c.type == QG_F16    ? chunk_dim<CACHE_F16>(a, c, sms, s)
+           : c.type == QG_BF16 ? chunk_dim<CACHE_BF16>(a, c, sms, s)
+                               : chunk_dim<CACHE_Q8>(a, c, sms, s);
 }
 
 int attn_chunk_dev_err_take(unsigned int *err) {

@@ -184,10 +184,10 @@ __device__ __forceinline__ int token_seq(const Batch &bt, int t, int lane) {
 }
 
 constexpr int ROPE_WARPS = 4;
-constexpr int ROPE_U = 4;  // heads whose loads are in flight together
+constexpr int ROPE_U = 2;  // heads whose loads are in flight together
 
 template <class I, int C, int EPL>
-__global__ void __launch_bounds__(ROPE_WARPS * 32) rope_append_kernel(const RopeArgs a) {
+__global__ void __launch_bounds__(ROPE_WARPS * 32, EPL == 8 ? 5 : 8) rope_append_kernel(const RopeArgs a) {
     using Q = typename CacheT<C>::Q;
     constexpr int D = EPL * 32;
     griddep_wait();
