@@ -113,57 +113,51 @@ static ChunkPlan chunk_plan_at(uint8_t *p, int64_t tiles) {
     return c;
 }
 
-constexpr int PLAN_THREADS = 1024;
+constexpr int PLAN_THREADS = 256, PLAN_SEQS = 1024;
 
 // An item costs its slot tiles and CHUNK_OV more for loading the queries and writing the result, in
 // the same unit; a range that ends inside that part leaves the item to the next CTA.
 constexpr int CHUNK_OV = 3;
 constexpr int CHUNK_MIN_UNITS = 4;  // a CTA takes at least
 
-// Inclusive prefix of v over the block; sum: the block's total.
-__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t *sh, int64_t &sum) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int64_t u = __shfl_up_sync(0xffffffffu, v, o);
-        if (lane >= o) v += u;
-    }
-    __syncthreads();
-    if (lane == 31) sh[warp] = v;
-    __syncthreads();
-    int64_t w = lane < PLAN_THREADS / 32 ? sh[lane] : 0;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int64_t u = __shfl_up_sync(0xffffffffu, w, o);
-        if (lane >= o) w += u;
-    }
-    sum = __shfl_sync(0xffffffffu, w, 31);
-    return v + (warp ? __shfl_sync(0xffffffffu, w, warp - 1) : 0);
-}
-
-// One block lists the row tiles of all sequences with their slot ranges.
+// One block lists the row tiles of all sequences with their slot ranges.  It stands before the
+// attention kernel in time, so it is built for few steps: one warp places the sequences' first tiles,
+// then a thread makes a tile and one barrier a prefix of their costs.
 __global__ void __launch_bounds__(PLAN_THREADS) attn_plan_kernel(const AttnArgs a, ChunkPlan p, int rows, int bn, int max_tiles) {
-    __shared__ int64_t sh[32];
-    __shared__ int off[PLAN_THREADS + 1];
+    __shared__ int64_t part[2][PLAN_THREADS / 32];
+    __shared__ int off[PLAN_SEQS + 1];
     griddep_wait();
     griddep_launch_dependents();
-    const int tid = threadIdx.x;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     int64_t cost_before = 0;
-    int tiles_before = 0;
-    for (int c0 = 0; c0 < a.bt.batch; c0 += PLAN_THREADS) {
-        const int nb = min(PLAN_THREADS, a.bt.batch - c0);
-        const int mine = tid < nb ? (seq_of(a.bt, c0 + tid).n * a.G + rows - 1) / rows : 0;
-        int64_t count;
-        const int64_t incl = block_scan(mine, sh, count);
+    int tiles_before = 0, flip = 0;
+    for (int c0 = 0; c0 < a.bt.batch; c0 += PLAN_SEQS) {
+        const int nb = min(PLAN_SEQS, a.bt.batch - c0);
+        if (c0) __syncthreads();
+        if (warp == 0) {
+            int before = 0;
+            for (int b0 = 0; b0 < nb; b0 += 32) {
+                int v = b0 + lane < nb ? (seq_of(a.bt, c0 + b0 + lane).n * a.G + rows - 1) / rows : 0;
+                const int mine = v;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int u = __shfl_up_sync(0xffffffffu, v, o);
+                    if (lane >= o) v += u;
+                }
+                if (b0 + lane < nb) off[b0 + lane] = before + v - mine;
+                before += __shfl_sync(0xffffffffu, v, 31);
+            }
+            if (lane == 0) off[nb] = before;
+        }
         __syncthreads();
-        if (tid == 0) off[0] = 0;
-        off[tid + 1] = (int)incl;
-        __syncthreads();
-        for (int r0 = 0; r0 < (int)count; r0 += PLAN_THREADS) {
-            const int r = r0 + tid;
+        const int count = off[nb];
+        for (int r0 = 0; r0 < count; r0 += PLAN_THREADS) {
+            const int r = r0 + tid, at = tiles_before + r;
             int64_t cost = 0;
             ChunkTile t{};
-            if (r < (int)count) {
+            // q_start that decreases could list more tiles than the call's tokens make: those are left out
+            const bool on = r < count && at < max_tiles;
+            if (on) {
                 int lo = 0, hi = nb;  // off[lo] <= r < off[hi]
                 while (hi - lo > 1) {
                     const int mid = (lo + hi) >> 1;
@@ -178,20 +172,30 @@ __global__ void __launch_bounds__(PLAN_THREADS) attn_plan_kernel(const AttnArgs 
                 const int end = s.len - s.n + tl + 1;  // slots that the last row sees
                 t.kb0 = from / bn;
                 t.nt = max(1, (end + bn - 1) / bn - t.kb0);
-                // q_start that decreases could list more tiles than the call's tokens make: those are left out
-                if (tiles_before + r < max_tiles) cost = (int64_t)(t.nt + CHUNK_OV) * a.Hk;
+                cost = (int64_t)(t.nt + CHUNK_OV) * a.Hk;
             }
-            int64_t sum;
-            const int64_t inc = block_scan(cost, sh, sum);
-            const int at = tiles_before + r;
-            if (r < (int)count && at < max_tiles) {
+            int64_t v = cost;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int64_t u = __shfl_up_sync(0xffffffffu, v, o);
+                if (lane >= o) v += u;
+            }
+            if (lane == 31) part[flip][warp] = v;
+            __syncthreads();
+            int64_t sum = 0;
+#pragma unroll
+            for (int w = 0; w < PLAN_THREADS / 32; ++w) {
+                if (w == warp) v += sum;
+                sum += part[flip][w];
+            }
+            if (on) {
                 p.tile[at] = t;
-                p.prefix[at] = cost_before + inc - cost;
+                p.prefix[at] = cost_before + v - cost;
             }
             cost_before += sum;
+            flip ^= 1;
         }
-        tiles_before += (int)count;
-        __syncthreads();
+        tiles_before += count;
     }
     if (tid == 0) {
         *p.total = cost_before;
@@ -519,50 +523,65 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
                     else if (a.lse)
                         a.lse[(int64_t)(k.t.first + pos - pos0) * a.Hq + k.h * a.G + g] = ls * LN2;
                 }
-                // 32 columns at a time through the warp's own shared memory, so that it writes whole sectors
-                const bool wide = !whole || a.out_f32;
-                const uint32_t st = base + Cfg::OUT_AT + warp * 4096;
-                const int per = wide ? 8 : 4;              // 16-byte chunks of a row's 32 columns
-                const int sub = lane / per, ch = lane % per, rows = 32 / per;
-                uint8_t *dst[8];                           // where the lane's rows go
+                const int mine = rr < nrows ? (k.t.first + pos - pos0) * a.Hq + k.h * a.G + g : -1;  // the thread's row of out
+                if (!whole) {
+                    // columns in groups of 4, rows within: a warp's store is 512 contiguous bytes
+                    float4 *dst = reinterpret_cast<float4 *>(part) + 128 * q + r;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int row = wr + i * rows + sub, orr = row0 + row;
-                    int og;
-                    const int ot = fast_div(min(orr, nrows - 1), a.G, mG, og);
-                    const int64_t orow = (int64_t)(k.t.first + ot) * a.Hq + k.h * a.G + og;
-                    dst[i] = orr >= nrows || i >= per ? nullptr
-                             : !whole ? reinterpret_cast<uint8_t *>(part + (size_t)(128 * q + row) * D)
-                                      : static_cast<uint8_t *>(a.out) + orow * (wide ? D * 4 : D * 2);
-                }
+                    for (int c = 0; c < D; c += 32) {
+                        uint32_t o[32];
+                        tmem_ld32(ocol + c, o);
+                        tmem_wait_ld(o);
+                        if (mine >= 0) {
 #pragma unroll
-                for (int c = 0; c < D; c += 32) {
-                    uint32_t o[32];
-                    tmem_ld32(ocol + c, o);
-                    tmem_wait_ld(o);
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * inv);
-                    if (wide) {
-#pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            sts128(st + lane * 128 + ((i ^ (lane & 7)) << 4), o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            sts128(st + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4), pack2<T>(__uint_as_float(o[8 * i]), __uint_as_float(o[8 * i + 1])),
-                                   pack2<T>(__uint_as_float(o[8 * i + 2]), __uint_as_float(o[8 * i + 3])),
-                                   pack2<T>(__uint_as_float(o[8 * i + 4]), __uint_as_float(o[8 * i + 5])),
-                                   pack2<T>(__uint_as_float(o[8 * i + 6]), __uint_as_float(o[8 * i + 7])));
-                    }
-                    __syncwarp();
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        if (dst[i]) {
-                            const int row = i * rows + sub;
-                            *reinterpret_cast<uint4 *>(dst[i] + (wide ? 4 * c : 2 * c) + 16 * ch) =
-                                lds128(wide ? st + row * 128 + ((ch ^ (row & 7)) << 4) : st + row * 64 + ((ch ^ ((row >> 1) & 3)) << 4));
+                            for (int i = 0; i < 8; ++i)
+                                dst[(c / 4 + i) * Cfg::ROWS] = make_float4(__uint_as_float(o[4 * i]) * inv, __uint_as_float(o[4 * i + 1]) * inv,
+                                                                           __uint_as_float(o[4 * i + 2]) * inv, __uint_as_float(o[4 * i + 3]) * inv);
                         }
-                    __syncwarp();
+                    }
+                } else {
+                    // 128 bytes of each row at a time through the warp's own shared memory, so that a store
+                    // writes whole lines of 4 rows
+                    const uint32_t st = base + Cfg::OUT_AT + warp * 4096;
+                    auto flush = [&](int at, int pitch) {  // bytes `at` .. of rows of `pitch` bytes
+                        __syncwarp();
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const int row = 4 * i + lane / 8, orow = __shfl_sync(0xffffffffu, mine, row);
+                            const uint4 v = lds128(st + row * 128 + (((lane & 7) ^ (row & 7)) << 4));
+                            if (orow >= 0) *reinterpret_cast<uint4 *>(static_cast<uint8_t *>(a.out) + (int64_t)orow * pitch + at + 16 * (lane & 7)) = v;
+                        }
+                        __syncwarp();
+                    };
+#pragma unroll
+                    for (int c = 0; c < D; c += 64) {
+                        uint32_t o[2][32];
+                        tmem_ld32(ocol + c, o[0]);
+                        tmem_ld32(ocol + c + 32, o[1]);
+                        tmem_wait_ld(o[0]);
+                        tmem_loaded(o[1]);
+#pragma unroll
+                        for (int x = 0; x < 2; ++x)
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) o[x][i] = __float_as_uint(__uint_as_float(o[x][i]) * inv);
+                        if (a.out_f32) {
+#pragma unroll
+                            for (int x = 0; x < 2; ++x) {
+#pragma unroll
+                                for (int i = 0; i < 8; ++i)
+                                    sts128(st + lane * 128 + ((i ^ (lane & 7)) << 4), o[x][4 * i], o[x][4 * i + 1], o[x][4 * i + 2], o[x][4 * i + 3]);
+                                flush((c + 32 * x) * 4, D * 4);
+                            }
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                const uint32_t *v = &o[i / 4][8 * (i % 4)];
+                                auto two = [&](int e) { return pack2<T>(__uint_as_float(v[e]), __uint_as_float(v[e + 1])); };
+                                sts128(st + lane * 128 + ((i ^ (lane & 7)) << 4), two(0), two(2), two(4), two(6));
+                            }
+                            flush(c * 2, D * 2);
+                        }
+                    }
                 }
                 tc_fence_before();  // the next item's products overwrite O once its P arrives
             } else if (nk.left > 0) {
@@ -598,8 +617,8 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
                 }
             }
         };
-        // S = Q K^T of slot tile j of the segment, whose keys are the next units
-        auto scores = [&](int j, bool both) {
+        // S = Q K^T of slot tile j of the segment, whose keys are units u ..
+        auto scores = [&](int j, bool both, uint32_t u) {
             const uint32_t t = n + j, buf = t % SB;
             // the buffer's last scores have been read, and P that took their place
             if constexpr (Cfg::S_TURNS) {
@@ -623,9 +642,9 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
             }
             const uint32_t dst = warp_uniform(s_col + buf * BN);
 #pragma unroll
-            for (int h = 0; h < KU; ++h, ++units) {
-                const uint32_t slot = units % NS;
-                mbar_wait(kv_full(slot), (units / NS) & 1);
+            for (int h = 0; h < KU; ++h, ++u) {
+                const uint32_t slot = u % NS;
+                mbar_wait(kv_full(slot), (u / NS) & 1);
                 tc_fence_after();
                 const uint32_t kd = warp_uniform((uint32_t)umma_desc_kmajor_sw128(kv0 + slot * Cfg::TILE));
                 const uint32_t qd = q_desc + h * Cfg::PKU * (128 * 128 / 16);
@@ -638,27 +657,26 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
                 umma_commit_w(leader, kv_empty(slot));
             }
         };
-        auto product = [&](uint32_t t, bool fresh) {  // O (+)= P V of slot tile t, whose values are the next units
+        // O (+)= P V over a half of slot tile t, whose values are units u ..
+        auto product = [&](uint32_t t, bool fresh, uint32_t u, auto which) {
+            constexpr int half = decltype(which)::value;
             const uint32_t buf = t % SB, src = warp_uniform(p_col + (Cfg::P_OVER ? buf * BN : 0));
+            const uint32_t slot = (KU == 2 ? u + half : u) % NS, phase = ((KU == 2 ? u + half : u) / NS) & 1;
+            mbar_wait(kv_full(slot), phase);
+            const uint32_t vd = warp_uniform((uint32_t)umma_desc_mnmajor_sw128(kv0 + slot * Cfg::TILE, VR * 128));
+            mbar_wait(half ? p_full(q, buf) : p_half(q, buf), (t / SB) & 1);
+            tc_fence_after();
+            __syncwarp();
 #pragma unroll
-            for (int h = 0; h < KU; ++h, ++units) {
-                const uint32_t slot = units % NS;
-                mbar_wait(kv_full(slot), (units / NS) & 1);
-                const uint32_t vd = warp_uniform((uint32_t)umma_desc_mnmajor_sw128(kv0 + slot * Cfg::TILE, VR * 128));
-#pragma unroll
-                for (int i = 0; i < VR / 16; ++i) {
-                    const int p = h * (VR / 16) + i;  // 16 slots of P
-                    if (p == 0 || p == BN / 32) {
-                        mbar_wait(p ? p_full(q, buf) : p_half(q, buf), (t / SB) & 1);
-                        tc_fence_after();
-                        __syncwarp();
-                    }
-                    umma_f16_ta_w(leader, o_col, src + 8 * p, vd + i * (2048 / 16), desc_hi, id_o, p ? 1u : !fresh);
-                }
-                if (h == KU - 1) umma_commit_w(leader, pv_done(q, buf));
-                umma_commit_w(leader, kv_empty(slot));
+            for (int i = 0; i < BN / 32; ++i) {
+                const int p = half * (BN / 32) + i;  // 16 slots of P
+                umma_f16_ta_w(leader, o_col, src + 8 * p, vd + (KU == 2 ? i : p) * (2048 / 16), desc_hi, id_o, p ? 1u : !fresh);
             }
+            if (half) umma_commit_w(leader, pv_done(q, buf));
+            if (half || KU == 2) umma_commit_w(leader, kv_empty(slot));
         };
+        using First = std::integral_constant<int, 0>;
+        using Second = std::integral_constant<int, 1>;
         while (k.left > 0) {
             const int taken = k.end() - k.blk();
             ++seg;
@@ -666,14 +684,21 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
                 mbar_wait(q_full(q), items & 1);
                 ++items;
                 const bool both = NQ == 2 && k.t.row0 + 128 < k.t.n * a.G;
-                scores(0, both);
+                scores(0, both, units);
+                uint32_t u = units + KU;
                 for (int j = 0; j < taken; ++j) {
-                    if (j + 1 < taken) scores(j + 1, both);
-                    product(n + j, j == 0);
+                    const bool more = j + 1 < taken;
+                    const uint32_t v = more ? u + KU : u;  // the values come after the next keys
+                    if (SB == 1) product(n + j, j == 0, v, First{});
+                    if (more) scores(j + 1, both, u);
+                    if (SB == 2) product(n + j, j == 0, v, First{});
+                    product(n + j, j == 0, v, Second{});
+                    u = v + KU;
                 }
+                units = u;
+                n += taken;
                 both_before = both;
                 if (both || q == 1) other += taken;
-                n += taken;
             } else {  // no rows in this tile: its share of every unit's release
                 other += taken;
                 for (int j = 0; j < 2 * KU * taken; ++j, ++units) {
@@ -775,8 +800,8 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
         // ------------------------------------------------------------ 8-bit codes to fp16 tiles
         // Thread ct converts the 16-code chunks i * 128 + ct of its warpgroup's units.  A block of 16 slots is
         // always in one page: lane b of each warp looks up block b of a tile, one tile ahead of the codes'
-        // loads, and leaves its offsets in a table of the warp's own; the loads of a unit are in flight
-        // while the warpgroup converts its unit before.
+        // loads, and leaves its offsets in a table of the warp's own.  The codes of the warpgroup's next
+        // unit are loaded chunk by chunk as this one's are converted.
         set_max_regs<Cfg::CONV_REGS >= Cfg::LAUNCH_REGS, Cfg::CONV_REGS>();
         const int cw = (warp - Cfg::CONV_WARP) / 4, ct = (tid - Cfg::CONV_WARP * 32) & 127;
         constexpr int PER = Cfg::TILE / 32 / 128;  // 16-code chunks per thread
@@ -852,39 +877,42 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
                 locate();
             }
         };
-        auto fetch_as = [&](Raw &w, const Unit &u, auto is_val) {
-            constexpr bool VAL = decltype(is_val)::value;
-            constexpr int CPR = VAL ? VC : KC, RPS = 128 / CPR;  // rows of a step of i
-            const bool last = !VAL || vt == kt;
+        // Where chunk i of a unit is read: set once per unit
+        struct From {
+            const int8_t *codes;
+            const uint16_t *steps;
+            uint32_t table;
+            int lg, row0, ch0, key0, seen_lo, len;
+            bool on, edge;
+        };
+        auto from_of = [&](const Unit &u) {
+            From f{};
+            f.on = u.on;
+            const bool last = !u.val || vt == kt;
             const Bounds p = last ? cur : prev;
-            const uint32_t table = places + (last ? flip : flip ^ 128);
-            const int8_t *codes = static_cast<const int8_t *>(VAL ? a.vc : a.kc);
-            const uint16_t *steps = reinterpret_cast<const uint16_t *>(VAL ? a.vd : a.kd);
-            const int row0 = VAL ? u.h * VR : 0, r0 = ct / CPR, ch = (VAL ? 0 : u.h * KC) + ct % CPR;
-            const bool edge = p.key0 < p.seen_lo || p.key0 + BN > p.len;
-            w.ok = 0;
-#pragma unroll
-            for (int i = 0; i < PER; ++i) {
-                // the step's rows lie in one block of 16, or in two where 32 rows make a step (dim 64)
-                const int row = row0 + i * RPS + r0, in = row & 15;
-                const uint4 t = lds128(table + (row >> 4) * 16);
-                const int64_t o = (int64_t)((uint64_t)t.y << 32 | t.x), d = (int64_t)((uint64_t)t.w << 32 | t.z);
-                bool ok = o >= 0;
-                if (edge) ok = ok && p.key0 + row >= p.seen_lo && p.key0 + row < p.len;
-                w.ok |= (uint32_t)ok << i;
-                // every load runs (page 0 where there is no slot): a load under a branch would be waited for there
-                w.c[i] = *reinterpret_cast<const uint4 *>(codes + (ok ? o : 0) + in * a.slot_stride + 16 * ch);
-                w.d[i] = steps[(ok ? d : 0) + in * (D / 32) + ch / 2];
-            }
+            f.table = places + (last ? flip : flip ^ 128);
+            f.codes = static_cast<const int8_t *>(u.val ? a.vc : a.kc);
+            f.steps = reinterpret_cast<const uint16_t *>(u.val ? a.vd : a.kd);
+            f.lg = u.val ? (D == 64 ? 2 : D == 128 ? 3 : 4) : (D == 64 ? 2 : 3);  // log2 of a row's chunks
+            f.row0 = u.val ? u.h * VR : 0;
+            f.ch0 = u.val ? 0 : u.h * KC;
+            f.key0 = p.key0, f.seen_lo = p.seen_lo, f.len = p.len;
+            f.edge = p.key0 < p.seen_lo || p.key0 + BN > p.len;
+            return f;
         };
-        auto fetch = [&](Raw &w, const Unit &u) {
-            if (!u.on) return;
-            if (u.val)
-                fetch_as(w, u, std::true_type{});
-            else
-                fetch_as(w, u, std::false_type{});
+        auto fetch1 = [&](Raw &w, const From &f, int i) {
+            const int x = i * 128 + ct, row = f.row0 + (x >> f.lg), ch = f.ch0 + (x & ((1 << f.lg) - 1)), in = row & 15;
+            const uint4 t = lds128(f.table + (row >> 4) * 16);
+            const int64_t o = (int64_t)((uint64_t)t.y << 32 | t.x), d = (int64_t)((uint64_t)t.w << 32 | t.z);
+            bool ok = o >= 0;
+            if (f.edge) ok = ok && f.key0 + row >= f.seen_lo && f.key0 + row < f.len;
+            w.ok = (w.ok & ~(1u << i)) | (uint32_t)ok << i;
+            // every load runs (page 0 where there is no slot): a load under a branch would be waited for there
+            w.c[i] = *reinterpret_cast<const uint4 *>(f.codes + (ok ? o : 0) + in * a.slot_stride + 16 * ch);
+            w.d[i] = f.steps[(ok ? d : 0) + in * (D / 32) + ch / 2];
         };
-        auto put_as = [&](const Raw &w, uint32_t dst, auto is_val) {
+        // Converts the unit in w into its place and refills w with the next one's codes, chunk by chunk
+        auto put_as = [&](Raw &w, uint32_t dst, const From &next, auto is_val) {
             constexpr bool VAL = decltype(is_val)::value;
             constexpr int CPR = VAL ? VC : KC, RPS = 128 / CPR;
             constexpr uint32_t PSTRIDE = (VAL ? VR : BN) * 128;
@@ -909,50 +937,43 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
 #pragma unroll
                 for (int y = 0; y < 2; ++y)
                     sts128(row_at + (((2 * (ch & 3) + y) ^ (row & 7)) << 4), h[4 * y], h[4 * y + 1], h[4 * y + 2], h[4 * y + 3]);
+                if (next.on) fetch1(w, next, i);
             }
         };
-        auto put = [&](const Raw &w, const Unit &u, uint32_t n) {  // unit number n
-            const uint32_t slot = n % NS;
-            if (n >= NS) mbar_wait(kv_empty(slot), (n / NS - 1) & 1);
-            if (u.val)
-                put_as(w, kv0 + slot * Cfg::TILE, std::true_type{});
-            else
-                put_as(w, kv0 + slot * Cfg::TILE, std::false_type{});
-            fence_proxy_async_smem();
-            mbar_arrive(kv_full(slot));
-        };
-        Raw ra, rb;
+        Raw raw;
+        raw.ok = 0;
         lookup();
         locate();
-        // every unit is listed by every warpgroup, each fetches its own
+        // every unit is listed by every warpgroup, each takes its own
         uint32_t n = 0;  // number of unit un
         next_unit();
-        auto own_unit = [&](bool first) {
-            if (!first) {
-                next_unit();
-                ++n;
-            }
+        auto own_unit = [&]() {
             while (un.on && (int)(n % Cfg::NCONV) != cw) {
                 next_unit();
                 ++n;
             }
         };
-        own_unit(true);
-        Unit ua = un, ub;
-        uint32_t na = n, nb;
-        fetch(ra, ua);
-        while (ua.on) {
-            own_unit(false);
-            ub = un;
-            nb = n;
-            fetch(rb, ub);
-            put(ra, ua, na);
-            if (!ub.on) break;
-            own_unit(false);
-            ua = un;
-            na = n;
-            fetch(ra, ua);
-            put(rb, ub, nb);
+        own_unit();
+        if (un.on) {
+            const From f = from_of(un);
+#pragma unroll
+            for (int i = 0; i < PER; ++i) fetch1(raw, f, i);
+        }
+        while (un.on) {
+            const Unit u = un;
+            const uint32_t slot = n % NS;
+            const uint32_t round = n / NS;
+            next_unit();
+            ++n;
+            own_unit();
+            const From f = from_of(un);
+            if (round > 0) mbar_wait(kv_empty(slot), (round - 1) & 1);
+            if (u.val)
+                put_as(raw, kv0 + slot * Cfg::TILE, f, std::true_type{});
+            else
+                put_as(raw, kv0 + slot * Cfg::TILE, f, std::false_type{});
+            fence_proxy_async_smem();
+            mbar_arrive(kv_full(slot));
         }
     }
     tc_fence_before();
@@ -964,10 +985,11 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
 }
 
 // Merges the partial results of the items that range boundaries cut: as attn_join_kernel, block
-// (x, y) for the item that CTA x described and the y-th quarter of its rows, each row by a warp.
+// (x, y) for the item that CTA x described, its y-th share.  Rows past the last hold nothing: theirs
+// are read but not written.
 template <class T, int D>
 __global__ void __launch_bounds__(256) attn_chunk_join_kernel(const AttnArgs a) {
-    constexpr int ROWS = ChunkCfg<CACHE_F16, D>::ROWS, V = D / 32;
+    constexpr int ROWS = ChunkCfg<CACHE_F16, D>::ROWS;
     griddep_wait();
     griddep_launch_dependents();
     const JoinDesc jd = a.desc[blockIdx.x];
@@ -976,35 +998,35 @@ __global__ void __launch_bounds__(256) attn_chunk_join_kernel(const AttnArgs a) 
     auto part = [&](int i) {  // the item ends the first range and starts the others
         return a.part + (size_t)(2 * ((int)blockIdx.x + i) + (i == 0 ? 1 : 0)) * attn_part_floats(ROWS, D);
     };
-#pragma unroll 2
-    for (int r = blockIdx.y * (ROWS / 4) + (threadIdx.x >> 5); r < (blockIdx.y + 1) * (ROWS / 4); r += 8) {
-        const int rr = jd.row0 + r;
-        if (rr >= jd.nrows) return;
+    // a warp takes a group of 4 columns of 32 rows, as they were written
+    const int warp = threadIdx.x >> 5;
+    constexpr int RG = ROWS / 32, CG = D / 4;  // row groups, column groups
+    for (int x = blockIdx.y * 8 + warp; x < RG * CG; x += 8 * gridDim.y) {
+        const int r = (x / CG) * 32 + lane, c = x % CG, rr = jd.row0 + r;
+        if (jd.row0 + (x / CG) * 32 >= jd.nrows) break;
         float mx = -INFINITY;
-        for (int i = lane; i < parts; i += 32) mx = fmaxf(mx, part(i)[(size_t)ROWS * D + r]);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        for (int i = 0; i < parts; ++i) mx = fmaxf(mx, part(i)[(size_t)ROWS * D + r]);
         const float mz = mx == -INFINITY ? 0.0f : mx;
-        float sum = 0.0f, v[V] = {};
+        float sum = 0.0f, v[4] = {};
 #pragma unroll 4
         for (int i = 0; i < parts; ++i) {
             const float *p = part(i);
             const float w = exp2_approx(p[(size_t)ROWS * D + r] - mz);
-            float x[V];
-            load_vec<float, V>(p + (size_t)r * D + lane * V, x);
+            const float4 o = reinterpret_cast<const float4 *>(p)[c * ROWS + r];
             sum += w;
-#pragma unroll
-            for (int e = 0; e < V; ++e) v[e] = fmaf(w, x[e], v[e]);
+            v[0] = fmaf(w, o.x, v[0]), v[1] = fmaf(w, o.y, v[1]), v[2] = fmaf(w, o.z, v[2]), v[3] = fmaf(w, o.w, v[3]);
         }
         const float inv = sum > 0.0f ? 1.0f / sum : sum;
 #pragma unroll
-        for (int e = 0; e < V; ++e) v[e] *= inv;
-        const int64_t row = (int64_t)(jd.first + rr / a.G) * a.Hq + jd.h * a.G + rr % a.G;
-        if (a.out_f32)
-            store_vec<float, V>(static_cast<float *>(a.out) + row * D + lane * V, v);
-        else
-            store_vec<T, V>(static_cast<T *>(a.out) + row * D + lane * V, v);
-        if (a.lse && lane == 0) a.lse[row] = sum > 0.0f ? (mz + log2_approx(sum)) * LN2 : sum == 0.0f ? -INFINITY : sum;
+        for (int e = 0; e < 4; ++e) v[e] *= inv;
+        if (rr < jd.nrows) {
+            const int64_t row = (int64_t)(jd.first + rr / a.G) * a.Hq + jd.h * a.G + rr % a.G;
+            if (a.out_f32)
+                store_vec<float, 4>(static_cast<float *>(a.out) + row * D + 4 * c, v);
+            else
+                store_vec<T, 4>(static_cast<T *>(a.out) + row * D + 4 * c, v);
+            if (a.lse && c == 0) a.lse[row] = sum > 0.0f ? (mz + log2_approx(sum)) * LN2 : sum == 0.0f ? -INFINITY : sum;
+        }
     }
 }
 
@@ -1048,7 +1070,7 @@ static int chunk_run(const AttnArgs &in, const qg_paged &c, int sms, cudaStream_
     if (!launch_programmatic(kern, dim3((unsigned)sms), Cfg::THREADS, Cfg::BYTES, s, a, plan, box, qsign, (int)qcopy, km, vm, qm)) return QG_ECUDA;
     if (sms == 1) return QG_OK;
     auto join = attn_chunk_join_kernel<T, D>;
-    return launch_programmatic(join, dim3((unsigned)(sms - 1), 4), 256, 0, s, a) ? QG_OK : QG_ECUDA;
+    return launch_programmatic(join, dim3((unsigned)(sms - 1), 16), 256, 0, s, a) ? QG_OK : QG_ECUDA;
 }
 
 template <int C>
