@@ -799,8 +799,6 @@ int qg_attn_paged(const void *q, int64_t ldq, int64_t hdq, int q_type, int token
     a.window = window;
     a.scale2 = scale * LOG2E;
     a.kd = static_cast<const f16 *>(cache->kd), a.vd = static_cast<const f16 *>(cache->vd);
-    a.kc = cache->k, a.vc = cache->v;
-    a.page_stride = cache->page_stride, a.head_stride = cache->head_stride, a.slot_stride = cache->slot_stride;
     a.step_stride = cache->step_stride;
     a.desc = static_cast<JoinDesc *>(ws);
     a.part = reinterpret_cast<float *>(a.desc + sms);

@@ -29,9 +29,8 @@ struct AttnArgs {
     int out_f32;       // out is fp32 instead of the queries' type
     int window;        // 0: none
     float scale2;      // scale * log2(e): the kernels work in powers of two
-    const void *kc, *vc;  // pools (read directly by the 8-bit chunk kernel)
     const f16 *kd, *vd;
-    int64_t page_stride, head_stride, slot_stride, step_stride;
+    int64_t step_stride;
     float *part;       // partial results (attn_part_floats each)
     JoinDesc *desc;    // one per CTA
 };

@@ -5,8 +5,8 @@
 // that share a cache head share each slot's copy.  A CTA multiplies NQ tiles of 128 rows with tiles
 // of BN slots:
 //   * producer: one warp copies the key and value tiles through the page table, a tiled TMA copy
-//     per page and 128-byte panel (pages end inside a tile); with 8-bit caches four warps fetch
-//     the codes instead and write step * code as fp16;
+//     per page and 128-byte panel (pages end inside a tile); from 8-bit caches it copies codes and
+//     steps, which one or two more warpgroups turn into tiles of step * code in fp16;
 //   * MMA warp: scores S = Q K^T (128 x BN, fp32 in tensor memory), then O += P V;
 //   * a warpgroup per row tile: each thread owns one row, so its maximum and sum need no
 //     exchange; it reads S, writes P = 2^(S - m) and, where the maximum has grown by more than
@@ -54,13 +54,17 @@ struct ChunkCfg {
     static constexpr int KU = D == 256 ? 2 : 1;
     static constexpr int PKU = NP / KU;          // panels of a key unit
     static constexpr int VR = BN / KU;           // rows of a value unit
-    static constexpr int NS = D == 64 ? 6 : 4;  // units in shared memory
+    static constexpr int NS = D == 64 ? 6 : Q8 ? 3 : 4;  // units in shared memory
     static constexpr uint32_t QB = 128 * D * 2;
     static constexpr uint32_t TILE = BN * D * 2 / KU;
     // P goes over the scores it came from where two score buffers alternate (dim 256), else beside them;
     // with dim 128 the row tiles take turns on one score buffer
     static constexpr bool P_OVER = D == 256, S_TURNS = D == 128;
     static constexpr int S_COLS = S_TURNS ? BN : NQ * SB * BN;
+    // 8-bit units as copied: NRAW areas of codes in swizzled rows of a panel each, then the steps of their rows
+    static constexpr int NRAW = 2;
+    static constexpr uint32_t CODES = BN * D / KU, STEPS = BN * (D / 32) * 2;
+    static constexpr int CPANEL = D < 128 ? D : 128, KCP = CODES / (BN * CPANEL), VCP = CODES / (VR * CPANEL);
     // Warpgroups: one per row tile, one whose first warps issue each row tile's products and the copies,
     // and those that convert 8-bit codes
     static constexpr int MMA_WARP = 4 * NQ;
@@ -76,13 +80,15 @@ struct ChunkCfg {
     static constexpr int CONV_REGS = !Q8 ? 0 : NQ == 2 ? 136 : 120;
     static_assert(WGS == 2 || NQ * ROW_REGS + ISSUE_REGS + NCONV * CONV_REGS == WGS * LAUNCH_REGS, "registers");
     static constexpr bool HOLD = !Q8 || D == 256;  // a row's scores fit a thread's registers
-    static constexpr int NBAR = 2 * NS + 2 * NQ + 4 * NQ * SB + 1;  // see the barriers below
-    static constexpr uint32_t OUT_AT = NQ * QB;  // 32 rows x 128 bytes of results per warp
-    static constexpr uint32_t KV_AT = OUT_AT + NQ * 4 * 4096;
-    static constexpr uint32_t BAR_AT = KV_AT + NS * TILE;
-    static constexpr uint32_t PLACES_AT = (BAR_AT + NBAR * 8 + 8 /* tensor memory address, turn */ + 15) / 16 * 16;
-    static constexpr uint32_t BYTES = PLACES_AT + NCONV * 4 * 256 + 1024 /* alignment */;
-    static_assert(OUT_AT % 1024 == 0 && KV_AT % 1024 == 0 && BAR_AT % 16 == 0 && TILE % 1024 == 0, "alignment");
+    static constexpr int NBAR = 2 * NS + 2 * NQ + 4 * NQ * SB + 1 + 2 * NRAW;  // see the barriers below
+    static constexpr uint32_t OUT_AT = NQ * QB;  // 32 rows x 64 bytes of results per warp
+    static constexpr uint32_t KV_AT = OUT_AT + NQ * 4 * 2048;
+    static constexpr uint32_t RAW_AT = KV_AT + NS * TILE;
+    static constexpr uint32_t BAR_AT = RAW_AT + (Q8 ? NRAW * (CODES + STEPS) : 0);
+    static constexpr uint32_t BYTES = BAR_AT + NBAR * 8 + 8 /* tensor memory address, turn */ + 1024 /* alignment */;
+    static_assert(OUT_AT % 1024 == 0 && KV_AT % 1024 == 0 && RAW_AT % 1024 == 0 && BAR_AT % 16 == 0 && TILE % 1024 == 0 && CODES % 1024 == 0 &&
+                      STEPS % 16 == 0,
+                  "alignment");
     // tensor memory columns
     static constexpr int O_COL = S_COLS;
     static constexpr int P_COL = O_COL + NQ * D;  // where P has columns of its own
@@ -276,6 +282,9 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
     auto pv_done = [&](int q, int b) { return bars + 8u * (2 * NS + NQ + 2 * NQ * SB + q * SB + b); };
     auto p_half = [&](int q, int b) { return bars + 8u * (2 * NS + NQ + 3 * NQ * SB + q * SB + b); };
     auto s_empty = [&](int q) { return bars + 8u * (2 * NS + NQ + 4 * NQ * SB + q); };
+    auto raw_full = [&](int s) { return bars + 8u * (Cfg::NBAR - 1 - 2 * Cfg::NRAW + s); };
+    auto raw_empty = [&](int s) { return bars + 8u * (Cfg::NBAR - 1 - Cfg::NRAW + s); };
+    const uint32_t raw_codes = base + Cfg::RAW_AT, raw_steps = raw_codes + Cfg::NRAW * Cfg::CODES;
     const uint32_t v_raw = bars + 8u * (Cfg::NBAR - 1), taddr_slot = bars + 8u * Cfg::NBAR, turn = taddr_slot + 4;
 
     if (tid == 0) {
@@ -284,6 +293,10 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
             mbar_init(kv_empty(s), NQ);
         }
         mbar_init(v_raw, 1);
+        for (int s = 0; s < Cfg::NRAW; ++s) {
+            mbar_init(raw_full(s), 1);
+            mbar_init(raw_empty(s), 128);
+        }
         for (int q = 0; q < NQ; ++q) {
             mbar_init(q_full(q), qcopy ? 1 : 128);
             mbar_init(s_empty(q), 128);
@@ -540,44 +553,40 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
                         }
                     }
                 } else {
-                    // 128 bytes of each row at a time through the warp's own shared memory, so that a store
-                    // writes whole lines of 4 rows
-                    const uint32_t st = base + Cfg::OUT_AT + warp * 4096;
+                    // 64 bytes of each row at a time through the warp's own shared memory, so that a store
+                    // writes whole sectors of 8 rows
+                    const uint32_t st = base + Cfg::OUT_AT + warp * 2048;
+                    auto place = [&](int row, int ch) { return st + row * 64 + ((ch ^ ((row >> 1) & 3)) << 4); };
                     auto flush = [&](int at, int pitch) {  // bytes `at` .. of rows of `pitch` bytes
                         __syncwarp();
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const int row = 4 * i + lane / 8, orow = __shfl_sync(0xffffffffu, mine, row);
-                            const uint4 v = lds128(st + row * 128 + (((lane & 7) ^ (row & 7)) << 4));
-                            if (orow >= 0) *reinterpret_cast<uint4 *>(static_cast<uint8_t *>(a.out) + (int64_t)orow * pitch + at + 16 * (lane & 7)) = v;
+                        for (int i = 0; i < 4; ++i) {
+                            const int row = 8 * i + lane / 4, orow = __shfl_sync(0xffffffffu, mine, row);
+                            const uint4 v = lds128(place(row, lane & 3));
+                            if (orow >= 0) *reinterpret_cast<uint4 *>(static_cast<uint8_t *>(a.out) + (int64_t)orow * pitch + at + 16 * (lane & 3)) = v;
                         }
                         __syncwarp();
                     };
 #pragma unroll
-                    for (int c = 0; c < D; c += 64) {
-                        uint32_t o[2][32];
-                        tmem_ld32(ocol + c, o[0]);
-                        tmem_ld32(ocol + c + 32, o[1]);
-                        tmem_wait_ld(o[0]);
-                        tmem_loaded(o[1]);
+                    for (int c = 0; c < D; c += 32) {
+                        uint32_t o[32];
+                        tmem_ld32(ocol + c, o);
+                        tmem_wait_ld(o);
 #pragma unroll
-                        for (int x = 0; x < 2; ++x)
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) o[x][i] = __float_as_uint(__uint_as_float(o[x][i]) * inv);
+                        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * inv);
                         if (a.out_f32) {
 #pragma unroll
                             for (int x = 0; x < 2; ++x) {
 #pragma unroll
-                                for (int i = 0; i < 8; ++i)
-                                    sts128(st + lane * 128 + ((i ^ (lane & 7)) << 4), o[x][4 * i], o[x][4 * i + 1], o[x][4 * i + 2], o[x][4 * i + 3]);
-                                flush((c + 32 * x) * 4, D * 4);
+                                for (int i = 0; i < 4; ++i)
+                                    sts128(place(lane, i), o[16 * x + 4 * i], o[16 * x + 4 * i + 1], o[16 * x + 4 * i + 2], o[16 * x + 4 * i + 3]);
+                                flush((c + 16 * x) * 4, D * 4);
                             }
                         } else {
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) {
-                                const uint32_t *v = &o[i / 4][8 * (i % 4)];
-                                auto two = [&](int e) { return pack2<T>(__uint_as_float(v[e]), __uint_as_float(v[e + 1])); };
-                                sts128(st + lane * 128 + ((i ^ (lane & 7)) << 4), two(0), two(2), two(4), two(6));
+                            for (int i = 0; i < 4; ++i) {
+                                auto two = [&](int e) { return pack2<T>(__uint_as_float(o[8 * i + e]), __uint_as_float(o[8 * i + e + 1])); };
+                                sts128(place(lane, i), two(0), two(2), two(4), two(6));
                             }
                             flush(c * 2, D * 2);
                         }
@@ -689,9 +698,8 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
                 for (int j = 0; j < taken; ++j) {
                     const bool more = j + 1 < taken;
                     const uint32_t v = more ? u + KU : u;  // the values come after the next keys
-                    if (SB == 1) product(n + j, j == 0, v, First{});
                     if (more) scores(j + 1, both, u);
-                    if (SB == 2) product(n + j, j == 0, v, First{});
+                    product(n + j, j == 0, v, First{});
                     product(n + j, j == 0, v, Second{});
                     u = v + KU;
                 }
@@ -711,7 +719,7 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
         // complete already on the normal path; after a wait gave up, let products in flight end
         if (lane == 0 && n) mbar_drain(pv_done(q, (n - 1) % SB), ((n - 1) / SB) & 1, DRAIN_NS);
         __syncwarp();
-        } else if (!Cfg::Q8 && warp == Cfg::MMA_WARP + NQ) {
+        } else if (warp == Cfg::MMA_WARP + NQ) {
         // ------------------------------------------------------------ copies
         // A unit is one box per page part and panel, each issued by a lane of its own.  Lane b looks up the
         // page of the tile's slots 16 b .. one tile ahead.
@@ -728,39 +736,63 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
             return p;
         };
         uint32_t raws = 0;
+        // Unit h of the keys or values of a tile; a lane's box and panel, and the 16 slots whose steps it copies
         auto copy = [&](const Place &p, int h, int head, bool val, int tile) {
-            const uint32_t slot = units % NS;
-            // Slots that no row sees may hold anything, and 0 * NaN is not 0: their values become zeros before
-            // the unit counts as full
-            int z0 = 0, z1 = VR;
-            if (val) {
-                const int key0 = (k.t.kb0 + tile) * BN + h * VR;
-                const int seen_lo = a.window ? max(0, k.t.len - k.t.n + k.t.row0 / a.G - a.window + 1) : 0;
-                z0 = min(VR, max(0, seen_lo - key0)), z1 = min(VR, max(0, k.t.len - key0));
-            }
-            const bool mend = z0 > 0 || z1 < VR;
-            const uint32_t bar = mend ? v_raw : kv_full(slot);
-            const int panels = val ? Cfg::NP : Cfg::PKU, rows = val ? VR : BN;
+            const int rows = val ? VR : BN, first = val ? h * VR : 0;
+            const int panels = Cfg::Q8 ? (val ? Cfg::VCP : Cfg::KCP) : (val ? Cfg::NP : Cfg::PKU);
             const int box = lane / panels, panel = lane % panels;
-            const int from = (val ? h * VR : 0) + box * box_rows;  // the box's first slot in the tile
+            const int from = first + box * box_rows;  // the box's first slot in the tile
             int page = __shfl_sync(0xffffffffu, p.page, (from / 16) & 31);
             const int s0 = __shfl_sync(0xffffffffu, p.slot, (from / 16) & 31);
             if ((unsigned)page >= (unsigned)a.bt.n_pages) page = a.bt.n_pages;
-            if (units >= NS) mbar_wait(kv_empty(slot), (units / NS - 1) & 1);
-            if (lane == 0) mbar_arrive_expect_tx(bar, Cfg::TILE);
-            __syncwarp();
-            if (box < rows / box_rows)
-                tma_load_4d(kv0 + slot * Cfg::TILE + panel * (rows * 128) + box * box_rows * 128, val ? &vmap : &kmap,
-                            64 * ((val ? 0 : h * Cfg::PKU) + panel), s0, head, page, bar);
-            if (mend) {
-                mbar_wait(v_raw, raws++ & 1);
-                for (int x = lane; x < (z0 + VR - z1) * (D / 8); x += 32) {
-                    const int row = x / (D / 8), ch = x % (D / 8);
-                    sts128(kv0 + slot * Cfg::TILE + (ch >> 3) * (VR * 128) + (row < z0 ? row : row - z0 + z1) * 128 + (ch & 7) * 16, 0u, 0u, 0u, 0u);
-                }
-                fence_proxy_async_smem();
+            if constexpr (Cfg::Q8) {
+                // codes and steps as they are, for the converting warpgroups
+                const uint32_t slot = units % Cfg::NRAW, bar = raw_full(slot);
+                const int bpage = __shfl_sync(0xffffffffu, p.page, (first / 16 + lane) & 31);
+                const int bslot = __shfl_sync(0xffffffffu, p.slot, (first / 16 + lane) & 31);
+                const bool here = lane < rows / 16, good = here && (unsigned)bpage < (unsigned)a.bt.n_pages;
+                constexpr uint32_t BS = 16 * (D / 32) * 2;  // bytes of 16 slots' steps
+                const uint32_t sdst = raw_steps + slot * Cfg::STEPS + lane * BS;
+                if (units >= Cfg::NRAW) mbar_wait(raw_empty(slot), (units / Cfg::NRAW - 1) & 1);
+                if (here && !good)
+                    for (uint32_t x = 0; x < BS; x += 16) sts128(sdst + x, 0u, 0u, 0u, 0u);
+                const uint32_t goods = __popc(__ballot_sync(0xffffffffu, good));
+                __syncwarp();  // the zeros are written before the arrival below
+                if (lane == 0) mbar_arrive_expect_tx(bar, Cfg::CODES + goods * BS);
                 __syncwarp();
-                if (lane == 0) mbar_arrive(kv_full(slot));
+                if (box < rows / box_rows)
+                    tma_load_4d(raw_codes + slot * Cfg::CODES + panel * (rows * Cfg::CPANEL) + box * box_rows * Cfg::CPANEL, val ? &vmap : &kmap,
+                                Cfg::CPANEL * ((val ? 0 : h) + panel), s0, head, page, bar);
+                if (good)
+                    bulk_g2s(sdst, (val ? a.vd : a.kd) + bpage * a.step_stride + ((int64_t)head * a.bt.page + bslot) * (D / 32), BS, bar);
+            } else {
+                const uint32_t slot = units % NS;
+                // Slots that no row sees may hold anything, and 0 * NaN is not 0: their values become zeros before
+                // the unit counts as full
+                int z0 = 0, z1 = VR;
+                if (val) {
+                    const int key0 = (k.t.kb0 + tile) * BN + h * VR;
+                    const int seen_lo = a.window ? max(0, k.t.len - k.t.n + k.t.row0 / a.G - a.window + 1) : 0;
+                    z0 = min(VR, max(0, seen_lo - key0)), z1 = min(VR, max(0, k.t.len - key0));
+                }
+                const bool mend = z0 > 0 || z1 < VR;
+                const uint32_t bar = mend ? v_raw : kv_full(slot);
+                if (units >= NS) mbar_wait(kv_empty(slot), (units / NS - 1) & 1);
+                if (lane == 0) mbar_arrive_expect_tx(bar, Cfg::TILE);
+                __syncwarp();
+                if (box < rows / box_rows)
+                    tma_load_4d(kv0 + slot * Cfg::TILE + panel * (rows * 128) + box * box_rows * 128, val ? &vmap : &kmap,
+                                64 * ((val ? 0 : h * Cfg::PKU) + panel), s0, head, page, bar);
+                if (mend) {
+                    mbar_wait(v_raw, raws++ & 1);
+                    for (int x = lane; x < (z0 + VR - z1) * (D / 8); x += 32) {
+                        const int row = x / (D / 8), ch = x % (D / 8);
+                        sts128(kv0 + slot * Cfg::TILE + (ch >> 3) * (VR * 128) + (row < z0 ? row : row - z0 + z1) * 128 + (ch & 7) * 16, 0u, 0u, 0u, 0u);
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(kv_full(slot));
+                }
             }
             ++units;
         };
@@ -791,189 +823,109 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
             }
             chunk_next(k, plan, a.Hk);
         }
-        if (lane == 0)
-            for (uint32_t s = 0; s < NS && s < units; ++s)
-                mbar_drain(kv_full(s), ((units - 1 - s) / NS) & 1, DRAIN_NS);
+        if (lane == 0) {  // complete already on the normal path
+            if constexpr (Cfg::Q8) {
+                for (uint32_t s = 0; s < Cfg::NRAW && s < units; ++s)
+                    mbar_drain(raw_full(s), ((units - 1 - s) / Cfg::NRAW) & 1, DRAIN_NS);
+            } else {
+                for (uint32_t s = 0; s < NS && s < units; ++s) mbar_drain(kv_full(s), ((units - 1 - s) / NS) & 1, DRAIN_NS);
+            }
+        }
         __syncwarp();
         }
     } else if constexpr (Cfg::Q8) {
         // ------------------------------------------------------------ 8-bit codes to fp16 tiles
-        // Thread ct converts the 16-code chunks i * 128 + ct of its warpgroup's units.  A block of 16 slots is
-        // always in one page: lane b of each warp looks up block b of a tile, one tile ahead of the codes'
-        // loads, and leaves its offsets in a table of the warp's own.  The codes of the warpgroup's next
-        // unit are loaded chunk by chunk as this one's are converted.
+        // Thread ct converts the 16-code chunks i * 128 + ct of its warpgroup's units: all of a unit's codes
+        // into registers, which frees their place for the next copy, then fp16 into the operand tile.
         set_max_regs<Cfg::CONV_REGS >= Cfg::LAUNCH_REGS, Cfg::CONV_REGS>();
         const int cw = (warp - Cfg::CONV_WARP) / 4, ct = (tid - Cfg::CONV_WARP * 32) & 127;
-        constexpr int PER = Cfg::TILE / 32 / 128;  // 16-code chunks per thread
-        constexpr int KC = Cfg::PKU * 4, VC = D / 16;  // chunks of a row in a key unit, in a value unit
-        const uint32_t places = base + Cfg::PLACES_AT + (warp - Cfg::CONV_WARP) * 256;  // two tiles x 8 blocks x (codes, steps)
-        struct Raw {
-            uint4 c[PER];
-            uint16_t d[PER];
-            uint32_t ok;  // bit i: chunk i is a slot's, else zeros
-        };
-        struct Bounds {  // of a tile
-            int key0, seen_lo, len;
-        };
-        struct Unit {
-            int on, val, h;
-        };
-        ChunkWalk nx = k;  // the tile whose pages are looked up
-        int nj = k.blk(), npage = -1;
-        auto lookup = [&]() {
-            const int key = (nx.t.kb0 + nj) * BN + 16 * lane;
-            npage = -1;
-            if (nx.left > 0 && lane < BN / 16 && key < nx.t.len) npage = a.bt.pages[nx.t.b * a.bt.table_stride + key / a.bt.page];
-        };
-        Bounds cur{}, prev{};
-        uint32_t flip = 0;  // table half of cur
-        auto locate = [&]() {  // cur: the tile that was looked up; looks up the one after
-            __syncwarp();  // the half of the table that is written has been read
-            prev = cur;
-            flip ^= 128;
-            cur.key0 = (nx.t.kb0 + nj) * BN;
-            cur.seen_lo = a.window ? max(0, nx.t.len - nx.t.n + nx.t.row0 / a.G - a.window + 1) : 0;
-            cur.len = nx.t.len;
-            if (lane < BN / 16) {
-                const int slot = (cur.key0 + 16 * lane) % a.bt.page;
-                const bool ok = nx.left > 0 && (unsigned)npage < (unsigned)a.bt.n_pages;
-                const int64_t at = ok ? npage * a.page_stride + nx.h * a.head_stride + slot * a.slot_stride : -1;
-                const int64_t dat = ok ? npage * a.step_stride + ((int64_t)nx.h * a.bt.page + slot) * (D / 32) : 0;
-                sts128(places + flip + 16 * lane, (uint32_t)at, (uint32_t)(at >> 32), (uint32_t)dat, (uint32_t)(dat >> 32));
-            }
-            __syncwarp();
-            if (nx.left > 0 && ++nj >= nx.end()) {
-                chunk_next(nx, plan, a.Hk);
-                nj = nx.blk();
-            }
-            lookup();
-        };
+        constexpr int PER = Cfg::CODES / 16 / 128;  // chunks per thread
         int kt = k.blk(), vt = -1, blk0 = kt, end = k.end();  // the last key and value tiles begun
-        Unit un{k.left > 0, 0, -1};
+        int h = -1;
+        bool val = false, on = k.left > 0;
         auto next_unit = [&]() {  // the order of the copies
-            if (++un.h < KU) return;
-            un.h = 0;
-            const bool was_val = un.val;
-            if (!was_val) {
+            if (++h < KU) return;
+            h = 0;
+            if (!val) {
                 if (kt == blk0 && kt + 1 < end) {
                     ++kt;
-                    locate();
                 } else {
-                    un.val = 1;
+                    val = true;
                     vt = max(blk0, kt - 1);
                 }
             } else if (kt + 1 < end) {
-                un.val = 0;
+                val = false;
                 ++kt;
-                locate();
             } else if (vt < kt) {
                 ++vt;
             } else {
                 chunk_next(k, plan, a.Hk);
-                un.val = 0;
-                un.on = k.left > 0;
+                val = false;
+                on = k.left > 0;
                 blk0 = kt = k.blk();
                 end = k.end();
-                locate();
             }
         };
-        // Where chunk i of a unit is read: set once per unit
-        struct From {
-            const int8_t *codes;
-            const uint16_t *steps;
-            uint32_t table;
-            int lg, row0, ch0, key0, seen_lo, len;
-            bool on, edge;
-        };
-        auto from_of = [&](const Unit &u) {
-            From f{};
-            f.on = u.on;
-            const bool last = !u.val || vt == kt;
-            const Bounds p = last ? cur : prev;
-            f.table = places + (last ? flip : flip ^ 128);
-            f.codes = static_cast<const int8_t *>(u.val ? a.vc : a.kc);
-            f.steps = reinterpret_cast<const uint16_t *>(u.val ? a.vd : a.kd);
-            f.lg = u.val ? (D == 64 ? 2 : D == 128 ? 3 : 4) : (D == 64 ? 2 : 3);  // log2 of a row's chunks
-            f.row0 = u.val ? u.h * VR : 0;
-            f.ch0 = u.val ? 0 : u.h * KC;
-            f.key0 = p.key0, f.seen_lo = p.seen_lo, f.len = p.len;
-            f.edge = p.key0 < p.seen_lo || p.key0 + BN > p.len;
-            return f;
-        };
-        auto fetch1 = [&](Raw &w, const From &f, int i) {
-            const int x = i * 128 + ct, row = f.row0 + (x >> f.lg), ch = f.ch0 + (x & ((1 << f.lg) - 1)), in = row & 15;
-            const uint4 t = lds128(f.table + (row >> 4) * 16);
-            const int64_t o = (int64_t)((uint64_t)t.y << 32 | t.x), d = (int64_t)((uint64_t)t.w << 32 | t.z);
-            bool ok = o >= 0;
-            if (f.edge) ok = ok && f.key0 + row >= f.seen_lo && f.key0 + row < f.len;
-            w.ok = (w.ok & ~(1u << i)) | (uint32_t)ok << i;
-            // every load runs (page 0 where there is no slot): a load under a branch would be waited for there
-            w.c[i] = *reinterpret_cast<const uint4 *>(f.codes + (ok ? o : 0) + in * a.slot_stride + 16 * ch);
-            w.d[i] = f.steps[(ok ? d : 0) + in * (D / 32) + ch / 2];
-        };
-        // Converts the unit in w into its place and refills w with the next one's codes, chunk by chunk
-        auto put_as = [&](Raw &w, uint32_t dst, const From &next, auto is_val) {
+        auto convert = [&](uint32_t n, auto is_val) {  // unit number n
             constexpr bool VAL = decltype(is_val)::value;
-            constexpr int CPR = VAL ? VC : KC, RPS = 128 / CPR;
-            constexpr uint32_t PSTRIDE = (VAL ? VR : BN) * 128;
+            constexpr int ROWSU = VAL ? VR : BN, CPR = Cfg::CODES / 16 / ROWSU, RPS = 128 / CPR;  // rows, chunks of a row, rows of a step of i
+            constexpr int CC = Cfg::CPANEL / 16;                                                  // chunks of a panel's row
+            const uint32_t raw = n % Cfg::NRAW, slot = n % NS;
             const int r0 = ct / CPR, ch = ct % CPR;
+            mbar_wait(raw_full(raw), (n / Cfg::NRAW) & 1);
+            uint4 c[PER];
+            uint32_t d[PER];
 #pragma unroll
             for (int i = 0; i < PER; ++i) {
                 const int row = i * RPS + r0;
-                const uint32_t dd = w.ok >> i & 1u ? w.d[i] | (uint32_t)w.d[i] << 16 : 0u;
-                const uint32_t in[4] = {w.c[i].x, w.c[i].y, w.c[i].z, w.c[i].w};
-                uint32_t h[8];
+                c[i] = lds128(raw_codes + raw * Cfg::CODES + (ch / CC) * (ROWSU * Cfg::CPANEL) + row * Cfg::CPANEL +
+                              (((ch % CC) ^ (Cfg::CPANEL == 128 ? row & 7 : (row >> 1) & 3)) << 4));
+                d[i] = lds16(raw_steps + raw * Cfg::STEPS + (row * (D / 32) + (VAL ? 0 : h * (Cfg::PKU * 2)) + ch / 2) * 2);
+            }
+            // slots that no row sees may hold anything: they become zeros
+            const int key0 = (k.t.kb0 + (VAL ? vt : kt)) * BN + (VAL ? h * VR : 0);
+            const int seen_lo = a.window ? max(0, k.t.len - k.t.n + k.t.row0 / a.G - a.window + 1) : 0;
+            if (key0 < seen_lo || key0 + ROWSU > k.t.len) {
+#pragma unroll
+                for (int i = 0; i < PER; ++i) {
+                    const int key = key0 + i * RPS + r0;
+                    if (key < seen_lo || key >= k.t.len) d[i] = 0;
+                }
+            }
+            fence_proxy_async_smem();
+            mbar_arrive(raw_empty(raw));
+            if (n >= NS) mbar_wait(kv_empty(slot), (n / NS - 1) & 1);
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                const int row = i * RPS + r0;
+                const uint32_t dd = d[i] | d[i] << 16;
+                const uint32_t in[4] = {c[i].x, c[i].y, c[i].z, c[i].w};
+                uint32_t x[8];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const uint32_t b = in[e] ^ 0x80808080u;
 #pragma unroll
                     for (int y = 0; y < 2; ++y) {
-                        const uint32_t c = codes_to_f16(b, y ? 0x4342 : 0x4140);
-                        const __half2 r = __hmul2(*reinterpret_cast<const __half2 *>(&c), *reinterpret_cast<const __half2 *>(&dd));
-                        h[2 * e + y] = *reinterpret_cast<const uint32_t *>(&r);
+                        const uint32_t f = codes_to_f16(b, y ? 0x4342 : 0x4140);
+                        const __half2 r = __hmul2(*reinterpret_cast<const __half2 *>(&f), *reinterpret_cast<const __half2 *>(&dd));
+                        x[2 * e + y] = *reinterpret_cast<const uint32_t *>(&r);
                     }
                 }
-                const uint32_t row_at = dst + (ch >> 2) * PSTRIDE + row * 128;
+                const uint32_t row_at = kv0 + slot * Cfg::TILE + (ch >> 2) * (ROWSU * 128) + row * 128;
 #pragma unroll
                 for (int y = 0; y < 2; ++y)
-                    sts128(row_at + (((2 * (ch & 3) + y) ^ (row & 7)) << 4), h[4 * y], h[4 * y + 1], h[4 * y + 2], h[4 * y + 3]);
-                if (next.on) fetch1(w, next, i);
+                    sts128(row_at + (((2 * (ch & 3) + y) ^ (row & 7)) << 4), x[4 * y], x[4 * y + 1], x[4 * y + 2], x[4 * y + 3]);
             }
-        };
-        Raw raw;
-        raw.ok = 0;
-        lookup();
-        locate();
-        // every unit is listed by every warpgroup, each takes its own
-        uint32_t n = 0;  // number of unit un
-        next_unit();
-        auto own_unit = [&]() {
-            while (un.on && (int)(n % Cfg::NCONV) != cw) {
-                next_unit();
-                ++n;
-            }
-        };
-        own_unit();
-        if (un.on) {
-            const From f = from_of(un);
-#pragma unroll
-            for (int i = 0; i < PER; ++i) fetch1(raw, f, i);
-        }
-        while (un.on) {
-            const Unit u = un;
-            const uint32_t slot = n % NS;
-            const uint32_t round = n / NS;
-            next_unit();
-            ++n;
-            own_unit();
-            const From f = from_of(un);
-            if (round > 0) mbar_wait(kv_empty(slot), (round - 1) & 1);
-            if (u.val)
-                put_as(raw, kv0 + slot * Cfg::TILE, f, std::true_type{});
-            else
-                put_as(raw, kv0 + slot * Cfg::TILE, f, std::false_type{});
             fence_proxy_async_smem();
             mbar_arrive(kv_full(slot));
+        };
+        next_unit();
+        for (uint32_t n = 0; on; ++n, next_unit()) {
+            if ((int)(n % Cfg::NCONV) != cw) continue;
+            if (val)
+                convert(n, std::true_type{});
+            else
+                convert(n, std::false_type{});
         }
     }
     tc_fence_before();
@@ -1058,7 +1010,7 @@ static int chunk_run(const AttnArgs &in, const qg_paged &c, int sms, cudaStream_
     const bool qcopy = 128 % a.G == 0 && !qsign;
     CUtensorMap qm{};
     if (qcopy && !attn_query_map(&qm, a, c.type == QG_BF16, D)) return QG_ECUDA;
-    if (!Cfg::Q8 && (!attn_tensor_map(&km, c, c.k, box) || !attn_tensor_map(&vm, c, c.v, box))) return QG_ECUDA;
+    if (!attn_tensor_map(&km, c, c.k, box) || !attn_tensor_map(&vm, c, c.v, box)) return QG_ECUDA;
     if (!launch_programmatic(attn_plan_kernel, dim3(1), PLAN_THREADS, 0, s, a, plan, Cfg::ROWS, Cfg::BN, (int)tiles)) return QG_ECUDA;
     auto kern = attn_chunk_kernel<C, D>;
     // the warpgroups trade registers out of exactly this allocation

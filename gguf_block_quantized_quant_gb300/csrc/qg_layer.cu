@@ -295,11 +295,11 @@ __global__ void __launch_bounds__(ROPE_WARPS * 32, EPL == 8 ? 5 : 8) rope_append
                 for (int i = 0; i < EPL; ++i) m = fmaxf(m, fabsf(x[u][i]));
 #pragma unroll
                 for (int o = 16 / EPL; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-                const float d = __fdiv_rn(m, 127.0f), id = d > 0.0f ? __fdiv_rn(1.0f, d) : 0.0f;
+                const float d = __fdiv_rn(m, 127.0f), id = m > 0.0f ? __fdividef(127.0f, m) : 0.0f;
                 uint32_t c[(EPL + 3) / 4] = {};
 #pragma unroll
                 for (int i = 0; i < EPL; ++i) {
-                    const int code = max(-127, min(127, (int)roundf(x[u][i] * id)));
+                    const int code = max(-127, min(127, __float2int_rn(x[u][i] * id)));
                     c[i / 4] |= ((uint32_t)code & 0xffu) << (8 * (i % 4));
                 }
                 int8_t *dst = static_cast<int8_t *>(pool) + at;
