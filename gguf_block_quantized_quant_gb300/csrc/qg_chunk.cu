@@ -871,7 +871,11 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
             constexpr int ROWSU = VAL ? VR : BN, CPR = Cfg::CODES / 16 / ROWSU, RPS = 128 / CPR;  // rows, chunks of a row, rows of a step of i
             constexpr int CC = Cfg::CPANEL / 16;                                                  // chunks of a panel's row
             const uint32_t raw = n % Cfg::NRAW, slot = n % NS;
-            const int r0 = ct / CPR, ch = ct % CPR;
+            // Eight lanes at a time read codes and write tiles without bank conflicts: four chunks of one row and
+            // the four of the other half of the next (both rows' panels meet at one bank otherwise)
+            const int odd = (ct >> 2) & 1;
+            const int r0 = CPR == 4 ? ct / 4 : 2 * (ct / (2 * CPR)) + odd;
+            const int ch = CPR == 4 ? ct % 4 : (CPR == 16 ? (ct >> 4 & 1) * 8 : 0) + 4 * (odd ^ (ct >> 3 & 1)) + (ct & 3);
             mbar_wait(raw_full(raw), (n / Cfg::NRAW) & 1);
             uint4 c[PER];
             uint32_t d[PER];
