@@ -835,8 +835,7 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
         }
     } else if constexpr (Cfg::Q8) {
         // ------------------------------------------------------------ 8-bit codes to fp16 tiles
-        // Thread ct converts the 16-code chunks i * 128 + ct of its warpgroup's units: all of a unit's codes
-        // into registers, which frees their place for the next copy, then fp16 into the operand tile.
+        // Thread ct converts every 128th 16-code chunk of its warpgroup's units.
         set_max_regs<Cfg::CONV_REGS >= Cfg::LAUNCH_REGS, Cfg::CONV_REGS>();
         const int cw = (warp - Cfg::CONV_WARP) / 4, ct = (tid - Cfg::CONV_WARP * 32) & 127;
         constexpr int PER = Cfg::CODES / 16 / 128;  // chunks per thread
@@ -877,33 +876,20 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
             const int r0 = CPR == 4 ? ct / 4 : 2 * (ct / (2 * CPR)) + odd;
             const int ch = CPR == 4 ? ct % 4 : (CPR == 16 ? (ct >> 4 & 1) * 8 : 0) + 4 * (odd ^ (ct >> 3 & 1)) + (ct & 3);
             mbar_wait(raw_full(raw), (n / Cfg::NRAW) & 1);
-            uint4 c[PER];
-            uint32_t d[PER];
-#pragma unroll
-            for (int i = 0; i < PER; ++i) {
-                const int row = i * RPS + r0;
-                c[i] = lds128(raw_codes + raw * Cfg::CODES + (ch / CC) * (ROWSU * Cfg::CPANEL) + row * Cfg::CPANEL +
-                              (((ch % CC) ^ (Cfg::CPANEL == 128 ? row & 7 : (row >> 1) & 3)) << 4));
-                d[i] = lds16(raw_steps + raw * Cfg::STEPS + (row * (D / 32) + (VAL ? 0 : h * (Cfg::PKU * 2)) + ch / 2) * 2);
-            }
             // slots that no row sees may hold anything: they become zeros
             const int key0 = (k.t.kb0 + (VAL ? vt : kt)) * BN + (VAL ? h * VR : 0);
             const int seen_lo = a.window ? max(0, k.t.len - k.t.n + k.t.row0 / a.G - a.window + 1) : 0;
-            if (key0 < seen_lo || key0 + ROWSU > k.t.len) {
-#pragma unroll
-                for (int i = 0; i < PER; ++i) {
-                    const int key = key0 + i * RPS + r0;
-                    if (key < seen_lo || key >= k.t.len) d[i] = 0;
-                }
-            }
-            fence_proxy_async_smem();
-            mbar_arrive(raw_empty(raw));
+            const int from = max(0, seen_lo - key0), to = k.t.len - key0;  // rows of slots
             if (n >= NS) mbar_wait(kv_empty(slot), (n / NS - 1) & 1);
-#pragma unroll
+            // a short loop: four roles run at once, and long unrolled code would miss in the instruction cache
+#pragma unroll 2
             for (int i = 0; i < PER; ++i) {
                 const int row = i * RPS + r0;
-                const uint32_t dd = d[i] | d[i] << 16;
-                const uint32_t in[4] = {c[i].x, c[i].y, c[i].z, c[i].w};
+                const uint4 c = lds128(raw_codes + raw * Cfg::CODES + (ch / CC) * (ROWSU * Cfg::CPANEL) + row * Cfg::CPANEL +
+                                       (((ch % CC) ^ (Cfg::CPANEL == 128 ? row & 7 : (row >> 1) & 3)) << 4));
+                const uint32_t d = lds16(raw_steps + raw * Cfg::STEPS + (row * (D / 32) + (VAL ? 0 : h * (Cfg::PKU * 2)) + ch / 2) * 2);
+                const uint32_t dd = row >= from && row < to ? d | d << 16 : 0u;
+                const uint32_t in[4] = {c.x, c.y, c.z, c.w};
                 uint32_t x[8];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
@@ -920,6 +906,7 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
                 for (int y = 0; y < 2; ++y)
                     sts128(row_at + (((2 * (ch & 3) + y) ^ (row & 7)) << 4), x[4 * y], x[4 * y + 1], x[4 * y + 2], x[4 * y + 3]);
             }
+            mbar_arrive(raw_empty(raw));
             fence_proxy_async_smem();
             mbar_arrive(kv_full(slot));
         };
