@@ -32,9 +32,11 @@ namespace qg {
 // instead of the 11 (8) bits of one fp16 (bf16) factor.
 constexpr int DEC_ROWS = 16;     // rows of a tile at most (NR = 2)
 constexpr int DEC_BLK = 16;      // slots per block: the least page size
-// An item costs its blocks and a fixed part more, in the same unit, for its queries and the merge of the
-// warps; a range that ends inside that part leaves the item to the next CTA.
-constexpr int dec_ov(bool q8) { return q8 ? 12 : 6; }
+// An item costs its blocks and a fixed part more, in the same unit, for its queries, its last incomplete
+// round of the warps and their merge; a range that ends inside that part leaves the item to the
+// next CTA.  Measured on 64 (48) ragged sequences of 300 to 16000 (100 to 12000) slots, fp16 with dim
+// 128 (8-bit with dim 256), us: 162 (83) with 6 (12), 159 (65.5) with 12 (24), 158 (63) with 20 (36).
+constexpr int dec_ov(bool q8) { return q8 ? 32 : 16; }
 constexpr int DEC_MIN_BLKS = 8;  // blocks a CTA takes at least
 
 template <int C, int D, int NR>
@@ -101,14 +103,22 @@ struct Walk {
     }
 };
 
-// Units of all sequences; the first `ctas` CTAs share them.  Whole warp: lane i takes every 32nd sequence.
+// Units of all sequences, and the CTAs that share them.  Whole warp: lane i takes every 32nd sequence.
 template <int ROWS, int OV>
-__device__ __forceinline__ int64_t walk_total(const AttnArgs &a) {
-    int64_t n = 0;
-    for (int b = threadIdx.x & 31; b < a.bt.batch; b += 32) n += SeqWork<ROWS, OV>(a, b).cost(a);
+__device__ __forceinline__ int64_t walk_total(const AttnArgs &a, int &ctas) {
+    int64_t units = 0, items = 0;
+    for (int b = threadIdx.x & 31; b < a.bt.batch; b += 32) {
+        const SeqWork<ROWS, OV> w(a, b);
+        units += w.cost(a);
+        items += (int64_t)w.nrt * a.Hk;
+    }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
-    return n;
+    for (int o = 16; o > 0; o >>= 1) {
+        units += __shfl_xor_sync(0xffffffffu, units, o);
+        items += __shfl_xor_sync(0xffffffffu, items, o);
+    }
+    ctas = (int)min((int64_t)gridDim.x, max((int64_t)1, (units - items * OV) / DEC_MIN_BLKS));
+    return units;
 }
 // The position of unit `at` (below the total); whole warp.
 template <int ROWS, int OV>
@@ -196,13 +206,20 @@ __global__ void __launch_bounds__(DecCfg<C, D, NR>::NW * 32, 1)
     __syncwarp();
     griddep_wait();
     griddep_launch_dependents();
-    if (warp == 0) {
-        const int64_t total = walk_total<ROWS, OV>(a);
-        const int ctas = (int)min((int64_t)gridDim.x, max((int64_t)1, total / (OV + DEC_MIN_BLKS)));
-        if (lane == 0) sh[0] = total, sh[1] = ctas, a.desc[blockIdx.x].parts = 0;
+    int64_t total;
+    int ctas;
+    if (a.bt.batch <= 128) {  // every warp for itself: nobody waits
+        total = walk_total<ROWS, OV>(a, ctas);
+    } else {
+        if (warp == 0) {
+            total = walk_total<ROWS, OV>(a, ctas);
+            if (lane == 0) sh[0] = total, sh[1] = ctas;
+        }
+        __syncthreads();
+        total = sh[0], ctas = (int)sh[1];
     }
-    __syncthreads();
-    const Ranges rg(sh[0], (int)sh[1]);
+    if (tid == 0) a.desc[blockIdx.x].parts = 0;
+    const Ranges rg(total, ctas);
     if ((int)blockIdx.x >= rg.ctas) return;
     const int64_t w0 = rg.start(blockIdx.x), w1 = rg.start(blockIdx.x + 1);
     if (w0 >= w1) return;
