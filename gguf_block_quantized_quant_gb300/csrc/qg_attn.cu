@@ -301,6 +301,7 @@ __global__ void __launch_bounds__(DecCfg<C, D, NR>::NW * 32, 1)
     };
     load_q(con);
     while (con.left > 0) {
+
         const int blk0 = con.blk(), end = con.end();
         const int h = con.item / con.w.nrt, rt = con.item % con.w.nrt;
         const Seq sq = con.w.sq;
@@ -433,16 +434,15 @@ __global__ void __launch_bounds__(DecCfg<C, D, NR>::NW * 32, 1)
                     pl[r][n] = movmatrix_t(pack2<T>(p0 - hf.x, p1 - hf.y));
                 }
             }
-            // slots that no row sees may hold anything: their values are taken as zero
-            const bool ragged = key0 + DEC_BLK > sq.len || key0 < seen_lo;
-            uint32_t vm[2] = {~0u, ~0u};
-            if (ragged) {
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int k0 = key0 + 8 * i + 2 * gc;
-                    vm[i] = (k0 < sq.len && k0 >= seen_lo ? 0x0000ffffu : 0u) |
-                            (k0 + 1 < sq.len && k0 + 1 >= seen_lo ? 0xffff0000u : 0u);
+            // slots that no row sees may hold anything: their values (the steps of their codes) become zeros
+            if (key0 + DEC_BLK > sq.len || key0 < seen_lo) {
+                constexpr int RB = Cfg::Q8 ? D / 32 * 2 : Cfg::PANEL;  // bytes of a row in one place
+                constexpr int PL = Cfg::Q8 ? 1 : Cfg::NP;
+                for (int x = lane; x < DEC_BLK * PL * (RB / 4); x += 32) {
+                    const int row = x / (RB / 4) % DEC_BLK, key = key0 + row;
+                    if (key >= sq.len || key < seen_lo) sts32((Cfg::Q8 ? vs : vt) + 4 * x, 0u);
                 }
+                __syncwarp();
             }
             if constexpr (!Cfg::Q8) {
                 const int row = (lane & 7) + ((lane >> 4) << 3);
@@ -451,12 +451,6 @@ __global__ void __launch_bounds__(DecCfg<C, D, NR>::NW * 32, 1)
                     const int ch = 2 * m + ((lane >> 3) & 1);
                     uint32_t f[4];
                     ldmatrix4_t(vt + (ch >> 3) * DEC_BLK * 128 + row * 128 + (((ch & 7) ^ (row & 7)) << 4), f);
-                    if (ragged) {
-                        f[0] &= vm[0];
-                        f[1] &= vm[0];
-                        f[2] &= vm[1];
-                        f[3] &= vm[1];
-                    }
 #pragma unroll
                     for (int r = 0; r < NR; ++r) {
                         mma16816<T>(o[r][m], f, ph[r][0], ph[r][1]);
@@ -506,7 +500,6 @@ __global__ void __launch_bounds__(DecCfg<C, D, NR>::NW * 32, 1)
                                     const uint32_t c = codes_to_f16(two, y ? 0x4342 : 0x4140);
                                     const __half2 v = __hmul2(*reinterpret_cast<const __half2 *>(&c), d[i]);
                                     f[2 * i + y] = *reinterpret_cast<const uint32_t *>(&v);
-                                    if (ragged) f[2 * i + y] &= vm[i];
                                 }
                             }
                             const int m = p * (EPR / 2) + 2 * e + x;

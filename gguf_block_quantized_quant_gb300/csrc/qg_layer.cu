@@ -152,8 +152,13 @@ static int norm_x(const NormArgs &a, int x_type, bool vec, cudaStream_t s) {
 // [-1/2, 1/2), go to sincospi.
 //
 // One warp takes one token and a run of its heads: the sines of the token are computed once
-// and used for all of them.  A lane holds D / 32 consecutive elements of a head (16 bytes of
-// fp32 at D = 128).  Bound by memory for many tokens; one token is a launch and two loads deep.
+// and used for all of them.  A lane holds both elements of its pairs, four pairs of one head, so
+// that rotating exchanges nothing between lanes and 32 / (D / 8) heads share an instruction
+// (rope_quads_kernel); 4096 tokens of 32 + 2 x 8 heads of 128, fp32 to an 8-bit cache: 29 us.
+// Rotated parts that are no multiple of 8 elements (64 for the keys of an 8-bit cache in halves,
+// whose blocks of 32 must not straddle) take rope_append_kernel: D / 32 consecutive elements per
+// lane, partners from other lanes, 41 us for the same.  Bound by memory for many tokens; one
+// token is a launch and two loads deep.
 struct RopeArgs {
     const void *q, *k, *v;
     int64_t ldq, hdq, ldk, hdk, ldv, hdv;  // elements between tokens, between heads
@@ -318,10 +323,167 @@ __global__ void __launch_bounds__(ROPE_WARPS * 32, EPL == 8 ? 5 : 8) rope_append
     }
 }
 
+// Codes and step of a block whose elements are spread over LANES neighbouring lanes: the Q8_0 rule.
+template <int LANES, int N>
+__device__ __forceinline__ void quant_q8(const float (&x)[N], uint32_t (&c)[N / 4], float &d) {
+    float m = 0.0f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) m = fmaxf(m, fabsf(x[i]));
+#pragma unroll
+    for (int o = LANES / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    d = __fdiv_rn(m, 127.0f);
+    const float id = m > 0.0f ? __fdividef(127.0f, m) : 0.0f;
+#pragma unroll
+    for (int w = 0; w < N / 4; ++w) {
+        c[w] = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            c[w] |= ((uint32_t)max(-127, min(127, __float2int_rn(x[4 * w + i] * id))) & 0xffu) << (8 * i);
+    }
+}
+
+// A lane's 8 elements of a head are two runs of 4 at e[0] and e[1]: four pairs (the runs half apart, or
+// adjacent with interleaved pairs), or 8 elements that pass through.
+template <class I, int C, int D>
+__global__ void __launch_bounds__(ROPE_WARPS * 32) rope_quads_kernel(const RopeArgs a) {
+    using Q = typename CacheT<C>::Q;
+    constexpr int LPH = D / 8, HPI = 32 / LPH;  // lanes of a head, heads of a step
+    griddep_wait();
+    griddep_launch_dependents();
+    const int lane = threadIdx.x & 31, c = lane % LPH, sub = lane / LPH;
+    const int heads = a.Hq + 2 * a.Hk, groups = (heads + a.hpw - 1) / a.hpw;
+    const int64_t item = (int64_t)blockIdx.x * ROPE_WARPS + (threadIdx.x >> 5);
+    if (item >= (int64_t)a.bt.tokens * groups) return;
+    const int t = (int)(item / groups), h0 = (int)(item % groups) * a.hpw, h1 = min(heads, h0 + a.hpw);
+
+    const int b = token_seq(a.bt, t, lane);
+    const Seq sq = seq_of(a.bt, b);
+    const int pos = sq.len - sq.n + (t - sq.first);
+    const bool valid = t >= sq.first && t < sq.first + sq.n && pos >= 0;
+    int page = -1, slot = 0;
+    if (valid) {
+        page = a.bt.pages[b * a.bt.table_stride + pos / a.bt.page];
+        slot = pos % a.bt.page;
+        if (page >= a.bt.n_pages) page = -1;
+    }
+
+    const int half = a.rot / 2;
+    const bool turns = 8 * c < a.rot;                       // the lane's elements are pairs
+    const bool split = !a.pairs && turns;                   // runs `half` apart
+    const int e0 = split ? 4 * c : 8 * c, e1 = split ? half + 4 * c : 8 * c + 4;
+    float cs[4] = {1.0f, 1.0f, 1.0f, 1.0f}, sn[4] = {};
+    if (turns && h0 < a.Hq + a.Hk) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const unsigned long long ph = (unsigned long long)(long long)pos * a.turns[4 * c + i];
+            sincospif((float)(int)(ph >> 32) * 0x1p-31f, &sn[i], &cs[i]);
+            cs[i] *= a.amp;
+            sn[i] *= a.amp;
+        }
+    }
+    const I *bq = static_cast<const I *>(a.q) + (int64_t)t * a.ldq, *bk = static_cast<const I *>(a.k) + (int64_t)t * a.ldk;
+    const I *bv = static_cast<const I *>(a.v) + (int64_t)t * a.ldv;
+    Q *qo = static_cast<Q *>(a.q_out) + (int64_t)t * a.Hq * D;
+    const int64_t place = page * a.page_stride + slot * a.slot_stride, steps = page * a.step_stride + (int64_t)slot * (D / 32);
+
+    for (int hb = h0; hb < h1; hb += HPI * ROPE_U) {
+        float x[ROPE_U][8];
+#pragma unroll
+        for (int u = 0; u < ROPE_U; ++u) {
+            const int h = min(hb + u * HPI + sub, h1 - 1);
+            const bool is_v = h >= a.Hq + a.Hk;
+            const I *src = h < a.Hq ? bq + h * a.hdq : is_v ? bv + (h - a.Hq - a.Hk) * a.hdv : bk + (h - a.Hq) * a.hdk;
+            float lo[4], hi[4];
+            load_vec<I, 4>(src + (is_v ? 8 * c : e0), lo);
+            load_vec<I, 4>(src + (is_v ? 8 * c + 4 : e1), hi);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[u][i] = lo[i], x[u][4 + i] = hi[i];
+        }
+#pragma unroll
+        for (int u = 0; u < ROPE_U; ++u) {
+            if (hb + u * HPI >= h1) break;  // whole warp
+            const int hh = hb + u * HPI + sub, h = min(hh, h1 - 1);
+            const bool live = hh < h1, is_q = h < a.Hq, is_v = h >= a.Hq + a.Hk;
+            const float *w = is_q ? a.wq : a.wk;
+            if (a.wq || a.wk) {
+                float s = 0.0f;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) s = fmaf(x[u][i], x[u][i], s);
+#pragma unroll
+                for (int o = LPH / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+                if (w && !is_v) {
+                    const float k = rsqrtf(s * (1.0f / D) + a.eps);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        x[u][i] *= k * w[e0 + i];
+                        x[u][4 + i] *= k * w[e1 + i];
+                    }
+                }
+            }
+            if (turns && !is_v) {
+                if (a.pairs) {  // pairs 0..3: elements (0, 1), (2, 3), ...
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float p = x[u][2 * i], q = x[u][2 * i + 1];
+                        x[u][2 * i] = fmaf(-q, sn[i], p * cs[i]);
+                        x[u][2 * i + 1] = fmaf(p, sn[i], q * cs[i]);
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float p = x[u][i], q = x[u][4 + i];
+                        x[u][i] = fmaf(-q, sn[i], p * cs[i]);
+                        x[u][4 + i] = fmaf(p, sn[i], q * cs[i]);
+                    }
+                }
+            }
+            const float lo[4] = {x[u][0], x[u][1], x[u][2], x[u][3]}, hi[4] = {x[u][4], x[u][5], x[u][6], x[u][7]};
+            if (is_q) {
+                if (live) {
+                    const float zero[4] = {};
+                    store_vec<Q, 4>(qo + h * D + e0, valid ? lo : zero);
+                    store_vec<Q, 4>(qo + h * D + e1, valid ? hi : zero);
+                }
+                if (C != CACHE_Q8 || __all_sync(0xffffffffu, is_q)) continue;
+            }
+            const int kh = is_v ? h - a.Hq - a.Hk : h - a.Hq, f0 = is_v ? 8 * c : e0, f1 = is_v ? 8 * c + 4 : e1;
+            const bool keep = live && !is_q && page >= 0;
+            if constexpr (C != CACHE_Q8) {
+                if (keep) {
+                    Q *dst = static_cast<Q *>(is_v ? a.vc : a.kc) + place + kh * a.head_stride;
+                    store_vec<Q, 4>(dst + f0, lo);
+                    store_vec<Q, 4>(dst + f1, hi);
+                }
+            } else {
+                // values, interleaved pairs and elements that pass through: blocks of 32 in 4 lanes; halves: the
+                // first runs of 8 lanes are one block, their second runs another
+                uint32_t cd[2], c0[1], c1[1];
+                float d, d0, d1;
+                quant_q8<4>(x[u], cd, d);
+                quant_q8<8>(lo, c0, d0);
+                quant_q8<8>(hi, c1, d1);
+                const bool halves = split && !is_v;
+                if (keep) {
+                    int8_t *dst = static_cast<int8_t *>(is_v ? a.vc : a.kc) + place + kh * a.head_stride;
+                    f16 *st = static_cast<f16 *>(is_v ? a.vd : a.kd) + steps + (int64_t)kh * a.bt.page * (D / 32);
+                    *reinterpret_cast<uint32_t *>(dst + f0) = halves ? c0[0] : cd[0];
+                    *reinterpret_cast<uint32_t *>(dst + f1) = halves ? c1[0] : cd[1];
+                    if (halves) {
+                        if (c % 8 == 0) st[f0 / 32] = __float2half_rn(d0), st[f1 / 32] = __float2half_rn(d1);
+                    } else if (c % 4 == 0) {
+                        st[f0 / 32] = __float2half_rn(d);
+                    }
+                }
+            }
+        }
+    }
+}
+
 template <class I, int C, int EPL>
 static int rope_launch(const RopeArgs &a, int64_t warps, cudaStream_t s) {
-    return launch_programmatic(rope_append_kernel<I, C, EPL>, dim3((unsigned)((warps + ROPE_WARPS - 1) / ROPE_WARPS)),
-                               ROPE_WARPS * 32, 0, s, a)
+    const bool quads = a.rot % 8 == 0 && (C != CACHE_Q8 || a.pairs || a.rot % 64 == 0);
+    return launch_programmatic(quads ? rope_quads_kernel<I, C, EPL * 32> : rope_append_kernel<I, C, EPL>,
+                               dim3((unsigned)((warps + ROPE_WARPS - 1) / ROPE_WARPS)), ROPE_WARPS * 32, 0, s, a)
                ? QG_OK
                : QG_ECUDA;
 }
@@ -434,11 +596,11 @@ int qg_rope_append(const void *q, int64_t ldq, int64_t hdq, const void *k, int64
     a.bt = paged_batch(*cache, tokens);
     a.Hq = q_heads, a.Hk = Hk, a.rot = rot, a.pairs = pairs != 0;
     a.amp = amp, a.eps = eps;
-    // few tokens: a warp per head (latency); many: up to 16 heads per warp share the sines, as
-    // long as the warps fill the machine
-    const int heads = q_heads + 2 * Hk;
+    // few tokens: a warp takes as many heads as it has room for in one step (latency); many: up to 24
+    // share the sines, as long as the warps fill the machine
+    const int heads = q_heads + 2 * Hk, step = 256 / D;
     const int64_t items = (int64_t)tokens * heads, fill = (int64_t)sms * 32;
-    a.hpw = (int)std::min<int64_t>(std::max<int64_t>(items / fill, 1), 16);
+    a.hpw = (int)std::min<int64_t>(std::max<int64_t>(items / fill / step, 1) * step, 24);
     const int64_t warps = (int64_t)tokens * ((heads + a.hpw - 1) / a.hpw);
     cudaStream_t s = (cudaStream_t)stream;
     switch (in_type) {
