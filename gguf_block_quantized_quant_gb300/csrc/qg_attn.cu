@@ -53,15 +53,17 @@ struct DecCfg {
     // and get more warps where the accumulators leave registers for them
     static constexpr int NW = D == 256 ? (Q8 ? (NR == 1 ? 12 : 8) : 6) : D == 128 ? (Q8 ? (NR == 1 ? 16 : 12) : 8) : (Q8 ? 16 : 12);
     static constexpr int MW = D == 256 && Q8 ? 32 : 64;      // columns merged at a time
-    static constexpr int ROOM = (222 * 1024 - NW * ROWS * (MW * 4 + 8)) / (NW * 2 * (TILE + STEPS));
+    static constexpr int ROOM = (222 * 1024 - NW * ROWS * (MW * 4 + 8) - (Q8 ? NR * D * 16 : 0)) / (NW * 2 * (TILE + STEPS));
     static constexpr int S = ROOM > 8 ? 8 : ROOM;
     static constexpr uint32_t RING = (uint32_t)NW * S * 2 * TILE;
     static constexpr uint32_t STEP_AT = RING;
     static constexpr uint32_t MERGE_AT = STEP_AT + (uint32_t)NW * S * 2 * STEPS;
     static constexpr uint32_t ML_AT = MERGE_AT + (uint32_t)NW * ROWS * MW * 4;
-    static constexpr uint32_t BAR_AT = ML_AT + (uint32_t)NW * ROWS * 8;
+    static constexpr uint32_t QS_AT = ML_AT + (uint32_t)NW * ROWS * 8;  // 8-bit: the item's queries, 16 bytes per lane and 32-element block
+    static constexpr uint32_t QS = Q8 ? NR * (D / 32) * 512 : 0;
+    static constexpr uint32_t BAR_AT = QS_AT + QS;
     static constexpr uint32_t BYTES = BAR_AT + (uint32_t)NW * S * 8 + 1024 /* alignment */;
-    static_assert(MERGE_AT % 16 == 0 && ML_AT % 8 == 0 && BAR_AT % 8 == 0 && S >= 2, "layout");
+    static_assert(MERGE_AT % 16 == 0 && ML_AT % 8 == 0 && QS_AT % 16 == 0 && BAR_AT % 8 == 0 && S >= 2, "layout");
 };
 
 // The blocks of one sequence: every item (cache head, row tile) of it has the same slots.
@@ -277,29 +279,37 @@ __global__ void __launch_bounds__(DecCfg<C, D, NR>::NW * 32, 1)
     const int gr = lane >> 2, gc = lane & 3;
     int slot = 0;
     uint32_t phase = 0;
-    // ---- queries as B fragments: row 8 r + gr
-    uint32_t qf[NR][MT][2];
+    // ---- queries as B fragments: row 8 r + gr.  Beside an 8-bit cache they are kept in shared memory for all
+    // warps, a lane's 8 elements of each 32-element block together: that leaves registers to the
+    // conversion and lets its loop over blocks be a loop, where unrolled code misses in the
+    // instruction cache
+    uint32_t qf[NR][Cfg::Q8 ? 1 : MT][2];
+    const uint32_t qs = base + Cfg::QS_AT + 16 * lane;
     auto load_q = [&](const Walk &k) {
         const int h = k.item / k.w.nrt, rt = k.item % k.w.nrt, nr = min(ROWS, k.w.sq.n * a.G - rt * ROWS);
-#pragma unroll
-        for (int r = 0; r < NR; ++r) {
-            // rows past the last are copies of it: nothing of them is written
+        auto row = [&](int r) {  // rows past the last are copies of it: nothing of them is written
             const int rr = rt * ROWS + min(8 * r + gr, nr - 1), t = rr / a.G, g = rr % a.G;
-            const T *src = static_cast<const T *>(a.q) + (int64_t)(k.w.sq.first + t) * a.ldq + (int64_t)(h * a.G + g) * a.hdq;
+            return static_cast<const T *>(a.q) + (int64_t)(k.w.sq.first + t) * a.ldq + (int64_t)(h * a.G + g) * a.hdq;
+        };
+        if constexpr (Cfg::Q8) {
+            for (int x = warp; x < NR * (D / 32); x += NW) {
+                const uint4 v = *reinterpret_cast<const uint4 *>(row(x / (D / 32)) + x % (D / 32) * 32 + 8 * gc);
+                sts128(qs + x * 512, v.x, v.y, v.z, v.w);
+            }
+        } else {
 #pragma unroll
-            for (int m = 0; m < MT; ++m) {
-                if constexpr (!Cfg::Q8) {
+            for (int r = 0; r < NR; ++r) {
+                const T *src = row(r);
+#pragma unroll
+                for (int m = 0; m < MT; ++m) {
                     qf[r][m][0] = *reinterpret_cast<const uint32_t *>(src + 16 * m + 2 * gc);
                     qf[r][m][1] = *reinterpret_cast<const uint32_t *>(src + 16 * m + 8 + 2 * gc);
-                } else {  // product 2 j + s of 32-element block j takes the lane's codes 4 s .. 4 s + 3 of its 8
-                    const uint2 v = *reinterpret_cast<const uint2 *>(src + (m >> 1) * 32 + gc * 8 + (m & 1) * 4);
-                    qf[r][m][0] = v.x;
-                    qf[r][m][1] = v.y;
                 }
             }
         }
     };
     load_q(con);
+    if (Cfg::Q8) __syncthreads();
     while (con.left > 0) {
 
         const int blk0 = con.blk(), end = con.end();
@@ -348,18 +358,17 @@ __global__ void __launch_bounds__(DecCfg<C, D, NR>::NW * 32, 1)
                     for (int r = 0; r < NR; ++r) mma16816<T>(s[r], f, qf[r][k][0], qf[r][k][1]);
                 }
             } else {
-#pragma unroll
+                // lane (gr, gc) takes codes 8 gc .. of each 32-element block of slots gr and gr + 8
+                const int half = gc >> 1, turn = Cfg::PANEL == 128 ? gr : gr >> 1;  // the rows' places in the swizzle
+                const uint32_t krow = kt + gr * Cfg::PANEL + (gc & 1) * 8;
+#pragma unroll 2
                 for (int j = 0; j < D / 32; ++j) {
-                    uint32_t f0[4], f1[4];  // codes 0..3 and 4..7 of the lane's 8 in the block, slots gr and gr + 8
+                    uint32_t f0[4], f1[4];  // codes 0..3 and 4..7 of the lane's 8, slots gr and gr + 8
+                    const uint32_t at = krow + (Cfg::PANEL == 128 ? (j >> 2) * (DEC_BLK * 128) + (((2 * (j & 3) + half) ^ turn) << 4)
+                                                                  : (((2 * j + half) ^ (turn & 3)) << 4));
 #pragma unroll
                     for (int n = 0; n < 2; ++n) {
-                        const int row = 8 * n + gr, byte = 32 * j + 8 * gc;
-                        uint32_t addr;
-                        if constexpr (Cfg::PANEL == 128)
-                            addr = kt + (byte >> 7) * DEC_BLK * 128 + row * 128 + ((((byte >> 4) & 7) ^ (row & 7)) << 4) + (byte & 15);
-                        else
-                            addr = kt + row * 64 + (((byte >> 4) ^ ((row >> 1) & 3)) << 4) + (byte & 15);
-                        uint2 v = lds64(addr);
+                        uint2 v = lds64(at + n * 8 * Cfg::PANEL);
                         v.x ^= 0x80808080u;
                         v.y ^= 0x80808080u;
                         f0[n] = codes_to_f16(v.x, 0x4140);
@@ -372,9 +381,10 @@ __global__ void __launch_bounds__(DecCfg<C, D, NR>::NW * 32, 1)
                     const float d1 = half_bits_to_float(lds16(ks + ((gr + 8) * (D / 32) + j) * 2));
 #pragma unroll
                     for (int r = 0; r < NR; ++r) {
+                        const uint4 q = lds128(qs + (r * (D / 32) + j) * 512);
                         float acc[4] = {};
-                        mma16816<T>(acc, f0, qf[r][2 * j][0], qf[r][2 * j][1]);
-                        mma16816<T>(acc, f1, qf[r][2 * j + 1][0], qf[r][2 * j + 1][1]);
+                        mma16816<T>(acc, f0, q.x, q.y);
+                        mma16816<T>(acc, f1, q.z, q.w);
                         s[r][0] = fmaf(acc[0], d0, s[r][0]);
                         s[r][1] = fmaf(acc[1], d0, s[r][1]);
                         s[r][2] = fmaf(acc[2], d1, s[r][2]);
@@ -524,7 +534,7 @@ __global__ void __launch_bounds__(DecCfg<C, D, NR>::NW * 32, 1)
         // ---- merge the warps' results; the next item's queries come in meanwhile
         Walk nxt = con;
         nxt.next(a);
-        if (nxt.left > 0) load_q(nxt);
+        if (!Cfg::Q8 && nxt.left > 0) load_q(nxt);
         const bool whole = blk0 == 0 && end == con.w.nblk;
         if (warp == 0 && blk0 == 0 && !whole) {
             const int64_t s0 = w1 - con.left - con.u;  // the item's first unit
@@ -541,7 +551,8 @@ __global__ void __launch_bounds__(DecCfg<C, D, NR>::NW * 32, 1)
                 l[r][i] += __shfl_xor_sync(0xffffffffu, l[r][i], 16);
                 if (gr == 0) ml[warp * ROWS + 8 * r + 2 * gc + i] = make_float2(mx[r][i], l[r][i]);
             }
-        __syncthreads();
+        __syncthreads();  // every warp has left the item's slots
+        if (Cfg::Q8 && nxt.left > 0) load_q(nxt);  // before the merge's last barrier
         float *part = a.part + (size_t)(2 * blockIdx.x + (blk0 == 0 ? 1 : 0)) * attn_part_floats(ROWS, D);
 #pragma unroll
         for (int r = 0; r < NR; ++r)
