@@ -156,7 +156,8 @@ static int norm_x(const NormArgs &a, int x_type, bool vec, cudaStream_t s) {
 // that rotating exchanges nothing between lanes and 32 / (D / 8) heads share an instruction
 // (rope_quads_kernel); 4096 tokens of 32 + 2 x 8 heads of 128, fp32 to an 8-bit cache: 29 us.
 // Rotated parts that are no multiple of 8 elements (64 for the keys of an 8-bit cache in halves,
-// whose blocks of 32 must not straddle) take rope_append_kernel: D / 32 consecutive elements per
+// whose blocks of 32 must not straddle), and heads of 64 off a boundary of 4 elements, take
+// rope_append_kernel: D / 32 consecutive elements per
 // lane, partners from other lanes, 41 us for the same.  Bound by memory for many tokens; one
 // token is a launch and two loads deep.
 struct RopeArgs {
@@ -170,6 +171,7 @@ struct RopeArgs {
     Batch bt;
     int Hq, Hk, rot, pairs;
     int hpw;  // heads per warp
+    bool runs4;  // every head of q, k and v starts on a boundary of 4 elements
     float amp, eps;
 };
 
@@ -481,7 +483,7 @@ __global__ void __launch_bounds__(ROPE_WARPS * 32) rope_quads_kernel(const RopeA
 
 template <class I, int C, int EPL>
 static int rope_launch(const RopeArgs &a, int64_t warps, cudaStream_t s) {
-    const bool quads = a.rot % 8 == 0 && (C != CACHE_Q8 || a.pairs || a.rot % 64 == 0);
+    const bool quads = a.runs4 && a.rot % 8 == 0 && (C != CACHE_Q8 || a.pairs || a.rot % 64 == 0);
     return launch_programmatic(quads ? rope_quads_kernel<I, C, EPL * 32> : rope_append_kernel<I, C, EPL>,
                                dim3((unsigned)((warps + ROPE_WARPS - 1) / ROPE_WARPS)), ROPE_WARPS * 32, 0, s, a)
                ? QG_OK
@@ -595,6 +597,9 @@ int qg_rope_append(const void *q, int64_t ldq, int64_t hdq, const void *k, int64
     a.step_stride = cache->step_stride;
     a.bt = paged_batch(*cache, tokens);
     a.Hq = q_heads, a.Hk = Hk, a.rot = rot, a.pairs = pairs != 0;
+    a.runs4 = true;
+    for (const void *p : {q, k, v}) a.runs4 = a.runs4 && host_aligned(p, 4 * es);
+    for (const int64_t n : {ldq, hdq, ldk, hdk, ldv, hdv}) a.runs4 = a.runs4 && n % 4 == 0;
     a.amp = amp, a.eps = eps;
     // few tokens: a warp takes as many heads as it has room for in one step (latency); many: up to 24
     // share the sines, as long as the warps fill the machine

@@ -301,7 +301,8 @@ int qg_rope_turns(int rot, double base, int scaling, double factor, double origi
  * a and b being elements j and j + rot/2 (pairs = 0) or 2j and 2j + 1 (pairs = 1); elements
  * from rot on pass through.  The phase is a 64-bit product, exact at any position.
  *   q, k, v: in_type; token t, head h at t * ld + h * hd elements (views of one projection's
- *   output); every head aligned to min(16 bytes, dim/32 elements).  turns: device, rot/2.
+ *   output); every head aligned to dim/32 elements, at most 16 bytes (to 4 elements
+ *   it takes the fast path).  turns: device, rot/2.
  *   q_out: tokens x q_heads x dim contiguous, QG_F16 (QG_BF16 beside a QG_BF16 cache). */
 int qg_rope_append(const void *q, int64_t ldq, int64_t hdq, const void *k, int64_t ldk, int64_t hdk, const void *v,
                    int64_t ldv, int64_t hdv, int in_type, int tokens, int q_heads, const uint64_t *turns, int rot, int pairs,

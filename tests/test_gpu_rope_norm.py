@@ -147,6 +147,33 @@ def test_rope_gated_query_layout(qg):
     assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("src", [F32, F16], ids=["f32", "f16"])
+@pytest.mark.parametrize("off", [(2, 0, 0), (0, 2, 0), (0, 0, 2)])
+@pytest.mark.parametrize("D,pairs", [(64, False), (64, True), (128, False), (256, True)])
+def test_rope_heads_off_a_vector_boundary(qg, src, off, D, pairs):
+    """Heads that start, or lie, dim / 32 elements off a boundary of four: a view's base, token stride or head stride."""
+    g = gen(8)
+    q_start, lens, pages, n = tables([5, 1], [20, 1], 16, 1, g)
+    k, v, _, _ = make_cache(F16, n, 2, 16, D, g)
+    base, row, head = (o * D // 64 for o in off)
+    hd = D + head
+    ld = 8 * hd + row
+    buf = torch.randn(base + 6 * ld, generator=g, device="cuda").to(src)
+    x = torch.as_strided(buf, (6, 8, D), (ld, hd, 1), base)
+    turns = qg.qg_rope_turns(D)[0]
+    got = qg.qg_rope_append(x[:, :4], x[:, 4:6], x[:, 6:], turns.cuda(), k, v, q_start, lens, pages, pairs=pairs)
+    pos = np.concatenate([np.arange(15, 20), np.zeros(1)]).astype(np.int64)
+    want = rotate(x.double(), pos, turns.numpy().view(np.uint64).tolist(), 1.0, pairs)
+    slack = 2.0 ** -20 * x.double().abs().amax(-1, keepdim=True) + 2.0 ** -24
+    bound = UNIT[F16] * want.abs() + slack
+    within(got, want[:, :4], bound[:, :4], "q")
+    pg = pages.cpu().numpy()[[0] * 5 + [1], pos // 16]
+    where = (torch.from_numpy(pg).long().cuda(), torch.from_numpy(pos % 16).cuda())
+    within(values(k, None)[where[0], :, where[1]], want[:, 4:6], bound[:, 4:6], "k")
+    want = x[:, 6:].double()
+    within(values(v, None)[where[0], :, where[1]], want, UNIT[F16] * want.abs() + 2.0 ** -24, "v")
+
+
 def test_rope_zero_and_extreme_blocks_of_q8(qg):
     g = gen(7)
     q_start, lens, pages, n = tables([2], [2], 16, 0, g)
