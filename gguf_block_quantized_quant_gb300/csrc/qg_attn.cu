@@ -361,7 +361,7 @@ __global__ void __launch_bounds__(DecCfg<C, D, NR>::NW * 32, 1)
                 // lane (gr, gc) takes codes 8 gc .. of each 32-element block of slots gr and gr + 8
                 const int half = gc >> 1, turn = Cfg::PANEL == 128 ? gr : gr >> 1;  // the rows' places in the swizzle
                 const uint32_t krow = kt + gr * Cfg::PANEL + (gc & 1) * 8;
-#pragma unroll 2
+#pragma unroll 4
                 for (int j = 0; j < D / 32; ++j) {
                     uint32_t f0[4], f1[4];  // codes 0..3 and 4..7 of the lane's 8, slots gr and gr + 8
                     const uint32_t at = krow + (Cfg::PANEL == 128 ? (j >> 2) * (DEC_BLK * 128) + (((2 * (j & 3) + half) ^ turn) << 4)
