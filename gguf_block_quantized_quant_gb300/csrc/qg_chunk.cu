@@ -27,9 +27,10 @@
 // P is rounded to the value's 16-bit type, the operand type of the product: one rounding of
 // relative size 2^-12 (2^-9) per factor on average beside that of the result.
 //
-// Work is counted in slot tiles over all items (row tile, cache head) and cut into one equal range
-// per CTA, so causal rows, ragged batches and a few rows over a long context all load the
-// machine evenly.  Bound by the tensor cores for long chunks, by the exponentials at dim 64.
+// Work is counted in slot tiles over all items (row tile, cache head).  Where dealing whole items out,
+// the largest first and back and forth over the CTAs, loads them evenly enough, that is done: no
+// partial results, nothing to merge.  Else the list is cut into one equal range per CTA, so that
+// ragged batches and a few rows over a long context load the machine evenly too.  Bound by the tensor cores for long chunks, by the exponentials at dim 64.
 #include <algorithm>
 #include <mutex>
 #include <set>
@@ -104,6 +105,7 @@ struct ChunkTile {
 struct ChunkPlan {
     int64_t *total;    // tiles of all items
     int *nrt;          // row tiles
+    int *dealt;        // whole items are dealt out: the tiles are in order of falling cost
     int64_t *prefix;   // tiles before each row tile (all cache heads)
     ChunkTile *tile;
 };
@@ -114,6 +116,7 @@ static ChunkPlan chunk_plan_at(uint8_t *p, int64_t tiles) {
     ChunkPlan c;
     c.total = reinterpret_cast<int64_t *>(p);
     c.nrt = reinterpret_cast<int *>(p + 8);
+    c.dealt = reinterpret_cast<int *>(p + 12);
     c.tile = reinterpret_cast<ChunkTile *>(p + 16);
     c.prefix = reinterpret_cast<int64_t *>(p + 16 + (size_t)tiles * sizeof(ChunkTile));
     return c;
@@ -124,19 +127,24 @@ constexpr int PLAN_THREADS = 256, PLAN_SEQS = 1024;
 // An item costs its slot tiles and CHUNK_OV more for loading the queries and writing the result, in
 // the same unit; a range that ends inside that part leaves the item to the next CTA.
 constexpr int CHUNK_OV = 3;
+constexpr int CHUNK_CUT = 4;        // what a cut costs a CTA: a partial result more, and its merge
 constexpr int CHUNK_MIN_UNITS = 4;  // a CTA takes at least
+
+// The k-th item of CTA c where whole items are dealt out back and forth.
+__device__ __forceinline__ int deal(int k, int c, int ctas) { return k & 1 ? (k + 1) * ctas - 1 - c : k * ctas + c; }
 
 // One block lists the row tiles of all sequences with their slot ranges.  It stands before the
 // attention kernel in time, so it is built for few steps: one warp places the sequences' first tiles,
 // then a thread makes a tile and one barrier a prefix of their costs.
-__global__ void __launch_bounds__(PLAN_THREADS) attn_plan_kernel(const AttnArgs a, ChunkPlan p, int rows, int bn, int max_tiles) {
+__global__ void __launch_bounds__(PLAN_THREADS) attn_plan_kernel(const AttnArgs a, ChunkPlan p, int rows, int bn, int max_tiles, int ctas) {
     __shared__ int64_t part[2][PLAN_THREADS / 32];
+    __shared__ int unit[PLAN_THREADS], sorted[PLAN_THREADS];
     __shared__ int off[PLAN_SEQS + 1];
     griddep_wait();
     griddep_launch_dependents();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     int64_t cost_before = 0;
-    int tiles_before = 0, flip = 0;
+    int tiles_before = 0, flip = 0, dealt = 0;
     for (int c0 = 0; c0 < a.bt.batch; c0 += PLAN_SEQS) {
         const int nb = min(PLAN_SEQS, a.bt.batch - c0);
         if (c0) __syncthreads();
@@ -194,8 +202,29 @@ __global__ void __launch_bounds__(PLAN_THREADS) attn_plan_kernel(const AttnArgs 
                 if (w == warp) v += sum;
                 sum += part[flip][w];
             }
+            // A single round of tiles: order them by falling cost and see how evenly whole items load the CTAs
+            int place = at;
+            if (a.bt.batch <= PLAN_SEQS && count <= PLAN_THREADS) {
+                const int mine = on ? t.nt + CHUNK_OV : 0;
+                unit[tid] = mine;
+                __syncthreads();
+                int rank = 0;
+#pragma unroll 8
+                for (int i = 0; i < count; ++i) rank += unit[i] > mine || (unit[i] == mine && i < tid);
+                if (on) sorted[rank] = mine;
+                __syncthreads();
+                const int items = min(count, max_tiles) * a.Hk;
+                int64_t most = 0;
+                for (int c = tid; c < ctas; c += PLAN_THREADS) {
+                    int64_t load = 0;
+                    for (int k = 0, i = c; i < items; ++k, i = deal(k, c, ctas)) load += sorted[i / a.Hk];
+                    most = max(most, load);
+                }
+                dealt = !__syncthreads_or((most - CHUNK_CUT) * ctas > sum);
+                if (dealt) place = rank;
+            }
             if (on) {
-                p.tile[at] = t;
+                p.tile[place] = t;
                 p.prefix[at] = cost_before + v - cost;
             }
             cost_before += sum;
@@ -206,6 +235,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) attn_plan_kernel(const AttnArgs 
     if (tid == 0) {
         *p.total = cost_before;
         *p.nrt = min(tiles_before, max_tiles);
+        *p.dealt = dealt;
     }
 }
 
@@ -213,7 +243,8 @@ __global__ void __launch_bounds__(PLAN_THREADS) attn_plan_kernel(const AttnArgs 
 struct ChunkWalk {
     ChunkTile t;
     int rt, h, u;  // row tile, cache head, unit of the item
-    int64_t left;  // units left in this CTA's range
+    int64_t left;  // units left in this CTA's range (of the item, where items are dealt out)
+    int turn;      // items dealt to this CTA before
     __device__ __forceinline__ int blk() const { return max(0, u - CHUNK_OV); }  // first slot tile of the segment
     __device__ __forceinline__ int end() const { return (int)min((int64_t)t.nt, max((int64_t)0, u + left - CHUNK_OV)); }
 };
@@ -239,10 +270,27 @@ __device__ __forceinline__ ChunkWalk chunk_find(const ChunkPlan &p, int nrt, int
     k.h = (int)(rem / (k.t.nt + CHUNK_OV));
     k.u = (int)(rem % (k.t.nt + CHUNK_OV));
     k.left = 0;
+    k.turn = 0;
     return k;
 }
-// On to the next item of the range; left is 0 at its end.
-__device__ __forceinline__ void chunk_next(ChunkWalk &k, const ChunkPlan &p, int Hk) {
+// The item of turn k.turn of this CTA out of `dealt` items; left is 0 where there is none.
+__device__ __forceinline__ void chunk_deal(ChunkWalk &k, const ChunkPlan &p, int Hk, int dealt) {
+    const int i = deal(k.turn, blockIdx.x, gridDim.x);
+    k.left = 0;
+    if (i >= dealt) return;
+    k.rt = i / Hk;
+    k.h = i % Hk;
+    k.t = chunk_tile(p, k.rt);
+    k.u = CHUNK_OV;
+    k.left = k.t.nt;
+}
+// On to the next item of the range, or of those dealt (dealt: how many, 0: ranges); left is 0 at the end.
+__device__ __forceinline__ void chunk_next(ChunkWalk &k, const ChunkPlan &p, int Hk, int dealt) {
+    if (dealt) {
+        ++k.turn;
+        chunk_deal(k, p, Hk, dealt);
+        return;
+    }
     k.left -= k.t.nt + CHUNK_OV - k.u;
     k.u = 0;
     // a rest of CHUNK_OV units or less holds no slot tile
@@ -324,7 +372,10 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
     const int64_t w0 = (int)blockIdx.x < ctas ? rg.start(blockIdx.x) : 0;
     const int64_t w1 = (int)blockIdx.x < ctas ? rg.start(blockIdx.x + 1) : 0;
     ChunkWalk k{};
-    if (w1 > w0) {
+    const int dealt = *plan.dealt ? *plan.nrt * a.Hk : 0;
+    if (dealt) {
+        chunk_deal(k, plan, a.Hk, dealt);
+    } else if (w1 > w0) {
         k = chunk_find(plan, *plan.nrt, w0);
         k.left = w1 - w0;
         if (k.end() <= k.blk()) k.left = 0;  // the range ends before the item's first slot tile
@@ -382,7 +433,7 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
             const int blk0 = k.blk(), end = k.end();
             const int nrows = k.t.n * a.G, row0 = k.t.row0 + 128 * q;
             ChunkWalk nk = k;
-            chunk_next(nk, plan, a.Hk);
+            chunk_next(nk, plan, a.Hk, dealt);
             if (row0 < nrows) {
                 if (!qcopy) load_q(k);  // the products that read the last ones are complete
                 const int rr = row0 + r, pos0 = k.t.len - k.t.n;
@@ -714,7 +765,7 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
                     if (lane == 0) mbar_arrive(kv_empty(units % NS));
                 }
             }
-            chunk_next(k, plan, a.Hk);
+            chunk_next(k, plan, a.Hk, dealt);
         }
         // complete already on the normal path; after a wait gave up, let products in flight end
         if (lane == 0 && n) mbar_drain(pv_done(q, (n - 1) % SB), ((n - 1) / SB) & 1, DRAIN_NS);
@@ -800,7 +851,7 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
         int nj = k.blk();
         auto ahead = [&]() {
             if (nx.left > 0 && ++nj >= nx.end()) {
-                chunk_next(nx, plan, a.Hk);
+                chunk_next(nx, plan, a.Hk, dealt);
                 nj = nx.blk();
             }
             return lookup(nx, nj);
@@ -821,7 +872,7 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
 #pragma unroll
                 for (int h = 0; h < KU; ++h) copy(prev, h, k.h, true, j);
             }
-            chunk_next(k, plan, a.Hk);
+            chunk_next(k, plan, a.Hk, dealt);
         }
         if (lane == 0) {  // complete already on the normal path
             if constexpr (Cfg::Q8) {
@@ -858,7 +909,7 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
             } else if (vt < kt) {
                 ++vt;
             } else {
-                chunk_next(k, plan, a.Hk);
+                chunk_next(k, plan, a.Hk, dealt);
                 val = false;
                 on = k.left > 0;
                 blk0 = kt = k.blk();
@@ -1003,7 +1054,7 @@ static int chunk_run(const AttnArgs &in, const qg_paged &c, int sms, cudaStream_
     CUtensorMap qm{};
     if (qcopy && !attn_query_map(&qm, a, c.type == QG_BF16, D)) return QG_ECUDA;
     if (!attn_tensor_map(&km, c, c.k, box) || !attn_tensor_map(&vm, c, c.v, box)) return QG_ECUDA;
-    if (!launch_programmatic(attn_plan_kernel, dim3(1), PLAN_THREADS, 0, s, a, plan, Cfg::ROWS, Cfg::BN, (int)tiles)) return QG_ECUDA;
+    if (!launch_programmatic(attn_plan_kernel, dim3(1), PLAN_THREADS, 0, s, a, plan, Cfg::ROWS, Cfg::BN, (int)tiles, sms)) return QG_ECUDA;
     auto kern = attn_chunk_kernel<C, D>;
     // the warpgroups trade registers out of exactly this allocation
     static const bool regs_ok = [] {
