@@ -80,7 +80,11 @@ struct ChunkCfg {
     static constexpr int ISSUE_REGS = WGS == 2 ? 0 : !Q8 ? 88 : NQ == 2 ? 72 : 64;
     static constexpr int CONV_REGS = !Q8 ? 0 : NQ == 2 ? 136 : 120;
     static_assert(WGS == 2 || NQ * ROW_REGS + ISSUE_REGS + NCONV * CONV_REGS == WGS * LAUNCH_REGS, "registers");
-    static constexpr bool HOLD = !Q8 || D == 256;  // a row's scores fit a thread's registers
+    // A row's scores stay in a thread's registers, all code unrolled, where two row tiles' warps run the
+    // same code (4096 tokens after 28000, dim 128: 1.53 ms; in short loops 2.7).  With one row tile, or
+    // converting warps beside it, two passes of 32 scores at a time in short loops are faster, as the roles then
+    // share the instruction cache: 512 tokens after 8000, dim 256, 8-bit 194 -> 168 us, fp16 140 -> 128
+    static constexpr bool HOLD = !Q8 && D != 256;
     static constexpr int NBAR = 2 * NS + 2 * NQ + 4 * NQ * SB + 1 + 2 * NRAW;  // see the barriers below
     static constexpr uint32_t OUT_AT = NQ * QB;  // 32 rows x 64 bytes of results per warp
     static constexpr uint32_t KV_AT = OUT_AT + NQ * 4 * 2048;
@@ -392,35 +396,40 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
         const uint32_t mG = (uint32_t)((0x100000000ull + a.G - 1) / a.G);
         constexpr int CPR = D / 8;  // 16-byte chunks of a row
         // Queries come as tiled copies where the G heads of whole tokens make 128 rows, else (and with a
-        // negative scale) through registers; either way into the products' operand layout
+        // negative scale) as 16-byte copies of each warp's rows; either way into the products' operand layout
+        // and while the item before is finished
+        auto query_at = [&](int x) {
+            const int row = wr + x / CPR, ch = x % CPR;
+            return qtile + (ch >> 3) * (128 * 128) + row * 128 + (((ch & 7) ^ (row & 7)) << 4);
+        };
         auto fetch_q = [&](const ChunkWalk &w) {
-            if (!qcopy) return;
-            if (r == 0 && w.t.row0 + 128 * q < w.t.n * a.G) {
+            const int nrows = w.t.n * a.G, row0 = w.t.row0 + 128 * q;
+            if (row0 >= nrows) return;
+            if (!qcopy) {
+#pragma unroll 1
+                for (int i = 0; i < CPR; ++i) {
+                    // rows past the last are any rows: nothing of them is written
+                    const int x = i * 32 + lane, rr = min(row0 + wr + x / CPR, nrows - 1);
+                    int g;
+                    const int t = fast_div(rr, a.G, mG, g);
+                    cp_async16(query_at(x), static_cast<const T *>(a.q) + (int64_t)(w.t.first + t) * a.ldq + (int64_t)(w.h * a.G + g) * a.hdq +
+                                                8 * (x % CPR));
+                }
+            } else if (r == 0) {
                 mbar_arrive_expect_tx(q_full(q), Cfg::QB);
 #pragma unroll
                 for (int p = 0; p < Cfg::NP; ++p)
-                    tma_load_4d(qtile + p * (128 * 128), &qmap, 64 * p, 0, w.h, w.t.first + (w.t.row0 + 128 * q) / a.G, q_full(q));
+                    tma_load_4d(qtile + p * (128 * 128), &qmap, 64 * p, 0, w.h, w.t.first + row0 / a.G, q_full(q));
             }
         };
-        auto load_q = [&](const ChunkWalk &w) {
-            const int nrows = w.t.n * a.G, row0 = w.t.row0 + 128 * q;
-#pragma unroll
-            for (int i0 = 0; i0 < CPR; i0 += 8) {
-                uint4 v[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    // rows past the last are any rows: nothing of them is written
-                    const int x = (i0 + i) * 32 + lane, rr = min(row0 + wr + x / CPR, nrows - 1);
-                    int g;
-                    const int t = fast_div(rr, a.G, mG, g);
-                    v[i] = *reinterpret_cast<const uint4 *>(static_cast<const T *>(a.q) + (int64_t)(w.t.first + t) * a.ldq +
-                                                            (int64_t)(w.h * a.G + g) * a.hdq + 8 * (x % CPR));
-                }
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int x = (i0 + i) * 32 + lane, row = wr + x / CPR, ch = x % CPR;
-                    sts128(qtile + (ch >> 3) * (128 * 128) + row * 128 + (((ch & 7) ^ (row & 7)) << 4), v[i].x ^ qsign, v[i].y ^ qsign,
-                           v[i].z ^ qsign, v[i].w ^ qsign);
+        auto finish_q = [&]() {  // the thread's own 16-byte copies
+            cp_async_wait();
+            if (qsign) {
+#pragma unroll 1
+                for (int i = 0; i < CPR; ++i) {
+                    const uint32_t at = query_at(i * 32 + lane);
+                    const uint4 v = lds128(at);
+                    sts128(at, v.x ^ qsign, v.y ^ qsign, v.z ^ qsign, v.w ^ qsign);
                 }
             }
             fence_proxy_async_smem();
@@ -435,7 +444,7 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
             ChunkWalk nk = k;
             chunk_next(nk, plan, a.Hk, dealt);
             if (row0 < nrows) {
-                if (!qcopy) load_q(k);  // the products that read the last ones are complete
+                if (!qcopy) finish_q();
                 const int rr = row0 + r, pos0 = k.t.len - k.t.n;
                 int g;
                 const int pos = pos0 + fast_div(rr, a.G, mG, g);
@@ -451,10 +460,7 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
                     const bool edge = key0 + BN - 1 > hi_min || key0 < lo_max;
                     mbar_wait(s_full(q, buf), (done / SB) & 1);
                     tc_fence_after();
-                    if (j + 1 == end && nk.left > 0) fetch_q(nk);  // no product reads this item's queries any more
-                    // All scores of the row in registers (HOLD), or 32 at a time in two passes where the
-                    // converting warps leave too few registers
-                    uint32_t s[Cfg::HOLD ? BN / 32 : 2][32];
+                    uint32_t s[Cfg::HOLD ? BN / 32 : 1][32];
                     auto mask = [&](uint32_t (&v)[32], int c0) {
                         if (edge) {
                             const int up = c_hi - c0, down = c_lo - c0;  // visible: down .. up
@@ -488,15 +494,13 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
                             mx = fmaxf(mx, top(s[c]));
                         }
                     } else {
-                        tmem_ld32(scol, s[0]);
-#pragma unroll
+#pragma unroll 1
                         for (int c = 0; c < BN / 32; ++c) {
-                            tmem_wait_ld(s[c & 1]);
-                            if (c + 1 < BN / 32) tmem_ld32(scol + 32 * (c + 1), s[(c + 1) & 1]);
-                            mask(s[c & 1], 32 * c);
-                            mx = fmaxf(mx, top(s[c & 1]));
+                            tmem_ld32(scol + 32 * c, s[0]);
+                            tmem_wait_ld(s[0]);
+                            mask(s[0], 32 * c);
+                            mx = fmaxf(mx, top(s[0]));
                         }
-                        tmem_ld32(scol, s[0]);
                     }
                     if (!Cfg::P_OVER && done > 0) {  // P's place is free again
                         mbar_wait(pv_done(q, 0), (done - 1) & 1);
@@ -530,14 +534,13 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
                     // ---- P: chunk c of 32 scores becomes columns (words of a row) 16 c .. 16 c + 15
                     const uint64_t sc2 = pack_f32x2(a.scale2, a.scale2), mz2 = pack_f32x2(-mz, -mz);
                     uint64_t sum[2] = {0ull, 0ull};
-#pragma unroll
+#pragma unroll (Cfg::HOLD ? BN / 32 : 1)
                     for (int c = 0; c < BN / 32; ++c) {
-                        uint32_t(&v)[32] = s[Cfg::HOLD ? c : c & 1];
+                        uint32_t(&v)[32] = s[Cfg::HOLD ? c : 0];
                         if constexpr (!Cfg::HOLD) {
+                            tmem_ld32(scol + 32 * c, v);
                             tmem_wait_ld(v);
-                            if (c + 1 < BN / 32) {
-                                tmem_ld32(scol + 32 * (c + 1), s[(c + 1) & 1]);
-                            } else if (!Cfg::P_OVER) {
+                            if (!Cfg::P_OVER && c + 1 == BN / 32) {
                                 tc_fence_before();
                                 mbar_arrive(s_empty(q));
                             }
@@ -569,6 +572,7 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
                     tc_fence_before();
                     mbar_arrive(p_full(q, buf));
                 }
+                if (nk.left > 0) fetch_q(nk);  // no product reads this item's queries any more
                 // ---- result
                 mbar_wait(pv_done(q, (done - 1) % SB), ((done - 1) / SB) & 1);
                 tc_fence_after();

@@ -182,6 +182,12 @@ __device__ __forceinline__ bool mbar_drain(uint32_t bar, uint32_t parity, unsign
 }
 constexpr unsigned long long DRAIN_NS = 100000000ull;  // 100 ms
 
+// 16 bytes from global to shared memory by the thread's own asynchronous copy, and the wait for all of them.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
 // 1-D bulk copy global -> shared (this CTA), completion counted on `bar` in bytes.
 // dst, src and bytes must all be multiples of 16.
 __device__ __forceinline__ void bulk_g2s(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
