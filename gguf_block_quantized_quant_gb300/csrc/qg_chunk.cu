@@ -21,16 +21,26 @@
 // half of P while the second is made.  Measured and dropped for dim 128 (4096 tokens after 28000,
 // 32/8 heads, bf16): P over its scores and a score buffer per row tile, so that a tile's scores
 // wait for its last value product, 1.98 ms; P in shared memory, whose bandwidth then is the bound,
-// 1.83 ms; now 1.55 ms (1.30 PFLOP/s).  No product relies on the order of another that writes different columns:
+// 1.83 ms; now 1.53 ms (1.32 PFLOP/s).  No product relies on the order of another that writes different columns:
 // each waits for the barrier of what it overwrites, and each row tile's products are issued by a
 // warp of their own.
 // P is rounded to the value's 16-bit type, the operand type of the product: one rounding of
-// relative size 2^-12 (2^-9) per factor on average beside that of the result.
+// relative size 2^-12 (2^-9) per factor on average beside that of the result.  8-bit keys and values
+// become fp16 operands, step * code rounded once (relative 2^-12): the tensor cores take no int8
+// beside fp16, and splitting the step off would need a product per block of 32.
+//
+// The roles run at once and their code shares the instruction cache, which is what a kernel with
+// converting warps is sensitive to: each role's loop is written once and left rolled (softmax in chunks of
+// 32 scores, one place for all copies, one for each product).  512 tokens after 8000, 24/4 heads of 256,
+// 8-bit: 194 us with the roles unrolled, 146 now (0.71 PFLOP/s); there the conversion and the chain scores ->
+// softmax -> values of the single row tile take about equally long, and neither hides the other
+// entirely.  With two row tiles and 16-bit caches the tensor cores are the bound for long chunks, the
+// exponentials (16 a clock and SM) at dim 64.
 //
 // Work is counted in slot tiles over all items (row tile, cache head).  Where dealing whole items out,
 // the largest first and back and forth over the CTAs, loads them evenly enough, that is done: no
 // partial results, nothing to merge.  Else the list is cut into one equal range per CTA, so that
-// ragged batches and a few rows over a long context load the machine evenly too.  Bound by the tensor cores for long chunks, by the exponentials at dim 64.
+// ragged batches and a few rows over a long context load the machine evenly too.
 #include <algorithm>
 #include <mutex>
 #include <set>
@@ -85,7 +95,7 @@ struct ChunkCfg {
     // converting warps beside it, two passes of 32 scores at a time in short loops are faster, as the roles then
     // share the instruction cache: 512 tokens after 8000, dim 256, 8-bit 194 -> 168 us, fp16 140 -> 128
     static constexpr bool HOLD = !Q8 && D != 256;
-    static constexpr int NBAR = 2 * NS + 2 * NQ + 4 * NQ * SB + 1 + 2 * NRAW;  // see the barriers below
+    static constexpr int NBAR = 2 * NS + 2 * NQ + 4 * NQ * SB + 1 + 2 * NRAW;
     static constexpr uint32_t OUT_AT = NQ * QB;  // 32 rows x 64 bytes of results per warp
     static constexpr uint32_t KV_AT = OUT_AT + NQ * 4 * 2048;
     static constexpr uint32_t RAW_AT = KV_AT + NS * TILE;
@@ -748,17 +758,17 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
                 mbar_wait(q_full(q), items & 1);
                 ++items;
                 const bool both = NQ == 2 && k.t.row0 + 128 < k.t.n * a.G;
-                scores(0, both, units);
-                uint32_t u = units + KU;
-                for (int j = 0; j < taken; ++j) {
-                    const bool more = j + 1 < taken;
-                    const uint32_t v = more ? u + KU : u;  // the values come after the next keys
-                    if (more) scores(j + 1, both, u);
-                    product(n + j, j == 0, v, First{});
-                    product(n + j, j == 0, v, Second{});
-                    u = v + KU;
+                for (int j = 0; j <= taken; ++j) {  // the values of a tile come after the next one's keys
+                    if (j < taken) {
+                        scores(j, both, units);
+                        units += KU;
+                    }
+                    if (j > 0) {
+                        product(n + j - 1, j == 1, units, First{});
+                        product(n + j - 1, j == 1, units, Second{});
+                        units += KU;
+                    }
                 }
-                units = u;
                 n += taken;
                 both_before = both;
                 if (both || q == 1) other += taken;
@@ -793,9 +803,9 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
         uint32_t raws = 0;
         // Unit h of the keys or values of a tile; a lane's box and panel, and the 16 slots whose steps it copies
         auto copy = [&](const Place &p, int h, int head, bool val, int tile) {
+            constexpr int KP = Cfg::Q8 ? Cfg::KCP : Cfg::PKU, VP = Cfg::Q8 ? Cfg::VCP : Cfg::NP;
             const int rows = val ? VR : BN, first = val ? h * VR : 0;
-            const int panels = Cfg::Q8 ? (val ? Cfg::VCP : Cfg::KCP) : (val ? Cfg::NP : Cfg::PKU);
-            const int box = lane / panels, panel = lane % panels;
+            const int box = val ? lane / VP : lane / KP, panel = val ? lane % VP : lane % KP;
             const int from = first + box * box_rows;  // the box's first slot in the tile
             int page = __shfl_sync(0xffffffffu, p.page, (from / 16) & 31);
             const int s0 = __shfl_sync(0xffffffffu, p.slot, (from / 16) & 31);
@@ -803,23 +813,21 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
             if constexpr (Cfg::Q8) {
                 // codes and steps as they are, for the converting warpgroups
                 const uint32_t slot = units % Cfg::NRAW, bar = raw_full(slot);
-                const int bpage = __shfl_sync(0xffffffffu, p.page, (first / 16 + lane) & 31);
-                const int bslot = __shfl_sync(0xffffffffu, p.slot, (first / 16 + lane) & 31);
-                const bool here = lane < rows / 16, good = here && (unsigned)bpage < (unsigned)a.bt.n_pages;
-                constexpr uint32_t BS = 16 * (D / 32) * 2;  // bytes of 16 slots' steps
-                const uint32_t sdst = raw_steps + slot * Cfg::STEPS + lane * BS;
+                const bool here = box * box_rows < rows, steps = here && panel == 0, good = steps && page < a.bt.n_pages;
+                const uint32_t BS = box_rows * (D / 32) * 2;  // bytes of a box's steps
+                const uint32_t sdst = raw_steps + slot * Cfg::STEPS + box * BS;
                 if (units >= Cfg::NRAW) mbar_wait(raw_empty(slot), (units / Cfg::NRAW - 1) & 1);
-                if (here && !good)
+                if (steps && !good)
                     for (uint32_t x = 0; x < BS; x += 16) sts128(sdst + x, 0u, 0u, 0u, 0u);
                 const uint32_t goods = __popc(__ballot_sync(0xffffffffu, good));
                 __syncwarp();  // the zeros are written before the arrival below
                 if (lane == 0) mbar_arrive_expect_tx(bar, Cfg::CODES + goods * BS);
                 __syncwarp();
-                if (box < rows / box_rows)
+                if (here)
                     tma_load_4d(raw_codes + slot * Cfg::CODES + panel * (rows * Cfg::CPANEL) + box * box_rows * Cfg::CPANEL, val ? &vmap : &kmap,
                                 Cfg::CPANEL * ((val ? 0 : h) + panel), s0, head, page, bar);
                 if (good)
-                    bulk_g2s(sdst, (val ? a.vd : a.kd) + bpage * a.step_stride + ((int64_t)head * a.bt.page + bslot) * (D / 32), BS, bar);
+                    bulk_g2s(sdst, (val ? a.vd : a.kd) + page * a.step_stride + ((int64_t)head * a.bt.page + s0) * (D / 32), BS, bar);
             } else {
                 const uint32_t slot = units % NS;
                 // Slots that no row sees may hold anything, and 0 * NaN is not 0: their values become zeros before
@@ -835,7 +843,7 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
                 if (units >= NS) mbar_wait(kv_empty(slot), (units / NS - 1) & 1);
                 if (lane == 0) mbar_arrive_expect_tx(bar, Cfg::TILE);
                 __syncwarp();
-                if (box < rows / box_rows)
+                if (box * box_rows < rows)
                     tma_load_4d(kv0 + slot * Cfg::TILE + panel * (rows * 128) + box * box_rows * 128, val ? &vmap : &kmap,
                                 64 * ((val ? 0 : h * Cfg::PKU) + panel), s0, head, page, bar);
                 if (mend) {
@@ -860,21 +868,22 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
             }
             return lookup(nx, nj);
         };
-        Place cur = lookup(nx, nj), next = ahead();
+        Place prev{}, cur = lookup(nx, nj), next = ahead();
         while (k.left > 0) {
             const int blk0 = k.blk(), end = k.end();
-#pragma unroll
-            for (int h = 0; h < KU; ++h) copy(cur, h, k.h, false, 0);
-            for (int j = blk0; j < end; ++j) {
-                const Place prev = cur;
-                cur = next;
-                next = ahead();
-                if (j + 1 < end) {
-#pragma unroll
-                    for (int h = 0; h < KU; ++h) copy(cur, h, k.h, false, 0);
+            // the values of a tile come after the next one's keys; one place for all copies keeps the code short
+#pragma unroll 1
+            for (int j = blk0; j <= end; ++j) {
+#pragma unroll 1
+                for (int x = j < end ? 0 : KU; x < (j > blk0 ? 2 * KU : KU); ++x) {
+                    const bool val = x >= KU;
+                    copy(Place{val ? prev.page : cur.page, val ? prev.slot : cur.slot}, val ? x - KU : x, k.h, val, j - 1);
                 }
-#pragma unroll
-                for (int h = 0; h < KU; ++h) copy(prev, h, k.h, true, j);
+                if (j < end) {
+                    prev = cur;
+                    cur = next;
+                    next = ahead();
+                }
             }
             chunk_next(k, plan, a.Hk, dealt);
         }
@@ -936,8 +945,8 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
             const int seen_lo = a.window ? max(0, k.t.len - k.t.n + k.t.row0 / a.G - a.window + 1) : 0;
             const int from = max(0, seen_lo - key0), to = k.t.len - key0;  // rows of slots
             if (n >= NS) mbar_wait(kv_empty(slot), (n / NS - 1) & 1);
-            // a short loop: the roles run at once, and longer code misses in the instruction cache (512 tokens after
-            // 8000, dim 256: 188 us against 192 unrolled twice, 203 four times, 244 whole)
+            // a short loop: the roles run at once and share the instruction cache (512 tokens after 8000, dim 256:
+            // 146 us as it is or unrolled twice, 149 four times)
 #pragma unroll 1
             for (int i = 0; i < PER; ++i) {
                 const int row = i * RPS + r0;
