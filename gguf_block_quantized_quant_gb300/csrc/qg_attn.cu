@@ -806,6 +806,7 @@ int qg_attn_paged(const void *q, int64_t ldq, int64_t hdq, int q_type, int token
     if (q_type != (cache->type == QG_BF16 ? QG_BF16 : QG_F16) || (out_type != q_type && out_type != QG_F32)) return QG_EINVAL;
     const int D = cache->dim;
     if (q_heads % cache->kv_heads || ldq < D || hdq < D) return QG_EINVAL;
+    if ((int64_t)tokens * q_heads > INT32_MAX) return QG_EINVAL;  // rows of out are counted in 32 bits
     if (!host_aligned(q, 16) || ldq % 8 || hdq % 8 || !host_aligned(out, 16) || !host_aligned(lse, 4)) return QG_EALIGN;
     if (!ws || ws_bytes < qg_attn_workspace_size(D, q_heads, cache->kv_heads, tokens, cache->batch)) return QG_EWORKSPACE;
     if (!host_aligned(ws, 16)) return QG_EALIGN;

@@ -576,6 +576,7 @@ int qg_rope_append(const void *q, int64_t ldq, int64_t hdq, const void *k, int64
     if (const int rc = paged_check(*cache)) return rc;
     const int D = cache->dim, Hk = cache->kv_heads;
     if (rot < 0 || rot > D || rot % 2 || (rot && !turns) || !(eps >= 0.0f) || q_heads % Hk) return QG_EINVAL;
+    if ((int64_t)tokens * (q_heads + 2 * (int64_t)Hk) > INT32_MAX) return QG_EINVAL;
     if (hdq < D || hdk < D || hdv < D || ldq < D || ldk < D || ldv < D) return QG_EINVAL;
     const int es = type_size(in_type);
     const size_t va = (size_t)std::min(16, D / 32 * es);  // bytes of one lane's load

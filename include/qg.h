@@ -303,7 +303,8 @@ int qg_rope_turns(int rot, double base, int scaling, double factor, double origi
  *   q, k, v: in_type; token t, head h at t * ld + h * hd elements (views of one projection's
  *   output); every head aligned to dim/32 elements, at most 16 bytes (to 4 elements
  *   it takes the fast path).  turns: device, rot/2.
- *   q_out: tokens x q_heads x dim contiguous, QG_F16 (QG_BF16 beside a QG_BF16 cache). */
+ *   q_out: tokens x q_heads x dim contiguous, QG_F16 (QG_BF16 beside a QG_BF16 cache).
+ *   tokens x (q_heads + 2 kv_heads) < 2^31. */
 int qg_rope_append(const void *q, int64_t ldq, int64_t hdq, const void *k, int64_t ldk, int64_t hdk, const void *v,
                    int64_t ldv, int64_t hdv, int in_type, int tokens, int q_heads, const uint64_t *turns, int rot, int pairs,
                    float amp, const float *wq, const float *wk, float eps, void *q_out, const qg_paged *cache,
@@ -317,6 +318,7 @@ int qg_rope_append(const void *q, int64_t ldq, int64_t hdq, const void *k, int64
  *   out: tokens x q_heads x dim contiguous, q_type or QG_F32.  lse: tokens x q_heads fp32
  *   natural logarithms of the sums (-inf where nothing is visible), or NULL.
  *   max_new: the longest chunk of the batch; it chooses between two kernels and nothing else.
+ *   tokens x q_heads < 2^31.
  *   ws: qg_attn_workspace_size(dim, q_heads, kv_heads, tokens, batch) bytes, 16-byte aligned. */
 int qg_attn_paged(const void *q, int64_t ldq, int64_t hdq, int q_type, int tokens, int q_heads, int max_new, float scale,
                   int window, void *out, int out_type, float *lse, const qg_paged *cache, void *ws, size_t ws_bytes,

@@ -90,6 +90,12 @@ def test_rope_arguments(qg):
         assert rope(L, **kw) == -3, kw
 
 
+def test_row_counts_beyond_32_bits(qg):
+    L = qg.lib()
+    assert attn(L, tokens=1 << 29, heads=4, n=1 << 60) == -1
+    assert rope(L, tokens=(1 << 31) - 1, heads=64) == -1
+
+
 def norm(L, **kw):
     a = dict(y=A, yt=0, ldy=64, res=A, rt=0, ldr=64, wpost=None, gate=None, ldg=0, wpre=A, eps=1e-6, ro=A, xo=A, xt=0, M=2, H=64)
     a.update(kw)
