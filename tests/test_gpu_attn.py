@@ -290,3 +290,14 @@ def test_refusals(qg):
         qg.qg_attn_paged(q, k[:, :, :8], v[:, :, :8], q_start, lens, pages)  # pages of 8 slots
     with pytest.raises(qg.QGError):
         qg.qg_attn_paged(q, k, v, q_start, lens, pages, window=-1)
+
+
+@pytest.mark.parametrize("kind", KINDS, ids=IDS)
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("H,Hk", [(4, 4), (6, 2), (12, 2), (16, 2)])
+def test_chunks_of_other_groups_and_signs(qg, kind, D, H, Hk):
+    """Row tiles that are no whole tokens, and negative scales, whose queries come another way; several items per CTA."""
+    new, past = [130, 1, 300, 45], [0, 700, 500, 90]
+    for scale in (None, -D ** -0.5):
+        check(qg, kind, H, Hk, D, 16, new, [n + p for n, p in zip(new, past)], scale=scale, window=200, seed=H)
+    check(qg, kind, H, Hk, D, 64, [60] * 40, [60 + 13 * i for i in range(40)], seed=H + 1)
