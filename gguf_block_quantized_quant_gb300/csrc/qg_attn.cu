@@ -30,6 +30,11 @@ namespace qg {
 // Bound by the read of the cache; the products take a small part of that time, which is why the
 // probabilities can go in as two addends (hi + lo): the value sums then keep fp32 accuracy
 // instead of the 11 (8) bits of one fp16 (bf16) factor.
+//
+// 64 ragged sequences of 300 to 16000 slots, 32/8 heads of 128, bf16: 157 us, 0.92 of the measured copy
+// bandwidth.  8-bit caches are bound by the issue of the conversion to fp16 pairs instead: 48
+// sequences of 100 to 12000, 24/4 heads of 256, 59 us (0.61); one of 32000 19.5 us; one of 700 9.4
+// us, the latency of two launches and a chain of loads.
 constexpr int DEC_ROWS = 16;     // rows of a tile at most (NR = 2)
 constexpr int DEC_BLK = 16;      // slots per block: the least page size
 // An item costs its blocks and a fixed part more, in the same unit, for its queries, its last incomplete
