@@ -95,7 +95,9 @@ struct ChunkCfg {
     // converting warps beside it, two passes of 32 scores at a time in short loops are faster, as the roles then
     // share the instruction cache: 512 tokens after 8000, dim 256, 8-bit 194 -> 168 us, fp16 140 -> 128
     static constexpr bool HOLD = !Q8 && D != 256;
-    static constexpr int NBAR = 2 * NS + 2 * NQ + 4 * NQ * SB + 1 + 2 * NRAW;
+    // Every converting warpgroup has its own barriers for copied codes, one per area (raw_bar)
+    static constexpr int NRAWBAR = NRAW * (NCONV > 1 ? NCONV : 1);
+    static constexpr int NBAR = 2 * NS + 2 * NQ + 4 * NQ * SB + 1 + NRAW + NRAWBAR;
     static constexpr uint32_t OUT_AT = NQ * QB;  // 32 rows x 64 bytes of results per warp
     static constexpr uint32_t KV_AT = OUT_AT + NQ * 4 * 2048;
     static constexpr uint32_t RAW_AT = KV_AT + NS * TILE;
@@ -347,7 +349,15 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
     auto pv_done = [&](int q, int b) { return bars + 8u * (2 * NS + NQ + 2 * NQ * SB + q * SB + b); };
     auto p_half = [&](int q, int b) { return bars + 8u * (2 * NS + NQ + 3 * NQ * SB + q * SB + b); };
     auto s_empty = [&](int q) { return bars + 8u * (2 * NS + NQ + 4 * NQ * SB + q); };
-    auto raw_full = [&](int s) { return bars + 8u * (Cfg::NBAR - 1 - 2 * Cfg::NRAW + s); };
+    // Codes of unit u arrive in area u % NRAW on barrier u % NRAWBAR, phase u / NRAWBAR.  With two converting
+    // warpgroups the units of an area go to them in turn; a barrier per area alone would let one of them
+    // wait for a phase while the one before, which only the other waited for, is still open, and take
+    // its parity for the answer.  So a barrier's units are all one warpgroup's, which waits for every phase.
+    // A full barrier says more: unit u was copied after unit u - NRAW had been converted, into a slot whose
+    // earlier tile had been used, so the converters' waits on kv_empty are one phase away at most too (NS = NRAW there)
+    static_assert(Cfg::NCONV <= 1 || (Cfg::NRAWBAR % Cfg::NCONV == 0 && Cfg::NRAWBAR % Cfg::NRAW == 0 && Cfg::NS == Cfg::NRAW),
+                  "one warpgroup per barrier");
+    auto raw_full = [&](int s) { return bars + 8u * (Cfg::NBAR - 1 - Cfg::NRAW - Cfg::NRAWBAR + s); };
     auto raw_empty = [&](int s) { return bars + 8u * (Cfg::NBAR - 1 - Cfg::NRAW + s); };
     const uint32_t raw_codes = base + Cfg::RAW_AT, raw_steps = raw_codes + Cfg::NRAW * Cfg::CODES;
     const uint32_t v_raw = bars + 8u * (Cfg::NBAR - 1), taddr_slot = bars + 8u * Cfg::NBAR, turn = taddr_slot + 4;
@@ -358,10 +368,8 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
             mbar_init(kv_empty(s), NQ);
         }
         mbar_init(v_raw, 1);
-        for (int s = 0; s < Cfg::NRAW; ++s) {
-            mbar_init(raw_full(s), 1);
-            mbar_init(raw_empty(s), 128);
-        }
+        for (int s = 0; s < Cfg::NRAWBAR; ++s) mbar_init(raw_full(s), 1);
+        for (int s = 0; s < Cfg::NRAW; ++s) mbar_init(raw_empty(s), 128);
         for (int q = 0; q < NQ; ++q) {
             mbar_init(q_full(q), qcopy ? 1 : 128);
             mbar_init(s_empty(q), 128);
@@ -815,7 +823,7 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
             if ((unsigned)page >= (unsigned)a.bt.n_pages) page = a.bt.n_pages;
             if constexpr (Cfg::Q8) {
                 // codes and steps as they are, for the converting warpgroups
-                const uint32_t slot = units % Cfg::NRAW, bar = raw_full(slot);
+                const uint32_t slot = units % Cfg::NRAW, bar = raw_full(units % Cfg::NRAWBAR);
                 const bool here = box * box_rows < rows, steps = here && panel == 0, good = steps && page < a.bt.n_pages;
                 const uint32_t BS = box_rows * (D / 32) * 2;  // bytes of a box's steps
                 const uint32_t sdst = raw_steps + slot * Cfg::STEPS + box * BS;
@@ -892,8 +900,8 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
         }
         if (lane == 0) {  // complete already on the normal path
             if constexpr (Cfg::Q8) {
-                for (uint32_t s = 0; s < Cfg::NRAW && s < units; ++s)
-                    mbar_drain(raw_full(s), ((units - 1 - s) / Cfg::NRAW) & 1, DRAIN_NS);
+                for (uint32_t s = 0; s < Cfg::NRAWBAR && s < units; ++s)
+                    mbar_drain(raw_full(s), ((units - 1 - s) / Cfg::NRAWBAR) & 1, DRAIN_NS);
             } else {
                 for (uint32_t s = 0; s < NS && s < units; ++s) mbar_drain(kv_full(s), ((units - 1 - s) / NS) & 1, DRAIN_NS);
             }
@@ -942,7 +950,7 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
             const int odd = (ct >> 2) & 1;
             const int r0 = CPR == 4 ? ct / 4 : 2 * (ct / (2 * CPR)) + odd;
             const int ch = CPR == 4 ? ct % 4 : (CPR == 16 ? (ct >> 4 & 1) * 8 : 0) + 4 * (odd ^ (ct >> 3 & 1)) + (ct & 3);
-            mbar_wait(raw_full(raw), (n / Cfg::NRAW) & 1);
+            mbar_wait(raw_full(n % Cfg::NRAWBAR), (n / Cfg::NRAWBAR) & 1);
             // slots that no row sees may hold anything: they become zeros
             const int key0 = (k.t.kb0 + (VAL ? vt : kt)) * BN + (VAL ? h * VR : 0);
             const int seen_lo = a.window ? max(0, k.t.len - k.t.n + k.t.row0 / a.G - a.window + 1) : 0;
