@@ -450,8 +450,9 @@ __global__ void __launch_bounds__(ROPE_WARPS * 32) rope_quads_kernel(const RopeA
                     store_vec<Q, 4>(qo + h * D + e0, valid ? lo : zero);
                     store_vec<Q, 4>(qo + h * D + e1, valid ? hi : zero);
                 }
-                if (C != CACHE_Q8 || __all_sync(0xffffffffu, is_q)) continue;
             }
+            // Lanes of queries that share a step with keys stay: the shuffles below are the whole warp's
+            if (min(hb + u * HPI + HPI, h1) <= a.Hq) continue;  // whole warp
             const int kh = is_v ? h - a.Hq - a.Hk : h - a.Hq, f0 = is_v ? 8 * c : e0, f1 = is_v ? 8 * c + 4 : e1;
             const bool keep = live && !is_q && page >= 0;
             if constexpr (C != CACHE_Q8) {
