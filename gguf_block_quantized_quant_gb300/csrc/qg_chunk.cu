@@ -828,8 +828,10 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
                 const uint32_t BS = box_rows * (D / 32) * 2;  // bytes of a box's steps
                 const uint32_t sdst = raw_steps + slot * Cfg::STEPS + box * BS;
                 if (units >= Cfg::NRAW) mbar_wait(raw_empty(slot), (units / Cfg::NRAW - 1) & 1);
-                if (steps && !good)
+                if (steps && !good) {
                     for (uint32_t x = 0; x < BS; x += 16) sts128(sdst + x, 0u, 0u, 0u, 0u);
+                    fence_proxy_async_smem();  // a later bulk copy writes the same place
+                }
                 const uint32_t goods = __popc(__ballot_sync(0xffffffffu, good));
                 __syncwarp();  // the zeros are written before the arrival below
                 if (lane == 0) mbar_arrive_expect_tx(bar, Cfg::CODES + goods * BS);
@@ -982,8 +984,9 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
                 for (int y = 0; y < 2; ++y)
                     sts128(row_at + (((2 * (ch & 3) + y) ^ (row & 7)) << 4), x[4 * y], x[4 * y + 1], x[4 * y + 2], x[4 * y + 3]);
             }
-            mbar_arrive(raw_empty(raw));
+            // the copies that come next write the codes' place, and the products read the tile, by the async proxy
             fence_proxy_async_smem();
+            mbar_arrive(raw_empty(raw));
             mbar_arrive(kv_full(slot));
         };
         next_unit();

@@ -32,3 +32,25 @@ def test_8bit_chunks_of_wide_heads_repeat_bit_for_bit(qg, page):
             cold.fill_(i)  # the cache comes from memory again
         assert torch.equal(first, call())
     assert qg.qg_device_error() == 0
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_steps_of_missing_and_present_pages_in_turn(qg, D):
+    """Chunks whose tiles lie on missing pages and on present ones in turn: zeros that the copying warp wrote
+    and steps that bulk copies bring follow each other in one place."""
+    g = gen(D)
+    page, new, kv = 16, [150, 64, 300], [2000, 1500, 900]
+    q_start, lens, pages, n = tables(new, kv, page, 3, g)
+    k, v, kd, vd = make_cache("q8", n, 2, page, D, g)
+    q = (2 * torch.randn((sum(new), 8, D), generator=g, device="cuda")).half()
+    holes = pages.clone()
+    for b, length in enumerate(kv):
+        gone = torch.rand(-(-length // page), generator=g, device="cuda") < 0.4
+        holes[b, :gone.numel()] = torch.where(gone, -1, holes[b, :gone.numel()])
+        k[pages[b, :gone.numel()][gone].long()] = 0
+        v[pages[b, :gone.numel()][gone].long()] = 0
+    want = qg.qg_attn_paged(q, k, v, q_start, lens, pages, kd=kd, vd=vd, max_new=300)
+    o, _, A, B = attention(q, k, v, kd, vd, new, kv, pages, D ** -0.5, 0)
+    within(want, o, attention_bound(o, A, B, F16, F16, True), "out")
+    for _ in range(20):
+        assert torch.equal(want, qg.qg_attn_paged(q, k, v, q_start, lens, holes, kd=kd, vd=vd, max_new=300))
