@@ -9,6 +9,7 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/cuda/EmptyTensor.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Dtype.h>
@@ -65,19 +66,39 @@ long integer(PyObject *o) {
 void on(const at::Device &d, const Tensor *t) {
     need(!t || t->device() == d, "all tensors of a call must be on one CUDA device");
 }
-void *stream_of(PyObject *o, const at::Device &d) {
-    if (o == Py_None) return c10::cuda::getCurrentCUDAStream(d.index()).stream();
-    void *p = PyLong_AsVoidPtr(o);
-    if (PyErr_Occurred()) throw Bad("a stream is a torch.cuda.Stream");
-    return p;
-}
 template <class T = void>
 T *ptr(const Tensor *t) {
     return t ? static_cast<T *>(t->data_ptr()) : nullptr;
 }
-Tensor empty(at::IntArrayRef shape, ScalarType t, const at::Device &d) {
-    return at::detail::empty_cuda(shape, t, d, std::nullopt);
-}
+// The stream of a call (the current one, or the one given) and the tensors made for it.  They come from that
+// stream's memory: memory of the current stream's, freed and handed out again in that stream's order, could
+// meet work of the call that is still running or work of the current stream that is not done yet.
+class Call {
+  public:
+    Call(PyObject *o, const at::Device &d) : device_(d), current_(c10::cuda::getCurrentCUDAStream(d.index())), stream_(current_.stream()) {
+        if (o == Py_None) return;
+        void *p = PyLong_AsVoidPtr(o);
+        if (PyErr_Occurred()) throw Bad("a stream is a torch.cuda.Stream");
+        if (p == stream_) return;
+        stream_ = static_cast<cudaStream_t>(p);
+        guard_.reset_stream(c10::cuda::getStreamFromExternal(stream_, d.index()));
+    }
+    void *stream() const { return stream_; }
+    // A workspace: the call is its only user.
+    Tensor workspace(int64_t bytes) const { return at::detail::empty_cuda({bytes}, ScalarType::Byte, device_, std::nullopt); }
+    // An output, which the caller reads on the current stream (once it has waited for the call).
+    Tensor output(at::IntArrayRef shape, ScalarType t) const {
+        Tensor x = at::detail::empty_cuda(shape, t, device_, std::nullopt);
+        if (guard_.current_stream()) c10::cuda::CUDACachingAllocator::recordStream(x.storage().data_ptr(), current_);
+        return x;
+    }
+
+  private:
+    at::Device device_;
+    c10::cuda::CUDAStream current_;
+    cudaStream_t stream_;
+    c10::cuda::OptionalCUDAStreamGuard guard_;
+};
 // Rows of a 2-D tensor whose last dimension is contiguous: elements between them.
 int64_t rows(const Tensor &t, const char *what) {
     need(t.dim() == 2 && t.is_cuda() && (t.stride(1) == 1 || t.size(1) == 1), what);
@@ -181,23 +202,24 @@ PyObject *norm_residual(PyObject *, PyObject *const *a, Py_ssize_t n) {
         weight(w_pre, H);
         weight(w_post, H);
         const c10::cuda::CUDAGuard dev(y.device());
+        const Call call(a[11], y.device());
         Tensor r, x;
         if (ro) {
             need(ro->sizes() == y.sizes() && ro->scalar_type() == rt && ro->is_contiguous(), "res_out is contiguous, with res's shape and type");
         } else {
-            r = empty({M, H}, rt, y.device());
+            r = call.output({M, H}, rt);
             ro = &r;
         }
         if (xo) {
             need(xo->sizes() == y.sizes() && xo->is_contiguous() && w_pre, "x_out is contiguous, with y's shape, and needs w_pre");
         } else if (w_pre) {
-            x = empty({M, H}, dtype(a[8], y.scalar_type()), y.device());
+            x = call.output({M, H}, dtype(a[8], y.scalar_type()));
             xo = &x;
         }
         const int rc = qg_norm_residual(y.data_ptr(), type_of(y.scalar_type()), ldy, ptr(res), type_of(rt), ldr, ptr<const float>(w_post),
                                         ptr(gate), ldg, ptr<const float>(w_pre), (float)number(a[7]), (float)number(a[5]),
                                         (float)number(a[6]), ro->data_ptr(), ptr(xo), xo ? type_of(xo->scalar_type()) : QG_F32, (int)M, (int)H,
-                                        stream_of(a[11], y.device()));
+                                        call.stream());
         if (rc) return PyLong_FromLong(rc);
         PyObject *pr = THPVariable_Wrap(*ro), *px = xo ? THPVariable_Wrap(*xo) : (Py_INCREF(Py_None), Py_None);
         PyObject *out = PyTuple_Pack(2, pr, px);
@@ -231,17 +253,18 @@ PyObject *rope_append(PyObject *, PyObject *const *a, Py_ssize_t n) {
         weight(wk, D);
         for (const Tensor *t : {&nk, &nv, turns, &k, wq, wk, qo}) on(q.device(), t);
         const c10::cuda::CUDAGuard dev(q.device());
+        const Call call(a[18], q.device());
         Tensor o;
         if (qo) {
             need(qo->sizes() == q.sizes() && qo->scalar_type() == dt && qo->is_contiguous(), "q_out is contiguous, with q's shape");
         } else {
-            o = empty({T, H, D}, dt, q.device());
+            o = call.output({T, H, D}, dt);
             qo = &o;
         }
         const int rc = qg_rope_append(hq.p, hq.ld, hq.hd, hk.p, hk.ld, hk.hd, hv.p, hv.ld, hv.hd, type_of(q.scalar_type()), (int)T, (int)H,
                                       ptr<const uint64_t>(turns), turns ? (int)(2 * turns->numel()) : 0, PyObject_IsTrue(a[11]),
                                       (float)number(a[12]), ptr<const float>(wq), ptr<const float>(wk), (float)number(a[15]), qo->data_ptr(),
-                                      &c, stream_of(a[18], q.device()));
+                                      &c, call.stream());
         return rc ? PyLong_FromLong(rc) : THPVariable_Wrap(*qo);
     });
 }
@@ -264,12 +287,13 @@ PyObject *attn_paged(PyObject *, PyObject *const *a, Py_ssize_t n) {
         need(!lse || (lse->dim() == 2 && lse->size(0) == T && lse->size(1) == H && lse->scalar_type() == ScalarType::Float && lse->is_contiguous()),
              "lse is a contiguous fp32 tensor (tokens, heads)");
         const c10::cuda::CUDAGuard dev(q.device());
+        const Call call(a[15], q.device());
         Tensor o, w;
         if (out) {
             need(out->sizes() == q.sizes() && out->is_contiguous() && (out->scalar_type() == qt || out->scalar_type() == ScalarType::Float),
                  "out is contiguous, with q's shape, in q's type or fp32");
         } else {
-            o = empty({T, H, D}, dtype(a[11], qt), q.device());
+            o = call.output({T, H, D}, dtype(a[11], qt));
             out = &o;
         }
         size_t nws;
@@ -278,14 +302,14 @@ PyObject *attn_paged(PyObject *, PyObject *const *a, Py_ssize_t n) {
         } else {
             nws = qg_attn_workspace_size((int)D, (int)H, c.kv_heads, (int)T, c.batch);
             if (nws == (size_t)-1) return PyLong_FromLong(QG_EINVAL);
-            w = empty({(int64_t)nws}, ScalarType::Byte, q.device());
+            w = call.workspace((int64_t)nws);
             ws = &w;
         }
         const long max_new = a[8] == Py_None ? (T + c.batch - 1) / std::max(c.batch, 1) : integer(a[8]);
         const double scale = a[9] == Py_None ? 1.0 / std::sqrt((double)D) : number(a[9]);
         const int rc = qg_attn_paged(hq.p, hq.ld, hq.hd, type_of(qt), (int)T, (int)H, (int)max_new, (float)scale, (int)integer(a[10]),
                                      out->data_ptr(), type_of(out->scalar_type()), ptr<float>(lse), &c, ws->data_ptr(), nws,
-                                     stream_of(a[15], q.device()));
+                                     call.stream());
         return rc ? PyLong_FromLong(rc) : THPVariable_Wrap(*out);
     });
 }
