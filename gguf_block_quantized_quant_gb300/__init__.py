@@ -131,10 +131,23 @@ def _dev(t):
     return t.device if t.is_cuda else torch.device("cuda", torch.cuda.current_device())
 
 
-def _out(shape, dtype, like):
+def _empty(shape, dtype, device, stream, seen):
+    """Device memory of a call on `stream`, from that stream's pool: memory of the current stream's could
+    be handed out again while the call still runs, or have readers there that are not done.  seen:
+    an output, which the caller reads on the current stream."""
+    if stream is None or stream == torch.cuda.current_stream(device):
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if seen:
+        t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
+def _out(shape, dtype, like, stream):
     """An output next to the activations: on their device, or page-locked host memory."""
     if like.is_cuda:
-        return torch.empty(shape, dtype=dtype, device=like.device)
+        return _empty(shape, dtype, like.device, stream, True)
     return torch.empty(shape, dtype=dtype, pin_memory=True)
 
 
@@ -148,7 +161,7 @@ def _check(rc: int, what: str):
         raise QGError(rc, what)
 
 
-def _ws(ws, size_query, like):
+def _ws(ws, size_query, like, stream):
     """The workspace and its byte count: the caller's (the C call checks its size), or a new
     one of qg_workspace_size bytes on the device of the activations `like` (size_query()
     and the device lookup run only then)."""
@@ -158,7 +171,7 @@ def _ws(ws, size_query, like):
     if nbytes == WS_INVALID:
         raise QGError(QG_EINVAL, "qg_workspace_size")
     if nbytes > 0:
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=_dev(like))
+        ws = _empty(nbytes, torch.uint8, _dev(like), stream, False)
     return ws, (0 if ws is None else ws.numel())
 
 
@@ -169,9 +182,9 @@ def qg_workspace_size(op: int, fmt: int, M: int, N: int, K: int, E: int = 0, top
 
 def qg_quantize_act(x, xq=None, xd=None, xs=None, stream=None):
     M, K = x.shape
-    xq = _out((M, K), torch.int8, x) if xq is None else xq
-    xd = _out((M, K // 32), torch.float32, x) if xd is None else xd
-    xs = _out((M, K // 32), torch.int32, x) if xs is None else xs
+    xq = _out((M, K), torch.int8, x, stream) if xq is None else xq
+    xd = _out((M, K // 32), torch.float32, x, stream) if xd is None else xd
+    xs = _out((M, K // 32), torch.int32, x, stream) if xs is None else xs
     _check(lib().qg_quantize_act(_ptr(x), M, K, _ptr(xq), _ptr(xd), _ptr(xs), _stream(stream)),
            "qg_quantize_act")
     return xq, xd, xs
@@ -179,9 +192,9 @@ def qg_quantize_act(x, xq=None, xd=None, xs=None, stream=None):
 
 def qg_quantize_act_s16(x, xq=None, xd=None, xs=None, stream=None):
     M, K = x.shape
-    xq = _out((M, K), torch.int16, x) if xq is None else xq
-    xd = _out((M, K // 32), torch.float32, x) if xd is None else xd
-    xs = _out((M, K // 32), torch.int32, x) if xs is None else xs
+    xq = _out((M, K), torch.int16, x, stream) if xq is None else xq
+    xd = _out((M, K // 32), torch.float32, x, stream) if xd is None else xd
+    xs = _out((M, K // 32), torch.int32, x, stream) if xs is None else xs
     _check(lib().qg_quantize_act_s16(_ptr(x), M, K, _ptr(xq), _ptr(xd), _ptr(xs), _stream(stream)),
            "qg_quantize_act_s16")
     return xq, xd, xs
@@ -189,8 +202,8 @@ def qg_quantize_act_s16(x, xq=None, xd=None, xs=None, stream=None):
 
 def qg_gemv(fmt: int, W, x, N: int, y=None, ws=None, stream=None):
     M, K = x.shape
-    y = _out((M, N), torch.float32, x) if y is None else y
-    ws, nws = _ws(ws, lambda: qg_workspace_size(QG_OP_GEMV, fmt, M, N, K), x)
+    y = _out((M, N), torch.float32, x, stream) if y is None else y
+    ws, nws = _ws(ws, lambda: qg_workspace_size(QG_OP_GEMV, fmt, M, N, K), x, stream)
     _check(lib().qg_gemv(fmt, _ptr(W, False), _ptr(x), _ptr(y), N, K, M, _ptr(ws, False), nws, _stream(stream)), "qg_gemv")
     return y
 
@@ -203,15 +216,15 @@ def qg_gemv_static_ws(fmt: int, W, x, N: int, y=None, stream=None):
     calls that may overlap on the GPU must be ordered on one stream.  The first call on a
     device looks up the scratch address and should come before any stream capture."""
     M, K = x.shape
-    y = _out((M, N), torch.float32, x) if y is None else y
+    y = _out((M, N), torch.float32, x, stream) if y is None else y
     _check(lib().qg_gemv_static_ws(fmt, _ptr(W, False), _ptr(x), _ptr(y), N, K, M, _stream(stream)), "qg_gemv_static_ws")
     return y
 
 
 def qg_gemv_q(fmt: int, W, xq, xd, xs, N: int, y=None, ws=None, stream=None):
     M, K = xq.shape
-    y = _out((M, N), torch.float32, xq) if y is None else y
-    ws, nws = _ws(ws, lambda: qg_workspace_size(QG_OP_GEMV_Q, fmt, M, N, K), xq)
+    y = _out((M, N), torch.float32, xq, stream) if y is None else y
+    ws, nws = _ws(ws, lambda: qg_workspace_size(QG_OP_GEMV_Q, fmt, M, N, K), xq, stream)
     _check(lib().qg_gemv_q(fmt, _ptr(W, False), _ptr(xq), _ptr(xd), _ptr(xs), _ptr(y), N, K, M, _ptr(ws, False), nws,
                            _stream(stream)), "qg_gemv_q")
     return y
@@ -221,8 +234,8 @@ def qg_moe_ffn(fmt: int, x, Wr, topk: int, Wg_exps, Wu_exps, Wd_exps, Wg_sh, Wu_
                y=None, topk_ids=None, topk_w=None, ws=None, stream=None):
     M, H = x.shape
     E = Wr.shape[0]
-    y = _out((M, H), torch.float32, x) if y is None else y
-    ws, nws = _ws(ws, lambda: qg_workspace_size(QG_OP_MOE_FFN, fmt, M, H, H, E, topk, I), x)
+    y = _out((M, H), torch.float32, x, stream) if y is None else y
+    ws, nws = _ws(ws, lambda: qg_workspace_size(QG_OP_MOE_FFN, fmt, M, H, H, E, topk, I), x, stream)
     _check(lib().qg_moe_ffn(fmt, _ptr(x), M, H, _ptr(Wr, False), E, topk, _ptr(Wg_exps, False), _ptr(Wu_exps, False), _ptr(Wd_exps, False),
                             _ptr(Wg_sh, False), _ptr(Wu_sh, False), _ptr(Wd_sh, False), I, _ptr(y), _ptr(topk_ids), _ptr(topk_w),
                             _ptr(ws, False), nws, _stream(stream)), "qg_moe_ffn")
@@ -233,8 +246,8 @@ def qg_moe_ffn_s16(fmt: int, x, Wr, topk: int, Wg_exps, Wu_exps, Wd_exps, Wg_sh,
                    y=None, topk_ids=None, topk_w=None, ws=None, stream=None):
     M, H = x.shape
     E = Wr.shape[0]
-    y = _out((M, H), torch.float32, x) if y is None else y
-    ws, nws = _ws(ws, lambda: qg_workspace_size(QG_OP_MOE_FFN_S16, fmt, M, H, H, E, topk, I), x)
+    y = _out((M, H), torch.float32, x, stream) if y is None else y
+    ws, nws = _ws(ws, lambda: qg_workspace_size(QG_OP_MOE_FFN_S16, fmt, M, H, H, E, topk, I), x, stream)
     _check(lib().qg_moe_ffn_s16(fmt, _ptr(x), M, H, _ptr(Wr, False), E, topk, _ptr(Wg_exps, False), _ptr(Wu_exps, False),
                                 _ptr(Wd_exps, False), _ptr(Wg_sh, False), _ptr(Wu_sh, False), _ptr(Wd_sh, False), I, _ptr(y), _ptr(topk_ids),
                                 _ptr(topk_w), _ptr(ws, False), nws, _stream(stream)), "qg_moe_ffn_s16")
@@ -243,8 +256,8 @@ def qg_moe_ffn_s16(fmt: int, x, Wr, topk: int, Wg_exps, Wu_exps, Wd_exps, Wg_sh,
 
 def qg_ffn_sublayer(fmt: int, Wg, Wu, Wd, x, I: int, y=None, ws=None, stream=None):
     M, H = x.shape
-    y = _out((M, H), torch.float32, x) if y is None else y
-    ws, nws = _ws(ws, lambda: qg_workspace_size(QG_OP_FFN_SUBLAYER, fmt, M, H, H, 0, 0, I), x)
+    y = _out((M, H), torch.float32, x, stream) if y is None else y
+    ws, nws = _ws(ws, lambda: qg_workspace_size(QG_OP_FFN_SUBLAYER, fmt, M, H, H, 0, 0, I), x, stream)
     _check(lib().qg_ffn_sublayer(fmt, _ptr(Wg, False), _ptr(Wu, False), _ptr(Wd, False), _ptr(x), _ptr(y), M, H, I, _ptr(ws, False), nws,
                                  _stream(stream)), "qg_ffn_sublayer")
     return y
@@ -270,8 +283,8 @@ def qg_ffn_ws_layout(fmt: int, M: int, H: int, I: int):
 
 def qg_block_dots(fmt: int, W, xq, xs, N: int, stream=None):
     M, K = xq.shape
-    dots = _out((M, N, K // 32), torch.int32, xq)
-    aux = _out((M, N, K // 32), torch.int32, xq)
+    dots = _out((M, N, K // 32), torch.int32, xq, stream)
+    aux = _out((M, N, K // 32), torch.int32, xq, stream)
     _check(lib().qg_block_dots(fmt, _ptr(W, False), _ptr(xq), _ptr(xs), N, K, M, _ptr(dots), _ptr(aux), _stream(stream)),
            "qg_block_dots")
     return dots, aux
@@ -280,8 +293,8 @@ def qg_block_dots(fmt: int, W, xq, xs, N: int, stream=None):
 def qg_prefill_gemm(fmt: int, W, x, N: int, y=None, ws=None, stream=None):
     """Prefill GEMM on the tensor cores: y = fp16(W) fp16(x)^T in fp32, for M >> 16 tokens."""
     M, K = x.shape
-    y = _out((M, N), torch.float32, x) if y is None else y
-    ws, nws = _ws(ws, lambda: qg_workspace_size(QG_OP_PREFILL, fmt, M, N, K), x)
+    y = _out((M, N), torch.float32, x, stream) if y is None else y
+    ws, nws = _ws(ws, lambda: qg_workspace_size(QG_OP_PREFILL, fmt, M, N, K), x, stream)
     _check(lib().qg_prefill_gemm(fmt, _ptr(W, False), _ptr(x), _ptr(y), N, K, M, _ptr(ws, False), nws,
                                  _stream(stream)), "qg_prefill_gemm")
     return y
@@ -289,7 +302,7 @@ def qg_prefill_gemm(fmt: int, W, x, N: int, y=None, ws=None, stream=None):
 
 def qg_dequant_f16(fmt: int, W, N: int, K: int, stream=None):
     """Test hook: the fp16 weights (uint16 bit patterns, N x K) the prefill GEMM multiplies."""
-    out = torch.empty((N, K), dtype=torch.int16, device=W.device)
+    out = _empty((N, K), torch.int16, W.device, stream, True)
     _check(lib().qg_dequant_f16(fmt, _ptr(W, False), N, K, _ptr(out), _stream(stream)), "qg_dequant_f16")
     return out
 

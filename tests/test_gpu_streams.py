@@ -56,3 +56,22 @@ def test_rope_and_norms(qg):
     crossed(qg, lambda s: [qg.qg_rope_append(x[:, :8], x[:, 8:10], x[:, 10:], turns, k, v, q_start, lens, pages, stream=s)], [40 * 8 * 128 * 2])
     y, w = torch.randn((64, 2048), generator=g, device="cuda"), torch.ones(2048, device="cuda")
     crossed(qg, lambda s: qg.qg_norm_residual(y, y, w, stream=s), [y.nbytes])
+
+
+def test_projections_and_ffn(qg):
+    import synth
+    g = synth.rng(5, salt=7)
+    N, K, fmt = 512, 1024, qg.Q4_K
+    w = lambda n, kk: torch.from_numpy(synth.weights(fmt, n, kk, g)).cuda().reshape(-1)  # noqa: E731
+    W, Wg, Wu, Wd = w(N, K), w(512, K), w(512, K), w(K, 512)
+    t = gen(3)
+    for M in (1, 4, 16):
+        x = torch.randn((M, K), generator=t, device="cuda")
+        crossed(qg, lambda s: [qg.qg_gemv(fmt, W, x, N, stream=s)], [qg.qg_workspace_size(qg.QG_OP_GEMV, fmt, M, N, K), M * N * 4])
+        crossed(qg, lambda s: [qg.qg_ffn_sublayer(fmt, Wg, Wu, Wd, x, 512, stream=s)],
+                [qg.qg_workspace_size(qg.QG_OP_FFN_SUBLAYER, fmt, M, K, K, I=512), M * K * 4])
+        crossed(qg, lambda s: list(qg.qg_quantize_act(x, stream=s)), [M * K, M * K // 8])
+        q = qg.qg_quantize_act(x)
+        crossed(qg, lambda s: [qg.qg_gemv_q(fmt, W, *q, N, stream=s)], [max(1, qg.qg_workspace_size(qg.QG_OP_GEMV_Q, fmt, M, N, K)), M * N * 4])
+    x = torch.randn((100, K), generator=t, device="cuda")
+    crossed(qg, lambda s: [qg.qg_prefill_gemm(fmt, W, x, N, stream=s)], [qg.qg_workspace_size(qg.QG_OP_PREFILL, fmt, 100, N, K), 100 * N * 4])
