@@ -80,7 +80,7 @@ struct SeqWork {
     __device__ __forceinline__ SeqWork() {}
     __device__ __forceinline__ SeqWork(const AttnArgs &a, int b) : sq(seq_of(a.bt, b)) {
         nrt = (sq.n * a.G + ROWS - 1) / ROWS;
-        const int low = a.window ? max(0, sq.len - sq.n - a.window + 1) : 0;
+        const int low = seen_from(sq.len - sq.n, a.window);
         kb0 = low / DEC_BLK;
         nblk = max(1, (sq.len + DEC_BLK - 1) / DEC_BLK - kb0);
     }
@@ -328,12 +328,12 @@ __global__ void __launch_bounds__(DecCfg<C, D, NR>::NW * 32, 1)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 hi[r][i] = sq.len - sq.n + (rt * ROWS + min(8 * r + 2 * gc + i, nr - 1)) / a.G;
-                lo[r][i] = a.window ? max(0, hi[r][i] - a.window + 1) : 0;
+                lo[r][i] = seen_from(hi[r][i], a.window);
             }
         const int t_first = rt * ROWS / a.G, t_last = (rt * ROWS + nr - 1) / a.G;
         const int hi_min = sq.len - sq.n + t_first;                                               // every row sees up to here
-        const int lo_max = a.window ? max(0, sq.len - sq.n + t_last - a.window + 1) : 0;          // and from here
-        const int seen_lo = a.window ? max(0, hi_min - a.window + 1) : 0;                         // some row sees from here
+        const int lo_max = seen_from(sq.len - sq.n + t_last, a.window);                           // and from here
+        const int seen_lo = seen_from(hi_min, a.window);                                          // some row sees from here
         float o[NR][MT][4];  // O^T: columns 16 m + gr, + 8 of rows 8 r + 2 gc, + 1
 #pragma unroll
         for (int r = 0; r < NR; ++r)

@@ -35,6 +35,10 @@ struct AttnArgs {
     JoinDesc *desc;    // one per CTA
 };
 
+// First slot that a row at position pos sees (window 0: all).  No difference that could pass 32 bits: a window
+// of 2^31 - 1 over a sequence that begins with padding (pos < 0) is a call like any other.
+__device__ __forceinline__ int seen_from(int pos, int window) { return window && pos >= window ? pos - window + 1 : 0; }
+
 // One partial result: rows x D fp32 (normalised), then rows base-2 logarithms of the sums.
 __host__ __device__ constexpr size_t attn_part_floats(int rows, int D) { return (size_t)rows * D + rows; }
 

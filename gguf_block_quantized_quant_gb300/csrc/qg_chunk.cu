@@ -201,7 +201,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) attn_plan_kernel(const AttnArgs 
                 t.row0 = (r - off[lo]) * rows;
                 t.first = s.first, t.n = s.n, t.len = s.len;
                 const int tf = t.row0 / a.G, tl = (min(t.row0 + rows, s.n * a.G) - 1) / a.G;  // first, last token
-                const int from = a.window ? max(0, s.len - s.n + tf - a.window + 1) : 0;
+                const int from = seen_from(s.len - s.n + tf, a.window);
                 const int end = s.len - s.n + tl + 1;  // slots that the last row sees
                 t.kb0 = from / bn;
                 t.nt = max(1, (end + bn - 1) / bn - t.kb0);
@@ -469,9 +469,9 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
                 const int rr = row0 + r, pos0 = k.t.len - k.t.n;
                 int g;
                 const int pos = pos0 + fast_div(rr, a.G, mG, g);
-                const int hi = rr < nrows ? pos : -1, lo = a.window ? max(0, pos - a.window + 1) : 0;
+                const int hi = rr < nrows ? pos : -1, lo = seen_from(pos, a.window);
                 const int hi_min = pos0 + row0 / a.G;  // every row sees up to here, and from lo_max on
-                const int lo_max = a.window ? max(0, pos0 + (min(row0 + 128, nrows) - 1) / a.G - a.window + 1) : 0;
+                const int lo_max = seen_from(pos0 + (min(row0 + 128, nrows) - 1) / a.G, a.window);
                 float m = -INFINITY, l = 0.0f;
                 for (int j = blk0; j < end; ++j, ++done) {
                     const int buf = SB == 1 ? 0 : (int)(done & 1);
@@ -848,7 +848,7 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
                 int z0 = 0, z1 = VR;
                 if (val) {
                     const int key0 = (k.t.kb0 + tile) * BN + h * VR;
-                    const int seen_lo = a.window ? max(0, k.t.len - k.t.n + k.t.row0 / a.G - a.window + 1) : 0;
+                    const int seen_lo = seen_from(k.t.len - k.t.n + k.t.row0 / a.G, a.window);
                     z0 = min(VR, max(0, seen_lo - key0)), z1 = min(VR, max(0, k.t.len - key0));
                 }
                 const bool mend = z0 > 0 || z1 < VR;
@@ -955,7 +955,7 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
             mbar_wait(raw_full(n % Cfg::NRAWBAR), (n / Cfg::NRAWBAR) & 1);
             // slots that no row sees may hold anything: they become zeros
             const int key0 = (k.t.kb0 + (VAL ? vt : kt)) * BN + (VAL ? h * VR : 0);
-            const int seen_lo = a.window ? max(0, k.t.len - k.t.n + k.t.row0 / a.G - a.window + 1) : 0;
+            const int seen_lo = seen_from(k.t.len - k.t.n + k.t.row0 / a.G, a.window);
             const int from = max(0, seen_lo - key0), to = k.t.len - key0;  // rows of slots
             if (n >= NS) mbar_wait(kv_empty(slot), (n / NS - 1) & 1);
             // a short loop: the roles run at once and share the instruction cache (512 tokens after 8000, dim 256:

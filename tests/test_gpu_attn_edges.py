@@ -2,7 +2,7 @@
 import pytest
 import torch
 
-from layer_testlib import F16, attention, attention_bound, gen, make_cache, tables, within
+from layer_testlib import BF16, F16, attention, attention_bound, gen, make_cache, tables, within
 from qg_testlib import qg_module
 
 pytestmark = pytest.mark.gpu
@@ -54,3 +54,20 @@ def test_steps_of_missing_and_present_pages_in_turn(qg, D):
     within(want, o, attention_bound(o, A, B, F16, F16, True), "out")
     for _ in range(20):
         assert torch.equal(want, qg.qg_attn_paged(q, k, v, q_start, lens, holes, kd=kd, vd=vd, max_new=300))
+
+
+@pytest.mark.parametrize("kind", [F16, BF16, "q8"], ids=["f16", "bf16", "q8"])
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 7, 1 << 30])
+def test_widest_windows_over_padded_sequences(qg, kind, window):
+    """"No window" as the largest number, where sequences begin with padding: the rows see what they see without."""
+    g = gen(3)
+    new, kv = [10, 1, 7], [3, 20, 0]
+    q_start, lens, pages, n = tables(new, kv, 16, 1, g)
+    k, v, kd, vd = make_cache(kind, n, 2, 16, 128, g)
+    q = torch.randn((18, 4, 128), generator=g, device="cuda").to(F16 if kind == "q8" else kind)
+    for hint in (1, 60):
+        lse = [torch.empty((18, 4), device="cuda") for _ in range(2)]
+        want, got = (qg.qg_attn_paged(q, k, v, q_start, lens, pages, kd=kd, vd=vd, max_new=hint, window=w, lse=s)
+                     for w, s in zip((0, window), lse))
+        assert torch.equal(want, got) and torch.equal(*lse)
+        assert (got[:7] == 0).all() and (got[7:11] != 0).any(-1).all() and (got[11:] == 0).all()
