@@ -58,10 +58,15 @@ double number(PyObject *o) {
     if (v == -1.0 && PyErr_Occurred()) throw Bad("expected a number");
     return v;
 }
-long integer(PyObject *o) {
-    const long v = PyLong_AsLong(o);
+// The C interface counts in int: what does not fit is refused, not cut.
+int narrow(int64_t v) {
+    need(v == (int64_t)(int)v, "a size or an integer argument is beyond 32 bits");
+    return (int)v;
+}
+int integer(PyObject *o) {
+    const int64_t v = PyLong_AsLongLong(o);
     if (v == -1 && PyErr_Occurred()) throw Bad("expected an integer");
-    return v;
+    return narrow(v);
 }
 void on(const at::Device &d, const Tensor *t) {
     need(!t || t->device() == d, "all tensors of a call must be on one CUDA device");
@@ -147,8 +152,8 @@ qg_paged paged(const Tensor &k, const Tensor &v, const Tensor *kd, const Tensor 
     need(q_start.is_contiguous() && kv_len.is_contiguous(), "q_start and kv_len must be contiguous");
     for (const Tensor *t : {&v, kd, vd, &q_start, &kv_len, &pages}) on(k.device(), t);
     c.type = type;
-    c.kv_heads = (int)h, c.dim = (int)dim, c.page = (int)page, c.n_pages = (int)n;
-    c.batch = (int)batch, c.table_width = (int)pages.size(1);
+    c.kv_heads = narrow(h), c.dim = narrow(dim), c.page = narrow(page), c.n_pages = narrow(n);
+    c.batch = narrow(batch), c.table_width = narrow(pages.size(1));
     c.page_stride = k.stride(0), c.head_stride = k.stride(1), c.slot_stride = k.stride(2);
     c.table_stride = batch > 1 ? pages.stride(0) : std::max(pages.size(1), pages.stride(0));
     c.k = k.data_ptr(), c.v = v.data_ptr();
@@ -218,7 +223,7 @@ PyObject *norm_residual(PyObject *, PyObject *const *a, Py_ssize_t n) {
         }
         const int rc = qg_norm_residual(y.data_ptr(), type_of(y.scalar_type()), ldy, ptr(res), type_of(rt), ldr, ptr<const float>(w_post),
                                         ptr(gate), ldg, ptr<const float>(w_pre), (float)number(a[7]), (float)number(a[5]),
-                                        (float)number(a[6]), ro->data_ptr(), ptr(xo), xo ? type_of(xo->scalar_type()) : QG_F32, (int)M, (int)H,
+                                        (float)number(a[6]), ro->data_ptr(), ptr(xo), xo ? type_of(xo->scalar_type()) : QG_F32, narrow(M), narrow(H),
                                         call.stream());
         if (rc) return PyLong_FromLong(rc);
         PyObject *pr = THPVariable_Wrap(*ro), *px = xo ? THPVariable_Wrap(*xo) : (Py_INCREF(Py_None), Py_None);
@@ -261,8 +266,8 @@ PyObject *rope_append(PyObject *, PyObject *const *a, Py_ssize_t n) {
             o = call.output({T, H, D}, dt);
             qo = &o;
         }
-        const int rc = qg_rope_append(hq.p, hq.ld, hq.hd, hk.p, hk.ld, hk.hd, hv.p, hv.ld, hv.hd, type_of(q.scalar_type()), (int)T, (int)H,
-                                      ptr<const uint64_t>(turns), turns ? (int)(2 * turns->numel()) : 0, PyObject_IsTrue(a[11]),
+        const int rc = qg_rope_append(hq.p, hq.ld, hq.hd, hk.p, hk.ld, hk.hd, hv.p, hv.ld, hv.hd, type_of(q.scalar_type()), narrow(T), narrow(H),
+                                      ptr<const uint64_t>(turns), turns ? narrow(2 * turns->numel()) : 0, PyObject_IsTrue(a[11]),
                                       (float)number(a[12]), ptr<const float>(wq), ptr<const float>(wk), (float)number(a[15]), qo->data_ptr(),
                                       &c, call.stream());
         return rc ? PyLong_FromLong(rc) : THPVariable_Wrap(*qo);
@@ -300,14 +305,14 @@ PyObject *attn_paged(PyObject *, PyObject *const *a, Py_ssize_t n) {
         if (ws) {
             nws = ws->nbytes();
         } else {
-            nws = qg_attn_workspace_size((int)D, (int)H, c.kv_heads, (int)T, c.batch);
+            nws = qg_attn_workspace_size(c.dim, narrow(H), c.kv_heads, narrow(T), c.batch);
             if (nws == (size_t)-1) return PyLong_FromLong(QG_EINVAL);
             w = call.workspace((int64_t)nws);
             ws = &w;
         }
-        const long max_new = a[8] == Py_None ? (T + c.batch - 1) / std::max(c.batch, 1) : integer(a[8]);
+        const int max_new = a[8] == Py_None ? narrow((T + c.batch - 1) / std::max(c.batch, 1)) : integer(a[8]);
         const double scale = a[9] == Py_None ? 1.0 / std::sqrt((double)D) : number(a[9]);
-        const int rc = qg_attn_paged(hq.p, hq.ld, hq.hd, type_of(qt), (int)T, (int)H, (int)max_new, (float)scale, (int)integer(a[10]),
+        const int rc = qg_attn_paged(hq.p, hq.ld, hq.hd, type_of(qt), narrow(T), narrow(H), max_new, (float)scale, integer(a[10]),
                                      out->data_ptr(), type_of(out->scalar_type()), ptr<float>(lse), &c, ws->data_ptr(), nws,
                                      call.stream());
         return rc ? PyLong_FromLong(rc) : THPVariable_Wrap(*out);

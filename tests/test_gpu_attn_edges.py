@@ -71,3 +71,16 @@ def test_widest_windows_over_padded_sequences(qg, kind, window):
                      for w, s in zip((0, window), lse))
         assert torch.equal(want, got) and torch.equal(*lse)
         assert (got[:7] == 0).all() and (got[7:11] != 0).any(-1).all() and (got[11:] == 0).all()
+
+
+def test_arguments_beyond_32_bits_are_refused(qg):
+    g = gen(4)
+    q_start, lens, pages, n = tables([1], [40], 16, 1, g)
+    k, v, _, _ = make_cache(F16, n, 2, 16, 128, g)
+    q = torch.randn((1, 4, 128), generator=g, device="cuda").half()
+    for kw in (dict(window=1 << 32), dict(window=(1 << 32) + 8), dict(window=1 << 70), dict(max_new=(1 << 32) + 1)):
+        with pytest.raises((ValueError, OverflowError)):
+            qg.qg_attn_paged(q, k, v, q_start, lens, pages, **kw)
+    with pytest.raises(ValueError):
+        qg.qg_norm_residual(torch.empty(((1 << 32) + 1, 1), dtype=F16, device="cuda"), None, None)
+    torch.cuda.empty_cache()
