@@ -47,12 +47,12 @@ __global__ void __launch_bounds__(1024) norm_residual_kernel(const NormArgs a) {
     griddep_launch_dependents();
     const int warp = threadIdx.x >> 5;
     const int nw = a.tpr >> 5, rg = warp / nw, w0 = rg * nw;
-    const int row = blockIdx.x * (blockDim.x / a.tpr) + rg;
-    const bool live = row < a.M;
+    const unsigned row = blockIdx.x * (blockDim.x / a.tpr) + rg;  // the last block's may pass 2^31
+    const bool live = row < (unsigned)a.M;
     const int i0 = (threadIdx.x - w0 * 32) * VEC, step = a.tpr * VEC;
-    const Y *y = static_cast<const Y *>(a.y) + (live ? row : 0) * a.ldy;
-    const Y *gate = a.gate ? static_cast<const Y *>(a.gate) + (live ? row : 0) * a.ldgate : nullptr;
-    const R *res = a.res ? static_cast<const R *>(a.res) + (live ? row : 0) * a.ldres : nullptr;
+    const Y *y = static_cast<const Y *>(a.y) + (int64_t)(live ? row : 0) * a.ldy;
+    const Y *gate = a.gate ? static_cast<const Y *>(a.gate) + (int64_t)(live ? row : 0) * a.ldgate : nullptr;
+    const R *res = a.res ? static_cast<const R *>(a.res) + (int64_t)(live ? row : 0) * a.ldres : nullptr;
     const float inv = 1.0f / (float)a.H;
 
     // places past the row's end load its start and count as zero: a load under a branch would be
@@ -128,7 +128,7 @@ static int norm_launch(NormArgs a, cudaStream_t s) {
     const int per = VEC * NV;
     a.tpr = (((a.H + per - 1) / per) + 31) / 32 * 32;
     const int rpb = a.tpr >= 256 ? 1 : 256 / a.tpr;  // short rows share a block
-    return launch_programmatic(norm_residual_kernel<Y, R, X, VEC, NV>, dim3((unsigned)((a.M + rpb - 1) / rpb)), rpb * a.tpr,
+    return launch_programmatic(norm_residual_kernel<Y, R, X, VEC, NV>, dim3(((unsigned)a.M + rpb - 1) / rpb), rpb * a.tpr,
                                0, s, a)
                ? QG_OK
                : QG_ECUDA;
