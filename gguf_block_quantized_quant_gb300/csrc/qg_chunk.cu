@@ -171,25 +171,27 @@ __global__ void __launch_bounds__(PLAN_THREADS) attn_plan_kernel(const AttnArgs 
             int before = 0;
             for (int b0 = 0; b0 < nb; b0 += 32) {
                 int v = b0 + lane < nb ? (seq_of(a.bt, c0 + b0 + lane).n * a.G + rows - 1) / rows : 0;
+                // q_start that decreases could list more tiles than the call's tokens make: counts stop there, and
+                // those past it are left out
+                v = min(v, max_tiles);
                 const int mine = v;
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) {
                     const int u = __shfl_up_sync(0xffffffffu, v, o);
                     if (lane >= o) v += u;
                 }
-                if (b0 + lane < nb) off[b0 + lane] = before + v - mine;
-                before += __shfl_sync(0xffffffffu, v, 31);
+                if (b0 + lane < nb) off[b0 + lane] = min(before + v - mine, max_tiles);
+                before = min(before + __shfl_sync(0xffffffffu, v, 31), max_tiles);
             }
             if (lane == 0) off[nb] = before;
         }
         __syncthreads();
-        const int count = off[nb];
+        const int count = min(off[nb], max_tiles - tiles_before);
         for (int r0 = 0; r0 < count; r0 += PLAN_THREADS) {
             const int r = r0 + tid, at = tiles_before + r;
             int64_t cost = 0;
             ChunkTile t{};
-            // q_start that decreases could list more tiles than the call's tokens make: those are left out
-            const bool on = r < count && at < max_tiles;
+            const bool on = r < count;
             if (on) {
                 int lo = 0, hi = nb;  // off[lo] <= r < off[hi]
                 while (hi - lo > 1) {
@@ -232,7 +234,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) attn_plan_kernel(const AttnArgs 
                 for (int i = 0; i < count; ++i) rank += unit[i] > mine || (unit[i] == mine && i < tid);
                 if (on) sorted[rank] = mine;
                 __syncthreads();
-                const int items = min(count, max_tiles) * a.Hk;
+                const int items = count * a.Hk;
                 int64_t most = 0;
                 for (int c = tid; c < ctas; c += PLAN_THREADS) {
                     int64_t load = 0;
@@ -253,7 +255,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) attn_plan_kernel(const AttnArgs 
     }
     if (tid == 0) {
         *p.total = cost_before;
-        *p.nrt = min(tiles_before, max_tiles);
+        *p.nrt = tiles_before;
         *p.dealt = dealt;
     }
 }

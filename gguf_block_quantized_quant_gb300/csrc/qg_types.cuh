@@ -171,13 +171,15 @@ struct Seq {
     int len;    // slots in use
 };
 
+constexpr int64_t MAX_SLOTS = 0x7fffff00;  // of a sequence: a tile that holds its last slot ends below 2^31
+
 // The sequence's lengths, held inside the caller's arrays: token rows inside [0, tokens), slots
-// inside the page table.
+// inside the page table (and below MAX_SLOTS).
 __device__ __forceinline__ Seq seq_of(const Batch &bt, int b) {
     Seq s;
     s.first = min(max(bt.q_start[b], 0), bt.tokens);
     s.n = min(max(bt.q_start[b + 1], s.first), bt.tokens) - s.first;
-    s.len = (int)min((int64_t)max(bt.kv_len[b], 0), (int64_t)bt.table_width * bt.page);
+    s.len = (int)min((int64_t)max(bt.kv_len[b], 0), min((int64_t)bt.table_width * bt.page, MAX_SLOTS));
     return s;
 }
 

@@ -84,3 +84,45 @@ def test_arguments_beyond_32_bits_are_refused(qg):
     with pytest.raises(ValueError):
         qg.qg_norm_residual(torch.empty(((1 << 32) + 1, 1), dtype=F16, device="cuda"), None, None)
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("kind", [F16, "q8"], ids=["f16", "q8"])
+def test_slots_up_to_the_last_that_counts(qg, kind):
+    """Positions next to 2^31 (one page, listed again and again), seen through a window."""
+    g = gen(6)
+    page, D, window, L = 1 << 20, 64, 200, 2 ** 31 - 256
+    k, v, kd, vd = make_cache(kind, 1, 1, page, D, g)
+    pages = torch.zeros((1, 1 << 11), dtype=torch.int32, device="cuda")
+    q = torch.randn((3, 4, D), generator=g, device="cuda").half()
+    q_start = torch.tensor([0, 3], dtype=torch.int32, device="cuda")
+    near = slice(L % page - 400, L % page)  # the last 400 slots, as a sequence of their own
+    short = [None if t is None else t[:, :, near].contiguous() for t in (k, v, kd, vd)]
+    for length in (L, 2 ** 31 - 1):  # held to L
+        lens = torch.tensor([length], dtype=torch.int32, device="cuda")
+        for hint in (1, 60):
+            got = qg.qg_attn_paged(q, k, v, q_start, lens, pages, kd=kd, vd=vd, max_new=hint, window=window)
+            ids = torch.zeros((1, 1), dtype=torch.int32, device="cuda")
+            o, _, A, B = attention(q, *short, [3], [400], ids, D ** -0.5, window)
+            within(got, o, attention_bound(o, A, B, F16, F16, kind == "q8"), "far")
+    torch.cuda.empty_cache()
+
+
+def test_q_start_that_decreases_stays_inside_the_arrays(qg):
+    """The rows' values are not defined then; every access is, and nothing else is written."""
+    g = gen(7)
+    batch, T = 3000, 600
+    k, v, _, _ = make_cache(F16, 8, 2, 16, 64, g)
+    pages = torch.arange(8, dtype=torch.int32, device="cuda").repeat(batch, 1)
+    q = torch.randn((T, 8, 64), generator=g, device="cuda").half()
+    lens = torch.full((batch,), 100, dtype=torch.int32, device="cuda")
+    need = qg.qg_attn_workspace_size(64, 8, 2, T, batch)
+    for n in (batch, 700, 5):
+        starts = torch.tensor([0, T] * (n // 2) + [0] * (1 + n % 2), dtype=torch.int32, device="cuda")[:n + 1].contiguous()
+        for hint in (1, 60):
+            need = qg.qg_attn_workspace_size(64, 8, 2, T, n)
+            ws = torch.full((need + 4096,), 7, dtype=torch.uint8, device="cuda")
+            out = torch.zeros((T + 64, 8, 64), dtype=F16, device="cuda")
+            qg.qg_attn_paged(q, k, v, starts, lens[:n], pages[:n], out=out[:T], ws=ws[:need], max_new=hint)
+            torch.cuda.synchronize()
+            assert (ws[need:] == 7).all() and (out[T:] == 0).all() and torch.isfinite(out).all()
+    assert qg.qg_device_error() == 0
