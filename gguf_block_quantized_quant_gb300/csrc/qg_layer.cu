@@ -556,7 +556,7 @@ int qg_rope_turns(int rot, double base, int scaling, double factor, double origi
     if (scaling == QG_ROPE_YARN) {
         const double per = half / std::log(base);
         lo = std::fmax(std::floor(per * std::log(original / (beta_fast * two_pi))), 0.0);
-        hi = std::fmin(std::ceil(per * std::log(original / (beta_slow * two_pi))), half - 1.0);
+        hi = std::fmin(std::ceil(per * std::log(original / (beta_slow * two_pi))), rot - 1.0);  // the ramp may end past the last pair
     }
     for (int j = 0; j < half; ++j) {
         const double f = std::pow(base, -(double)j / half);

@@ -289,7 +289,9 @@ typedef struct qg_paged {
  * position: turns[j] = floor(2^64 * f_j / (2 pi)) for j < rot/2, f_j = base^(-2j/rot) scaled by
  *   PLAIN: nothing.   LINEAR: f / factor.   NTK: base * factor^(rot/(rot-2)) as the base.
  *   YARN: f / factor * ramp + f * (1 - ramp), ramp rising from 0 to 1 between the pairs that
- *   turn beta_fast and beta_slow times within `original` positions.
+ *   turn beta_fast and beta_slow times within `original` positions: from pair max(floor(e(beta_fast)), 0)
+ *   to pair min(ceil(e(beta_slow)), rot - 1), e(n) = rot ln(original / (2 pi n)) / (2 ln base); the
+ *   second may lie past the last pair, which then keeps a part of its own frequency.
  * *amp (may be NULL) receives the factor of the rotated values: 0.1 ln(factor) + 1 for YARN,
  * else 1.  Host function: turns is host memory (upload it once). */
 int qg_rope_turns(int rot, double base, int scaling, double factor, double original, double beta_fast, double beta_slow,
