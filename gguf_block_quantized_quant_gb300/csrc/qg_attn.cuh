@@ -29,6 +29,7 @@ struct AttnArgs {
     int out_f32;       // out is fp32 instead of the queries' type
     int window;        // 0: none
     float scale2;      // scale * log2(e): the kernels work in powers of two
+    float scale_p2;    // the power of two below it (chunk kernel)
     const f16 *kd, *vd;
     int64_t step_stride;
     float *part;       // partial results (attn_part_floats each)

@@ -42,6 +42,7 @@
 // partial results, nothing to merge.  Else the list is cut into one equal range per CTA, so that
 // ragged batches and a few rows over a long context load the machine evenly too.
 #include <algorithm>
+#include <cmath>
 #include <mutex>
 #include <set>
 #include <utility>
@@ -327,6 +328,11 @@ __device__ __forceinline__ int chunk_ctas(int64_t total, int max_ctas) {
     return (int)min((int64_t)max_ctas, max((int64_t)1, total / CHUNK_MIN_UNITS));
 }
 
+// Whether a row's scaled maximum is so large that S * scale2 - m * scale2 is not near 0 at S = m any more: the
+// product with m is rounded to a multiple of 1/2 and more.  The factor is a power of two then, whose products
+// are exact; the scores themselves are off by more than what that changes.
+__device__ __forceinline__ bool chunk_far(float m, float scale2) { return !(fabsf(m * scale2) < 4194304.0f); }
+
 // ----------------------------------------------------------------------------- kernel
 template <int C, int D>
 __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
@@ -357,8 +363,7 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
     // its parity for the answer.  So a barrier's units are all one warpgroup's, which waits for every phase.
     // A full barrier says more: unit u was copied after unit u - NRAW had been converted, into a slot whose
     // earlier tile had been used, so the converters' waits on kv_empty are one phase away at most too (NS = NRAW there)
-    static_assert(Cfg::NCONV <= 1 || (Cfg::NRAWBAR % Cfg::NCONV == 0 && Cfg::NRAWBAR % Cfg::NRAW == 0 && Cfg::NS == Cfg::NRAW),
-                  "one warpgroup per barrier");
+    static_assert(Cfg::NCONV <= 1 || Cfg::NS == Cfg::NRAW, "phases of kv_empty");
     auto raw_full = [&](int s) { return bars + 8u * (Cfg::NBAR - 1 - Cfg::NRAW - Cfg::NRAWBAR + s); };
     auto raw_empty = [&](int s) { return bars + 8u * (Cfg::NBAR - 1 - Cfg::NRAW + s); };
     const uint32_t raw_codes = base + Cfg::RAW_AT, raw_steps = raw_codes + Cfg::NRAW * Cfg::CODES;
@@ -553,9 +558,12 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
                             tmem_wait_st();
                         }
                     }
-                    const float mz = (m == -INFINITY ? 0.0f : m) * a.scale2;
+                    // exponents x = S * sc - mz
+                    const bool far = chunk_far(m, a.scale2);
+                    const float sc = far ? a.scale_p2 : a.scale2;
+                    const float mz = m == -INFINITY ? 0.0f : m * sc;
                     // ---- P: chunk c of 32 scores becomes columns (words of a row) 16 c .. 16 c + 15
-                    const uint64_t sc2 = pack_f32x2(a.scale2, a.scale2), mz2 = pack_f32x2(-mz, -mz);
+                    const uint64_t sc2 = pack_f32x2(sc, sc), mz2 = pack_f32x2(-mz, -mz);
                     uint64_t sum[2] = {0ull, 0ull};
 #pragma unroll (Cfg::HOLD ? BN / 32 : 1)
                     for (int c = 0; c < BN / 32; ++c) {
@@ -1077,6 +1085,7 @@ static int chunk_run(const AttnArgs &in, const qg_paged &c, int sms, cudaStream_
     // a scale of zero is a small one (masked scores stay -inf)
     const uint32_t qsign = a.scale2 < 0.0f ? 0x80008000u : 0u;
     a.scale2 = std::max(std::abs(a.scale2), 1e-30f);
+    a.scale_p2 = std::exp2(std::floor(std::log2(a.scale2)));
     const int box = gcd(c.page, Cfg::VR);
     CUtensorMap km{}, vm{};
     const bool qcopy = 128 % a.G == 0 && !qsign;

@@ -2,7 +2,7 @@
 import pytest
 import torch
 
-from layer_testlib import BF16, F16, attention, attention_bound, gen, make_cache, tables, within
+from layer_testlib import BF16, F16, UNIT, attention, attention_bound, gen, make_cache, sequence, tables, within
 from qg_testlib import qg_module
 
 pytestmark = pytest.mark.gpu
@@ -126,3 +126,40 @@ def test_q_start_that_decreases_stays_inside_the_arrays(qg):
             torch.cuda.synchronize()
             assert (ws[need:] == 7).all() and (out[T:] == 0).all() and torch.isfinite(out).all()
     assert qg.qg_device_error() == 0
+
+
+@pytest.mark.parametrize("kind,spread,scale", [(F16, 60.0, 8.0), (F16, 2000.0, 1.0), (F16, 2000.0, -3.0), (BF16, 1e3, 0.7), (BF16, 1e6, 1.0), (BF16, 3e3, 77.0)])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_scores_of_millions_and_more(qg, kind, spread, scale, D):
+    """Softmax of such scores is one slot where it leads by more than the scores' own error: that slot's values
+    come out, and nothing becomes zero or infinite."""
+    g = gen(D)
+    new, kv = [150, 4, 1], [700, 333, 90]
+    q_start, lens, pages, n = tables(new, kv, 32, 1, g)
+    k, v, _, _ = make_cache(kind, n, 2, 32, D, g)
+    k.mul_(spread)
+    q = (spread * torch.randn((155, 4, D), generator=g, device="cuda")).to(kind)
+    o, want_lse, A, B = attention(q, k, v, None, None, new, kv, pages, scale, 0)
+    for hint in (1, 150):
+        lse = torch.empty((155, 4), device="cuda")
+        out = qg.qg_attn_paged(q, k, v, q_start, lens, pages, scale=scale, lse=lse, max_new=hint)
+        assert torch.isfinite(out).all() and torch.isfinite(lse).all()
+        # |lse - want| within the scores' error dS of the bound's derivation
+        assert ((lse.double() - want_lse).abs() <= 2.0 ** -18 * B + 1).all()
+        # the weight of the leading slot from the reference: o is one row of v (A = |o|) where it leads by far
+        clear = ((A - o.abs()) == 0).all(-1) & lead(q, k, kv, new, pages, scale, 2.0 ** -17 * B + 40)
+        assert clear.float().mean() > 0.5
+        within(out[clear], o[clear], 3 * UNIT[kind] * o[clear].abs() + 2.0 ** -16, "out")
+
+
+def lead(q, k, kv, new, pages, scale, least):
+    """Rows whose largest visible score leads the next by `least`."""
+    out, at = torch.zeros(q.shape[:2], dtype=torch.bool, device=q.device), 0
+    for b, (n, L) in enumerate(zip(new, kv)):
+        kk = sequence(k, None, pages[b], L).repeat_interleave(q.shape[1] // k.shape[1], 0)
+        z = (q[at:at + n].double().transpose(0, 1) @ kk.transpose(1, 2)) * scale
+        z = z.masked_fill(torch.arange(L, device=q.device)[None] > torch.arange(L - n, L, device=q.device)[:, None], -float("inf"))
+        top = z.topk(2, -1).values
+        out[at:at + n] = (top[..., 0] - top[..., 1]).transpose(0, 1) > least[at:at + n]
+        at += n
+    return out
