@@ -188,6 +188,15 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
                      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// The exponent that probabilities are taken relative to, for scores of at most v: they may be up to 2^15 in
+// fp16, so that those down to 2^-40 of the largest are still seen by the products (at 2^-25, the end with the
+// largest at 1, 33000 slots 17.4 nats below it lost 9e-4 of the result while the sum counted them).  bf16 has
+// fp32's range.  From 2^23 on v - 15 is too coarse for that.
+template <class T>
+__device__ __forceinline__ float p_top(float v) {
+    return std::is_same<T, f16>::value && fabsf(v) < 8388608.0f ? v - 15.0f : v;
+}
+
 template <int C, int D, int NR>
 __global__ void __launch_bounds__(DecCfg<C, D, NR>::NW * 32, 1)
     attn_rows_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
@@ -415,7 +424,7 @@ __global__ void __launch_bounds__(DecCfg<C, D, NR>::NW * 32, 1)
                     v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
                     v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
                     v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
-                    mn[r][i] = fmaxf(mx[r][i], v);
+                    mn[r][i] = fmaxf(mx[r][i], p_top<T>(v));
                     grown = grown || mn[r][i] > mx[r][i];
                 }
             }

@@ -11,7 +11,8 @@
 //   * a warpgroup per row tile: each thread owns one row, so its maximum and sum need no
 //     exchange; it reads S, writes P = 2^(S - m) and, where the maximum has grown by more than
 //     2^8, rescales O.  Up to there a stale maximum is as good: O and the sum carry the same
-//     factor and P stays below 2^8.
+//     factor.  In fp16 P is 2^(S - m + 7), at most 2^15: slots down to 2^-32 of the largest are
+//     seen by the products, where at 2^-25 a long flat tail was lost that the sum counted.
 // What a row tile's warpgroup does for one slot tile (read S, maximum, exponentials, write P) takes
 // about as long as the tile's two products with their latencies, so the next scores have to run
 // under it: a score buffer is free again as soon as its rows are in registers, as P has columns of
@@ -96,6 +97,7 @@ struct ChunkCfg {
     // converting warps beside it, two passes of 32 scores at a time in short loops are faster, as the roles then
     // share the instruction cache: 512 tokens after 8000, dim 256, 8-bit 194 -> 168 us, fp16 140 -> 128
     static constexpr bool HOLD = !Q8 && D != 256;
+    static constexpr float P_SHIFT = C == CACHE_BF16 ? 0.0f : 7.0f;  // base-2 exponent that P has more
     // Every converting warpgroup has its own barriers for copied codes, one per area (raw_bar)
     static constexpr int NRAWBAR = NRAW * (NCONV > 1 ? NCONV : 1);
     static constexpr int NBAR = 2 * NS + 2 * NQ + 4 * NQ * SB + 1 + NRAW + NRAWBAR;
@@ -561,7 +563,7 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
                     // exponents x = S * sc - mz
                     const bool far = chunk_far(m, a.scale2);
                     const float sc = far ? a.scale_p2 : a.scale2;
-                    const float mz = m == -INFINITY ? 0.0f : m * sc;
+                    const float mz = m == -INFINITY ? -Cfg::P_SHIFT : far ? m * sc : m * sc - Cfg::P_SHIFT;
                     // ---- P: chunk c of 32 scores becomes columns (words of a row) 16 c .. 16 c + 15
                     const uint64_t sc2 = pack_f32x2(sc, sc), mz2 = pack_f32x2(-mz, -mz);
                     uint64_t sum[2] = {0ull, 0ull};
@@ -614,7 +616,9 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
                     if (lane == 0) a.desc[blockIdx.x] = JoinDesc{parts, k.t.first, k.h, k.t.row0, k.t.n * a.G, {}};
                 }
                 const float inv = l > 0.0f ? 1.0f / l : l;  // nothing visible: 0
-                const float ls = l > 0.0f ? (m == -INFINITY ? 0.0f : m) * a.scale2 + log2_approx(l) : l == 0.0f ? -INFINITY : l;
+                const float top = m == -INFINITY ? 0.0f : m * a.scale2;
+                const float ls = l > 0.0f ? top + (log2_approx(l) - (chunk_far(m, a.scale2) && m != -INFINITY ? 0.0f : Cfg::P_SHIFT))
+                                          : l == 0.0f ? -INFINITY : l;
                 float *part = a.part + (size_t)(2 * blockIdx.x + (blk0 == 0 ? 1 : 0)) * attn_part_floats(Cfg::ROWS, D);
                 if (rr < nrows) {
                     if (!whole)

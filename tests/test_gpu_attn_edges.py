@@ -128,6 +128,46 @@ def test_q_start_that_decreases_stays_inside_the_arrays(qg):
     assert qg.qg_device_error() == 0
 
 
+@pytest.mark.parametrize("kind", [F16, BF16, "q8"], ids=["f16", "bf16", "q8"])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("new", [1, 2, 40])
+@pytest.mark.parametrize("batch", [1, 152])
+def test_one_dominant_slot_over_a_long_tail(qg, kind, D, new, batch):
+    """The first slot 17.4 nats above 33000 others, each of which is 2^-25 of it and all together 1e-3: what the
+    sum counts, the products have to see.  One sequence is split over CTAs; 152 (the same one) are not."""
+    g = gen(D + new)
+    page, L = 64, 33001
+    q_start, lens, pages, n = tables([new], [L], page, 1, g)
+    k, v, kd, vd = make_cache(kind, n, 1, page, D, g)
+    dtype = F16 if kind == "q8" else kind
+    q = 0.01 * torch.randn((new, 4, D), generator=g, device="cuda")
+    q[..., 0] = 4
+    at = 17.4 * D ** 0.5 / 4
+    first = int(pages[0, 0])
+    k.copy_((k.float() * 0.05).round() if kind == "q8" else k * 0.05)
+    k[..., 0] = 0
+    k[first, 0, 0] = 0
+    k[first, 0, 0, 0] = 127 if kind == "q8" else at
+    if kind == "q8":
+        kd[first, 0, 0, 0] = at / 127
+    v.abs_()  # a tail of one sign
+    q = q.to(dtype)
+    starts = torch.arange(batch + 1, dtype=torch.int32, device="cuda") * new
+    lse = torch.empty((batch * new, 4), device="cuda")
+    out = qg.qg_attn_paged(q.repeat(batch, 1, 1), k, v, starts, lens.repeat(batch), pages.repeat(batch, 1), kd=kd, vd=vd,
+                           out_dtype=torch.float32, lse=lse, max_new=new)
+    o, want_lse, A, B = attention(q, k, v, kd, vd, [new], [L], pages, D ** -0.5, 0)
+    chunk = new * 4 > 16
+    # P in two addends in the row kernel; in the chunk kernel's fp16 each slot is held to 2^-32 of the largest at worst
+    bound = attention_bound(o, A, B, dtype, torch.float32, kind == "q8", exact_p=not chunk)
+    if chunk:
+        bound = bound + L * 2.0 ** -32 * 5
+    for i in range(batch):
+        within(out[i * new:(i + 1) * new], o, bound, "out")
+    tol = (2.0 ** -18 + (2.0 ** -11 if kind == "q8" and chunk else 0)) * B + 2.0 ** -18 + 2.0 ** -22 * want_lse.abs()
+    assert ((lse.double().view(batch, new, 4) - want_lse).abs() <= tol).all()
+
+
 @pytest.mark.parametrize("kind,spread,scale", [(F16, 60.0, 8.0), (F16, 2000.0, 1.0), (F16, 2000.0, -3.0), (BF16, 1e3, 0.7), (BF16, 1e6, 1.0), (BF16, 3e3, 77.0)])
 @pytest.mark.parametrize("D", [64, 128, 256])
 def test_scores_of_millions_and_more(qg, kind, spread, scale, D):
