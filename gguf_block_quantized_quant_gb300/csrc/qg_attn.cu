@@ -28,8 +28,11 @@ namespace qg {
 // accumulator to operand layout by a transposing move within the warp.
 //
 // Bound by the read of the cache; the products take a small part of that time, which is why the
-// probabilities can go in as two addends (hi + lo): the value sums then keep fp32 accuracy
-// instead of the 11 (8) bits of one fp16 (bf16) factor.
+// probabilities can go in as two addends (hi + lo): over a 16-bit cache the value sums are then those of
+// factors of 22 (16) bits instead of the 11 (8) of one fp16 (bf16) factor.  8-bit keys are whole numbers in the
+// products, their steps applied to the sums of 32 in fp32; 8-bit values go in as step * code rounded once
+// to fp16 (relative 2^-12 on average, 2^-11 at most), as their step, one per 32 columns of a slot, has no place
+// in a factor that all columns share.
 //
 // 64 ragged sequences of 300 to 16000 slots, 32/8 heads of 128, bf16: 157 us, 0.92 of the measured copy
 // bandwidth.  8-bit caches are bound by the issue of the conversion to fp16 pairs instead: 48

@@ -203,3 +203,20 @@ def lead(q, k, kv, new, pages, scale, least):
         out[at:at + n] = (top[..., 0] - top[..., 1]).transpose(0, 1) > least[at:at + n]
         at += n
     return out
+
+
+@pytest.mark.parametrize("kind", [F16, BF16, "q8"], ids=["f16", "bf16", "q8"])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("H,Hk,new", [(8, 2, [1] * 5), (12, 1, [1] * 5), (4, 2, [4, 7, 5, 8, 6]), (5, 1, [3, 1, 2, 3, 3])])
+def test_fp32_out_of_few_rows(qg, kind, D, H, Hk, new):
+    """Up to 16 rows: probabilities in two addends, 8-bit keys exact; of the roundings to 16 bits only that of
+    an 8-bit value is left."""
+    g = gen(D + H)
+    kv = [7, 100, 999, 2500, 40]
+    q_start, lens, pages, n = tables(new, kv, 48, 1, g)
+    k, v, kd, vd = make_cache(kind, n, Hk, 48, D, g)
+    dtype = F16 if kind == "q8" else kind
+    q = (2 * torch.randn((sum(new), H, D), generator=g, device="cuda")).to(dtype)
+    out = qg.qg_attn_paged(q, k, v, q_start, lens, pages, kd=kd, vd=vd, out_dtype=torch.float32, max_new=max(new))
+    o, _, A, B = attention(q, k, v, kd, vd, new, kv, pages, D ** -0.5, 0)
+    within(out, o, attention_bound(o, A, B, dtype, torch.float32, kind == "q8", exact_p=True), "out")
