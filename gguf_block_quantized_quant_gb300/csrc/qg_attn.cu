@@ -643,7 +643,8 @@ __global__ void __launch_bounds__(DecCfg<C, D, NR>::NW * 32, 1)
         if (lane == 0) mbar_drain(bars + 8 * s, (s < slot ? phase : phase ^ 1), DRAIN_NS);
 }
 
-// Merges the partial results of the items that range boundaries cut.  Block (x, y): the item that
+// Merges the partial results of the items that range boundaries cut, and clears the rows of tokens that belong to no
+// sequence (the last x: the last CTA leaves no item to others).  Block (x, y): the item that
 // CTA x described, its row y.  Partial i carries weight 2^(lse_i - max); the warps take every
 // JOIN_WARPS-th partial.
 constexpr int JOIN_WARPS = 8;
@@ -656,6 +657,10 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) attn_join_kernel(const AttnAr
     griddep_wait();
     griddep_launch_dependents();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, r = blockIdx.y;
+    if (blockIdx.x == gridDim.x - 1) {
+        clear_outside<T>(a, D);
+        return;
+    }
     const JoinDesc jd = a.desc[blockIdx.x];
     const int parts = jd.parts, rr = jd.row0 + r;
     if (parts == 0 || rr >= jd.nrows) return;
@@ -773,10 +778,9 @@ static int attn_rows_run(const AttnArgs &a, const qg_paged &c, int sms, cudaStre
     if (!allow_smem((const void *)kern, Cfg::BYTES)) return QG_ECUDA;
     const int ctas = std::min(sms, JOIN_MAX);
     if (!launch_programmatic(kern, dim3((unsigned)ctas), Cfg::NW * 32, Cfg::BYTES, s, a, km, vm)) return QG_ECUDA;
-    if (ctas == 1) return QG_OK;
     const int rows = (int)std::min<int64_t>(Cfg::ROWS, (int64_t)a.bt.tokens * a.G);
     auto join = attn_join_kernel<typename CacheT<C>::Q, D, NR>;
-    return launch_programmatic(join, dim3((unsigned)(ctas - 1), (unsigned)rows), JOIN_WARPS * 32, 0, s, a) ? QG_OK : QG_ECUDA;
+    return launch_programmatic(join, dim3((unsigned)ctas, (unsigned)rows), JOIN_WARPS * 32, 0, s, a) ? QG_OK : QG_ECUDA;
 }
 template <int C, int NR>
 static int attn_rows_dim(const AttnArgs &a, const qg_paged &c, int sms, cudaStream_t s) {

@@ -91,6 +91,22 @@ __device__ __forceinline__ uint32_t lds16(uint32_t a) {
     return v;
 }
 
+// Tokens before the first sequence's and after the last one's see nothing: zeros, and -inf as the logarithm.  The last
+// column of a join kernel's blocks writes them, so that the others' chain of loads is not longer for it (T: type
+// of the queries).
+template <class T>
+__device__ __forceinline__ void clear_outside(const AttnArgs &a, int D) {
+    const int lo = min(max(a.bt.q_start[0], 0), a.bt.tokens), hi = min(max(a.bt.q_start[a.bt.batch], 0), a.bt.tokens);
+    for (int64_t i = blockIdx.y; i < (int64_t)lo + a.bt.tokens - hi; i += gridDim.y) {
+        const int64_t row = (i < lo ? i : hi + i - lo) * a.Hq;
+        uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint8_t *>(a.out) + row * D * (a.out_f32 ? 4 : sizeof(T)));
+        const int chunks = a.Hq * (D / (a.out_f32 ? 4 : 8));
+        for (int x = threadIdx.x; x < chunks; x += blockDim.x) dst[x] = make_uint4(0, 0, 0, 0);
+        if (a.lse)
+            for (int x = threadIdx.x; x < a.Hq; x += blockDim.x) a.lse[row + x] = -INFINITY;
+    }
+}
+
 // 4-D tiled copy global -> shared: box at (element, slot, head, page); out-of-range pages give
 // zeros.  The element coordinate is always a multiple of 128 bytes (64 where rows are 64).
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map, int e, int slot, int head, int page,

@@ -1020,14 +1020,18 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
     }
 }
 
-// Merges the partial results of the items that range boundaries cut: as attn_join_kernel, block
-// (x, y) for the item that CTA x described, its y-th share.  Rows past the last hold nothing: theirs
+// Merges the partial results of the items that range boundaries cut and clears the rows of no sequence: as
+// attn_join_kernel, block (x, y) for the item that CTA x described, its y-th share.  Rows past the last hold nothing: theirs
 // are read but not written.
 template <class T, int D>
 __global__ void __launch_bounds__(256) attn_chunk_join_kernel(const AttnArgs a) {
     constexpr int ROWS = ChunkCfg<CACHE_F16, D>::ROWS;
     griddep_wait();
     griddep_launch_dependents();
+    if (blockIdx.x == gridDim.x - 1) {
+        clear_outside<T>(a, D);
+        return;
+    }
     const JoinDesc jd = a.desc[blockIdx.x];
     const int parts = jd.parts, lane = threadIdx.x & 31;
     if (parts == 0) return;
@@ -1105,9 +1109,8 @@ static int chunk_run(const AttnArgs &in, const qg_paged &c, int sms, cudaStream_
     }();
     if (!regs_ok || !allow_smem((const void *)kern, Cfg::BYTES)) return QG_ECUDA;
     if (!launch_programmatic(kern, dim3((unsigned)sms), Cfg::THREADS, Cfg::BYTES, s, a, plan, box, qsign, (int)qcopy, km, vm, qm)) return QG_ECUDA;
-    if (sms == 1) return QG_OK;
     auto join = attn_chunk_join_kernel<T, D>;
-    return launch_programmatic(join, dim3((unsigned)(sms - 1), 16), 256, 0, s, a) ? QG_OK : QG_ECUDA;
+    return launch_programmatic(join, dim3((unsigned)sms, 16), 256, 0, s, a) ? QG_OK : QG_ECUDA;
 }
 
 template <int C>

@@ -265,7 +265,8 @@ int qg_norm_residual(const void *y, int y_type, int64_t ldy, const void *res, in
  * Sequence b has the new tokens q_start[b] .. q_start[b+1] - 1 of the call, which are the
  * last of its kv_len[b] slots; token i of n is at position kv_len[b] - n + i.  Its slot at
  * position p is slot p % page of page pages[b * table_stride + p / page].  A position below 0
- * (kv_len < n) marks padding: nothing is appended for it and its outputs are zero.  Lengths
+ * (kv_len < n) marks padding, as do tokens before q_start[0] and from q_start[batch] on (a call of fixed
+ * size that is not full): nothing is appended for them and their outputs are zero.  Lengths
  * are held inside the arrays (token rows to the call's tokens, kv_len to table_width pages and to
  * 2^31 - 256);
  * page ids outside 0 .. n_pages - 1 read as zeros and are not written. */

@@ -220,3 +220,28 @@ def test_fp32_out_of_few_rows(qg, kind, D, H, Hk, new):
     out = qg.qg_attn_paged(q, k, v, q_start, lens, pages, kd=kd, vd=vd, out_dtype=torch.float32, max_new=max(new))
     o, _, A, B = attention(q, k, v, kd, vd, new, kv, pages, D ** -0.5, 0)
     within(out, o, attention_bound(o, A, B, dtype, torch.float32, kind == "q8", exact_p=True), "out")
+
+
+@pytest.mark.parametrize("kind", [F16, BF16, "q8"], ids=["f16", "bf16", "q8"])
+@pytest.mark.parametrize("out_dtype", [None, torch.float32], ids=["same", "f32"])
+def test_tokens_of_no_sequence_come_out_as_zeros(qg, kind, out_dtype):
+    """Rows before the first sequence's and after the last one's, in calls of a fixed size."""
+    g = gen(5)
+    new, kv = [3, 0, 20], [50, 9, 333]
+    q_start, lens, pages, n = tables(new, kv, 16, 1, g)
+    k, v, kd, vd = make_cache(kind, n, 2, 16, 64, g)
+    for T, lead_in in ((23, 0), (24, 1), (400, 7), (23 + 600, 600)):
+        q = torch.randn((T, 6, 64), generator=g, device="cuda").to(F16 if kind == "q8" else kind)
+        for hint in (1, 20):
+            out = torch.full((T, 6, 64), 3.0, device="cuda").to(out_dtype or q.dtype)
+            lse = torch.zeros((T, 6), device="cuda")
+            qg.qg_attn_paged(q, k, v, q_start + lead_in, lens, pages, kd=kd, vd=vd, out=out, lse=lse, max_new=hint)
+            inside = slice(lead_in, lead_in + 23)
+            want_lse = torch.empty((23, 6), device="cuda")
+            want = qg.qg_attn_paged(q[inside], k, v, q_start, lens, pages, kd=kd, vd=vd, out_dtype=out_dtype, lse=want_lse, max_new=hint)
+            assert torch.equal(out[inside], want) and torch.equal(lse[inside], want_lse)
+            rest = torch.ones(T, dtype=torch.bool, device="cuda")
+            rest[inside] = False
+            assert (out[rest] == 0).all() and (lse[rest] == -float("inf")).all()
+    none = torch.zeros_like(q_start)  # no sequence has a token
+    assert (qg.qg_attn_paged(q, k, v, none, lens, pages, kd=kd, vd=vd, max_new=0) == 0).all()
