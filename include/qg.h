@@ -261,7 +261,8 @@ int qg_norm_residual(const void *y, int y_type, int64_t ldy, const void *res, in
  * aligned and have the same strides.  Types: QG_F16, QG_BF16, or QG_Q8_0: int8 codes with one
  * fp16 step per 32 elements, the value being step * code (the rule of the Q8_0 block, codes
  * and steps in pools of their own: kd, vd: n_pages pages step_stride elements apart, each
- * kv_heads x page x dim/32 contiguous).
+ * kv_heads x page x dim/32 contiguous).  The attention forms such values in fp16: those beyond
+ * 65504 (steps above 515.75 with codes to match) are out of its range, as they are of a QG_F16 cache's.
  * Sequence b has the new tokens q_start[b] .. q_start[b+1] - 1 of the call, which are the
  * last of its kv_len[b] slots; token i of n is at position kv_len[b] - n + i.  Its slot at
  * position p is slot p % page of page pages[b * table_stride + p / page].  A position below 0

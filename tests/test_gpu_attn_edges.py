@@ -245,3 +245,24 @@ def test_tokens_of_no_sequence_come_out_as_zeros(qg, kind, out_dtype):
             assert (out[rest] == 0).all() and (lse[rest] == -float("inf")).all()
     none = torch.zeros_like(q_start)  # no sequence has a token
     assert (qg.qg_attn_paged(q, k, v, none, lens, pages, kd=kd, vd=vd, max_new=0) == 0).all()
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("step", [515.5, 2.0 ** -14, 2.0 ** -24])
+def test_8bit_values_at_both_ends_of_their_range(qg, D, step):
+    """Codes of +-127 with the largest step whose values fp16 holds, and with the smallest steps there are."""
+    g = gen(D)
+    new, kv = [1, 2, 60], [100, 33, 400]
+    q_start, lens, pages, n = tables(new, kv, 16, 1, g)
+    k, v, kd, vd = make_cache("q8", n, 2, 16, D, g)
+    k[:, :, ::3] = 127
+    v[:, :, 1::3] = -127
+    kd.fill_(step)
+    vd.fill_(step)
+    q = torch.randn((63, 8, D), generator=g, device="cuda").half()
+    scale = 0.05 / (60 * step * D ** 0.5)
+    o, _, A, B = attention(q, k, v, kd, vd, new, kv, pages, scale, 0)
+    for hint in (1, 60):
+        out = qg.qg_attn_paged(q, k, v, q_start, lens, pages, kd=kd, vd=vd, scale=scale, out_dtype=torch.float32, max_new=hint)
+        # fp16 products below 2^-14 are rounded to multiples of 2^-24
+        within(out, o, attention_bound(o, A, B, F16, torch.float32, True) + 2.0 ** -25, "out")
