@@ -194,6 +194,13 @@ __device__ __forceinline__ int token_seq(const Batch &bt, int t, int lane) {
     return lo;
 }
 
+// The larger one; NaN where one is (fmaxf would drop it, and the cache would read finite).
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
 constexpr int ROPE_WARPS = 4;
 constexpr int ROPE_U = 2;  // heads whose loads are in flight together
 
@@ -303,9 +310,9 @@ __global__ void __launch_bounds__(ROPE_WARPS * 32, EPL == 8 ? 5 : 8) rope_append
                 // the Q8_0 rule: step = amax / 127 per 32 elements, codes by the unrounded step
                 float m = 0.0f;
 #pragma unroll
-                for (int i = 0; i < EPL; ++i) m = fmaxf(m, fabsf(x[u][i]));
+                for (int i = 0; i < EPL; ++i) m = max_nan(m, fabsf(x[u][i]));
 #pragma unroll
-                for (int o = 16 / EPL; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+                for (int o = 16 / EPL; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
                 const float d = __fdiv_rn(m, 127.0f), id = m > 0.0f ? __fdividef(127.0f, m) : 0.0f;
                 uint32_t c[(EPL + 3) / 4] = {};
 #pragma unroll
@@ -334,9 +341,9 @@ template <int LANES, int N>
 __device__ __forceinline__ void quant_q8(const float (&x)[N], uint32_t (&c)[N / 4], float &d) {
     float m = 0.0f;
 #pragma unroll
-    for (int i = 0; i < N; ++i) m = fmaxf(m, fabsf(x[i]));
+    for (int i = 0; i < N; ++i) m = max_nan(m, fabsf(x[i]));
 #pragma unroll
-    for (int o = LANES / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    for (int o = LANES / 2; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
     d = __fdiv_rn(m, 127.0f);
     const float id = m > 0.0f ? __fdividef(127.0f, m) : 0.0f;
 #pragma unroll

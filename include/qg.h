@@ -309,6 +309,7 @@ int qg_rope_turns(int rot, double base, int scaling, double factor, double origi
  *   output); every head aligned to dim/32 elements, at most 16 bytes (to 4 elements
  *   it takes the fast path).  turns: device, rot/2.
  *   q_out: tokens x q_heads x dim contiguous, QG_F16 (QG_BF16 beside a QG_BF16 cache).
+ *   A block of 32 with an infinity or a NaN becomes NaN in a QG_Q8_0 cache.
  *   tokens x (q_heads + 2 kv_heads) < 2^31. */
 int qg_rope_append(const void *q, int64_t ldq, int64_t hdq, const void *k, int64_t ldk, int64_t hdk, const void *v,
                    int64_t ldv, int64_t hdv, int in_type, int tokens, int q_heads, const uint64_t *turns, int rot, int pairs,

@@ -2,7 +2,7 @@
 import pytest
 import torch
 
-from layer_testlib import BF16, F16, F32
+from layer_testlib import BF16, F16, F32, gen, make_cache, tables, values
 from qg_testlib import qg_module
 from test_gpu_rope_norm import rope_check
 
@@ -32,3 +32,32 @@ def test_norm_of_as_many_rows_as_an_int_counts(qg, rows):
     assert x is None and torch.equal(r, -y)  # as values: 0 + -1 * 0 is +0
     del y, r
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("D,rot,pairs", [(64, 64, False), (128, 128, True), (256, 64, False), (128, 0, False), (64, 20, False), (128, 96, False), (256, 30, True)])
+def test_8bit_blocks_with_a_value_that_is_not_finite(qg, bad, D, rot, pairs):
+    """They read as NaN, as a block of 32 whose step is not finite; the others hold what they held."""
+    g = gen(D)
+    q_start, lens, pages, n = tables([3], [20], 16, 0, g)
+    x = torch.randn((3, 4, D), generator=g, device="cuda")
+    turns = qg.qg_rope_turns(rot)[0].cuda() if rot else None
+    reads = []
+    for poisoned in (False, True):
+        k, v, kd, vd = make_cache("q8", n, 1, 16, D, gen(1))
+        y = x.clone()
+        if poisoned:
+            y[1, 2, D - 3] = bad  # the key: its last block, and its partner's where that is rotated
+            y[2, 3, 5] = bad      # the value: its first block
+        qg.qg_rope_append(y[:, :2], y[:, 2:3], y[:, 3:], turns, k, v, q_start, lens, pages, kd=kd, vd=vd, pairs=pairs)
+        reads.append([(values(a, b)[pages[0, 1].long(), 0, 1:4]) for a, b in ((k, kd), (v, vd))])
+    (k0, v0), (k1, v1) = reads
+    hit = torch.zeros((3, D // 32), dtype=torch.bool, device="cuda")
+    hit[1, -1] = True
+    if rot == D:
+        hit[1, (D - 3 if pairs else D // 2 - 3) // 32] = True
+    hit = hit.repeat_interleave(32, -1)
+    assert torch.isnan(k1[hit]).all() and torch.equal(k1[~hit], k0[~hit])
+    hit = torch.zeros((3, D), dtype=torch.bool, device="cuda")
+    hit[2, :32] = True
+    assert torch.isnan(v1[hit]).all() and torch.equal(v1[~hit], v0[~hit])
