@@ -290,7 +290,8 @@ __global__ void __launch_bounds__(ROPE_WARPS * 32, EPL == 8 ? 5 : 8) rope_append
                     }
                 }
 #pragma unroll
-                for (int i = 0; i < EPL; ++i) x[u][i] = fmaf(p[i], sn[i], x[u][i] * cs[i]);
+                for (int i = 0; i < EPL; ++i)
+                    if (e0 + i < a.rot) x[u][i] = fmaf(p[i], sn[i], x[u][i] * cs[i]);
             }
             if (is_q) {
                 if (!valid) {

@@ -61,3 +61,18 @@ def test_8bit_blocks_with_a_value_that_is_not_finite(qg, bad, D, rot, pairs):
     hit = torch.zeros((3, D), dtype=torch.bool, device="cuda")
     hit[2, :32] = True
     assert torch.isnan(v1[hit]).all() and torch.equal(v1[~hit], v0[~hit])
+
+
+@pytest.mark.parametrize("kind", [F16, BF16], ids=["f16", "bf16"])
+@pytest.mark.parametrize("D,rot,pairs", [(64, 0, False), (64, 20, False), (128, 62, True), (128, 96, False), (128, 64, False), (256, 30, False)])
+def test_infinities_past_the_rotated_part_pass_through(qg, kind, D, rot, pairs):
+    g = gen(D)
+    q_start, lens, pages, n = tables([2], [9], 16, 0, g)
+    k, v, _, _ = make_cache(kind, n, 1, 16, D, g)
+    x = torch.randn((2, 4, D), generator=g, device="cuda")
+    x[..., D - 1], x[..., rot] = float("inf"), -float("inf")
+    turns = qg.qg_rope_turns(rot)[0].cuda() if rot else None
+    q = qg.qg_rope_append(x[:, :2], x[:, 2:3], x[:, 3:], turns, k, v, q_start, lens, pages, pairs=pairs)
+    key = k[pages[0, 0].long(), 0, 7:9]
+    assert torch.equal(q[..., rot:], x[:, :2, rot:].to(kind)) and torch.equal(key[:, rot:], x[:, 2, rot:].to(kind))
+    assert torch.isfinite(q[..., :rot]).all() and torch.isfinite(key[:, :rot]).all()
