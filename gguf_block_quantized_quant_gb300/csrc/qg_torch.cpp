@@ -128,8 +128,14 @@ Heads heads(const Tensor &t, const char *what) {
 qg_paged paged(const Tensor &k, const Tensor &v, const Tensor *kd, const Tensor *vd, const Tensor &q_start, const Tensor &kv_len,
                const Tensor &pages) {
     const int type = type_of(k.scalar_type());
+    // the stride of a dimension of one element says nothing
+    auto strides = [](const Tensor &a, const Tensor &b) {
+        for (int i = 0; i < 4; ++i)
+            if (a.size(i) > 1 && a.stride(i) != b.stride(i)) return false;
+        return true;
+    };
     need(k.dim() == 4 && (type == QG_F16 || type == QG_BF16 || type == QG_Q8_0) && v.scalar_type() == k.scalar_type() &&
-             v.sizes() == k.sizes() && v.strides() == k.strides() && k.is_cuda(),
+             v.sizes() == k.sizes() && strides(k, v) && k.is_cuda(),
          "cache pools are fp16, bf16 or int8 CUDA tensors (pages, kv_heads, page, dim) of one shape, type and layout");
     need(k.stride(3) == 1, "cache pools must be contiguous along the head dimension");
     const int64_t n = k.size(0), h = k.size(1), page = k.size(2), dim = k.size(3);
@@ -140,9 +146,9 @@ qg_paged paged(const Tensor &k, const Tensor &v, const Tensor *kd, const Tensor 
         const int64_t blocks = dim / 32;
         for (const Tensor *s : {kd, vd})
             need(s->dim() == 4 && s->size(0) == n && s->size(1) == h && s->size(2) == page && s->size(3) == blocks &&
-                     s->stride(3) == 1 && s->stride(2) == blocks && s->stride(1) == page * blocks && s->stride(0) == kd->stride(0),
+                     s->stride(3) == 1 && s->stride(2) == blocks && (h == 1 || s->stride(1) == page * blocks) && strides(*s, *kd),
                  "steps have shape (pages, kv_heads, page, dim / 32), contiguous within a page");
-        c.step_stride = kd->stride(0);
+        c.step_stride = n > 1 ? kd->stride(0) : h * page * blocks;
     }
     for (const Tensor *t : {&q_start, &kv_len, &pages})
         need(t->scalar_type() == ScalarType::Int, "q_start, kv_len and pages are int32 tensors");
@@ -154,7 +160,9 @@ qg_paged paged(const Tensor &k, const Tensor &v, const Tensor *kd, const Tensor 
     c.type = type;
     c.kv_heads = narrow(h), c.dim = narrow(dim), c.page = narrow(page), c.n_pages = narrow(n);
     c.batch = narrow(batch), c.table_width = narrow(pages.size(1));
-    c.page_stride = k.stride(0), c.head_stride = k.stride(1), c.slot_stride = k.stride(2);
+    c.slot_stride = k.stride(2);
+    c.head_stride = h > 1 ? k.stride(1) : page * c.slot_stride;
+    c.page_stride = n > 1 ? k.stride(0) : h * page * c.slot_stride;
     c.table_stride = batch > 1 ? pages.stride(0) : std::max(pages.size(1), pages.stride(0));
     c.k = k.data_ptr(), c.v = v.data_ptr();
     c.kd = type == QG_Q8_0 ? kd->data_ptr() : nullptr, c.vd = type == QG_Q8_0 ? vd->data_ptr() : nullptr;

@@ -266,3 +266,29 @@ def test_8bit_values_at_both_ends_of_their_range(qg, D, step):
         out = qg.qg_attn_paged(q, k, v, q_start, lens, pages, kd=kd, vd=vd, scale=scale, out_dtype=torch.float32, max_new=hint)
         # fp16 products below 2^-14 are rounded to multiples of 2^-24
         within(out, o, attention_bound(o, A, B, F16, torch.float32, True) + 2.0 ** -25, "out")
+
+
+@pytest.mark.parametrize("kind", [F16, "q8"], ids=["f16", "q8"])
+@pytest.mark.parametrize("pages,heads", [(6, 1), (1, 2), (1, 1)])
+def test_strides_of_dimensions_of_one_element_say_nothing(qg, kind, pages, heads):
+    """Pools and steps of one head or one page whose strides there are any."""
+    g = gen(8)
+    page, D = 32, 64
+    k, v, kd, vd = make_cache(kind, pages, heads, page, D, g)
+    table = torch.arange(pages, dtype=torch.int32, device="cuda")[None]
+    L = pages * page - 3
+    q_start, lens = torch.tensor([0, 2], dtype=torch.int32, device="cuda"), torch.tensor([L], dtype=torch.int32, device="cuda")
+    q = torch.randn((2, 4, D), generator=g, device="cuda").half()
+
+    def odd(t, other):
+        if t is None:
+            return None
+        s = list(t.stride())
+        for i in (0, 1):
+            if t.shape[i] == 1:
+                s[i] = other
+        return t.as_strided(t.shape, s)
+    for hint in (1, 60):
+        want = qg.qg_attn_paged(q, k, v, q_start, lens, table, kd=kd, vd=vd, max_new=hint)
+        got = qg.qg_attn_paged(q, odd(k, 1), odd(v, 3), q_start, lens, table, kd=odd(kd, 1), vd=odd(vd, 5), max_new=hint)
+        assert torch.equal(want, got)
