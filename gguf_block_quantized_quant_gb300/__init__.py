@@ -371,8 +371,9 @@ def qg_attn_paged(q, k, v, q_start, kv_len, pages, kd=None, vd=None, max_new: in
                   window: int = 0, out_dtype=None, out=None, lse=None, ws=None, stream=None):
     """Causal attention of new tokens q (tokens, heads, dim) over the paged pools k, v
     (pages, kv_heads, page, dim).  max_new: the longest chunk, where the caller knows it (it
-    only chooses the kernel); scale: default dim ** -0.5; out_dtype: q's type or fp32; lse:
-    optional fp32 (tokens, heads) output.  Returns out (tokens, heads, dim)."""
+    only chooses the kernel; by default tokens that divide evenly over the sequences count as chunks of
+    one length, else as one chunk among single tokens); scale: default dim ** -0.5; out_dtype:
+    q's type or fp32; lse: optional fp32 (tokens, heads) output.  Returns out (tokens, heads, dim)."""
     return _done((_module or _torch_module()).attn_paged(
         q, k, v, q_start, kv_len, pages, kd, vd, max_new, scale, window, out_dtype, out, lse, ws,
         None if stream is None else stream.cuda_stream), "qg_attn_paged")

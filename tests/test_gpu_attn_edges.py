@@ -292,3 +292,16 @@ def test_strides_of_dimensions_of_one_element_say_nothing(qg, kind, pages, heads
         want = qg.qg_attn_paged(q, k, v, q_start, lens, table, kd=kd, vd=vd, max_new=hint)
         got = qg.qg_attn_paged(q, odd(k, 1), odd(v, 3), q_start, lens, table, kd=odd(kd, 1), vd=odd(vd, 5), max_new=hint)
         assert torch.equal(want, got)
+
+
+@pytest.mark.parametrize("new,longest", [([1] * 6, 1), ([2] * 6, 2), ([1, 1, 1, 1, 1, 60], 60), ([1, 40, 1], 40), ([300], 300), ([1] * 63 + [130], 130)])
+def test_default_of_the_longest_chunk(qg, new, longest):
+    """Without max_new the kernel is the one that the longest chunk takes (the two round differently)."""
+    g = gen(9)
+    kv = [n + 500 + 37 * i for i, n in enumerate(new)]
+    q_start, lens, pages, n = tables(new, kv, 16, 1, g)
+    k, v, _, _ = make_cache(F16, n, 2, 16, 64, g)
+    q = torch.randn((sum(new), 8, 64), generator=g, device="cuda").half()
+    rows, chunk = (qg.qg_attn_paged(q, k, v, q_start, lens, pages, max_new=m, out_dtype=torch.float32) for m in (1, 300))
+    assert not torch.equal(rows, chunk)
+    assert torch.equal(qg.qg_attn_paged(q, k, v, q_start, lens, pages, out_dtype=torch.float32), rows if longest * 4 <= 16 else chunk)
