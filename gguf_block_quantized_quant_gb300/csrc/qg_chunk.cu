@@ -1081,6 +1081,26 @@ size_t attn_chunk_workspace(int D, int G, int tokens, int batch, int sms) {
 
 static int gcd(int a, int b) { return b ? gcd(b, a % b) : a; }
 
+// What the kernel needs of the current device, asked once for each; a failure is not remembered.
+template <int C, int D>
+static bool chunk_ready() {
+    using Cfg = ChunkCfg<C, D>;
+    static std::mutex mu;
+    static std::set<int> done;
+    const void *kern = (const void *)attn_chunk_kernel<C, D>;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return false;
+    std::lock_guard<std::mutex> lock(mu);
+    if (done.count(dev)) return true;
+    if (Cfg::WGS > 2) {  // the warpgroups trade registers out of exactly this allocation
+        cudaFuncAttributes fa;
+        if (cudaFuncGetAttributes(&fa, kern) != cudaSuccess || fa.numRegs != Cfg::LAUNCH_REGS) return false;
+    }
+    if (!allow_smem(kern, Cfg::BYTES)) return false;
+    done.insert(dev);
+    return true;
+}
+
 template <int C, int D>
 static int chunk_run(const AttnArgs &in, const qg_paged &c, int sms, cudaStream_t s) {
     using Cfg = ChunkCfg<C, D>;
@@ -1100,14 +1120,9 @@ static int chunk_run(const AttnArgs &in, const qg_paged &c, int sms, cudaStream_
     CUtensorMap qm{};
     if (qcopy && !attn_query_map(&qm, a, c.type == QG_BF16, D)) return QG_ECUDA;
     if (!attn_tensor_map(&km, c, c.k, box) || !attn_tensor_map(&vm, c, c.v, box)) return QG_ECUDA;
+    if (!chunk_ready<C, D>()) return QG_ECUDA;
     if (!launch_programmatic(attn_plan_kernel, dim3(1), PLAN_THREADS, 0, s, a, plan, Cfg::ROWS, Cfg::BN, (int)tiles, sms)) return QG_ECUDA;
     auto kern = attn_chunk_kernel<C, D>;
-    // the warpgroups trade registers out of exactly this allocation
-    static const bool regs_ok = [] {
-        cudaFuncAttributes fa;
-        return Cfg::WGS == 2 || (cudaFuncGetAttributes(&fa, (const void *)attn_chunk_kernel<C, D>) == cudaSuccess && fa.numRegs == Cfg::LAUNCH_REGS);
-    }();
-    if (!regs_ok || !allow_smem((const void *)kern, Cfg::BYTES)) return QG_ECUDA;
     if (!launch_programmatic(kern, dim3((unsigned)sms), Cfg::THREADS, Cfg::BYTES, s, a, plan, box, qsign, (int)qcopy, km, vm, qm)) return QG_ECUDA;
     auto join = attn_chunk_join_kernel<T, D>;
     return launch_programmatic(join, dim3((unsigned)sms, 16), 256, 0, s, a) ? QG_OK : QG_ECUDA;
