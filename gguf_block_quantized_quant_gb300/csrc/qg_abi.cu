@@ -212,7 +212,7 @@ __global__ void wait_expiry_kernel(unsigned long long limit_ns) {
 // The small kernels ask for the same L1 / shared-memory split as the engine (all shared),
 // so that an SM does not have to change its configuration between them and the engine and
 // they can run beside an engine CTA.  Set once per kernel and device.
-bool prefer_shared(const void *kern) {
+static bool prefer_shared(const void *kern) {
     static std::mutex mu;
     static std::set<std::pair<const void *, int>> done;
     int dev = 0;
@@ -249,23 +249,11 @@ int launch_splitk_reduce(const float *part, int KS, long MN, float *y, cudaStrea
     return cudaGetLastError() == cudaSuccess ? 0 : QG_ECUDA;
 }
 
-// Launch with programmatic stream serialization: the kernel may start while the previous
-// kernel in the stream is still running (it must griddep_wait() before touching its data).
+// A small kernel before (or between) the engine's: programmatic launch beside it.
 template <class... KArgs, class... Args>
-static int launch_pdl(void (*kern)(KArgs...), int grid, int block, cudaStream_t s, Args... args) {
+static int launch_pdl(void (*kern)(KArgs...), int grid, int block, cudaStream_t s, const Args &...args) {
     if (!prefer_shared((const void *)kern)) return QG_ECUDA;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)grid);
-    cfg.blockDim = dim3((unsigned)block);
-    cfg.dynamicSmemBytes = 0;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, kern, static_cast<KArgs>(args)...) != cudaSuccess) return QG_ECUDA;
-    return cudaGetLastError() == cudaSuccess ? 0 : QG_ECUDA;
+    return launch_programmatic(kern, dim3((unsigned)grid), block, 0, s, args...) ? QG_OK : QG_ECUDA;
 }
 
 int launch_prep_tiles(const float *x, const float *u, float *h_out, const int8_t *xq, const float *xd,

@@ -97,6 +97,7 @@ struct ChunkCfg {
     // converting warps beside it, two passes of 32 scores at a time in short loops are faster, as the roles then
     // share the instruction cache: 512 tokens after 8000, dim 256, 8-bit 194 -> 168 us, fp16 140 -> 128
     static constexpr bool HOLD = !Q8 && D != 256;
+    static_assert(!(HOLD && P_OVER), "scores in registers free their buffer at once");
     static constexpr float P_SHIFT = C == CACHE_BF16 ? 0.0f : 7.0f;  // base-2 exponent that P has more
     // Every converting warpgroup has its own barriers for copied codes, one per area (raw_bar)
     static constexpr int NRAWBAR = NRAW * (NCONV > 1 ? NCONV : 1);
@@ -514,10 +515,8 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
                         tmem_wait_ld(s[0]);
 #pragma unroll
                         for (int c = 1; c < BN / 32; ++c) tmem_loaded(s[c]);
-                        if (!Cfg::P_OVER) {
-                            tc_fence_before();
-                            mbar_arrive(s_empty(q));
-                        }
+                        tc_fence_before();
+                        mbar_arrive(s_empty(q));  // P has columns of its own here
 #pragma unroll
                         for (int c = 0; c < BN / 32; ++c) {
                             mask(s[c], 32 * c);

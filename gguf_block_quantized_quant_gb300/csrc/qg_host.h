@@ -10,8 +10,6 @@ namespace qg {
 int device_sms();
 // SM count for planning when no device is usable: 152 then (qg_abi.cu).
 int device_sms_planning();
-// Asks once per kernel and device for the all-shared L1 split of the streaming engine (qg_abi.cu).
-bool prefer_shared(const void *kern);
 
 // Asks once per kernel and device for `bytes` of dynamic shared memory (qg_attn.cu).
 bool allow_smem(const void *kern, uint32_t bytes);
