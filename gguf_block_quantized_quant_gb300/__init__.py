@@ -317,6 +317,11 @@ def _torch_module():
     global _module
     if _module is None:
         lib()
+        built_for = _build.module_is_for()
+        if built_for != _build._torch_id():
+            raise RuntimeError(f"the module of the decoder-layer calls ({_build.TORCH_MODULE}) is " +
+                               ("missing" if built_for is None else f"built for {built_for}, this is {_build._torch_id()}") +
+                               "; build it (python -c 'import __graft_entry__ as g; g.build()'). There is no CPU fallback.")
         loader = importlib.machinery.ExtensionFileLoader("qg_torch", _build.TORCH_MODULE)
         spec = importlib.util.spec_from_file_location("qg_torch", _build.TORCH_MODULE, loader=loader)
         _module = importlib.util.module_from_spec(spec)

@@ -4,7 +4,8 @@ The CUDA sources are compiled in parallel: the C-ABI and decoder-layer translati
 ``qg_fmt.cu`` once per block format (``-DQG_FMT=<GGUF type id>``).  The library links the
 shared CUDA runtime so that it shares the process's runtime state (current device,
 streams) with PyTorch.  ``qg_torch.so`` (g++, against the installed torch's headers) is the Python
-module that marshals torch tensors for the decoder-layer calls.
+module that marshals torch tensors for the decoder-layer calls.  The library does not depend on it:
+where it cannot be built, ``build()`` warns, and those calls say so when they are made.
 """
 from __future__ import annotations
 
@@ -13,7 +14,9 @@ import glob
 import os
 import shutil
 import subprocess
+import sys
 import sysconfig
+import warnings
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -22,6 +25,7 @@ INCLUDE = os.path.join(ROOT, "include")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT_DIR, "libqg.so")
 TORCH_MODULE = os.path.join(OUT_DIR, "qg_torch.so")
+TORCH_STAMP = TORCH_MODULE + ".for"  # the torch and the Python that the module was built for
 
 FORMATS = {"q4_0": 2, "q4_1": 3, "q5_0": 6, "q5_1": 7, "q8_0": 8, "q2_k": 10, "q3_k": 11, "q4_k": 12, "q5_k": 13,
            "q6_k": 14, "iq4_nl": 20, "iq4_xs": 23}
@@ -41,8 +45,12 @@ def _cuda_lib_dir() -> str:
 
 
 def _sources():
-    return sorted(glob.glob(os.path.join(CSRC, "*.cu")) + glob.glob(os.path.join(CSRC, "*.cpp")) + glob.glob(os.path.join(CSRC, "*.cuh")) +
+    return sorted(glob.glob(os.path.join(CSRC, "*.cu")) + glob.glob(os.path.join(CSRC, "*.cuh")) +
                   glob.glob(os.path.join(CSRC, "*.h")) + [os.path.join(INCLUDE, "qg.h"), __file__])
+
+
+def _torch_sources():
+    return [os.path.join(CSRC, "qg_torch.cpp"), os.path.join(INCLUDE, "qg.h"), __file__]
 
 
 def _flags(extra=()):
@@ -58,11 +66,29 @@ def _units():
     return units
 
 
+def _newer(out, sources) -> bool:
+    return os.path.exists(out) and all(os.path.getmtime(s) <= os.path.getmtime(out) for s in sources)
+
+
+def _torch_id() -> str:
+    import torch
+    return f"torch {torch.__version__}, {sys.implementation.cache_tag}"
+
+
+def module_is_for() -> str | None:
+    """The torch and Python that the module was built for (None: there is no module)."""
+    if not (os.path.exists(TORCH_MODULE) and os.path.exists(TORCH_STAMP)):
+        return None
+    with open(TORCH_STAMP) as f:
+        return f.read()
+
+
 def up_to_date() -> bool:
-    if not (os.path.exists(LIB) and os.path.exists(TORCH_MODULE)):
-        return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(TORCH_MODULE))
-    return all(os.path.getmtime(s) <= t for s in _sources())
+    return _newer(LIB, _sources()) and _module_up_to_date()
+
+
+def _module_up_to_date() -> bool:
+    return _newer(TORCH_MODULE, _torch_sources()) and module_is_for() == _torch_id()
 
 
 def _torch_commands(out):
@@ -80,48 +106,65 @@ def _torch_commands(out):
     return compile_cmd, link_cmd
 
 
-def build(force: bool = False, verbose: bool = False, jobs: int | None = None) -> str:
-    """Compile (if needed) and return the path of libqg.so."""
-    if not force and up_to_date():
-        return LIB
-    os.makedirs(OUT_DIR, exist_ok=True)
+def _run(cmd, what):
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{what} failed:\n{r.stderr[-6000:]}")
+    return r
+
+
+def _build_lib(verbose, jobs):
     nvcc = _nvcc()
 
     def compile_one(u):
         src, obj, extra = u
-        cmd = [nvcc, *_flags(extra), "-c", src, "-o", obj]
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError(f"nvcc failed for {os.path.basename(obj)}:\n{r.stderr[-6000:]}")
+        r = _run([nvcc, *_flags(extra), "-c", src, "-o", obj], f"nvcc for {os.path.basename(obj)}")
         if verbose and r.stderr.strip():
             print(r.stderr)
         return obj
 
-    def run(cmd, what):
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError(f"{what} failed:\n{r.stderr[-6000:]}")
-
     units = _units()
-    tmp_torch = TORCH_MODULE + f".tmp{os.getpid()}"
-    torch_compile, torch_link = _torch_commands(tmp_torch)
     workers = jobs or min(len(units), max(1, os.cpu_count() or 1))
     with cf.ThreadPoolExecutor(max_workers=workers) as ex:
-        module = ex.submit(run, torch_compile, "g++ for qg_torch.o")
         objs = list(ex.map(compile_one, units))
-        module.result()
     tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [nvcc, *ARCH, "-shared", "-cudart", "shared", "-o", tmp, *objs,
-           "-Xlinker", f"-rpath,{_cuda_lib_dir()}"]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link of libqg.so failed:\n{r.stderr[-6000:]}")
+    _run([nvcc, *ARCH, "-shared", "-cudart", "shared", "-o", tmp, *objs, "-Xlinker", f"-rpath,{_cuda_lib_dir()}"], "link of libqg.so")
     os.replace(tmp, LIB)
-    run(torch_link, "link of qg_torch.so")
-    os.replace(tmp_torch, TORCH_MODULE)
+
+
+def _build_module(compiled, link_cmd, tmp):
+    """Links the module once the library is there.  compiled: the future of its compilation."""
+    try:
+        compiled.result()
+        _run(link_cmd, "link of qg_torch.so")
+    except (RuntimeError, OSError) as e:
+        for stale in (TORCH_MODULE, TORCH_STAMP):
+            if os.path.exists(stale):
+                os.remove(stale)
+        warnings.warn(f"libqg.so is built, but not the module of the decoder-layer calls (qg_norm_residual, qg_rope_append, "
+                      f"qg_attn_paged) for this torch; those calls will raise.  {e}", stacklevel=3)
+        return
+    os.replace(tmp, TORCH_MODULE)
+    with open(TORCH_STAMP, "w") as f:
+        f.write(_torch_id())
+
+
+def build(force: bool = False, verbose: bool = False, jobs: int | None = None) -> str:
+    """Compile (if needed) and return the path of libqg.so."""
+    lib = force or not _newer(LIB, _sources())
+    module = force or not _module_up_to_date()
+    os.makedirs(OUT_DIR, exist_ok=True)
+    with cf.ThreadPoolExecutor(max_workers=1) as ex:
+        if module:
+            tmp = TORCH_MODULE + f".tmp{os.getpid()}"
+            compile_cmd, link_cmd = _torch_commands(tmp)
+            compiled = ex.submit(_run, compile_cmd, "g++ for qg_torch.o")
+        if lib:
+            _build_lib(verbose, jobs)
+        if module:
+            _build_module(compiled, link_cmd, tmp)
     return LIB
 
 
 if __name__ == "__main__":
-    import sys
     print(build(force="--force" in sys.argv, verbose="-v" in sys.argv))
