@@ -34,10 +34,11 @@ namespace qg {
 // to fp16 (relative 2^-12 on average, 2^-11 at most), as their step, one per 32 columns of a slot, has no place
 // in a factor that all columns share.
 //
-// 64 ragged sequences of 300 to 16000 slots, 32/8 heads of 128, bf16: 157 us, 0.92 of the measured copy
-// bandwidth.  8-bit caches are bound by the issue of the conversion to fp16 pairs instead: 48
-// sequences of 100 to 12000, 24/4 heads of 256, 59 us (0.61); one of 32000 19.5 us; one of 700 9.4
-// us, the latency of two launches and a chain of loads.
+// 64 ragged sequences of 300 to 16000 slots, 32/8 heads of 128, bf16: 156 us, 0.93 of the measured copy
+// bandwidth; 4 new tokens each in fp16 (16 rows) 231 us (0.82).  8-bit caches are bound by the latency of each
+// warp's chain from codes to fp16 pairs to products, with three or four warps a scheduler and half of the
+// issue slots in use: 48 sequences of 100 to 12000, 24/4 heads of 256, 60 us (0.59); one of 32000 19.7 us.
+// One of 700 9.3 us, as long in a graph: two launches that wait for each other and a chain of loads.
 constexpr int DEC_ROWS = 16;     // rows of a tile at most (NR = 2)
 constexpr int DEC_BLK = 16;      // slots per block: the least page size
 // An item costs its blocks and a fixed part more, in the same unit, for its queries, its last incomplete

@@ -9,7 +9,8 @@
 //     steps, which one or two more warpgroups turn into tiles of step * code in fp16;
 //   * MMA warp: scores S = Q K^T (128 x BN, fp32 in tensor memory), then O += P V;
 //   * a warpgroup per row tile: each thread owns one row, so its maximum and sum need no
-//     exchange; it reads S, writes P = 2^(S - m) and, where the maximum has grown by more than
+//     exchange (the running maximum and sum are those of Milakov and Gimelshein, Online normalizer
+//     calculation for softmax, 2018, here rescaled only now and then); it reads S, writes P = 2^(S - m) and, where the maximum has grown by more than
 //     2^8, rescales O.  Up to there a stale maximum is as good: O and the sum carry the same
 //     factor.  In fp16 P is 2^(S - m + 7), at most 2^15: slots down to 2^-32 of the largest are
 //     seen by the products, where at 2^-25 a long flat tail was lost that the sum counted.
@@ -22,7 +23,7 @@
 // half of P while the second is made.  Measured and dropped for dim 128 (4096 tokens after 28000,
 // 32/8 heads, bf16): P over its scores and a score buffer per row tile, so that a tile's scores
 // wait for its last value product, 1.98 ms; P in shared memory, whose bandwidth then is the bound,
-// 1.83 ms; now 1.53 ms (1.32 PFLOP/s).  No product relies on the order of another that writes different columns:
+// 1.83 ms; now 1.52 ms (1.33 PFLOP/s).  No product relies on the order of another that writes different columns:
 // each waits for the barrier of what it overwrites, and each row tile's products are issued by a
 // warp of their own.
 // P is rounded to the value's 16-bit type, the operand type of the product: one rounding of
@@ -35,7 +36,9 @@
 // 32 scores, one place for all copies, one for each product).  512 tokens after 8000, 24/4 heads of 256,
 // 8-bit: 194 us with the roles unrolled, 146 now (0.71 PFLOP/s); there the conversion and the chain scores ->
 // softmax -> values of the single row tile take about equally long, and neither hides the other
-// entirely.  With two row tiles and 16-bit caches the tensor cores are the bound for long chunks, the
+// entirely.  512 after 8000 of 32/8 heads, 8-bit: 77 us at dim 64, 128 at 128, where one converting warpgroup
+// feeds two row tiles and the softmax reads its scores twice (16-bit: 55 and 71; 131 at dim 256 against
+// 179).  With two row tiles and 16-bit caches the tensor cores are the bound for long chunks, the
 // exponentials (16 a clock and SM) at dim 64.
 //
 // Work is counted in slot tiles over all items (row tile, cache head).  Where dealing whole items out,

@@ -16,8 +16,9 @@ namespace qg {
 // Everything is fp32 between the loads and the one rounding of each output; x is formed from
 // the unrounded r.  Bound by memory: each input is read once and each output written once,
 // the row staying in registers between the two reductions.  4096 rows of 5120 (fp32 with gate
-// and residual, bf16 out): 60 us, 0.93 of the measured copy bandwidth; one row: 5 us, the launch and
-// two reductions.
+// and residual, bf16 out): 59.4 us, 0.94 of the measured copy bandwidth; one row: 5 us a call, 3.0 in a
+// graph, the launch and two reductions.  Rows off the vector boundary take loads of one element: 4096 rows of
+// 5121, fp32, 145 us (0.34), against 50 for 5120.
 struct NormArgs {
     const void *y, *res, *gate;
     const float *w_post, *w_pre;
@@ -157,13 +158,15 @@ static int norm_x(const NormArgs &a, int x_type, bool vec, cudaStream_t s) {
 // and used for all of them.  A lane holds both elements of its pairs, four pairs of one head, so
 // that rotating exchanges nothing between lanes and 32 / (D / 8) heads share an instruction
 // (rope_quads_kernel); 4096 tokens of 32 + 2 x 8 heads of 128, fp32 to an 8-bit cache: 30 us
-// (0.70 of the measured copy bandwidth; to fp16 26.6 us, 0.84), with 8 to 16 heads a warp 33, with
-// more warps resident and fewer registers 37.
+// (0.70 of the measured copy bandwidth; to fp16 26.3 us, 0.85), with 8 to 16 heads a warp 33, with
+// more warps resident and fewer registers 37.  To 8 bits each lane quantizes its elements in every grouping
+// (blocks in 4 lanes, two runs in 8) and keeps the one that holds, so that no lane branches.
 // Rotated parts that are no multiple of 8 elements (64 for the keys of an 8-bit cache in halves,
 // whose blocks of 32 must not straddle), and heads of 64 off a boundary of 4 elements, take
 // rope_append_kernel: D / 32 consecutive elements per
-// lane, partners from other lanes, 41 us for the same.  Bound by memory for many tokens; one
-// token is a launch and two loads deep.
+// lane, partners from other lanes; the same with 96 (100) elements rotated in halves 39 (45) us.  The first is
+// bound by memory for many tokens; one token is a launch and two loads deep (4.7 us a call, 3.1 in a
+// graph).
 struct RopeArgs {
     const void *q, *k, *v;
     int64_t ldq, hdq, ldk, hdk, ldv, hdv;  // elements between tokens, between heads

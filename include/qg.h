@@ -319,7 +319,9 @@ int qg_rope_append(const void *q, int64_t ldq, int64_t hdq, const void *k, int64
 /* Attention of the new tokens over the cache: for token t at position p and query head g,
  *   o = sum_j softmax_j(scale * q.k_j) v_j   over   max(0, p - window + 1) <= j <= p
  * (window 0: from 0), keys and values of cache head g / (q_heads / kv_heads).  Scores, the
- * running maximum and the sums are fp32.
+ * running maximum and the sums are fp32.  Slots that no row of the call sees may hold anything.  A value
+ * that is not finite in a slot that some rows of a sequence see may reach its other rows too: they share
+ * products, with a probability of 0 as the factor.
  *   q: q_type (QG_BF16 beside a QG_BF16 cache, else QG_F16); token t, head g at t * ldq + g * hdq.
  *   out: tokens x q_heads x dim contiguous, q_type or QG_F32.  lse: tokens x q_heads fp32
  *   natural logarithms of the sums (-inf where nothing is visible), or NULL.
