@@ -122,7 +122,7 @@ struct Heads {
 Heads heads(const Tensor &t, const char *what) {
     need(t.dim() == 3 && t.is_cuda() && t.stride(2) == 1, what);
     const int64_t d = t.size(2);
-    return {t.data_ptr(), t.size(0) > 1 ? t.stride(0) : std::max(d, t.stride(0)), t.size(1) > 1 ? t.stride(1) : d};
+    return {t.data_ptr(), t.size(0) > 1 ? t.stride(0) : d, t.size(1) > 1 ? t.stride(1) : d};  // a stride of one element says nothing
 }
 
 qg_paged paged(const Tensor &k, const Tensor &v, const Tensor *kd, const Tensor *vd, const Tensor &q_start, const Tensor &kv_len,

@@ -305,3 +305,20 @@ def test_default_of_the_longest_chunk(qg, new, longest):
     rows, chunk = (qg.qg_attn_paged(q, k, v, q_start, lens, pages, max_new=m, out_dtype=torch.float32) for m in (1, 300))
     assert not torch.equal(rows, chunk)
     assert torch.equal(qg.qg_attn_paged(q, k, v, q_start, lens, pages, out_dtype=torch.float32), rows if longest * 4 <= 16 else chunk)
+
+
+def test_one_token_of_rows_at_any_distance(qg):
+    """One row of a buffer whose rows are an odd number of elements apart."""
+    g = gen(10)
+    q_start, lens, pages, n = tables([1], [40], 16, 1, g)
+    k, v, _, _ = make_cache(F16, n, 2, 16, 64, g)
+    wide = torch.randn((3, 8 * 64 + 1), generator=g, device="cuda").half()
+    row = wide[:, :512].unflatten(1, (8, 64))[:1]
+    assert row.stride(0) == 513
+    for hint in (1, 60):
+        want = qg.qg_attn_paged(row[:, :4].contiguous(), k, v, q_start, lens, pages, max_new=hint)
+        assert torch.equal(qg.qg_attn_paged(row[:, :4], k, v, q_start, lens, pages, max_new=hint), want)
+    turns = qg.qg_rope_turns(64)[0].cuda()
+    parts = row[:, :4], row[:, 4:6], row[:, 6:]
+    want = qg.qg_rope_append(*(p.contiguous() for p in parts), turns, k, v, q_start, lens, pages)
+    assert torch.equal(qg.qg_rope_append(*parts, turns, k, v, q_start, lens, pages), want)
