@@ -215,15 +215,10 @@ __global__ void wait_expiry_kernel(unsigned long long limit_ns) {
 static bool prefer_shared(const void *kern) {
     static std::mutex mu;
     static std::set<std::pair<const void *, int>> done;
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return false;
-    std::lock_guard<std::mutex> lock(mu);
-    if (done.count({kern, dev})) return true;
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout,
-                             (int)cudaSharedmemCarveoutMaxShared) != cudaSuccess)
-        return false;
-    done.insert({kern, dev});
-    return true;
+    return once_per_device(done, mu, kern, [&] {
+        return cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                    (int)cudaSharedmemCarveoutMaxShared) == cudaSuccess;
+    });
 }
 
 int launch_quant_act(const float *x, int M, int K, long ldx, int8_t *xq, float *xd, int32_t *xs, cudaStream_t s) {

@@ -1083,24 +1083,20 @@ size_t attn_chunk_workspace(int D, int G, int tokens, int batch, int sms) {
 
 static int gcd(int a, int b) { return b ? gcd(b, a % b) : a; }
 
-// What the kernel needs of the current device, asked once for each; a failure is not remembered.
+// Whether the current device gives the kernel what it needs.
 template <int C, int D>
 static bool chunk_ready() {
     using Cfg = ChunkCfg<C, D>;
     static std::mutex mu;
-    static std::set<int> done;
+    static std::set<std::pair<const void *, int>> done;
     const void *kern = (const void *)attn_chunk_kernel<C, D>;
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return false;
-    std::lock_guard<std::mutex> lock(mu);
-    if (done.count(dev)) return true;
-    if (Cfg::WGS > 2) {  // the warpgroups trade registers out of exactly this allocation
-        cudaFuncAttributes fa;
-        if (cudaFuncGetAttributes(&fa, kern) != cudaSuccess || fa.numRegs != Cfg::LAUNCH_REGS) return false;
-    }
-    if (!allow_smem(kern, Cfg::BYTES)) return false;
-    done.insert(dev);
-    return true;
+    return once_per_device(done, mu, kern, [&] {
+        if (Cfg::WGS > 2) {  // the warpgroups trade registers out of exactly this allocation
+            cudaFuncAttributes fa;
+            if (cudaFuncGetAttributes(&fa, kern) != cudaSuccess || fa.numRegs != Cfg::LAUNCH_REGS) return false;
+        }
+        return allow_smem(kern, Cfg::BYTES);
+    });
 }
 
 template <int C, int D>

@@ -4,6 +4,10 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <mutex>
+#include <set>
+#include <utility>
+
 namespace qg {
 
 // SM count of the current device, or a negative status (qg_abi.cu).
@@ -13,6 +17,23 @@ int device_sms_planning();
 
 // Asks once per kernel and device for `bytes` of dynamic shared memory (qg_attn.cu).
 bool allow_smem(const void *kern, uint32_t bytes);
+
+// Runs ask(kern) once per kernel and device and says whether it held; a failure is not remembered.  Nothing is thrown: the
+// callers stand below C entry points.
+template <class Ask>
+bool once_per_device(std::set<std::pair<const void *, int>> &done, std::mutex &mu, const void *kern, Ask &&ask) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return false;
+    try {
+        const std::lock_guard<std::mutex> lock(mu);
+        if (done.count({kern, dev})) return true;
+        if (!ask()) return false;
+        done.insert({kern, dev});
+        return true;
+    } catch (...) {
+        return false;
+    }
+}
 
 inline bool host_aligned(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
 
