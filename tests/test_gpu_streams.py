@@ -75,3 +75,18 @@ def test_projections_and_ffn(qg):
         crossed(qg, lambda s: [qg.qg_gemv_q(fmt, W, *q, N, stream=s)], [max(1, qg.qg_workspace_size(qg.QG_OP_GEMV_Q, fmt, M, N, K)), M * N * 4])
     x = torch.randn((100, K), generator=t, device="cuda")
     crossed(qg, lambda s: [qg.qg_prefill_gemm(fmt, W, x, N, stream=s)], [qg.qg_workspace_size(qg.QG_OP_PREFILL, fmt, 100, N, K), 100 * N * 4])
+
+
+def test_the_default_stream_given_from_another(qg):
+    """The default stream's handle is 0; it is a stream like any other."""
+    y, w = torch.randn((64, 2048), generator=gen(4), device="cuda"), torch.ones(2048, device="cuda")
+    want = qg.qg_norm_residual(y, y, w)
+    q = qg.qg_quantize_act(y)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)
+        got = qg.qg_norm_residual(y, y, w, stream=torch.cuda.default_stream())
+        again = qg.qg_quantize_act(y, stream=torch.cuda.default_stream())
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip((*got, *again), (*want, *q)))
