@@ -46,7 +46,8 @@ EXPORTS = ("qg_quantize_act", "qg_gemv", "qg_gemv_q", "qg_moe_ffn", "qg_ffn_subl
            "qg_moe_ws_layout", "qg_ffn_ws_layout", "qg_block_dots", "qg_device_error", "qg_strerror",
            "qg_version", "qg_gemv_static_ws", "qg_quantize_act_s16", "qg_moe_ffn_s16", "qg_moe_s16_ws_layout",
            "qg_prefill_gemm", "qg_dequant_f16", "qg_test_wait_expiry", "qg_norm_residual", "qg_rope_turns",
-           "qg_rope_append", "qg_attn_paged", "qg_attn_workspace_size")
+           "qg_rope_append", "qg_attn_paged", "qg_attn_workspace_size", "qg_rope_append_at", "qg_attn_shaped", "qg_attn_tree",
+           "qg_tree_masks", "qg_cache_keep", "qg_logits_adjust")
 QG_STATIC_WS_BYTES = 2097152  # include/qg.h
 
 
@@ -91,6 +92,12 @@ def lib() -> ctypes.CDLL:
         L.qg_rope_turns.argtypes = [I] + [ctypes.c_double, I] + [ctypes.c_double] * 4 + [P, ctypes.POINTER(F)]
         L.qg_rope_append.argtypes = [P, Q, Q, P, Q, Q, P, Q, Q, I, I, I, P, I, I, F, P, P, F, P, ctypes.c_char_p, P]
         L.qg_attn_paged.argtypes = [P, Q, Q, I, I, I, I, F, I, P, I, P, ctypes.c_char_p, P, S, P]
+        L.qg_rope_append_at.argtypes = [P, Q, Q, P, Q, Q, P, Q, Q, I, I, I, P, I, I, F, P, P, F, P, P, ctypes.c_char_p, P]
+        L.qg_attn_shaped.argtypes = [P, Q, Q, I, I, I, I, F, I, F, P, P, P, P, I, P, ctypes.c_char_p, P, S, P]
+        L.qg_attn_tree.argtypes = [P, Q, Q, I, I, I, I, F, I, F, P, P, I, P, P, I, P, ctypes.c_char_p, P, S, P]
+        L.qg_tree_masks.argtypes = [P, P, P, I, I, P, I, P, P]
+        L.qg_cache_keep.argtypes = [P, Q, P, I, I, Q, Q, P, ctypes.c_char_p, P]
+        L.qg_logits_adjust.argtypes = [P, I, Q, P, I, Q, I, I, ctypes.c_char_p, P]
         L.qg_attn_workspace_size.argtypes = [I, I, I, I, I]
         L.qg_attn_workspace_size.restype = S
         L.qg_device_error.argtypes = [ctypes.POINTER(ctypes.c_uint)]
@@ -358,14 +365,15 @@ def qg_rope_turns(rot: int, base: float = 10000.0, scaling: int = ROPE_PLAIN, fa
 
 
 def qg_rope_append(q, nk, nv, turns, k, v, q_start, kv_len, pages, kd=None, vd=None, pairs: bool = False, amp: float = 1.0,
-                   wq=None, wk=None, eps: float = 1e-6, q_dtype=None, q_out=None, stream=None):
+                   wq=None, wk=None, eps: float = 1e-6, q_dtype=None, q_out=None, stream=None, positions=None):
     """Rotates the new tokens' q (tokens, heads, dim) and nk (tokens, kv_heads, dim) by their
     positions and appends nk and nv to the pools k, v (pages, kv_heads, page, dim); the steps of
-    an int8 cache go to kd, vd.  turns: int64 CUDA tensor of rot / 2.  Returns the rotated q,
+    an int8 cache go to kd, vd.  turns: int64 CUDA tensor of rot / 2.  positions: int32 (tokens,), the
+    rotary positions where they are not the slots (drafts of a tree).  Returns the rotated q,
     fp16 (bf16 beside a bf16 cache; q_dtype, if given, has to be that)."""
     return _done((_module or _torch_module()).rope_append(
         q, nk, nv, turns, k, v, q_start, kv_len, pages, kd, vd, pairs, amp, wq, wk, eps, q_dtype, q_out,
-        None if stream is None else stream.cuda_stream), "qg_rope_append")
+        None if stream is None else stream.cuda_stream, positions), "qg_rope_append")
 
 
 def qg_attn_workspace_size(dim: int, q_heads: int, kv_heads: int, tokens: int, batch: int) -> int:
@@ -382,6 +390,63 @@ def qg_attn_paged(q, k, v, q_start, kv_len, pages, kd=None, vd=None, max_new: in
     return _done((_module or _torch_module()).attn_paged(
         q, k, v, q_start, kv_len, pages, kd, vd, max_new, scale, window, out_dtype, out, lse, ws,
         None if stream is None else stream.cuda_stream), "qg_attn_paged")
+
+
+def qg_attn_shaped(q, k, v, q_start, kv_len, pages, kd=None, vd=None, cap: float = 0.0, slopes=None, prefix=None, first=None,
+                   max_new: int | None = None, scale: float | None = None, window: int = 0, out_dtype=None, out=None, lse=None, ws=None,
+                   stream=None):
+    """qg_attn_paged with other scores and masks: scores capped at +-cap by cap * tanh(z / cap) (0: not),
+    less slopes[head] * distance (fp32 (heads,)); the first prefix[b] slots (int32 (batch,)) seen by every
+    token of sequence b, and no token seeing slots before its first[t] (int32 (tokens,)), the start of
+    its document.  Returns out (tokens, heads, dim)."""
+    return _done((_module or _torch_module()).attn_shaped(
+        q, k, v, q_start, kv_len, pages, kd, vd, max_new, scale, window, out_dtype, out, lse, ws,
+        None if stream is None else stream.cuda_stream, cap, slopes, prefix, first), "qg_attn_shaped")
+
+
+def qg_attn_tree(q, k, v, q_start, kv_len, pages, tree, positions=None, kd=None, vd=None, cap: float = 0.0, slopes=None,
+                 max_new: int | None = None, scale: float | None = None, window: int = 0, out_dtype=None, out=None, lse=None, ws=None,
+                 stream=None):
+    """Attention of trees of drafted tokens, which are the new tokens of their sequences: each sees the
+    slots before the drafts and the drafts whose bits are set in its row of tree (int32 (tokens, words),
+    bit i % 32 of word i // 32 for draft i of its sequence).  positions: int32 (tokens,), where they
+    are not the slots (for window and slopes).  qg_tree_masks makes both.  Others as qg_attn_shaped."""
+    return _done((_module or _torch_module()).attn_tree(
+        q, k, v, q_start, kv_len, pages, kd, vd, max_new, scale, window, out_dtype, out, lse, ws,
+        None if stream is None else stream.cuda_stream, tree, positions, cap, slopes), "qg_attn_tree")
+
+
+def qg_tree_masks(parents, q_start, kv_len, words: int, tree=None, positions=None, stream=None):
+    """(tree, positions) of drafted trees from parents (int32 (tokens,): the index among its sequence's
+    drafts of the one that a draft follows, -1 for a root).  words: 32-bit words of a mask, for up to
+    32 * words drafts of a sequence."""
+    return _done((_module or _torch_module()).tree_masks(
+        parents, q_start, kv_len, words, tree, positions, None if stream is None else stream.cuda_stream), "qg_tree_masks")
+
+
+def qg_cache_keep(k, v, q_start, kv_len, pages, keep, keep_len, kd=None, vd=None, kv_out=None, stream=None):
+    """Keeps the drafts keep[b, :keep_len[b]] (int32, rising indices among the sequence's drafts) of every
+    sequence: their keys and values move together behind the slots before the drafts.  Pools may have a
+    dimension of layers in front.  Returns the new lengths (kv_out, which may be kv_len itself)."""
+    return _done((_module or _torch_module()).cache_keep(
+        k, v, q_start, kv_len, pages, keep, keep_len, kd, vd, kv_out, None if stream is None else stream.cuda_stream), "qg_cache_keep")
+
+
+def qg_logits_adjust(logits, out=None, out_dtype=None, seq=None, history=None, history_len=None, prompt_len=None, repetition=None,
+                     frequency=None, presence=None, bias_start=None, bias_ids=None, bias=None, allow=None, drafts=None, tree=None,
+                     q_start=None, stream=None):
+    """Logits (rows, ids) with biases, penalties for ids said before and a grammar mask, before sampling.
+
+    seq: int32 (rows,), the sequence of each row (default: row i is sequence i).  history: int32
+    (sequences, longest), what each has said, history_len ids, the first prompt_len of them its prompt.
+    repetition, frequency, presence: fp32 (sequences,).  bias_start (int32, sequences + 1) delimits each
+    sequence's part of bias_ids and bias (of several entries for one id the last counts).  allow: int32
+    (rows, words), bit v % 32 of word v // 32 set where id v is allowed; others become -inf.  drafts,
+    tree, q_start: the row's own draft and those that it follows count as said (as in qg_attn_tree).
+    Returns out (default fp32); out may be logits itself."""
+    return _done((_module or _torch_module()).logits_adjust(
+        logits, out, out_dtype, seq, history, history_len, prompt_len, repetition, frequency, presence, bias_start, bias_ids, bias, allow,
+        drafts, tree, q_start, None if stream is None else stream.cuda_stream), "qg_logits_adjust")
 
 
 def qg_test_wait_expiry(limit_ns: int, stream=None):

@@ -1,7 +1,8 @@
 """Builds libqg.so in-tree with nvcc for sm_103a (GB300), and the torch marshalling module beside it.
 
-The CUDA sources are compiled in parallel: the C-ABI and decoder-layer translation units once, and
-``qg_fmt.cu`` once per block format (``-DQG_FMT=<GGUF type id>``).  The library links the
+The CUDA sources are compiled in parallel: the C-ABI and decoder-layer translation units once,
+``qg_fmt.cu`` once per block format (``-DQG_FMT=<GGUF type id>``) and the attention kernels once for each
+kind of scores and masks (``-DQG_MOD``).  The library links the
 shared CUDA runtime so that it shares the process's runtime state (current device,
 streams) with PyTorch.  ``qg_torch.so`` (g++, against the installed torch's headers) is the Python
 module that marshals torch tensors for the decoder-layer calls.  The library does not depend on it:
@@ -29,6 +30,8 @@ TORCH_STAMP = TORCH_MODULE + ".for"  # the torch and the Python that the module 
 
 FORMATS = {"q4_0": 2, "q4_1": 3, "q5_0": 6, "q5_1": 7, "q8_0": 8, "q2_k": 10, "q3_k": 11, "q4_k": 12, "q5_k": 13,
            "q6_k": 14, "iq4_nl": 20, "iq4_xs": 23}
+# the attention kernels and what they are compiled for (MOD_PLAIN, MOD_SHAPED, MOD_CAPPED of csrc/qg_attn.cuh)
+ATTENTION = {"qg_rows": (1, 0), "qg_chunk": (2, 1, 0)}
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -59,7 +62,9 @@ def _flags(extra=()):
 
 
 def _units():
-    units = [(os.path.join(CSRC, f"{u}.cu"), os.path.join(OUT_DIR, f"{u}.o"), []) for u in ("qg_chunk", "qg_attn", "qg_layer", "qg_abi")]
+    units = [(os.path.join(CSRC, f"{u}.cu"), os.path.join(OUT_DIR, f"{u}_{mod}.o"), [f"-DQG_MOD={mod}"])
+             for u, mods in ATTENTION.items() for mod in mods]
+    units += [(os.path.join(CSRC, f"{u}.cu"), os.path.join(OUT_DIR, f"{u}.o"), []) for u in ("qg_attn", "qg_layer", "qg_draft", "qg_abi")]
     for name, fid in FORMATS.items():
         units.append((os.path.join(CSRC, "qg_fmt.cu"), os.path.join(OUT_DIR, f"qg_fmt_{name}.o"),
                       [f"-DQG_FMT={fid}"]))
@@ -142,7 +147,7 @@ def _build_module(compiled, link_cmd, tmp):
             if os.path.exists(stale):
                 os.remove(stale)
         warnings.warn(f"libqg.so is built, but not the module of the decoder-layer calls (qg_norm_residual, qg_rope_append, "
-                      f"qg_attn_paged) for this torch; those calls will raise.  {e}", stacklevel=3)
+                      f"qg_attn_paged and those beside them) for this torch; those calls will raise.  {e}", stacklevel=3)
         return
     os.replace(tmp, TORCH_MODULE)
     with open(TORCH_STAMP, "w") as f:

@@ -19,6 +19,21 @@ struct JoinDesc {
     int pad[3];
 };
 
+// What the kernels are compiled for (QG_MOD): causal or windowed attention; the same with other masks and a bias
+// that falls with the distance; and that with capped scores too.
+enum { MOD_PLAIN, MOD_SHAPED, MOD_CAPPED };
+
+// What changes scores and masks (null: nothing), as the kernels read it.
+struct Shape {
+    float cap_in, cap_out;     // score = cap_out * tanh(cap_in * S), in powers of two (cap_out 0: not capped)
+    const float *slopes;       // Hq
+    const int32_t *prefix;     // batch: the first slots, which every token of the sequence sees
+    const int32_t *first;      // tokens: no slot before it is seen
+    const uint32_t *tree;      // tokens x words: bit j: the sequence's new token j is seen
+    int words;
+    const int32_t *positions;  // tokens, beside a tree: positions where they are not the slots
+};
+
 struct AttnArgs {
     Batch bt;
     const void *q;
@@ -34,11 +49,63 @@ struct AttnArgs {
     int64_t step_stride;
     float *part;       // partial results (attn_part_floats each)
     JoinDesc *desc;    // one per CTA
+    Shape sh;
 };
 
 // First slot that a row at position pos sees (window 0: all).  No difference that could pass 32 bits: a window
 // of 2^31 - 1 over a sequence that begins with padding (pos < 0) is a call like any other.
 __device__ __forceinline__ int seen_from(int pos, int window) { return window && pos >= window ? pos - window + 1 : 0; }
+
+// The slots that new token i of sequence b sees: lo .. hi, and beside a tree those of its mask, which start at slot
+// `base` of the sequence.  A token that sees nothing has hi = -1 and lo = INT_MAX.
+struct Seen {
+    int hi, lo, pos;
+};
+__device__ __forceinline__ Seen seen_by(const AttnArgs &a, const Seq &s, int b, int i) {
+    const int slot = s.len - s.n + i, t = s.first + i;
+    Seen r{-1, 0x7fffffff, slot};
+    if (slot < 0) return r;  // padding
+    if (a.sh.tree) {
+        if (a.sh.positions) r.pos = a.sh.positions[t];
+        r.hi = s.len - s.n - 1;
+        r.lo = min(seen_from(r.pos, a.window), 0x7ffffffe);
+    } else {
+        r.hi = a.sh.prefix ? min(max(slot, a.sh.prefix[b] - 1), s.len - 1) : slot;
+        r.lo = seen_from(slot, a.window);
+        if (a.sh.first) r.lo = max(r.lo, a.sh.first[t]);
+        if (r.lo > r.hi) r.hi = -1, r.lo = 0x7fffffff;
+    }
+    return r;
+}
+// The first slot that the token needs, its own mask's included.
+__device__ __forceinline__ int needs_from(const AttnArgs &a, const Seq &s, const Seen &v) {
+    return a.sh.tree && v.lo != 0x7fffffff ? min(v.lo, max(s.len - s.n, 0)) : v.lo;
+}
+// The first slot that some token of the sequence needs.  A function of its own: it is asked for in many places.
+static __device__ __noinline__ int first_needed(const int32_t *first, const int32_t *positions, int window, int base, int n, int len) {
+    int low = len;
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) {
+        const int slot = base + i;  // below 0: padding
+        const int from = first ? max(first[i], seen_from(slot, window)) : min(seen_from(positions ? positions[i] : slot, window), max(base, 0));
+        if (slot >= 0 && (!first || from <= len - 1)) low = min(low, from);
+    }
+    return low;
+}
+// 32 bits of a row of a tree's mask from bit `at` on; the bits before 0 are set, those past the row are not.
+__device__ __forceinline__ uint32_t tree_bits(const uint32_t *row, int words, int at) {
+    const int w = at >> 5;
+    const uint32_t lo = w < 0 ? 0xffffffffu : w < words ? row[w] : 0u, hi = w + 1 < 0 ? 0xffffffffu : w + 1 < words ? row[w + 1] : 0u;
+    return __funnelshift_r(lo, hi, at & 31);
+}
+
+// tanh(x) for |x| <= TANH_NEAR: x times a polynomial in x^2 (our own fit to the least largest relative error: 7e-7 as
+// evaluated).  Beyond it 1 - 2 / (1 + e^2x), which loses small x in the 1.
+constexpr float TANH_NEAR = 0.75f;
+__device__ __forceinline__ float tanh_near(float x) {
+    const float u = x * x;
+    return x * fmaf(u, fmaf(u, fmaf(u, fmaf(u, 0x1.a7ad9ep-7f, -0x1.9a0facp-5f), 0x1.0f8b42p-3f), -0x1.554802p-2f), 0x1.ffffeep-1f);
+}
 
 // One partial result: rows x D fp32 (normalised), then rows base-2 logarithms of the sums.
 __host__ __device__ constexpr size_t attn_part_floats(int rows, int D) { return (size_t)rows * D + rows; }
@@ -59,6 +126,8 @@ struct Ranges {
         return n;
     }
 };
+
+constexpr int DEC_ROWS = 16;  // rows of a tile of the row kernel at most
 
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LN2 = 0.6931471805599453f;
@@ -134,9 +203,23 @@ __device__ __forceinline__ uint32_t codes_to_f16(uint32_t biased, uint32_t sel) 
     return *reinterpret_cast<const uint32_t *>(&r);
 }
 
-// The chunk kernel (qg_chunk.cu): many rows per sequence, and its workspace.
+__device__ __forceinline__ float tanh_any(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + exp2_approx(x * (2.0f * LOG2E))));
+    return fabsf(x) <= TANH_NEAR ? tanh_near(x) : fmaf(-2.0f, r, 1.0f);
+}
+
+// The kernels by what they are compiled for: rows (qg_rows.cu, PLAIN and SHAPED, which caps too): up to 8 nr rows of
+// heads per sequence and cache head at a time; chunk (qg_chunk.cu): many, and its workspace.  _take: reads and clears the
+// device error word.
+template <int MOD>
+int attn_rows(const AttnArgs &a, const qg_paged &c, int nr, int sms, cudaStream_t s);
+template <int MOD>
 int attn_chunk(const AttnArgs &a, const qg_paged &c, int sms, cudaStream_t s);
 size_t attn_chunk_workspace(int D, int G, int tokens, int batch, int sms);
+template <int MOD>
+int attn_rows_dev_err_take(unsigned int *err);
+template <int MOD>
 int attn_chunk_dev_err_take(unsigned int *err);
 
 }  // namespace qg

@@ -1,5 +1,6 @@
 // qg_chunk.cu -- attention of chunks of new tokens over a paged cache on the 5th-generation tensor
-// cores: the plan of the row tiles, the kernel, and the merge of items that were cut.
+// cores: the plan of the row tiles, the kernel, and the merge of items that were cut.  Compiled once
+// for each QG_MOD.
 //
 // Row r of a sequence is query head g = r % G of a cache head and new token r / G, so the G heads
 // that share a cache head share each slot's copy.  A CTA multiplies NQ tiles of 128 rows with tiles
@@ -55,6 +56,10 @@
 #include "qg_launch.h"
 #include "qg_tcgen05.cuh"
 #include "qg_umma.h"
+
+#ifndef QG_MOD
+#error "QG_MOD is MOD_PLAIN, MOD_SHAPED or MOD_CAPPED"
+#endif
 
 namespace qg {
 
@@ -123,7 +128,8 @@ struct ChunkCfg {
 // ----------------------------------------------------------------------------- plan
 struct ChunkTile {
     int b, row0, kb0, nt;     // sequence, first row, first slot tile, slot tiles (at least 1)
-    int first, n, len, pad;   // Seq of b
+    int first, n, len;        // Seq of b
+    int lo;                   // the first slot that some row sees (not of the plain kernels)
 };
 struct ChunkPlan {
     int64_t *total;    // tiles of all items
@@ -132,9 +138,8 @@ struct ChunkPlan {
     int64_t *prefix;   // tiles before each row tile (all cache heads)
     ChunkTile *tile;
 };
-// Row tiles of a call at most, and the bytes of its plan.
+// Row tiles of a call at most.
 static int64_t chunk_max_tiles(int rows, int G, int tokens, int batch) { return (int64_t)tokens * G / rows + batch; }
-static size_t chunk_plan_bytes(int64_t tiles) { return 16 + (size_t)tiles * (sizeof(int64_t) + sizeof(ChunkTile)) + 16; }
 static ChunkPlan chunk_plan_at(uint8_t *p, int64_t tiles) {
     ChunkPlan c;
     c.total = reinterpret_cast<int64_t *>(p);
@@ -162,10 +167,12 @@ __device__ __forceinline__ int deal(int k, int c, int ctas) { return k & 1 ? (k 
 // One block lists the row tiles of all sequences with their slot ranges.  It stands before the
 // attention kernel in time, so it is built for few steps: one warp places the sequences' first tiles,
 // then a thread makes a tile and one barrier a prefix of their costs.
+template <int MOD>
 __global__ void __launch_bounds__(PLAN_THREADS) attn_plan_kernel(const AttnArgs a, ChunkPlan p, int rows, int bn, int max_tiles, int ctas) {
     __shared__ int64_t part[2][PLAN_THREADS / 32];
     __shared__ int unit[PLAN_THREADS], sorted[PLAN_THREADS];
     __shared__ int off[PLAN_SEQS + 1];
+    __shared__ int2 range[MOD == MOD_PLAIN ? 1 : PLAN_THREADS];  // per tile of a round: first slot seen, end of those seen
     griddep_wait();
     griddep_launch_dependents();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -199,19 +206,45 @@ __global__ void __launch_bounds__(PLAN_THREADS) attn_plan_kernel(const AttnArgs 
             int64_t cost = 0;
             ChunkTile t{};
             const bool on = r < count;
-            if (on) {
-                int lo = 0, hi = nb;  // off[lo] <= r < off[hi]
+            auto sequence = [&](int x) {  // whose tile x is
+                int lo = 0, hi = nb;      // off[lo] <= x < off[hi]
                 while (hi - lo > 1) {
                     const int mid = (lo + hi) >> 1;
-                    if (off[mid] <= r) lo = mid; else hi = mid;
+                    if (off[mid] <= x) lo = mid; else hi = mid;
                 }
+                return lo;
+            };
+            if constexpr (MOD != MOD_PLAIN) {
+                // a warp takes a tile's tokens, so that their loads are few and side by side
+                if (r0) __syncthreads();
+                for (int x = r0 + warp; x < min(count, r0 + PLAN_THREADS); x += PLAN_THREADS / 32) {
+                    const int b = sequence(x), row0 = (x - off[b]) * rows;
+                    const Seq s = seq_of(a.bt, c0 + b);
+                    int from = s.len, end = 0;
+                    for (int i = row0 / a.G + lane; i <= (min(row0 + rows, s.n * a.G) - 1) / a.G; i += 32) {
+                        const Seen v = seen_by(a, s, c0 + b, i);
+                        from = min(from, needs_from(a, s, v));
+                        end = max(end, a.sh.tree ? s.len : v.hi + 1);
+                    }
+                    from = __reduce_min_sync(0xffffffffu, from);
+                    end = __reduce_max_sync(0xffffffffu, end);
+                    if (lane == 0) range[x - r0] = make_int2(from, end);
+                }
+                __syncthreads();
+            }
+            if (on) {
+                const int lo = sequence(r);
                 const Seq s = seq_of(a.bt, c0 + lo);
                 t.b = c0 + lo;
                 t.row0 = (r - off[lo]) * rows;
                 t.first = s.first, t.n = s.n, t.len = s.len;
                 const int tf = t.row0 / a.G, tl = (min(t.row0 + rows, s.n * a.G) - 1) / a.G;  // first, last token
-                const int from = seen_from(s.len - s.n + tf, a.window);
-                const int end = s.len - s.n + tl + 1;  // slots that the last row sees
+                int from = seen_from(s.len - s.n + tf, a.window);
+                int end = s.len - s.n + tl + 1;  // slots that the last row sees
+                if constexpr (MOD != MOD_PLAIN) {
+                    from = range[tid].x, end = range[tid].y;
+                    t.lo = from;
+                }
                 t.kb0 = from / bn;
                 t.nt = max(1, (end + bn - 1) / bn - t.kb0);
                 cost = (int64_t)(t.nt + CHUNK_OV) * a.Hk;
@@ -339,8 +372,16 @@ __device__ __forceinline__ int chunk_ctas(int64_t total, int max_ctas) {
 // are exact; the scores themselves are off by more than what that changes.
 __device__ __forceinline__ bool chunk_far(float m, float scale2) { return !(fabsf(m * scale2) < 4194304.0f); }
 
+// The position of slot `key`; one load at a time, as many registers are in use where it is called.
+__device__ __forceinline__ float slot_position(const AttnArgs &a, int first, int base, int n, int key) {
+    int p = key;
+    if (key >= base && key < base + n)
+        asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(p) : "l"(a.sh.positions + first + (key - base)));
+    return (float)p;
+}
+
 // ----------------------------------------------------------------------------- kernel
-template <int C, int D>
+template <int C, int D, int MOD>
 __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
     attn_chunk_kernel(const AttnArgs a, const ChunkPlan plan, int box_rows, uint32_t qsign, int qcopy, const __grid_constant__ CUtensorMap kmap,
                       const __grid_constant__ CUtensorMap vmap, const __grid_constant__ CUtensorMap qmap) {
@@ -482,9 +523,24 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
                 const int rr = row0 + r, pos0 = k.t.len - k.t.n;
                 int g;
                 const int pos = pos0 + fast_div(rr, a.G, mG, g);
-                const int hi = rr < nrows ? pos : -1, lo = seen_from(pos, a.window);
-                const int hi_min = pos0 + row0 / a.G;  // every row sees up to here, and from lo_max on
-                const int lo_max = seen_from(pos0 + (min(row0 + 128, nrows) - 1) / a.G, a.window);
+                int hi = rr < nrows ? pos : -1, lo = seen_from(pos, a.window);
+                int hi_min = pos0 + row0 / a.G;  // every row sees up to here, and from lo_max on
+                int lo_max = seen_from(pos0 + (min(row0 + 128, nrows) - 1) / a.G, a.window);
+                int row_pos = pos;  // the position that distances count from
+                const uint32_t *tree = nullptr;
+                float slope = 0.0f;
+                if constexpr (MOD != MOD_PLAIN) {
+                    const int i = min(pos, k.t.len - 1) - pos0;  // rows past the last are copies of it
+                    const Seen v = seen_by(a, Seq{k.t.first, k.t.n, k.t.len}, k.t.b, i);
+                    hi = v.hi, lo = v.lo, row_pos = v.pos;
+                    hi_min = __reduce_min_sync(0xffffffffu, hi);
+                    lo_max = __reduce_max_sync(0xffffffffu, lo);
+                    if (a.sh.tree && lo != 0x7fffffff) tree = a.sh.tree + (int64_t)(k.t.first + i) * a.sh.words;
+                    if (a.sh.slopes) slope = a.sh.slopes[k.h * a.G + g] * LOG2E;
+                }
+                // scores that are no multiple of S any more are formed at once, their factor is 1 then
+                const bool bent = MOD == MOD_CAPPED || (MOD == MOD_SHAPED && a.sh.slopes);
+                const float scale2 = bent ? 1.0f : a.scale2, scale_p2 = bent ? 1.0f : a.scale_p2;
                 float m = -INFINITY, l = 0.0f;
                 for (int j = blk0; j < end; ++j, ++done) {
                     const int buf = SB == 1 ? 0 : (int)(done & 1);
@@ -498,7 +554,12 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
                     auto mask = [&](uint32_t (&v)[32], int c0) {
                         if (edge) {
                             const int up = c_hi - c0, down = c_lo - c0;  // visible: down .. up
-                            const uint32_t see = (up < 0 ? 0u : 0xffffffffu >> (31 - min(up, 31))) & (down > 31 ? 0u : 0xffffffffu << max(down, 0));
+                            uint32_t see = (up < 0 ? 0u : 0xffffffffu >> (31 - min(up, 31))) & (down > 31 ? 0u : 0xffffffffu << max(down, 0));
+                            if constexpr (MOD != MOD_PLAIN) {
+                                const int room = k.t.len - key0 - c0, old = pos0 - key0 - c0;  // slots in use, those before the new tokens
+                                if (tree && old < 32)
+                                    see |= tree_bits(tree, a.sh.words, -old) & (old > 0 ? 0xffffffffu << old : 0xffffffffu) & (room <= 0 ? 0u : 0xffffffffu >> (32 - min(room, 32)));
+                            }
 #pragma unroll
                             for (int i = 0; i < 32; ++i)
                                 if (!(see >> i & 1u)) v[i] = 0xff800000u;  // -inf
@@ -511,6 +572,39 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
                             x[(i / 2) & 3] = fmaxf(fmaxf(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), x[(i / 2) & 3]);
                         return fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
                     };
+                    // scores as powers of two's exponents, from S (MOD_PLAIN: they are S * scale2)
+                    auto bend = [&](uint32_t (&v)[32], int c0) {
+                        if constexpr (MOD == MOD_CAPPED) {
+                            float far = 0.0f;
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * a.sh.cap_in);
+#pragma unroll
+                            for (int i = 0; i < 32; i += 2) far = fmaxf(fmaxf(fabsf(__uint_as_float(v[i])), fabsf(__uint_as_float(v[i + 1]))), far);
+                            if (__any_sync(0xffffffffu, far > TANH_NEAR)) {
+#pragma unroll
+                                for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(a.sh.cap_out * tanh_any(__uint_as_float(v[i])));
+                            } else {
+#pragma unroll
+                                for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(a.sh.cap_out * tanh_near(__uint_as_float(v[i])));
+                            }
+                        } else if (bent) {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * a.scale2);
+                        }
+                        if (MOD != MOD_PLAIN && a.sh.slopes) {
+                            const int key = key0 + c0;
+                            if (a.sh.positions && key + 32 > pos0) {  // new tokens are where the caller says
+                                const float d = (float)row_pos;
+#pragma unroll
+                                for (int i = 0; i < 32; ++i)
+                                    v[i] = __float_as_uint(fmaf(-slope, fabsf(d - slot_position(a, k.t.first, pos0, k.t.n, key + i)), __uint_as_float(v[i])));
+                            } else {
+                                const float d = (float)(row_pos - key);
+#pragma unroll
+                                for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(fmaf(-slope, fabsf(d - (float)i), __uint_as_float(v[i])));
+                            }
+                        }
+                    };
                     float mx = -INFINITY;
                     if constexpr (Cfg::HOLD) {
 #pragma unroll
@@ -522,17 +616,21 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
                         mbar_arrive(s_empty(q));  // P has columns of its own here
 #pragma unroll
                         for (int c = 0; c < BN / 32; ++c) {
+                            bend(s[c], 32 * c);
                             mask(s[c], 32 * c);
                             mx = fmaxf(mx, top(s[c]));
                         }
                     } else {
+                        const bool late = MOD == MOD_CAPPED && !a.sh.slopes;  // a cap alone keeps the order: bend the maximum
 #pragma unroll 1
                         for (int c = 0; c < BN / 32; ++c) {
                             tmem_ld32(scol + 32 * c, s[0]);
                             tmem_wait_ld(s[0]);
+                            if (!late) bend(s[0], 32 * c);
                             mask(s[0], 32 * c);
                             mx = fmaxf(mx, top(s[0]));
                         }
+                        if (late && mx != -INFINITY) mx = a.sh.cap_out * tanh_any(mx * a.sh.cap_in);
                     }
                     if (!Cfg::P_OVER && done > 0) {  // P's place is free again
                         mbar_wait(pv_done(q, 0), (done - 1) & 1);
@@ -542,9 +640,9 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
                     if (j == blk0) {
                         m = mx;
                     } else {
-                        const bool grown = (mx - m) * a.scale2 > 8.0f || (m == -INFINITY && mx > m);
+                        const bool grown = (mx - m) * scale2 > 8.0f || (m == -INFINITY && mx > m);
                         if (__any_sync(0xffffffffu, grown)) {
-                            const float mn = fmaxf(m, mx), f = mn > m ? exp2_approx((m - mn) * a.scale2) : 1.0f;
+                            const float mn = fmaxf(m, mx), f = mn > m ? exp2_approx((m - mn) * scale2) : 1.0f;
                             m = mn;
                             l *= f;
                             if (Cfg::P_OVER) {
@@ -563,8 +661,8 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
                         }
                     }
                     // exponents x = S * sc - mz
-                    const bool far = chunk_far(m, a.scale2);
-                    const float sc = far ? a.scale_p2 : a.scale2;
+                    const bool far = chunk_far(m, scale2);
+                    const float sc = far ? scale_p2 : scale2;
                     const float mz = m == -INFINITY ? -Cfg::P_SHIFT : far ? m * sc : m * sc - Cfg::P_SHIFT;
                     // ---- P: chunk c of 32 scores becomes columns (words of a row) 16 c .. 16 c + 15
                     const uint64_t sc2 = pack_f32x2(sc, sc), mz2 = pack_f32x2(-mz, -mz);
@@ -579,6 +677,7 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
                                 tc_fence_before();
                                 mbar_arrive(s_empty(q));
                             }
+                            bend(v, 32 * c);
                             mask(v, 32 * c);
                         }
                         uint32_t p[16];
@@ -618,8 +717,8 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
                     if (lane == 0) a.desc[blockIdx.x] = JoinDesc{parts, k.t.first, k.h, k.t.row0, k.t.n * a.G, {}};
                 }
                 const float inv = l > 0.0f ? 1.0f / l : l;  // nothing visible: 0
-                const float top = m == -INFINITY ? 0.0f : m * a.scale2;
-                const float ls = l > 0.0f ? top + (log2_approx(l) - (chunk_far(m, a.scale2) && m != -INFINITY ? 0.0f : Cfg::P_SHIFT))
+                const float top = m == -INFINITY ? 0.0f : m * scale2;
+                const float ls = l > 0.0f ? top + (log2_approx(l) - (chunk_far(m, scale2) && m != -INFINITY ? 0.0f : Cfg::P_SHIFT))
                                           : l == 0.0f ? -INFINITY : l;
                 float *part = a.part + (size_t)(2 * blockIdx.x + (blk0 == 0 ? 1 : 0)) * attn_part_floats(Cfg::ROWS, D);
                 if (rr < nrows) {
@@ -864,7 +963,7 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
                 int z0 = 0, z1 = VR;
                 if (val) {
                     const int key0 = (k.t.kb0 + tile) * BN + h * VR;
-                    const int seen_lo = seen_from(k.t.len - k.t.n + k.t.row0 / a.G, a.window);
+                    const int seen_lo = MOD == MOD_PLAIN ? seen_from(k.t.len - k.t.n + k.t.row0 / a.G, a.window) : k.t.lo;
                     z0 = min(VR, max(0, seen_lo - key0)), z1 = min(VR, max(0, k.t.len - key0));
                 }
                 const bool mend = z0 > 0 || z1 < VR;
@@ -971,7 +1070,7 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
             mbar_wait(raw_full(n % Cfg::NRAWBAR), (n / Cfg::NRAWBAR) & 1);
             // slots that no row sees may hold anything: they become zeros
             const int key0 = (k.t.kb0 + (VAL ? vt : kt)) * BN + (VAL ? h * VR : 0);
-            const int seen_lo = seen_from(k.t.len - k.t.n + k.t.row0 / a.G, a.window);
+            const int seen_lo = MOD == MOD_PLAIN ? seen_from(k.t.len - k.t.n + k.t.row0 / a.G, a.window) : k.t.lo;
             const int from = max(0, seen_lo - key0), to = k.t.len - key0;  // rows of slots
             if (n >= NS) mbar_wait(kv_empty(slot), (n / NS - 1) & 1);
             // a short loop: the roles run at once and share the instruction cache (512 tokens after 8000, dim 256:
@@ -1073,6 +1172,8 @@ __global__ void __launch_bounds__(256) attn_chunk_join_kernel(const AttnArgs a) 
 }
 
 // ----------------------------------------------------------------------------- host
+#if QG_MOD == 0  // MOD_PLAIN: once in the library
+static size_t chunk_plan_bytes(int64_t tiles) { return 16 + (size_t)tiles * (sizeof(int64_t) + sizeof(ChunkTile)) + 16; }
 static int chunk_rows(int D) { return D == 256 ? 128 : 256; }
 
 size_t attn_chunk_workspace(int D, int G, int tokens, int batch, int sms) {
@@ -1081,15 +1182,17 @@ size_t attn_chunk_workspace(int D, int G, int tokens, int batch, int sms) {
     return parts + chunk_plan_bytes(chunk_max_tiles(rows, G, tokens, batch));
 }
 
+#endif
+
 static int gcd(int a, int b) { return b ? gcd(b, a % b) : a; }
 
 // Whether the current device gives the kernel what it needs.
-template <int C, int D>
+template <int C, int D, int MOD>
 static bool chunk_ready() {
     using Cfg = ChunkCfg<C, D>;
     static std::mutex mu;
     static std::set<std::pair<const void *, int>> done;
-    const void *kern = (const void *)attn_chunk_kernel<C, D>;
+    const void *kern = (const void *)attn_chunk_kernel<C, D, MOD>;
     return once_per_device(done, mu, kern, [&] {
         if (Cfg::WGS > 2) {  // the warpgroups trade registers out of exactly this allocation
             cudaFuncAttributes fa;
@@ -1099,7 +1202,7 @@ static bool chunk_ready() {
     });
 }
 
-template <int C, int D>
+template <int C, int D, int MOD>
 static int chunk_run(const AttnArgs &in, const qg_paged &c, int sms, cudaStream_t s) {
     using Cfg = ChunkCfg<C, D>;
     using T = typename CacheT<C>::Q;
@@ -1111,6 +1214,7 @@ static int chunk_run(const AttnArgs &in, const qg_paged &c, int sms, cudaStream_
     // a scale of zero is a small one (masked scores stay -inf)
     const uint32_t qsign = a.scale2 < 0.0f ? 0x80008000u : 0u;
     a.scale2 = std::max(std::abs(a.scale2), 1e-30f);
+    a.sh.cap_in = std::abs(a.sh.cap_in);
     a.scale_p2 = std::exp2(std::floor(std::log2(a.scale2)));
     const int box = gcd(c.page, Cfg::VR);
     CUtensorMap km{}, vm{};
@@ -1118,29 +1222,35 @@ static int chunk_run(const AttnArgs &in, const qg_paged &c, int sms, cudaStream_
     CUtensorMap qm{};
     if (qcopy && !attn_query_map(&qm, a, c.type == QG_BF16, D)) return QG_ECUDA;
     if (!attn_tensor_map(&km, c, c.k, box) || !attn_tensor_map(&vm, c, c.v, box)) return QG_ECUDA;
-    if (!chunk_ready<C, D>()) return QG_ECUDA;
-    if (!launch_programmatic(attn_plan_kernel, dim3(1), PLAN_THREADS, 0, s, a, plan, Cfg::ROWS, Cfg::BN, (int)tiles, sms)) return QG_ECUDA;
-    auto kern = attn_chunk_kernel<C, D>;
+    if (!chunk_ready<C, D, MOD>()) return QG_ECUDA;
+    if (!launch_programmatic(attn_plan_kernel<MOD>, dim3(1), PLAN_THREADS, 0, s, a, plan, Cfg::ROWS, Cfg::BN, (int)tiles, sms)) return QG_ECUDA;
+    auto kern = attn_chunk_kernel<C, D, MOD>;
     if (!launch_programmatic(kern, dim3((unsigned)sms), Cfg::THREADS, Cfg::BYTES, s, a, plan, box, qsign, (int)qcopy, km, vm, qm)) return QG_ECUDA;
     auto join = attn_chunk_join_kernel<T, D>;
     return launch_programmatic(join, dim3((unsigned)sms, 16), 256, 0, s, a) ? QG_OK : QG_ECUDA;
 }
 
-template <int C>
+template <int C, int MOD>
 static int chunk_dim(const AttnArgs &a, const qg_paged &c, int sms, cudaStream_t s) {
-    return c.dim == 64 ? chunk_run<C, 64>(a, c, sms, s) : c.dim == 128 ? chunk_run<C, 128>(a, c, sms, s) : chunk_run<C, 256>(a, c, sms, s);
+    return c.dim == 64    ? chunk_run<C, 64, MOD>(a, c, sms, s)
+           : c.dim == 128 ? chunk_run<C, 128, MOD>(a, c, sms, s)
+                          : chunk_run<C, 256, MOD>(a, c, sms, s);
 }
+template <int MOD>
 int attn_chunk(const AttnArgs &a, const qg_paged &c, int sms, cudaStream_t s) {
-    return c.type == QG_F16    ? chunk_dim<CACHE_F16>(a, c, sms, s)
-           : c.type == QG_BF16 ? chunk_dim<CACHE_BF16>(a, c, sms, s)
-                               : chunk_dim<CACHE_Q8>(a, c, sms, s);
+    return c.type == QG_F16    ? chunk_dim<CACHE_F16, MOD>(a, c, sms, s)
+           : c.type == QG_BF16 ? chunk_dim<CACHE_BF16, MOD>(a, c, sms, s)
+                               : chunk_dim<CACHE_Q8, MOD>(a, c, sms, s);
 }
+template int attn_chunk<QG_MOD>(const AttnArgs &, const qg_paged &, int, cudaStream_t);
 
+template <int MOD>
 int attn_chunk_dev_err_take(unsigned int *err) {
     unsigned int zero = 0;
     if (cudaMemcpyFromSymbol(err, g_qg_dev_err, sizeof(*err)) != cudaSuccess) return QG_ECUDA;
     if (cudaMemcpyToSymbol(g_qg_dev_err, &zero, sizeof(zero)) != cudaSuccess) return QG_ECUDA;
     return QG_OK;
 }
+template int attn_chunk_dev_err_take<QG_MOD>(unsigned int *);
 
 }  // namespace qg

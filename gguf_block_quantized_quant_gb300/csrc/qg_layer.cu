@@ -178,6 +178,7 @@ struct RopeArgs {
     Batch bt;
     int Hq, Hk, rot, pairs;
     int hpw;  // heads per warp
+    const int32_t *positions;  // of the tokens, where they are not their slots
     bool runs4;  // every head of q, k and v starts on a boundary of 4 elements
     float amp, eps;
 };
@@ -229,6 +230,7 @@ __global__ void __launch_bounds__(ROPE_WARPS * 32, EPL == 8 ? 5 : 8) rope_append
         slot = pos % a.bt.page;
         if (page >= a.bt.n_pages) page = -1;
     }
+    const int turn = a.positions ? a.positions[t] : pos;
 
     const int e0 = lane * EPL, half = a.rot / 2;
     const bool near = !a.pairs && half % EPL == 0;  // a pair's two elements sit at one place of two lanes
@@ -240,7 +242,7 @@ __global__ void __launch_bounds__(ROPE_WARPS * 32, EPL == 8 ? 5 : 8) rope_append
         const int e = e0 + i;
         if (e < a.rot && h0 < a.Hq + a.Hk) {
             const int j = a.pairs ? e >> 1 : (e < half ? e : e - half);
-            const unsigned long long ph = (unsigned long long)(long long)pos * a.turns[j];
+            const unsigned long long ph = (unsigned long long)(long long)turn * a.turns[j];
             float s, c;
             sincospif((float)(int)(ph >> 32) * 0x1p-31f, &s, &c);
             cs[i] = c * a.amp;
@@ -383,6 +385,7 @@ __global__ void __launch_bounds__(ROPE_WARPS * 32) rope_quads_kernel(const RopeA
         slot = pos % a.bt.page;
         if (page >= a.bt.n_pages) page = -1;
     }
+    const int turn = a.positions ? a.positions[t] : pos;
 
     const int half = a.rot / 2;
     const bool turns = 8 * c < a.rot;                       // the lane's elements are pairs
@@ -392,7 +395,7 @@ __global__ void __launch_bounds__(ROPE_WARPS * 32) rope_quads_kernel(const RopeA
     if (turns && h0 < a.Hq + a.Hk) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const unsigned long long ph = (unsigned long long)(long long)pos * a.turns[4 * c + i];
+            const unsigned long long ph = (unsigned long long)(long long)turn * a.turns[4 * c + i];
             sincospif((float)(int)(ph >> 32) * 0x1p-31f, &sn[i], &cs[i]);
             cs[i] *= a.amp;
             sn[i] *= a.amp;
@@ -516,9 +519,6 @@ static int rope_cache(const RopeArgs &a, int type, int D, int64_t warps, cudaStr
                              : rope_dim<I, CACHE_Q8>(a, D, warps, s);
 }
 
-static bool float_type(int t) { return t == QG_F32 || t == QG_F16 || t == QG_BF16; }
-static int type_size(int t) { return t == QG_F32 ? 4 : 2; }
-
 }  // namespace qg
 
 using namespace qg;
@@ -588,6 +588,14 @@ int qg_rope_append(const void *q, int64_t ldq, int64_t hdq, const void *k, int64
                    int64_t ldv, int64_t hdv, int in_type, int tokens, int q_heads, const uint64_t *turns, int rot, int pairs,
                    float amp, const float *wq, const float *wk, float eps, void *q_out, const qg_paged *cache,
                    void *stream) {
+    return qg_rope_append_at(q, ldq, hdq, k, ldk, hdk, v, ldv, hdv, in_type, tokens, q_heads, turns, rot, pairs, amp, wq, wk, eps, nullptr,
+                             q_out, cache, stream);
+}
+
+int qg_rope_append_at(const void *q, int64_t ldq, int64_t hdq, const void *k, int64_t ldk, int64_t hdk, const void *v,
+                      int64_t ldv, int64_t hdv, int in_type, int tokens, int q_heads, const uint64_t *turns, int rot, int pairs,
+                      float amp, const float *wq, const float *wk, float eps, const int32_t *positions, void *q_out,
+                      const qg_paged *cache, void *stream) {
     if (!q || !k || !v || !q_out || !cache || !float_type(in_type) || tokens < 1 || q_heads < 1) return QG_EINVAL;
     if (const int rc = paged_check(*cache)) return rc;
     const int D = cache->dim, Hk = cache->kv_heads;
@@ -600,7 +608,9 @@ int qg_rope_append(const void *q, int64_t ldq, int64_t hdq, const void *k, int64
         if (!host_aligned(p, va)) return QG_EALIGN;
     for (const int64_t n : {ldq, hdq, ldk, hdk, ldv, hdv})
         if ((size_t)(n * es) % va) return QG_EALIGN;
-    if (!host_aligned(q_out, 16) || !host_aligned(turns, 8) || !host_aligned(wq, 4) || !host_aligned(wk, 4)) return QG_EALIGN;
+    if (!host_aligned(q_out, 16) || !host_aligned(turns, 8) || !host_aligned(wq, 4) || !host_aligned(wk, 4) ||
+        !host_aligned(positions, 4))
+        return QG_EALIGN;
     const int sms = device_sms();
     if (sms < 0) return sms;
     RopeArgs a{};
@@ -618,6 +628,7 @@ int qg_rope_append(const void *q, int64_t ldq, int64_t hdq, const void *k, int64
     for (const void *p : {q, k, v}) a.runs4 = a.runs4 && host_aligned(p, 4 * es);
     for (const int64_t n : {ldq, hdq, ldk, hdk, ldv, hdv}) a.runs4 = a.runs4 && n % 4 == 0;
     a.amp = amp, a.eps = eps;
+    a.positions = positions;
     // few tokens: a warp takes as many heads as it has room for in one step (latency); many: up to 24
     // share the sines, as long as the warps fill the machine
     const int heads = q_heads + 2 * Hk, step = 256 / D;

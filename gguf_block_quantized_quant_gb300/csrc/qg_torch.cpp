@@ -16,6 +16,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <stdexcept>
+#include <tuple>
 
 #include "../../include/qg.h"
 
@@ -114,6 +115,15 @@ void weight(const Tensor *w, int64_t n) {
          "norm weights are contiguous fp32 tensors of the width they scale");
 }
 
+// A contiguous int32 (fp32) tensor of n elements, or None.
+const Tensor *list(PyObject *o, ScalarType t, int64_t n, const char *what) {
+    const Tensor *x = maybe(o, what);
+    need(!x || (x->scalar_type() == t && x->numel() == n && x->is_contiguous()), what);
+    return x;
+}
+const Tensor *ints(PyObject *o, int64_t n, const char *what) { return list(o, ScalarType::Int, n, what); }
+const Tensor *floats(PyObject *o, int64_t n, const char *what) { return list(o, ScalarType::Float, n, what); }
+
 struct Heads {
     const void *p;
     int64_t ld, hd;
@@ -181,6 +191,13 @@ PyObject *guarded(Fn &&fn) {
     }
     return nullptr;
 }
+PyObject *pair(const Tensor &a, const Tensor &b) {  // an undefined one is None
+    PyObject *pa = THPVariable_Wrap(a), *pb = THPVariable_Wrap(b);
+    PyObject *out = PyTuple_Pack(2, pa, pb);
+    Py_XDECREF(pa);
+    Py_XDECREF(pb);
+    return out;
+}
 bool arguments(Py_ssize_t have, Py_ssize_t want) {
     if (have == want) return true;
     PyErr_Format(PyExc_TypeError, "expected %zd arguments, got %zd", want, have);
@@ -234,17 +251,13 @@ PyObject *norm_residual(PyObject *, PyObject *const *a, Py_ssize_t n) {
                                         (float)number(a[6]), ro->data_ptr(), ptr(xo), xo ? type_of(xo->scalar_type()) : QG_F32, narrow(M), narrow(H),
                                         call.stream());
         if (rc) return PyLong_FromLong(rc);
-        PyObject *pr = THPVariable_Wrap(*ro), *px = xo ? THPVariable_Wrap(*xo) : (Py_INCREF(Py_None), Py_None);
-        PyObject *out = PyTuple_Pack(2, pr, px);
-        Py_XDECREF(pr);
-        Py_XDECREF(px);
-        return out;
+        return pair(*ro, xo ? *xo : Tensor());
     });
 }
 
-// (q, nk, nv, turns, k, v, q_start, kv_len, pages, kd, vd, pairs, amp, wq, wk, eps, q_dtype, q_out, stream)
+// (q, nk, nv, turns, k, v, q_start, kv_len, pages, kd, vd, pairs, amp, wq, wk, eps, q_dtype, q_out, stream, positions)
 PyObject *rope_append(PyObject *, PyObject *const *a, Py_ssize_t n) {
-    if (!arguments(n, 19)) return nullptr;
+    if (!arguments(n, 20)) return nullptr;
     return guarded([&]() -> PyObject * {
         const Tensor &q = tensor(a[0], "q is a tensor"), &nk = tensor(a[1], "nk is a tensor"), &nv = tensor(a[2], "nv is a tensor");
         const Tensor *turns = maybe(a[3], "turns is a tensor or None");
@@ -264,7 +277,8 @@ PyObject *rope_append(PyObject *, PyObject *const *a, Py_ssize_t n) {
         need(!turns || (turns->scalar_type() == ScalarType::Long && turns->is_contiguous()), "turns is a contiguous int64 tensor");
         weight(wq, D);
         weight(wk, D);
-        for (const Tensor *t : {&nk, &nv, turns, &k, wq, wk, qo}) on(q.device(), t);
+        const Tensor *positions = ints(a[19], T, "positions is a contiguous int32 tensor, one per token, or None");
+        for (const Tensor *t : {&nk, &nv, turns, &k, wq, wk, qo, positions}) on(q.device(), t);
         const c10::cuda::CUDAGuard dev(q.device());
         const Call call(a[18], q.device());
         Tensor o;
@@ -274,10 +288,10 @@ PyObject *rope_append(PyObject *, PyObject *const *a, Py_ssize_t n) {
             o = call.output({T, H, D}, dt);
             qo = &o;
         }
-        const int rc = qg_rope_append(hq.p, hq.ld, hq.hd, hk.p, hk.ld, hk.hd, hv.p, hv.ld, hv.hd, type_of(q.scalar_type()), narrow(T), narrow(H),
-                                      ptr<const uint64_t>(turns), turns ? narrow(2 * turns->numel()) : 0, PyObject_IsTrue(a[11]),
-                                      (float)number(a[12]), ptr<const float>(wq), ptr<const float>(wk), (float)number(a[15]), qo->data_ptr(),
-                                      &c, call.stream());
+        const int rc = qg_rope_append_at(hq.p, hq.ld, hq.hd, hk.p, hk.ld, hk.hd, hv.p, hv.ld, hv.hd, type_of(q.scalar_type()), narrow(T), narrow(H),
+                                         ptr<const uint64_t>(turns), turns ? narrow(2 * turns->numel()) : 0, PyObject_IsTrue(a[11]),
+                                         (float)number(a[12]), ptr<const float>(wq), ptr<const float>(wk), (float)number(a[15]), ptr<const int32_t>(positions),
+                                         qo->data_ptr(), &c, call.stream());
         return rc ? PyLong_FromLong(rc) : THPVariable_Wrap(*qo);
     });
 }
@@ -293,9 +307,10 @@ int longest_guess(int64_t tokens, int64_t batch) {
     return narrow(tokens % batch == 0 ? tokens / batch : std::max(tokens - batch + 1, (tokens + batch - 1) / batch));
 }
 
-// (q, k, v, q_start, kv_len, pages, kd, vd, max_new, scale, window, out_dtype, out, lse, ws, stream)
-PyObject *attn_paged(PyObject *, PyObject *const *a, Py_ssize_t n) {
-    if (!arguments(n, 16)) return nullptr;
+// What the attention calls have in common: (q, k, v, q_start, kv_len, pages, kd, vd, max_new, scale, window, out_dtype, out, lse, ws,
+// stream).  more(device, tokens, heads, batch) checks a call's other tensors and returns its C call on the common arguments.
+template <class More>
+PyObject *attention(PyObject *const *a, More &&more) {
     return guarded([&]() -> PyObject * {
         const Tensor &q = tensor(a[0], "q is a tensor"), &k = tensor(a[1], "k is a tensor"), &v = tensor(a[2], "v is a tensor");
         const Tensor &q_start = tensor(a[3], "q_start is a tensor"), &kv_len = tensor(a[4], "kv_len is a tensor"), &pages = tensor(a[5], "pages is a tensor");
@@ -310,6 +325,7 @@ PyObject *attn_paged(PyObject *, PyObject *const *a, Py_ssize_t n) {
         for (const Tensor *t : {&k, out, lse, ws}) on(q.device(), t);
         need(!lse || (lse->dim() == 2 && lse->size(0) == T && lse->size(1) == H && lse->scalar_type() == ScalarType::Float && lse->is_contiguous()),
              "lse is a contiguous fp32 tensor (tokens, heads)");
+        const auto run = more(q.device(), T, H, c.batch);
         const c10::cuda::CUDAGuard dev(q.device());
         const Call call(a[15], q.device());
         Tensor o, w;
@@ -331,9 +347,193 @@ PyObject *attn_paged(PyObject *, PyObject *const *a, Py_ssize_t n) {
         }
         const int max_new = a[8] == Py_None ? longest_guess(T, c.batch) : integer(a[8]);
         const double scale = a[9] == Py_None ? 1.0 / std::sqrt((double)D) : number(a[9]);
-        const int rc = qg_attn_paged(hq.p, hq.ld, hq.hd, type_of(qt), narrow(T), narrow(H), max_new, (float)scale, integer(a[10]),
-                                     out->data_ptr(), type_of(out->scalar_type()), ptr<float>(lse), &c, ws->data_ptr(), nws,
+        const auto first = std::make_tuple(hq.p, hq.ld, hq.hd, type_of(qt), narrow(T), narrow(H), max_new, (float)scale, integer(a[10]));
+        const auto last = std::make_tuple(out->data_ptr(), type_of(out->scalar_type()), ptr<float>(lse), &c, ws->data_ptr(), nws, call.stream());
+        const int rc = run(first, last);
+        return rc ? PyLong_FromLong(rc) : THPVariable_Wrap(*out);
+    });
+}
+
+// As attention().
+PyObject *attn_paged(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    if (!arguments(n, 16)) return nullptr;
+    return attention(a, [](const at::Device &, int64_t, int64_t, int64_t) {
+        return [](const auto &first, const auto &last) { return std::apply(qg_attn_paged, std::tuple_cat(first, last)); };
+    });
+}
+
+// As attention(), then (cap, slopes, prefix, first)
+PyObject *attn_shaped(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    if (!arguments(n, 20)) return nullptr;
+    return attention(a, [&](const at::Device &d, int64_t T, int64_t H, int64_t batch) {
+        const Tensor *slopes = floats(a[17], H, "slopes is a contiguous fp32 tensor, one per head, or None");
+        const Tensor *prefix = ints(a[18], batch, "prefix is a contiguous int32 tensor, one per sequence, or None");
+        const Tensor *from = ints(a[19], T, "first is a contiguous int32 tensor, one per token, or None");
+        for (const Tensor *t : {slopes, prefix, from}) on(d, t);
+        const auto mine = std::make_tuple((float)number(a[16]), ptr<const float>(slopes), ptr<const int32_t>(prefix), ptr<const int32_t>(from));
+        return [mine](const auto &first, const auto &last) { return std::apply(qg_attn_shaped, std::tuple_cat(first, mine, last)); };
+    });
+}
+
+// Words of a row of a tree's masks.
+int tree_words(const Tensor &t, int64_t rows) {
+    need(t.dim() == 2 && t.scalar_type() == ScalarType::Int && t.size(0) == rows && t.size(1) > 0 && t.is_contiguous(),
+         "tree is a contiguous int32 tensor (tokens, words)");
+    return narrow(t.size(1));
+}
+
+// As attention(), then (tree, positions, cap, slopes)
+PyObject *attn_tree(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    if (!arguments(n, 20)) return nullptr;
+    return attention(a, [&](const at::Device &d, int64_t T, int64_t H, int64_t) {
+        const Tensor &tree = tensor(a[16], "tree is a tensor");
+        const int words = tree_words(tree, T);
+        const Tensor *positions = ints(a[17], T, "positions is a contiguous int32 tensor, one per token, or None");
+        const Tensor *slopes = floats(a[19], H, "slopes is a contiguous fp32 tensor, one per head, or None");
+        for (const Tensor *t : {&tree, positions, slopes}) on(d, t);
+        const auto mine = std::make_tuple((float)number(a[18]), ptr<const float>(slopes), static_cast<const uint32_t *>(tree.data_ptr()), words,
+                                          ptr<const int32_t>(positions));
+        return [mine](const auto &first, const auto &last) { return std::apply(qg_attn_tree, std::tuple_cat(first, mine, last)); };
+    });
+}
+
+// (parents, q_start, kv_len, words, tree, positions, stream)
+PyObject *tree_masks(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    if (!arguments(n, 7)) return nullptr;
+    return guarded([&]() -> PyObject * {
+        const Tensor &parents = tensor(a[0], "parents is a tensor"), &q_start = tensor(a[1], "q_start is a tensor"), &kv_len = tensor(a[2], "kv_len is a tensor");
+        const int64_t T = parents.numel(), batch = kv_len.numel();
+        const int words = integer(a[3]);
+        need(parents.is_cuda(), "parents is a CUDA tensor");
+        for (const Tensor *t : {&parents, &q_start, &kv_len})
+            need(t->scalar_type() == ScalarType::Int && t->is_contiguous(), "parents, q_start and kv_len are contiguous int32 tensors");
+        need(q_start.numel() == batch + 1, "q_start has batch + 1 entries");
+        need(words > 0, "words is at least 1");
+        const Tensor *tree = ints(a[4], T * words, "tree is a contiguous int32 tensor (tokens, words)");
+        const Tensor *positions = ints(a[5], T, "positions is a contiguous int32 tensor, one per token");
+        for (const Tensor *t : {&q_start, &kv_len, tree, positions}) on(parents.device(), t);
+        const c10::cuda::CUDAGuard dev(parents.device());
+        const Call call(a[6], parents.device());
+        Tensor m, p;
+        if (!tree) tree = &(m = call.output({T, words}, ScalarType::Int));
+        if (!positions) positions = &(p = call.output({T}, ScalarType::Int));
+        const int rc = qg_tree_masks(ptr<const int32_t>(&parents), ptr<const int32_t>(&q_start), ptr<const int32_t>(&kv_len), narrow(T), narrow(batch),
+                                     static_cast<uint32_t *>(tree->data_ptr()), words, ptr<int32_t>(positions), call.stream());
+        return rc ? PyLong_FromLong(rc) : pair(*tree, *positions);
+    });
+}
+
+// (k, v, q_start, kv_len, pages, keep, keep_len, kd, vd, kv_out, stream)
+PyObject *cache_keep(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    if (!arguments(n, 11)) return nullptr;
+    return guarded([&]() -> PyObject * {
+        const Tensor &k = tensor(a[0], "k is a tensor"), &v = tensor(a[1], "v is a tensor");
+        const Tensor &q_start = tensor(a[2], "q_start is a tensor"), &kv_len = tensor(a[3], "kv_len is a tensor"), &pages = tensor(a[4], "pages is a tensor");
+        const Tensor &keep = tensor(a[5], "keep is a tensor"), &keep_len = tensor(a[6], "keep_len is a tensor");
+        const Tensor *kd = maybe(a[7], "kd is a tensor or None"), *vd = maybe(a[8], "vd is a tensor or None");
+        const bool stacked = k.dim() == 5;  // (layers, pages, kv_heads, page, dim)
+        const int64_t layers = stacked ? k.size(0) : 1;
+        int64_t apart = 0, steps_apart = 0;
+        qg_paged c;
+        if (stacked) {
+            need(layers > 0 && v.dim() == 5 && v.size(0) == layers && (layers == 1 || v.stride(0) == k.stride(0)),
+                 "pools of several layers are (layers, pages, kv_heads, page, dim), keys and values of one layout");
+            Tensor d0, d1;
+            if (kd && vd) {
+                need(kd->dim() == 5 && vd->dim() == 5 && kd->size(0) == layers && vd->size(0) == layers && (layers == 1 || vd->stride(0) == kd->stride(0)),
+                     "steps of several layers are (layers, pages, kv_heads, page, dim / 32)");
+                d0 = kd->select(0, 0), d1 = vd->select(0, 0);
+                steps_apart = kd->stride(0);
+            }
+            apart = k.stride(0);
+            c = paged(k.select(0, 0), v.select(0, 0), kd ? &d0 : nullptr, vd ? &d1 : nullptr, q_start, kv_len, pages);
+        } else {
+            c = paged(k, v, kd, vd, q_start, kv_len, pages);
+        }
+        need(keep.dim() == 2 && keep.scalar_type() == ScalarType::Int && keep.size(0) == c.batch && (keep.stride(1) == 1 || keep.size(1) == 1),
+             "keep is an int32 tensor (batch, width), contiguous along the width");
+        need(keep_len.scalar_type() == ScalarType::Int && keep_len.numel() == c.batch && keep_len.is_contiguous(), "keep_len is a contiguous int32 tensor, one per sequence");
+        const Tensor *kv_out = ints(a[9], c.batch, "kv_out is a contiguous int32 tensor, one per sequence, or None");
+        for (const Tensor *t : {&keep, &keep_len, kv_out}) on(k.device(), t);
+        const c10::cuda::CUDAGuard dev(k.device());
+        const Call call(a[10], k.device());
+        Tensor o;
+        if (!kv_out) kv_out = &(o = call.output({c.batch}, ScalarType::Int));
+        const int rc = qg_cache_keep(ptr<const int32_t>(&keep), c.batch > 1 ? keep.stride(0) : std::max(keep.size(1), keep.stride(0)),
+                                     ptr<const int32_t>(&keep_len), narrow(keep.size(1)), narrow(layers), apart, steps_apart, ptr<int32_t>(kv_out), &c,
                                      call.stream());
+        return rc ? PyLong_FromLong(rc) : THPVariable_Wrap(*kv_out);
+    });
+}
+
+// (logits, out, out_dtype, seq, history, history_len, prompt_len, repetition, frequency, presence, bias_start, bias_ids, bias, allow,
+// drafts, tree, q_start, stream)
+PyObject *logits_adjust(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    if (!arguments(n, 18)) return nullptr;
+    return guarded([&]() -> PyObject * {
+        const Tensor &x = tensor(a[0], "logits is a tensor");
+        const int64_t ld = rows(x, "logits is a CUDA tensor (rows, ids), contiguous along the ids");
+        const int64_t R = x.size(0), V = x.size(1);
+        need(is_float(x.scalar_type()), "logits are fp32, fp16 or bf16");
+        qg_logits h{};
+        // the sequences: as many as there are histories, lengths, penalties or lists of biases; else as rows
+        int64_t batch = -1;
+        const Tensor *history = maybe(a[4], "history is a tensor or None");
+        if (history) {
+            need(history->dim() == 2 && history->scalar_type() == ScalarType::Int && (history->stride(1) == 1 || history->size(1) <= 1),
+                 "history is an int32 tensor (sequences, ids), contiguous along the ids");
+            batch = history->size(0);
+            h.history_stride = batch > 1 ? history->stride(0) : history->size(1);
+            h.history_width = narrow(history->size(1));
+        }
+        const Tensor *start = maybe(a[10], "bias_start is a tensor or None"), *q_start = maybe(a[16], "q_start is a tensor or None");
+        for (const auto &[t, more] : {std::make_pair(maybe(a[7], "repetition is a tensor or None"), 0), std::make_pair(maybe(a[8], "frequency is a tensor or None"), 0),
+                                      std::make_pair(maybe(a[9], "presence is a tensor or None"), 0), std::make_pair(start, 1), std::make_pair(q_start, 1)})
+            if (t && batch < 0) batch = t->numel() - more;
+        if (batch < 0) batch = R;
+        const Tensor *seq = ints(a[3], R, "seq is a contiguous int32 tensor, one per row, or None");
+        const char *lengths = "history_len and prompt_len are contiguous int32 tensors, one per sequence";
+        const Tensor *len = ints(a[5], batch, lengths), *prompt = ints(a[6], batch, lengths);
+        const char *penalties = "repetition, frequency and presence are contiguous fp32 tensors, one per sequence";
+        const Tensor *rep = floats(a[7], batch, penalties), *freq = floats(a[8], batch, penalties), *pres = floats(a[9], batch, penalties);
+        need(!history || len, "a history needs history_len");
+        ints(a[10], batch + 1, "bias_start is a contiguous int32 tensor of sequences + 1 entries");
+        const Tensor *ids = maybe(a[11], "bias_ids is a tensor or None");
+        need(!start || ids, "bias_start needs bias_ids and bias");
+        if (ids) ints(a[11], ids->numel(), "bias_ids is a contiguous int32 tensor");
+        const Tensor *bias = floats(a[12], ids ? ids->numel() : 0, "bias is a contiguous fp32 tensor, one per id of bias_ids");
+        need(!start || bias, "bias_start needs bias_ids and bias");
+        const Tensor *allow = maybe(a[13], "allow is a tensor or None");
+        need(!allow || (allow->dim() == 2 && allow->scalar_type() == ScalarType::Int && allow->size(0) == R && allow->size(1) >= (V + 31) / 32 &&
+                        (allow->stride(1) == 1 || allow->size(1) == 1)),
+             "allow is an int32 tensor (rows, words of 32 ids), contiguous along the words");
+        const Tensor *drafts = ints(a[14], R, "drafts is a contiguous int32 tensor, one per row, or None"), *tree = maybe(a[15], "tree is a tensor or None");
+        need(!drafts == !tree && (!drafts || q_start), "drafts, tree and q_start go together");
+        if (tree) h.words = tree_words(*tree, R);
+        ints(a[16], batch + 1, "q_start is a contiguous int32 tensor of sequences + 1 entries");
+        const Tensor *out = maybe(a[1], "out is a tensor or None");
+        for (const Tensor *t : {out, seq, history, len, prompt, rep, freq, pres, start, ids, bias, allow, drafts, tree, q_start}) on(x.device(), t);
+        const c10::cuda::CUDAGuard dev(x.device());
+        const Call call(a[17], x.device());
+        Tensor o;
+        int64_t ldo = V;
+        if (out) {
+            ldo = rows(*out, "out is a CUDA tensor (rows, ids), contiguous along the ids");
+            need(out->sizes() == x.sizes() && is_float(out->scalar_type()), "out has the shape of logits, in fp32, fp16 or bf16");
+        } else {
+            out = &(o = call.output({R, V}, dtype(a[2], ScalarType::Float)));
+            need(is_float(out->scalar_type()), "out is fp32, fp16 or bf16");
+        }
+        h.batch = narrow(batch);
+        auto ip = [](const Tensor *t) { return ptr<const int32_t>(t); };
+        auto fp = [](const Tensor *t) { return ptr<const float>(t); };
+        h.seq = ip(seq), h.history = ip(history), h.history_len = ip(len), h.prompt_len = ip(prompt);
+        h.repetition = fp(rep), h.frequency = fp(freq), h.presence = fp(pres);
+        if (ids && ids->numel() > 0) h.bias_start = ip(start), h.bias_ids = ip(ids), h.bias = fp(bias), h.bias_entries = narrow(ids->numel());
+        h.allow = ptr<const uint32_t>(allow), h.allow_stride = allow ? (R > 1 ? allow->stride(0) : allow->size(1)) : 0;
+        h.drafts = ip(drafts), h.tree = ptr<const uint32_t>(tree), h.q_start = ip(q_start);
+        const int rc = qg_logits_adjust(x.data_ptr(), type_of(x.scalar_type()), ld, out->data_ptr(), type_of(out->scalar_type()), ldo, narrow(R), narrow(V), &h,
+                                        call.stream());
         return rc ? PyLong_FromLong(rc) : THPVariable_Wrap(*out);
     });
 }
@@ -341,6 +541,11 @@ PyObject *attn_paged(PyObject *, PyObject *const *a, Py_ssize_t n) {
 PyMethodDef methods[] = {
     {"norm_residual", reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(norm_residual)), METH_FASTCALL, nullptr},
     {"rope_append", reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(rope_append)), METH_FASTCALL, nullptr},
+    {"attn_shaped", reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(attn_shaped)), METH_FASTCALL, nullptr},
+    {"attn_tree", reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(attn_tree)), METH_FASTCALL, nullptr},
+    {"tree_masks", reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(tree_masks)), METH_FASTCALL, nullptr},
+    {"cache_keep", reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(cache_keep)), METH_FASTCALL, nullptr},
+    {"logits_adjust", reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(logits_adjust)), METH_FASTCALL, nullptr},
     {"attn_paged", reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(attn_paged)), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };

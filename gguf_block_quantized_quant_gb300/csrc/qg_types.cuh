@@ -183,6 +183,10 @@ __device__ __forceinline__ Seq seq_of(const Batch &bt, int b) {
     return s;
 }
 
+// Element types of activations (host).
+inline bool float_type(int t) { return t == QG_F32 || t == QG_F16 || t == QG_BF16; }
+inline int type_size(int t) { return t == QG_F32 ? 4 : 2; }
+
 // Argument checks that every call with a cache makes (host).
 inline int paged_check(const qg_paged &c) {
     if (c.type != QG_F16 && c.type != QG_BF16 && c.type != QG_Q8_0) return QG_EINVAL;

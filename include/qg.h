@@ -332,6 +332,97 @@ int qg_attn_paged(const void *q, int64_t ldq, int64_t hdq, int q_type, int token
                   int window, void *out, int out_type, float *lse, const qg_paged *cache, void *ws, size_t ws_bytes,
                   void *stream);
 
+/* Attention of the new tokens over the cache as qg_attn_paged, with scores and masks of other kinds (0 or NULL: as there):
+ *   z = scale * q.k;   z = cap * tanh(z / cap)   (cap > 0);   z = z - slopes[g] * |p - j|   (query head g, slot j)
+ * over the slots   max(0, p - window + 1, first[t]) <= j <= max(p, prefix[b] - 1),   j < kv_len[b].
+ *   cap: finite, with finite scale / cap.   slopes: q_heads fp32.
+ *   prefix: batch; the first prefix[b] slots are seen by every token of the sequence, its earlier ones too, as far as they
+ *   are appended and window and first allow.   first: tokens; the first slot of the document that token t belongs to, in
+ *   slots of its sequence (tokens of a packed prompt; 0 where a token sees everything before it).  Values at or below 0 allow
+ *   all, and a token whose range is empty gives zeros and -inf.
+ * Slots before the first one that a row of the call sees may hold anything, as may those from kv_len on; those between have
+ * to be finite (a probability of 0 times infinity is not 0).  lse is over the z above.
+ * Other arguments, limits, errors and the workspace as qg_attn_paged. */
+int qg_attn_shaped(const void *q, int64_t ldq, int64_t hdq, int q_type, int tokens, int q_heads, int max_new, float scale, int window,
+                   float cap, const float *slopes, const int32_t *prefix, const int32_t *first, void *out, int out_type, float *lse,
+                   const qg_paged *cache, void *ws, size_t ws_bytes, void *stream);
+
+/* Attention of trees of drafted tokens: the n new tokens of a sequence are drafts that follow one another as a tree (or
+ * in any other order) and sit in its last n slots.  Token i of the sequence (row t of the call, slot kv_len - n + i) sees
+ *   every slot j < kv_len - n before the drafts, as far as j > p - window (window 0: all), p being its position, and
+ *   draft i' of its own sequence where bit i' % 32 of tree[t * words + i' / 32] is set (its own bit with them: nothing is added).
+ *   positions: tokens, or NULL where a token's position is its slot; p of the window and of the distance |p - p'|, in which
+ *   a draft's p' is its own position too.  Drafts from 32 * words on are seen by none.
+ *   cap, slopes: as qg_attn_shaped.  Values in the slots of all drafts have to be finite; a token that sees nothing gives zeros.
+ * Other arguments, limits, errors and the workspace as qg_attn_paged; qg_tree_masks makes tree and positions. */
+int qg_attn_tree(const void *q, int64_t ldq, int64_t hdq, int q_type, int tokens, int q_heads, int max_new, float scale, int window,
+                 float cap, const float *slopes, const uint32_t *tree, int words, const int32_t *positions, void *out, int out_type,
+                 float *lse, const qg_paged *cache, void *ws, size_t ws_bytes, void *stream);
+
+/* Masks and positions of drafted trees from their parents: parents[t] is the index, among the drafts of t's sequence, of the
+ * draft that token t follows; it stands before it.  Anything else (-1, say) is a root, which follows the sequence itself.
+ *   tree[t * words ..]: the bits of t and of all that it follows;   positions[t] = kv_len - n + its depth (a root: 0).
+ *   parents, positions: tokens int32; tree: tokens x words; q_start, kv_len: as in qg_paged.
+ * A sequence has at most 32 * words drafts and 1024; those beyond are roots of their own with no bits.  Rows of tokens of no sequence become zeros.
+ *   1 <= words <= 32.  Both are made once for all layers. */
+int qg_tree_masks(const int32_t *parents, const int32_t *q_start, const int32_t *kv_len, int tokens, int batch, uint32_t *tree, int words,
+                  int32_t *positions, void *stream);
+
+/* qg_rope_append where a token's rotary position is not its slot: positions (tokens int32, NULL: the slots) turn, the slots
+ * still say where keys and values go.  Drafts of a tree rotate by their depth. */
+int qg_rope_append_at(const void *q, int64_t ldq, int64_t hdq, const void *k, int64_t ldk, int64_t hdk, const void *v,
+                      int64_t ldv, int64_t hdv, int in_type, int tokens, int q_heads, const uint64_t *turns, int rot, int pairs,
+                      float amp, const float *wq, const float *wk, float eps, const int32_t *positions, void *q_out,
+                      const qg_paged *cache, void *stream);
+
+/* Moves the accepted drafts of every sequence together and drops the others: slot base + keep[b * keep_stride + i] becomes slot
+ * base + i for i < keep_len[b] (base = kv_len - n), keys and values of all heads, in every layer; kv_out[b] = base + keep_len[b].
+ *   keep: batch rows of `width` int32, indices among the sequence's drafts, rising; keep_len: batch, held to 0 .. min(width, n).
+ *   An index below i or from n on moves nothing: slot base + i stays as it is.
+ *   cache: the first layer's; layer l has its pools layer_stride elements further on (steps: step_layer_stride), multiples
+ *   of 16 bytes.  kv_out: batch int32; it may be the array of cache->kv_len.
+ *   cache->q_start gives the drafts.   1 <= width <= 1024; 1 <= layers, batch <= 65535.  A page id outside the pool reads as zeros
+ *   and is not written, as in the other calls. */
+int qg_cache_keep(const int32_t *keep, int64_t keep_stride, const int32_t *keep_len, int width, int layers, int64_t layer_stride,
+                  int64_t step_layer_stride, int32_t *kv_out, const qg_paged *cache, void *stream);
+
+/* What qg_logits_adjust does to the logits of a row; members that are NULL do nothing.  A row belongs to sequence seq[row]
+ * (NULL: row is the sequence); ids outside 0 .. V - 1 and sequences outside 0 .. batch - 1 change nothing. */
+typedef struct qg_logits {
+    int batch;                      /* sequences                                                       */
+    int words;                      /* 32-bit words of a row of tree                                   */
+    int history_width;              /* ids that a row of history holds                                 */
+    int bias_entries;               /* entries of the two lists of biases                              */
+    const int32_t *seq;             /* rows                                                            */
+    const int32_t *history;         /* batch x history_stride token ids: what the sequence says so far */
+    const int32_t *history_len;     /* batch; needed beside history                                    */
+    const int32_t *prompt_len;      /* batch: the first ids of history that are its prompt, or NULL: none */
+    int64_t history_stride;
+    const float *repetition, *frequency, *presence; /* batch                                           */
+    const int32_t *bias_start;      /* batch + 1: the sequence's entries in the two lists below        */
+    const int32_t *bias_ids;
+    const float *bias;
+    const uint32_t *allow;          /* rows x allow_stride words: bit v % 32 of word v / 32 allows id v */
+    int64_t allow_stride;
+    const int32_t *drafts;          /* rows: the drafted token whose successor the row's logits choose */
+    const uint32_t *tree;           /* rows x words, as in qg_attn_tree: the drafts that the row follows */
+    const int32_t *q_start;         /* batch + 1: the rows of each sequence                            */
+} qg_logits;
+
+/* Logits before sampling, per row and id v, in fp32 and rounded once:
+ *   x = logits + bias of v (of several entries for one id the last one counts)
+ *   x = x > 0 ? x / repetition : x * repetition        where v occurs in the history or among the row's drafts
+ *   x = x - frequency * n - (n > 0 ? presence : 0)      n: how often v occurs after the prompt, the row's drafts included
+ *   x = -inf                                            where the row's mask does not allow v
+ * The row's drafts are those of its mask in tree, its own with them (rows q_start[s] + i of the call).
+ *   logits: rows ld elements apart, type; out: rows ldo apart, out_type (any of the three); it may be logits itself with the
+ *   same type and ldo = ld, and then only what changes is read and written.
+ * Limits: rows, V >= 1, rows * ceil((V + 3) / 8192) < 2^31; up to 2^30 ids of a history count.  Rows of ids that start on boundaries of 4
+ * elements, or equally far behind one in logits and out, take vector loads; any alignment of whole elements works.
+ * Lengths and starts are held inside the arrays. */
+int qg_logits_adjust(const void *logits, int type, int64_t ld, void *out, int out_type, int64_t ldo, int rows, int V, const qg_logits *how,
+                     void *stream);
+
 /* Bytes of qg_attn_paged's workspace ((size_t)-1: invalid arguments); depends on the current
  * device's SM count as qg_workspace_size does. */
 size_t qg_attn_workspace_size(int dim, int q_heads, int kv_heads, int tokens, int batch);
