@@ -30,8 +30,8 @@ TORCH_STAMP = TORCH_MODULE + ".for"  # the torch and the Python that the module 
 
 FORMATS = {"q4_0": 2, "q4_1": 3, "q5_0": 6, "q5_1": 7, "q8_0": 8, "q2_k": 10, "q3_k": 11, "q4_k": 12, "q5_k": 13,
            "q6_k": 14, "iq4_nl": 20, "iq4_xs": 23}
-# the attention kernels and what they are compiled for (MOD_PLAIN, MOD_SHAPED, MOD_CAPPED of csrc/qg_attn.cuh)
-ATTENTION = {"qg_rows": (1, 0), "qg_chunk": (2, 1, 0)}
+# the attention kernels and what they are compiled for (MOD_PLAIN to MOD_BIASED of csrc/qg_attn.cuh)
+ATTENTION = {"qg_rows": (1, 0), "qg_chunk": (3, 2, 1, 0)}
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -66,11 +66,11 @@ bool attn_tensor_map(CUtensorMap *map, const qg_paged &c, const void *base, int 
 }
 
 int attn_dev_err_take(unsigned int *err) {
-    unsigned int v[5] = {};
+    unsigned int v[6] = {};
     *err = 0;
     for (const int rc : {attn_rows_dev_err_take<MOD_PLAIN>(&v[0]), attn_chunk_dev_err_take<MOD_PLAIN>(&v[1]),
                          attn_rows_dev_err_take<MOD_SHAPED>(&v[2]), attn_chunk_dev_err_take<MOD_SHAPED>(&v[3]),
-                         attn_chunk_dev_err_take<MOD_CAPPED>(&v[4])})
+                         attn_chunk_dev_err_take<MOD_CAPPED>(&v[4]), attn_chunk_dev_err_take<MOD_BIASED>(&v[5])})
         if (rc) return rc;
     for (const unsigned int x : v) *err |= x;
     return QG_OK;
@@ -112,7 +112,9 @@ static int attn_plain(const AttnArgs &a, const qg_paged &c, int max_new, int sms
 }
 static int attn_other(const AttnArgs &a, const qg_paged &c, int max_new, int sms, cudaStream_t s) {
     if ((int64_t)max_new * a.G > DEC_ROWS)
-        return a.sh.cap_out > 0.0f ? attn_chunk<MOD_CAPPED>(a, c, sms, s) : attn_chunk<MOD_SHAPED>(a, c, sms, s);
+        return a.sh.slopes            ? attn_chunk<MOD_BIASED>(a, c, sms, s)
+               : a.sh.cap_out > 0.0f ? attn_chunk<MOD_CAPPED>(a, c, sms, s)
+                                     : attn_chunk<MOD_SHAPED>(a, c, sms, s);
     return attn_rows<MOD_SHAPED>(a, c, (int64_t)max_new * a.G <= 8 ? 1 : 2, sms, s);
 }
 

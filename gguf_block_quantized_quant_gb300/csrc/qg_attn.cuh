@@ -19,13 +19,15 @@ struct JoinDesc {
     int pad[3];
 };
 
-// What the kernels are compiled for (QG_MOD): causal or windowed attention; the same with other masks and a bias
-// that falls with the distance; and that with capped scores too.
-enum { MOD_PLAIN, MOD_SHAPED, MOD_CAPPED };
+// What the kernels are compiled for (QG_MOD): causal or windowed attention; the same with other masks; with those and
+// capped scores; and with those and a bias that falls with the distance, capped scores or not.  The row kernel is
+// compiled for the first and for MOD_SHAPED, which does the rest there too.
+enum { MOD_PLAIN, MOD_SHAPED, MOD_CAPPED, MOD_BIASED };
 
 // What changes scores and masks (null: nothing), as the kernels read it.
 struct Shape {
     float cap_in, cap_out;     // score = cap_out * tanh(cap_in * S), in powers of two (cap_out 0: not capped)
+    float poly[5];             // cap_out times the coefficients of tanh_near (chunk kernel)
     const float *slopes;       // Hq
     const int32_t *prefix;     // batch: the first slots, which every token of the sequence sees
     const int32_t *first;      // tokens: no slot before it is seen
@@ -102,9 +104,10 @@ __device__ __forceinline__ uint32_t tree_bits(const uint32_t *row, int words, in
 // tanh(x) for |x| <= TANH_NEAR: x times a polynomial in x^2 (our own fit to the least largest relative error: 7e-7 as
 // evaluated).  Beyond it 1 - 2 / (1 + e^2x), which loses small x in the 1.
 constexpr float TANH_NEAR = 0.75f;
+constexpr float TANH_C0 = 0x1.ffffeep-1f, TANH_C1 = -0x1.554802p-2f, TANH_C2 = 0x1.0f8b42p-3f, TANH_C3 = -0x1.9a0facp-5f, TANH_C4 = 0x1.a7ad9ep-7f;
 __device__ __forceinline__ float tanh_near(float x) {
     const float u = x * x;
-    return x * fmaf(u, fmaf(u, fmaf(u, fmaf(u, 0x1.a7ad9ep-7f, -0x1.9a0facp-5f), 0x1.0f8b42p-3f), -0x1.554802p-2f), 0x1.ffffeep-1f);
+    return x * fmaf(u, fmaf(u, fmaf(u, fmaf(u, TANH_C4, TANH_C3), TANH_C2), TANH_C1), TANH_C0);
 }
 
 // One partial result: rows x D fp32 (normalised), then rows base-2 logarithms of the sums.
@@ -135,6 +138,11 @@ constexpr float LN2 = 0.6931471805599453f;
 __device__ __forceinline__ float exp2_approx(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
 __device__ __forceinline__ float log2_approx(float x) {
@@ -204,12 +212,11 @@ __device__ __forceinline__ uint32_t codes_to_f16(uint32_t biased, uint32_t sel) 
 }
 
 __device__ __forceinline__ float tanh_any(float x) {
-    float r;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + exp2_approx(x * (2.0f * LOG2E))));
+    const float r = rcp_approx(1.0f + exp2_approx(x * (2.0f * LOG2E)));
     return fabsf(x) <= TANH_NEAR ? tanh_near(x) : fmaf(-2.0f, r, 1.0f);
 }
 
-// The kernels by what they are compiled for: rows (qg_rows.cu, PLAIN and SHAPED, which caps too): up to 8 nr rows of
+// The kernels by what they are compiled for: rows (qg_rows.cu): up to 8 nr rows of
 // heads per sequence and cache head at a time; chunk (qg_chunk.cu): many, and its workspace.  _take: reads and clears the
 // device error word.
 template <int MOD>

@@ -536,10 +536,10 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
                     hi_min = __reduce_min_sync(0xffffffffu, hi);
                     lo_max = __reduce_max_sync(0xffffffffu, lo);
                     if (a.sh.tree && lo != 0x7fffffff) tree = a.sh.tree + (int64_t)(k.t.first + i) * a.sh.words;
-                    if (a.sh.slopes) slope = a.sh.slopes[k.h * a.G + g] * LOG2E;
+                    if (MOD == MOD_BIASED) slope = a.sh.slopes[k.h * a.G + g] * LOG2E;
                 }
                 // scores that are no multiple of S any more are formed at once, their factor is 1 then
-                const bool bent = MOD == MOD_CAPPED || (MOD == MOD_SHAPED && a.sh.slopes);
+                constexpr bool bent = MOD == MOD_CAPPED || MOD == MOD_BIASED;
                 const float scale2 = bent ? 1.0f : a.scale2, scale_p2 = bent ? 1.0f : a.scale_p2;
                 float m = -INFINITY, l = 0.0f;
                 for (int j = blk0; j < end; ++j, ++done) {
@@ -551,7 +551,7 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
                     mbar_wait(s_full(q, buf), (done / SB) & 1);
                     tc_fence_after();
                     uint32_t s[Cfg::HOLD ? BN / 32 : 1][32];
-                    auto mask = [&](uint32_t (&v)[32], int c0) {
+                    auto mask = [&](uint32_t (&v)[32], int c0, uint32_t other) {  // what is not seen becomes `other`
                         if (edge) {
                             const int up = c_hi - c0, down = c_lo - c0;  // visible: down .. up
                             uint32_t see = (up < 0 ? 0u : 0xffffffffu >> (31 - min(up, 31))) & (down > 31 ? 0u : 0xffffffffu << max(down, 0));
@@ -562,9 +562,10 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
                             }
 #pragma unroll
                             for (int i = 0; i < 32; ++i)
-                                if (!(see >> i & 1u)) v[i] = 0xff800000u;  // -inf
+                                if (!(see >> i & 1u)) v[i] = other;
                         }
                     };
+                    constexpr uint32_t HIDDEN = 0xff800000u;  // -inf
                     auto top = [&](const uint32_t (&v)[32]) {
                         float x[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -572,36 +573,61 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
                             x[(i / 2) & 3] = fmaxf(fmaxf(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), x[(i / 2) & 3]);
                         return fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
                     };
-                    // scores as powers of two's exponents, from S (MOD_PLAIN: they are S * scale2)
-                    auto bend = [&](uint32_t (&v)[32], int c0) {
-                        if constexpr (MOD == MOD_CAPPED) {
-                            float far = 0.0f;
+                    // From S to the scores as powers of two's exponents, where these are no multiple of S
+                    auto capped = [&](uint32_t (&v)[32], int c0) {
+                        float far = 0.0f;
+                        mask(v, c0, 0u);  // whatever unseen slots hold chooses nothing
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * a.sh.cap_in);
+                        for (int i = 0; i < 32; i += 2) far = fmaxf(fmaxf(fabsf(__uint_as_float(v[i])), fabsf(__uint_as_float(v[i + 1]))), far);
+                        if (far * a.sh.cap_in > TANH_NEAR) {  // a row with scores around the cap: 1 - 2 / (1 + e^2x) is exact enough beside those
+                            const float k = a.sh.cap_in * (2.0f * LOG2E), m2 = -2.0f * a.sh.cap_out;
 #pragma unroll
-                            for (int i = 0; i < 32; i += 2) far = fmaxf(fmaxf(fabsf(__uint_as_float(v[i])), fabsf(__uint_as_float(v[i + 1]))), far);
-                            if (__any_sync(0xffffffffu, far > TANH_NEAR)) {
-#pragma unroll
-                                for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(a.sh.cap_out * tanh_any(__uint_as_float(v[i])));
-                            } else {
-#pragma unroll
-                                for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(a.sh.cap_out * tanh_near(__uint_as_float(v[i])));
+                            for (int i = 0; i < 32; ++i) {
+                                const float e = exp2_approx(__uint_as_float(v[i]) * k);
+                                v[i] = __float_as_uint(fmaf(m2, rcp_approx(1.0f + e), a.sh.cap_out));
                             }
-                        } else if (bent) {
+                        } else {
+                            const uint64_t in2 = pack_f32x2(a.sh.cap_in, a.sh.cap_in);
+                            uint64_t k[5];
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * a.scale2);
+                            for (int i = 0; i < 5; ++i) k[i] = pack_f32x2(a.sh.poly[i], a.sh.poly[i]);
+#pragma unroll
+                            for (int i = 0; i < 32; i += 2) {
+                                const uint64_t x = mul_f32x2(pack_b32x2(v[i], v[i + 1]), in2), u = mul_f32x2(x, x);
+                                const uint64_t y = mul_f32x2(x, fma_f32x2(u, fma_f32x2(u, fma_f32x2(u, fma_f32x2(u, k[4], k[3]), k[2]), k[1]), k[0]));
+                                float y0, y1;
+                                unpack_f32x2(y, y0, y1);
+                                v[i] = __float_as_uint(y0), v[i + 1] = __float_as_uint(y1);
+                            }
                         }
-                        if (MOD != MOD_PLAIN && a.sh.slopes) {
+                    };
+                    auto bend = [&](uint32_t (&v)[32], int c0) {
+                        if constexpr (MOD == MOD_CAPPED) capped(v, c0);
+                        if constexpr (MOD == MOD_BIASED) {
+                            float in = a.scale2;
+                            if (a.sh.cap_out > 0.0f) {
+                                capped(v, c0);
+                                in = 1.0f;
+                            }
                             const int key = key0 + c0;
-                            if (a.sh.positions && key + 32 > pos0) {  // new tokens are where the caller says
-                                const float d = (float)row_pos;
+                            const float d = (float)(row_pos - key);
+                            if (!a.sh.prefix && !a.sh.positions) {  // what is ahead of the row is not seen: no sign to take off
+                                const uint64_t in2 = pack_f32x2(in, in), s2 = pack_f32x2(slope, slope), d2 = pack_f32x2(-slope * d, -slope * d);
+#pragma unroll
+                                for (int i = 0; i < 32; i += 2) {
+                                    const uint64_t y = fma_f32x2(pack_b32x2(v[i], v[i + 1]), in2, fma_f32x2(s2, pack_f32x2((float)i, (float)(i + 1)), d2));
+                                    float y0, y1;
+                                    unpack_f32x2(y, y0, y1);
+                                    v[i] = __float_as_uint(y0), v[i + 1] = __float_as_uint(y1);
+                                }
+                            } else if (a.sh.positions && key + 32 > pos0) {  // new tokens are where the caller says
 #pragma unroll
                                 for (int i = 0; i < 32; ++i)
-                                    v[i] = __float_as_uint(fmaf(-slope, fabsf(d - slot_position(a, k.t.first, pos0, k.t.n, key + i)), __uint_as_float(v[i])));
+                                    v[i] = __float_as_uint(fmaf(__uint_as_float(v[i]), in,
+                                                                -slope * fabsf((float)row_pos - slot_position(a, k.t.first, pos0, k.t.n, key + i))));
                             } else {
-                                const float d = (float)(row_pos - key);
 #pragma unroll
-                                for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(fmaf(-slope, fabsf(d - (float)i), __uint_as_float(v[i])));
+                                for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(fmaf(__uint_as_float(v[i]), in, -slope * fabsf(d - (float)i)));
                             }
                         }
                     };
@@ -617,17 +643,17 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
 #pragma unroll
                         for (int c = 0; c < BN / 32; ++c) {
                             bend(s[c], 32 * c);
-                            mask(s[c], 32 * c);
+                            mask(s[c], 32 * c, HIDDEN);
                             mx = fmaxf(mx, top(s[c]));
                         }
                     } else {
-                        const bool late = MOD == MOD_CAPPED && !a.sh.slopes;  // a cap alone keeps the order: bend the maximum
+                        constexpr bool late = MOD == MOD_CAPPED;  // a cap alone keeps the order: bend the maximum
 #pragma unroll 1
                         for (int c = 0; c < BN / 32; ++c) {
                             tmem_ld32(scol + 32 * c, s[0]);
                             tmem_wait_ld(s[0]);
                             if (!late) bend(s[0], 32 * c);
-                            mask(s[0], 32 * c);
+                            mask(s[0], 32 * c, HIDDEN);
                             mx = fmaxf(mx, top(s[0]));
                         }
                         if (late && mx != -INFINITY) mx = a.sh.cap_out * tanh_any(mx * a.sh.cap_in);
@@ -678,7 +704,7 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
                                 mbar_arrive(s_empty(q));
                             }
                             bend(v, 32 * c);
-                            mask(v, 32 * c);
+                            mask(v, 32 * c, HIDDEN);
                         }
                         uint32_t p[16];
 #pragma unroll
@@ -1215,6 +1241,8 @@ static int chunk_run(const AttnArgs &in, const qg_paged &c, int sms, cudaStream_
     const uint32_t qsign = a.scale2 < 0.0f ? 0x80008000u : 0u;
     a.scale2 = std::max(std::abs(a.scale2), 1e-30f);
     a.sh.cap_in = std::abs(a.sh.cap_in);
+    constexpr float fit[5] = {TANH_C0, TANH_C1, TANH_C2, TANH_C3, TANH_C4};
+    for (int i = 0; i < 5; ++i) a.sh.poly[i] = fit[i] * a.sh.cap_out;
     a.scale_p2 = std::exp2(std::floor(std::log2(a.scale2)));
     const int box = gcd(c.page, Cfg::VR);
     CUtensorMap km{}, vm{};

@@ -139,68 +139,121 @@ __global__ void __launch_bounds__(KEEP_THREADS) keep_lengths_kernel(const KeepAr
 }
 
 // ----------------------------------------------------------------------------- logits
-// A block takes a segment of one row.  It counts the ids of the segment that the row's history and drafts hold in shared
-// memory (a word per id: the count, bit 31 for ids of the prompt), notes the last bias entry of each id and the segment's
-// bits of the mask there, and then streams the logits past that.  Whole numbers are added, so the order of the
-// atomics changes nothing.  Bound by memory: the logits are read and written once; every block of a row
-// reads its history again (from L2), which is why segments are as long as leaves four blocks per SM.
+// A block takes a segment of a few rows, one after the other.  It counts the ids of the segment that the row's history and drafts
+// hold in shared memory (a word per id: the count, bit 31 for ids of the prompt) and notes the last bias entry of each
+// id there; rows of one sequence share that, but for their drafts, which are added before a row and taken off after it.  The logits
+// are on their way to registers meanwhile.  Whole numbers are added, so the order of the atomics changes nothing.
+// Bound by memory: the logits are read and written once; what hides the chain of dependent loads before them (sequence,
+// lengths, ids) are the other blocks of the SM.
 struct LogitsArgs {
     const void *x;
     void *out;
     int64_t ld, ldo;  // elements
     int V, seg;       // seg: ids of a segment, a multiple of 128
-    int rows, in_place, has_bias;
+    int rows, group;  // group: rows of a block
+    int in_place, has_bias;
     qg_logits how;
 };
 
-constexpr int LOGITS_THREADS = 512, LOGITS_SEG = 8192, LOGITS_U = 4;
+constexpr int LOGITS_THREADS = 256, LOGITS_U = 4, LOGITS_SEG = LOGITS_THREADS * LOGITS_U * 4;
+
+// Four elements as they come.
+template <class T>
+struct Raw4 {
+    uint2 w;
+    __device__ __forceinline__ void load(const T *p) { w = *reinterpret_cast<const uint2 *>(p); }
+    __device__ __forceinline__ void set(int k, T x) { reinterpret_cast<T *>(&w)[k] = x; }
+    __device__ __forceinline__ void get(float (&v)[4]) const {
+        const float2 a = unpack2<T>(w.x), b = unpack2<T>(w.y);
+        v[0] = a.x, v[1] = a.y, v[2] = b.x, v[3] = b.y;
+    }
+};
+template <>
+struct Raw4<float> {
+    float4 w;
+    __device__ __forceinline__ void load(const float *p) { w = *reinterpret_cast<const float4 *>(p); }
+    __device__ __forceinline__ void set(int k, float x) { reinterpret_cast<float *>(&w)[k] = x; }
+    __device__ __forceinline__ void get(float (&v)[4]) const { v[0] = w.x, v[1] = w.y, v[2] = w.z, v[3] = w.w; }
+};
 
 template <class I, class O>
-__global__ void __launch_bounds__(LOGITS_THREADS) logits_kernel(const LogitsArgs a) {
+__global__ void __launch_bounds__(LOGITS_THREADS, 4) logits_kernel(const LogitsArgs a) {
     extern __shared__ __align__(16) uint32_t lg_smem[];
     uint32_t *count = lg_smem;
-    uint32_t *mask = count + a.seg;      // seg / 32 words
+    uint32_t *mask = count + a.seg;       // seg / 32 words
     uint32_t *entry = mask + a.seg / 32;  // seg words, where there are biases
     const int tid = threadIdx.x;
     const int segs = (a.V + 3 + a.seg - 1) / a.seg;
-    const int64_t row = blockIdx.x / segs;
-    const I *x = static_cast<const I *>(a.x) + row * a.ld;
-    O *out = static_cast<O *>(a.out) + row * a.ldo;
-    // Places of a row are counted from the boundary of 4 elements before its start in `out`; id v is at place v + lead
-    const int lead = (int)((reinterpret_cast<uintptr_t>(out) / sizeof(O)) & 3);
-    const bool vec = (reinterpret_cast<uintptr_t>(x) / sizeof(I) & 3) == lead;
-    const int p0 = (int)(blockIdx.x % segs) * a.seg, ids0 = p0 - lead;  // the segment's first place and id (below 0 in the first)
-    const int n = min(a.seg, a.V + lead - p0);            // places of it up to the row's end
-    if (n <= 0) return;
+    const int row0 = (int)(blockIdx.x / segs) * a.group, row1 = min(row0 + a.group, a.rows);
+    const int p0 = (int)(blockIdx.x % segs) * a.seg;
     griddep_wait();
     griddep_launch_dependents();
 
-    const int s = a.how.seq ? a.how.seq[row] : (int)min(row, (int64_t)0x7fffffff);
-    const bool known = (unsigned)s < (unsigned)a.how.batch;
-    for (int i = tid; i < a.seg / 4; i += LOGITS_THREADS) reinterpret_cast<uint4 *>(count)[i] = make_uint4(0, 0, 0, 0);
-    if (a.has_bias)
-        for (int i = tid; i < a.seg / 4; i += LOGITS_THREADS) reinterpret_cast<uint4 *>(entry)[i] = make_uint4(0, 0, 0, 0);
-    if (a.how.allow) {
-        const uint32_t *allow = a.how.allow + row * a.how.allow_stride;
-        const int words = (a.V + 31) / 32;
-        for (int i = tid; i < a.seg / 32; i += LOGITS_THREADS) {
-            const int at = ids0 + 32 * i, w = at >> 5;  // at may be below 0
-            const uint32_t lo = w >= 0 && w < words ? allow[w] : 0u, hi = w + 1 < words ? allow[w + 1] : 0u;
-            mask[i] = __funnelshift_r(lo, hi, at & 31);
-        }
-    }
+    int held = -2, held_ids0 = 0;  // the sequence (-1: none) whose ids are counted, and the segment's first id then
     float rep = 1.0f, freq = 0.0f, pres = 0.0f;
     const float *bias = nullptr;
-    if (known) {
-        if (a.how.repetition) rep = a.how.repetition[s];
-        if (a.how.frequency) freq = a.how.frequency[s];
-        if (a.how.presence) pres = a.how.presence[s];
-    }
-    __syncthreads();
-    if (known) {
+    for (int row = row0; row < row1; ++row) {
+        const I *x = static_cast<const I *>(a.x) + row * a.ld;
+        O *out = static_cast<O *>(a.out) + row * a.ldo;
+        // Places of a row are counted from the boundary of 4 elements before its start in `out`; id v is at place v + lead
+        const int lead = (int)((reinterpret_cast<uintptr_t>(out) / sizeof(O)) & 3);
+        const bool vec = (reinterpret_cast<uintptr_t>(x) / sizeof(I) & 3) == lead;
+        const int ids0 = p0 - lead;                 // the segment's first id (below 0 in the first)
+        const int n = min(a.seg, a.V + lead - p0);  // places of it up to the row's end
+        if (n <= 0) continue;                       // the last row's lead may need a segment that this one's does not
+        const int s = a.how.seq ? a.how.seq[row] : row;
+        const bool known = (unsigned)s < (unsigned)a.how.batch;
+        const bool in_place = std::is_same<I, O>::value && a.in_place;
+        auto whole = [&](int q) { return vec && ids0 + 4 * q >= 0 && 4 * q + 4 <= n; };
+        auto fetch = [&](Raw4<I> &v, int q) {
+            const int id = ids0 + 4 * q;
+            if (whole(q)) {
+                v.load(x + id);
+            } else {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) v.set(k, id + k >= 0 && 4 * q + k < n ? x[id + k] : from_f32<I>(0.0f));
+            }
+        };
+        Raw4<I> v[LOGITS_U];
+        if (!in_place) {
+#pragma unroll
+            for (int u = 0; u < LOGITS_U; ++u)
+                if (4 * (tid + u * LOGITS_THREADS) < n) fetch(v[u], tid + u * LOGITS_THREADS);
+        }
+        if (a.how.allow) {
+            const uint32_t *allow = a.how.allow + row * a.how.allow_stride;
+            const int words = (a.V + 31) / 32;
+            for (int i = tid; i < a.seg / 32; i += LOGITS_THREADS) {
+                const int at = ids0 + 32 * i, w = at >> 5;  // at may be below 0
+                const uint32_t lo = w >= 0 && w < words ? allow[w] : 0u, hi = w + 1 < words ? allow[w + 1] : 0u;
+                mask[i] = __funnelshift_r(lo, hi, at & 31);
+            }
+        }
         auto place = [&](int id) { return (unsigned)id < (unsigned)a.V ? id - ids0 : -1; };
-        if (a.how.history) {
-            const int len = min(max(a.how.history_len[s], 0), min(a.how.history_width, 1 << 30)), said = a.how.prompt_len ? a.how.prompt_len[s] : 0;
+        const bool fresh = (known ? s : -1) != held || ids0 != held_ids0;
+        if (fresh) {
+            held = known ? s : -1;
+            held_ids0 = ids0;
+            for (int i = tid; i < a.seg / 4; i += LOGITS_THREADS) reinterpret_cast<uint4 *>(count)[i] = make_uint4(0, 0, 0, 0);
+            if (a.has_bias)
+                for (int i = tid; i < a.seg / 4; i += LOGITS_THREADS) reinterpret_cast<uint4 *>(entry)[i] = make_uint4(0, 0, 0, 0);
+            rep = 1.0f, freq = pres = 0.0f;
+            int len = 0, said = 0, start = 0, entries = 0;
+            if (known) {
+                if (a.how.repetition) rep = a.how.repetition[s];
+                if (a.how.frequency) freq = a.how.frequency[s];
+                if (a.how.presence) pres = a.how.presence[s];
+                if (a.how.history) {
+                    len = min(max(a.how.history_len[s], 0), min(a.how.history_width, 1 << 30));
+                    said = a.how.prompt_len ? a.how.prompt_len[s] : 0;
+                }
+                if (a.has_bias) {
+                    start = min(max(a.how.bias_start[s], 0), a.how.bias_entries);
+                    entries = min(a.how.bias_start[s + 1], a.how.bias_entries) - start;
+                    bias = a.how.bias + start;
+                }
+            }
+            __syncthreads();
             const int32_t *h = a.how.history + s * a.how.history_stride;
             auto add = [&](int id, int i) {
                 const int at = place(id);
@@ -212,89 +265,74 @@ __global__ void __launch_bounds__(LOGITS_THREADS) logits_kernel(const LogitsArgs
             };
             const int head = min(len, (int)(-(reinterpret_cast<intptr_t>(h) / 4) & 3)), quads = (len - head) / 4;
             if (tid < head) add(h[tid], tid);
-#pragma unroll 2
+#pragma unroll 4
             for (int i = tid; i < quads; i += LOGITS_THREADS) {
-                const int4 v = reinterpret_cast<const int4 *>(h + head)[i];
+                const int4 w = reinterpret_cast<const int4 *>(h + head)[i];
                 const int at = head + 4 * i;
-                add(v.x, at), add(v.y, at + 1), add(v.z, at + 2), add(v.w, at + 3);
+                add(w.x, at), add(w.y, at + 1), add(w.z, at + 2), add(w.w, at + 3);
             }
             const int tail = head + 4 * quads + tid;
             if (tail < len) add(h[tail], tail);
-        }
-        if (a.how.drafts) {
-            const int first = min(max(a.how.q_start[s], 0), a.rows), drafts = min(max(a.how.q_start[s + 1], 0), a.rows) - first;
-            const int bits = (int)min((int64_t)drafts, (int64_t)32 * a.how.words);
-            const uint32_t *tree = a.how.tree + row * a.how.words;
-            for (int i = tid; i < bits; i += LOGITS_THREADS)
-                if (tree[i >> 5] >> (i & 31) & 1) {
-                    const int at = place(a.how.drafts[first + i]);
-                    if ((unsigned)at < (unsigned)n) atomicAdd(count + at, 1u);
-                }
-        }
-        if (a.has_bias) {
-            const int start = min(max(a.how.bias_start[s], 0), a.how.bias_entries), entries = min(a.how.bias_start[s + 1], a.how.bias_entries) - start;
-            bias = a.how.bias + start;
             for (int i = tid; i < entries; i += LOGITS_THREADS) {
                 const int at = place(a.how.bias_ids[start + i]);
                 if ((unsigned)at < (unsigned)n) atomicMax(entry + at, (uint32_t)i + 1u);
             }
         }
-    }
-    __syncthreads();
-
-    auto adjust = [&](float v, uint32_t c, uint32_t e, bool allowed) {
-        if (e) v += bias[e - 1];
-        if (c) {
-            v = v > 0.0f ? __fdiv_rn(v, rep) : v * rep;
-            const uint32_t times = c & 0x7fffffffu;
-            if (times) v = fmaf(-freq, (float)times, v) - pres;
-        }
-        return allowed ? v : -INFINITY;
-    };
-    const bool in_place = std::is_same<I, O>::value && a.in_place;
-    for (int q0 = tid; q0 < (n + 3) / 4; q0 += LOGITS_THREADS * LOGITS_U) {
-        float v[LOGITS_U][4];
-        uint4 c[LOGITS_U], e[LOGITS_U];
-        uint32_t ok[LOGITS_U];
-        bool whole[LOGITS_U], go[LOGITS_U];
-#pragma unroll
-        for (int u = 0; u < LOGITS_U; ++u) {
-            const int q = q0 + u * LOGITS_THREADS, at = 4 * q, id = ids0 + at;
-            go[u] = at < n;
-            if (!go[u]) continue;
-            whole[u] = vec && id >= 0 && at + 4 <= n;
-            c[u] = reinterpret_cast<const uint4 *>(count)[q];
-            e[u] = a.has_bias ? reinterpret_cast<const uint4 *>(entry)[q] : make_uint4(0, 0, 0, 0);
-            ok[u] = a.how.allow ? mask[at >> 5] >> (at & 31) & 15u : 15u;
-            if (in_place) {
-                const bool same = ok[u] == 15u && !(c[u].x | c[u].y | c[u].z | c[u].w | e[u].x | e[u].y | e[u].z | e[u].w);
-                go[u] = !same;
-                if (same || (ok[u] == 0u && whole[u])) {
-                    v[u][0] = v[u][1] = v[u][2] = v[u][3] = 0.0f;
-                    continue;
+        auto path = [&](uint32_t by) {  // the row's drafts
+            if (!known || !a.how.drafts) return;
+            const int first = min(max(a.how.q_start[s], 0), a.rows), drafts = min(max(a.how.q_start[s + 1], 0), a.rows) - first;
+            const int bits = (int)min((int64_t)drafts, (int64_t)32 * a.how.words);
+            const uint32_t *tree = a.how.tree + (int64_t)row * a.how.words;
+            for (int i = tid; i < bits; i += LOGITS_THREADS)
+                if (tree[i >> 5] >> (i & 31) & 1) {
+                    const int at = place(a.how.drafts[first + i]);
+                    if ((unsigned)at < (unsigned)n) atomicAdd(count + at, by);
                 }
+        };
+        path(1u);
+        __syncthreads();
+
+        auto adjust = [&](float y, uint32_t c, uint32_t e) {
+            if (e) y += bias[e - 1];
+            if (c) {
+                y = y > 0.0f ? __fdiv_rn(y, rep) : y * rep;
+                const uint32_t times = c & 0x7fffffffu;
+                if (times) y = fmaf(-freq, (float)times, y) - pres;
             }
-            if (whole[u]) {
-                load_vec<I, 4>(x + id, v[u]);
-            } else {
-#pragma unroll
-                for (int k = 0; k < 4; ++k) v[u][k] = id + k >= 0 && at + k < n ? to_f32(x[id + k]) : 0.0f;
-            }
-        }
+            return y;
+        };
 #pragma unroll
         for (int u = 0; u < LOGITS_U; ++u) {
-            if (!go[u]) continue;
-            const int at = 4 * (q0 + u * LOGITS_THREADS), id = ids0 + at;
-            const uint32_t cs[4] = {c[u].x, c[u].y, c[u].z, c[u].w}, es[4] = {e[u].x, e[u].y, e[u].z, e[u].w};
+            const int q = tid + u * LOGITS_THREADS, at = 4 * q, id = ids0 + at;
+            if (at >= n) break;
+            const uint4 c = reinterpret_cast<const uint4 *>(count)[q];
+            const uint4 e = a.has_bias ? reinterpret_cast<const uint4 *>(entry)[q] : make_uint4(0, 0, 0, 0);
+            const uint32_t ok = a.how.allow ? mask[at >> 5] >> (at & 31) & 15u : 15u;
+            const bool touched = (c.x | c.y | c.z | c.w | e.x | e.y | e.z | e.w) != 0;
+            if (in_place) {
+                if (ok == 15u && !touched) continue;
+                if (ok != 0u || !whole(q)) fetch(v[u], q);
+            }
+            float y[4];
+            v[u].get(y);
+            if (touched) {
+                y[0] = adjust(y[0], c.x, e.x), y[1] = adjust(y[1], c.y, e.y);
+                y[2] = adjust(y[2], c.z, e.z), y[3] = adjust(y[3], c.w, e.w);
+            }
 #pragma unroll
-            for (int k = 0; k < 4; ++k) v[u][k] = adjust(v[u][k], cs[k], es[k], ok[u] >> k & 1);
-            if (whole[u]) {
-                store_vec<O, 4>(out + id, v[u]);
+            for (int k = 0; k < 4; ++k) y[k] = ok >> k & 1 ? y[k] : -INFINITY;
+            if (whole(q)) {
+                store_vec<O, 4>(out + id, y);
             } else {
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                    if (id + k >= 0 && at + k < n) out[id + k] = from_f32<O>(v[u][k]);
+                    if (id + k >= 0 && at + k < n) out[id + k] = from_f32<O>(y[k]);
             }
+        }
+        if (row + 1 < row1) {
+            __syncthreads();
+            path(0xffffffffu);  // off again
+            if (a.how.drafts) __syncthreads();
         }
     }
 }
@@ -305,9 +343,9 @@ static int64_t logits_segments(int V, int seg) { return ((int64_t)V + 3 + seg - 
 template <class I, class O>
 static int logits_launch(const LogitsArgs &a, cudaStream_t s) {
     const uint32_t bytes = (uint32_t)a.seg * (a.has_bias ? 8 : 4) + a.seg / 8;
-    auto kern = logits_kernel<I, O>;
-    if (bytes > 48 * 1024 && !allow_smem((const void *)kern, LOGITS_SEG * 8 + LOGITS_SEG / 8)) return QG_ECUDA;
-    return launch_programmatic(kern, dim3((unsigned)(a.rows * logits_segments(a.V, a.seg))), LOGITS_THREADS, bytes, s, a) ? QG_OK : QG_ECUDA;
+    const int64_t groups = (a.rows + (int64_t)a.group - 1) / a.group;
+    return launch_programmatic(logits_kernel<I, O>, dim3((unsigned)(groups * logits_segments(a.V, a.seg))), LOGITS_THREADS, bytes, s, a) ? QG_OK
+                                                                                                                                       : QG_ECUDA;
 }
 template <class I>
 static int logits_out(const LogitsArgs &a, int out_type, cudaStream_t s) {
@@ -392,11 +430,11 @@ int qg_logits_adjust(const void *logits, int type, int64_t ld, void *out, int ou
                           (const void *)h.bias_ids, (const void *)h.bias, (const void *)h.allow, (const void *)h.drafts, (const void *)h.tree,
                           (const void *)h.q_start})
         if (!host_aligned(p, 4)) return QG_EALIGN;
-    LogitsArgs a{logits, out, ld, ldo, V, 0, rows, out == logits, h.bias_start != nullptr, h};
-    const int planned = device_sms_planning();
-    // about four blocks per SM, of no more than LOGITS_SEG ids
-    const int64_t share = (int64_t)rows * V / (4 * (int64_t)planned) / 128 * 128 + 128;
-    a.seg = (int)std::min<int64_t>(std::max<int64_t>(share, 512), LOGITS_SEG);
+    LogitsArgs a{logits, out, ld, ldo, V, 0, rows, 1, out == logits, h.bias_start != nullptr, h};
+    const int64_t fill = 4 * (int64_t)device_sms_planning();  // blocks that run at once
+    a.seg = (int)std::min<int64_t>(std::max<int64_t>(rows * (int64_t)V / fill / 128 * 128 + 128, 512), LOGITS_SEG);
+    // rows that may share a sequence share a block, as long as every SM has a few blocks to overlap
+    if (h.seq && sequences) a.group = (int)std::min<int64_t>(std::max<int64_t>(rows * logits_segments(V, a.seg) / (2 * fill), 1), 8);
     if (rows * logits_segments(V, a.seg) > INT32_MAX) return QG_EINVAL;
     const int sms = device_sms();
     if (sms < 0) return sms;
