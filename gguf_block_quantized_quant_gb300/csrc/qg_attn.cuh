@@ -27,7 +27,9 @@ enum { MOD_PLAIN, MOD_SHAPED, MOD_CAPPED, MOD_BIASED };
 // What changes scores and masks (null: nothing), as the kernels read it.
 struct Shape {
     float cap_in, cap_out;     // score = cap_out * tanh(cap_in * S), in powers of two (cap_out 0: not capped)
-    float poly[5];             // cap_out times the coefficients of tanh_near (chunk kernel)
+    float poly[5];             // chunk kernel: cap_out times the coefficients of tanh_near,
+    float small[3];            // those of tanh_small, in S: score = S (small[0] + S^2 (small[1] + S^2 small[2])) up to
+    float small_to;            // this |S| (below 0: nowhere)
     const float *slopes;       // Hq
     const int32_t *prefix;     // batch: the first slots, which every token of the sequence sees
     const int32_t *first;      // tokens: no slot before it is seen
@@ -105,6 +107,9 @@ __device__ __forceinline__ uint32_t tree_bits(const uint32_t *row, int words, in
 // evaluated).  Beyond it 1 - 2 / (1 + e^2x), which loses small x in the 1.
 constexpr float TANH_NEAR = 0.75f;
 constexpr float TANH_C0 = 0x1.ffffeep-1f, TANH_C1 = -0x1.554802p-2f, TANH_C2 = 0x1.0f8b42p-3f, TANH_C3 = -0x1.9a0facp-5f, TANH_C4 = 0x1.a7ad9ep-7f;
+// And x (S0 + x^2 (S1 + x^2 S2)) for |x| <= TANH_SMALL: 5e-7.
+constexpr float TANH_SMALL = 0.25f;
+constexpr float TANH_S0 = 0x1.fffff2p-1f, TANH_S1 = -0x1.553762p-2f, TANH_S2 = 0x1.06ff0ap-3f;
 __device__ __forceinline__ float tanh_near(float x) {
     const float u = x * x;
     return x * fmaf(u, fmaf(u, fmaf(u, fmaf(u, TANH_C4, TANH_C3), TANH_C2), TANH_C1), TANH_C0);

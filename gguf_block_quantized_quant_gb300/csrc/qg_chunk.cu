@@ -150,7 +150,9 @@ static ChunkPlan chunk_plan_at(uint8_t *p, int64_t tiles) {
     return c;
 }
 
-constexpr int PLAN_THREADS = 256, PLAN_SEQS = 1024;
+constexpr int PLAN_SEQS = 1024, PLAN_ORDERED = 256;  // tiles at most that are put in order
+// Masks of other kinds have every token's range looked up: more warps for that
+constexpr int plan_threads(int mod) { return mod == MOD_PLAIN ? 256 : 1024; }
 
 // An item costs its slot tiles and CHUNK_OV more for loading the queries and writing the result, in
 // the same unit; a range that ends inside that part leaves the item to the next CTA.  Measured with 1,
@@ -168,11 +170,13 @@ __device__ __forceinline__ int deal(int k, int c, int ctas) { return k & 1 ? (k 
 // attention kernel in time, so it is built for few steps: one warp places the sequences' first tiles,
 // then a thread makes a tile and one barrier a prefix of their costs.
 template <int MOD>
-__global__ void __launch_bounds__(PLAN_THREADS) attn_plan_kernel(const AttnArgs a, ChunkPlan p, int rows, int bn, int max_tiles, int ctas) {
+__global__ void __launch_bounds__(plan_threads(MOD)) attn_plan_kernel(const AttnArgs a, ChunkPlan p, int rows, int bn, int max_tiles, int ctas) {
+    constexpr int PLAN_THREADS = plan_threads(MOD);
     __shared__ int64_t part[2][PLAN_THREADS / 32];
-    __shared__ int unit[PLAN_THREADS], sorted[PLAN_THREADS];
+    __shared__ int unit[PLAN_ORDERED], sorted[PLAN_ORDERED];
     __shared__ int off[PLAN_SEQS + 1];
     __shared__ int2 range[MOD == MOD_PLAIN ? 1 : PLAN_THREADS];  // per tile of a round: first slot seen, end of those seen
+    __shared__ Seq seqs[MOD == MOD_PLAIN ? 1 : PLAN_SEQS];
     griddep_wait();
     griddep_launch_dependents();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -184,7 +188,12 @@ __global__ void __launch_bounds__(PLAN_THREADS) attn_plan_kernel(const AttnArgs 
         if (warp == 0) {
             int before = 0;
             for (int b0 = 0; b0 < nb; b0 += 32) {
-                int v = b0 + lane < nb ? (seq_of(a.bt, c0 + b0 + lane).n * a.G + rows - 1) / rows : 0;
+                int v = 0;
+                if (b0 + lane < nb) {
+                    const Seq s = seq_of(a.bt, c0 + b0 + lane);
+                    v = (s.n * a.G + rows - 1) / rows;
+                    if constexpr (MOD != MOD_PLAIN) seqs[b0 + lane] = s;
+                }
                 // q_start that decreases could list more tiles than the call's tokens make: counts stop there, and
                 // those past it are left out
                 v = min(v, max_tiles);
@@ -219,8 +228,12 @@ __global__ void __launch_bounds__(PLAN_THREADS) attn_plan_kernel(const AttnArgs 
                 if (r0) __syncthreads();
                 for (int x = r0 + warp; x < min(count, r0 + PLAN_THREADS); x += PLAN_THREADS / 32) {
                     const int b = sequence(x), row0 = (x - off[b]) * rows;
-                    const Seq s = seq_of(a.bt, c0 + b);
+                    const Seq s = seqs[b];
                     int from = s.len, end = 0;
+                    if (a.sh.tree && !a.window) {  // every slot
+                        if (lane == 0) range[x - r0] = make_int2(0, s.len);
+                        continue;
+                    }
                     for (int i = row0 / a.G + lane; i <= (min(row0 + rows, s.n * a.G) - 1) / a.G; i += 32) {
                         const Seen v = seen_by(a, s, c0 + b, i);
                         from = min(from, needs_from(a, s, v));
@@ -234,7 +247,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) attn_plan_kernel(const AttnArgs 
             }
             if (on) {
                 const int lo = sequence(r);
-                const Seq s = seq_of(a.bt, c0 + lo);
+                const Seq s = MOD == MOD_PLAIN ? seq_of(a.bt, c0 + lo) : seqs[lo];
                 t.b = c0 + lo;
                 t.row0 = (r - off[lo]) * rows;
                 t.first = s.first, t.n = s.n, t.len = s.len;
@@ -265,13 +278,13 @@ __global__ void __launch_bounds__(PLAN_THREADS) attn_plan_kernel(const AttnArgs 
             }
             // A single round of tiles: order them by falling cost and see how evenly whole items load the CTAs
             int place = at;
-            if (a.bt.batch <= PLAN_SEQS && count <= PLAN_THREADS) {
+            if (a.bt.batch <= PLAN_SEQS && count <= PLAN_ORDERED) {
                 const int mine = on ? t.nt + CHUNK_OV : 0;
-                unit[tid] = mine;
+                if (tid < PLAN_ORDERED) unit[tid] = mine;
                 __syncthreads();
                 int rank = 0;
 #pragma unroll 8
-                for (int i = 0; i < count; ++i) rank += unit[i] > mine || (unit[i] == mine && i < tid);
+                for (int i = 0; i < (on ? count : 0); ++i) rank += unit[i] > mine || (unit[i] == mine && i < tid);
                 if (on) sorted[rank] = mine;
                 __syncthreads();
                 const int items = count * a.Hk;
@@ -551,21 +564,22 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
                     mbar_wait(s_full(q, buf), (done / SB) & 1);
                     tc_fence_after();
                     uint32_t s[Cfg::HOLD ? BN / 32 : 1][32];
-                    auto mask = [&](uint32_t (&v)[32], int c0, uint32_t other) {  // what is not seen becomes `other`
-                        if (edge) {
-                            const int up = c_hi - c0, down = c_lo - c0;  // visible: down .. up
-                            uint32_t see = (up < 0 ? 0u : 0xffffffffu >> (31 - min(up, 31))) & (down > 31 ? 0u : 0xffffffffu << max(down, 0));
-                            if constexpr (MOD != MOD_PLAIN) {
-                                const int room = k.t.len - key0 - c0, old = pos0 - key0 - c0;  // slots in use, those before the new tokens
-                                if (tree && old < 32)
-                                    see |= tree_bits(tree, a.sh.words, -old) & (old > 0 ? 0xffffffffu << old : 0xffffffffu) & (room <= 0 ? 0u : 0xffffffffu >> (32 - min(room, 32)));
-                            }
-#pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                if (!(see >> i & 1u)) v[i] = other;
-                        }
-                    };
                     constexpr uint32_t HIDDEN = 0xff800000u;  // -inf
+                    auto hide = [&](uint32_t (&v)[32], int c0, uint32_t other) {  // what is not seen becomes `other`
+                        const int up = c_hi - c0, down = c_lo - c0;                   // visible: down .. up
+                        uint32_t see = (up < 0 ? 0u : 0xffffffffu >> (31 - min(up, 31))) & (down > 31 ? 0u : 0xffffffffu << max(down, 0));
+                        if constexpr (MOD != MOD_PLAIN) {
+                            const int room = k.t.len - key0 - c0, old = pos0 - key0 - c0;  // slots in use, those before the new tokens
+                            if (tree && old < 32)
+                                see |= tree_bits(tree, a.sh.words, -old) & (old > 0 ? 0xffffffffu << old : 0xffffffffu) & (room <= 0 ? 0u : 0xffffffffu >> (32 - min(room, 32)));
+                        }
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (!(see >> i & 1u)) v[i] = other;
+                    };
+                    auto mask = [&](uint32_t (&v)[32], int c0) {
+                        if (edge) hide(v, c0, HIDDEN);
+                    };
                     auto top = [&](const uint32_t (&v)[32]) {
                         float x[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -573,13 +587,25 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
                             x[(i / 2) & 3] = fmaxf(fmaxf(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), x[(i / 2) & 3]);
                         return fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
                     };
-                    // From S to the scores as powers of two's exponents, where these are no multiple of S
-                    auto capped = [&](uint32_t (&v)[32], int c0) {
-                        float far = 0.0f;
-                        mask(v, c0, 0u);  // whatever unseen slots hold chooses nothing
+                    // From S to the scores as powers of two's exponents, where these are no multiple of S: capped by what the row's
+                    // largest |S| allows (most, if not all, rows are below a quarter of the cap: three coefficients)
+                    float most = 0.0f;
+                    auto reach = [&](const uint32_t (&v)[32]) {
+                        float hi = 0.0f, lo = 0.0f;  // their maximum is there already, where nothing is masked
 #pragma unroll
-                        for (int i = 0; i < 32; i += 2) far = fmaxf(fmaxf(fabsf(__uint_as_float(v[i])), fabsf(__uint_as_float(v[i + 1]))), far);
-                        if (far * a.sh.cap_in > TANH_NEAR) {  // a row with scores around the cap: 1 - 2 / (1 + e^2x) is exact enough beside those
+                        for (int i = 0; i < 32; i += 2) {
+                            hi = fmaxf(fmaxf(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), hi);
+                            lo = fminf(fminf(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), lo);
+                        }
+                        most = fmaxf(most, fmaxf(hi, -lo));
+                    };
+                    auto small_cap = [&](uint64_t x) {  // the factor of S up to a quarter of the cap
+                        const uint64_t u = mul_f32x2(x, x);
+                        return fma_f32x2(u, fma_f32x2(u, pack_f32x2(a.sh.small[2], a.sh.small[2]), pack_f32x2(a.sh.small[1], a.sh.small[1])),
+                                         pack_f32x2(a.sh.small[0], a.sh.small[0]));
+                    };
+                    auto capped = [&](uint32_t (&v)[32]) {
+                        if (most * a.sh.cap_in > TANH_NEAR) {  // 1 - 2 / (1 + e^2x) is exact enough beside the row's largest
                             const float k = a.sh.cap_in * (2.0f * LOG2E), m2 = -2.0f * a.sh.cap_out;
 #pragma unroll
                             for (int i = 0; i < 32; ++i) {
@@ -601,26 +627,35 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
                             }
                         }
                     };
-                    auto bend = [&](uint32_t (&v)[32], int c0) {
-                        if constexpr (MOD == MOD_CAPPED) capped(v, c0);
-                        if constexpr (MOD == MOD_BIASED) {
+                    // MOD_BIASED, by tile: what is seen of it lies where its place says and behind the warp's rows, so that the bias is
+                    // linear, without a cap (LINEAR) or with one far from the scores (LINEAR_CAP); else GENERAL
+                    enum { GENERAL, LINEAR, LINEAR_CAP };
+                    auto bend = [&](uint32_t (&v)[32], int c0, auto kind) {
+                        constexpr int KIND = decltype(kind)::value;
+                        const int key = key0 + c0;
+                        const float d = (float)(row_pos - key);
+                        if constexpr (KIND != GENERAL) {
+                            // the bias of every eighth slot is the last one's and 8 slopes: three sums, half an instruction each
+                            const uint64_t in2 = pack_f32x2(a.scale2, a.scale2), step = pack_f32x2(8.0f * slope, 8.0f * slope);
+                            uint64_t at[4];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) at[i] = pack_f32x2(-slope * (d - (float)(2 * i)), -slope * (d - (float)(2 * i + 1)));
+#pragma unroll
+                            for (int i = 0; i < 32; i += 2) {
+                                uint64_t &b = at[(i / 2) & 3];
+                                const uint64_t x = pack_b32x2(v[i], v[i + 1]), y = fma_f32x2(x, KIND == LINEAR_CAP ? small_cap(x) : in2, b);
+                                if (i < 24) b = add_f32x2(b, step);
+                                float y0, y1;
+                                unpack_f32x2(y, y0, y1);
+                                v[i] = __float_as_uint(y0), v[i + 1] = __float_as_uint(y1);
+                            }
+                        } else if constexpr (MOD == MOD_BIASED) {
                             float in = a.scale2;
                             if (a.sh.cap_out > 0.0f) {
-                                capped(v, c0);
+                                capped(v);
                                 in = 1.0f;
                             }
-                            const int key = key0 + c0;
-                            const float d = (float)(row_pos - key);
-                            if (!a.sh.prefix && !a.sh.positions) {  // what is ahead of the row is not seen: no sign to take off
-                                const uint64_t in2 = pack_f32x2(in, in), s2 = pack_f32x2(slope, slope), d2 = pack_f32x2(-slope * d, -slope * d);
-#pragma unroll
-                                for (int i = 0; i < 32; i += 2) {
-                                    const uint64_t y = fma_f32x2(pack_b32x2(v[i], v[i + 1]), in2, fma_f32x2(s2, pack_f32x2((float)i, (float)(i + 1)), d2));
-                                    float y0, y1;
-                                    unpack_f32x2(y, y0, y1);
-                                    v[i] = __float_as_uint(y0), v[i + 1] = __float_as_uint(y1);
-                                }
-                            } else if (a.sh.positions && key + 32 > pos0) {  // new tokens are where the caller says
+                            if (a.sh.positions && key + 32 > pos0) {  // new tokens are where the caller says
 #pragma unroll
                                 for (int i = 0; i < 32; ++i)
                                     v[i] = __float_as_uint(fmaf(__uint_as_float(v[i]), in,
@@ -631,7 +666,37 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
                             }
                         }
                     };
+                    // Chunks of 32 scores, all of them held or one at a time
+                    auto load = [&](int c) {
+                        if constexpr (!Cfg::HOLD) {
+                            tmem_ld32(scol + 32 * c, s[0]);
+                            tmem_wait_ld(s[0]);
+                        }
+                    };
+                    auto each = [&](auto &&step) {
+#pragma unroll (Cfg::HOLD ? BN / 32 : 1)
+                        for (int c = 0; c < BN / 32; ++c) {
+                            load(c);
+                            step(s[Cfg::HOLD ? c : 0], 32 * c);
+                        }
+                    };
                     float mx = -INFINITY;
+                    // The row's maximum.  Kinds of tiles have loops of their own: a branch per 32 scores keeps the
+                    // compiler from running one chunk's steps under another's (2048 tokens after 6000, dim 128, capped: 360 us)
+                    auto largest = [&](auto kind, auto is_edge) {
+                        each([&](uint32_t (&v)[32], int c0) {
+                            if constexpr (MOD == MOD_CAPPED) {
+                                if constexpr (decltype(is_edge)::value) hide(v, c0, 0u);  // whatever unseen slots hold chooses nothing
+                                reach(v);
+                            }
+                            bend(v, c0, kind);
+                            if constexpr (decltype(is_edge)::value) hide(v, c0, HIDDEN);
+                            mx = fmaxf(mx, top(v));
+                        });
+                    };
+                    using General = std::integral_constant<int, GENERAL>;
+                    using Linear = std::integral_constant<int, LINEAR>;
+                    using LinearCap = std::integral_constant<int, LINEAR_CAP>;
                     if constexpr (Cfg::HOLD) {
 #pragma unroll
                         for (int c = 0; c < BN / 32; ++c) tmem_ld32(scol + 32 * c, s[c]);
@@ -640,24 +705,45 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
                         for (int c = 1; c < BN / 32; ++c) tmem_loaded(s[c]);
                         tc_fence_before();
                         mbar_arrive(s_empty(q));  // P has columns of its own here
-#pragma unroll
-                        for (int c = 0; c < BN / 32; ++c) {
-                            bend(s[c], 32 * c);
-                            mask(s[c], 32 * c, HIDDEN);
-                            mx = fmaxf(mx, top(s[c]));
-                        }
-                    } else {
-                        constexpr bool late = MOD == MOD_CAPPED;  // a cap alone keeps the order: bend the maximum
-#pragma unroll 1
-                        for (int c = 0; c < BN / 32; ++c) {
-                            tmem_ld32(scol + 32 * c, s[0]);
-                            tmem_wait_ld(s[0]);
-                            if (!late) bend(s[0], 32 * c);
-                            mask(s[0], 32 * c, HIDDEN);
-                            mx = fmaxf(mx, top(s[0]));
-                        }
-                        if (late && mx != -INFINITY) mx = a.sh.cap_out * tanh_any(mx * a.sh.cap_in);
                     }
+                    int kind = GENERAL;
+                    if constexpr (!bent) {
+                        each([&](uint32_t (&v)[32], int c0) {
+                            mask(v, c0);
+                            mx = fmaxf(mx, top(v));
+                        });
+                    } else if constexpr (MOD == MOD_CAPPED) {
+                        if (!edge)
+                            largest(General{}, std::false_type{});
+                        else
+                            largest(General{}, std::true_type{});
+                    } else {
+                        if (a.sh.cap_out > 0.0f) {
+                            if (!edge)
+                                each([&](uint32_t (&v)[32], int) { reach(v); });
+                            else
+                                each([&](uint32_t (&v)[32], int c0) {
+                                    hide(v, c0, 0u);
+                                    reach(v);
+                                });
+                        }
+                        if (!(a.sh.positions && key0 + BN > pos0) && __all_sync(0xffffffffu, row_pos >= min(hi, key0 + BN - 1)))
+                            kind = a.sh.cap_out == 0.0f ? LINEAR : __any_sync(0xffffffffu, most > a.sh.small_to) ? GENERAL : LINEAR_CAP;
+                        if (kind == LINEAR && !edge)
+                            largest(Linear{}, std::false_type{});
+                        else if (kind == LINEAR)
+                            largest(Linear{}, std::true_type{});
+                        else if (kind == LINEAR_CAP && !edge)
+                            largest(LinearCap{}, std::false_type{});
+                        else if (kind == LINEAR_CAP)
+                            largest(LinearCap{}, std::true_type{});
+                        else if (!edge)
+                            largest(General{}, std::false_type{});
+                        else
+                            largest(General{}, std::true_type{});
+                    }
+                    if constexpr (MOD == MOD_CAPPED)  // a cap keeps the order: the maximum is bent alone
+                        if (mx != -INFINITY) mx = a.sh.cap_out * tanh_any(mx * a.sh.cap_in);
                     if (!Cfg::P_OVER && done > 0) {  // P's place is free again
                         mbar_wait(pv_done(q, 0), (done - 1) & 1);
                         tc_fence_after();
@@ -693,9 +779,7 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
                     // ---- P: chunk c of 32 scores becomes columns (words of a row) 16 c .. 16 c + 15
                     const uint64_t sc2 = pack_f32x2(sc, sc), mz2 = pack_f32x2(-mz, -mz);
                     uint64_t sum[2] = {0ull, 0ull};
-#pragma unroll (Cfg::HOLD ? BN / 32 : 1)
-                    for (int c = 0; c < BN / 32; ++c) {
-                        uint32_t(&v)[32] = s[Cfg::HOLD ? c : 0];
+                    auto chunk = [&](int c, uint32_t(&v)[32], auto is_small) {
                         if constexpr (!Cfg::HOLD) {
                             tmem_ld32(scol + 32 * c, v);
                             tmem_wait_ld(v);
@@ -703,15 +787,28 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
                                 tc_fence_before();
                                 mbar_arrive(s_empty(q));
                             }
-                            bend(v, 32 * c);
-                            mask(v, 32 * c, HIDDEN);
+                            if constexpr (MOD == MOD_BIASED) {
+                                if (kind == LINEAR)
+                                    bend(v, 32 * c, Linear{});
+                                else if (kind == LINEAR_CAP)
+                                    bend(v, 32 * c, LinearCap{});
+                                else
+                                    bend(v, 32 * c, General{});
+                            }
+                            mask(v, 32 * c);
+                        }
+                        if constexpr (MOD == MOD_CAPPED && !decltype(is_small)::value) {
+                            capped(v);
+                            mask(v, 32 * c);
                         }
                         uint32_t p[16];
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
-                            const uint64_t x = fma_f32x2(pack_b32x2(v[2 * i], v[2 * i + 1]), sc2, mz2);
+                            const uint64_t y = pack_b32x2(v[2 * i], v[2 * i + 1]);
+                            uint64_t w = sc2;
+                            if constexpr (decltype(is_small)::value) w = small_cap(y);
                             float x0, x1;
-                            unpack_f32x2(x, x0, x1);
+                            unpack_f32x2(fma_f32x2(y, w, mz2), x0, x1);
                             x0 = exp2_approx(x0);
                             x1 = exp2_approx(x1);
                             sum[i & 1] = add_f32x2(sum[i & 1], pack_f32x2(x0, x1));
@@ -723,6 +820,30 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
                             tc_fence_before();
                             mbar_arrive(p_half(q, buf));
                         }
+                    };
+                    auto all = [&](auto is_small) {
+                        if constexpr (Cfg::HOLD && MOD != MOD_PLAIN && MOD != MOD_SHAPED) {
+                            // two chunks in the code, the other two moved into their place
+#pragma unroll 1
+                            for (int c = 0; c < BN / 32; c += 2) {
+                                chunk(c, s[0], is_small);
+                                chunk(c + 1, s[1], is_small);
+#pragma unroll
+                                for (int i = 0; i < 32; ++i) s[0][i] = s[2][i], s[1][i] = s[3][i];
+                            }
+                        } else {
+#pragma unroll (Cfg::HOLD ? BN / 32 : 1)
+                            for (int c = 0; c < BN / 32; ++c) chunk(c, s[Cfg::HOLD ? c : 0], is_small);
+                        }
+                    };
+                    if constexpr (MOD == MOD_CAPPED) {
+                        // rows whose scores stay below a quarter of the cap, as most do: three coefficients, and no products beside those of the exponents
+                        if (!__any_sync(0xffffffffu, most > a.sh.small_to))
+                            all(std::true_type{});
+                        else
+                            all(std::false_type{});
+                    } else {
+                        all(std::false_type{});
                     }
                     float l0, l1, l2, l3;
                     unpack_f32x2(sum[0], l0, l1);
@@ -1243,6 +1364,16 @@ static int chunk_run(const AttnArgs &in, const qg_paged &c, int sms, cudaStream_
     a.sh.cap_in = std::abs(a.sh.cap_in);
     constexpr float fit[5] = {TANH_C0, TANH_C1, TANH_C2, TANH_C3, TANH_C4};
     for (int i = 0; i < 5; ++i) a.sh.poly[i] = fit[i] * a.sh.cap_out;
+    constexpr float near[3] = {TANH_S0, TANH_S1, TANH_S2};
+    a.sh.small_to = -1.0f;
+    if (a.sh.cap_out > 0.0f) {
+        const double in = a.sh.cap_in, last = near[2] * (double)a.sh.cap_out * std::pow(in, 5);
+        // powers of S up to the fifth and these are well inside fp32's range, or the form in x is taken
+        if (in > 1e-7 && in < 1e5 && last > 1e-36 && last < 1e30) {
+            for (int i = 0; i < 3; ++i) a.sh.small[i] = (float)(near[i] * (double)a.sh.cap_out * std::pow(in, 2 * i + 1));
+            a.sh.small_to = TANH_SMALL / a.sh.cap_in;
+        }
+    }
     a.scale_p2 = std::exp2(std::floor(std::log2(a.scale2)));
     const int box = gcd(c.page, Cfg::VR);
     CUtensorMap km{}, vm{};
@@ -1251,7 +1382,7 @@ static int chunk_run(const AttnArgs &in, const qg_paged &c, int sms, cudaStream_
     if (qcopy && !attn_query_map(&qm, a, c.type == QG_BF16, D)) return QG_ECUDA;
     if (!attn_tensor_map(&km, c, c.k, box) || !attn_tensor_map(&vm, c, c.v, box)) return QG_ECUDA;
     if (!chunk_ready<C, D, MOD>()) return QG_ECUDA;
-    if (!launch_programmatic(attn_plan_kernel<MOD>, dim3(1), PLAN_THREADS, 0, s, a, plan, Cfg::ROWS, Cfg::BN, (int)tiles, sms)) return QG_ECUDA;
+    if (!launch_programmatic(attn_plan_kernel<MOD>, dim3(1), plan_threads(MOD), 0, s, a, plan, Cfg::ROWS, Cfg::BN, (int)tiles, sms)) return QG_ECUDA;
     auto kern = attn_chunk_kernel<C, D, MOD>;
     if (!launch_programmatic(kern, dim3((unsigned)sms), Cfg::THREADS, Cfg::BYTES, s, a, plan, box, qsign, (int)qcopy, km, vm, qm)) return QG_ECUDA;
     auto join = attn_chunk_join_kernel<T, D>;

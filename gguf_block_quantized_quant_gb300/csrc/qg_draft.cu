@@ -139,30 +139,37 @@ __global__ void __launch_bounds__(KEEP_THREADS) keep_lengths_kernel(const KeepAr
 }
 
 // ----------------------------------------------------------------------------- logits
-// A block takes a segment of a few rows, one after the other.  It counts the ids of the segment that the row's history and drafts
-// hold in shared memory (a word per id: the count, bit 31 for ids of the prompt) and notes the last bias entry of each
-// id there; rows of one sequence share that, but for their drafts, which are added before a row and taken off after it.  The logits
-// are on their way to registers meanwhile.  Whole numbers are added, so the order of the atomics changes nothing.
-// Bound by memory: the logits are read and written once; what hides the chain of dependent loads before them (sequence,
-// lengths, ids) are the other blocks of the SM.
+// A block takes a segment of ids for a few rows.  For each sequence among them it counts the ids of the segment that the history
+// holds in shared memory (a word per id), notes the last bias entry of each, and lists the ids so touched; the drafts that each
+// row follows, few or none of which fall into a segment, are listed per row.  The logits of all its rows stream past the mask
+// without a barrier, and the listed ids go over that.  Whole numbers are added, so the order of the atomics changes
+// nothing but the lists'.
+// Bound by memory: the logits are read and written once.  What has to be hidden is the chain of dependent loads before the
+// listed ids (sequence, lengths, ids, logits): other blocks of the SM do, and rows of one sequence share it.  Measured and dropped for
+// 192 rows of 131071, bf16 to fp32: a row at a time with its counts beside the stream, 97 us, with a list 108.
 struct LogitsArgs {
     const void *x;
     void *out;
     int64_t ld, ldo;  // elements
-    int V, seg;       // seg: ids of a segment, a multiple of 128
+    int V, seg;       // seg: ids of a segment, a multiple of 8
     int rows, group;  // group: rows of a block
     int in_place, has_bias;
     qg_logits how;
 };
 
-constexpr int LOGITS_THREADS = 256, LOGITS_U = 4, LOGITS_SEG = LOGITS_THREADS * LOGITS_U * 4;
+constexpr int LOGITS_HISTORY = 1 << 29;  // ids of a history that count; with the drafts below TIMES
+constexpr int LOGITS_THREADS = 256, LOGITS_U = 4, LOGITS_SEG = 4096, LOGITS_GROUP = 16;
+constexpr int LOGITS_PATH = 30;          // drafts of a row in a segment that are listed; where there are more, all are looked through
+
+// A word of the counts: how often the id was said after the prompt, that it was said before, that it has a bias.  No id
+// whose word is 0 is listed.
+constexpr uint32_t SAID = 0x80000000u, BIASED = 0x40000000u, TIMES = 0x3fffffffu;
 
 // Four elements as they come.
 template <class T>
 struct Raw4 {
     uint2 w;
     __device__ __forceinline__ void load(const T *p) { w = *reinterpret_cast<const uint2 *>(p); }
-    __device__ __forceinline__ void set(int k, T x) { reinterpret_cast<T *>(&w)[k] = x; }
     __device__ __forceinline__ void get(float (&v)[4]) const {
         const float2 a = unpack2<T>(w.x), b = unpack2<T>(w.y);
         v[0] = a.x, v[1] = a.y, v[2] = b.x, v[3] = b.y;
@@ -172,177 +179,200 @@ template <>
 struct Raw4<float> {
     float4 w;
     __device__ __forceinline__ void load(const float *p) { w = *reinterpret_cast<const float4 *>(p); }
-    __device__ __forceinline__ void set(int k, float x) { reinterpret_cast<float *>(&w)[k] = x; }
     __device__ __forceinline__ void get(float (&v)[4]) const { v[0] = w.x, v[1] = w.y, v[2] = w.z, v[3] = w.w; }
 };
 
+// The row's bit of id v, and four from it on (v + 3 < V).
+__device__ __forceinline__ uint32_t allowed(const uint32_t *row, int v) { return row[v >> 5] >> (v & 31) & 1u; }
+__device__ __forceinline__ uint32_t allowed4(const uint32_t *row, int v) { return __funnelshift_r(row[v >> 5], row[(v + 3) >> 5], v & 31) & 15u; }
+
+// Ids id0 .. id1 - 1 of a row, past the mask.
 template <class I, class O>
-__global__ void __launch_bounds__(LOGITS_THREADS, 4) logits_kernel(const LogitsArgs a) {
-    extern __shared__ __align__(16) uint32_t lg_smem[];
-    uint32_t *count = lg_smem;
-    uint32_t *mask = count + a.seg;       // seg / 32 words
-    uint32_t *entry = mask + a.seg / 32;  // seg words, where there are biases
+__device__ __forceinline__ void logits_stream(const LogitsArgs &a, int row, int id0, int id1) {
     const int tid = threadIdx.x;
-    const int segs = (a.V + 3 + a.seg - 1) / a.seg;
-    const int row0 = (int)(blockIdx.x / segs) * a.group, row1 = min(row0 + a.group, a.rows);
-    const int p0 = (int)(blockIdx.x % segs) * a.seg;
-    griddep_wait();
-    griddep_launch_dependents();
-
-    int held = -2, held_ids0 = 0;  // the sequence (-1: none) whose ids are counted, and the segment's first id then
-    float rep = 1.0f, freq = 0.0f, pres = 0.0f;
-    const float *bias = nullptr;
-    for (int row = row0; row < row1; ++row) {
-        const I *x = static_cast<const I *>(a.x) + row * a.ld;
-        O *out = static_cast<O *>(a.out) + row * a.ldo;
-        // Places of a row are counted from the boundary of 4 elements before its start in `out`; id v is at place v + lead
-        const int lead = (int)((reinterpret_cast<uintptr_t>(out) / sizeof(O)) & 3);
-        const bool vec = (reinterpret_cast<uintptr_t>(x) / sizeof(I) & 3) == lead;
-        const int ids0 = p0 - lead;                 // the segment's first id (below 0 in the first)
-        const int n = min(a.seg, a.V + lead - p0);  // places of it up to the row's end
-        if (n <= 0) continue;                       // the last row's lead may need a segment that this one's does not
-        const int s = a.how.seq ? a.how.seq[row] : row;
-        const bool known = (unsigned)s < (unsigned)a.how.batch;
-        const bool in_place = std::is_same<I, O>::value && a.in_place;
-        auto whole = [&](int q) { return vec && ids0 + 4 * q >= 0 && 4 * q + 4 <= n; };
-        auto fetch = [&](Raw4<I> &v, int q) {
-            const int id = ids0 + 4 * q;
-            if (whole(q)) {
-                v.load(x + id);
-            } else {
-#pragma unroll
-                for (int k = 0; k < 4; ++k) v.set(k, id + k >= 0 && 4 * q + k < n ? x[id + k] : from_f32<I>(0.0f));
-            }
-        };
-        Raw4<I> v[LOGITS_U];
-        if (!in_place) {
-#pragma unroll
-            for (int u = 0; u < LOGITS_U; ++u)
-                if (4 * (tid + u * LOGITS_THREADS) < n) fetch(v[u], tid + u * LOGITS_THREADS);
-        }
-        if (a.how.allow) {
-            const uint32_t *allow = a.how.allow + row * a.how.allow_stride;
-            const int words = (a.V + 31) / 32;
-            for (int i = tid; i < a.seg / 32; i += LOGITS_THREADS) {
-                const int at = ids0 + 32 * i, w = at >> 5;  // at may be below 0
-                const uint32_t lo = w >= 0 && w < words ? allow[w] : 0u, hi = w + 1 < words ? allow[w + 1] : 0u;
-                mask[i] = __funnelshift_r(lo, hi, at & 31);
-            }
-        }
-        auto place = [&](int id) { return (unsigned)id < (unsigned)a.V ? id - ids0 : -1; };
-        const bool fresh = (known ? s : -1) != held || ids0 != held_ids0;
-        if (fresh) {
-            held = known ? s : -1;
-            held_ids0 = ids0;
-            for (int i = tid; i < a.seg / 4; i += LOGITS_THREADS) reinterpret_cast<uint4 *>(count)[i] = make_uint4(0, 0, 0, 0);
-            if (a.has_bias)
-                for (int i = tid; i < a.seg / 4; i += LOGITS_THREADS) reinterpret_cast<uint4 *>(entry)[i] = make_uint4(0, 0, 0, 0);
-            rep = 1.0f, freq = pres = 0.0f;
-            int len = 0, said = 0, start = 0, entries = 0;
-            if (known) {
-                if (a.how.repetition) rep = a.how.repetition[s];
-                if (a.how.frequency) freq = a.how.frequency[s];
-                if (a.how.presence) pres = a.how.presence[s];
-                if (a.how.history) {
-                    len = min(max(a.how.history_len[s], 0), min(a.how.history_width, 1 << 30));
-                    said = a.how.prompt_len ? a.how.prompt_len[s] : 0;
-                }
-                if (a.has_bias) {
-                    start = min(max(a.how.bias_start[s], 0), a.how.bias_entries);
-                    entries = min(a.how.bias_start[s + 1], a.how.bias_entries) - start;
-                    bias = a.how.bias + start;
-                }
-            }
-            __syncthreads();
-            const int32_t *h = a.how.history + s * a.how.history_stride;
-            auto add = [&](int id, int i) {
-                const int at = place(id);
-                if ((unsigned)at >= (unsigned)n) return;
-                if (i < said)
-                    atomicOr(count + at, 0x80000000u);
-                else
-                    atomicAdd(count + at, 1u);
-            };
-            const int head = min(len, (int)(-(reinterpret_cast<intptr_t>(h) / 4) & 3)), quads = (len - head) / 4;
-            if (tid < head) add(h[tid], tid);
-#pragma unroll 4
-            for (int i = tid; i < quads; i += LOGITS_THREADS) {
-                const int4 w = reinterpret_cast<const int4 *>(h + head)[i];
-                const int at = head + 4 * i;
-                add(w.x, at), add(w.y, at + 1), add(w.z, at + 2), add(w.w, at + 3);
-            }
-            const int tail = head + 4 * quads + tid;
-            if (tail < len) add(h[tail], tail);
-            for (int i = tid; i < entries; i += LOGITS_THREADS) {
-                const int at = place(a.how.bias_ids[start + i]);
-                if ((unsigned)at < (unsigned)n) atomicMax(entry + at, (uint32_t)i + 1u);
-            }
-        }
-        auto path = [&](uint32_t by) {  // the row's drafts
-            if (!known || !a.how.drafts) return;
-            const int first = min(max(a.how.q_start[s], 0), a.rows), drafts = min(max(a.how.q_start[s + 1], 0), a.rows) - first;
-            const int bits = (int)min((int64_t)drafts, (int64_t)32 * a.how.words);
-            const uint32_t *tree = a.how.tree + (int64_t)row * a.how.words;
-            for (int i = tid; i < bits; i += LOGITS_THREADS)
-                if (tree[i >> 5] >> (i & 31) & 1) {
-                    const int at = place(a.how.drafts[first + i]);
-                    if ((unsigned)at < (unsigned)n) atomicAdd(count + at, by);
-                }
-        };
-        path(1u);
-        __syncthreads();
-
-        auto adjust = [&](float y, uint32_t c, uint32_t e) {
-            if (e) y += bias[e - 1];
-            if (c) {
-                y = y > 0.0f ? __fdiv_rn(y, rep) : y * rep;
-                const uint32_t times = c & 0x7fffffffu;
-                if (times) y = fmaf(-freq, (float)times, y) - pres;
-            }
-            return y;
-        };
+    const I *x = static_cast<const I *>(a.x) + row * a.ld;
+    O *out = static_cast<O *>(a.out) + row * a.ldo;
+    const uint32_t *allow = a.how.allow ? a.how.allow + row * a.how.allow_stride : nullptr;
+    const bool in_place = std::is_same<I, O>::value && a.in_place;
+    if (in_place && !allow) return;
+    auto one = [&](int v) {
+        const bool ok = !allow || allowed(allow, v);
+        if (!(in_place && ok)) out[v] = ok ? from_f32<O>(to_f32(x[v])) : from_f32<O>(-INFINITY);
+    };
+    // vectors start where four elements of `out` do; x has to be at the same place between its own boundaries
+    const int lead = (int)((reinterpret_cast<uintptr_t>(out + id0) / sizeof(O)) & 3);
+    if ((int)((reinterpret_cast<uintptr_t>(x + id0) / sizeof(I)) & 3) != lead) {
+        for (int v = id0 + tid; v < id1; v += LOGITS_THREADS) one(v);
+        return;
+    }
+    const int head = min((4 - lead) & 3, id1 - id0), quads = (id1 - id0 - head) / 4, v0 = id0 + head, left = id1 - v0 - 4 * quads;
+    if (tid < head) one(id0 + tid);
+    if (tid < left) one(id1 - left + tid);
+    for (int q0 = tid; q0 < quads; q0 += LOGITS_THREADS * LOGITS_U) {
+        Raw4<I> r[LOGITS_U];
+        uint32_t ok[LOGITS_U];
 #pragma unroll
         for (int u = 0; u < LOGITS_U; ++u) {
-            const int q = tid + u * LOGITS_THREADS, at = 4 * q, id = ids0 + at;
-            if (at >= n) break;
-            const uint4 c = reinterpret_cast<const uint4 *>(count)[q];
-            const uint4 e = a.has_bias ? reinterpret_cast<const uint4 *>(entry)[q] : make_uint4(0, 0, 0, 0);
-            const uint32_t ok = a.how.allow ? mask[at >> 5] >> (at & 31) & 15u : 15u;
-            const bool touched = (c.x | c.y | c.z | c.w | e.x | e.y | e.z | e.w) != 0;
-            if (in_place) {
-                if (ok == 15u && !touched) continue;
-                if (ok != 0u || !whole(q)) fetch(v[u], q);
-            }
+            const int q = q0 + u * LOGITS_THREADS, v = v0 + 4 * q;
+            if (q >= quads) continue;
+            ok[u] = allow ? allowed4(allow, v) : 15u;
+            if (!in_place || (ok[u] != 0u && ok[u] != 15u)) r[u].load(x + v);
+        }
+#pragma unroll
+        for (int u = 0; u < LOGITS_U; ++u) {
+            const int q = q0 + u * LOGITS_THREADS;
+            if (q >= quads || (in_place && ok[u] == 15u)) continue;
             float y[4];
-            v[u].get(y);
-            if (touched) {
-                y[0] = adjust(y[0], c.x, e.x), y[1] = adjust(y[1], c.y, e.y);
-                y[2] = adjust(y[2], c.z, e.z), y[3] = adjust(y[3], c.w, e.w);
+            r[u].get(y);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) y[k] = ok[u] >> k & 1 ? y[k] : -INFINITY;
+            store_vec<O, 4>(out + v0 + 4 * q, y);
+        }
+    }
+}
+
+template <class I, class O>
+__global__ void __launch_bounds__(LOGITS_THREADS, 5) logits_kernel(const __grid_constant__ LogitsArgs a) {
+    extern __shared__ __align__(16) uint32_t lg_smem[];
+    __shared__ int touched, seqs[LOGITS_GROUP], paths[LOGITS_GROUP];
+    __shared__ uint16_t path[LOGITS_GROUP][LOGITS_PATH];
+    uint32_t *count = lg_smem;
+    uint32_t *entry = count + a.seg;                                                       // where there are biases
+    uint16_t *list = reinterpret_cast<uint16_t *>(entry + (a.has_bias ? a.seg : 0));
+    const int tid = threadIdx.x;
+    const int segs = (int)(((int64_t)a.V + a.seg - 1) / a.seg);
+    const int row0 = (int)(blockIdx.x / segs) * a.group, rows = min(a.group, a.rows - row0);
+    const int id0 = (int)(blockIdx.x % segs) * a.seg, id1 = min(id0 + a.seg, a.V), n = id1 - id0;
+    griddep_wait();
+    griddep_launch_dependents();
+    if (tid < rows) {
+        const int s = a.how.seq ? a.how.seq[row0 + tid] : row0 + tid;
+        seqs[tid] = (unsigned)s < (unsigned)a.how.batch ? s : -1;
+    }
+    for (int i = tid; i < a.seg / 4; i += LOGITS_THREADS) reinterpret_cast<uint4 *>(count)[i] = make_uint4(0, 0, 0, 0);
+    if (a.has_bias)
+        for (int i = tid; i < a.seg / 4; i += LOGITS_THREADS) reinterpret_cast<uint4 *>(entry)[i] = make_uint4(0, 0, 0, 0);
+    if (tid < LOGITS_GROUP) paths[tid] = 0;
+    if (tid == 0) touched = 0;
+    __syncthreads();
+
+    for (int r0 = 0, r1; r0 < rows; r0 = r1) {  // rows r0 .. r1 - 1 of the block belong to sequence s
+        const int s = seqs[r0];
+        for (r1 = r0 + 1; r1 < rows && seqs[r1] == s; ++r1) {}
+        auto listed = [&](int at, uint32_t before) {
+            if (before == 0) list[atomicAdd(&touched, 1)] = (uint16_t)at;
+        };
+        const float *bias = nullptr;
+        float rep = 1.0f, freq = 0.0f, pres = 0.0f;
+        int first = 0, bits = 0;  // of the sequence's drafts
+        if (s >= 0) {
+            if (a.how.repetition) rep = a.how.repetition[s];
+            if (a.how.frequency) freq = a.how.frequency[s];
+            if (a.how.presence) pres = a.how.presence[s];
+            if (a.how.drafts) {
+                first = min(max(a.how.q_start[s], 0), a.rows);
+                bits = (int)min((int64_t)(min(max(a.how.q_start[s + 1], 0), a.rows) - first), (int64_t)32 * a.how.words);
             }
-#pragma unroll
-            for (int k = 0; k < 4; ++k) y[k] = ok >> k & 1 ? y[k] : -INFINITY;
-            if (whole(q)) {
-                store_vec<O, 4>(out + id, y);
-            } else {
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    if (id + k >= 0 && at + k < n) out[id + k] = from_f32<O>(y[k]);
+            int start = 0, entries = 0;
+            if (a.has_bias) {
+                start = min(max(a.how.bias_start[s], 0), a.how.bias_entries);
+                entries = min(a.how.bias_start[s + 1], a.how.bias_entries) - start;
+                bias = a.how.bias + start;
+            }
+            if (a.how.history) {
+                const int len = min(max(a.how.history_len[s], 0), min(a.how.history_width, LOGITS_HISTORY));
+                const int said = a.how.prompt_len ? a.how.prompt_len[s] : 0;
+                const int32_t *h = a.how.history + s * a.how.history_stride;
+                auto add = [&](int id, int i) {
+                    const unsigned at = (unsigned)id - (unsigned)id0;  // ids below 0 are far away
+                    if (at < (unsigned)n) listed((int)at, i < said ? atomicOr(count + at, SAID) : atomicAdd(count + at, 1u));
+                };
+                const int head = min(len, (int)(-(reinterpret_cast<intptr_t>(h) / 4) & 3)), quads = (len - head) / 4;
+                if (tid < head) add(h[tid], tid);
+#pragma unroll 4
+                for (int i = tid; i < quads; i += LOGITS_THREADS) {
+                    const int4 w = reinterpret_cast<const int4 *>(h + head)[i];
+                    const int at = head + 4 * i;
+                    add(w.x, at), add(w.y, at + 1), add(w.z, at + 2), add(w.w, at + 3);
+                }
+                const int tail = head + 4 * quads + tid;
+                if (tail < len) add(h[tail], tail);
+            }
+            for (int i = tid; i < entries; i += LOGITS_THREADS) {
+                const unsigned at = (unsigned)a.how.bias_ids[start + i] - (unsigned)id0;
+                if (at >= (unsigned)n) continue;
+                listed((int)at, atomicOr(count + at, BIASED));
+                atomicMax(entry + at, (uint32_t)i + 1u);
             }
         }
-        if (row + 1 < row1) {
+        // the drafts that row r0 + r of the block follows: bit i, its place in the segment (or beyond it)
+        auto follows = [&](int r, int i) { return a.how.tree[(int64_t)(row0 + r) * a.how.words + (i >> 5)] >> (i & 31) & 1u; };
+        auto draft = [&](int i) { return (unsigned)a.how.drafts[first + i] - (unsigned)id0; };
+        for (int64_t x = tid; x < (int64_t)(r1 - r0) * bits; x += LOGITS_THREADS) {
+            const int r = r0 + (int)(x / bits), i = (int)(x % bits);
+            const unsigned at = draft(i);
+            if (follows(r, i) && at < (unsigned)n) {
+                const int k = atomicAdd(&paths[r], 1);
+                if (k < LOGITS_PATH) path[r][k] = (uint16_t)at;
+            }
+        }
+        if (r0 == 0)
+            for (int r = 0; r < rows; ++r) logits_stream<I, O>(a, row0 + r, id0, id1);
+        __syncthreads();  // what is listed goes over what the stream wrote
+
+        auto put = [&](int r, unsigned at, uint32_t c) {  // c: the id's word with the row's drafts
+            const int row = row0 + r, id = id0 + (int)at;
+            if (a.how.allow && !allowed(a.how.allow + row * a.how.allow_stride, id)) return;
+            float y = to_f32(static_cast<const I *>(a.x)[row * a.ld + id]);
+            if (c & BIASED) y += bias[entry[at] - 1];
+            if (c & ~BIASED) y = y > 0.0f ? __fdiv_rn(y, rep) : y * rep;
+            if (c & TIMES) y = fmaf(-freq, (float)(c & TIMES), y) - pres;
+            static_cast<O *>(a.out)[row * a.ldo + id] = from_f32<O>(y);
+        };
+        auto times = [&](int r, unsigned at) {  // how often the row's drafts say the id
+            uint32_t k = 0;
+            if (paths[r] <= LOGITS_PATH) {
+                for (int i = 0; i < paths[r]; ++i) k += path[r][i] == at;
+            } else {
+                for (int i = 0; i < bits; ++i) k += follows(r, i) && draft(i) == at;
+            }
+            return k;
+        };
+        const int ids = touched;
+        for (int r = r0; r < r1; ++r) {
+            for (int i = tid; i < ids; i += LOGITS_THREADS) {
+                const unsigned at = list[i];
+                put(r, at, count[at] + times(r, at));
+            }
+            // ids that the row's drafts alone say: each once, at its first place
+            const bool all = paths[r] > LOGITS_PATH;
+            const int most = all ? bits : paths[r];
+            for (int i = tid; i < most; i += LOGITS_THREADS) {
+                const unsigned at = all ? draft(i) : path[r][i];
+                if (at >= (unsigned)n || count[at] != 0 || (all && !follows(r, i))) continue;
+                bool again = false;
+                for (int k = 0; k < i && !again; ++k) again = all ? follows(r, k) && draft(k) == at : path[r][k] == at;
+                if (!again) put(r, at, times(r, at));
+            }
+        }
+        if (r1 < rows) {  // another sequence
             __syncthreads();
-            path(0xffffffffu);  // off again
-            if (a.how.drafts) __syncthreads();
+            for (int i = tid; i < ids; i += LOGITS_THREADS) {
+                count[list[i]] = 0u;
+                if (a.has_bias) entry[list[i]] = 0u;
+            }
+            if (tid == 0) touched = 0;
+            __syncthreads();
         }
     }
 }
 
 // Segments of a row, and whether they and the rows are counted in 32 bits.
-static int64_t logits_segments(int V, int seg) { return ((int64_t)V + 3 + seg - 1) / seg; }
+static int64_t logits_segments(int V, int seg) { return ((int64_t)V + seg - 1) / seg; }
 
 template <class I, class O>
 static int logits_launch(const LogitsArgs &a, cudaStream_t s) {
-    const uint32_t bytes = (uint32_t)a.seg * (a.has_bias ? 8 : 4) + a.seg / 8;
+    const uint32_t bytes = (uint32_t)a.seg * (a.has_bias ? 10 : 6);
     const int64_t groups = (a.rows + (int64_t)a.group - 1) / a.group;
     return launch_programmatic(logits_kernel<I, O>, dim3((unsigned)(groups * logits_segments(a.V, a.seg))), LOGITS_THREADS, bytes, s, a) ? QG_OK
                                                                                                                                        : QG_ECUDA;
@@ -431,10 +461,14 @@ int qg_logits_adjust(const void *logits, int type, int64_t ld, void *out, int ou
                           (const void *)h.q_start})
         if (!host_aligned(p, 4)) return QG_EALIGN;
     LogitsArgs a{logits, out, ld, ldo, V, 0, rows, 1, out == logits, h.bias_start != nullptr, h};
-    const int64_t fill = 4 * (int64_t)device_sms_planning();  // blocks that run at once
+    const int64_t fill = 5 * (int64_t)device_sms_planning();  // blocks that run at once
     a.seg = (int)std::min<int64_t>(std::max<int64_t>(rows * (int64_t)V / fill / 128 * 128 + 128, 512), LOGITS_SEG);
-    // rows that may share a sequence share a block, as long as every SM has a few blocks to overlap
-    if (h.seq && sequences) a.group = (int)std::min<int64_t>(std::max<int64_t>(rows * logits_segments(V, a.seg) / (2 * fill), 1), 8);
+    // rows that may share a sequence share a block, as long as the blocks fill the machine
+    if (h.seq && sequences) a.group = (int)std::min<int64_t>(std::max<int64_t>(rows * logits_segments(V, a.seg) / fill, 1), LOGITS_GROUP);
+#ifdef QG_TUNE
+    if (getenv("LG_SEG")) a.seg = atoi(getenv("LG_SEG"));
+    if (getenv("LG_GROUP")) a.group = atoi(getenv("LG_GROUP"));
+#endif
     if (rows * logits_segments(V, a.seg) > INT32_MAX) return QG_EINVAL;
     const int sms = device_sms();
     if (sms < 0) return sms;

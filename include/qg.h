@@ -417,7 +417,7 @@ typedef struct qg_logits {
  * The row's drafts are those of its mask in tree, its own with them (rows q_start[s] + i of the call).
  *   logits: rows ld elements apart, type; out: rows ldo apart, out_type (any of the three); it may be logits itself with the
  *   same type and ldo = ld, and then only what changes is read and written.
- * Limits: rows, V >= 1, rows * ceil((V + 3) / 4096) < 2^31; up to 2^30 ids of a history count.  Rows of ids that start on boundaries of 4
+ * Limits: rows, V >= 1, rows * ceil(V / 512) < 2^31; up to 2^29 ids of a history count.  Rows of ids that start on boundaries of 4
  * elements, or equally far behind one in logits and out, take vector loads; any alignment of whole elements works.
  * Lengths and starts are held inside the arrays. */
 int qg_logits_adjust(const void *logits, int type, int64_t ld, void *out, int out_type, int64_t ldo, int rows, int V, const qg_logits *how,
