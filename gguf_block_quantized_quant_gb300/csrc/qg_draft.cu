@@ -139,23 +139,28 @@ __global__ void __launch_bounds__(KEEP_THREADS) keep_lengths_kernel(const KeepAr
 }
 
 // ----------------------------------------------------------------------------- logits
-// A block takes a segment of ids for a few rows.  For each sequence among them it counts the ids of the segment that the history
-// holds in shared memory (a word per id), notes the last bias entry of each, and lists the ids so touched; the drafts that each
-// row follows, few or none of which fall into a segment, are listed per row.  The logits of all its rows stream past the mask
-// without a barrier, and the listed ids go over that.  Whole numbers are added, so the order of the atomics changes
-// nothing but the lists'.
-// Bound by memory: the logits are read and written once.  What has to be hidden is the chain of dependent loads before the
-// listed ids (sequence, lengths, ids, logits): other blocks of the SM do, and rows of one sequence share it.  Measured and dropped for
-// 192 rows of 131071, bf16 to fp32: a row at a time with its counts beside the stream, 97 us, with a list 108.
+// What changes most logits, the mask, and what changes a few, biases and penalties, are apart: the logits stream past the
+// mask, then the ids that have a bias or were said go over that.  For these a block takes a segment of ids for a few rows.  For each
+// sequence among them it counts the ids of the segment that the history holds in shared memory (a word per id), notes
+// the last bias entry of each, and lists the ids so touched; the drafts that each row follows, few or none of which fall into a
+// segment, are listed per row.  Whole numbers are added, so the order of the atomics changes nothing but the lists'.
+// The stream is bound by memory, the rest by a chain of dependent loads (sequence, lengths, ids, logits).  Small calls do both in
+// one kernel; large ones stream in a kernel of many light blocks, under whose end the counts of a second are made.  One
+// kernel for 192 rows of 131071, bf16 to fp32: 97 us with the counts beside the stream, 60 to 70 with lists, as the chains
+// of the few blocks that fit an SM do not hide each other.
 struct LogitsArgs {
     const void *x;
     void *out;
     int64_t ld, ldo;  // elements
-    int V, seg;       // seg: ids of a segment, a multiple of 8
+    int V, seg;       // seg: ids of a segment at most, a multiple of 8
+    int shift;        // a segment holds every 2^shift-th id, as often said ones are near each other; 0: neighbouring ids, to stream them
     int rows, group;  // group: rows of a block
-    int in_place, has_bias;
+    int in_place, stream, counts, has_bias;  // stream: the logits go past the mask here too; counts: some row has a history, drafts or biases
     qg_logits how;
 };
+
+// Segments of a row.
+__host__ __device__ constexpr int logits_segments(int V, int seg, int shift = 0) { return shift ? 1 << shift : (int)(((int64_t)V + seg - 1) / seg); }
 
 constexpr int LOGITS_HISTORY = 1 << 29;  // ids of a history that count; with the drafts below TIMES
 constexpr int LOGITS_THREADS = 256, LOGITS_U = 4, LOGITS_SEG = 4096, LOGITS_GROUP = 16;
@@ -165,11 +170,11 @@ constexpr int LOGITS_PATH = 30;          // drafts of a row in a segment that ar
 // whose word is 0 is listed.
 constexpr uint32_t SAID = 0x80000000u, BIASED = 0x40000000u, TIMES = 0x3fffffffu;
 
-// Four elements as they come.
+// Four elements as they come, read once: the second-level cache is for the output.
 template <class T>
 struct Raw4 {
     uint2 w;
-    __device__ __forceinline__ void load(const T *p) { w = *reinterpret_cast<const uint2 *>(p); }
+    __device__ __forceinline__ void load(const T *p) { w = __ldcs(reinterpret_cast<const uint2 *>(p)); }
     __device__ __forceinline__ void get(float (&v)[4]) const {
         const float2 a = unpack2<T>(w.x), b = unpack2<T>(w.y);
         v[0] = a.x, v[1] = a.y, v[2] = b.x, v[3] = b.y;
@@ -178,7 +183,7 @@ struct Raw4 {
 template <>
 struct Raw4<float> {
     float4 w;
-    __device__ __forceinline__ void load(const float *p) { w = *reinterpret_cast<const float4 *>(p); }
+    __device__ __forceinline__ void load(const float *p) { w = __ldcs(reinterpret_cast<const float4 *>(p)); }
     __device__ __forceinline__ void get(float (&v)[4]) const { v[0] = w.x, v[1] = w.y, v[2] = w.z, v[3] = w.w; }
 };
 
@@ -189,7 +194,7 @@ __device__ __forceinline__ uint32_t allowed4(const uint32_t *row, int v) { retur
 // Ids id0 .. id1 - 1 of a row, past the mask.
 template <class I, class O>
 __device__ __forceinline__ void logits_stream(const LogitsArgs &a, int row, int id0, int id1) {
-    const int tid = threadIdx.x;
+    const int tid = LOGITS_THREADS - 1 - threadIdx.x;  // the first warps have the ids of a short history to count
     const I *x = static_cast<const I *>(a.x) + row * a.ld;
     O *out = static_cast<O *>(a.out) + row * a.ldo;
     const uint32_t *allow = a.how.allow ? a.how.allow + row * a.how.allow_stride : nullptr;
@@ -232,7 +237,7 @@ __device__ __forceinline__ void logits_stream(const LogitsArgs &a, int row, int 
 }
 
 template <class I, class O>
-__global__ void __launch_bounds__(LOGITS_THREADS, 5) logits_kernel(const __grid_constant__ LogitsArgs a) {
+__global__ void __launch_bounds__(LOGITS_THREADS, 4) logits_kernel(const __grid_constant__ LogitsArgs a) {
     extern __shared__ __align__(16) uint32_t lg_smem[];
     __shared__ int touched, seqs[LOGITS_GROUP], paths[LOGITS_GROUP];
     __shared__ uint16_t path[LOGITS_GROUP][LOGITS_PATH];
@@ -240,16 +245,23 @@ __global__ void __launch_bounds__(LOGITS_THREADS, 5) logits_kernel(const __grid_
     uint32_t *entry = count + a.seg;                                                       // where there are biases
     uint16_t *list = reinterpret_cast<uint16_t *>(entry + (a.has_bias ? a.seg : 0));
     const int tid = threadIdx.x;
-    const int segs = (int)(((int64_t)a.V + a.seg - 1) / a.seg);
+    const int segs = logits_segments(a.V, a.seg, a.shift);
     const int row0 = (int)(blockIdx.x / segs) * a.group, rows = min(a.group, a.rows - row0);
-    const int id0 = (int)(blockIdx.x % segs) * a.seg, id1 = min(id0 + a.seg, a.V), n = id1 - id0;
-    griddep_wait();
-    griddep_launch_dependents();
+    const int seg = (int)(blockIdx.x % segs), id0 = a.shift ? seg : seg * a.seg, id1 = a.shift ? a.V : min(id0 + a.seg, a.V);
+    const int n = (int)(((int64_t)id1 - id0 + (1 << a.shift) - 1) >> a.shift);
+    // the place of an id in the segment, from n on for others; ids below 0 are far away
+    auto place = [&](int id) {
+        const unsigned d = (unsigned)id - (unsigned)id0;
+        return d & ((1u << a.shift) - 1u) ? 0xffffffffu : d >> a.shift;
+    };
+    // after a stream kernel nothing of its is read yet, and what that waited for is complete
+    if (a.stream) griddep_wait();
     if (tid < rows) {
         const int s = a.how.seq ? a.how.seq[row0 + tid] : row0 + tid;
         seqs[tid] = (unsigned)s < (unsigned)a.how.batch ? s : -1;
     }
-    for (int i = tid; i < a.seg / 4; i += LOGITS_THREADS) reinterpret_cast<uint4 *>(count)[i] = make_uint4(0, 0, 0, 0);
+    if (a.counts)
+        for (int i = tid; i < a.seg / 4; i += LOGITS_THREADS) reinterpret_cast<uint4 *>(count)[i] = make_uint4(0, 0, 0, 0);
     if (a.has_bias)
         for (int i = tid; i < a.seg / 4; i += LOGITS_THREADS) reinterpret_cast<uint4 *>(entry)[i] = make_uint4(0, 0, 0, 0);
     if (tid < LOGITS_GROUP) paths[tid] = 0;
@@ -284,7 +296,7 @@ __global__ void __launch_bounds__(LOGITS_THREADS, 5) logits_kernel(const __grid_
                 const int said = a.how.prompt_len ? a.how.prompt_len[s] : 0;
                 const int32_t *h = a.how.history + s * a.how.history_stride;
                 auto add = [&](int id, int i) {
-                    const unsigned at = (unsigned)id - (unsigned)id0;  // ids below 0 are far away
+                    const unsigned at = place(id);
                     if (at < (unsigned)n) listed((int)at, i < said ? atomicOr(count + at, SAID) : atomicAdd(count + at, 1u));
                 };
                 const int head = min(len, (int)(-(reinterpret_cast<intptr_t>(h) / 4) & 3)), quads = (len - head) / 4;
@@ -299,7 +311,7 @@ __global__ void __launch_bounds__(LOGITS_THREADS, 5) logits_kernel(const __grid_
                 if (tail < len) add(h[tail], tail);
             }
             for (int i = tid; i < entries; i += LOGITS_THREADS) {
-                const unsigned at = (unsigned)a.how.bias_ids[start + i] - (unsigned)id0;
+                const unsigned at = place(a.how.bias_ids[start + i]);
                 if (at >= (unsigned)n) continue;
                 listed((int)at, atomicOr(count + at, BIASED));
                 atomicMax(entry + at, (uint32_t)i + 1u);
@@ -307,7 +319,7 @@ __global__ void __launch_bounds__(LOGITS_THREADS, 5) logits_kernel(const __grid_
         }
         // the drafts that row r0 + r of the block follows: bit i, its place in the segment (or beyond it)
         auto follows = [&](int r, int i) { return a.how.tree[(int64_t)(row0 + r) * a.how.words + (i >> 5)] >> (i & 31) & 1u; };
-        auto draft = [&](int i) { return (unsigned)a.how.drafts[first + i] - (unsigned)id0; };
+        auto draft = [&](int i) { return place(a.how.drafts[first + i]); };
         for (int64_t x = tid; x < (int64_t)(r1 - r0) * bits; x += LOGITS_THREADS) {
             const int r = r0 + (int)(x / bits), i = (int)(x % bits);
             const unsigned at = draft(i);
@@ -316,18 +328,44 @@ __global__ void __launch_bounds__(LOGITS_THREADS, 5) logits_kernel(const __grid_
                 if (k < LOGITS_PATH) path[r][k] = (uint16_t)at;
             }
         }
-        if (r0 == 0)
-            for (int r = 0; r < rows; ++r) logits_stream<I, O>(a, row0 + r, id0, id1);
+        if (r0 == 0) {
+            if (a.stream) {
+                griddep_launch_dependents();
+                for (int r = 0; r < rows; ++r) logits_stream<I, O>(a, row0 + r, id0, id1);
+            } else {
+                griddep_wait();
+                griddep_launch_dependents();
+            }
+        }
         __syncthreads();  // what is listed goes over what the stream wrote
 
-        auto put = [&](int r, unsigned at, uint32_t c) {  // c: the id's word with the row's drafts
-            const int row = row0 + r, id = id0 + (int)at;
-            if (a.how.allow && !allowed(a.how.allow + row * a.how.allow_stride, id)) return;
-            float y = to_f32(static_cast<const I *>(a.x)[row * a.ld + id]);
-            if (c & BIASED) y += bias[entry[at] - 1];
-            if (c & ~BIASED) y = y > 0.0f ? __fdiv_rn(y, rep) : y * rep;
-            if (c & TIMES) y = fmaf(-freq, (float)(c & TIMES), y) - pres;
-            static_cast<O *>(a.out)[row * a.ldo + id] = from_f32<O>(y);
+        // Ids with the words c that the row's drafts leave them: loads of several are in flight together.  What the stream wrote is
+        // the logit itself, masked, and nearer by than that, but where the output is narrower; -inf stays what it is
+        constexpr int MANY = 4;
+        constexpr bool WRITTEN = std::is_same<I, O>::value || std::is_same<O, float>::value;
+        auto put = [&](const int (&r)[MANY], const unsigned (&at)[MANY], const uint32_t (&c)[MANY], int have) {
+            float y[MANY];
+            bool ok[MANY];
+#pragma unroll
+            for (int u = 0; u < MANY; ++u) {
+                const int row = row0 + r[u], id = id0 + (int)(at[u] << a.shift);
+                ok[u] = u < have;
+                if (!ok[u]) continue;
+                if constexpr (WRITTEN) {
+                    y[u] = to_f32(static_cast<const O *>(a.out)[row * a.ldo + id]);
+                } else {
+                    y[u] = to_f32(static_cast<const I *>(a.x)[row * a.ld + id]);
+                    if (a.how.allow) ok[u] = allowed(a.how.allow + row * a.how.allow_stride, id);
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < MANY; ++u) {
+                if (!ok[u] || y[u] == -INFINITY) continue;
+                if (c[u] & BIASED) y[u] += bias[entry[at[u]] - 1];
+                if (c[u] & ~BIASED) y[u] = y[u] > 0.0f ? __fdiv_rn(y[u], rep) : y[u] * rep;
+                if (c[u] & TIMES) y[u] = fmaf(-freq, (float)(c[u] & TIMES), y[u]) - pres;
+                static_cast<O *>(a.out)[(row0 + r[u]) * a.ldo + id0 + (int)(at[u] << a.shift)] = from_f32<O>(y[u]);
+            }
         };
         auto times = [&](int r, unsigned at) {  // how often the row's drafts say the id
             uint32_t k = 0;
@@ -339,20 +377,45 @@ __global__ void __launch_bounds__(LOGITS_THREADS, 5) logits_kernel(const __grid_
             return k;
         };
         const int ids = touched;
-        for (int r = r0; r < r1; ++r) {
-            for (int i = tid; i < ids; i += LOGITS_THREADS) {
-                const unsigned at = list[i];
-                put(r, at, count[at] + times(r, at));
+        for (int x = tid; x < (r1 - r0) * ids; x += LOGITS_THREADS * MANY) {
+            int r[MANY], have = 0;
+            unsigned at[MANY];
+            uint32_t c[MANY];
+#pragma unroll
+            for (int u = 0; u < MANY; ++u) {
+                const int y = x + u * LOGITS_THREADS;
+                if (y >= (r1 - r0) * ids) break;
+                r[u] = r0 + y / ids;
+                at[u] = list[y % ids];
+                c[u] = count[at[u]] + times(r[u], at[u]);
+                have = u + 1;
             }
-            // ids that the row's drafts alone say: each once, at its first place
-            const bool all = paths[r] > LOGITS_PATH;
-            const int most = all ? bits : paths[r];
-            for (int i = tid; i < most; i += LOGITS_THREADS) {
-                const unsigned at = all ? draft(i) : path[r][i];
-                if (at >= (unsigned)n || count[at] != 0 || (all && !follows(r, i))) continue;
+            put(r, at, c, have);
+        }
+        // ids that a row's drafts alone say: each once, at its first place among them
+        auto one = [&](int r, unsigned at) {
+            const int rs[MANY] = {r};
+            const unsigned ats[MANY] = {at};
+            const uint32_t cs[MANY] = {times(r, at)};
+            put(rs, ats, cs, 1);
+        };
+        if (bits > 0) {
+            for (int x = tid; x < (r1 - r0) * LOGITS_PATH; x += LOGITS_THREADS) {
+                const int r = r0 + x / LOGITS_PATH, k = x % LOGITS_PATH;
+                if (paths[r] > LOGITS_PATH || k >= paths[r] || count[path[r][k]] != 0) continue;
                 bool again = false;
-                for (int k = 0; k < i && !again; ++k) again = all ? follows(r, k) && draft(k) == at : path[r][k] == at;
-                if (!again) put(r, at, times(r, at));
+                for (int i = 0; i < k; ++i) again = again || path[r][i] == path[r][k];
+                if (!again) one(r, path[r][k]);
+            }
+            for (int r = r0; r < r1; ++r) {  // rows with more than the list holds
+                if (paths[r] <= LOGITS_PATH) continue;
+                for (int i = tid; i < bits; i += LOGITS_THREADS) {
+                    const unsigned at = draft(i);
+                    if (at >= (unsigned)n || count[at] != 0 || !follows(r, i)) continue;
+                    bool again = false;
+                    for (int k = 0; k < i && !again; ++k) again = follows(r, k) && draft(k) == at;
+                    if (!again) one(r, at);
+                }
             }
         }
         if (r1 < rows) {  // another sequence
@@ -367,22 +430,38 @@ __global__ void __launch_bounds__(LOGITS_THREADS, 5) logits_kernel(const __grid_
     }
 }
 
-// Segments of a row, and whether they and the rows are counted in 32 bits.
-static int64_t logits_segments(int V, int seg) { return ((int64_t)V + seg - 1) / seg; }
+template <class I, class O>
+__global__ void __launch_bounds__(LOGITS_THREADS, 8) logits_stream_kernel(const __grid_constant__ LogitsArgs a) {
+    griddep_wait();
+    griddep_launch_dependents();
+    const int segs = (a.V + LOGITS_SEG - 1) / LOGITS_SEG;
+    const int64_t total = (int64_t)a.rows * segs;
+    for (int64_t i = blockIdx.x; i < total; i += gridDim.x) {
+        const int id0 = (int)(i % segs) * LOGITS_SEG;
+        logits_stream<I, O>(a, (int)(i / segs), id0, min(id0 + LOGITS_SEG, a.V));
+    }
+}
 
 template <class I, class O>
-static int logits_launch(const LogitsArgs &a, cudaStream_t s) {
+static int logits_launch(LogitsArgs a, int sms, cudaStream_t s) {
+    if (!a.stream && !(a.in_place && !a.how.allow)) {
+        const int64_t blocks = std::min<int64_t>((int64_t)a.rows * logits_segments(a.V, LOGITS_SEG), 8 * (int64_t)sms);
+        if (!launch_programmatic(logits_stream_kernel<I, O>, dim3((unsigned)blocks), LOGITS_THREADS, 0, s, a)) return QG_ECUDA;
+        if (!a.counts) return QG_OK;
+    } else if (!a.stream) {
+        a.stream = 1;  // nothing streams, but the kernel is the call's first
+    }
     const uint32_t bytes = (uint32_t)a.seg * (a.has_bias ? 10 : 6);
     const int64_t groups = (a.rows + (int64_t)a.group - 1) / a.group;
-    return launch_programmatic(logits_kernel<I, O>, dim3((unsigned)(groups * logits_segments(a.V, a.seg))), LOGITS_THREADS, bytes, s, a) ? QG_OK
+    return launch_programmatic(logits_kernel<I, O>, dim3((unsigned)(groups * logits_segments(a.V, a.seg, a.shift))), LOGITS_THREADS, bytes, s, a) ? QG_OK
                                                                                                                                        : QG_ECUDA;
 }
 template <class I>
-static int logits_out(const LogitsArgs &a, int out_type, cudaStream_t s) {
+static int logits_out(const LogitsArgs &a, int out_type, int sms, cudaStream_t s) {
     switch (out_type) {
-    case QG_F32: return logits_launch<I, float>(a, s);
-    case QG_F16: return logits_launch<I, f16>(a, s);
-    default: return logits_launch<I, bf16>(a, s);
+    case QG_F32: return logits_launch<I, float>(a, sms, s);
+    case QG_F16: return logits_launch<I, f16>(a, sms, s);
+    default: return logits_launch<I, bf16>(a, sms, s);
     }
 }
 
@@ -460,23 +539,24 @@ int qg_logits_adjust(const void *logits, int type, int64_t ld, void *out, int ou
                           (const void *)h.bias_ids, (const void *)h.bias, (const void *)h.allow, (const void *)h.drafts, (const void *)h.tree,
                           (const void *)h.q_start})
         if (!host_aligned(p, 4)) return QG_EALIGN;
-    LogitsArgs a{logits, out, ld, ldo, V, 0, rows, 1, out == logits, h.bias_start != nullptr, h};
-    const int64_t fill = 5 * (int64_t)device_sms_planning();  // blocks that run at once
+    const int64_t fill = 4 * (int64_t)device_sms_planning();  // blocks of the kernel with the counts that run at once
+    const bool counts = h.history || h.drafts || h.bias_start;
+    LogitsArgs a{logits, out, ld, ldo, V, 0, 0, rows, 1, out == logits, 1, counts, h.bias_start != nullptr, h};
     a.seg = (int)std::min<int64_t>(std::max<int64_t>(rows * (int64_t)V / fill / 128 * 128 + 128, 512), LOGITS_SEG);
-    // rows that may share a sequence share a block, as long as the blocks fill the machine
-    if (h.seq && sequences) a.group = (int)std::min<int64_t>(std::max<int64_t>(rows * logits_segments(V, a.seg) / fill, 1), LOGITS_GROUP);
-#ifdef QG_TUNE
-    if (getenv("LG_SEG")) a.seg = atoi(getenv("LG_SEG"));
-    if (getenv("LG_GROUP")) a.group = atoi(getenv("LG_GROUP"));
-#endif
-    if (rows * logits_segments(V, a.seg) > INT32_MAX) return QG_EINVAL;
+    // One kernel up to where its blocks run at once, else as many rows for each block of the second as let them
+    a.stream = (int64_t)rows * logits_segments(V, a.seg) <= fill;
+    if (!a.stream) {
+        for (a.seg = LOGITS_SEG; (int64_t)a.seg << a.shift < V; ++a.shift) {}
+        a.group = (int)std::min<int64_t>((((int64_t)rows << a.shift) + fill - 1) / fill, LOGITS_GROUP);
+    }
+    if ((int64_t)rows * logits_segments(V, a.seg, a.shift) > INT32_MAX) return QG_EINVAL;
     const int sms = device_sms();
     if (sms < 0) return sms;
     cudaStream_t s = (cudaStream_t)stream;
     switch (type) {
-    case QG_F32: return logits_out<float>(a, out_type, s);
-    case QG_F16: return logits_out<f16>(a, out_type, s);
-    default: return logits_out<bf16>(a, out_type, s);
+    case QG_F32: return logits_out<float>(a, out_type, sms, s);
+    case QG_F16: return logits_out<f16>(a, out_type, sms, s);
+    default: return logits_out<bf16>(a, out_type, sms, s);
     }
 }
 

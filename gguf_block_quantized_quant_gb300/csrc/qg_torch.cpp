@@ -135,30 +135,32 @@ Heads heads(const Tensor &t, const char *what) {
     return {t.data_ptr(), t.size(0) > 1 ? t.stride(0) : d, t.size(1) > 1 ? t.stride(1) : d};  // a stride of one element says nothing
 }
 
+// layers: pools of several layers have that dimension in front; they are described by the first one.
 qg_paged paged(const Tensor &k, const Tensor &v, const Tensor *kd, const Tensor *vd, const Tensor &q_start, const Tensor &kv_len,
-               const Tensor &pages) {
-    const int type = type_of(k.scalar_type());
+               const Tensor &pages, bool layers = false) {
+    const int type = type_of(k.scalar_type()), z = layers ? 1 : 0;
     // the stride of a dimension of one element says nothing
     auto strides = [](const Tensor &a, const Tensor &b) {
-        for (int i = 0; i < 4; ++i)
+        for (int64_t i = 0; i < a.dim(); ++i)
             if (a.size(i) > 1 && a.stride(i) != b.stride(i)) return false;
         return true;
     };
-    need(k.dim() == 4 && (type == QG_F16 || type == QG_BF16 || type == QG_Q8_0) && v.scalar_type() == k.scalar_type() &&
+    need(k.dim() == 4 + z && (type == QG_F16 || type == QG_BF16 || type == QG_Q8_0) && v.scalar_type() == k.scalar_type() &&
              v.sizes() == k.sizes() && strides(k, v) && k.is_cuda(),
          "cache pools are fp16, bf16 or int8 CUDA tensors (pages, kv_heads, page, dim) of one shape, type and layout");
-    need(k.stride(3) == 1, "cache pools must be contiguous along the head dimension");
-    const int64_t n = k.size(0), h = k.size(1), page = k.size(2), dim = k.size(3);
+    need(k.stride(3 + z) == 1, "cache pools must be contiguous along the head dimension");
+    const int64_t n = k.size(z), h = k.size(1 + z), page = k.size(2 + z), dim = k.size(3 + z);
     qg_paged c{};
     if (type == QG_Q8_0) {
         need(kd && vd && kd->scalar_type() == ScalarType::Half && vd->scalar_type() == ScalarType::Half,
              "an int8 cache needs fp16 steps kd and vd");
         const int64_t blocks = dim / 32;
         for (const Tensor *s : {kd, vd})
-            need(s->dim() == 4 && s->size(0) == n && s->size(1) == h && s->size(2) == page && s->size(3) == blocks &&
-                     s->stride(3) == 1 && s->stride(2) == blocks && (h == 1 || s->stride(1) == page * blocks) && strides(*s, *kd),
+            need(s->dim() == 4 + z && (!layers || s->size(0) == k.size(0)) && s->size(z) == n && s->size(1 + z) == h && s->size(2 + z) == page &&
+                     s->size(3 + z) == blocks && s->stride(3 + z) == 1 && s->stride(2 + z) == blocks && (h == 1 || s->stride(1 + z) == page * blocks) &&
+                     strides(*s, *kd),
                  "steps have shape (pages, kv_heads, page, dim / 32), contiguous within a page");
-        c.step_stride = n > 1 ? kd->stride(0) : h * page * blocks;
+        c.step_stride = n > 1 ? kd->stride(z) : h * page * blocks;
     }
     for (const Tensor *t : {&q_start, &kv_len, &pages})
         need(t->scalar_type() == ScalarType::Int, "q_start, kv_len and pages are int32 tensors");
@@ -170,9 +172,9 @@ qg_paged paged(const Tensor &k, const Tensor &v, const Tensor *kd, const Tensor 
     c.type = type;
     c.kv_heads = narrow(h), c.dim = narrow(dim), c.page = narrow(page), c.n_pages = narrow(n);
     c.batch = narrow(batch), c.table_width = narrow(pages.size(1));
-    c.slot_stride = k.stride(2);
-    c.head_stride = h > 1 ? k.stride(1) : page * c.slot_stride;
-    c.page_stride = n > 1 ? k.stride(0) : h * page * c.slot_stride;
+    c.slot_stride = k.stride(2 + z);
+    c.head_stride = h > 1 ? k.stride(1 + z) : page * c.slot_stride;
+    c.page_stride = n > 1 ? k.stride(z) : h * page * c.slot_stride;
     c.table_stride = batch > 1 ? pages.stride(0) : std::max(pages.size(1), pages.stride(0));
     c.k = k.data_ptr(), c.v = v.data_ptr();
     c.kd = type == QG_Q8_0 ? kd->data_ptr() : nullptr, c.vd = type == QG_Q8_0 ? vd->data_ptr() : nullptr;
@@ -433,23 +435,9 @@ PyObject *cache_keep(PyObject *, PyObject *const *a, Py_ssize_t n) {
         const Tensor *kd = maybe(a[7], "kd is a tensor or None"), *vd = maybe(a[8], "vd is a tensor or None");
         const bool stacked = k.dim() == 5;  // (layers, pages, kv_heads, page, dim)
         const int64_t layers = stacked ? k.size(0) : 1;
-        int64_t apart = 0, steps_apart = 0;
-        qg_paged c;
-        if (stacked) {
-            need(layers > 0 && v.dim() == 5 && v.size(0) == layers && (layers == 1 || v.stride(0) == k.stride(0)),
-                 "pools of several layers are (layers, pages, kv_heads, page, dim), keys and values of one layout");
-            Tensor d0, d1;
-            if (kd && vd) {
-                need(kd->dim() == 5 && vd->dim() == 5 && kd->size(0) == layers && vd->size(0) == layers && (layers == 1 || vd->stride(0) == kd->stride(0)),
-                     "steps of several layers are (layers, pages, kv_heads, page, dim / 32)");
-                d0 = kd->select(0, 0), d1 = vd->select(0, 0);
-                steps_apart = kd->stride(0);
-            }
-            apart = k.stride(0);
-            c = paged(k.select(0, 0), v.select(0, 0), kd ? &d0 : nullptr, vd ? &d1 : nullptr, q_start, kv_len, pages);
-        } else {
-            c = paged(k, v, kd, vd, q_start, kv_len, pages);
-        }
+        need(!stacked || layers > 0, "pools of several layers are (layers, pages, kv_heads, page, dim)");
+        const qg_paged c = paged(k, v, kd, vd, q_start, kv_len, pages, stacked);
+        const int64_t apart = stacked ? k.stride(0) : 0, steps_apart = stacked && c.type == QG_Q8_0 ? kd->stride(0) : 0;
         need(keep.dim() == 2 && keep.scalar_type() == ScalarType::Int && keep.size(0) == c.batch && (keep.stride(1) == 1 || keep.size(1) == 1),
              "keep is an int32 tensor (batch, width), contiguous along the width");
         need(keep_len.scalar_type() == ScalarType::Int && keep_len.numel() == c.batch && keep_len.is_contiguous(), "keep_len is a contiguous int32 tensor, one per sequence");

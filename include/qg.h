@@ -413,7 +413,7 @@ typedef struct qg_logits {
  *   x = logits + bias of v (of several entries for one id the last one counts)
  *   x = x > 0 ? x / repetition : x * repetition        where v occurs in the history or among the row's drafts
  *   x = x - frequency * n - (n > 0 ? presence : 0)      n: how often v occurs after the prompt, the row's drafts included
- *   x = -inf                                            where the row's mask does not allow v
+ *   x = -inf                                            where the row's mask does not allow v, or the logit is that already
  * The row's drafts are those of its mask in tree, its own with them (rows q_start[s] + i of the call).
  *   logits: rows ld elements apart, type; out: rows ldo apart, out_type (any of the three); it may be logits itself with the
  *   same type and ldo = ld, and then only what changes is read and written.
