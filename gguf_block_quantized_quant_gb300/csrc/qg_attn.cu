@@ -110,8 +110,21 @@ static int attn_plain(const AttnArgs &a, const qg_paged &c, int max_new, int sms
     if ((int64_t)max_new * a.G > DEC_ROWS) return attn_chunk<MOD_PLAIN>(a, c, sms, s);
     return attn_rows<MOD_PLAIN>(a, c, (int64_t)max_new * a.G <= 8 ? 1 : 2, sms, s);
 }
+// With several row tiles per sequence and cache head the row kernel reads the cache as often, but spares the plan and some
+// microseconds of the chunk kernel's start: that wins where the tiles are few and the caches, as large as the page table
+// allows, small.  us, chunk and row kernel (fp16, 32/8 heads of 128): 16 drafts of one sequence after 1000 18.6, 15.8; 8
+// after 4000 22.1, 17.5; 32 after 1000 20.9, 22.2; 8 of 4 sequences after 1000 22.0, 20.9; 16 after 300 20.2, 21.7.  (16-bit
+// heads of 256: 8 after 1000 18.5, 19.8.)
+static bool few_rows(const AttnArgs &a, const qg_paged &c, int max_new) {
+    const int64_t rows = (int64_t)max_new * a.G;
+    if (rows <= DEC_ROWS) return true;
+    const int64_t tiles = (rows + DEC_ROWS - 1) / DEC_ROWS;
+    if (tiles * c.batch * a.Hk > 64 || (c.dim == 256 && c.type != QG_Q8_0)) return false;
+    const int64_t slot = 2 * (int64_t)a.Hk * (c.type == QG_Q8_0 ? c.dim + c.dim / 16 : c.dim * 2);
+    return (tiles - 1) * c.batch * std::min<int64_t>((int64_t)c.table_width * c.page, MAX_SLOTS) <= (int64_t)(16 << 20) / slot;
+}
 static int attn_other(const AttnArgs &a, const qg_paged &c, int max_new, int sms, cudaStream_t s) {
-    if ((int64_t)max_new * a.G > DEC_ROWS)
+    if (!few_rows(a, c, max_new))
         return a.sh.slopes            ? attn_chunk<MOD_BIASED>(a, c, sms, s)
                : a.sh.cap_out > 0.0f ? attn_chunk<MOD_CAPPED>(a, c, sms, s)
                                      : attn_chunk<MOD_SHAPED>(a, c, sms, s);

@@ -114,8 +114,9 @@ struct ChunkCfg {
     static constexpr uint32_t KV_AT = OUT_AT + NQ * 4 * 2048;
     static constexpr uint32_t RAW_AT = KV_AT + NS * TILE;
     static constexpr uint32_t BAR_AT = RAW_AT + (Q8 ? NRAW * (CODES + STEPS) : 0);
-    static constexpr uint32_t BYTES = BAR_AT + NBAR * 8 + 8 /* tensor memory address, turn */ + 1024 /* alignment */;
-    static_assert(OUT_AT % 1024 == 0 && KV_AT % 1024 == 0 && RAW_AT % 1024 == 0 && BAR_AT % 16 == 0 && TILE % 1024 == 0 && CODES % 1024 == 0 &&
+    static constexpr uint32_t HALVES_AT = BAR_AT + NBAR * 8 + 8 /* tensor memory address, turn */;  // what shared row tiles exchange
+    static constexpr uint32_t BYTES = HALVES_AT + (NQ == 2 ? 2 * 128 * 8 : 0) + 1024 /* alignment */;
+    static_assert(OUT_AT % 1024 == 0 && KV_AT % 1024 == 0 && RAW_AT % 1024 == 0 && BAR_AT % 16 == 0 && HALVES_AT % 8 == 0 && TILE % 1024 == 0 && CODES % 1024 == 0 &&
                       STEPS % 16 == 0,
                   "alignment");
     // tensor memory columns
@@ -151,8 +152,10 @@ static ChunkPlan chunk_plan_at(uint8_t *p, int64_t tiles) {
 }
 
 constexpr int PLAN_SEQS = 1024, PLAN_ORDERED = 256;  // tiles at most that are put in order
-// Masks of other kinds have every token's range looked up: more warps for that
-constexpr int plan_threads(int mod) { return mod == MOD_PLAIN ? 256 : 1024; }
+// Threads of the plan.  Where every token's range is looked up, as documents and a tree's positions in a window ask for, 32 warps
+// do that (4 sequences of 2000 tokens in documents: 8 warps took 10 us more)
+__host__ __device__ inline bool plan_scans(const AttnArgs &a) { return a.sh.first || (a.sh.tree && a.window); }
+constexpr int PLAN_THREADS = 256, PLAN_SCAN_THREADS = 1024;
 
 // An item costs its slot tiles and CHUNK_OV more for loading the queries and writing the result, in
 // the same unit; a range that ends inside that part leaves the item to the next CTA.  Measured with 1,
@@ -169,14 +172,14 @@ __device__ __forceinline__ int deal(int k, int c, int ctas) { return k & 1 ? (k 
 // One block lists the row tiles of all sequences with their slot ranges.  It stands before the
 // attention kernel in time, so it is built for few steps: one warp places the sequences' first tiles,
 // then a thread makes a tile and one barrier a prefix of their costs.
-template <int MOD>
-__global__ void __launch_bounds__(plan_threads(MOD)) attn_plan_kernel(const AttnArgs a, ChunkPlan p, int rows, int bn, int max_tiles, int ctas) {
-    constexpr int PLAN_THREADS = plan_threads(MOD);
-    __shared__ int64_t part[2][PLAN_THREADS / 32];
+template <int MOD, bool SCANS>
+__global__ void __launch_bounds__(SCANS ? PLAN_SCAN_THREADS : PLAN_THREADS) attn_plan_kernel(const AttnArgs a, ChunkPlan p, int rows, int bn, int max_tiles, int ctas) {
+    constexpr int THREADS = SCANS ? PLAN_SCAN_THREADS : PLAN_THREADS;
+    __shared__ int64_t part[2][THREADS / 32];
     __shared__ int unit[PLAN_ORDERED], sorted[PLAN_ORDERED];
     __shared__ int off[PLAN_SEQS + 1];
-    __shared__ int2 range[MOD == MOD_PLAIN ? 1 : PLAN_THREADS];  // per tile of a round: first slot seen, end of those seen
-    __shared__ Seq seqs[MOD == MOD_PLAIN ? 1 : PLAN_SEQS];
+    __shared__ int2 range[SCANS ? THREADS : 1];  // per tile of a round: first slot seen, end of those seen
+    __shared__ Seq seqs[SCANS ? PLAN_SEQS : 1];
     griddep_wait();
     griddep_launch_dependents();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -192,7 +195,7 @@ __global__ void __launch_bounds__(plan_threads(MOD)) attn_plan_kernel(const Attn
                 if (b0 + lane < nb) {
                     const Seq s = seq_of(a.bt, c0 + b0 + lane);
                     v = (s.n * a.G + rows - 1) / rows;
-                    if constexpr (MOD != MOD_PLAIN) seqs[b0 + lane] = s;
+                    if constexpr (SCANS) seqs[b0 + lane] = s;
                 }
                 // q_start that decreases could list more tiles than the call's tokens make: counts stop there, and
                 // those past it are left out
@@ -210,7 +213,7 @@ __global__ void __launch_bounds__(plan_threads(MOD)) attn_plan_kernel(const Attn
         }
         __syncthreads();
         const int count = min(off[nb], max_tiles - tiles_before);
-        for (int r0 = 0; r0 < count; r0 += PLAN_THREADS) {
+        for (int r0 = 0; r0 < count; r0 += THREADS) {
             const int r = r0 + tid, at = tiles_before + r;
             int64_t cost = 0;
             ChunkTile t{};
@@ -223,17 +226,13 @@ __global__ void __launch_bounds__(plan_threads(MOD)) attn_plan_kernel(const Attn
                 }
                 return lo;
             };
-            if constexpr (MOD != MOD_PLAIN) {
+            if constexpr (SCANS) {
                 // a warp takes a tile's tokens, so that their loads are few and side by side
                 if (r0) __syncthreads();
-                for (int x = r0 + warp; x < min(count, r0 + PLAN_THREADS); x += PLAN_THREADS / 32) {
+                for (int x = r0 + warp; x < min(count, r0 + THREADS); x += THREADS / 32) {
                     const int b = sequence(x), row0 = (x - off[b]) * rows;
                     const Seq s = seqs[b];
                     int from = s.len, end = 0;
-                    if (a.sh.tree && !a.window) {  // every slot
-                        if (lane == 0) range[x - r0] = make_int2(0, s.len);
-                        continue;
-                    }
                     for (int i = row0 / a.G + lane; i <= (min(row0 + rows, s.n * a.G) - 1) / a.G; i += 32) {
                         const Seen v = seen_by(a, s, c0 + b, i);
                         from = min(from, needs_from(a, s, v));
@@ -247,7 +246,7 @@ __global__ void __launch_bounds__(plan_threads(MOD)) attn_plan_kernel(const Attn
             }
             if (on) {
                 const int lo = sequence(r);
-                const Seq s = MOD == MOD_PLAIN ? seq_of(a.bt, c0 + lo) : seqs[lo];
+                const Seq s = SCANS ? seqs[lo] : seq_of(a.bt, c0 + lo);
                 t.b = c0 + lo;
                 t.row0 = (r - off[lo]) * rows;
                 t.first = s.first, t.n = s.n, t.len = s.len;
@@ -255,7 +254,12 @@ __global__ void __launch_bounds__(plan_threads(MOD)) attn_plan_kernel(const Attn
                 int from = seen_from(s.len - s.n + tf, a.window);
                 int end = s.len - s.n + tl + 1;  // slots that the last row sees
                 if constexpr (MOD != MOD_PLAIN) {
-                    from = range[tid].x, end = range[tid].y;
+                    if (SCANS)
+                        from = range[tid].x, end = range[tid].y;
+                    else if (a.sh.tree)
+                        from = 0, end = s.len;
+                    else if (a.sh.prefix)
+                        end = max(end, min(a.sh.prefix[t.b], s.len));
                     t.lo = from;
                 }
                 t.kb0 = from / bn;
@@ -272,7 +276,7 @@ __global__ void __launch_bounds__(plan_threads(MOD)) attn_plan_kernel(const Attn
             __syncthreads();
             int64_t sum = 0;
 #pragma unroll
-            for (int w = 0; w < PLAN_THREADS / 32; ++w) {
+            for (int w = 0; w < THREADS / 32; ++w) {
                 if (w == warp) v += sum;
                 sum += part[flip][w];
             }
@@ -289,7 +293,7 @@ __global__ void __launch_bounds__(plan_threads(MOD)) attn_plan_kernel(const Attn
                 __syncthreads();
                 const int items = count * a.Hk;
                 int64_t most = 0;
-                for (int c = tid; c < ctas; c += PLAN_THREADS) {
+                for (int c = tid; c < ctas; c += THREADS) {
                     int64_t load = 0;
                     for (int k = 0, i = c; i < items; ++k, i = deal(k, c, ctas)) load += sorted[i / a.Hk];
                     most = max(most, load);
@@ -590,14 +594,12 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
                     // From S to the scores as powers of two's exponents, where these are no multiple of S: capped by what the row's
                     // largest |S| allows (most, if not all, rows are below a quarter of the cap: three coefficients)
                     float most = 0.0f;
-                    auto reach = [&](const uint32_t (&v)[32]) {
-                        float hi = 0.0f, lo = 0.0f;  // their maximum is there already, where nothing is masked
+                    auto reach = [&](const uint32_t (&v)[32]) {  // below 0; the maximum says the rest
+                        float lo[2] = {-most, 0.0f};
 #pragma unroll
-                        for (int i = 0; i < 32; i += 2) {
-                            hi = fmaxf(fmaxf(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), hi);
-                            lo = fminf(fminf(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), lo);
-                        }
-                        most = fmaxf(most, fmaxf(hi, -lo));
+                        for (int i = 0; i < 32; i += 2)
+                            lo[(i / 2) & 1] = fminf(fminf(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), lo[(i / 2) & 1]);
+                        most = -fminf(lo[0], lo[1]);
                     };
                     auto small_cap = [&](uint64_t x) {  // the factor of S up to a quarter of the cap
                         const uint64_t u = mul_f32x2(x, x);
@@ -719,13 +721,11 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
                             largest(General{}, std::true_type{});
                     } else {
                         if (a.sh.cap_out > 0.0f) {
-                            if (!edge)
-                                each([&](uint32_t (&v)[32], int) { reach(v); });
-                            else
-                                each([&](uint32_t (&v)[32], int c0) {
-                                    hide(v, c0, 0u);
-                                    reach(v);
-                                });
+                            each([&](uint32_t (&v)[32], int c0) {
+                                if (edge) hide(v, c0, 0u);
+                                reach(v);
+                                most = fmaxf(most, top(v));
+                            });
                         }
                         if (!(a.sh.positions && key0 + BN > pos0) && __all_sync(0xffffffffu, row_pos >= min(hi, key0 + BN - 1)))
                             kind = a.sh.cap_out == 0.0f ? LINEAR : __any_sync(0xffffffffu, most > a.sh.small_to) ? GENERAL : LINEAR_CAP;
@@ -742,8 +742,10 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
                         else
                             largest(General{}, std::true_type{});
                     }
-                    if constexpr (MOD == MOD_CAPPED)  // a cap keeps the order: the maximum is bent alone
+                    if constexpr (MOD == MOD_CAPPED) {  // a cap keeps the order: the maximum is bent alone
+                        most = fmaxf(most, mx);
                         if (mx != -INFINITY) mx = a.sh.cap_out * tanh_any(mx * a.sh.cap_in);
+                    }
                     if (!Cfg::P_OVER && done > 0) {  // P's place is free again
                         mbar_wait(pv_done(q, 0), (done - 1) & 1);
                         tc_fence_after();
@@ -1382,7 +1384,10 @@ static int chunk_run(const AttnArgs &in, const qg_paged &c, int sms, cudaStream_
     if (qcopy && !attn_query_map(&qm, a, c.type == QG_BF16, D)) return QG_ECUDA;
     if (!attn_tensor_map(&km, c, c.k, box) || !attn_tensor_map(&vm, c, c.v, box)) return QG_ECUDA;
     if (!chunk_ready<C, D, MOD>()) return QG_ECUDA;
-    if (!launch_programmatic(attn_plan_kernel<MOD>, dim3(1), plan_threads(MOD), 0, s, a, plan, Cfg::ROWS, Cfg::BN, (int)tiles, sms)) return QG_ECUDA;
+    const bool scans = MOD != MOD_PLAIN && plan_scans(a);
+    if (!launch_programmatic(scans ? attn_plan_kernel<MOD, MOD != MOD_PLAIN> : attn_plan_kernel<MOD, false>, dim3(1),
+                             scans ? PLAN_SCAN_THREADS : PLAN_THREADS, 0, s, a, plan, Cfg::ROWS, Cfg::BN, (int)tiles, sms))
+        return QG_ECUDA;
     auto kern = attn_chunk_kernel<C, D, MOD>;
     if (!launch_programmatic(kern, dim3((unsigned)sms), Cfg::THREADS, Cfg::BYTES, s, a, plan, box, qsign, (int)qcopy, km, vm, qm)) return QG_ECUDA;
     auto join = attn_chunk_join_kernel<T, D>;
