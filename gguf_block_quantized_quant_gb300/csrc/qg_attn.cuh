@@ -74,7 +74,7 @@ __device__ __forceinline__ Seen seen_by(const AttnArgs &a, const Seq &s, int b, 
         r.hi = s.len - s.n - 1;
         r.lo = min(seen_from(r.pos, a.window), 0x7ffffffe);
     } else {
-        r.hi = a.sh.prefix ? min(max(slot, a.sh.prefix[b] - 1), s.len - 1) : slot;
+        r.hi = a.sh.prefix ? min(max(slot, max(a.sh.prefix[b], 0) - 1), s.len - 1) : slot;
         r.lo = seen_from(slot, a.window);
         if (a.sh.first) r.lo = max(r.lo, a.sh.first[t]);
         if (r.lo > r.hi) r.hi = -1, r.lo = 0x7fffffff;

@@ -254,10 +254,11 @@ __global__ void __launch_bounds__(LOGITS_THREADS, 4) logits_kernel(const __grid_
         const unsigned d = (unsigned)id - (unsigned)id0;
         return d & ((1u << a.shift) - 1u) ? 0xffffffffu : d >> a.shift;
     };
-    // after a stream kernel nothing of its is read yet, and what that waited for is complete
+    // After a stream kernel nothing that it writes is read yet, and what that waited for is complete; the ids are read past
+    // the first-level cache, which may hold what was there before
     if (a.stream) griddep_wait();
     if (tid < rows) {
-        const int s = a.how.seq ? a.how.seq[row0 + tid] : row0 + tid;
+        const int s = a.how.seq ? __ldcg(a.how.seq + row0 + tid) : row0 + tid;
         seqs[tid] = (unsigned)s < (unsigned)a.how.batch ? s : -1;
     }
     if (a.counts)
@@ -278,48 +279,48 @@ __global__ void __launch_bounds__(LOGITS_THREADS, 4) logits_kernel(const __grid_
         float rep = 1.0f, freq = 0.0f, pres = 0.0f;
         int first = 0, bits = 0;  // of the sequence's drafts
         if (s >= 0) {
-            if (a.how.repetition) rep = a.how.repetition[s];
-            if (a.how.frequency) freq = a.how.frequency[s];
-            if (a.how.presence) pres = a.how.presence[s];
+            if (a.how.repetition) rep = __ldcg(a.how.repetition + s);
+            if (a.how.frequency) freq = __ldcg(a.how.frequency + s);
+            if (a.how.presence) pres = __ldcg(a.how.presence + s);
             if (a.how.drafts) {
-                first = min(max(a.how.q_start[s], 0), a.rows);
-                bits = (int)min((int64_t)(min(max(a.how.q_start[s + 1], 0), a.rows) - first), (int64_t)32 * a.how.words);
+                first = min(max(__ldcg(a.how.q_start + s), 0), a.rows);
+                bits = (int)min((int64_t)(min(max(__ldcg(a.how.q_start + s + 1), 0), a.rows) - first), (int64_t)32 * a.how.words);
             }
             int start = 0, entries = 0;
             if (a.has_bias) {
-                start = min(max(a.how.bias_start[s], 0), a.how.bias_entries);
-                entries = min(a.how.bias_start[s + 1], a.how.bias_entries) - start;
+                start = min(max(__ldcg(a.how.bias_start + s), 0), a.how.bias_entries);
+                entries = min(__ldcg(a.how.bias_start + s + 1), a.how.bias_entries) - start;
                 bias = a.how.bias + start;
             }
             if (a.how.history) {
-                const int len = min(max(a.how.history_len[s], 0), min(a.how.history_width, LOGITS_HISTORY));
-                const int said = a.how.prompt_len ? a.how.prompt_len[s] : 0;
+                const int len = min(max(__ldcg(a.how.history_len + s), 0), min(a.how.history_width, LOGITS_HISTORY));
+                const int said = a.how.prompt_len ? __ldcg(a.how.prompt_len + s) : 0;
                 const int32_t *h = a.how.history + s * a.how.history_stride;
                 auto add = [&](int id, int i) {
                     const unsigned at = place(id);
                     if (at < (unsigned)n) listed((int)at, i < said ? atomicOr(count + at, SAID) : atomicAdd(count + at, 1u));
                 };
                 const int head = min(len, (int)(-(reinterpret_cast<intptr_t>(h) / 4) & 3)), quads = (len - head) / 4;
-                if (tid < head) add(h[tid], tid);
+                if (tid < head) add(__ldcg(h + tid), tid);
 #pragma unroll 4
                 for (int i = tid; i < quads; i += LOGITS_THREADS) {
-                    const int4 w = reinterpret_cast<const int4 *>(h + head)[i];
+                    const int4 w = __ldcg(reinterpret_cast<const int4 *>(h + head) + i);
                     const int at = head + 4 * i;
                     add(w.x, at), add(w.y, at + 1), add(w.z, at + 2), add(w.w, at + 3);
                 }
                 const int tail = head + 4 * quads + tid;
-                if (tail < len) add(h[tail], tail);
+                if (tail < len) add(__ldcg(h + tail), tail);
             }
             for (int i = tid; i < entries; i += LOGITS_THREADS) {
-                const unsigned at = place(a.how.bias_ids[start + i]);
+                const unsigned at = place(__ldcg(a.how.bias_ids + start + i));
                 if (at >= (unsigned)n) continue;
                 listed((int)at, atomicOr(count + at, BIASED));
                 atomicMax(entry + at, (uint32_t)i + 1u);
             }
         }
         // the drafts that row r0 + r of the block follows: bit i, its place in the segment (or beyond it)
-        auto follows = [&](int r, int i) { return a.how.tree[(int64_t)(row0 + r) * a.how.words + (i >> 5)] >> (i & 31) & 1u; };
-        auto draft = [&](int i) { return place(a.how.drafts[first + i]); };
+        auto follows = [&](int r, int i) { return __ldcg(a.how.tree + (int64_t)(row0 + r) * a.how.words + (i >> 5)) >> (i & 31) & 1u; };
+        auto draft = [&](int i) { return place(__ldcg(a.how.drafts + first + i)); };
         for (int64_t x = tid; x < (int64_t)(r1 - r0) * bits; x += LOGITS_THREADS) {
             const int r = r0 + (int)(x / bits), i = (int)(x % bits);
             const unsigned at = draft(i);

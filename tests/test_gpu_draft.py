@@ -2,6 +2,7 @@
 import math
 import random
 
+import numpy as np
 import pytest
 import torch
 
@@ -59,9 +60,8 @@ def plain(x, case):
                     y[r, i] -= freq * n + pres
                     mag[r, i] += abs(freq) * n + abs(pres)
         if case.get("allow"):
-            for i in range(V):
-                if not case["allow"][r] >> i & 1:
-                    y[r, i] = -math.inf
+            bits = np.frombuffer(case["allow"][r].to_bytes(-(-V // 8), "little"), dtype=np.uint8)
+            y[r, torch.from_numpy(np.unpackbits(bits, bitorder="little")[:V] == 0)] = -math.inf
     return y.cuda(), mag.cuda()
 
 
@@ -172,6 +172,48 @@ def test_parts(qg, what):
 def test_drafts(qg, words, rows, batch):
     x = torch.randn((rows, 500), generator=gen(rows), device="cuda")
     check(qg, x, make(rows, rows, 500, batch=batch, drafts=True, words=words))
+
+
+@pytest.mark.parametrize("dtype,out", [(F32, F32), (BF16, F32), (F16, F32), (F32, BF16), (BF16, F16)])
+def test_large_calls_in_two_kernels(qg, dtype, out):
+    """Enough rows and ids that the stream has a kernel of its own; rows of a sequence together, apart and of none; in place."""
+    V, rows, batch = 20001, 170, 11
+    x = (3 * torch.randn((rows, V), generator=gen(7), device="cuda")).to(dtype)
+    c = make(70, rows, V, batch=batch, drafts=True, words=1, longest=3000)
+    got = check(qg, x, c, out_dtype=out)
+    r = random.Random(5)
+    for s in range(len(c["seq"])):
+        if r.random() < 0.3:
+            c["seq"][s] = r.randrange(batch)
+    c.pop("tree"), c.pop("drafts")
+    check(qg, x, c, out_dtype=out)
+    for part in ("bias", "history", "allow"):
+        less = {k: v for k, v in c.items() if k != part and not (part == "history" and k == "prompt")}
+        check(qg, x, less, out_dtype=out)
+    if dtype == out:
+        y = x.clone()
+        call(qg, y, c, out=y)
+        assert torch.equal(y.nan_to_num(7.0), call(qg, x, c, out_dtype=out).nan_to_num(7.0))
+        c.pop("allow")
+        y = x.clone()
+        call(qg, y, c, out=y)
+        assert torch.equal(y, call(qg, x, c, out_dtype=out))
+    assert got.shape == x.shape
+
+
+@pytest.mark.parametrize("V", [200, 9000])
+def test_many_drafts_of_one_segment(qg, V):
+    """A chain of 200 drafts, most of them a few ids: more than a row's list of a segment holds."""
+    n = 200
+    c = make(3, n, V, batch=1, drafts=True, words=7)
+    r = random.Random(1)
+    c["drafts"] = [r.choice([5, 6, 7, r.randrange(V)]) for _ in range(n)]
+    c["tree"] = [(1 << i + 1) - 1 for i in range(n)]
+    c["seq"] = [0] * n
+    x = torch.randn((n, V), generator=gen(2), device="cuda")
+    check(qg, x, c)
+    c.pop("history"), c.pop("prompt"), c.pop("bias")
+    check(qg, x, c)
 
 
 def test_special_values(qg):
@@ -355,3 +397,78 @@ def test_rotary_positions_beside_the_slots(qg, kind, rot, pairs):
         for mine, other in ((k, k2), (v, v2), (kd, kd2), (vd, vd2)):
             if mine is not None:
                 assert torch.equal(mine[at, :, slot % page], other[0, :, p % page])
+
+
+# ----------------------------------------------------------------------------- streams and devices
+def test_other_streams(qg):
+    from test_gpu_streams import crossed
+    g = gen(3)
+    q_start, lens, pages, n = tables([40, 1], [300, 90], 16, 1, g)
+    k, v, _, _ = make_cache(F16, n, 2, 16, 128, g)
+    q = torch.randn((41, 8, 128), generator=g, device="cuda").half()
+    tree = words_of([(1 << i + 1) - 1 for m in (40, 1) for i in range(m)], 2)
+    ws = qg.qg_attn_workspace_size(128, 8, 2, 41, 2)
+    crossed(qg, lambda s: [qg.qg_attn_shaped(q, k, v, q_start, lens, pages, cap=9.0, max_new=40, stream=s)], [ws, q.nbytes])
+    crossed(qg, lambda s: [qg.qg_attn_tree(q, k, v, q_start, lens, pages, tree, max_new=1, stream=s)], [ws, q.nbytes])
+    parents = ints([-1] + list(range(39)) + [-1])
+    crossed(qg, lambda s: list(qg.qg_tree_masks(parents, q_start, lens, 2, stream=s)), [41 * 4, 41 * 8])
+    keep, one = ints([[0, 5, 9], [0, 0, 0]]), ints([1, 1])
+    crossed(qg, lambda s: [qg.qg_cache_keep(k, v, q_start, lens, pages, keep, one, stream=s)], [8])
+    x = torch.randn((300, 20000), generator=g, device="cuda")
+    h, m = torch.randint(0, 20000, (300, 50), generator=g, device="cuda", dtype=torch.int32), ints([50] * 300)
+    rep = torch.full((300,), 1.5, device="cuda")
+    crossed(qg, lambda s: [qg.qg_logits_adjust(x, history=h, history_len=m, repetition=rep, stream=s)], [x.nbytes])
+
+
+def test_inputs_written_just_before(qg):
+    """What the calls read is the last thing that the stream wrote, by a kernel that has just ended."""
+    x = torch.randn((300, 20000), generator=gen(4), device="cuda")
+    h, m = torch.zeros((300, 60), dtype=torch.int32, device="cuda"), ints([60] * 300)
+    rep = torch.full((300,), 1.5, device="cuda")
+    wanted = [torch.randint(0, 20000, (300, 60), generator=gen(i), device="cuda", dtype=torch.int32) for i in range(6)]
+    want = [qg.qg_logits_adjust(x, history=w, history_len=m, repetition=rep).clone() for w in wanted]
+    got = []
+    for w in wanted:
+        h.copy_(w)
+        got.append(qg.qg_logits_adjust(x, history=h, history_len=m, repetition=rep))
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+
+
+def test_bad_tensors_are_refused(qg):
+    g = gen(5)
+    q_start, lens, pages, n = tables([3], [30], 16, 1, g)
+    k, v, _, _ = make_cache(F16, n, 2, 16, 64, g)
+    q = torch.randn((3, 4, 64), generator=g, device="cuda").half()
+    where = (q, k, v, q_start, lens, pages)
+    tree = ints([[1], [3], [7]])
+    for kw in (dict(slopes=torch.ones(3, device="cuda")), dict(slopes=torch.ones(4, device="cuda").half()), dict(slopes=torch.ones(4)),
+               dict(prefix=ints([1, 2])), dict(first=ints([0, 0])), dict(first=ints([0, 0, 0]).long())):
+        with pytest.raises(ValueError):
+            qg.qg_attn_shaped(*where, **kw)
+    for bad in (tree[:2], tree.long(), tree.view(-1), torch.zeros((3, 0), dtype=torch.int32, device="cuda"), ints([[1, 0], [3, 0], [7, 0]]).t()):
+        with pytest.raises(ValueError):
+            qg.qg_attn_tree(*where, bad)
+    with pytest.raises(ValueError):
+        qg.qg_attn_tree(*where, tree, positions=ints([1, 2]))
+    for cap in (-1.0, math.nan, math.inf):
+        with pytest.raises(qg.QGError):
+            qg.qg_attn_shaped(*where, cap=cap)
+    for args in ((ints([-1, 0, 1]), q_start, lens, 0), (ints([-1, 0, 1]).long(), q_start, lens, 1), (ints([-1, 0, 1]), q_start, ints([30, 1]), 1)):
+        with pytest.raises(ValueError):
+            qg.qg_tree_masks(*args)
+    with pytest.raises(qg.QGError):
+        qg.qg_tree_masks(ints([-1, 0, 1]), q_start, lens, 33)
+    keep, one = ints([[0, 2]]), ints([2])
+    for args in ((k, v[:, :1], q_start, lens, pages, keep, one), (k, v, q_start, lens, pages, keep.view(-1), one), (k, v, q_start, lens, pages, keep, ints([1, 1])),
+                 (k, v, q_start, lens, pages, keep.long(), one), (k[None], v, q_start, lens, pages, keep, one)):
+        with pytest.raises(ValueError):
+            qg.qg_cache_keep(*args)
+    x = torch.randn((2, 100), generator=g, device="cuda")
+    h = ints([[1, 2], [3, 4]])
+    for kw in (dict(history=h), dict(history=h, history_len=ints([1])), dict(repetition=torch.ones(2)), dict(bias_start=ints([0, 1, 2])),
+               dict(allow=ints([[1, 2, 3], [1, 2, 3]])), dict(drafts=ints([1, 2])), dict(seq=ints([0])), dict(out=torch.empty((2, 99), device="cuda")),
+               dict(out=torch.empty((2, 100), dtype=torch.int32, device="cuda")), dict(out_dtype=torch.int8)):
+        with pytest.raises(ValueError):
+            qg.qg_logits_adjust(x, **kw)
