@@ -595,11 +595,11 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
                     // largest |S| allows (most, if not all, rows are below a quarter of the cap: three coefficients)
                     float most = 0.0f;
                     auto reach = [&](const uint32_t (&v)[32]) {  // below 0; the maximum says the rest
-                        float lo[2] = {-most, 0.0f};
+                        float lo[4] = {};
 #pragma unroll
                         for (int i = 0; i < 32; i += 2)
-                            lo[(i / 2) & 1] = fminf(fminf(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), lo[(i / 2) & 1]);
-                        most = -fminf(lo[0], lo[1]);
+                            lo[(i / 2) & 3] = fminf(fminf(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), lo[(i / 2) & 3]);
+                        most = fmaxf(most, -fminf(fminf(lo[0], lo[1]), fminf(lo[2], lo[3])));
                     };
                     auto small_cap = [&](uint64_t x) {  // the factor of S up to a quarter of the cap
                         const uint64_t u = mul_f32x2(x, x);
@@ -824,19 +824,8 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
                         }
                     };
                     auto all = [&](auto is_small) {
-                        if constexpr (Cfg::HOLD && MOD != MOD_PLAIN && MOD != MOD_SHAPED) {
-                            // two chunks in the code, the other two moved into their place
-#pragma unroll 1
-                            for (int c = 0; c < BN / 32; c += 2) {
-                                chunk(c, s[0], is_small);
-                                chunk(c + 1, s[1], is_small);
-#pragma unroll
-                                for (int i = 0; i < 32; ++i) s[0][i] = s[2][i], s[1][i] = s[3][i];
-                            }
-                        } else {
 #pragma unroll (Cfg::HOLD ? BN / 32 : 1)
-                            for (int c = 0; c < BN / 32; ++c) chunk(c, s[Cfg::HOLD ? c : 0], is_small);
-                        }
+                        for (int c = 0; c < BN / 32; ++c) chunk(c, s[Cfg::HOLD ? c : 0], is_small);
                     };
                     if constexpr (MOD == MOD_CAPPED) {
                         // rows whose scores stay below a quarter of the cap, as most do: three coefficients, and no products beside those of the exponents

@@ -549,6 +549,9 @@ int qg_logits_adjust(const void *logits, int type, int64_t ld, void *out, int ou
     if (!a.stream) {
         for (a.seg = LOGITS_SEG; (int64_t)a.seg << a.shift < V; ++a.shift) {}
         a.group = (int)std::min<int64_t>((((int64_t)rows << a.shift) + fill - 1) / fill, LOGITS_GROUP);
+        // rows that divide evenly over the sequences are taken for runs of as many: a block takes whole ones
+        const int run = h.seq && h.batch > 0 && rows % h.batch == 0 ? rows / h.batch : 1;
+        if (run <= LOGITS_GROUP) a.group = std::min((a.group + run - 1) / run, LOGITS_GROUP / run) * run;
     }
     if ((int64_t)rows * logits_segments(V, a.seg, a.shift) > INT32_MAX) return QG_EINVAL;
     const int sms = device_sms();
