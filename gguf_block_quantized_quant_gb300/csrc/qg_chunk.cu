@@ -629,7 +629,7 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
                             }
                         }
                     };
-                    // MOD_BIASED, by tile: what is seen of it lies where its place says and behind the warp's rows, so that the bias is
+                    // MOD_BIASED, by tile: it holds no drafts of a tree, and what is seen of it lies behind the warp's rows, so that the bias is
                     // linear, without a cap (LINEAR) or with one far from the scores (LINEAR_CAP); else GENERAL
                     enum { GENERAL, LINEAR, LINEAR_CAP };
                     auto bend = [&](uint32_t (&v)[32], int c0, auto kind) {
@@ -727,7 +727,7 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
                                 most = fmaxf(most, top(v));
                             });
                         }
-                        if (!(a.sh.positions && key0 + BN > pos0) && __all_sync(0xffffffffu, row_pos >= min(hi, key0 + BN - 1)))
+                        if (!(a.sh.tree && key0 + BN > pos0) && __all_sync(0xffffffffu, row_pos >= min(hi, key0 + BN - 1)))
                             kind = a.sh.cap_out == 0.0f ? LINEAR : __any_sync(0xffffffffu, most > a.sh.small_to) ? GENERAL : LINEAR_CAP;
                         if (kind == LINEAR && !edge)
                             largest(Linear{}, std::false_type{});

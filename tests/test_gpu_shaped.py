@@ -106,7 +106,7 @@ def test_prefixes(qg, kind, D):
     """Prefixes of nothing, inside the new tokens, ending before them, of all, beyond the length, negative; with windows."""
     new, kv = [1, 1, 40, 200, 200, 300, 3], [50, 9, 40, 200, 333, 300, 3]
     for window in (0, 50):
-        check(qg, kind, 4, 2, D, 16, new, kv, prefix=[0, 100, 20, 150, 100, 1 << 30, -5], window=window, seed=window)
+        check(qg, kind, 4, 2, D, 16, new, kv, prefix=[0, 100, 20, 150, 100, (1 << 31) - 1, -(1 << 31)], window=window, seed=window)
     check(qg, kind, 4, 4, D, 48, [2, 4], [80, 4], prefix=[79, 4])
 
 
@@ -213,6 +213,8 @@ def test_masks_of_any_bits(qg, kind):
         for G in (1, 3):
             check(qg, kind, 2 * G, 2, 128, 16, new, kv, tree=bits, words=words, seed=T)
             check(qg, kind, G, 1, 64, 16, new, kv, tree=bits, words=words, window=3, seed=T, slopes=alibi(G), positions=[kv[0] - 2] * T)
+            # drafts that see later ones, whose distance counts as any
+            check(qg, kind, 2 * G, 2, 128, 16, new, kv, tree=bits, words=words, seed=T, slopes=alibi(2 * G), cap=(0.0, 25.0)[G // 3])
 
 
 def test_rows_of_a_tree_that_see_nothing(qg):
@@ -291,3 +293,42 @@ def test_results_do_not_depend_on_timing_and_replay(qg):
             graph.replay()
             torch.cuda.synchronize()
             assert torch.equal(out, want)
+
+
+def test_rows_and_tokens_of_no_sequence(qg):
+    """Tokens before the first sequence's and behind the last one's give zeros; what the masks hold for them is not looked at."""
+    g = gen(6)
+    new, kv = [30, 2], [90, 40]
+    q_start, lens, pages, n = tables(new, kv, 16, 1, g)
+    k, v, _, _ = make_cache(F16, n, 2, 16, 64, g)
+    q = torch.randn((40, 4, 64), generator=g, device="cuda").half()
+    bits, pos = random_trees(new, kv, seed=2)
+    pad = lambda x, fill: [fill] * 3 + list(x) + [fill] * 5  # noqa: E731
+    for hint in (1, 30):
+        out = qg.qg_attn_tree(q, k, v, q_start + 3, lens, pages, words_of(pad(bits, 0xffffffff), 1), positions=ints(pad(pos, -9)), max_new=hint)
+        want = qg.qg_attn_tree(q[3:35].contiguous(), k, v, q_start, lens, pages, words_of(bits, 1), positions=ints(pos), max_new=hint)
+        assert torch.equal(out[3:35], want) and (out[:3] == 0).all() and (out[35:] == 0).all()
+        first = [0] * 10 + [70] * 20 + [0, 39]
+        out = qg.qg_attn_shaped(q, k, v, q_start + 3, lens, pages, first=ints(pad(first, 1 << 30)), cap=9.0, max_new=hint)
+        want = qg.qg_attn_shaped(q[3:35].contiguous(), k, v, q_start, lens, pages, first=ints(first), cap=9.0, max_new=hint)
+        assert torch.equal(out[3:35], want) and (out[:3] == 0).all() and (out[35:] == 0).all()
+
+
+def test_bad_lengths_and_pages_stay_inside(qg):
+    """Lengths, starts and page ids beyond the arrays are held to them, whatever the masks."""
+    g = gen(7)
+    k, v, _, _ = make_cache(F16, 6, 2, 16, 64, g)
+    q = torch.randn((20, 4, 64), generator=g, device="cuda").half()
+    pages = ints([[0, 1, 99], [-4, 2, 1 << 30]])
+    tree, positions, first = words_of([(1 << 32) - 1] * 20, 1), ints([1 << 30, -5] * 10), ints([-3, 1 << 30] * 10)
+    for starts in ([0, 10, 20], [-7, 15, 900], [5, 2, 20], [0, 0, 0]):
+        for lens in ([48, 48], [1 << 30, -5], [0, 3]):
+            for hint in (1, 20):
+                a = qg.qg_attn_tree(q, k, v, ints(starts), ints(lens), pages, tree, positions=positions, window=7, slopes=alibi(4), cap=5.0, max_new=hint)
+                b = qg.qg_attn_shaped(q, k, v, ints(starts), ints(lens), pages, prefix=ints([1 << 30, -1]), first=first, cap=5.0, max_new=hint)
+                torch.cuda.synchronize()
+                assert a.shape == b.shape == q.shape and qg.qg_device_error() == 0
+        qg.qg_tree_masks(ints([7, -9] * 10), ints(starts), ints([48, -2]), 1)
+        for keep_len in ([5, 5], [99, -1]):
+            qg.qg_cache_keep(k, v, ints(starts), ints([48, 40]), pages, ints([[0, 3, 5, 1 << 30, -8], [9, 9, 9, 9, 9]]), ints(keep_len))
+        torch.cuda.synchronize()
