@@ -42,6 +42,17 @@
 // 179).  With two row tiles and 16-bit caches the tensor cores are the bound for long chunks, the
 // exponentials (16 a clock and SM) at dim 64.
 //
+// Other masks and scores (QG_MOD) change the softmax role, the plan and what the copies zero, nothing of the products:
+//   * a row sees an interval of slots (documents, prefixes, windows), and beside a tree the drafts of its mask, whose bits
+//     it reads for the tiles that hold them; the plan takes each row tile's union;
+//   * a cap keeps the order of a row's scores, so the maximum is capped alone, and the exponents' factor of S becomes
+//     a polynomial in S^2: three coefficients where all rows of the warp stay below a quarter of the cap (relative error 5e-7), else
+//     five or 1 - 2 / (1 + e^2x).  2048 tokens after 6000, 32/8 heads of 128, bf16: 258 us against 196 uncapped (64: 206 against
+//     152, 256: 423 against 380, 8-bit 428 against 385).  The minimum that tells a row's reach and the second form take 45 of
+//     the 60 us; by the largest size in the maximum's place 251, one form for both with factors in registers 268;
+//   * a bias by distance is linear over tiles behind the rows: sums of eight slopes, half an instruction per score, 234 us (with
+//     the distance formed for each slot 350).
+//
 // Work is counted in slot tiles over all items (row tile, cache head).  Where dealing whole items out,
 // the largest first and back and forth over the CTAs, loads them evenly enough, that is done: no
 // partial results, nothing to merge.  Else the list is cut into one equal range per CTA, so that
@@ -683,8 +694,8 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
                         }
                     };
                     float mx = -INFINITY;
-                    // The row's maximum.  Kinds of tiles have loops of their own: a branch per 32 scores keeps the
-                    // compiler from running one chunk's steps under another's (2048 tokens after 6000, dim 128, capped: 360 us)
+                    // The row's maximum.  Kinds of tiles have loops of their own: a branch per 32 scores keeps the compiler from
+                    // running one chunk's steps under another's (2048 tokens after 6000, dim 128, capped: 360 us with, 282 without)
                     auto largest = [&](auto kind, auto is_edge) {
                         each([&](uint32_t (&v)[32], int c0) {
                             if constexpr (MOD == MOD_CAPPED) {

@@ -60,7 +60,8 @@ __global__ void __launch_bounds__(TREE_THREADS) tree_masks_kernel(const int32_t 
 // A thread owns 16 bytes of every slot of a head (4 bytes of its steps) and moves them for all kept drafts in order,
 // KEEP_U loads in flight.  Index i takes from keep[i] >= i only, so a place is never written before what is still to be
 // read from it: within a thread in order, and no two threads meet at a byte.  A launch and four dependent loads (lengths,
-// indices, pages, data); the bytes that move are few.
+// indices, pages, data); the bytes that move are few: 5 of 16 drafts in one layer of 8 heads of 128 2.6 us in a graph (4 to 5 called
+// one by one), 6 of 48 in 32 sequences and 16 layers 5.5 us, of which the bytes are 2.8.
 constexpr int KEEP_THREADS = 256, KEEP_MAX = 1024, KEEP_U = 8;
 
 struct KeepArgs {
@@ -147,7 +148,8 @@ __global__ void __launch_bounds__(KEEP_THREADS) keep_lengths_kernel(const KeepAr
 // The stream is bound by memory, the rest by a chain of dependent loads (sequence, lengths, ids, logits).  Small calls do both in
 // one kernel; large ones stream in a kernel of many light blocks, under whose end the counts of a second are made.  One
 // kernel for 192 rows of 131071, bf16 to fp32: 97 us with the counts beside the stream, 60 to 70 with lists, as the chains
-// of the few blocks that fit an SM do not hide each other.
+// of the few blocks that fit an SM do not hide each other; two kernels 48 us, of which the stream is 28 (0.83 of the
+// measured copy bandwidth).  One row of 32000, fp32, a history of 600: 4.2 us.
 struct LogitsArgs {
     const void *x;
     void *out;
