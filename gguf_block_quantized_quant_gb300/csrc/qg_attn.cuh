@@ -85,17 +85,6 @@ __device__ __forceinline__ Seen seen_by(const AttnArgs &a, const Seq &s, int b, 
 __device__ __forceinline__ int needs_from(const AttnArgs &a, const Seq &s, const Seen &v) {
     return a.sh.tree && v.lo != 0x7fffffff ? min(v.lo, max(s.len - s.n, 0)) : v.lo;
 }
-// The first slot that some token of the sequence needs.  A function of its own: it is asked for in many places.
-static __device__ __noinline__ int first_needed(const int32_t *first, const int32_t *positions, int window, int base, int n, int len) {
-    int low = len;
-#pragma unroll 4
-    for (int i = 0; i < n; ++i) {
-        const int slot = base + i;  // below 0: padding
-        const int from = first ? max(first[i], seen_from(slot, window)) : min(seen_from(positions ? positions[i] : slot, window), max(base, 0));
-        if (slot >= 0 && (!first || from <= len - 1)) low = min(low, from);
-    }
-    return low;
-}
 // 32 bits of a row of a tree's mask from bit `at` on; the bits before 0 are set, those past the row are not.
 __device__ __forceinline__ uint32_t tree_bits(const uint32_t *row, int words, int at) {
     const int w = at >> 5;

@@ -78,6 +78,17 @@ struct DecCfg {
     static_assert(MERGE_AT % 16 == 0 && ML_AT % 8 == 0 && QS_AT % 16 == 0 && BAR_AT % 8 == 0 && S >= 2, "layout");
 };
 
+// The first slot that some token of the sequence needs.  A function of its own: it is asked for in many places.
+static __device__ __noinline__ int first_needed(const int32_t *first, const int32_t *positions, int window, int base, int n, int len) {
+    int low = len;
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) {
+        const int slot = base + i;  // below 0: padding
+        const int from = first ? max(first[i], seen_from(slot, window)) : min(seen_from(positions ? positions[i] : slot, window), max(base, 0));
+        if (slot >= 0 && (!first || from <= len - 1)) low = min(low, from);
+    }
+    return low;
+}
 // The blocks of one sequence: every item (cache head, row tile) of it has the same slots.
 template <int ROWS, int OV, int MOD>
 struct SeqWork {

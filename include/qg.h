@@ -69,7 +69,7 @@ enum qg_format {
 };
 
 /* Element types of the decoder-layer operators (qg_norm_residual, qg_rope_append,
- * qg_attn_paged), numbered by their GGUF type ids.  A cache is QG_F16, QG_BF16 or QG_Q8_0. */
+ * qg_attn_paged and those beside them), numbered by their GGUF type ids.  A cache is QG_F16, QG_BF16 or QG_Q8_0. */
 enum qg_type { QG_F32 = 0, QG_F16 = 1, QG_BF16 = 30 };
 
 /* Frequency scalings of qg_rope_turns(). */
