@@ -85,6 +85,9 @@ __device__ __forceinline__ Seen seen_by(const AttnArgs &a, const Seq &s, int b, 
 __device__ __forceinline__ int needs_from(const AttnArgs &a, const Seq &s, const Seen &v) {
     return a.sh.tree && v.lo != 0x7fffffff ? min(v.lo, max(s.len - s.n, 0)) : v.lo;
 }
+// How far positions are apart.  Whole numbers are subtracted, as fp32 does not hold positions past 2^24, and to one without
+// a sign, as a caller's positions may be 2^32 apart.
+__device__ __forceinline__ float distance(int p, int j) { return (float)__sad(p, j, 0u); }
 // 32 bits of a row of a tree's mask from bit `at` on; the bits before 0 are set, those past the row are not.
 __device__ __forceinline__ uint32_t tree_bits(const uint32_t *row, int words, int at) {
     const int w = at >> 5;

@@ -401,11 +401,11 @@ __device__ __forceinline__ int chunk_ctas(int64_t total, int max_ctas) {
 __device__ __forceinline__ bool chunk_far(float m, float scale2) { return !(fabsf(m * scale2) < 4194304.0f); }
 
 // The position of slot `key`; one load at a time, as many registers are in use where it is called.
-__device__ __forceinline__ float slot_position(const AttnArgs &a, int first, int base, int n, int key) {
+__device__ __forceinline__ int slot_position(const AttnArgs &a, int first, int base, int n, int key) {
     int p = key;
     if (key >= base && key < base + n)
         asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(p) : "l"(a.sh.positions + first + (key - base)));
-    return (float)p;
+    return p;
 }
 
 // ----------------------------------------------------------------------------- kernel
@@ -646,8 +646,8 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
                     auto bend = [&](uint32_t (&v)[32], int c0, auto kind) {
                         constexpr int KIND = decltype(kind)::value;
                         const int key = key0 + c0;
-                        const float d = (float)(row_pos - key);
                         if constexpr (KIND != GENERAL) {
+                            const float d = (float)(row_pos - key);  // row_pos is not below 0, or the row sees nothing here
                             // the bias of every eighth slot is the last one's and 8 slopes: three sums, half an instruction each
                             const uint64_t in2 = pack_f32x2(a.scale2, a.scale2), step = pack_f32x2(8.0f * slope, 8.0f * slope);
                             uint64_t at[4];
@@ -672,8 +672,9 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
 #pragma unroll
                                 for (int i = 0; i < 32; ++i)
                                     v[i] = __float_as_uint(fmaf(__uint_as_float(v[i]), in,
-                                                                -slope * fabsf((float)row_pos - slot_position(a, k.t.first, pos0, k.t.n, key + i))));
+                                                                -slope * distance(row_pos, slot_position(a, k.t.first, pos0, k.t.n, key + i))));
                             } else {
+                                const float d = row_pos < key ? -distance(row_pos, key) : distance(row_pos, key);
 #pragma unroll
                                 for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(fmaf(__uint_as_float(v[i]), in, -slope * fabsf(d - (float)i)));
                             }

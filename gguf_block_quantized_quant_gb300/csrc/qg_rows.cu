@@ -475,7 +475,7 @@ __global__ void __launch_bounds__(DecCfg<C, D, NR>::NW * 32, 1)
                         const int drafted = key - base_slot;  // the slot's place among the new tokens
                         if (a.sh.slopes) {
                             const int at = a.sh.positions && drafted >= 0 && drafted < sq.n ? a.sh.positions[sq.first + drafted] : key;
-                            s[r][j] = fmaf(-slope[r][i], fabsf((float)pos[r][i] - (float)at), s[r][j]);
+                            s[r][j] = fmaf(-slope[r][i], distance(pos[r][i], at), s[r][j]);
                         }
                         if (edge) {
                             bool see = key <= hi[r][i] && key >= lo[r][i];
