@@ -46,10 +46,12 @@
 //   * a row sees an interval of slots (documents, prefixes, windows), and beside a tree the drafts of its mask, whose bits
 //     it reads for the tiles that hold them; the plan takes each row tile's union;
 //   * a cap keeps the order of a row's scores, so the maximum is capped alone, and the exponents' factor of S becomes
-//     a polynomial in S^2: three coefficients where all rows of the warp stay below a quarter of the cap (relative error 5e-7), else
-//     five or 1 - 2 / (1 + e^2x).  2048 tokens after 6000, 32/8 heads of 128, bf16: 258 us against 196 uncapped (64: 206 against
-//     152, 256: 423 against 380, 8-bit 428 against 385).  The minimum that tells a row's reach and the second form take 45 of
-//     the 60 us; by the largest size in the maximum's place 251, one form for both with factors in registers 268;
+//     a polynomial in S^2: three coefficients where all rows of the warp stay below a quarter of the cap (relative error 5e-7), five
+//     up to three quarters (7e-7), and where some score lies beyond, three for each score up to a quarter and 1 - 2 / (1 + e^2x) for the
+//     others (2^-20).  2048 tokens after 6000, 32/8 heads, fp16, dims 64, 128, 256 and 8-bit 128, us: 151, 197, 377, 383 uncapped; caps of 50
+//     with scores of a spread of 2 (the first form) 203, 251, 414, 427, of 8 (the second and third) 439, 535, 475, 587, of 20 (the third) 484, 570,
+//     561, 639: two more special functions per score.  In the first form the minimum that tells a row's reach and the code of the others
+//     take most of what it has over the uncapped kernel.  Beside a bias the first and the third;
 //   * a bias by distance is linear over tiles behind the rows: sums of eight slopes, half an instruction per score, 234 us (with
 //     the distance formed for each slot 350).
 //
@@ -602,8 +604,8 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
                             x[(i / 2) & 3] = fmaxf(fmaxf(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), x[(i / 2) & 3]);
                         return fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
                     };
-                    // From S to the scores as powers of two's exponents, where these are no multiple of S: capped by what the row's
-                    // largest |S| allows (most, if not all, rows are below a quarter of the cap: three coefficients)
+                    // From S to the scores as powers of two's exponents, where these are no multiple of S: capped by what the largest |S| of
+                    // the warp's rows allows
                     float most = 0.0f;
                     auto reach = [&](const uint32_t (&v)[32]) {  // below 0; the maximum says the rest
                         float lo[4] = {};
@@ -618,12 +620,24 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
                                          pack_f32x2(a.sh.small[0], a.sh.small[0]));
                     };
                     auto capped = [&](uint32_t (&v)[32]) {
-                        if (most * a.sh.cap_in > TANH_NEAR) {  // 1 - 2 / (1 + e^2x) is exact enough beside the row's largest
+                        if (MOD == MOD_BIASED || __any_sync(0xffffffffu, most * a.sh.cap_in > TANH_NEAR)) {
+                            // 1 - 2 / (1 + e^2x) is off by some 2^-22 of the cap whatever x is, and the scores that count need not be the
+                            // largest in size: up to a quarter of the cap each takes the three coefficients (beyond, that is 2^-20 relative).
+                            // The warp as one: rows apart by their own reach had warps run both branches, and with five coefficients beside
+                            // this form for each score dim 128 took 799 us where it takes 535, as the compiler branched for each pair.  Beside a
+                            // bias this form is the only one: one code more there cost plain biases 5 %, and caps that are reached 15 %.  Where
+                            // small_to is below 0, |S| is over 7e6 and its own sum no better than 2^-22 of the cap, or the cap so small that this is nothing
                             const float k = a.sh.cap_in * (2.0f * LOG2E), m2 = -2.0f * a.sh.cap_out;
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) {
-                                const float e = exp2_approx(__uint_as_float(v[i]) * k);
-                                v[i] = __float_as_uint(fmaf(m2, rcp_approx(1.0f + e), a.sh.cap_out));
+                            for (int i = 0; i < 32; i += 2) {
+                                const uint64_t x = pack_b32x2(v[i], v[i + 1]);
+                                float y[2];
+                                unpack_f32x2(mul_f32x2(x, small_cap(x)), y[0], y[1]);
+#pragma unroll
+                                for (int j = 0; j < 2; ++j) {
+                                    const float z = __uint_as_float(v[i + j]), e = exp2_approx(z * k), t = fmaf(m2, rcp_approx(1.0f + e), a.sh.cap_out);
+                                    v[i + j] = __float_as_uint(fabsf(z) <= a.sh.small_to ? y[j] : t);
+                                }
                             }
                         } else {
                             const uint64_t in2 = pack_f32x2(a.sh.cap_in, a.sh.cap_in);
@@ -840,7 +854,7 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
                         for (int c = 0; c < BN / 32; ++c) chunk(c, s[Cfg::HOLD ? c : 0], is_small);
                     };
                     if constexpr (MOD == MOD_CAPPED) {
-                        // rows whose scores stay below a quarter of the cap, as most do: three coefficients, and no products beside those of the exponents
+                        // where all scores stay below a quarter of the cap: three coefficients, and no products beside those of the exponents
                         if (!__any_sync(0xffffffffu, most > a.sh.small_to))
                             all(std::true_type{});
                         else

@@ -1,9 +1,9 @@
-"""qg_attn_shaped and qg_attn_tree where fp32 is short: distances between positions that fp32 does not hold."""
+"""qg_attn_shaped and qg_attn_tree where fp32 is short: distances between positions that fp32 does not hold, scores near 0 under large caps."""
 import pytest
 import torch
 
 from draft_testlib import attention, bounds, intervals
-from layer_testlib import BF16, F16, F32, gen, make_cache, within
+from layer_testlib import BF16, F16, F32, gen, make_cache, tables, within
 from qg_testlib import qg_module
 from test_gpu_shaped import alibi, check, ints, random_trees
 
@@ -50,3 +50,40 @@ def test_distances_between_positions_past_2_to_24(qg, kind, D, start):
     for hint in (1, 130):
         check(qg, kind, 4, 2, D, 16, new, kv, tree=bits, words=5, positions=[start + x for x in depth], slopes=alibi(4), max_new=hint, seed=D)
         check(qg, kind, 2, 1, D, 32, new, kv, tree=bits, words=5, positions=[start + x for x in depth], slopes=alibi(2), cap=15.0, window=50, max_new=hint)
+
+
+@pytest.mark.parametrize("biased", [False, True])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("kind", KINDS, ids=IDS)
+def test_caps_where_only_unlikely_scores_reach_them(qg, kind, D, biased):
+    """Scores near 0 lead and others lie at the lower end of a large cap, so that the fit of tanh near 0 counts and not that of its ends.
+
+    With entries of 1 and -1 in u, keys are u / 32 or -112 u and queries 33 to 128 times u / 64: products and their sums are whole
+    multiples of 2^-11 below 2^5, or of 2^-2 below 2^17, and exact in fp32, as are 8-bit keys in fp16 (codes 1 and -112, steps 2^-5 and 1)
+    and scale / cap.  What is left for the scores near 0, z = 1 to 4, is the fit and the products around it, 2^-19 z, and the rounding of exponents and
+    of the logarithm, 2^-22 of each; exponentials and their sum in fp32 are 2^-18 on the logarithm.  Scores near the lower end,
+    below -0.69 caps, have a probability of 0.  (2^-22 of the cap would be 1e-3.)"""
+    g, page, Hk, H, n, cap = gen(D), 32, 2, 4, 300, 4096.0
+    q_start, lens, pages, n_pages = tables([n, 1], [n, n], page, 1, g)
+    u = torch.randint(0, 2, (Hk, D), generator=g, device="cuda") * 2 - 1
+    k, v, kd, vd = make_cache(kind, n_pages, Hk, page, D, g)
+    far = torch.arange(n_pages * page, device="cuda").view(n_pages, 1, page, 1) % 16 == 5
+    keys = u.view(1, Hk, 1, D) * torch.where(far, -112.0, 2.0 ** -5)
+    if kind == "q8":
+        step = torch.where(far, 1.0, 2.0 ** -5)
+        k.copy_((keys / step).to(torch.int8))
+        kd.copy_(step.expand(n_pages, Hk, page, D // 32))
+    else:
+        k.copy_(keys)
+    c = torch.randint(33, 129, (n + 1, H, 1), generator=g, device="cuda").double() / 64
+    q = (c * u.repeat_interleave(H // Hk, 0)).to(F16 if kind == "q8" else kind)
+    scale = 64.0 / D
+    slopes = torch.zeros((H,), device="cuda") if biased else None
+    for hint in (1, n):
+        lse = torch.empty((n + 1, H), device="cuda")
+        qg.qg_attn_shaped(q, k, v, q_start, lens, pages, kd=kd, vd=vd, cap=cap, slopes=slopes, scale=scale, max_new=hint, lse=lse)
+        want = attention(q, k, v, kd, vd, [n, 1], [n, n], pages, scale, intervals([n, 1], [n, n]), cap, slopes)[1]
+        bound = 2.0 ** -18 + 2.0 ** -19 * 4 + 2.0 ** -22 * (4 + want.abs())
+        worst = ((lse.double() - want).abs() / bound).max().item()
+        assert worst <= 1, (hint, worst)
+    assert qg.qg_device_error() == 0
