@@ -127,9 +127,8 @@ struct ChunkCfg {
     static constexpr uint32_t KV_AT = OUT_AT + NQ * 4 * 2048;
     static constexpr uint32_t RAW_AT = KV_AT + NS * TILE;
     static constexpr uint32_t BAR_AT = RAW_AT + (Q8 ? NRAW * (CODES + STEPS) : 0);
-    static constexpr uint32_t HALVES_AT = BAR_AT + NBAR * 8 + 8 /* tensor memory address, turn */;  // what shared row tiles exchange
-    static constexpr uint32_t BYTES = HALVES_AT + (NQ == 2 ? 2 * 128 * 8 : 0) + 1024 /* alignment */;
-    static_assert(OUT_AT % 1024 == 0 && KV_AT % 1024 == 0 && RAW_AT % 1024 == 0 && BAR_AT % 16 == 0 && HALVES_AT % 8 == 0 && TILE % 1024 == 0 && CODES % 1024 == 0 &&
+    static constexpr uint32_t BYTES = BAR_AT + NBAR * 8 + 8 /* tensor memory address, turn */ + 1024 /* alignment */;
+    static_assert(OUT_AT % 1024 == 0 && KV_AT % 1024 == 0 && RAW_AT % 1024 == 0 && BAR_AT % 16 == 0 && TILE % 1024 == 0 && CODES % 1024 == 0 &&
                       STEPS % 16 == 0,
                   "alignment");
     // tensor memory columns
