@@ -71,7 +71,7 @@
 #include "qg_umma.h"
 
 #ifndef QG_MOD
-#error "QG_MOD is MOD_PLAIN, MOD_SHAPED or MOD_CAPPED"
+#error "QG_MOD is MOD_PLAIN, MOD_SHAPED, MOD_CAPPED or MOD_BIASED"
 #endif
 
 namespace qg {
