@@ -2,7 +2,7 @@
 import pytest
 import torch
 
-from draft_testlib import attention, bounds, intervals
+from draft_testlib import attention, bounds, intervals, trees, words_of
 from layer_testlib import BF16, F16, F32, gen, make_cache, tables, within
 from qg_testlib import qg_module
 from test_gpu_shaped import alibi, check, ints, random_trees
@@ -87,3 +87,55 @@ def test_caps_where_only_unlikely_scores_reach_them(qg, kind, D, biased):
         worst = ((lse.double() - want).abs() / bound).max().item()
         assert worst <= 1, (hint, worst)
     assert qg.qg_device_error() == 0
+
+
+@pytest.mark.parametrize("kind", KINDS, ids=IDS)
+def test_scores_in_the_row_kernel(qg, kind):
+    """Caps and biases to the last bits that fp32 leaves them.  The row kernel multiplies 8-bit codes as they are and probabilities as two
+    addends, so that scores are off as on 16-bit caches and, but for 8-bit values, the result as by its rounding alone (bounds' term of the
+    probabilities' type is fp32's; the 2^-16 beside it holds two addends of 8 bits)."""
+    for D in (64, 128, 256):
+        for new, kv, tree in (([1, 1, 1], [3, 333, 2500], False), ([2, 1, 3], [40, 900, 3], False), ([5, 8], [700, 8], True)):
+            g = gen(D)
+            q_start, lens, pages, n_pages = tables(new, kv, 32, 1, g)
+            k, v, kd, vd = make_cache(kind, n_pages, 2, 32, D, g)
+            q = (2 * torch.randn((sum(new), 4, D), generator=g, device="cuda")).to(F16 if kind == "q8" else kind)
+            bits, pos = random_trees(new, kv, seed=D)
+            views = trees(new, kv, bits, pos) if tree else intervals(new, kv)
+            for cap, slopes in ((3.0, None), (30.0, None), (0.0, alibi(4)), (20.0, alibi(4) / 8)):
+                lse = torch.empty((sum(new), 4), device="cuda")
+                kw = dict(kd=kd, vd=vd, cap=cap, slopes=slopes, max_new=1, lse=lse, out_dtype=F32)
+                if tree:
+                    out = qg.qg_attn_tree(q, k, v, q_start, lens, pages, words_of(bits, 1), positions=ints(pos), **kw)
+                else:
+                    out = qg.qg_attn_shaped(q, k, v, q_start, lens, pages, **kw)
+                ref = attention(q, k, v, kd, vd, new, kv, pages, D ** -0.5, views, cap, slopes)
+                bound, lse_bound = bounds(*ref, F32, F32, kind == "q8")
+                within(out, ref[0], bound, "out")
+                assert ((lse.double() - ref[1]).abs() <= lse_bound).all()
+    assert qg.qg_device_error() == 0
+
+
+# ----------------------------------------------------------------------------- plans of many tiles
+def documents(new, kv_len, every):
+    """The first slot of each token's document: one begins at every `every`-th new token; those before the first go on with the past."""
+    return [max(0, L - n + i // every * every if i >= every else 0) for n, L in zip(new, kv_len) for i in range(n)]
+
+
+@pytest.mark.parametrize("sequences,tokens", [(9, 490), (3, 1300), (20, 460)])
+def test_plans_of_hundreds_and_thousands_of_row_tiles(qg, sequences, tokens):
+    """Eight tokens to a row tile (16 heads to a cache head of 256): 561, 490 and 1172 tiles, past what the plan puts in order and past a
+    round of its threads, where it looks every token's range up."""
+    new = [tokens + 3 * (b % 5) for b in range(sequences)]
+    kv = [n + (0, 5, 70)[b % 3] for b, n in enumerate(new)]
+    check(qg, F16, 16, 1, 256, 64, new, kv, first=documents(new, kv, 37), cap=20.0, window=90, seed=sequences)
+
+
+def test_plans_of_more_sequences_than_a_round(qg):
+    """2100 sequences, most of a token or none: the plan's lists of sequences are made anew twice."""
+    new = [(1, 0, 3, 9, 1, 2)[b % 6] for b in range(2100)]
+    kv = [n + (0, 3, 17, 40)[b % 4] for b, n in enumerate(new)]
+    check(qg, F16, 16, 1, 64, 16, new, kv, first=documents(new, kv, 4), max_new=30, seed=1)
+    check(qg, "q8", 16, 1, 256, 16, new, kv, slopes=alibi(16), max_new=30, seed=2)
+    bits, pos = random_trees(new, kv, seed=4)
+    check(qg, BF16, 16, 1, 128, 16, new, kv, tree=bits, positions=pos, window=20, cap=9.0, max_new=30, seed=3)
