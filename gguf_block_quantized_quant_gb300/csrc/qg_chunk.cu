@@ -619,27 +619,29 @@ __global__ void __launch_bounds__(ChunkCfg<C, D>::THREADS, 1)
                                          pack_f32x2(a.sh.small[0], a.sh.small[0]));
                     };
                     auto capped = [&](uint32_t (&v)[32]) {
+                        const uint64_t in2 = pack_f32x2(a.sh.cap_in, a.sh.cap_in);
                         if (MOD == MOD_BIASED || __any_sync(0xffffffffu, most * a.sh.cap_in > TANH_NEAR)) {
                             // 1 - 2 / (1 + e^2x) is off by some 2^-22 of the cap whatever x is, and the scores that count need not be the
                             // largest in size: up to a quarter of the cap each takes the three coefficients (beyond, that is 2^-20 relative).
                             // The warp as one: rows apart by their own reach had warps run both branches, and with five coefficients beside
                             // this form for each score dim 128 took 799 us where it takes 535, as the compiler branched for each pair.  Beside a
-                            // bias this form is the only one: one code more there cost plain biases 5 %, and caps that are reached 15 %.  Where
-                            // small_to is below 0, |S| is over 7e6 and its own sum no better than 2^-22 of the cap, or the cap so small that this is nothing
+                            // bias this form is the only one: one code more there cost plain biases 5 %, and caps that are reached 15 %
                             const float k = a.sh.cap_in * (2.0f * LOG2E), m2 = -2.0f * a.sh.cap_out;
+                            const float c0 = TANH_S0 * a.sh.cap_out, c1 = TANH_S1 * a.sh.cap_out, c2 = TANH_S2 * a.sh.cap_out;
+                            const uint64_t p0 = pack_f32x2(c0, c0), p1 = pack_f32x2(c1, c1), p2 = pack_f32x2(c2, c2);
 #pragma unroll
                             for (int i = 0; i < 32; i += 2) {
-                                const uint64_t x = pack_b32x2(v[i], v[i + 1]);
-                                float y[2];
-                                unpack_f32x2(mul_f32x2(x, small_cap(x)), y[0], y[1]);
+                                const uint64_t x = mul_f32x2(pack_b32x2(v[i], v[i + 1]), in2), u = mul_f32x2(x, x);
+                                float z[2], y[2];
+                                unpack_f32x2(x, z[0], z[1]);
+                                unpack_f32x2(mul_f32x2(x, fma_f32x2(u, fma_f32x2(u, p2, p1), p0)), y[0], y[1]);
 #pragma unroll
                                 for (int j = 0; j < 2; ++j) {
-                                    const float z = __uint_as_float(v[i + j]), e = exp2_approx(z * k), t = fmaf(m2, rcp_approx(1.0f + e), a.sh.cap_out);
-                                    v[i + j] = __float_as_uint(fabsf(z) <= a.sh.small_to ? y[j] : t);
+                                    const float e = exp2_approx(__uint_as_float(v[i + j]) * k), t = fmaf(m2, rcp_approx(1.0f + e), a.sh.cap_out);
+                                    v[i + j] = __float_as_uint(fabsf(z[j]) <= TANH_SMALL ? y[j] : t);
                                 }
                             }
                         } else {
-                            const uint64_t in2 = pack_f32x2(a.sh.cap_in, a.sh.cap_in);
                             uint64_t k[5];
 #pragma unroll
                             for (int i = 0; i < 5; ++i) k[i] = pack_f32x2(a.sh.poly[i], a.sh.poly[i]);

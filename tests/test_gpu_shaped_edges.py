@@ -139,3 +139,12 @@ def test_plans_of_more_sequences_than_a_round(qg):
     check(qg, "q8", 16, 1, 256, 16, new, kv, slopes=alibi(16), max_new=30, seed=2)
     bits, pos = random_trees(new, kv, seed=4)
     check(qg, BF16, 16, 1, 128, 16, new, kv, tree=bits, positions=pos, window=20, cap=9.0, max_new=30, seed=3)
+
+
+@pytest.mark.parametrize("cap", [1e-3, 1.0, 4.0, 20.0, 1e4, 1e8, 1e30])
+@pytest.mark.parametrize("scale", [0.0, 1.0, -0.25, None])
+def test_caps_and_biases_against_the_scores_size(qg, cap, scale):
+    """Scores far beyond the cap, around it and far below, beside biases that count, and that are nothing; in prefixes ahead of their rows too."""
+    for slopes in (alibi(4), torch.zeros((4,), device="cuda")):
+        for kind, D in ((F16, 128), (BF16, 256), ("q8", 64), ("q8", 256)):
+            check(qg, kind, 4, 2, D, 16, [1, 90], [300, 400], cap=cap, scale=scale, slopes=slopes, prefix=[0, 380])
