@@ -1,5 +1,6 @@
 // qg_attn.cu -- attention over a paged cache: the C entry points and tensor maps.
 #include <algorithm>
+#include <cfloat>
 #include <cmath>
 #include <mutex>
 #include <set>
@@ -131,9 +132,10 @@ static int attn_other(const AttnArgs &a, const qg_paged &c, int max_new, int sms
     return attn_rows<MOD_SHAPED>(a, c, (int64_t)max_new * a.G <= 8 ? 1 : 2, sms, s);
 }
 
-// The cap and the slopes of a call.
+// The cap and the slopes of a call.  A quotient scale / cap below the normal numbers has lost the bits of the scale.
 static int shape_check(float scale, float cap, const float *slopes) {
-    if (!(cap >= 0.0f) || (cap > 0.0f && !(std::isfinite(scale / cap) && std::isfinite(cap * LOG2E)))) return QG_EINVAL;
+    if (!(cap >= 0.0f)) return QG_EINVAL;
+    if (cap > 0.0f && (!std::isfinite(scale / cap) || !std::isfinite(cap * LOG2E) || (scale != 0.0f && std::abs(scale / cap) < FLT_MIN))) return QG_EINVAL;
     return host_aligned(slopes, 4) ? QG_OK : QG_EALIGN;
 }
 static void shape_scores(AttnArgs &a, float scale, float cap, const float *slopes) {

@@ -335,7 +335,7 @@ int qg_attn_paged(const void *q, int64_t ldq, int64_t hdq, int q_type, int token
 /* Attention of the new tokens over the cache as qg_attn_paged, with scores and masks of other kinds (0 or NULL: as there):
  *   z = scale * q.k;   z = cap * tanh(z / cap)   (cap > 0);   z = z - slopes[g] * |p - j|   (query head g, slot j)
  * over the slots   max(0, p - window + 1, first[t]) <= j <= max(p, prefix[b] - 1),   j < kv_len[b].
- *   cap: finite, with finite scale / cap.   slopes: q_heads fp32.
+ *   cap: finite, with scale / cap finite and 0 or a normal number.   slopes: q_heads fp32.
  *   prefix: batch; the first prefix[b] slots are seen by every token of the sequence, its earlier ones too, as far as they
  *   are appended and window and first allow.   first: tokens; the first slot of the document that token t belongs to, in
  *   slots of its sequence (tokens of a packed prompt; 0 where a token sees everything before it).  Values at or below 0 allow
