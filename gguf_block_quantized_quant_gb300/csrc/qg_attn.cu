@@ -115,7 +115,8 @@ static int attn_plain(const AttnArgs &a, const qg_paged &c, int max_new, int sms
 // microseconds of the chunk kernel's start: that wins where the tiles are few and the caches, as large as the page table
 // allows, small.  us, chunk and row kernel (fp16, 32/8 heads of 128): 16 drafts of one sequence after 1000 18.6, 15.8; 8
 // after 4000 22.1, 17.5; 32 after 1000 20.9, 22.2; 8 of 4 sequences after 1000 22.0, 20.9; 16 after 300 20.2, 21.7.  (16-bit
-// heads of 256: 8 after 1000 18.5, 19.8.)
+// heads of 256: 8 after 1000 18.5, 19.8.)  The host knows no lengths but the table's: one as wide as the longest sequence that a
+// server allows sends a small tree to the chunk kernel whatever its length.
 static bool few_rows(const AttnArgs &a, const qg_paged &c, int max_new) {
     const int64_t rows = (int64_t)max_new * a.G;
     if (rows <= DEC_ROWS) return true;

@@ -48,12 +48,13 @@
 //   * a cap keeps the order of a row's scores, so the maximum is capped alone, and the exponents' factor of S becomes
 //     a polynomial in S^2: three coefficients where all rows of the warp stay below a quarter of the cap (relative error 5e-7), five
 //     up to three quarters (7e-7), and where some score lies beyond, three for each score up to a quarter and 1 - 2 / (1 + e^2x) for the
-//     others (2^-20).  2048 tokens after 6000, 32/8 heads, fp16, dims 64, 128, 256 and 8-bit 128, us: 151, 197, 377, 383 uncapped; caps of 50
-//     with scores of a spread of 2 (the first form) 203, 251, 414, 427, of 8 (the second and third) 439, 535, 475, 587, of 20 (the third) 484, 570,
-//     561, 639: two more special functions per score.  In the first form the minimum that tells a row's reach and the code of the others
-//     take most of what it has over the uncapped kernel.  Beside a bias the first and the third;
-//   * a bias by distance is linear over tiles behind the rows: sums of eight slopes, half an instruction per score, 234 us (with
-//     the distance formed for each slot 350).
+//     others (2^-20).  2048 tokens after 6000, 32/8 heads, fp16, dims 64, 128, 256 and 8-bit 128, us: 152, 199, 378, 387 uncapped; caps of 50
+//     with scores of a spread of 2 (the first form) 201, 252, 416, 438, of 8 (the second and third) 446, 542, 477, 589, of 20 (the third) 494, 567,
+//     577, 638: two more special functions per score, which the exponents' own share a pipe with.  In the first form the minimum that
+//     tells a row's reach and the code of the others take most of what it has over the uncapped kernel;
+//   * a bias by distance is linear over tiles behind the rows: sums of eight slopes, half an instruction per score, 194, 249, 471, 523 us;
+//     with a cap too, in the first or the third form, 322, 384, 635, 719 (spread 2): the reach is a pass of its own, and where scores are
+//     not held (dim 256, 8-bit) caps and biases are formed in the pass of the maximum and again in that of the exponents.
 //
 // Work is counted in slot tiles over all items (row tile, cache head).  Where dealing whole items out,
 // the largest first and back and forth over the CTAs, loads them evenly enough, that is done: no

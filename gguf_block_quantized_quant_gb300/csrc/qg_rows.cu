@@ -100,8 +100,9 @@ struct SeqWork {
         nrt = (sq.n * a.G + ROWS - 1) / ROWS;
         int low = seen_from(sq.len - sq.n, a.window);
         if constexpr (MOD != MOD_PLAIN) {
-            // The tokens' own first slots, where they are as few as this kernel is chosen for; else all slots, which
-            // is more to read and the same result
+            // The tokens' own first slots, where they are as few as a tile has rows.  For more (trees that come here for their
+            // short page tables, or a hint that was too low) all slots: the same result, and more to read where a window hides the
+            // past, of which short tables hold some 16 MB for all row tiles
             if (a.sh.first || (a.sh.tree && a.window)) {
                 low = sq.n > ROWS ? 0
                                   : first_needed(a.sh.first ? a.sh.first + sq.first : nullptr, a.sh.positions ? a.sh.positions + sq.first : nullptr,

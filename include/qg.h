@@ -342,6 +342,10 @@ int qg_attn_paged(const void *q, int64_t ldq, int64_t hdq, int q_type, int token
  *   all, and a token whose range is empty gives zeros and -inf.
  * Slots before the first one that a row of the call sees may hold anything, as may those from kv_len on; those between have
  * to be finite (a probability of 0 times infinity is not 0).  lse is over the z above.
+ * tanh is off by at most 2^-19 of its value, and |p - j| is a difference of whole numbers, rounded once to fp32.  Which of the two
+ * kernels is taken goes by max_new, the heads and the most slots that the page table can name, and changes the rounding: the one
+ * for single tokens and small trees multiplies probabilities as two 16-bit addends and 8-bit keys as they are, the one for
+ * chunks rounds probabilities once to q_type and 8-bit keys, step * code, once to fp16; both round 8-bit values once to fp16.
  * Other arguments, limits, errors and the workspace as qg_attn_paged. */
 int qg_attn_shaped(const void *q, int64_t ldq, int64_t hdq, int q_type, int tokens, int q_heads, int max_new, float scale, int window,
                    float cap, const float *slopes, const int32_t *prefix, const int32_t *first, void *out, int out_type, float *lse,
@@ -353,7 +357,7 @@ int qg_attn_shaped(const void *q, int64_t ldq, int64_t hdq, int q_type, int toke
  *   draft i' of its own sequence where bit i' % 32 of tree[t * words + i' / 32] is set (its own bit with them: nothing is added).
  *   positions: tokens, or NULL where a token's position is its slot; p of the window and of the distance |p - p'|, in which
  *   a draft's p' is its own position too.  Drafts from 32 * words on are seen by none.
- *   cap, slopes: as qg_attn_shaped.  Values in the slots of all drafts have to be finite; a token that sees nothing gives zeros.
+ *   cap, slopes, the kernels and their rounding: as qg_attn_shaped.  Values in the slots of all drafts have to be finite; a token that sees nothing gives zeros.
  * Other arguments, limits, errors and the workspace as qg_attn_paged; qg_tree_masks makes tree and positions. */
 int qg_attn_tree(const void *q, int64_t ldq, int64_t hdq, int q_type, int tokens, int q_heads, int max_new, float scale, int window,
                  float cap, const float *slopes, const uint32_t *tree, int words, const int32_t *positions, void *out, int out_type,
